@@ -17,6 +17,9 @@ float32 or all four bfloat16. A: [d_inner, d_state] float32; D: [d_inner]
 float32 (``scan_fwd_ex``: or None, no skip term). y has the dtype of x. All
 tensors on the current CUDA (HIP) device, contiguous. ``scan_fwd_ex`` selects
 the scan direction and order, and multi-direction sums (SSM2D_* flags).
+
+The operators around the scan (layer norm, rotary positions with several axes,
+the gated delta rule) are in ``ops``, and reached from here too.
 """
 from __future__ import annotations
 
@@ -30,6 +33,7 @@ __all__ = [
     "status_string",
     "sync_check", "set_spin_limit", "release_workspaces", "set_epoch_for_test", "fwd_kernels", "exported_names",
     "Ssm2dError",
+    "layer_norm_fwd", "layer_norm_bwd", "rope_fwd", "rope_bwd", "gated_delta_fwd", "gated_delta_step",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -378,3 +382,16 @@ def scan_bwd_mamba(x, delta, A, B, C, D, dy, z=None, delta_bias=None, *, delta_s
         [_ptr(g.get(k)) for k in ("dx", "ddelta", "dA", "dB", "dC", "dD", "dz", "ddelta_bias", "dh_init", "dhh_init")]
     _call(fn, lib, x.device, args + [batch, d_inner, d_state, H, W, flags, _stream_handle(stream)])
     return g
+
+
+_OPS = ("layer_norm_fwd", "layer_norm_bwd", "rope_fwd", "rope_bwd", "gated_delta_fwd", "gated_delta_step")
+
+
+def __getattr__(name):
+    """The operators of ``ops``, imported with their first use (they need torch at import; this module does not)."""
+    if name in _OPS:
+        from . import ops
+
+        globals().update({n: getattr(ops, n) for n in _OPS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -19,6 +19,8 @@ _VARIANTS = ("g4", "g8", "flipw", "vfirst", "flipw_vfirst", "acc", "flipw_acc", 
              "rowc", "rowc_vfirst", "states_rowc", "states_flipw_rowc", "bwd_rowc", "bwd_edges_rowc", "bwd_ltr_rowc",
              "bwd_ltr_edges_rowc", "narrow")
 SOURCES = ["ssm2d.hip"] + [f"scan2d_{t}_{v}.hip" for t in ("f32", "bf16") for v in _VARIANTS]
+# the operators around the scan
+SOURCES += ["layer_norm.hip", "rope.hip", "delta.hip", "delta_step.hip"]
 LIB = os.path.join(PKG, "libssm2d.so")
 INCLUDE = os.path.join(ROOT, "include")
 
