@@ -132,7 +132,7 @@ int ssm2d_rope_bf16(const uint16_t *q, const uint16_t *k, const int32_t *positio
  * [sequences][heads][d_k][d_v], the state before the first and after the last
  * token; an empty sequence passes its state on. h_last may be h_init.
  * Limits: d_k <= SSM2D_DELTA_MAX_DK, d_v <= SSM2D_DELTA_MAX_DV, sequences *
- * heads < 2^24, tokens < 2^31 - 64; d_k, d_v >= 1 when there is work.
+ * heads < 2^24, heads < 2^15, tokens < 2^31 - 64 and chunks of 64 tokens < 2^22.
  *
  * The forward and backward work on chunks of 64 tokens with matrix
  * instructions: products of fp32 operands split into three bf16 parts each, so
@@ -154,6 +154,25 @@ int ssm2d_gated_delta_fwd(const float *q, const float *k, const float *v, const 
 int ssm2d_gated_delta_fwd_bf16(const uint16_t *q, const uint16_t *k, const uint16_t *v, const float *g,
                                const float *beta, const float *h_init, const int32_t *cu_seqlens, uint16_t *o,
                                float *h_last, const ssm2d_delta_shape *shape, float scale, void *stream);
+
+/* Gradients of a loss through gated_delta_fwd, given dout = dL/do (like v,
+ * strides do_stride) and dh_last = dL/dh_last (NULL: zeros): dq, dk (dense
+ * [batch][tokens][heads_qk][d_k], summed over the heads that share them), dv
+ * (dense like v), dg, dbeta (dense float32 [batch][tokens][heads]) and dh_init
+ * (NULL: not stored; like h_init, may be dh_last). The forward's chunk states
+ * are computed again. Workspaces: per head and chunk of 64 tokens, with
+ * d_k' = d_k rounded up to 32, 64 or 128 and d_v' = d_v to a multiple of 32,
+ * 19712 + 4 (d_k' + 64) d_v' bytes for the forward and 38144 + 4 (2 d_k' +
+ * 192) d_v' for the backward; heads are taken in passes that keep this within
+ * 16 GiB where one key head's share allows. */
+int ssm2d_gated_delta_bwd(const float *q, const float *k, const float *v, const float *g, const float *beta,
+                          const float *h_init, const int32_t *cu_seqlens, const float *dout, const float *dh_last,
+                          float *dq, float *dk, float *dv, float *dg, float *dbeta, float *dh_init,
+                          const ssm2d_delta_shape *shape, float scale, void *stream);
+int ssm2d_gated_delta_bwd_bf16(const uint16_t *q, const uint16_t *k, const uint16_t *v, const float *g, const float *beta,
+                               const float *h_init, const int32_t *cu_seqlens, const uint16_t *dout,
+                               const float *dh_last, uint16_t *dq, uint16_t *dk, uint16_t *dv, float *dg, float *dbeta,
+                               float *dh_init, const ssm2d_delta_shape *shape, float scale, void *stream);
 
 /* The recurrence token by token, for serving: the state stays in fp32 in
  * `state` ([batch][heads][d_k][d_v], read and rewritten in place). Any number

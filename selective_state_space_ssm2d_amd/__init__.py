@@ -33,7 +33,7 @@ __all__ = [
     "status_string",
     "sync_check", "set_spin_limit", "release_workspaces", "set_epoch_for_test", "fwd_kernels", "exported_names",
     "Ssm2dError",
-    "layer_norm_fwd", "layer_norm_bwd", "rope_fwd", "rope_bwd", "gated_delta_fwd", "gated_delta_step",
+    "layer_norm_fwd", "layer_norm_bwd", "rope_fwd", "rope_bwd", "gated_delta_fwd", "gated_delta_bwd", "gated_delta_step",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -384,7 +384,7 @@ def scan_bwd_mamba(x, delta, A, B, C, D, dy, z=None, delta_bias=None, *, delta_s
     return g
 
 
-_OPS = ("layer_norm_fwd", "layer_norm_bwd", "rope_fwd", "rope_bwd", "gated_delta_fwd", "gated_delta_step")
+_OPS = ("layer_norm_fwd", "layer_norm_bwd", "rope_fwd", "rope_bwd", "gated_delta_fwd", "gated_delta_bwd", "gated_delta_step")
 
 
 def __getattr__(name):

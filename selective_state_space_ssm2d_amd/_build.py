@@ -20,7 +20,8 @@ _VARIANTS = ("g4", "g8", "flipw", "vfirst", "flipw_vfirst", "acc", "flipw_acc", 
              "bwd_ltr_edges_rowc", "narrow")
 SOURCES = ["ssm2d.hip"] + [f"scan2d_{t}_{v}.hip" for t in ("f32", "bf16") for v in _VARIANTS]
 # the operators around the scan
-SOURCES += ["layer_norm.hip", "rope.hip", "delta.hip", "delta_step.hip"]
+SOURCES += ["layer_norm.hip", "rope.hip", "delta.hip", "delta_step.hip",
+            "delta_chunk_bf16.hip", "delta_chunk_bf16_bwd.hip", "delta_chunk_f32.hip", "delta_chunk_f32_bwd.hip"]
 LIB = os.path.join(PKG, "libssm2d.so")
 INCLUDE = os.path.join(ROOT, "include")
 

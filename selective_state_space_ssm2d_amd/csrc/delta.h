@@ -26,4 +26,18 @@ struct DeltaArgs {
 template <typename T>
 int delta_step(const DeltaArgs &a);
 
+// In chunks of 64 tokens (delta_chunk.h).
+template <typename T>
+int delta_chunk_fwd(const DeltaArgs &a);
+template <typename T>
+int delta_chunk_bwd(const DeltaArgs &a);
+template <>
+int delta_chunk_fwd<float>(const DeltaArgs &a);
+template <>
+int delta_chunk_fwd<uint16_t>(const DeltaArgs &a);
+template <>
+int delta_chunk_bwd<float>(const DeltaArgs &a);
+template <>
+int delta_chunk_bwd<uint16_t>(const DeltaArgs &a);
+
 }  // namespace ssm2d_impl

@@ -7,6 +7,8 @@
 namespace ssm2d_impl {
 namespace {
 
+constexpr long kFewTokens = 16;
+
 int fill(DeltaArgs *a, const ssm2d_delta_shape *sh, float scale, void *stream, bool *work)
 {
     *work = false;
@@ -17,7 +19,7 @@ int fill(DeltaArgs *a, const ssm2d_delta_shape *sh, float scale, void *stream, b
     if (sh->heads_qk > 0 ? sh->heads % sh->heads_qk != 0 : sh->heads != 0) return SSM2D_ERR_BAD_DIM;
     const int64_t seqs = sh->n_seq > 0 ? sh->n_seq : sh->batch;
     if (sh->d_k > SSM2D_DELTA_MAX_DK || sh->d_v > SSM2D_DELTA_MAX_DV || sh->tokens >= (int64_t{1} << 31) - 64 ||
-        sh->heads >= (1 << 24) || seqs >= (1 << 24) || seqs * std::max<int64_t>(sh->heads, 1) >= (1 << 24))
+        sh->heads >= (1 << 15) || seqs >= (1 << 24) || seqs * std::max<int64_t>(sh->heads, 1) >= (1 << 24))
         return SSM2D_ERR_UNSUPPORTED;
     a->batch = sh->batch, a->tokens = sh->tokens, a->n_seq = sh->n_seq;
     a->hk = static_cast<int>(sh->heads_qk), a->h = static_cast<int>(sh->heads);
@@ -79,8 +81,29 @@ int fwd_entry(const T *q, const T *k, const T *v, const float *g, const float *b
     if (misaligned_in<T>(a)) return SSM2D_ERR_MISALIGNED;
     return run(a, [&]() -> int {
         if (a.tokens == 0) return pass_states_on(a, h_init, h_last);
-        if (a.n_seq > 0) return SSM2D_ERR_UNSUPPORTED;
-        return delta_step<T>(a);
+        // a few tokens: the recurrence itself, one launch and no workspace
+        if (a.n_seq == 0 && a.tokens <= kFewTokens) return delta_step<T>(a);
+        return delta_chunk_fwd<T>(a);
+    });
+}
+
+template <typename T>
+int bwd_entry(const T *q, const T *k, const T *v, const float *g, const float *beta, const float *h_init, const int32_t *cu, const T *dout,
+              const float *dh_last, T *dq, T *dk, T *dv, float *dg, float *dbeta, float *dh_init, const ssm2d_delta_shape *sh, float scale,
+              void *stream)
+{
+    DeltaArgs a{};
+    bool work = false;
+    const int st = fill(&a, sh, scale, stream, &work);
+    if (st != SSM2D_OK || !work) return st;
+    a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.h_init = h_init, a.cu = a.n_seq > 0 ? cu : nullptr, a.dout = dout, a.dh_last = dh_last;
+    a.dq = dq, a.dk = dk, a.dv = dv, a.dg = dg, a.dbeta = dbeta, a.dh_init = dh_init;
+    if (a.tokens > 0 && (!q || !k || !v || !g || !beta || !dout || !dq || !dk || !dv || !dg || !dbeta || (a.n_seq > 0 && !cu)))
+        return SSM2D_ERR_NULLPTR;
+    if (misaligned_in<T>(a)) return SSM2D_ERR_MISALIGNED;
+    return run(a, [&]() -> int {
+        if (a.tokens == 0) return pass_states_on(a, dh_last, dh_init);
+        return delta_chunk_bwd<T>(a);
     });
 }
 
@@ -115,6 +138,23 @@ int ssm2d_gated_delta_fwd_bf16(const uint16_t *q, const uint16_t *k, const uint1
                                const ssm2d_delta_shape *shape, float scale, void *stream)
 {
     return ssm2d_impl::fwd_entry<uint16_t>(q, k, v, g, beta, h_init, cu_seqlens, o, h_last, shape, scale, stream);
+}
+
+int ssm2d_gated_delta_bwd(const float *q, const float *k, const float *v, const float *g, const float *beta, const float *h_init,
+                          const int32_t *cu_seqlens, const float *dout, const float *dh_last, float *dq, float *dk, float *dv, float *dg,
+                          float *dbeta, float *dh_init, const ssm2d_delta_shape *shape, float scale, void *stream)
+{
+    return ssm2d_impl::bwd_entry<float>(q, k, v, g, beta, h_init, cu_seqlens, dout, dh_last, dq, dk, dv, dg, dbeta, dh_init, shape, scale,
+                                        stream);
+}
+
+int ssm2d_gated_delta_bwd_bf16(const uint16_t *q, const uint16_t *k, const uint16_t *v, const float *g, const float *beta,
+                               const float *h_init, const int32_t *cu_seqlens, const uint16_t *dout, const float *dh_last, uint16_t *dq,
+                               uint16_t *dk, uint16_t *dv, float *dg, float *dbeta, float *dh_init, const ssm2d_delta_shape *shape,
+                               float scale, void *stream)
+{
+    return ssm2d_impl::bwd_entry<uint16_t>(q, k, v, g, beta, h_init, cu_seqlens, dout, dh_last, dq, dk, dv, dg, dbeta, dh_init, shape,
+                                           scale, stream);
 }
 
 int ssm2d_gated_delta_step(const float *q, const float *k, const float *v, const float *g, const float *beta, float *state, float *o,

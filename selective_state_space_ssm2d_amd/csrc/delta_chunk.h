@@ -1,0 +1,1241 @@
+// libssm2d: the gated delta rule in chunks of 64 tokens, forward and backward.
+//
+// With G_i the running sum of g over a chunk, gamma_i = e^G_i and
+// Gam_ij = e^(G_i - G_j), a chunk that starts from S0 has (rows = tokens)
+//   R = V - gamma K S0,   N_ij = Gam_ij k_i . k_j (j < i),   B = diag(beta)
+//   E = (I + N B)^-1 R,   U = B E
+//   O = scale (gamma Q S0 + P U),   P_ij = Gam_ij q_i . k_j (j <= i)
+//   S1 = gamma_last S0 + K^T (Gam_last U)
+// With M = (I + N B)^-1 N (strictly lower; no division by beta) both inverses
+// the passes need are products: E = R - M (B R), and for the adjoint of U,
+// dR = dU - M^T (B dU). Given dO and the adjoint D1 of S1:
+//   dU = scale P^T dO + Gam_last K D1
+//   dV = B dR,   dbeta_i = dR_i . E_i
+//   D0 = gamma_last D1 + Q^T (scale gamma dO) - K^T (gamma B dR)
+// and, with Pd_ij = scale Gam_ij dO_i . U_j (j <= i) and
+// Nd_ij = -beta_i Gam_ij dR_i . U_j (j < i),
+//   dQ = scale gamma dO S0^T + Pd K
+//   dK = Rk + Ck,   Rk = -gamma B dR S0^T + Nd K,   Ck = Gam_last U D1^T + Pd^T Q + Nd^T K
+//   dG_i = q_i . dQ_i + k_i . Rk_i - k_i . Ck_i, and at the chunk's end
+//   also gamma_last <S0, D1> + sum_j k_j . (Gam_last U D1^T)_j;  dg = suffix sums of dG.
+//
+// Kernels: delta_prep (per chunk: the gates and M), delta_z (scale P^T dO),
+// delta_seq (the chain over chunks, S0 and E, and in the backward at the same
+// time the chain of adjoints, D1 and dR), delta_out (O) and delta_local (the
+// gradients of a chunk). Only delta_seq is sequential.
+//
+// Precision: an fp32 operand goes through the matrix cores as the sum of
+// three bf16 parts, cut off exactly (8 + 8 + 8 bits); products keep the six
+// terms down to 2^-24 of the largest, so every product is as exact as in fp32
+// at 6/16 of its matrix instructions' time. bf16 inputs are one part (three
+// terms against an fp32 operand). Only delta_out of a bf16 result uses two
+// parts (2^-16, against the 2^-9 of the result's own rounding).
+//
+// Fragments: v_mfma_f32_16x16x32_bf16 with lane l holding row (column) l % 16
+// and, of the 32 summed indices, 4 (l / 16) + j and 16 + 4 (l / 16) + j, j < 4.
+// That is the order in which the accumulators of two stacked 16 x 16 tiles
+// lie, so a result becomes the next product's operand in registers; LDS tiles
+// give it by two 8-byte reads along rows, or two transposing reads down rows.
+#pragma once
+
+#include "delta.h"
+
+namespace ssm2d_impl {
+
+constexpr int kC = 64;  // tokens a chunk
+
+struct ChunkParams {
+    const void *q, *k, *v, *dout;
+    const float *g, *beta, *h_init, *dh_last;
+    const int *cu;
+    void *o, *dq, *dk, *dv;
+    float *h_last, *dg, *dbeta, *dh_init;
+    // workspace, by [slot][head of this pass]
+    float *gates;                       // [5][kC]: gamma, Gam_last, beta, G and its rounding error
+    uint4 *m, *mt;                      // -M, -M^T: 6 fragments x 3 parts
+    float *s0, *d1;                     // [KD][dvp]
+    float *e, *dr, *z;                  // [kC][dvp]
+    long batch, tokens, n_seq, slots, chunks_b;  // chunks_b: chunks of a batch entry
+    int hk, h, rep, dk_, dv_, dvp;
+    int hk0, nhk, nh;                   // this pass: key heads hk0 .. hk0 + nhk - 1, nh = nhk * rep heads
+    long qs[3], ks[3], vs[3], os[3], gs[3], bs[3];
+    float scale;
+    int vec_qk, vec_do;                 // rows of q and k, of dout can be read 16 bytes at a time
+    int vec_o, vec_dqk;                 // rows of o, of dq and dk can be written four elements at a time
+};
+
+using bfrag = __bf16 __attribute__((ext_vector_type(8)));
+using facc = float __attribute__((ext_vector_type(4)));
+using half4 = short __attribute__((ext_vector_type(4)));
+
+// Where a chunk lies.
+struct Place {
+    long b;   // batch entry (addresses)
+    long t0;  // its first token there
+    int len;  // tokens, 1 .. kC (0: no such chunk)
+};
+
+struct Seq {
+    long b, t0, len, slot0;  // slot0: the slot of its first chunk
+};
+
+__device__ __forceinline__ long packed_at(const ChunkParams &p, long s)
+{
+    const long c = p.cu[s];
+    return c < 0 ? 0 : (c > p.tokens ? p.tokens : c);
+}
+
+// Sequence s. Packed sequences' chunks get slots from cu / 64 + s on: at
+// least as many as they need before the next sequence's, without a table.
+__device__ __forceinline__ Seq find_seq(const ChunkParams &p, long s)
+{
+    if (p.n_seq == 0) return {s, 0, p.tokens, s * p.chunks_b};
+    const long a = packed_at(p, s), e = packed_at(p, s + 1);
+    return {0, a, e > a ? e - a : 0, a / kC + s};
+}
+
+__device__ __forceinline__ Place find_chunk(const ChunkParams &p, long slot)
+{
+    Seq q;
+    if (p.n_seq == 0) {
+        q = find_seq(p, slot / p.chunks_b);
+    } else {
+        long lo = 0, hi = p.n_seq - 1;  // the last sequence whose slots start at or before this one
+        while (lo < hi) {
+            const long mid = (lo + hi + 1) / 2;
+            if (packed_at(p, mid) / kC + mid <= slot) lo = mid;
+            else hi = mid - 1;
+        }
+        q = find_seq(p, lo);
+    }
+    const long at = (slot - q.slot0) * kC;
+    if (at < 0 || at >= q.len) return {0, 0, 0};
+    return {q.b, q.t0 + at, static_cast<int>(q.len - at < kC ? q.len - at : kC)};
+}
+
+// ------------------------------------------------------------------ parts
+
+__device__ __forceinline__ unsigned top16(unsigned hi, unsigned lo) { return __builtin_amdgcn_perm(hi, lo, 0x07060302u); }
+
+// N parts of two values, each part's pair in one word.
+template <int N>
+__device__ __forceinline__ void split2(float a, float b, unsigned (&w)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const unsigned ua = __float_as_uint(a), ub = __float_as_uint(b);
+        w[i] = top16(ub, ua);
+        if (i + 1 < N) {
+            a -= __uint_as_float(ua & 0xffff0000u);
+            b -= __uint_as_float(ub & 0xffff0000u);
+        }
+    }
+}
+
+union FragBits {
+    bfrag f;
+    unsigned w[4];
+    uint4 q;
+    half4 h[2];
+};
+
+// The operand that two stacked accumulator tiles make.
+template <int N>
+__device__ __forceinline__ void split_acc(const facc &lo, const facc &hi, bfrag (&f)[N])
+{
+    FragBits b[N];
+    unsigned w[N];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        split2<N>(lo[2 * i], lo[2 * i + 1], w);
+#pragma unroll
+        for (int n = 0; n < N; ++n) b[n].w[i] = w[n];
+        split2<N>(hi[2 * i], hi[2 * i + 1], w);
+#pragma unroll
+        for (int n = 0; n < N; ++n) b[n].w[2 + i] = w[n];
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) f[n] = b[n].f;
+}
+
+// acc += a b over the parts whose product reaches the last place kept.
+template <int NA, int NB>
+__device__ __forceinline__ void mma(facc &acc, const bfrag (&a)[NA], const bfrag (&b)[NB])
+{
+    constexpr int kMax = NA > NB ? NA : NB;
+#pragma unroll
+    for (int s = kMax - 1; s >= 0; --s)  // small terms first
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            const int j = s - i;
+            if (j >= 0 && j < NB) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc, 0, 0, 0);
+        }
+}
+
+// A tile in LDS: NP parts of [ROWS][COLS] bf16, rows padded by 16 bytes (the
+// 16 rows of a fragment then start 4 banks apart, both ways of reading).
+template <int NP, int ROWS, int COLS>
+struct Tile {
+    static constexpr int kLd = COLS + 8, kPart = ROWS * kLd, kBytes = NP * kPart * 2;
+    uint16_t *p;
+    // rows r0 .. r0 + 15, summed index along the rows from c0
+    __device__ __forceinline__ void rows(int r0, int c0, bfrag (&f)[NP]) const
+    {
+        const int l = threadIdx.x % 64;
+        const uint16_t *a = p + (r0 + l % 16) * kLd + c0 + 4 * (l / 16);
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            FragBits b;
+            b.h[0] = *reinterpret_cast<const half4 *>(a + n * kPart);
+            b.h[1] = *reinterpret_cast<const half4 *>(a + n * kPart + 16);
+            f[n] = b.f;
+        }
+    }
+    // columns c0 .. c0 + 15, summed index down the rows from r0
+    __device__ __forceinline__ void cols(int r0, int c0, bfrag (&f)[NP]) const
+    {
+        using lds4 = __attribute__((address_space(3))) half4 *;
+        const int l = threadIdx.x % 64;
+        uint16_t *a = p + (r0 + 4 * (l / 16) + (l % 16) / 4) * kLd + c0 + 4 * (l % 4);
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            FragBits b;
+            b.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(a + n * kPart));
+            b.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(a + n * kPart + 16 * kLd));
+            f[n] = b.f;
+        }
+    }
+    // four neighbours of a row
+    __device__ __forceinline__ void put4(int r, int c, float x0, float x1, float x2, float x3) const
+    {
+        unsigned a[NP], b[NP];
+        split2<NP>(x0, x1, a);
+        split2<NP>(x2, x3, b);
+#pragma unroll
+        for (int n = 0; n < NP; ++n) *reinterpret_cast<uint2 *>(p + n * kPart + r * kLd + c) = make_uint2(a[n], b[n]);
+    }
+    __device__ __forceinline__ void get4(int r, int c, float (&x)[4]) const
+    {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = 0.0f;
+#pragma unroll
+        for (int n = NP - 1; n >= 0; --n) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(p + n * kPart + r * kLd + c);
+            x[0] += bf16_lo(w.x), x[1] += bf16_hi(w.x), x[2] += bf16_lo(w.y), x[3] += bf16_hi(w.y);
+        }
+    }
+};
+
+template <typename T>
+constexpr int kParts = sizeof(T) == 2 ? 1 : 3;  // parts of an input
+
+// ------------------------------------------------------------------ staging
+
+// 16 bytes of row t (of `len`) of a tensor whose rows hold n elements.
+template <typename T>
+__device__ __forceinline__ void load_piece(Raw<T, 16 / static_cast<int>(sizeof(T))> &r, const T *row, int c, int n, bool live, bool vec)
+{
+    constexpr int N = 16 / static_cast<int>(sizeof(T));
+    if (!live || c >= n) {
+        r.clear();
+    } else if (vec) {
+        r.load(row + c);
+    } else {
+        float x[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[j] = c + j < n ? widen1(row[c + j]) : 0.0f;
+        r.set(x);
+    }
+}
+
+template <typename T, int COLS>
+__device__ __forceinline__ void put_piece(const Tile<kParts<T>, kC, COLS> &t, int r, int c, const Raw<T, 16 / static_cast<int>(sizeof(T))> &x)
+{
+    if constexpr (sizeof(T) == 2) *reinterpret_cast<uint4 *>(t.p + r * t.kLd + c) = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+    else t.put4(r, c, x.get(0), x.get(1), x.get(2), x.get(3));
+}
+
+// A chunk's rows of q or k (COLS wide, zeros past n and past the chunk): read
+// to registers, then put into LDS.
+template <typename T, int COLS, int THREADS>
+struct Stage {
+    static constexpr int N = 16 / static_cast<int>(sizeof(T)), kRow = COLS / N, kAll = kC * kRow, kEach = (kAll + THREADS - 1) / THREADS;
+    Raw<T, N> r[kEach];
+    __device__ __forceinline__ void load(const T *base, long stride, int len, int n, bool vec)
+    {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int at = i * THREADS + threadIdx.x;
+            const int row = at / kRow, c = (at % kRow) * N;
+            load_piece<T>(r[i], base + row * stride, c, n, at < kAll && row < len, vec);
+        }
+    }
+    __device__ __forceinline__ void put(const Tile<kParts<T>, kC, COLS> &t) const
+    {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int at = i * THREADS + threadIdx.x;
+            if (kAll % THREADS == 0 || at < kAll) put_piece<T, COLS>(t, at / kRow, (at % kRow) * N, r[i]);
+        }
+    }
+};
+
+// ------------------------------------------------------------------ gates
+
+// gamma, Gam_last, beta, G's two parts of a chunk into out[5][kC], by the
+// first wave. G is summed in fp64 and kept as two floats, so that differences
+// of large sums stay exact. Below -1e4 a decay is 0 in any sum: held there,
+// so that -inf gives 0 and not inf - inf.
+__device__ __forceinline__ void make_gates(const ChunkParams &p, const Place &c, int head, float *out)
+{
+    const int i = threadIdx.x;
+    if (i >= kC) return;
+    float g = 0.0f, b = 0.0f;
+    if (i < c.len) {
+        g = p.g[c.b * p.gs[0] + (c.t0 + i) * p.gs[1] + head * p.gs[2]];
+        g = g < -1e4f ? -1e4f : g;
+        b = p.beta[c.b * p.bs[0] + (c.t0 + i) * p.bs[1] + head * p.bs[2]];
+    }
+    double s = g;
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) {
+        const double u = __shfl_up(s, m, 64);
+        if (i >= m) s += u;
+    }
+    const double last = __shfl(s, 63, 64);
+    out[i] = expf(static_cast<float>(s));
+    out[kC + i] = expf(static_cast<float>(last - s));
+    out[2 * kC + i] = b;
+    const float hi = static_cast<float>(s);
+    out[3 * kC + i] = hi;
+    out[4 * kC + i] = static_cast<float>(s - hi);
+}
+__device__ __forceinline__ float gam(const float *gt, int i, int j)
+{
+    return expf((gt[3 * kC + i] - gt[3 * kC + j]) + (gt[4 * kC + i] - gt[4 * kC + j]));
+}
+
+constexpr int kGates = 5 * kC;
+constexpr int kMFrags = 6;             // fragments of M that are not zero
+constexpr int kMWords = kMFrags * 3 * 64;  // uint4 of one head's M
+// fragment of M for rows 16 rt .., columns 32 ks .. (ks <= rt / 2)
+__host__ __device__ constexpr int m_frag(int rt, int ks) { return rt < 2 ? rt : 2 * rt - 2 + ks; }
+// fragment of M^T for rows 16 rt .., columns 32 ks .. (ks >= rt / 2)
+__host__ __device__ constexpr int mt_frag(int rt, int ks) { return rt < 2 ? 2 * rt + ks : 2 + rt; }
+
+// ------------------------------------------------------------------ delta_prep
+
+__device__ __forceinline__ facc mfma4(float a, float b, facc c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
+
+// Gates and M of one chunk for the heads that share key head hk0 + blockIdx.y.
+// M block by block: the 16 x 16 blocks on the diagonal by substitution, a
+// column a lane, then the blocks below by M21 = (I - M22 B2) N21 (I - B1 M11)
+// for halves of 32 and of 64, in fp32 matrix instructions (20 products of 16^3
+// a head: small beside the split products elsewhere).
+template <typename T, int KD, bool BWD>
+__global__ __launch_bounds__(256) void delta_prep(ChunkParams p)
+{
+    constexpr int NP = kParts<T>, kLdM = 68;
+    __shared__ __align__(16) uint16_t kbuf[Tile<NP, kC, KD>::kBytes / 2];
+    __shared__ __align__(16) float sn[kC * kLdM], sm[kC * kLdM], gt[kGates];
+    const long slot = blockIdx.x;
+    const Place c = find_chunk(p, slot);
+    if (c.len == 0) return;
+    const int hk = p.hk0 + blockIdx.y, wave = threadIdx.x / 64, l = threadIdx.x % 64, g4 = l / 16, l16 = l % 16;
+    const Tile<NP, kC, KD> kt{kbuf};
+    {
+        Stage<T, KD, 256> st;
+        st.load(static_cast<const T *>(p.k) + c.b * p.ks[0] + c.t0 * p.ks[1] + hk * p.ks[2], p.ks[1], c.len, p.dk_, p.vec_qk);
+        st.put(kt);
+    }
+    __syncthreads();
+    facc kk[4];  // rows 16 wave + 4 g4 + r, columns 16 ct + l16
+#pragma unroll
+    for (int ct = 0; ct < 4; ++ct) {
+        kk[ct] = facc{0, 0, 0, 0};
+        if (ct > wave) continue;
+#pragma unroll
+        for (int ks = 0; ks < KD / 32; ++ks) {
+            bfrag a[NP], b[NP];
+            kt.rows(16 * wave, 32 * ks, a);
+            kt.rows(16 * ct, 32 * ks, b);
+            mma<NP, NP>(kk[ct], a, b);
+        }
+    }
+    for (int r = 0; r < p.rep; ++r) {
+        const int hl = blockIdx.y * p.rep + r;  // head of this pass
+        __syncthreads();
+        make_gates(p, c, hk * p.rep + r, gt);
+        __syncthreads();
+        const long at = slot * p.nh + hl;
+        for (int i = threadIdx.x; i < kGates; i += 256) p.gates[at * kGates + i] = gt[i];
+        // N
+#pragma unroll
+        for (int ct = 0; ct < 4; ++ct)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int row = 16 * wave + 4 * g4 + j, col = 16 * ct + l16;
+                sn[row * kLdM + col] = col < row ? gam(gt, row, col) * kk[ct][j] : 0.0f;
+                if (ct > wave) sm[row * kLdM + col] = 0.0f;
+            }
+        __syncthreads();
+        const float *beta = gt + 2 * kC;
+        {   // diagonal block `wave`, column l16 (each 16 lanes the same)
+            const int o = 16 * wave;
+            float m[16], mb[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float s = sn[(o + i) * kLdM + o + l16];
+#pragma unroll
+                for (int k = 0; k < i; ++k) s = fmaf(-sn[(o + i) * kLdM + o + k], mb[k], s);
+                m[i] = i > l16 ? s : 0.0f;
+                mb[i] = beta[o + i] * m[i];
+            }
+            if (g4 == 0) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sm[(o + i) * kLdM + o + l16] = m[i];
+            }
+        }
+        __syncthreads();
+        if (wave < 2) {  // blocks (1, 0) and (3, 2); summed index 4 g4 + s
+            const int r0 = 32 * wave + 16, c0 = 32 * wave;
+            facc x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = sn[(r0 + 4 * g4 + j) * kLdM + c0 + l16];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int k = c0 + 4 * g4 + s;
+                x = mfma4(-sn[(r0 + l16) * kLdM + k] * beta[k], sm[k * kLdM + c0 + l16], x);
+            }
+            facc y = x;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int k = r0 + 4 * g4 + s;
+                y = mfma4(-sm[(r0 + l16) * kLdM + k] * beta[k], x[s], y);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sm[(r0 + 4 * g4 + j) * kLdM + c0 + l16] = y[j];
+        }
+        __syncthreads();
+        {   // rows 32 .. 63, columns 0 .. 31: one tile a wave
+            const int r0 = 32 + 16 * (wave / 2), c0 = 16 * (wave % 2);
+            facc x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = sn[(r0 + 4 * g4 + j) * kLdM + c0 + l16];
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const int k = 16 * (s / 4) + 4 * g4 + s % 4;
+                x = mfma4(-sn[(r0 + l16) * kLdM + k] * beta[k], sm[k * kLdM + c0 + l16], x);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sm[(r0 + 4 * g4 + j) * kLdM + c0 + l16] = x[j];
+            __syncthreads();
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const int k = 32 + 16 * (s / 4) + 4 * g4 + s % 4;
+                x = mfma4(-sm[(r0 + l16) * kLdM + k] * beta[k], sm[k * kLdM + c0 + l16], x);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sm[(r0 + 4 * g4 + j) * kLdM + c0 + l16] = x[j];
+        }
+        __syncthreads();
+        // fragments of -M (and -M^T), three parts each
+        for (int f = wave; f < (BWD ? 2 : 1) * kMFrags; f += 4) {
+            const bool tr = f >= kMFrags;
+            const int n = tr ? f - kMFrags : f;
+            int rt, ks;
+            if (!tr) rt = n < 2 ? n : 2 + (n - 2) / 2, ks = n < 2 ? 0 : (n - 2) % 2;
+            else rt = n < 4 ? n / 2 : n - 2, ks = n < 4 ? n % 2 : 1;
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int row = 16 * rt + l16, k = 32 * ks + 16 * (j / 4) + 4 * g4 + j % 4;
+                x[j] = -(tr ? sm[k * kLdM + row] : sm[row * kLdM + k]);
+            }
+            unsigned w[4][3];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) split2<3>(x[2 * j], x[2 * j + 1], w[j]);
+            uint4 *out = (tr ? p.mt : p.m) + at * kMWords + n * 3 * 64 + l;
+#pragma unroll
+            for (int q = 0; q < 3; ++q) out[q * 64] = make_uint4(w[0][q], w[1][q], w[2][q], w[3][q]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ P
+
+// Rows 16 rt .. of scale Gam_ij q_i . k_j (j <= i) into `out`, by one wave:
+// lane token i = 16 rt + l % 16, four neighbouring j at a time.
+template <typename T, int KD, int NPP>
+__device__ __forceinline__ void make_p(const Tile<kParts<T>, kC, KD> &qt, const Tile<kParts<T>, kC, KD> &kt, const float *gt, float scale,
+                                       int rt, const Tile<NPP, kC, kC> &out)
+{
+    constexpr int NP = kParts<T>;
+    const int l = threadIdx.x % 64, i = 16 * rt + l % 16;
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt) {
+        facc acc = {0, 0, 0, 0};
+        if (jt <= rt) {
+#pragma unroll
+            for (int ks = 0; ks < KD / 32; ++ks) {
+                bfrag a[NP], b[NP];
+                kt.rows(16 * jt, 32 * ks, a);
+                qt.rows(16 * rt, 32 * ks, b);
+                mma<NP, NP>(acc, a, b);
+            }
+        }
+        const int j0 = 16 * jt + 4 * (l / 16);
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = j0 + j <= i ? scale * gam(gt, i, j0 + j) * acc[j] : 0.0f;
+        out.put4(i, j0, x[0], x[1], x[2], x[3]);
+    }
+}
+
+// Z = scale P^T dO of one chunk and head: workgroup (slot, head).
+template <typename T, int KD>
+__global__ __launch_bounds__(256) void delta_z(ChunkParams p)
+{
+    constexpr int NP = kParts<T>, VS = 32;
+    using KT = Tile<NP, kC, KD>;
+    using PT = Tile<3, kC, kC>;
+    using VT = Tile<NP, kC, VS>;
+    extern __shared__ __align__(16) uint16_t lds[];
+    const long slot = blockIdx.x;
+    const Place c = find_chunk(p, slot);
+    if (c.len == 0) return;
+    const int hl = blockIdx.y, head = p.hk0 * p.rep + hl, hk = head / p.rep, wave = threadIdx.x / 64, l = threadIdx.x % 64;
+    const KT qt{lds}, kt{lds + KT::kBytes / 2};
+    const PT pt{lds + KT::kBytes};
+    const VT ot{lds + KT::kBytes + PT::kBytes / 2};
+    float *gt = reinterpret_cast<float *>(lds + KT::kBytes + PT::kBytes / 2 + VT::kBytes / 2);
+    {
+        Stage<T, KD, 256> a, b;
+        a.load(static_cast<const T *>(p.q) + c.b * p.qs[0] + c.t0 * p.qs[1] + hk * p.qs[2], p.qs[1], c.len, p.dk_, p.vec_qk);
+        b.load(static_cast<const T *>(p.k) + c.b * p.ks[0] + c.t0 * p.ks[1] + hk * p.ks[2], p.ks[1], c.len, p.dk_, p.vec_qk);
+        make_gates(p, c, head, gt);
+        a.put(qt);
+        b.put(kt);
+    }
+    __syncthreads();
+    make_p<T, KD, 3>(qt, kt, gt, p.scale, wave, pt);
+    const T *op = static_cast<const T *>(p.dout) + c.b * p.os[0] + c.t0 * p.os[1] + head * p.os[2];
+    float *zp = p.z + (slot * p.nh + hl) * kC * p.dvp;
+    for (int v0 = 0; v0 < p.dvp; v0 += VS) {
+        __syncthreads();
+        {
+            Stage<T, VS, 256> st;
+            st.load(op + v0, p.os[1], c.len, p.dv_ - v0, p.vec_do);
+            st.put(ot);
+        }
+        __syncthreads();
+        // rows v, columns tokens j = 16 wave ..: four neighbouring v a lane
+        facc acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            if (32 * ks + 31 < 16 * wave) continue;  // i >= j
+            bfrag b[3];
+            pt.cols(32 * ks, 16 * wave, b);
+#pragma unroll
+            for (int vt = 0; vt < 2; ++vt) {
+                bfrag a[NP];
+                ot.cols(32 * ks, 16 * vt, a);
+                mma<NP, 3>(acc[vt], a, b);
+            }
+        }
+#pragma unroll
+        for (int vt = 0; vt < 2; ++vt)
+            *reinterpret_cast<facc *>(zp + (16 * wave + l % 16) * p.dvp + v0 + 16 * vt + 4 * (l / 16)) = acc[vt];
+    }
+}
+
+// ------------------------------------------------------------------ delta_seq
+
+// What a chunk's step reads from LDS: K (and Q in the backward), M's
+// fragments and the gates.
+template <typename T, int KD, bool BWD>
+struct SeqBuf {
+    static constexpr int kTile = Tile<kParts<T>, kC, KD>::kBytes;
+    static constexpr int kBytes = (BWD ? 2 : 1) * kTile + kMWords * 16 + 3 * kC * 4;
+    // two buffers where they fit beside each other
+    static constexpr int kBufs = 2 * kBytes <= 160 * 1024 ? 2 : 1;
+};
+
+template <typename T, int KD, bool BWD>
+struct SeqStage {
+    Stage<T, KD, 256> k, q;
+    uint4 m[(kMWords + 255) / 256];
+    float g;
+    __device__ __forceinline__ void load(const ChunkParams &p, long b, long t0, int len, int hk, long at)
+    {
+        k.load(static_cast<const T *>(p.k) + b * p.ks[0] + t0 * p.ks[1] + hk * p.ks[2], p.ks[1], len, p.dk_, p.vec_qk);
+        if constexpr (BWD) q.load(static_cast<const T *>(p.q) + b * p.qs[0] + t0 * p.qs[1] + hk * p.qs[2], p.qs[1], len, p.dk_, p.vec_qk);
+        const uint4 *src = (BWD ? p.mt : p.m) + at * kMWords;
+#pragma unroll
+        for (int i = 0; i < (kMWords + 255) / 256; ++i) {
+            const int w = i * 256 + threadIdx.x;
+            m[i] = w < kMWords ? src[w] : make_uint4(0, 0, 0, 0);
+        }
+        g = threadIdx.x < 3 * kC ? p.gates[at * kGates + threadIdx.x] : 0.0f;
+    }
+    __device__ __forceinline__ void put(uint16_t *lds) const
+    {
+        constexpr int kTile = SeqBuf<T, KD, BWD>::kTile / 2;
+        k.put(Tile<kParts<T>, kC, KD>{lds});
+        if constexpr (BWD) q.put(Tile<kParts<T>, kC, KD>{lds + kTile});
+        uint16_t *rest = lds + (BWD ? 2 : 1) * kTile;
+        uint4 *mm = reinterpret_cast<uint4 *>(rest);
+#pragma unroll
+        for (int i = 0; i < (kMWords + 255) / 256; ++i) {
+            const int w = i * 256 + threadIdx.x;
+            if (w < kMWords) mm[w] = m[i];
+        }
+        if (threadIdx.x < 3 * kC) reinterpret_cast<float *>(rest + kMWords * 8)[threadIdx.x] = g;
+    }
+};
+
+// The chain over a sequence's chunks for 16 columns of the state a wave (64 a
+// workgroup). Columns are independent, so waves only share what they read.
+// The state [KD][16] stays in accumulators, from which it is cut into operands.
+template <typename T, int KD, bool BWD>
+__device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
+{
+    constexpr int NP = kParts<T>, NT = KD / 16;
+    using Buf = SeqBuf<T, KD, BWD>;
+    const int wave = threadIdx.x / 64, l = threadIdx.x % 64, g4 = l / 16, l16 = l % 16;
+    const long s = blockIdx.x / p.nh;
+    const int hl = static_cast<int>(blockIdx.x - s * p.nh), head = p.hk0 * p.rep + hl, hk = head / p.rep;
+    const int v0 = blockIdx.y * 64 + wave * 16;
+    const bool act = v0 < p.dvp;      // this wave has columns
+    const int col = v0 + l16;
+    const bool live = col < p.dv_;    // this lane's column is not padding
+    const Seq q = find_seq(p, s);
+    const long n = (q.len + kC - 1) / kC;
+    const long state = ((s * p.h + head) * p.dk_) * p.dv_;
+    const float *init = BWD ? p.dh_last : p.h_init;
+    facc S[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int row = 16 * t + 4 * g4 + j;
+            S[t][j] = (init && live && row < p.dk_) ? init[state + static_cast<long>(row) * p.dv_ + col] : 0.0f;
+        }
+    auto len_of = [&](long c) { return static_cast<int>(q.len - c * kC < kC ? q.len - c * kC : kC); };
+    auto chunk = [&](long i) { return BWD ? n - 1 - i : i; };
+    // a column of the chunk's rows of v (dO and Z in the backward), 16 tokens a lane
+    float x0[16], x1[16];
+    auto load_cols = [&](long c) {
+        const int len = len_of(c);
+        const long at = ((q.slot0 + c) * p.nh + hl);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int row = 16 * t + 4 * g4 + j;
+                const bool ok = live && row < len;
+                if constexpr (BWD) {
+                    x0[4 * t + j] = ok ? widen1(static_cast<const T *>(p.dout)[q.b * p.os[0] + (q.t0 + c * kC + row) * p.os[1] + head * p.os[2] + col]) : 0.0f;
+                    x1[4 * t + j] = act ? p.z[(at * kC + row) * p.dvp + col] : 0.0f;
+                } else {
+                    x0[4 * t + j] = ok ? widen1(static_cast<const T *>(p.v)[q.b * p.vs[0] + (q.t0 + c * kC + row) * p.vs[1] + head * p.vs[2] + col]) : 0.0f;
+                }
+            }
+    };
+    SeqStage<T, KD, BWD> st;
+    auto fetch = [&](long c) { st.load(p, q.b, q.t0 + c * kC, len_of(c), hk, (q.slot0 + c) * p.nh + hl); };
+    if (n > 0) {
+        fetch(chunk(0));
+        load_cols(chunk(0));
+        st.put(lds);
+    }
+    for (long i = 0; i < n; ++i) {
+        const long c = chunk(i), at = (q.slot0 + c) * p.nh + hl;
+        uint16_t *buf = lds + (Buf::kBufs == 2 ? (i & 1) * (Buf::kBytes / 2) : 0);
+        __syncthreads();
+        facc X[4];
+        float y0[16];
+#pragma unroll
+        for (int t = 0; t < 16; ++t) y0[t] = x0[t];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) X[t][j] = BWD ? x1[4 * t + j] : 0.0f;
+        if (i + 1 < n) {
+            fetch(chunk(i + 1));
+            load_cols(chunk(i + 1));
+        }
+        if (act) {
+            const Tile<NP, kC, KD> kt{buf}, qt{buf + Buf::kTile / 2};
+            uint16_t *rest = buf + (BWD ? 2 : 1) * (Buf::kTile / 2);
+            const uint4 *mm = reinterpret_cast<const uint4 *>(rest);
+            const float *gt = reinterpret_cast<const float *>(rest + kMWords * 8);
+            float *keep = (BWD ? p.d1 : p.s0) + at * KD * p.dvp + col;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) keep[(16 * t + 4 * g4 + j) * p.dvp] = S[t][j];
+            // Y = K S, then the right-hand side: V - gamma Y, or Z + Gam_last Y
+            facc Y[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) Y[t] = facc{0, 0, 0, 0};
+#pragma unroll
+            for (int ks = 0; ks < KD / 32; ++ks) {
+                bfrag b[3];
+                split_acc<3>(S[2 * ks], S[2 * ks + 1], b);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    bfrag a[NP];
+                    kt.rows(16 * t, 32 * ks, a);
+                    mma<NP, 3>(Y[t], a, b);
+                }
+            }
+            facc W[4];  // beta times it
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const facc ga = *reinterpret_cast<const facc *>(gt + 16 * t + 4 * g4), gl = *reinterpret_cast<const facc *>(gt + kC + 16 * t + 4 * g4),
+                           be = *reinterpret_cast<const facc *>(gt + 2 * kC + 16 * t + 4 * g4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    X[t][j] = BWD ? fmaf(gl[j], Y[t][j], X[t][j]) : fmaf(-ga[j], Y[t][j], y0[4 * t + j]);
+                    W[t][j] = be[j] * X[t][j];
+                }
+            }
+            // E = R - M (B R), or dR = dU - M^T (B dU)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                bfrag b[3];
+                split_acc<3>(W[2 * ks], W[2 * ks + 1], b);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    if (BWD ? ks < t / 2 : ks > t / 2) continue;
+                    const uint4 *f = mm + (BWD ? mt_frag(t, ks) : m_frag(t, ks)) * 3 * 64 + l;
+                    bfrag a[3];
+#pragma unroll
+                    for (int n3 = 0; n3 < 3; ++n3) {
+                        FragBits fb;
+                        fb.q = f[n3 * 64];
+                        a[n3] = fb.f;
+                    }
+                    mma<3, 3>(X[t], a, b);
+                }
+            }
+            float *ep = (BWD ? p.dr : p.e) + at * kC * p.dvp + col;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) ep[(16 * t + 4 * g4 + j) * p.dvp] = X[t][j];
+            facc W2[4];
+            const int len = len_of(c);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const facc ga = *reinterpret_cast<const facc *>(gt + 16 * t + 4 * g4), gl = *reinterpret_cast<const facc *>(gt + kC + 16 * t + 4 * g4),
+                           be = *reinterpret_cast<const facc *>(gt + 2 * kC + 16 * t + 4 * g4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float bx = be[j] * X[t][j];
+                    if constexpr (BWD) {
+                        const int row = 16 * t + 4 * g4 + j;
+                        if (live && row < len)
+                            store1(static_cast<T *>(p.dv) + ((q.b * p.tokens + q.t0 + c * kC + row) * p.h + head) * p.dv_ + col, bx);
+                        W[t][j] = -ga[j] * bx;
+                        W2[t][j] = p.scale * ga[j] * y0[4 * t + j];
+                    } else {
+                        W[t][j] = gl[j] * bx;
+                    }
+                }
+            }
+            const float last = gt[kC - 1];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) S[t][j] *= last;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                bfrag b[3], b2[3];
+                split_acc<3>(W[2 * ks], W[2 * ks + 1], b);
+                if constexpr (BWD) split_acc<3>(W2[2 * ks], W2[2 * ks + 1], b2);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    bfrag a[NP];
+                    kt.cols(32 * ks, 16 * t, a);
+                    mma<NP, 3>(S[t], a, b);
+                    if constexpr (BWD) {
+                        qt.cols(32 * ks, 16 * t, a);
+                        mma<NP, 3>(S[t], a, b2);
+                    }
+                }
+            }
+        }
+        if (i + 1 < n) {
+            if constexpr (Buf::kBufs == 1) __syncthreads();
+            st.put(lds + (Buf::kBufs == 2 ? ((i + 1) & 1) * (Buf::kBytes / 2) : 0));
+        }
+    }
+    float *out = BWD ? p.dh_init : p.h_last;
+    if (out && live) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int row = 16 * t + 4 * g4 + j;
+                if (row < p.dk_) out[state + static_cast<long>(row) * p.dv_ + col] = S[t][j];
+            }
+    }
+}
+
+// GRAD: workgroups of blockIdx.z = 1 run the adjoints' chain, at the same time.
+template <typename T, int KD, bool GRAD>
+__global__ __launch_bounds__(256, 1) void delta_seq(ChunkParams p)
+{
+    extern __shared__ __align__(16) uint16_t lds[];
+    if constexpr (GRAD) {
+        if (blockIdx.z == 1) {
+            seq_chain<T, KD, true>(p, lds);
+            return;
+        }
+    }
+    seq_chain<T, KD, false>(p, lds);
+}
+
+// ------------------------------------------------------------------ delta_out
+
+// O of one chunk and head: workgroup (slot, head), 32 columns at a time.
+template <typename T, int KD>
+struct OutLds {
+    static constexpr int NP = kParts<T>, NPO = sizeof(T) == 2 ? 2 : 3, VS = 32;
+    using KT = Tile<NP, kC, KD>;
+    using PT = Tile<NPO, kC, kC>;
+    using ST = Tile<NPO, KD, VS>;
+    using UT = Tile<NPO, kC, VS>;
+    // K is done with when the first slices come
+    static constexpr int kSlices = ST::kBytes + UT::kBytes, kShared = KT::kBytes > kSlices ? KT::kBytes : kSlices;
+    static constexpr int kBytes = KT::kBytes + PT::kBytes + kShared + kGates * 4;
+};
+
+template <typename T, int KD>
+__global__ __launch_bounds__(256) void delta_out(ChunkParams p)
+{
+    using L = OutLds<T, KD>;
+    constexpr int NP = L::NP, NPO = L::NPO, VS = L::VS;
+    extern __shared__ __align__(16) uint16_t lds[];
+    const long slot = blockIdx.x;
+    const Place c = find_chunk(p, slot);
+    if (c.len == 0) return;
+    const int hl = blockIdx.y, head = p.hk0 * p.rep + hl, hk = head / p.rep, wave = threadIdx.x / 64, l = threadIdx.x % 64;
+    const long at = slot * p.nh + hl;
+    const typename L::KT qt{lds}, kt{lds + L::KT::kBytes / 2 + L::PT::kBytes / 2};
+    const typename L::PT pt{lds + L::KT::kBytes / 2};
+    const typename L::ST st{kt.p};
+    const typename L::UT ut{kt.p + L::ST::kBytes / 2};
+    float *gt = reinterpret_cast<float *>(kt.p + L::kShared / 2);
+    {
+        Stage<T, KD, 256> a, b;
+        a.load(static_cast<const T *>(p.q) + c.b * p.qs[0] + c.t0 * p.qs[1] + hk * p.qs[2], p.qs[1], c.len, p.dk_, p.vec_qk);
+        b.load(static_cast<const T *>(p.k) + c.b * p.ks[0] + c.t0 * p.ks[1] + hk * p.ks[2], p.ks[1], c.len, p.dk_, p.vec_qk);
+        for (int i = threadIdx.x; i < kGates; i += 256) gt[i] = p.gates[at * kGates + i];
+        a.put(qt);
+        b.put(kt);
+    }
+    __syncthreads();
+    make_p<T, KD, NPO>(qt, kt, gt, p.scale, wave, pt);
+    const int i = 16 * wave + l % 16;
+    const float lead = p.scale * gt[i];
+    T *op = static_cast<T *>(p.o) + ((c.b * p.tokens + c.t0 + i) * p.h + head) * p.dv_;
+    for (int v0 = 0; v0 < p.dvp; v0 += VS) {
+        __syncthreads();
+        for (int w = threadIdx.x; w < KD * VS / 4; w += 256) {
+            const int row = w / (VS / 4), col = 4 * (w % (VS / 4));
+            const facc x = *reinterpret_cast<const facc *>(p.s0 + (at * KD + row) * p.dvp + v0 + col);
+            st.put4(row, col, x[0], x[1], x[2], x[3]);
+        }
+        for (int w = threadIdx.x; w < kC * VS / 4; w += 256) {
+            const int row = w / (VS / 4), col = 4 * (w % (VS / 4));
+            const facc x = *reinterpret_cast<const facc *>(p.e + (at * kC + row) * p.dvp + v0 + col);
+            const float b = gt[2 * kC + row];
+            ut.put4(row, col, b * x[0], b * x[1], b * x[2], b * x[3]);
+        }
+        __syncthreads();
+        // rows v, columns tokens i: four neighbouring v a lane
+        facc acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+        for (int ks = 0; ks < KD / 32; ++ks) {
+            bfrag b[NP];
+            qt.rows(16 * wave, 32 * ks, b);
+#pragma unroll
+            for (int vt = 0; vt < 2; ++vt) {
+                bfrag a[NPO];
+                st.cols(32 * ks, 16 * vt, a);
+                mma<NPO, NP>(acc[vt], a, b);
+            }
+        }
+#pragma unroll
+        for (int vt = 0; vt < 2; ++vt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[vt][j] *= lead;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            if (32 * ks > 16 * wave + 15) continue;  // j <= i
+            bfrag b[NPO];
+            pt.rows(16 * wave, 32 * ks, b);
+#pragma unroll
+            for (int vt = 0; vt < 2; ++vt) {
+                bfrag a[NPO];
+                ut.cols(32 * ks, 16 * vt, a);
+                mma<NPO, NPO>(acc[vt], a, b);
+            }
+        }
+        if (i < c.len) {
+#pragma unroll
+            for (int vt = 0; vt < 2; ++vt) {
+                const int v = v0 + 16 * vt + 4 * (l / 16);
+                if (p.vec_o && v + 4 <= p.dv_) {
+                    Raw<T, 4> r;
+                    float x[4] = {acc[vt][0], acc[vt][1], acc[vt][2], acc[vt][3]};
+                    r.set(x);
+                    r.store(op + v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (v + j < p.dv_) store1(op + v + j, acc[vt][j]);
+                }
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ delta_local
+
+// LDS of delta_local: slices of 32 columns first, then Q, K and the two
+// triangular matrices in the same place.
+template <typename T, int KD>
+struct LocalLds {
+    static constexpr int NP = kParts<T>, VS = 32;
+    using KT = Tile<NP, kC, KD>;
+    using PT = Tile<3, kC, kC>;
+    using OT = Tile<NP, kC, VS>;
+    using UT = Tile<3, kC, VS>;
+    using ST = Tile<3, KD, VS>;
+    static constexpr int kSlices = OT::kBytes + 2 * UT::kBytes + 2 * ST::kBytes, kAfter = 2 * KT::kBytes + 2 * PT::kBytes;
+    static constexpr int kMain = kSlices > kAfter ? kSlices : kAfter;
+    // gates, sums of dG and dbeta (a row a wave or half), sums over the chunk
+    static constexpr int kSums = kGates + 2 * kC + kC + 16;
+    static constexpr int kBytes = kMain + kSums * 4;
+};
+
+template <typename T, int KD>
+__global__ __launch_bounds__(512, 1) void delta_local(ChunkParams p)
+{
+    using L = LocalLds<T, KD>;
+    constexpr int NP = L::NP, VS = L::VS, NT = KD / 32;  // NT: tiles of 16 dims a wave
+    extern __shared__ __align__(16) uint16_t lds[];
+    const long slot = blockIdx.x;
+    const Place c = find_chunk(p, slot);
+    if (c.len == 0) return;
+    const int hk = p.hk0 + blockIdx.y, wave = threadIdx.x / 64, l = threadIdx.x % 64, g4 = l / 16;
+    const int rt = wave % 4, half = wave / 4, i = 16 * rt + l % 16;  // this wave's tokens; its half of the dims and of the columns j
+    const typename L::OT ot{lds};
+    const typename L::UT ut{lds + L::OT::kBytes / 2}, rt_{ut.p + L::UT::kBytes / 2};
+    const typename L::ST st{rt_.p + L::UT::kBytes / 2}, dt{st.p + L::ST::kBytes / 2};
+    const typename L::KT qt{lds}, kt{lds + L::KT::kBytes / 2};
+    const typename L::PT pt{lds + L::KT::kBytes}, nt{pt.p + L::PT::kBytes / 2};
+    float *gt = reinterpret_cast<float *>(lds + L::kMain / 2), *sg = gt + kGates, *sb = sg + 2 * kC, *sw = sb + kC;
+    facc dq[NT], dk[NT];  // rows 16 (half NT + t) + 4 g4 + r (dims), column i, over the heads of the group
+#pragma unroll
+    for (int t = 0; t < NT; ++t) dq[t] = dk[t] = facc{0, 0, 0, 0};
+    for (int r = 0; r < p.rep; ++r) {
+        const int hl = blockIdx.y * p.rep + r, head = hk * p.rep + r;
+        const long at = slot * p.nh + hl;
+        __syncthreads();
+        for (int w = threadIdx.x; w < kGates; w += 512) gt[w] = p.gates[at * kGates + w];
+        if (threadIdx.x < kC) sb[threadIdx.x] = 0.0f;
+        __syncthreads();
+        const T *op = static_cast<const T *>(p.dout) + c.b * p.os[0] + c.t0 * p.os[1] + head * p.os[2];
+        facc aq[NT], ar[NT], ac[NT], ap[2], an[2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) aq[t] = ar[t] = ac[t] = facc{0, 0, 0, 0};
+#pragma unroll
+        for (int t = 0; t < 2; ++t) ap[t] = an[t] = facc{0, 0, 0, 0};
+        float sd = 0.0f;  // <S0, D1>, this thread's part
+        for (int v0 = 0; v0 < p.dvp; v0 += VS) {
+            {
+                Stage<T, VS, 512> so;
+                so.load(op + v0, p.os[1], c.len, p.dv_ - v0, p.vec_do);
+                so.put(ot);
+            }
+            {   // 64 x 32: one piece a thread
+                const int row = threadIdx.x / 8, col = 4 * (threadIdx.x % 8);
+                const facc x = *reinterpret_cast<const facc *>(p.e + (at * kC + row) * p.dvp + v0 + col);
+                const facc y = *reinterpret_cast<const facc *>(p.dr + (at * kC + row) * p.dvp + v0 + col);
+                const float b = gt[2 * kC + row];
+                ut.put4(row, col, b * x[0], b * x[1], b * x[2], b * x[3]);
+                rt_.put4(row, col, y[0], y[1], y[2], y[3]);
+                const float dot = lane_sum<8>(x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3]);
+                if (threadIdx.x % 8 == 0) sb[row] += dot;
+            }
+#pragma unroll
+            for (int w = threadIdx.x; w < KD * VS / 4; w += 512) {
+                const int row = w / (VS / 4), col = 4 * (w % (VS / 4));
+                const facc x = *reinterpret_cast<const facc *>(p.s0 + (at * KD + row) * p.dvp + v0 + col);
+                const facc y = *reinterpret_cast<const facc *>(p.d1 + (at * KD + row) * p.dvp + v0 + col);
+                st.put4(row, col, x[0], x[1], x[2], x[3]);
+                dt.put4(row, col, y[0], y[1], y[2], y[3]);
+                sd += x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3];
+            }
+            __syncthreads();
+            bfrag fo[NP], fr[3], fu[3];
+            ot.rows(16 * rt, 0, fo);
+            rt_.rows(16 * rt, 0, fr);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int jt = 2 * half + t;
+                if (jt > rt) continue;
+                bfrag a[3];
+                ut.rows(16 * jt, 0, a);
+                mma<3, NP>(ap[t], a, fo);
+                mma<3, 3>(an[t], a, fr);
+            }
+            ut.rows(16 * rt, 0, fu);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                bfrag a[3];
+                st.rows(16 * (half * NT + t), 0, a);
+                mma<3, NP>(aq[t], a, fo);
+                mma<3, 3>(ar[t], a, fr);
+                dt.rows(16 * (half * NT + t), 0, a);
+                mma<3, 3>(ac[t], a, fu);
+            }
+            __syncthreads();
+        }
+        {   // rows' factors, and the triangular matrices into LDS
+            const float ga = gt[i], gl = gt[kC + i], be = gt[2 * kC + i];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    aq[t][j] *= p.scale * ga;
+                    ar[t][j] *= -ga * be;
+                    ac[t][j] *= gl;
+                }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int j0 = 16 * (2 * half + t) + 4 * g4;
+                float x[4], y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float f = j0 + j <= i ? gam(gt, i, j0 + j) : 0.0f;
+                    x[j] = j0 + j <= i ? p.scale * f * ap[t][j] : 0.0f;
+                    y[j] = j0 + j < i ? -be * f * an[t][j] : 0.0f;
+                }
+                pt.put4(i, j0, x[0], x[1], x[2], x[3]);
+                nt.put4(i, j0, y[0], y[1], y[2], y[3]);
+            }
+            Stage<T, KD, 512> a, b;
+            a.load(static_cast<const T *>(p.q) + c.b * p.qs[0] + c.t0 * p.qs[1] + hk * p.qs[2], p.qs[1], c.len, p.dk_, p.vec_qk);
+            b.load(static_cast<const T *>(p.k) + c.b * p.ks[0] + c.t0 * p.ks[1] + hk * p.ks[2], p.ks[1], c.len, p.dk_, p.vec_qk);
+            a.put(qt);
+            b.put(kt);
+        }
+        __syncthreads();
+        float end = 0.0f;  // sum over this lane's dims of k . (Gam_last U D1^T)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float x[4];
+            kt.get4(i, 16 * (half * NT + t) + 4 * g4, x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) end += x[j] * ac[t][j];
+        }
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            if (32 * ks <= 16 * rt + 15) {  // j <= i
+                bfrag fp[3], fn[3];
+                pt.rows(16 * rt, 32 * ks, fp);
+                nt.rows(16 * rt, 32 * ks, fn);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    bfrag a[NP];
+                    kt.cols(32 * ks, 16 * (half * NT + t), a);
+                    mma<NP, 3>(aq[t], a, fp);
+                    mma<NP, 3>(ar[t], a, fn);
+                }
+            }
+            if (32 * ks + 31 >= 16 * rt) {  // this wave's tokens as j, i >= j
+                bfrag fp[3], fn[3];
+                pt.cols(32 * ks, 16 * rt, fp);
+                nt.cols(32 * ks, 16 * rt, fn);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    bfrag a[NP];
+                    qt.cols(32 * ks, 16 * (half * NT + t), a);
+                    mma<NP, 3>(ac[t], a, fp);
+                    kt.cols(32 * ks, 16 * (half * NT + t), a);
+                    mma<NP, 3>(ac[t], a, fn);
+                }
+            }
+        }
+        float dg = 0.0f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float x[4], y[4];
+            qt.get4(i, 16 * (half * NT + t) + 4 * g4, x);
+            kt.get4(i, 16 * (half * NT + t) + 4 * g4, y);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                dg += x[j] * aq[t][j] + y[j] * (ar[t][j] - ac[t][j]);
+                dq[t][j] += aq[t][j];
+                dk[t][j] += ar[t][j] + ac[t][j];
+            }
+        }
+        dg += __shfl_xor(dg, 16, 64);
+        dg += __shfl_xor(dg, 32, 64);
+        if (g4 == 0) sg[half * kC + i] = dg;
+        end = lane_sum<64>(end);
+        sd = lane_sum<64>(sd);
+        if (l == 0) sw[wave] = end, sw[8 + wave] = sd;
+        __syncthreads();
+        if (threadIdx.x < kC) {
+            const int t = threadIdx.x;
+            float e = 0.0f, d = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) e += sw[w], d += sw[8 + w];
+            float s = sg[t] + sg[kC + t];
+#pragma unroll
+            for (int m = 1; m < 64; m *= 2) {
+                const float u = __shfl_down(s, m, 64);
+                if (t + m < 64) s += u;
+            }
+            if (t < c.len) {
+                const long out = (c.b * p.tokens + c.t0 + t) * p.h + head;
+                p.dg[out] = s + e + gt[kC - 1] * d;
+                p.dbeta[out] = sb[t];
+            }
+        }
+    }
+    if (i < c.len) {
+        const long row = ((c.b * p.tokens + c.t0 + i) * p.hk + hk) * p.dk_;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int d0 = 16 * (half * NT + t) + 4 * g4;
+            T *a = static_cast<T *>(p.dq) + row + d0, *b = static_cast<T *>(p.dk) + row + d0;
+            if (p.vec_dqk && d0 + 4 <= p.dk_) {
+                float x[4] = {dq[t][0], dq[t][1], dq[t][2], dq[t][3]}, y[4] = {dk[t][0], dk[t][1], dk[t][2], dk[t][3]};
+                Raw<T, 4> w;
+                w.set(x);
+                w.store(a);
+                w.set(y);
+                w.store(b);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (d0 + j < p.dk_) store1(a + j, dq[t][j]), store1(b + j, dk[t][j]);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+template <typename T>
+bool rows_aligned(const void *p, const long (&st)[3], int n)
+{
+    constexpr int N = 16 / static_cast<int>(sizeof(T));
+    return !off_by(p, 16) && n % N == 0 && st[0] % N == 0 && st[1] % N == 0 && st[2] % N == 0;
+}
+
+template <typename F>
+int big_lds(F *kernel, int bytes)
+{
+    if (bytes <= 64 * 1024) return SSM2D_OK;
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    return e == hipSuccess ? SSM2D_OK : hip_fail(e);
+}
+
+// Workspace of one pass at most (heads beyond it take another pass).
+constexpr double kMostBytes = 16.0 * (1u << 30);
+
+template <typename T, int KD, bool GRAD>
+int chunk_passes(const DeltaArgs &a)
+{
+    ChunkParams p{};
+    p.q = a.q, p.k = a.k, p.v = a.v, p.dout = a.dout, p.g = a.g, p.beta = a.beta, p.h_init = a.h_init, p.dh_last = a.dh_last, p.cu = a.cu;
+    p.o = a.o, p.dq = a.dq, p.dk = a.dk, p.dv = a.dv, p.h_last = a.h_last, p.dg = a.dg, p.dbeta = a.dbeta, p.dh_init = a.dh_init;
+    p.batch = a.batch, p.tokens = a.tokens, p.n_seq = a.n_seq;
+    p.chunks_b = (a.tokens + kC - 1) / kC;
+    p.slots = a.n_seq > 0 ? a.tokens / kC + a.n_seq : a.batch * p.chunks_b;
+    if (p.slots >= (1 << 22)) return SSM2D_ERR_UNSUPPORTED;  // (grids; far beyond memory but for tiny heads)
+    p.hk = a.hk, p.h = a.h, p.rep = a.h / a.hk, p.dk_ = a.dk_, p.dv_ = a.dv_, p.dvp = (a.dv_ + 31) / 32 * 32;
+    for (int i = 0; i < 3; ++i) {
+        p.qs[i] = a.qs[i], p.ks[i] = a.ks[i], p.vs[i] = a.vs[i], p.os[i] = a.os[i], p.gs[i] = a.gs[i], p.bs[i] = a.bs[i];
+    }
+    p.scale = a.scale;
+    p.vec_qk = rows_aligned<T>(a.q, a.qs, a.dk_) && rows_aligned<T>(a.k, a.ks, a.dk_);
+    p.vec_do = GRAD && rows_aligned<T>(a.dout, a.os, a.dv_);
+    p.vec_o = !GRAD && a.dv_ % 4 == 0 && !off_by(a.o, 4 * sizeof(T));
+    p.vec_dqk = GRAD && a.dk_ % 4 == 0 && !off_by(a.dq, 4 * sizeof(T)) && !off_by(a.dk, 4 * sizeof(T));
+    const long seqs = a.n_seq > 0 ? a.n_seq : a.batch;
+    // bytes of one head's chunks, in the order they are laid out
+    const size_t n = static_cast<size_t>(p.slots);
+    const size_t gates = n * kGates * 4, mm = n * kMWords * 16, st = n * KD * p.dvp * 4, row = n * kC * p.dvp * 4;
+    const size_t each = gates + (GRAD ? 2 : 1) * (mm + st + row) + (GRAD ? row : 0);
+    const int nhk = static_cast<int>(std::max(1.0, std::min<double>(a.hk, kMostBytes / (static_cast<double>(each) * p.rep))));
+    void *ws = nullptr;
+    int rc = get_aux_ws(a.dev, a.stream, kSlotDelta, each * p.rep * nhk, &ws);
+    if (rc != SSM2D_OK) return rc;
+    const hipStream_t s = static_cast<hipStream_t>(a.stream);
+    for (p.hk0 = 0; p.hk0 < a.hk; p.hk0 += nhk) {
+        p.nhk = std::min(nhk, a.hk - p.hk0);
+        p.nh = p.nhk * p.rep;
+        unsigned char *w = static_cast<unsigned char *>(ws);
+        auto take = [&](size_t bytes) {
+            unsigned char *at = w;
+            w += bytes * p.nh;
+            return at;
+        };
+        p.m = reinterpret_cast<uint4 *>(take(mm));
+        p.s0 = reinterpret_cast<float *>(take(st));
+        p.e = reinterpret_cast<float *>(take(row));
+        if (GRAD) {
+            p.mt = reinterpret_cast<uint4 *>(take(mm));
+            p.d1 = reinterpret_cast<float *>(take(st));
+            p.dr = reinterpret_cast<float *>(take(row));
+            p.z = reinterpret_cast<float *>(take(row));
+        }
+        p.gates = reinterpret_cast<float *>(take(gates));
+        const unsigned slots = static_cast<unsigned>(p.slots), nk = static_cast<unsigned>(p.nhk), nh = static_cast<unsigned>(p.nh);
+        delta_prep<T, KD, GRAD><<<dim3(slots, nk), dim3(256), 0, s>>>(p);
+        if ((rc = launched()) != SSM2D_OK) return rc;
+        if constexpr (GRAD) {
+            constexpr int kZ = 2 * Tile<kParts<T>, kC, KD>::kBytes + Tile<3, kC, kC>::kBytes + Tile<kParts<T>, kC, 32>::kBytes + kGates * 4;
+            if ((rc = big_lds(delta_z<T, KD>, kZ)) != SSM2D_OK) return rc;
+            delta_z<T, KD><<<dim3(slots, nh), dim3(256), kZ, s>>>(p);
+            if ((rc = launched()) != SSM2D_OK) return rc;
+        }
+        constexpr int kF = SeqBuf<T, KD, false>::kBufs * SeqBuf<T, KD, false>::kBytes, kB = SeqBuf<T, KD, true>::kBufs * SeqBuf<T, KD, true>::kBytes;
+        constexpr int kSeq = GRAD && kB > kF ? kB : kF;
+        if ((rc = big_lds(delta_seq<T, KD, GRAD>, kSeq)) != SSM2D_OK) return rc;
+        delta_seq<T, KD, GRAD><<<dim3(static_cast<unsigned>(seqs * p.nh), static_cast<unsigned>((p.dvp + 63) / 64), GRAD ? 2 : 1), dim3(256), kSeq, s>>>(p);
+        if ((rc = launched()) != SSM2D_OK) return rc;
+        if constexpr (GRAD) {
+            constexpr int kL = LocalLds<T, KD>::kBytes;
+            if ((rc = big_lds(delta_local<T, KD>, kL)) != SSM2D_OK) return rc;
+            delta_local<T, KD><<<dim3(slots, nk), dim3(512), kL, s>>>(p);
+        } else {
+            constexpr int kO = OutLds<T, KD>::kBytes;
+            if ((rc = big_lds(delta_out<T, KD>, kO)) != SSM2D_OK) return rc;
+            delta_out<T, KD><<<dim3(slots, nh), dim3(256), kO, s>>>(p);
+        }
+        if ((rc = launched()) != SSM2D_OK) return rc;
+    }
+    return SSM2D_OK;
+}
+
+template <typename T, bool GRAD>
+int chunk_kd(const DeltaArgs &a)
+{
+    if (a.dk_ <= 32) return chunk_passes<T, 32, GRAD>(a);
+    if (a.dk_ <= 64) return chunk_passes<T, 64, GRAD>(a);
+    return chunk_passes<T, 128, GRAD>(a);
+}
+
+}  // namespace ssm2d_impl

@@ -8,6 +8,7 @@ the HIP stream to libssm2d.so; every operator runs in the library's kernels.
     g = layer_norm_bwd(x, weight, mean, rstd, dy)       # dict: dx, dweight, dbias
     q, k = rope_fwd(q, k, positions, inv_freq, sections)
     o = gated_delta_fwd(q, k, v, g, beta)               # sequences, packed with cu_seqlens=...
+    g = gated_delta_bwd(q, k, v, g, beta, do)           # dict: dq, dk, dv, dg, dbeta, dh_init
     o = gated_delta_step(q, k, v, g, beta, state)       # one token, state updated in place
 
 x, q, k, v and gradients of them: float32 or bfloat16; weights, statistics, g,
@@ -25,7 +26,7 @@ import torch
 
 from . import ERR_HIP, OK, Ssm2dError, load_library
 
-__all__ = ["layer_norm_fwd", "layer_norm_bwd", "rope_fwd", "rope_bwd", "gated_delta_fwd", "gated_delta_step"]
+__all__ = ["layer_norm_fwd", "layer_norm_bwd", "rope_fwd", "rope_bwd", "gated_delta_fwd", "gated_delta_bwd", "gated_delta_step"]
 
 LN_MAX_N, ROPE_MAX_AXES, ROPE_MAX_D, DELTA_MAX_DK, DELTA_MAX_DV = 16384, 4, 1024, 128, 1024
 ROPE_INTERLEAVED, ROPE_INVERSE = 1, 2
@@ -49,6 +50,7 @@ _SIGNATURES = {
     "ssm2d_layer_norm_bwd": [_vp] * 8 + [_i64] * 7 + [_vp],
     "ssm2d_rope": [_vp] * 6 + [ctypes.POINTER(_RopeShape), ctypes.c_uint32, _vp],
     "ssm2d_gated_delta_fwd": [_vp] * 9 + [ctypes.POINTER(_DeltaShape), ctypes.c_float, _vp],
+    "ssm2d_gated_delta_bwd": [_vp] * 15 + [ctypes.POINTER(_DeltaShape), ctypes.c_float, _vp],
     "ssm2d_gated_delta_step": [_vp] * 7 + [ctypes.POINTER(_DeltaShape), ctypes.c_float, _vp],
 }
 _bound = {}
@@ -291,6 +293,25 @@ def gated_delta_fwd(q, k, v, g, beta, *, scale=None, h_init=None, cu_seqlens=Non
     _run(fn, dev, stream, (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(h_init), _ptr(cu_seqlens),
                            o.data_ptr(), _ptr(h_last), shape, q.shape[3] ** -0.5 if scale is None else float(scale)))
     return (o, h_last) if return_last_state else o
+
+
+def gated_delta_bwd(q, k, v, g, beta, do, *, scale=None, h_init=None, dh_last=None, cu_seqlens=None, out=None, stream=None):
+    """Gradients of gated_delta_fwd for do = dL/do and dh_last = dL/dh_last
+    (None: zeros): a dict dq, dk, dv (their inputs' dtype), dg, dbeta (float32),
+    and dh_init when h_init or dh_last is given. ``out`` may supply any of them."""
+    fn = _entry("ssm2d_gated_delta_bwd", q.dtype)
+    dev, seqs, shape = _delta_check(q, k, v, g, beta, cu_seqlens, do)
+    states = (seqs, v.shape[2], q.shape[3], v.shape[3])
+    _on_gpu(dev, h_init=h_init, dh_last=dh_last)
+    _f32(states, h_init=h_init, dh_last=dh_last)
+    out = out or {}
+    r = {n: _out(n, out.get(n), t.shape, t.dtype, dev, stream) for n, t in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta))}
+    if h_init is not None or dh_last is not None:
+        r["dh_init"] = _out("dh_init", out.get("dh_init"), states, torch.float32, dev, stream)
+    _run(fn, dev, stream, (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(h_init), _ptr(cu_seqlens),
+                           do.data_ptr(), _ptr(dh_last), *(r[n].data_ptr() for n in ("dq", "dk", "dv", "dg", "dbeta")), _ptr(r.get("dh_init")),
+                           shape, q.shape[3] ** -0.5 if scale is None else float(scale)))
+    return r
 
 
 def gated_delta_step(q, k, v, g, beta, state, *, scale=None, o=None, stream=None):
