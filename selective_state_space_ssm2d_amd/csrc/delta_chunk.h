@@ -44,6 +44,8 @@ namespace ssm2d_impl {
 
 constexpr int kC = 64;  // tokens a chunk
 
+using word4 = unsigned __attribute__((ext_vector_type(4)));  // (a register value; the uint4 struct is copied through memory)
+
 struct ChunkParams {
     const void *q, *k, *v, *dout;
     const float *g, *beta, *h_init, *dh_last;
@@ -52,9 +54,14 @@ struct ChunkParams {
     float *h_last, *dg, *dbeta, *dh_init;
     // workspace, by [slot][head of this pass]
     float *gates;                       // [5][kC]: gamma, Gam_last, beta, G and its rounding error
-    uint4 *m, *mt;                      // -M, -M^T: 6 fragments x 3 parts
+    word4 *m, *mt;                      // -M, -M^T: 6 fragments x 3 parts
     float *s0, *d1;                     // [KD][dvp]
     float *e, *dr, *z;                  // [kC][dvp]
+    // by [sequence][head of this pass][segment]: a segment's transition
+    // [KD][KD], its state from zero and then its first state (forward and
+    // adjoint) [KD][dvp]
+    float *seg_a, *seg_s, *seg_d;
+    int nseg, seg_len;                  // segments of the longest sequence, chunks a segment
     long batch, tokens, n_seq, slots, chunks_b;  // chunks_b: chunks of a batch entry
     int hk, h, rep, dk_, dv_, dvp;
     int hk0, nhk, nh;                   // this pass: key heads hk0 .. hk0 + nhk - 1, nh = nhk * rep heads
@@ -135,7 +142,7 @@ __device__ __forceinline__ void split2(float a, float b, unsigned (&w)[N])
 union FragBits {
     bfrag f;
     unsigned w[4];
-    uint4 q;
+    word4 q;
     half4 h[2];
 };
 
@@ -170,6 +177,32 @@ __device__ __forceinline__ void mma(facc &acc, const bfrag (&a)[NA], const bfrag
             const int j = s - i;
             if (j >= 0 && j < NB) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc, 0, 0, 0);
         }
+}
+
+// acc[t] += a[t] b for all t, the same terms: one term of every t before the
+// next, so that no product waits for the one before it.
+template <int NA, int NB, int NT>
+__device__ __forceinline__ void mma_each(facc (&acc)[NT], const bfrag (&a)[NT][NA], const bfrag (&b)[NB])
+{
+    constexpr int kMax = NA > NB ? NA : NB;
+#pragma unroll
+    for (int s = kMax - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            const int j = s - i;
+            if (j < 0 || j >= NB) continue;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[t][i], b[j], acc[t], 0, 0, 0);
+        }
+}
+
+// A workgroup barrier for what goes through LDS alone: unlike __syncthreads it
+// does not wait for global loads and stores still in flight.
+__device__ __forceinline__ void lds_barrier()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 // A tile in LDS: NP parts of [ROWS][COLS] bf16, rows padded by 16 bytes (the
@@ -231,51 +264,58 @@ constexpr int kParts = sizeof(T) == 2 ? 1 : 3;  // parts of an input
 
 // ------------------------------------------------------------------ staging
 
-// 16 bytes of row t (of `len`) of a tensor whose rows hold n elements.
-template <typename T>
-__device__ __forceinline__ void load_piece(Raw<T, 16 / static_cast<int>(sizeof(T))> &r, const T *row, int c, int n, bool live, bool vec)
-{
-    constexpr int N = 16 / static_cast<int>(sizeof(T));
-    if (!live || c >= n) {
-        r.clear();
-    } else if (vec) {
-        r.load(row + c);
-    } else {
-        float x[N];
-#pragma unroll
-        for (int j = 0; j < N; ++j) x[j] = c + j < n ? widen1(row[c + j]) : 0.0f;
-        r.set(x);
-    }
-}
-
-template <typename T, int COLS>
-__device__ __forceinline__ void put_piece(const Tile<kParts<T>, kC, COLS> &t, int r, int c, const Raw<T, 16 / static_cast<int>(sizeof(T))> &x)
-{
-    if constexpr (sizeof(T) == 2) *reinterpret_cast<uint4 *>(t.p + r * t.kLd + c) = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
-    else t.put4(r, c, x.get(0), x.get(1), x.get(2), x.get(3));
-}
-
-// A chunk's rows of q or k (COLS wide, zeros past n and past the chunk): read
-// to registers, then put into LDS.
+// A chunk's rows of q, k or dO (COLS wide, zeros past n and past the chunk):
+// read to registers, later put into LDS. Places outside are read at the nearest
+// one inside (len >= 1, n >= 1) and cleared when they are put: anything that
+// looks at a load's result right after it would wait for it there.
 template <typename T, int COLS, int THREADS>
 struct Stage {
     static constexpr int N = 16 / static_cast<int>(sizeof(T)), kRow = COLS / N, kAll = kC * kRow, kEach = (kAll + THREADS - 1) / THREADS;
-    Raw<T, N> r[kEach];
-    __device__ __forceinline__ void load(const T *base, long stride, int len, int n, bool vec)
+    word4 r[kEach];
+    int len, n;
+    __device__ __forceinline__ void load(const T *base, long stride, int len_, int n_, bool vec)
     {
+        len = len_, n = n_;
+        if (vec) {  // (n is a multiple of N)
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const int at = i * THREADS + threadIdx.x;
-            const int row = at / kRow, c = (at % kRow) * N;
-            load_piece<T>(r[i], base + row * stride, c, n, at < kAll && row < len, vec);
+            for (int i = 0; i < kEach; ++i) {
+                const int at = i * THREADS + threadIdx.x, row = at / kRow, c = (at % kRow) * N;
+                r[i] = *reinterpret_cast<const word4 *>(base + min(row, len - 1) * stride + min(c, n - N));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const int at = i * THREADS + threadIdx.x, row = at / kRow, c = (at % kRow) * N;
+                r[i] = gather(base + min(row, len - 1) * stride, c, n);
+            }
         }
+    }
+    // 16 bytes element by element; past n: the last element
+    static __device__ __forceinline__ word4 gather(const T *src, int c, int n)
+    {
+        unsigned w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (sizeof(T) == 2) w[j] = src[min(c + 2 * j, n - 1)] | (static_cast<unsigned>(src[min(c + 2 * j + 1, n - 1)]) << 16);
+            else w[j] = __float_as_uint(src[min(c + j, n - 1)]);
+        }
+        return word4{w[0], w[1], w[2], w[3]};
     }
     __device__ __forceinline__ void put(const Tile<kParts<T>, kC, COLS> &t) const
     {
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            const int at = i * THREADS + threadIdx.x;
-            if (kAll % THREADS == 0 || at < kAll) put_piece<T, COLS>(t, at / kRow, (at % kRow) * N, r[i]);
+            const int at = i * THREADS + threadIdx.x, row = at / kRow, c = (at % kRow) * N;
+            if (kAll % THREADS != 0 && at >= kAll) continue;
+            const int left = row < len ? n - c : 0;  // elements that are inside
+            unsigned w[4] = {r[i][0], r[i][1], r[i][2], r[i][3]};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (sizeof(T) == 2) w[j] = left > 2 * j + 1 ? w[j] : (left > 2 * j ? w[j] & 0xffffu : 0u);
+                else w[j] = left > j ? w[j] : 0u;
+            }
+            if constexpr (sizeof(T) == 2) *reinterpret_cast<word4 *>(t.p + row * t.kLd + c) = word4{w[0], w[1], w[2], w[3]};
+            else t.put4(row, c, __uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2]), __uint_as_float(w[3]));
         }
     }
 };
@@ -317,7 +357,7 @@ __device__ __forceinline__ float gam(const float *gt, int i, int j)
 
 constexpr int kGates = 5 * kC;
 constexpr int kMFrags = 6;             // fragments of M that are not zero
-constexpr int kMWords = kMFrags * 3 * 64;  // uint4 of one head's M
+constexpr int kMWords = kMFrags * 3 * 64;  // word4 of one head's M
 // fragment of M for rows 16 rt .., columns 32 ks .. (ks <= rt / 2)
 __host__ __device__ constexpr int m_frag(int rt, int ks) { return rt < 2 ? rt : 2 * rt - 2 + ks; }
 // fragment of M^T for rows 16 rt .., columns 32 ks .. (ks >= rt / 2)
@@ -456,9 +496,9 @@ __global__ __launch_bounds__(256) void delta_prep(ChunkParams p)
             unsigned w[4][3];
 #pragma unroll
             for (int j = 0; j < 4; ++j) split2<3>(x[2 * j], x[2 * j + 1], w[j]);
-            uint4 *out = (tr ? p.mt : p.m) + at * kMWords + n * 3 * 64 + l;
+            word4 *out = (tr ? p.mt : p.m) + at * kMWords + n * 3 * 64 + l;
 #pragma unroll
-            for (int q = 0; q < 3; ++q) out[q * 64] = make_uint4(w[0][q], w[1][q], w[2][q], w[3][q]);
+            for (int q = 0; q < 3; ++q) out[q * 64] = word4{w[0][q], w[1][q], w[2][q], w[3][q]};
         }
     }
 }
@@ -565,19 +605,19 @@ struct SeqBuf {
 template <typename T, int KD, bool BWD>
 struct SeqStage {
     Stage<T, KD, 256> k, q;
-    uint4 m[(kMWords + 255) / 256];
+    word4 m[(kMWords + 255) / 256];
     float g;
     __device__ __forceinline__ void load(const ChunkParams &p, long b, long t0, int len, int hk, long at)
     {
         k.load(static_cast<const T *>(p.k) + b * p.ks[0] + t0 * p.ks[1] + hk * p.ks[2], p.ks[1], len, p.dk_, p.vec_qk);
         if constexpr (BWD) q.load(static_cast<const T *>(p.q) + b * p.qs[0] + t0 * p.qs[1] + hk * p.qs[2], p.qs[1], len, p.dk_, p.vec_qk);
-        const uint4 *src = (BWD ? p.mt : p.m) + at * kMWords;
+        const word4 *src = (BWD ? p.mt : p.m) + at * kMWords;
 #pragma unroll
         for (int i = 0; i < (kMWords + 255) / 256; ++i) {
             const int w = i * 256 + threadIdx.x;
-            m[i] = w < kMWords ? src[w] : make_uint4(0, 0, 0, 0);
+            m[i] = src[min(w, kMWords - 1)];
         }
-        g = threadIdx.x < 3 * kC ? p.gates[at * kGates + threadIdx.x] : 0.0f;
+        g = p.gates[at * kGates + min(static_cast<int>(threadIdx.x), 3 * kC - 1)];
     }
     __device__ __forceinline__ void put(uint16_t *lds) const
     {
@@ -585,7 +625,7 @@ struct SeqStage {
         k.put(Tile<kParts<T>, kC, KD>{lds});
         if constexpr (BWD) q.put(Tile<kParts<T>, kC, KD>{lds + kTile});
         uint16_t *rest = lds + (BWD ? 2 : 1) * kTile;
-        uint4 *mm = reinterpret_cast<uint4 *>(rest);
+        word4 *mm = reinterpret_cast<word4 *>(rest);
 #pragma unroll
         for (int i = 0; i < (kMWords + 255) / 256; ++i) {
             const int w = i * 256 + threadIdx.x;
@@ -598,154 +638,193 @@ struct SeqStage {
 // The chain over a sequence's chunks for 16 columns of the state a wave (64 a
 // workgroup). Columns are independent, so waves only share what they read.
 // The state [KD][16] stays in accumulators, from which it is cut into operands.
-template <typename T, int KD, bool BWD>
+//
+// A sequence whose chain would leave most of the chip idle is cut into
+// segments: the chain is linear in its first state, S_end = A S_start + b, so
+// PROBE runs every segment from zero (b) and, in the forward, with KD more
+// columns from the unit matrix and v = 0 (A); delta_join goes over the
+// segments; then they run at once from their true first states. The adjoint's
+// transition is A^T.
+template <typename T, int KD, bool BWD, bool PROBE>
 __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
 {
     constexpr int NP = kParts<T>, NT = KD / 16;
     using Buf = SeqBuf<T, KD, BWD>;
-    const int wave = threadIdx.x / 64, l = threadIdx.x % 64, g4 = l / 16, l16 = l % 16;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64, g4 = l / 16, l16 = l % 16;
     const long s = blockIdx.x / p.nh;
     const int hl = static_cast<int>(blockIdx.x - s * p.nh), head = p.hk0 * p.rep + hl, hk = head / p.rep;
-    const int v0 = blockIdx.y * 64 + wave * 16;
-    const bool act = v0 < p.dvp;      // this wave has columns
-    const int col = v0 + l16;
-    const bool live = col < p.dv_;    // this lane's column is not padding
+    const int seg = blockIdx.z % p.nseg;
     const Seq q = find_seq(p, s);
-    const long n = (q.len + kC - 1) / kC;
+    const long n_all = (q.len + kC - 1) / kC;
+    const int ns = n_all > 0 ? static_cast<int>((n_all + p.seg_len - 1) / p.seg_len) : 1;  // of this sequence
+    if (seg >= ns || (PROBE && ns == 1)) return;
+    const long c0 = static_cast<long>(seg) * p.seg_len, c1 = min(n_all, c0 + p.seg_len), n = c1 - c0;
+    int v0 = blockIdx.y * 64 + wave * 16;
+    const bool unit = PROBE && !BWD && v0 >= p.dvp;  // this wave's columns are the unit matrix's
+    if (unit) v0 -= p.dvp;
+    const bool act = v0 < (unit ? KD : p.dvp);  // this wave has columns
+    if (PROBE && BWD && static_cast<int>(blockIdx.y) * 64 >= p.dvp) return;
+    const int col = v0 + l16;
+    const bool live = !unit && col < p.dv_;  // this lane's column is not padding
+    const int colv = min(col, p.dv_ - 1);  // (where lanes without a column read)
+    const unsigned lane_at = 4 * g4 * p.dvp + l16;  // of this lane's first row and column in a [..][dvp] matrix
     const long state = ((s * p.h + head) * p.dk_) * p.dv_;
     const float *init = BWD ? p.dh_last : p.h_init;
+    const long segs = (static_cast<long>(blockIdx.x) * p.nseg + seg) * KD;
+    float *joined = (BWD ? p.seg_d : p.seg_s) + segs * p.dvp + v0;
     facc S[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int row = 16 * t + 4 * g4 + j;
-            S[t][j] = (init && live && row < p.dk_) ? init[state + static_cast<long>(row) * p.dv_ + col] : 0.0f;
+            if constexpr (PROBE) {
+                S[t][j] = (unit && row == col) ? 1.0f : 0.0f;
+            } else if (p.nseg > 1) {
+                S[t][j] = act ? (joined + (16 * t + j) * p.dvp)[lane_at] : 0.0f;
+            } else {
+                S[t][j] = init ? init[state + static_cast<long>(min(row, p.dk_ - 1)) * p.dv_ + colv] : 0.0f;
+                S[t][j] = (live && row < p.dk_) ? S[t][j] : 0.0f;
+            }
         }
     auto len_of = [&](long c) { return static_cast<int>(q.len - c * kC < kC ? q.len - c * kC : kC); };
-    auto chunk = [&](long i) { return BWD ? n - 1 - i : i; };
+    auto chunk = [&](long i) { return BWD ? c1 - 1 - i : c0 + i; };
     // a column of the chunk's rows of v (dO and Z in the backward), 16 tokens a lane
-    float x0[16], x1[16];
-    auto load_cols = [&](long c) {
+    T x0[16];
+    float x1[16];
+    auto load_cols = [&](long c) __attribute__((always_inline)) {
         const int len = len_of(c);
-        const long at = ((q.slot0 + c) * p.nh + hl);
+        const T *src = BWD ? static_cast<const T *>(p.dout) + q.b * p.os[0] + (q.t0 + c * kC) * p.os[1] + head * p.os[2] + colv
+                           : static_cast<const T *>(p.v) + q.b * p.vs[0] + (q.t0 + c * kC) * p.vs[1] + head * p.vs[2] + colv;
+        const long step = BWD ? p.os[1] : p.vs[1];
+        if (len == kC) {
+            const T *lane = src + 4 * g4 * step;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int row = 16 * t + 4 * g4 + j;
-                const bool ok = live && row < len;
-                if constexpr (BWD) {
-                    x0[4 * t + j] = ok ? widen1(static_cast<const T *>(p.dout)[q.b * p.os[0] + (q.t0 + c * kC + row) * p.os[1] + head * p.os[2] + col]) : 0.0f;
-                    x1[4 * t + j] = act ? p.z[(at * kC + row) * p.dvp + col] : 0.0f;
-                } else {
-                    x0[4 * t + j] = ok ? widen1(static_cast<const T *>(p.v)[q.b * p.vs[0] + (q.t0 + c * kC + row) * p.vs[1] + head * p.vs[2] + col]) : 0.0f;
-                }
-            }
+                for (int j = 0; j < 4; ++j) x0[4 * t + j] = lane[(16 * t + j) * step];
+        } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x0[4 * t + j] = src[min(16 * t + 4 * g4 + j, len - 1) * step];
+        }
+        if constexpr (BWD) {
+            const float *z = p.z + ((q.slot0 + c) * p.nh + hl) * kC * p.dvp + (act && !unit ? v0 : 0);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x1[4 * t + j] = (z + (16 * t + j) * p.dvp)[lane_at];
+        }
     };
     SeqStage<T, KD, BWD> st;
-    auto fetch = [&](long c) { st.load(p, q.b, q.t0 + c * kC, len_of(c), hk, (q.slot0 + c) * p.nh + hl); };
+    auto fetch = [&](long c) __attribute__((always_inline)) { st.load(p, q.b, q.t0 + c * kC, len_of(c), hk, (q.slot0 + c) * p.nh + hl); };
+    float y0[16], y1[16];  // the step's rows of v (dO and Z)
+    auto take_cols = [&](long c) __attribute__((always_inline)) {
+        const int len = len_of(c);
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            y0[t] = (live && 16 * (t / 4) + 4 * g4 + t % 4 < len) ? widen1(x0[t]) : 0.0f;
+            asm volatile("" : "+v"(y0[t]));  // (here, and not where it is used)
+            if constexpr (BWD) {
+                y1[t] = x1[t];
+                asm volatile("" : "+v"(y1[t]));
+            }
+        }
+    };
+    auto keep_state = [&](long c) __attribute__((always_inline)) {
+        float *keep = (BWD ? p.d1 : p.s0) + ((q.slot0 + c) * p.nh + hl) * KD * p.dvp + v0;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) (keep + (16 * t + j) * p.dvp)[lane_at] = S[t][j];
+    };
     if (n > 0) {
         fetch(chunk(0));
         load_cols(chunk(0));
         st.put(lds);
+        take_cols(chunk(0));
+        if (!PROBE && act) keep_state(chunk(0));
     }
+    // One step: read the next chunk, compute this one, put what was read, store
+    // this one's results. The stores come last: loads and stores share one
+    // counter, so a wait for a load would also wait for the stores before it,
+    // and these get a whole step to finish.
     for (long i = 0; i < n; ++i) {
         const long c = chunk(i), at = (q.slot0 + c) * p.nh + hl;
         uint16_t *buf = lds + (Buf::kBufs == 2 ? (i & 1) * (Buf::kBytes / 2) : 0);
-        __syncthreads();
-        facc X[4];
-        float y0[16];
-#pragma unroll
-        for (int t = 0; t < 16; ++t) y0[t] = x0[t];
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) X[t][j] = BWD ? x1[4 * t + j] : 0.0f;
+        lds_barrier();
         if (i + 1 < n) {
             fetch(chunk(i + 1));
             load_cols(chunk(i + 1));
         }
+        facc X[4];
+        float o0[16];
         if (act) {
             const Tile<NP, kC, KD> kt{buf}, qt{buf + Buf::kTile / 2};
             uint16_t *rest = buf + (BWD ? 2 : 1) * (Buf::kTile / 2);
-            const uint4 *mm = reinterpret_cast<const uint4 *>(rest);
+            const word4 *mm = reinterpret_cast<const word4 *>(rest);
             const float *gt = reinterpret_cast<const float *>(rest + kMWords * 8);
-            float *keep = (BWD ? p.d1 : p.s0) + at * KD * p.dvp + col;
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) keep[(16 * t + 4 * g4 + j) * p.dvp] = S[t][j];
             // Y = K S, then the right-hand side: V - gamma Y, or Z + Gam_last Y
             facc Y[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) Y[t] = facc{0, 0, 0, 0};
 #pragma unroll
             for (int ks = 0; ks < KD / 32; ++ks) {
-                bfrag b[3];
-                split_acc<3>(S[2 * ks], S[2 * ks + 1], b);
+                bfrag b[3], a[4][NP];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    bfrag a[NP];
-                    kt.rows(16 * t, 32 * ks, a);
-                    mma<NP, 3>(Y[t], a, b);
-                }
+                for (int t = 0; t < 4; ++t) kt.rows(16 * t, 32 * ks, a[t]);
+                split_acc<3>(S[2 * ks], S[2 * ks + 1], b);
+                mma_each<NP, 3, 4>(Y, a, b);
             }
-            facc W[4];  // beta times it
+            facc ga[4], gl[4], be[4], W[4];  // W: beta times the right-hand side
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const facc ga = *reinterpret_cast<const facc *>(gt + 16 * t + 4 * g4), gl = *reinterpret_cast<const facc *>(gt + kC + 16 * t + 4 * g4),
-                           be = *reinterpret_cast<const facc *>(gt + 2 * kC + 16 * t + 4 * g4);
+                ga[t] = *reinterpret_cast<const facc *>(gt + 16 * t + 4 * g4);
+                gl[t] = *reinterpret_cast<const facc *>(gt + kC + 16 * t + 4 * g4);
+                be[t] = *reinterpret_cast<const facc *>(gt + 2 * kC + 16 * t + 4 * g4);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    X[t][j] = BWD ? fmaf(gl[j], Y[t][j], X[t][j]) : fmaf(-ga[j], Y[t][j], y0[4 * t + j]);
-                    W[t][j] = be[j] * X[t][j];
+                    X[t][j] = BWD ? fmaf(gl[t][j], Y[t][j], y1[4 * t + j]) : fmaf(-ga[t][j], Y[t][j], y0[4 * t + j]);
+                    W[t][j] = be[t][j] * X[t][j];
                 }
             }
             // E = R - M (B R), or dR = dU - M^T (B dU)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                bfrag b[3];
+                bfrag b[3], a[4][3];
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    if (BWD ? ks >= t / 2 : ks <= t / 2)
+#pragma unroll
+                        for (int n3 = 0; n3 < 3; ++n3) {
+                            FragBits fb;
+                            fb.q = mm[((BWD ? mt_frag(t, ks) : m_frag(t, ks)) * 3 + n3) * 64 + l];
+                            a[t][n3] = fb.f;
+                        }
                 split_acc<3>(W[2 * ks], W[2 * ks + 1], b);
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    if (BWD ? ks < t / 2 : ks > t / 2) continue;
-                    const uint4 *f = mm + (BWD ? mt_frag(t, ks) : m_frag(t, ks)) * 3 * 64 + l;
-                    bfrag a[3];
+                for (int sum = 2; sum >= 0; --sum)
 #pragma unroll
-                    for (int n3 = 0; n3 < 3; ++n3) {
-                        FragBits fb;
-                        fb.q = f[n3 * 64];
-                        a[n3] = fb.f;
-                    }
-                    mma<3, 3>(X[t], a, b);
-                }
+                    for (int u = 0; u <= sum; ++u)
+#pragma unroll
+                        for (int t = 0; t < 4; ++t)
+                            if (BWD ? ks >= t / 2 : ks <= t / 2) X[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[t][u], b[sum - u], X[t], 0, 0, 0);
             }
-            float *ep = (BWD ? p.dr : p.e) + at * kC * p.dvp + col;
+            facc W2[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) ep[(16 * t + 4 * g4 + j) * p.dvp] = X[t][j];
-            facc W2[4];
-            const int len = len_of(c);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const facc ga = *reinterpret_cast<const facc *>(gt + 16 * t + 4 * g4), gl = *reinterpret_cast<const facc *>(gt + kC + 16 * t + 4 * g4),
-                           be = *reinterpret_cast<const facc *>(gt + 2 * kC + 16 * t + 4 * g4);
-#pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float bx = be[j] * X[t][j];
+                    const float bx = be[t][j] * X[t][j];
                     if constexpr (BWD) {
-                        const int row = 16 * t + 4 * g4 + j;
-                        if (live && row < len)
-                            store1(static_cast<T *>(p.dv) + ((q.b * p.tokens + q.t0 + c * kC + row) * p.h + head) * p.dv_ + col, bx);
-                        W[t][j] = -ga[j] * bx;
-                        W2[t][j] = p.scale * ga[j] * y0[4 * t + j];
+                        o0[4 * t + j] = bx;
+                        W[t][j] = -ga[t][j] * bx;
+                        W2[t][j] = p.scale * ga[t][j] * y0[4 * t + j];
                     } else {
-                        W[t][j] = gl[j] * bx;
+                        W[t][j] = gl[t][j] * bx;
                     }
                 }
-            }
             const float last = gt[kC - 1];
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -753,28 +832,62 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
                 for (int j = 0; j < 4; ++j) S[t][j] *= last;
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                bfrag b[3], b2[3];
-                split_acc<3>(W[2 * ks], W[2 * ks + 1], b);
-                if constexpr (BWD) split_acc<3>(W2[2 * ks], W2[2 * ks + 1], b2);
+                bfrag b[3], a[NT][NP];
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    bfrag a[NP];
-                    kt.cols(32 * ks, 16 * t, a);
-                    mma<NP, 3>(S[t], a, b);
-                    if constexpr (BWD) {
-                        qt.cols(32 * ks, 16 * t, a);
-                        mma<NP, 3>(S[t], a, b2);
-                    }
+                for (int t = 0; t < NT; ++t) kt.cols(32 * ks, 16 * t, a[t]);
+                split_acc<3>(W[2 * ks], W[2 * ks + 1], b);
+                mma_each<NP, 3, NT>(S, a, b);
+                if constexpr (BWD) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) qt.cols(32 * ks, 16 * t, a[t]);
+                    split_acc<3>(W2[2 * ks], W2[2 * ks + 1], b);
+                    mma_each<NP, 3, NT>(S, a, b);
                 }
             }
         }
         if (i + 1 < n) {
-            if constexpr (Buf::kBufs == 1) __syncthreads();
+            if constexpr (Buf::kBufs == 1) lds_barrier();
             st.put(lds + (Buf::kBufs == 2 ? ((i + 1) & 1) * (Buf::kBytes / 2) : 0));
+            take_cols(chunk(i + 1));
+        }
+        asm volatile("" ::: "memory");  // (no store goes up past the waits above)
+        if (!PROBE && act) {
+            float *ep = (BWD ? p.dr : p.e) + at * kC * p.dvp + v0;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) (ep + (16 * t + j) * p.dvp)[lane_at] = X[t][j];
+            if (i + 1 < n) keep_state(chunk(i + 1));
+            if constexpr (BWD) {
+                const int len = len_of(c);
+                const long step = static_cast<long>(p.h) * p.dv_;
+                T *dvo = static_cast<T *>(p.dv) + ((q.b * p.tokens + q.t0 + c * kC) * p.h + head) * p.dv_ + 4 * g4 * step + col;
+                if (live) {
+                    if (len == kC) {
+#pragma unroll
+                        for (int t = 0; t < 16; ++t) store1(dvo + (16 * (t / 4) + t % 4) * step, o0[t]);
+                    } else {
+#pragma unroll
+                        for (int t = 0; t < 16; ++t)
+                            if (16 * (t / 4) + 4 * g4 + t % 4 < len) store1(dvo + (16 * (t / 4) + t % 4) * step, o0[t]);
+                    }
+                }
+            }
         }
     }
+    if constexpr (PROBE) {
+        if (!act) return;
+        float *end = unit ? p.seg_a + segs * KD + v0 : joined;
+        const int ld = unit ? KD : p.dvp;
+        const unsigned at = 4 * g4 * ld + l16;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) (end + (16 * t + j) * ld)[at] = S[t][j];
+        return;
+    }
     float *out = BWD ? p.dh_init : p.h_last;
-    if (out && live) {
+    if (out && live && seg == (BWD ? 0 : ns - 1)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -785,18 +898,106 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
     }
 }
 
-// GRAD: workgroups of blockIdx.z = 1 run the adjoints' chain, at the same time.
-template <typename T, int KD, bool GRAD>
+// Workgroups (sequence and head, 64 columns, segment); with GRAD those of the
+// upper half of blockIdx.z run the adjoints' chain, at the same time.
+template <typename T, int KD, bool GRAD, bool PROBE>
 __global__ __launch_bounds__(256, 1) void delta_seq(ChunkParams p)
 {
     extern __shared__ __align__(16) uint16_t lds[];
     if constexpr (GRAD) {
-        if (blockIdx.z == 1) {
-            seq_chain<T, KD, true>(p, lds);
+        if (static_cast<int>(blockIdx.z) >= p.nseg) {
+            seq_chain<T, KD, true, PROBE>(p, lds);
             return;
         }
     }
-    seq_chain<T, KD, false>(p, lds);
+    seq_chain<T, KD, false, PROBE>(p, lds);
+}
+
+// First states of the segments: S over a sequence's segments, S <- A S + b
+// (adjoint: D <- A^T D + b from the last one), each stored in b's place.
+// Workgroup (sequence and head, 64 columns, forward or adjoint); A goes
+// through LDS in three parts, 16 columns of the state a wave as in seq_chain.
+template <typename T, int KD, bool GRAD>
+__global__ __launch_bounds__(256, 1) void delta_join(ChunkParams p)
+{
+    using AT = Tile<3, KD, KD>;
+    constexpr int NT = KD / 16, kPieces = KD * KD / 4 / 256;
+    extern __shared__ __align__(16) uint16_t lds[];
+    const AT at{lds};
+    const bool bwd = GRAD && blockIdx.z == 1;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64, g4 = l / 16, l16 = l % 16;
+    const long s = blockIdx.x / p.nh;
+    const int hl = static_cast<int>(blockIdx.x - s * p.nh), head = p.hk0 * p.rep + hl;
+    const Seq q = find_seq(p, s);
+    const long n_all = (q.len + kC - 1) / kC;
+    const int ns = n_all > 0 ? static_cast<int>((n_all + p.seg_len - 1) / p.seg_len) : 1;
+    const int v0 = blockIdx.y * 64 + wave * 16, col = v0 + l16;
+    const bool act = v0 < p.dvp, live = col < p.dv_;
+    const unsigned lane_at = 4 * g4 * p.dvp + l16;
+    const float *init = bwd ? p.dh_last : p.h_init;
+    const long state = ((s * p.h + head) * p.dk_) * p.dv_;
+    facc S[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int row = 16 * t + 4 * g4 + j;
+            S[t][j] = init ? init[state + static_cast<long>(min(row, p.dk_ - 1)) * p.dv_ + min(col, p.dv_ - 1)] : 0.0f;
+            S[t][j] = (live && row < p.dk_) ? S[t][j] : 0.0f;
+        }
+    facc a[kPieces];
+    auto seg = [&](int i) { return static_cast<long>(blockIdx.x) * p.nseg + (bwd ? ns - 1 - i : i); };
+    auto fetch = [&](int i) __attribute__((always_inline)) {
+        const float *src = p.seg_a + seg(i) * KD * KD;
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) a[k] = *reinterpret_cast<const facc *>(src + (k * 256 + threadIdx.x) * 4);
+    };
+    if (ns > 1) fetch(0);
+    for (int i = 0; i < ns; ++i) {
+        float *at_s = (bwd ? p.seg_d : p.seg_s) + seg(i) * KD * p.dvp + v0;
+        const bool more = i + 1 < ns;  // (the last segment's end is the chain's own)
+        facc b[NT];
+        if (act) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) b[t][j] = more ? (at_s + (16 * t + j) * p.dvp)[lane_at] : 0.0f;
+        }
+        if (more) {
+            lds_barrier();  // (the last A has been read)
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+                const int w = (k * 256 + threadIdx.x) * 4;
+                at.put4(w / KD, w % KD, a[k][0], a[k][1], a[k][2], a[k][3]);
+            }
+            lds_barrier();
+            if (i + 2 < ns) fetch(i + 1);
+        }
+        if (!act) continue;
+        facc out[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) out[t] = S[t];
+        if (more) {
+#pragma unroll
+            for (int ks = 0; ks < KD / 32; ++ks) {
+                bfrag f[3];
+                split_acc<3>(S[2 * ks], S[2 * ks + 1], f);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    bfrag m[3];
+                    if (bwd) at.cols(32 * ks, 16 * t, m);
+                    else at.rows(16 * t, 32 * ks, m);
+                    mma<3, 3>(b[t], m, f);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) S[t] = b[t];
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) (at_s + (16 * t + j) * p.dvp)[lane_at] = out[t][j];
+    }
 }
 
 // ------------------------------------------------------------------ delta_out
@@ -1151,6 +1352,38 @@ int big_lds(F *kernel, int bytes)
     return e == hipSuccess ? SSM2D_OK : hip_fail(e);
 }
 
+// Segments of the chains. Whole, a chain of n chunks takes n steps, and the
+// `chains` * vb workgroups of all chains (twice that with the adjoints') may
+// leave compute units idle. In P segments: ceil(n / P) steps of the probes
+// (pb blocks of columns a chain), about a step a segment to join them, and
+// ceil(n / P) steps again. The P with the fewest steps is taken, counting
+// rounds of 256 workgroups. Packed sequences' lengths are on the device: there
+// a segment is as long as makes the segments of all tokens 256 workgroups (at
+// least 8 chunks), and sequences no longer than that are not cut.
+inline void plan_segments(ChunkParams &p, long chains, bool grad, int vb, int pb)
+{
+    constexpr long kUnits = 256;
+    const long dirs = grad ? 2 : 1;
+    p.nseg = 1;
+    if (p.n_seq > 0) {
+        const long total = p.tokens / kC + 1, heads = chains / p.n_seq;
+        const long len = std::max<long>(8, (total * heads * vb * dirs + kUnits - 1) / kUnits);
+        p.seg_len = static_cast<int>(len);
+        if (chains * vb * dirs < 4 * kUnits) p.nseg = static_cast<int>(std::min<long>((total + len - 1) / len, 1024));
+        if (p.nseg > 1) p.seg_len = static_cast<int>((total + p.nseg - 1) / p.nseg);
+        else p.seg_len = static_cast<int>(total);
+        return;
+    }
+    const long n = p.chunks_b, w = chains * vb * dirs, w1 = chains * (pb + (grad ? vb : 0));
+    long best = n * ((w + kUnits - 1) / kUnits), at = 1;
+    for (long k = 2; k <= std::min<long>(n / 4, 256); ++k) {
+        const long len = (n + k - 1) / k, steps = len * ((w1 * k + kUnits - 1) / kUnits + (w * k + kUnits - 1) / kUnits) + k;
+        if (steps < best) best = steps, at = k;
+    }
+    p.seg_len = static_cast<int>((n + at - 1) / at);
+    p.nseg = static_cast<int>((n + p.seg_len - 1) / p.seg_len);
+}
+
 // Workspace of one pass at most (heads beyond it take another pass).
 constexpr double kMostBytes = 16.0 * (1u << 30);
 
@@ -1178,9 +1411,14 @@ int chunk_passes(const DeltaArgs &a)
     const size_t n = static_cast<size_t>(p.slots);
     const size_t gates = n * kGates * 4, mm = n * kMWords * 16, st = n * KD * p.dvp * 4, row = n * kC * p.dvp * 4;
     const size_t each = gates + (GRAD ? 2 : 1) * (mm + st + row) + (GRAD ? row : 0);
+    constexpr int kDirs = GRAD ? 2 : 1;
+    const int vb = (p.dvp + 63) / 64, pb = (p.dvp + KD + 63) / 64;
     const int nhk = static_cast<int>(std::max(1.0, std::min<double>(a.hk, kMostBytes / (static_cast<double>(each) * p.rep))));
+    plan_segments(p, seqs * p.rep * nhk, GRAD, vb, pb);
+    const size_t sa = static_cast<size_t>(p.nseg) * KD * KD * 4, ss = static_cast<size_t>(p.nseg) * KD * p.dvp * 4;
+    const size_t seg_each = p.nseg > 1 ? static_cast<size_t>(seqs) * (sa + kDirs * ss) : 0;
     void *ws = nullptr;
-    int rc = get_aux_ws(a.dev, a.stream, kSlotDelta, each * p.rep * nhk, &ws);
+    int rc = get_aux_ws(a.dev, a.stream, kSlotDelta, (each + seg_each) * p.rep * nhk, &ws);
     if (rc != SSM2D_OK) return rc;
     const hipStream_t s = static_cast<hipStream_t>(a.stream);
     for (p.hk0 = 0; p.hk0 < a.hk; p.hk0 += nhk) {
@@ -1192,16 +1430,21 @@ int chunk_passes(const DeltaArgs &a)
             w += bytes * p.nh;
             return at;
         };
-        p.m = reinterpret_cast<uint4 *>(take(mm));
+        p.m = reinterpret_cast<word4 *>(take(mm));
         p.s0 = reinterpret_cast<float *>(take(st));
         p.e = reinterpret_cast<float *>(take(row));
         if (GRAD) {
-            p.mt = reinterpret_cast<uint4 *>(take(mm));
+            p.mt = reinterpret_cast<word4 *>(take(mm));
             p.d1 = reinterpret_cast<float *>(take(st));
             p.dr = reinterpret_cast<float *>(take(row));
             p.z = reinterpret_cast<float *>(take(row));
         }
         p.gates = reinterpret_cast<float *>(take(gates));
+        if (p.nseg > 1) {
+            p.seg_a = reinterpret_cast<float *>(take(seqs * sa));
+            p.seg_s = reinterpret_cast<float *>(take(seqs * ss));
+            if (GRAD) p.seg_d = reinterpret_cast<float *>(take(seqs * ss));
+        }
         const unsigned slots = static_cast<unsigned>(p.slots), nk = static_cast<unsigned>(p.nhk), nh = static_cast<unsigned>(p.nh);
         delta_prep<T, KD, GRAD><<<dim3(slots, nk), dim3(256), 0, s>>>(p);
         if ((rc = launched()) != SSM2D_OK) return rc;
@@ -1213,8 +1456,17 @@ int chunk_passes(const DeltaArgs &a)
         }
         constexpr int kF = SeqBuf<T, KD, false>::kBufs * SeqBuf<T, KD, false>::kBytes, kB = SeqBuf<T, KD, true>::kBufs * SeqBuf<T, KD, true>::kBytes;
         constexpr int kSeq = GRAD && kB > kF ? kB : kF;
-        if ((rc = big_lds(delta_seq<T, KD, GRAD>, kSeq)) != SSM2D_OK) return rc;
-        delta_seq<T, KD, GRAD><<<dim3(static_cast<unsigned>(seqs * p.nh), static_cast<unsigned>((p.dvp + 63) / 64), GRAD ? 2 : 1), dim3(256), kSeq, s>>>(p);
+        const unsigned chains = static_cast<unsigned>(seqs * p.nh);
+        if (p.nseg > 1) {
+            constexpr int kJ = Tile<3, KD, KD>::kBytes;
+            if ((rc = big_lds(delta_seq<T, KD, GRAD, true>, kSeq)) != SSM2D_OK || (rc = big_lds(delta_join<T, KD, GRAD>, kJ)) != SSM2D_OK) return rc;
+            delta_seq<T, KD, GRAD, true><<<dim3(chains, static_cast<unsigned>(pb), kDirs * p.nseg), dim3(256), kSeq, s>>>(p);
+            if ((rc = launched()) != SSM2D_OK) return rc;
+            delta_join<T, KD, GRAD><<<dim3(chains, static_cast<unsigned>(vb), kDirs), dim3(256), kJ, s>>>(p);
+            if ((rc = launched()) != SSM2D_OK) return rc;
+        }
+        if ((rc = big_lds(delta_seq<T, KD, GRAD, false>, kSeq)) != SSM2D_OK) return rc;
+        delta_seq<T, KD, GRAD, false><<<dim3(chains, static_cast<unsigned>(vb), kDirs * p.nseg), dim3(256), kSeq, s>>>(p);
         if ((rc = launched()) != SSM2D_OK) return rc;
         if constexpr (GRAD) {
             constexpr int kL = LocalLds<T, KD>::kBytes;
