@@ -55,6 +55,8 @@ struct ChunkParams {
     // workspace, by [slot][head of this pass]
     float *gates;                       // [5][kC]: gamma, Gam_last, beta, G and its rounding error
     word4 *m, *mt;                      // -M, -M^T: 6 fragments x 3 parts
+    // (matrices as accumulator tiles: 16 columns after 16, of each 16 rows after
+    // 16, of each the 64 lanes' four values: column lane % 16, rows 4 (lane / 16) + j)
     float *s0, *d1;                     // [KD][dvp]
     float *e, *dr, *z;                  // [kC][dvp]
     // by [sequence][head of this pass][segment]: a segment's transition
@@ -67,7 +69,7 @@ struct ChunkParams {
     int hk0, nhk, nh;                   // this pass: key heads hk0 .. hk0 + nhk - 1, nh = nhk * rep heads
     long qs[3], ks[3], vs[3], os[3], gs[3], bs[3];
     float scale;
-    int vec_qk, vec_do;                 // rows of q and k, of dout can be read 16 bytes at a time
+    int vec_qk, vec_do, vec_v;          // rows of q and k, of dout, of v can be read 16 bytes at a time
     int vec_o, vec_dqk;                 // rows of o, of dq and dk can be written four elements at a time
 };
 
@@ -205,6 +207,10 @@ __device__ __forceinline__ void lds_barrier()
     asm volatile("" ::: "memory");
 }
 
+// The LDS address behind a pointer into it: its low half (a cast between the
+// address spaces would test for null first).
+__device__ __forceinline__ unsigned lds_offset(const void *p) { return static_cast<unsigned>(reinterpret_cast<uintptr_t>(p)); }
+
 // A tile in LDS: NP parts of [ROWS][COLS] bf16, rows padded by 16 bytes (the
 // 16 rows of a fragment then start 4 banks apart, both ways of reading).
 template <int NP, int ROWS, int COLS>
@@ -229,12 +235,12 @@ struct Tile {
     {
         using lds4 = __attribute__((address_space(3))) half4 *;
         const int l = threadIdx.x % 64;
-        uint16_t *a = p + (r0 + 4 * (l / 16) + (l % 16) / 4) * kLd + c0 + 4 * (l % 4);
+        const unsigned at = lds_offset(p + (r0 + 4 * (l / 16) + (l % 16) / 4) * kLd + c0 + 4 * (l % 4));
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
             FragBits b;
-            b.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(a + n * kPart));
-            b.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(a + n * kPart + 16 * kLd));
+            b.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(at + n * kPart * 2));
+            b.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(at + (n * kPart + 16 * kLd) * 2));
             f[n] = b.f;
         }
     }
@@ -570,73 +576,108 @@ __global__ __launch_bounds__(256) void delta_z(ChunkParams p)
             st.put(ot);
         }
         __syncthreads();
-        // rows v, columns tokens j = 16 wave ..: four neighbouring v a lane
+        // rows tokens j = 16 wave .., columns v
         facc acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
             if (32 * ks + 31 < 16 * wave) continue;  // i >= j
-            bfrag b[3];
-            pt.cols(32 * ks, 16 * wave, b);
+            bfrag a[3];
+            pt.cols(32 * ks, 16 * wave, a);
 #pragma unroll
             for (int vt = 0; vt < 2; ++vt) {
-                bfrag a[NP];
-                ot.cols(32 * ks, 16 * vt, a);
-                mma<NP, 3>(acc[vt], a, b);
+                bfrag b[NP];
+                ot.cols(32 * ks, 16 * vt, b);
+                mma<3, NP>(acc[vt], a, b);
             }
         }
 #pragma unroll
-        for (int vt = 0; vt < 2; ++vt)
-            *reinterpret_cast<facc *>(zp + (16 * wave + l % 16) * p.dvp + v0 + 16 * vt + 4 * (l / 16)) = acc[vt];
+        for (int vt = 0; vt < 2; ++vt) *reinterpret_cast<facc *>(zp + (v0 + 16 * vt) * kC + wave * 256 + l * 4) = acc[vt];
     }
 }
 
 // ------------------------------------------------------------------ delta_seq
 
 // What a chunk's step reads from LDS: K (and Q in the backward), M's
-// fragments and the gates.
-template <typename T, int KD, bool BWD>
+// fragments, the gates and, of bf16 inputs, the columns of v (dO).
+template <typename T, int KD, bool BWD, int THREADS>
 struct SeqBuf {
+    static constexpr int kCols = THREADS / 4;
+    static constexpr bool kStaged = sizeof(T) == 2;
     static constexpr int kTile = Tile<kParts<T>, kC, KD>::kBytes;
-    static constexpr int kBytes = (BWD ? 2 : 1) * kTile + kMWords * 16 + 3 * kC * 4;
+    static constexpr int kRest = kMWords * 16 + 4 * kC * 4, kV = kStaged ? Tile<1, kC, kCols>::kBytes : 0;
+    static constexpr int kBytes = (BWD ? 2 : 1) * kTile + kRest + kV;
     // two buffers where they fit beside each other
     static constexpr int kBufs = 2 * kBytes <= 160 * 1024 ? 2 : 1;
 };
 
-template <typename T, int KD, bool BWD>
+// 16 bytes a lane from global memory into LDS at `to` + 16 lane, without a
+// register in between. Done when vmcnt says so.
+__device__ __forceinline__ void load_to_lds(const word4 *from, void *to)
+{
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) unsigned *)from,
+                                     (__attribute__((address_space(3))) unsigned *)lds_offset(to), 16, 0, 0);
+}
+
+// The next step's inputs. With two buffers M and the gates go straight to
+// LDS; K and Q pass through registers, which pad and cut them.
+template <typename T, int KD, bool BWD, int THREADS>
 struct SeqStage {
-    Stage<T, KD, 256> k, q;
-    word4 m[(kMWords + 255) / 256];
+    using Buf = SeqBuf<T, KD, BWD, THREADS>;
+    static constexpr bool kDirect = Buf::kBufs == 2;
+    static constexpr int kLines = (kMWords + 3 * kC / 4) / 64 + 1, kEach = (kMWords + THREADS - 1) / THREADS;  // kLines: 1 KiB each
+    Stage<T, KD, THREADS> k, q;
+    Stage<T, Buf::kCols, THREADS> v;
+    word4 m[kDirect ? 1 : kEach];
     float g;
-    __device__ __forceinline__ void load(const ChunkParams &p, long b, long t0, int len, int hk, long at)
+    __device__ __forceinline__ void load(const ChunkParams &p, long b, long t0, int len, int hk, long at, uint16_t *lds)
     {
         k.load(static_cast<const T *>(p.k) + b * p.ks[0] + t0 * p.ks[1] + hk * p.ks[2], p.ks[1], len, p.dk_, p.vec_qk);
         if constexpr (BWD) q.load(static_cast<const T *>(p.q) + b * p.qs[0] + t0 * p.qs[1] + hk * p.qs[2], p.qs[1], len, p.dk_, p.vec_qk);
         const word4 *src = (BWD ? p.mt : p.m) + at * kMWords;
+        if constexpr (kDirect) {
+            word4 *to = reinterpret_cast<word4 *>(lds + (BWD ? 2 : 1) * (Buf::kTile / 2));
+            const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64;
+            const word4 *gates = reinterpret_cast<const word4 *>(p.gates + at * kGates);
 #pragma unroll
-        for (int i = 0; i < (kMWords + 255) / 256; ++i) {
-            const int w = i * 256 + threadIdx.x;
-            m[i] = src[min(w, kMWords - 1)];
+            for (int i = 0; i < (kLines + THREADS / 64 - 1) / (THREADS / 64); ++i) {
+                const int line = i * (THREADS / 64) + wave;
+                if (line < kMWords / 64) load_to_lds(src + line * 64 + l, to + line * 64);
+                else if (line == kMWords / 64) load_to_lds(gates + l, to + kMWords);  // (gamma, Gam_last, beta, G: 1 KiB)
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) m[i] = src[min(i * THREADS + static_cast<int>(threadIdx.x), kMWords - 1)];
+            g = p.gates[at * kGates + min(static_cast<int>(threadIdx.x), 3 * kC - 1)];
         }
-        g = p.gates[at * kGates + min(static_cast<int>(threadIdx.x), 3 * kC - 1)];
+    }
+    // the workgroup's columns of v (dO) from c0 on: n of them
+    __device__ __forceinline__ void load_v(const T *base, long stride, int len, int n, bool vec)
+    {
+        if constexpr (Buf::kStaged) v.load(base, stride, len, n, vec);
     }
     __device__ __forceinline__ void put(uint16_t *lds) const
     {
-        constexpr int kTile = SeqBuf<T, KD, BWD>::kTile / 2;
+        constexpr int kTile = Buf::kTile / 2;
+        if constexpr (Buf::kStaged) v.put(Tile<1, kC, Buf::kCols>{lds + (BWD ? 2 : 1) * kTile + Buf::kRest / 2});
         k.put(Tile<kParts<T>, kC, KD>{lds});
         if constexpr (BWD) q.put(Tile<kParts<T>, kC, KD>{lds + kTile});
-        uint16_t *rest = lds + (BWD ? 2 : 1) * kTile;
-        word4 *mm = reinterpret_cast<word4 *>(rest);
+        if constexpr (kDirect) {
+            __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): what load() sent to LDS has arrived
+        } else {
+            uint16_t *rest = lds + (BWD ? 2 : 1) * kTile;
+            word4 *mm = reinterpret_cast<word4 *>(rest);
 #pragma unroll
-        for (int i = 0; i < (kMWords + 255) / 256; ++i) {
-            const int w = i * 256 + threadIdx.x;
-            if (w < kMWords) mm[w] = m[i];
+            for (int i = 0; i < kEach; ++i) {
+                const int w = i * THREADS + threadIdx.x;
+                if (w < kMWords) mm[w] = m[i];
+            }
+            if (threadIdx.x < 3 * kC) reinterpret_cast<float *>(rest + kMWords * 8)[threadIdx.x] = g;
         }
-        if (threadIdx.x < 3 * kC) reinterpret_cast<float *>(rest + kMWords * 8)[threadIdx.x] = g;
     }
 };
 
-// The chain over a sequence's chunks for 16 columns of the state a wave (64 a
-// workgroup). Columns are independent, so waves only share what they read.
+// The chain over a sequence's chunks for 16 columns of the state a wave (64 or
+// 128 a workgroup). Columns are independent, so waves only share what they read.
 // The state [KD][16] stays in accumulators, from which it is cut into operands.
 //
 // A sequence whose chain would leave most of the chip idle is cut into
@@ -645,11 +686,11 @@ struct SeqStage {
 // columns from the unit matrix and v = 0 (A); delta_join goes over the
 // segments; then they run at once from their true first states. The adjoint's
 // transition is A^T.
-template <typename T, int KD, bool BWD, bool PROBE>
+template <typename T, int KD, bool BWD, bool PROBE, int THREADS>
 __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
 {
     constexpr int NP = kParts<T>, NT = KD / 16;
-    using Buf = SeqBuf<T, KD, BWD>;
+    using Buf = SeqBuf<T, KD, BWD, THREADS>;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64, g4 = l / 16, l16 = l % 16;
     const long s = blockIdx.x / p.nh;
     const int hl = static_cast<int>(blockIdx.x - s * p.nh), head = p.hk0 * p.rep + hl, hk = head / p.rep;
@@ -659,88 +700,110 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
     const int ns = n_all > 0 ? static_cast<int>((n_all + p.seg_len - 1) / p.seg_len) : 1;  // of this sequence
     if (seg >= ns || (PROBE && ns == 1)) return;
     const long c0 = static_cast<long>(seg) * p.seg_len, c1 = min(n_all, c0 + p.seg_len), n = c1 - c0;
-    int v0 = blockIdx.y * 64 + wave * 16;
+    int v0 = blockIdx.y * (THREADS / 4) + wave * 16;
     const bool unit = PROBE && !BWD && v0 >= p.dvp;  // this wave's columns are the unit matrix's
     if (unit) v0 -= p.dvp;
     const bool act = v0 < (unit ? KD : p.dvp);  // this wave has columns
-    if (PROBE && BWD && static_cast<int>(blockIdx.y) * 64 >= p.dvp) return;
+    if (PROBE && BWD && static_cast<int>(blockIdx.y) * (THREADS / 4) >= p.dvp) return;
     const int col = v0 + l16;
     const bool live = !unit && col < p.dv_;  // this lane's column is not padding
     const int colv = min(col, p.dv_ - 1);  // (where lanes without a column read)
-    const unsigned lane_at = 4 * g4 * p.dvp + l16;  // of this lane's first row and column in a [..][dvp] matrix
     const long state = ((s * p.h + head) * p.dk_) * p.dv_;
     const float *init = BWD ? p.dh_last : p.h_init;
     const long segs = (static_cast<long>(blockIdx.x) * p.nseg + seg) * KD;
-    float *joined = (BWD ? p.seg_d : p.seg_s) + segs * p.dvp + v0;
+    float *joined = (BWD ? p.seg_d : p.seg_s) + segs * p.dvp + v0 * KD + l * 4;
     facc S[NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t) {
+        if (!PROBE && p.nseg > 1) {
+            S[t] = act ? *reinterpret_cast<const facc *>(joined + t * 256) : facc{0, 0, 0, 0};
+            continue;
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int row = 16 * t + 4 * g4 + j;
             if constexpr (PROBE) {
                 S[t][j] = (unit && row == col) ? 1.0f : 0.0f;
-            } else if (p.nseg > 1) {
-                S[t][j] = act ? (joined + (16 * t + j) * p.dvp)[lane_at] : 0.0f;
             } else {
                 S[t][j] = init ? init[state + static_cast<long>(min(row, p.dk_ - 1)) * p.dv_ + colv] : 0.0f;
                 S[t][j] = (live && row < p.dk_) ? S[t][j] : 0.0f;
             }
         }
+    }
     auto len_of = [&](long c) { return static_cast<int>(q.len - c * kC < kC ? q.len - c * kC : kC); };
     auto chunk = [&](long i) { return BWD ? c1 - 1 - i : c0 + i; };
     // a column of the chunk's rows of v (dO and Z in the backward), 16 tokens a lane
     T x0[16];
-    float x1[16];
+    facc x1[4];
+    const T *vp = BWD ? static_cast<const T *>(p.dout) + q.b * p.os[0] + head * p.os[2] : static_cast<const T *>(p.v) + q.b * p.vs[0] + head * p.vs[2];
+    const long vstep = BWD ? p.os[1] : p.vs[1];
+    SeqStage<T, KD, BWD, THREADS> st;
+    const int wg0 = min(static_cast<int>(blockIdx.y) * Buf::kCols, (p.dv_ - 1) / 16 * 16);  // (workgroups of the unit matrix alone read any)
     auto load_cols = [&](long c) __attribute__((always_inline)) {
         const int len = len_of(c);
-        const T *src = BWD ? static_cast<const T *>(p.dout) + q.b * p.os[0] + (q.t0 + c * kC) * p.os[1] + head * p.os[2] + colv
-                           : static_cast<const T *>(p.v) + q.b * p.vs[0] + (q.t0 + c * kC) * p.vs[1] + head * p.vs[2] + colv;
-        const long step = BWD ? p.os[1] : p.vs[1];
-        if (len == kC) {
-            const T *lane = src + 4 * g4 * step;
+        const T *src = vp + (q.t0 + c * kC) * vstep;
+        if constexpr (Buf::kStaged) {
+            st.load_v(src + wg0, vstep, len, p.dv_ - wg0, BWD ? p.vec_do : p.vec_v);
+        } else if (len == kC) {  // (the lane's part of the offset in 32 bits: see the limit on strides)
+            const unsigned lane = 4 * g4 * static_cast<unsigned>(vstep) + colv;
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x0[4 * t + j] = lane[(16 * t + j) * step];
+            for (int t = 0; t < 16; ++t) x0[t] = (src + (16 * (t / 4) + t % 4) * vstep)[lane];
         } else {
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x0[4 * t + j] = src[min(16 * t + 4 * g4 + j, len - 1) * step];
+            for (int t = 0; t < 16; ++t) x0[t] = (src + colv)[min(16 * (t / 4) + 4 * g4 + t % 4, len - 1) * vstep];
         }
         if constexpr (BWD) {
-            const float *z = p.z + ((q.slot0 + c) * p.nh + hl) * kC * p.dvp + (act && !unit ? v0 : 0);
+            const float *z = p.z + ((q.slot0 + c) * p.nh + hl) * kC * p.dvp + (act && !unit ? v0 : 0) * kC + l * 4;
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x1[4 * t + j] = (z + (16 * t + j) * p.dvp)[lane_at];
+            for (int t = 0; t < 4; ++t) x1[t] = *reinterpret_cast<const facc *>(z + t * 256);
         }
     };
-    SeqStage<T, KD, BWD> st;
-    auto fetch = [&](long c) __attribute__((always_inline)) { st.load(p, q.b, q.t0 + c * kC, len_of(c), hk, (q.slot0 + c) * p.nh + hl); };
-    float y0[16], y1[16];  // the step's rows of v (dO and Z)
+    auto fetch = [&](long c, uint16_t *to) __attribute__((always_inline)) {
+        st.load(p, q.b, q.t0 + c * kC, len_of(c), hk, (q.slot0 + c) * p.nh + hl, to);
+    };
+    facc y0[4], y1[4];  // the step's rows of v (dO) and Z
     auto take_cols = [&](long c) __attribute__((always_inline)) {
         const int len = len_of(c);
 #pragma unroll
-        for (int t = 0; t < 16; ++t) {
-            y0[t] = (live && 16 * (t / 4) + 4 * g4 + t % 4 < len) ? widen1(x0[t]) : 0.0f;
-            asm volatile("" : "+v"(y0[t]));  // (here, and not where it is used)
+        for (int t = 0; t < 4; ++t) {
+            if constexpr (!Buf::kStaged) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    y0[t][j] = (live && 16 * t + 4 * g4 + j < len) ? widen1(x0[4 * t + j]) : 0.0f;
+                    asm volatile("" : "+v"(y0[t][j]));  // (here, and not where it is used)
+                }
+            }
             if constexpr (BWD) {
                 y1[t] = x1[t];
                 asm volatile("" : "+v"(y1[t]));
             }
         }
     };
+    // (staged columns: 16 tokens of column l16 by a transposing read, which gives an accumulator's rows)
+    auto staged_cols = [&](uint16_t *buf) __attribute__((always_inline)) {
+        if constexpr (Buf::kStaged) {
+            const Tile<1, kC, Buf::kCols> vt{buf + (BWD ? 2 : 1) * (Buf::kTile / 2) + Buf::kRest / 2};
+#pragma unroll
+            for (int t = 0; t < 4; t += 2) {
+                bfrag f[1];
+                vt.cols(16 * t, 16 * wave, f);
+                FragBits x;
+                x.f = f[0];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    y0[t + w / 2][2 * (w % 2)] = live ? bf16_lo(x.w[w]) : 0.0f;
+                    y0[t + w / 2][2 * (w % 2) + 1] = live ? bf16_hi(x.w[w]) : 0.0f;
+                }
+            }
+        }
+    };
     auto keep_state = [&](long c) __attribute__((always_inline)) {
-        float *keep = (BWD ? p.d1 : p.s0) + ((q.slot0 + c) * p.nh + hl) * KD * p.dvp + v0;
+        float *keep = (BWD ? p.d1 : p.s0) + ((q.slot0 + c) * p.nh + hl) * KD * p.dvp + v0 * KD + l * 4;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) (keep + (16 * t + j) * p.dvp)[lane_at] = S[t][j];
+        for (int t = 0; t < NT; ++t) *reinterpret_cast<facc *>(keep + t * 256) = S[t];
     };
     if (n > 0) {
-        fetch(chunk(0));
+        fetch(chunk(0), lds);
         load_cols(chunk(0));
         st.put(lds);
         take_cols(chunk(0));
@@ -753,9 +816,10 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
     for (long i = 0; i < n; ++i) {
         const long c = chunk(i), at = (q.slot0 + c) * p.nh + hl;
         uint16_t *buf = lds + (Buf::kBufs == 2 ? (i & 1) * (Buf::kBytes / 2) : 0);
+        uint16_t *next = lds + (Buf::kBufs == 2 ? ((i + 1) & 1) * (Buf::kBytes / 2) : 0);
         lds_barrier();
         if (i + 1 < n) {
-            fetch(chunk(i + 1));
+            fetch(chunk(i + 1), next);
             load_cols(chunk(i + 1));
         }
         facc X[4];
@@ -765,6 +829,7 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
             uint16_t *rest = buf + (BWD ? 2 : 1) * (Buf::kTile / 2);
             const word4 *mm = reinterpret_cast<const word4 *>(rest);
             const float *gt = reinterpret_cast<const float *>(rest + kMWords * 8);
+            staged_cols(buf);
             // Y = K S, then the right-hand side: V - gamma Y, or Z + Gam_last Y
             facc Y[4];
 #pragma unroll
@@ -785,7 +850,7 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
                 be[t] = *reinterpret_cast<const facc *>(gt + 2 * kC + 16 * t + 4 * g4);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    X[t][j] = BWD ? fmaf(gl[t][j], Y[t][j], y1[4 * t + j]) : fmaf(-ga[t][j], Y[t][j], y0[4 * t + j]);
+                    X[t][j] = BWD ? fmaf(gl[t][j], Y[t][j], y1[t][j]) : fmaf(-ga[t][j], Y[t][j], y0[t][j]);
                     W[t][j] = be[t][j] * X[t][j];
                 }
             }
@@ -820,7 +885,7 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
                     if constexpr (BWD) {
                         o0[4 * t + j] = bx;
                         W[t][j] = -ga[t][j] * bx;
-                        W2[t][j] = p.scale * ga[t][j] * y0[4 * t + j];
+                        W2[t][j] = p.scale * ga[t][j] * y0[t][j];
                     } else {
                         W[t][j] = gl[t][j] * bx;
                     }
@@ -847,16 +912,14 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
         }
         if (i + 1 < n) {
             if constexpr (Buf::kBufs == 1) lds_barrier();
-            st.put(lds + (Buf::kBufs == 2 ? ((i + 1) & 1) * (Buf::kBytes / 2) : 0));
+            st.put(next);
             take_cols(chunk(i + 1));
         }
         asm volatile("" ::: "memory");  // (no store goes up past the waits above)
         if (!PROBE && act) {
-            float *ep = (BWD ? p.dr : p.e) + at * kC * p.dvp + v0;
+            float *ep = (BWD ? p.dr : p.e) + at * kC * p.dvp + v0 * kC + l * 4;
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) (ep + (16 * t + j) * p.dvp)[lane_at] = X[t][j];
+            for (int t = 0; t < 4; ++t) *reinterpret_cast<facc *>(ep + t * 256) = X[t];
             if (i + 1 < n) keep_state(chunk(i + 1));
             if constexpr (BWD) {
                 const int len = len_of(c);
@@ -877,13 +940,9 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
     }
     if constexpr (PROBE) {
         if (!act) return;
-        float *end = unit ? p.seg_a + segs * KD + v0 : joined;
-        const int ld = unit ? KD : p.dvp;
-        const unsigned at = 4 * g4 * ld + l16;
+        float *end = unit ? p.seg_a + segs * KD + v0 * KD + l * 4 : joined;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) (end + (16 * t + j) * ld)[at] = S[t][j];
+        for (int t = 0; t < NT; ++t) *reinterpret_cast<facc *>(end + t * 256) = S[t];
         return;
     }
     float *out = BWD ? p.dh_init : p.h_last;
@@ -898,30 +957,31 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
     }
 }
 
-// Workgroups (sequence and head, 64 columns, segment); with GRAD those of the
+// Workgroups (sequence and head, 64 or 128 columns, segment); with GRAD those of the
 // upper half of blockIdx.z run the adjoints' chain, at the same time.
-template <typename T, int KD, bool GRAD, bool PROBE>
-__global__ __launch_bounds__(256, 1) void delta_seq(ChunkParams p)
+template <typename T, int KD, bool GRAD, bool PROBE, int THREADS>
+__global__ __launch_bounds__(THREADS, 1) void delta_seq(ChunkParams p)
 {
     extern __shared__ __align__(16) uint16_t lds[];
     if constexpr (GRAD) {
         if (static_cast<int>(blockIdx.z) >= p.nseg) {
-            seq_chain<T, KD, true, PROBE>(p, lds);
+            seq_chain<T, KD, true, PROBE, THREADS>(p, lds);
             return;
         }
     }
-    seq_chain<T, KD, false, PROBE>(p, lds);
+    seq_chain<T, KD, false, PROBE, THREADS>(p, lds);
 }
 
 // First states of the segments: S over a sequence's segments, S <- A S + b
 // (adjoint: D <- A^T D + b from the last one), each stored in b's place.
-// Workgroup (sequence and head, 64 columns, forward or adjoint); A goes
-// through LDS in three parts, 16 columns of the state a wave as in seq_chain.
-template <typename T, int KD, bool GRAD>
-__global__ __launch_bounds__(256, 1) void delta_join(ChunkParams p)
+// Workgroup (sequence and head, 64 or 128 columns, forward or adjoint); A goes
+// through LDS in three parts (its transpose: a piece of A is four neighbours
+// of a column), 16 columns of the state a wave as in seq_chain.
+template <typename T, int KD, bool GRAD, int THREADS>
+__global__ __launch_bounds__(THREADS, 1) void delta_join(ChunkParams p)
 {
     using AT = Tile<3, KD, KD>;
-    constexpr int NT = KD / 16, kPieces = KD * KD / 4 / 256;
+    constexpr int NT = KD / 16, kAll = KD * KD / 4, kPieces = (kAll + THREADS - 1) / THREADS, kGroup = NT < 4 ? NT : 4;
     extern __shared__ __align__(16) uint16_t lds[];
     const AT at{lds};
     const bool bwd = GRAD && blockIdx.z == 1;
@@ -931,9 +991,8 @@ __global__ __launch_bounds__(256, 1) void delta_join(ChunkParams p)
     const Seq q = find_seq(p, s);
     const long n_all = (q.len + kC - 1) / kC;
     const int ns = n_all > 0 ? static_cast<int>((n_all + p.seg_len - 1) / p.seg_len) : 1;
-    const int v0 = blockIdx.y * 64 + wave * 16, col = v0 + l16;
+    const int v0 = blockIdx.y * (THREADS / 4) + wave * 16, col = v0 + l16;
     const bool act = v0 < p.dvp, live = col < p.dv_;
-    const unsigned lane_at = 4 * g4 * p.dvp + l16;
     const float *init = bwd ? p.dh_last : p.h_init;
     const long state = ((s * p.h + head) * p.dk_) * p.dv_;
     facc S[NT];
@@ -945,62 +1004,83 @@ __global__ __launch_bounds__(256, 1) void delta_join(ChunkParams p)
             S[t][j] = init ? init[state + static_cast<long>(min(row, p.dk_ - 1)) * p.dv_ + min(col, p.dv_ - 1)] : 0.0f;
             S[t][j] = (live && row < p.dk_) ? S[t][j] : 0.0f;
         }
-    facc a[kPieces];
+    facc a[kPieces], b[NT];
     auto seg = [&](int i) { return static_cast<long>(blockIdx.x) * p.nseg + (bwd ? ns - 1 - i : i); };
-    auto fetch = [&](int i) __attribute__((always_inline)) {
+    auto place = [&](int i) { return (bwd ? p.seg_d : p.seg_s) + seg(i) * KD * p.dvp + (act ? v0 : 0) * KD + l * 4; };
+    auto fetch = [&](int i) __attribute__((always_inline)) {  // (the last segment's A and b are not needed; nor, maybe, there)
         const float *src = p.seg_a + seg(i) * KD * KD;
 #pragma unroll
-        for (int k = 0; k < kPieces; ++k) a[k] = *reinterpret_cast<const facc *>(src + (k * 256 + threadIdx.x) * 4);
+        for (int k = 0; k < kPieces; ++k) a[k] = *reinterpret_cast<const facc *>(src + min(k * THREADS + static_cast<int>(threadIdx.x), kAll - 1) * 4);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) b[t] = *reinterpret_cast<const facc *>(place(i) + t * 256);
     };
     if (ns > 1) fetch(0);
-    for (int i = 0; i < ns; ++i) {
-        float *at_s = (bwd ? p.seg_d : p.seg_s) + seg(i) * KD * p.dvp + v0;
-        const bool more = i + 1 < ns;  // (the last segment's end is the chain's own)
-        facc b[NT];
-        if (act) {
+    for (int i = 0; i + 1 < ns; ++i) {
+        lds_barrier();  // (the last A has been read)
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) b[t][j] = more ? (at_s + (16 * t + j) * p.dvp)[lane_at] : 0.0f;
+        for (int k = 0; k < kPieces; ++k) {
+            const int w = k * THREADS + threadIdx.x, tile = w / 64;
+            if (kAll % THREADS == 0 || w < kAll)
+                at.put4(16 * (tile / NT) + w % 16, 16 * (tile % NT) + 4 * (w % 64 / 16), a[k][0], a[k][1], a[k][2], a[k][3]);
         }
-        if (more) {
-            lds_barrier();  // (the last A has been read)
-#pragma unroll
-            for (int k = 0; k < kPieces; ++k) {
-                const int w = (k * 256 + threadIdx.x) * 4;
-                at.put4(w / KD, w % KD, a[k][0], a[k][1], a[k][2], a[k][3]);
-            }
-            lds_barrier();
-            if (i + 2 < ns) fetch(i + 1);
-        }
-        if (!act) continue;
         facc out[NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) out[t] = S[t];
-        if (more) {
+        for (int t = 0; t < NT; ++t) {
+            out[t] = S[t];
+            S[t] = b[t];
+        }
+        float *to = place(i);
+        lds_barrier();
+        if (i + 2 < ns) fetch(i + 1);
+        if (act) {
 #pragma unroll
             for (int ks = 0; ks < KD / 32; ++ks) {
                 bfrag f[3];
-                split_acc<3>(S[2 * ks], S[2 * ks + 1], f);
+                split_acc<3>(out[2 * ks], out[2 * ks + 1], f);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    bfrag m[3];
-                    if (bwd) at.cols(32 * ks, 16 * t, m);
-                    else at.rows(16 * t, 32 * ks, m);
-                    mma<3, 3>(b[t], m, f);
+                for (int t = 0; t < NT; t += kGroup) {
+                    bfrag m[kGroup][3];
+                    facc acc[kGroup];
+#pragma unroll
+                    for (int u = 0; u < kGroup; ++u) {
+                        if (bwd) at.rows(16 * (t + u), 32 * ks, m[u]);
+                        else at.cols(32 * ks, 16 * (t + u), m[u]);
+                        acc[u] = S[t + u];
+                    }
+                    mma_each<3, 3, kGroup>(acc, m, f);
+#pragma unroll
+                    for (int u = 0; u < kGroup; ++u) S[t + u] = acc[u];
                 }
             }
 #pragma unroll
-            for (int t = 0; t < NT; ++t) S[t] = b[t];
+            for (int t = 0; t < NT; ++t) *reinterpret_cast<facc *>(to + t * 256) = out[t];
         }
+    }
+    if (act) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) (at_s + (16 * t + j) * p.dvp)[lane_at] = out[t][j];
+        for (int t = 0; t < NT; ++t) *reinterpret_cast<facc *>(place(ns - 1) + t * 256) = S[t];
     }
 }
 
 // ------------------------------------------------------------------ delta_out
+
+// 32 columns of a matrix of ROWS rows, as it lies in the workspace, into LDS
+// transposed (a piece is four neighbours of a column), times factor[row].
+template <int NP, int ROWS, int THREADS>
+__device__ __forceinline__ void put_slice(const Tile<NP, 32, ROWS> &to, const float *from, const float *factor)
+{
+    constexpr int kAll = ROWS * 32 / 4, kEach = (kAll + THREADS - 1) / THREADS;
+    facc x[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) x[i] = *reinterpret_cast<const facc *>(from + min(i * THREADS + static_cast<int>(threadIdx.x), kAll - 1) * 4);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int w = i * THREADS + threadIdx.x, tile = w / 64, row = 16 * (tile % (ROWS / 16)) + 4 * (w % 64 / 16);
+        if (kAll % THREADS != 0 && w >= kAll) continue;
+        if (factor) x[i] *= *reinterpret_cast<const facc *>(factor + row);
+        to.put4(16 * (tile / (ROWS / 16)) + w % 16, row, x[i][0], x[i][1], x[i][2], x[i][3]);
+    }
+}
 
 // O of one chunk and head: workgroup (slot, head), 32 columns at a time.
 template <typename T, int KD>
@@ -1008,8 +1088,8 @@ struct OutLds {
     static constexpr int NP = kParts<T>, NPO = sizeof(T) == 2 ? 2 : 3, VS = 32;
     using KT = Tile<NP, kC, KD>;
     using PT = Tile<NPO, kC, kC>;
-    using ST = Tile<NPO, KD, VS>;
-    using UT = Tile<NPO, kC, VS>;
+    using ST = Tile<NPO, VS, KD>;  // transposed
+    using UT = Tile<NPO, VS, kC>;
     // K is done with when the first slices come
     static constexpr int kSlices = ST::kBytes + UT::kBytes, kShared = KT::kBytes > kSlices ? KT::kBytes : kSlices;
     static constexpr int kBytes = KT::kBytes + PT::kBytes + kShared + kGates * 4;
@@ -1046,17 +1126,8 @@ __global__ __launch_bounds__(256) void delta_out(ChunkParams p)
     T *op = static_cast<T *>(p.o) + ((c.b * p.tokens + c.t0 + i) * p.h + head) * p.dv_;
     for (int v0 = 0; v0 < p.dvp; v0 += VS) {
         __syncthreads();
-        for (int w = threadIdx.x; w < KD * VS / 4; w += 256) {
-            const int row = w / (VS / 4), col = 4 * (w % (VS / 4));
-            const facc x = *reinterpret_cast<const facc *>(p.s0 + (at * KD + row) * p.dvp + v0 + col);
-            st.put4(row, col, x[0], x[1], x[2], x[3]);
-        }
-        for (int w = threadIdx.x; w < kC * VS / 4; w += 256) {
-            const int row = w / (VS / 4), col = 4 * (w % (VS / 4));
-            const facc x = *reinterpret_cast<const facc *>(p.e + (at * kC + row) * p.dvp + v0 + col);
-            const float b = gt[2 * kC + row];
-            ut.put4(row, col, b * x[0], b * x[1], b * x[2], b * x[3]);
-        }
+        put_slice<NPO, KD, 256>(st, p.s0 + at * KD * p.dvp + v0 * KD, nullptr);
+        put_slice<NPO, kC, 256>(ut, p.e + at * kC * p.dvp + v0 * kC, gt + 2 * kC);
         __syncthreads();
         // rows v, columns tokens i: four neighbouring v a lane
         facc acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
@@ -1067,7 +1138,7 @@ __global__ __launch_bounds__(256) void delta_out(ChunkParams p)
 #pragma unroll
             for (int vt = 0; vt < 2; ++vt) {
                 bfrag a[NPO];
-                st.cols(32 * ks, 16 * vt, a);
+                st.rows(16 * vt, 32 * ks, a);
                 mma<NPO, NP>(acc[vt], a, b);
             }
         }
@@ -1083,7 +1154,7 @@ __global__ __launch_bounds__(256) void delta_out(ChunkParams p)
 #pragma unroll
             for (int vt = 0; vt < 2; ++vt) {
                 bfrag a[NPO];
-                ut.cols(32 * ks, 16 * vt, a);
+                ut.rows(16 * vt, 32 * ks, a);
                 mma<NPO, NPO>(acc[vt], a, b);
             }
         }
@@ -1116,12 +1187,12 @@ struct LocalLds {
     using KT = Tile<NP, kC, KD>;
     using PT = Tile<3, kC, kC>;
     using OT = Tile<NP, kC, VS>;
-    using UT = Tile<3, kC, VS>;
-    using ST = Tile<3, KD, VS>;
+    using UT = Tile<3, VS, kC>;  // transposed
+    using ST = Tile<3, VS, KD>;
     static constexpr int kSlices = OT::kBytes + 2 * UT::kBytes + 2 * ST::kBytes, kAfter = 2 * KT::kBytes + 2 * PT::kBytes;
     static constexpr int kMain = kSlices > kAfter ? kSlices : kAfter;
     // gates, sums of dG and dbeta (a row a wave or half), sums over the chunk
-    static constexpr int kSums = kGates + 2 * kC + kC + 16;
+    static constexpr int kSums = kGates + 2 * kC + 2 * kC + 16;
     static constexpr int kBytes = kMain + kSums * 4;
 };
 
@@ -1141,7 +1212,7 @@ __global__ __launch_bounds__(512, 1) void delta_local(ChunkParams p)
     const typename L::ST st{rt_.p + L::UT::kBytes / 2}, dt{st.p + L::ST::kBytes / 2};
     const typename L::KT qt{lds}, kt{lds + L::KT::kBytes / 2};
     const typename L::PT pt{lds + L::KT::kBytes}, nt{pt.p + L::PT::kBytes / 2};
-    float *gt = reinterpret_cast<float *>(lds + L::kMain / 2), *sg = gt + kGates, *sb = sg + 2 * kC, *sw = sb + kC;
+    float *gt = reinterpret_cast<float *>(lds + L::kMain / 2), *sg = gt + kGates, *sb = sg + 2 * kC, *sw = sb + 2 * kC;
     facc dq[NT], dk[NT];  // rows 16 (half NT + t) + 4 g4 + r (dims), column i, over the heads of the group
 #pragma unroll
     for (int t = 0; t < NT; ++t) dq[t] = dk[t] = facc{0, 0, 0, 0};
@@ -1150,7 +1221,6 @@ __global__ __launch_bounds__(512, 1) void delta_local(ChunkParams p)
         const long at = slot * p.nh + hl;
         __syncthreads();
         for (int w = threadIdx.x; w < kGates; w += 512) gt[w] = p.gates[at * kGates + w];
-        if (threadIdx.x < kC) sb[threadIdx.x] = 0.0f;
         __syncthreads();
         const T *op = static_cast<const T *>(p.dout) + c.b * p.os[0] + c.t0 * p.os[1] + head * p.os[2];
         facc aq[NT], ar[NT], ac[NT], ap[2], an[2];
@@ -1158,53 +1228,53 @@ __global__ __launch_bounds__(512, 1) void delta_local(ChunkParams p)
         for (int t = 0; t < NT; ++t) aq[t] = ar[t] = ac[t] = facc{0, 0, 0, 0};
 #pragma unroll
         for (int t = 0; t < 2; ++t) ap[t] = an[t] = facc{0, 0, 0, 0};
-        float sd = 0.0f;  // <S0, D1>, this thread's part
+        float sd = 0.0f;              // <S0, D1>, this thread's part
+        facc db = {0, 0, 0, 0};       // dR . E of this thread's four tokens and its columns
+        const int tok = 16 * (threadIdx.x / 64 % 4) + 4 * g4, pcol = 16 * (threadIdx.x / 256) + l % 16;
         for (int v0 = 0; v0 < p.dvp; v0 += VS) {
             {
                 Stage<T, VS, 512> so;
                 so.load(op + v0, p.os[1], c.len, p.dv_ - v0, p.vec_do);
                 so.put(ot);
             }
-            {   // 64 x 32: one piece a thread
-                const int row = threadIdx.x / 8, col = 4 * (threadIdx.x % 8);
-                const facc x = *reinterpret_cast<const facc *>(p.e + (at * kC + row) * p.dvp + v0 + col);
-                const facc y = *reinterpret_cast<const facc *>(p.dr + (at * kC + row) * p.dvp + v0 + col);
-                const float b = gt[2 * kC + row];
-                ut.put4(row, col, b * x[0], b * x[1], b * x[2], b * x[3]);
-                rt_.put4(row, col, y[0], y[1], y[2], y[3]);
-                const float dot = lane_sum<8>(x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3]);
-                if (threadIdx.x % 8 == 0) sb[row] += dot;
+            {   // 64 x 32: one piece a thread, four tokens of a column
+                const facc x = *reinterpret_cast<const facc *>(p.e + at * kC * p.dvp + v0 * kC + threadIdx.x * 4);
+                const facc y = *reinterpret_cast<const facc *>(p.dr + at * kC * p.dvp + v0 * kC + threadIdx.x * 4);
+                const facc u = x * *reinterpret_cast<const facc *>(gt + 2 * kC + tok);
+                ut.put4(pcol, tok, u[0], u[1], u[2], u[3]);
+                rt_.put4(pcol, tok, y[0], y[1], y[2], y[3]);
+                db += x * y;
             }
 #pragma unroll
             for (int w = threadIdx.x; w < KD * VS / 4; w += 512) {
-                const int row = w / (VS / 4), col = 4 * (w % (VS / 4));
-                const facc x = *reinterpret_cast<const facc *>(p.s0 + (at * KD + row) * p.dvp + v0 + col);
-                const facc y = *reinterpret_cast<const facc *>(p.d1 + (at * KD + row) * p.dvp + v0 + col);
-                st.put4(row, col, x[0], x[1], x[2], x[3]);
-                dt.put4(row, col, y[0], y[1], y[2], y[3]);
+                const facc x = *reinterpret_cast<const facc *>(p.s0 + at * KD * p.dvp + v0 * KD + w * 4);
+                const facc y = *reinterpret_cast<const facc *>(p.d1 + at * KD * p.dvp + v0 * KD + w * 4);
+                const int tile = w / 64, row = 16 * (tile % (KD / 16)) + 4 * (w % 64 / 16), col = 16 * (tile / (KD / 16)) + w % 16;
+                st.put4(col, row, x[0], x[1], x[2], x[3]);
+                dt.put4(col, row, y[0], y[1], y[2], y[3]);
                 sd += x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3];
             }
             __syncthreads();
             bfrag fo[NP], fr[3], fu[3];
             ot.rows(16 * rt, 0, fo);
-            rt_.rows(16 * rt, 0, fr);
+            rt_.cols(0, 16 * rt, fr);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const int jt = 2 * half + t;
                 if (jt > rt) continue;
                 bfrag a[3];
-                ut.rows(16 * jt, 0, a);
+                ut.cols(0, 16 * jt, a);
                 mma<3, NP>(ap[t], a, fo);
                 mma<3, 3>(an[t], a, fr);
             }
-            ut.rows(16 * rt, 0, fu);
+            ut.cols(0, 16 * rt, fu);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 bfrag a[3];
-                st.rows(16 * (half * NT + t), 0, a);
+                st.cols(0, 16 * (half * NT + t), a);
                 mma<3, NP>(aq[t], a, fo);
                 mma<3, 3>(ar[t], a, fr);
-                dt.rows(16 * (half * NT + t), 0, a);
+                dt.cols(0, 16 * (half * NT + t), a);
                 mma<3, 3>(ac[t], a, fu);
             }
             __syncthreads();
@@ -1291,6 +1361,9 @@ __global__ __launch_bounds__(512, 1) void delta_local(ChunkParams p)
         dg += __shfl_xor(dg, 16, 64);
         dg += __shfl_xor(dg, 32, 64);
         if (g4 == 0) sg[half * kC + i] = dg;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) db[j] = lane_sum<16>(db[j]);
+        if (l % 16 == 0) *reinterpret_cast<facc *>(sb + (threadIdx.x / 256) * kC + tok) = db;
         end = lane_sum<64>(end);
         sd = lane_sum<64>(sd);
         if (l == 0) sw[wave] = end, sw[8 + wave] = sd;
@@ -1309,7 +1382,7 @@ __global__ __launch_bounds__(512, 1) void delta_local(ChunkParams p)
             if (t < c.len) {
                 const long out = (c.b * p.tokens + c.t0 + t) * p.h + head;
                 p.dg[out] = s + e + gt[kC - 1] * d;
-                p.dbeta[out] = sb[t];
+                p.dbeta[out] = sb[t] + sb[kC + t];
             }
         }
     }
@@ -1396,6 +1469,8 @@ int chunk_passes(const DeltaArgs &a)
     p.batch = a.batch, p.tokens = a.tokens, p.n_seq = a.n_seq;
     p.chunks_b = (a.tokens + kC - 1) / kC;
     p.slots = a.n_seq > 0 ? a.tokens / kC + a.n_seq : a.batch * p.chunks_b;
+    // (a lane's offset in a chunk's rows of v and dout is kept in 32 bits)
+    if (a.tokens > 1 && (a.vs[1] < 0 || a.vs[1] >= (1 << 26) || (GRAD && (a.os[1] < 0 || a.os[1] >= (1 << 26))))) return SSM2D_ERR_UNSUPPORTED;
     if (p.slots >= (1 << 22)) return SSM2D_ERR_UNSUPPORTED;  // (grids; far beyond memory but for tiny heads)
     p.hk = a.hk, p.h = a.h, p.rep = a.h / a.hk, p.dk_ = a.dk_, p.dv_ = a.dv_, p.dvp = (a.dv_ + 31) / 32 * 32;
     for (int i = 0; i < 3; ++i) {
@@ -1404,6 +1479,7 @@ int chunk_passes(const DeltaArgs &a)
     p.scale = a.scale;
     p.vec_qk = rows_aligned<T>(a.q, a.qs, a.dk_) && rows_aligned<T>(a.k, a.ks, a.dk_);
     p.vec_do = GRAD && rows_aligned<T>(a.dout, a.os, a.dv_);
+    p.vec_v = rows_aligned<T>(a.v, a.vs, a.dv_);
     p.vec_o = !GRAD && a.dv_ % 4 == 0 && !off_by(a.o, 4 * sizeof(T));
     p.vec_dqk = GRAD && a.dk_ % 4 == 0 && !off_by(a.dq, 4 * sizeof(T)) && !off_by(a.dk, 4 * sizeof(T));
     const long seqs = a.n_seq > 0 ? a.n_seq : a.batch;
@@ -1412,7 +1488,10 @@ int chunk_passes(const DeltaArgs &a)
     const size_t gates = n * kGates * 4, mm = n * kMWords * 16, st = n * KD * p.dvp * 4, row = n * kC * p.dvp * 4;
     const size_t each = gates + (GRAD ? 2 : 1) * (mm + st + row) + (GRAD ? row : 0);
     constexpr int kDirs = GRAD ? 2 : 1;
-    const int vb = (p.dvp + 63) / 64, pb = (p.dvp + KD + 63) / 64;
+    // columns a workgroup of the chains: 128 share what they read of a chunk,
+    // narrower states leave half of those waves idle
+    const bool wide = !GRAD && p.dvp > 64;
+    const int cols = wide ? 128 : 64, vb = (p.dvp + cols - 1) / cols, pb = (p.dvp + KD + cols - 1) / cols;
     const int nhk = static_cast<int>(std::max(1.0, std::min<double>(a.hk, kMostBytes / (static_cast<double>(each) * p.rep))));
     plan_segments(p, seqs * p.rep * nhk, GRAD, vb, pb);
     const size_t sa = static_cast<size_t>(p.nseg) * KD * KD * 4, ss = static_cast<size_t>(p.nseg) * KD * p.dvp * 4;
@@ -1454,20 +1533,39 @@ int chunk_passes(const DeltaArgs &a)
             delta_z<T, KD><<<dim3(slots, nh), dim3(256), kZ, s>>>(p);
             if ((rc = launched()) != SSM2D_OK) return rc;
         }
-        constexpr int kF = SeqBuf<T, KD, false>::kBufs * SeqBuf<T, KD, false>::kBytes, kB = SeqBuf<T, KD, true>::kBufs * SeqBuf<T, KD, true>::kBytes;
-        constexpr int kSeq = GRAD && kB > kF ? kB : kF;
         const unsigned chains = static_cast<unsigned>(seqs * p.nh);
+        auto run_chains = [&](auto probe, auto threads) -> int {
+            constexpr bool PROBE = decltype(probe)::value;
+            constexpr int THREADS = decltype(threads)::value;
+            using F = SeqBuf<T, KD, false, THREADS>;
+            using B = SeqBuf<T, KD, true, THREADS>;
+            constexpr int kF = F::kBufs * F::kBytes, kB = B::kBufs * B::kBytes, kSeq = GRAD && kB > kF ? kB : kF;
+            const int st2 = big_lds(delta_seq<T, KD, GRAD, PROBE, THREADS>, kSeq);
+            if (st2 != SSM2D_OK) return st2;
+            delta_seq<T, KD, GRAD, PROBE, THREADS>
+                <<<dim3(chains, static_cast<unsigned>(PROBE ? pb : vb), kDirs * p.nseg), dim3(THREADS), kSeq, s>>>(p);
+            return launched();
+        };
+        auto chains_of = [&](auto probe) -> int {
+            if constexpr (!GRAD) {
+                if (wide) return run_chains(probe, std::integral_constant<int, 512>{});
+            }
+            return run_chains(probe, std::integral_constant<int, 256>{});
+        };
         if (p.nseg > 1) {
-            constexpr int kJ = Tile<3, KD, KD>::kBytes;
-            if ((rc = big_lds(delta_seq<T, KD, GRAD, true>, kSeq)) != SSM2D_OK || (rc = big_lds(delta_join<T, KD, GRAD>, kJ)) != SSM2D_OK) return rc;
-            delta_seq<T, KD, GRAD, true><<<dim3(chains, static_cast<unsigned>(pb), kDirs * p.nseg), dim3(256), kSeq, s>>>(p);
-            if ((rc = launched()) != SSM2D_OK) return rc;
-            delta_join<T, KD, GRAD><<<dim3(chains, static_cast<unsigned>(vb), kDirs), dim3(256), kJ, s>>>(p);
-            if ((rc = launched()) != SSM2D_OK) return rc;
+            if ((rc = chains_of(std::true_type{})) != SSM2D_OK) return rc;
+            auto join = [&](auto threads) -> int {
+                constexpr int THREADS = decltype(threads)::value, kJ = Tile<3, KD, KD>::kBytes;
+                const int st2 = big_lds(delta_join<T, KD, GRAD, THREADS>, kJ);
+                if (st2 != SSM2D_OK) return st2;
+                delta_join<T, KD, GRAD, THREADS>
+                    <<<dim3(chains, static_cast<unsigned>((p.dvp + THREADS / 4 - 1) / (THREADS / 4)), kDirs), dim3(THREADS), kJ, s>>>(p);
+                return launched();
+            };
+            rc = p.dvp > 64 ? join(std::integral_constant<int, 512>{}) : join(std::integral_constant<int, 256>{});
+            if (rc != SSM2D_OK) return rc;
         }
-        if ((rc = big_lds(delta_seq<T, KD, GRAD, false>, kSeq)) != SSM2D_OK) return rc;
-        delta_seq<T, KD, GRAD, false><<<dim3(chains, static_cast<unsigned>(vb), kDirs * p.nseg), dim3(256), kSeq, s>>>(p);
-        if ((rc = launched()) != SSM2D_OK) return rc;
+        if ((rc = chains_of(std::false_type{})) != SSM2D_OK) return rc;
         if constexpr (GRAD) {
             constexpr int kL = LocalLds<T, KD>::kBytes;
             if ((rc = big_lds(delta_local<T, KD>, kL)) != SSM2D_OK) return rc;
