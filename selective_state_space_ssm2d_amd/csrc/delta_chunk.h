@@ -329,8 +329,9 @@ struct Stage {
 // ------------------------------------------------------------------ gates
 
 // gamma, Gam_last, beta, G's two parts of a chunk into out[5][kC], by the
-// first wave. G is summed in fp64 and kept as two floats, so that differences
-// of large sums stay exact. Below -1e4 a decay is 0 in any sum: held there,
+// first wave. G is summed in fp64 and kept as two floats in units of log 2 (the
+// hardware's exponential, exact to a unit of the last place, takes powers of
+// two), so that differences of large sums stay exact. Below -1e4 a decay is 0 in any sum: held there,
 // so that -inf gives 0 and not inf - inf.
 __device__ __forceinline__ void make_gates(const ChunkParams &p, const Place &c, int head, float *out)
 {
@@ -342,15 +343,15 @@ __device__ __forceinline__ void make_gates(const ChunkParams &p, const Place &c,
         g = g < -1e4f ? -1e4f : g;
         b = p.beta[c.b * p.bs[0] + (c.t0 + i) * p.bs[1] + head * p.bs[2]];
     }
-    double s = g;
+    double s = g * 1.4426950408889634;
 #pragma unroll
     for (int m = 1; m < 64; m *= 2) {
         const double u = __shfl_up(s, m, 64);
         if (i >= m) s += u;
     }
     const double last = __shfl(s, 63, 64);
-    out[i] = expf(static_cast<float>(s));
-    out[kC + i] = expf(static_cast<float>(last - s));
+    out[i] = __builtin_amdgcn_exp2f(static_cast<float>(s));
+    out[kC + i] = __builtin_amdgcn_exp2f(static_cast<float>(last - s));
     out[2 * kC + i] = b;
     const float hi = static_cast<float>(s);
     out[3 * kC + i] = hi;
@@ -358,7 +359,7 @@ __device__ __forceinline__ void make_gates(const ChunkParams &p, const Place &c,
 }
 __device__ __forceinline__ float gam(const float *gt, int i, int j)
 {
-    return expf((gt[3 * kC + i] - gt[3 * kC + j]) + (gt[4 * kC + i] - gt[4 * kC + j]));
+    return __builtin_amdgcn_exp2f((gt[3 * kC + i] - gt[3 * kC + j]) + (gt[4 * kC + i] - gt[4 * kC + j]));
 }
 
 constexpr int kGates = 5 * kC;
@@ -379,15 +380,20 @@ __device__ __forceinline__ facc mfma4(float a, float b, facc c) { return __built
 // for halves of 32 and of 64, in fp32 matrix instructions (20 products of 16^3
 // a head: small beside the split products elsewhere).
 template <typename T, int KD, bool BWD>
-__global__ __launch_bounds__(256) void delta_prep(ChunkParams p)
+__global__ __launch_bounds__(256, 3) void delta_prep(ChunkParams p)
 {
-    constexpr int NP = kParts<T>, kLdM = 68;
-    __shared__ __align__(16) uint16_t kbuf[Tile<NP, kC, KD>::kBytes / 2];
-    __shared__ __align__(16) float sn[kC * kLdM], sm[kC * kLdM], gt[kGates];
+    // K is done with when N and M come: they share its place, so that four
+    // workgroups fit a compute unit (the phases below wait for one another)
+    constexpr int NP = kParts<T>, kLdM = 68, kNM = 2 * kC * kLdM * 4, kK = Tile<NP, kC, KD>::kBytes;
+    __shared__ __align__(16) unsigned char buf[kK > kNM ? kK : kNM];
+    __shared__ __align__(16) float gt[kGates];
+    uint16_t *kbuf = reinterpret_cast<uint16_t *>(buf);
+    float *sn = reinterpret_cast<float *>(buf), *sm = sn + kC * kLdM;
     const long slot = blockIdx.x;
     const Place c = find_chunk(p, slot);
     if (c.len == 0) return;
-    const int hk = p.hk0 + blockIdx.y, wave = threadIdx.x / 64, l = threadIdx.x % 64, g4 = l / 16, l16 = l % 16;
+    const int hk = p.hk0 + blockIdx.y, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64;
+    int g4 = l / 16, l16 = l % 16;
     const Tile<NP, kC, KD> kt{kbuf};
     {
         Stage<T, KD, 256> st;
@@ -410,32 +416,53 @@ __global__ __launch_bounds__(256) void delta_prep(ChunkParams p)
     }
     for (int r = 0; r < p.rep; ++r) {
         const int hl = blockIdx.y * p.rep + r;  // head of this pass
+        asm volatile("" : "+v"(g4), "+v"(l16));  // (else the addresses of the whole body are kept across heads, in 200 registers)
         __syncthreads();
         make_gates(p, c, hk * p.rep + r, gt);
         __syncthreads();
         const long at = slot * p.nh + hl;
         for (int i = threadIdx.x; i < kGates; i += 256) p.gates[at * kGates + i] = gt[i];
-        // N
+        {   // N (in the blocks on the diagonal with its mirror image, read below)
+            const facc hi = *reinterpret_cast<const facc *>(gt + 3 * kC + 16 * wave + 4 * g4), lo = *reinterpret_cast<const facc *>(gt + 4 * kC + 16 * wave + 4 * g4);
 #pragma unroll
-        for (int ct = 0; ct < 4; ++ct)
+            for (int ct = 0; ct < 4; ++ct) {
+                const int col = 16 * ct + l16;
+                const float chi = gt[3 * kC + col], clo = gt[4 * kC + col];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int row = 16 * wave + 4 * g4 + j, col = 16 * ct + l16;
-                sn[row * kLdM + col] = col < row ? gam(gt, row, col) * kk[ct][j] : 0.0f;
-                if (ct > wave) sm[row * kLdM + col] = 0.0f;
+                for (int j = 0; j < 4; ++j) {
+                    const int row = 16 * wave + 4 * g4 + j;
+                    if (ct > wave) {
+                        sm[row * kLdM + col] = 0.0f;
+                    } else {
+                        const float d = (hi[j] - chi) + (lo[j] - clo);
+                        sn[row * kLdM + col] = col == row ? 0.0f : __builtin_amdgcn_exp2f(col < row ? d : -d) * kk[ct][j];
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
+        }
         __syncthreads();
         const float *beta = gt + 2 * kC;
         {   // diagonal block `wave`, column l16 (each 16 lanes the same)
             const int o = 16 * wave;
-            float m[16], mb[16];
+            // (row i is final once rows before it have been taken off; then it
+            // is taken off the rows below, which do not wait for one another)
+            float m[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                float s = sn[(o + i) * kLdM + o + l16];
+                const float x = sn[(o + i) * kLdM + o + l16];
+                m[i] = i > l16 ? x : 0.0f;
+            }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int k = 0; k < i; ++k) s = fmaf(-sn[(o + i) * kLdM + o + k], mb[k], s);
-                m[i] = i > l16 ? s : 0.0f;
-                mb[i] = beta[o + i] * m[i];
+            for (int i = 1; i < 15; ++i) {
+                facc row[4];  // N below row i in column i, from its mirror image
+#pragma unroll
+                for (int k = (i + 1) / 4; k < 4; ++k) row[k] = *reinterpret_cast<const facc *>(sn + (o + i) * kLdM + o + 4 * k);
+                const float x = beta[o + i] * m[i];
+#pragma unroll
+                for (int k = i + 1; k < 16; ++k) m[k] = fmaf(-row[k / 4][k % 4], x, m[k]);
+                if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);  // (else all rows are read at once, into 120 registers)
             }
             if (g4 == 0) {
 #pragma unroll
@@ -1428,33 +1455,27 @@ int big_lds(F *kernel, int bytes)
 // Segments of the chains. Whole, a chain of n chunks takes n steps, and the
 // `chains` * vb workgroups of all chains (twice that with the adjoints') may
 // leave compute units idle. In P segments: ceil(n / P) steps of the probes
-// (pb blocks of columns a chain), about a step a segment to join them, and
+// (pb blocks of columns a chain), `join` of a step a segment to join them, and
 // ceil(n / P) steps again. The P with the fewest steps is taken, counting
-// rounds of 256 workgroups. Packed sequences' lengths are on the device: there
-// a segment is as long as makes the segments of all tokens 256 workgroups (at
-// least 8 chunks), and sequences no longer than that are not cut.
-inline void plan_segments(ChunkParams &p, long chains, bool grad, int vb, int pb)
+// rounds of `units` workgroups. Packed sequences' lengths are on the device:
+// there the counts are bounds (at most total / len + n_seq segments hold
+// tokens, at most total / len of one sequence), and a sequence no longer than
+// a segment is not cut.
+inline void plan_segments(ChunkParams &p, long chains, bool grad, int vb, int pb, long units, double join)
 {
-    constexpr long kUnits = 256;
-    const long dirs = grad ? 2 : 1;
+    const bool packed = p.n_seq > 0;
+    const long n = packed ? p.tokens / kC + 1 : p.chunks_b, dirs = grad ? 2 : 1;
+    const long heads = packed ? chains / p.n_seq : chains, extra = packed ? p.n_seq : 0;
+    auto rounds = [&](long workgroups) { return (workgroups + units - 1) / units; };
     p.nseg = 1;
-    if (p.n_seq > 0) {
-        const long total = p.tokens / kC + 1, heads = chains / p.n_seq;
-        const long len = std::max<long>(8, (total * heads * vb * dirs + kUnits - 1) / kUnits);
-        p.seg_len = static_cast<int>(len);
-        if (chains * vb * dirs < 4 * kUnits) p.nseg = static_cast<int>(std::min<long>((total + len - 1) / len, 1024));
-        if (p.nseg > 1) p.seg_len = static_cast<int>((total + p.nseg - 1) / p.nseg);
-        else p.seg_len = static_cast<int>(total);
-        return;
-    }
-    const long n = p.chunks_b, w = chains * vb * dirs, w1 = chains * (pb + (grad ? vb : 0));
-    long best = n * ((w + kUnits - 1) / kUnits), at = 1;
+    p.seg_len = static_cast<int>(n);
+    if (chains * vb * dirs >= 4 * units) return;
+    double best = static_cast<double>(n * rounds(chains * vb * dirs));
     for (long k = 2; k <= std::min<long>(n / 4, 256); ++k) {
-        const long len = (n + k - 1) / k, steps = len * ((w1 * k + kUnits - 1) / kUnits + (w * k + kUnits - 1) / kUnits) + k;
-        if (steps < best) best = steps, at = k;
+        const long len = (n + k - 1) / k, segs = (k + extra) * heads;
+        const double steps = static_cast<double>(len * (rounds(segs * (pb + (grad ? vb : 0))) + rounds(segs * vb * dirs))) + join * static_cast<double>(k);
+        if (steps < best) best = steps, p.seg_len = static_cast<int>(len), p.nseg = static_cast<int>((n + len - 1) / len);
     }
-    p.seg_len = static_cast<int>((n + at - 1) / at);
-    p.nseg = static_cast<int>((n + p.seg_len - 1) / p.seg_len);
 }
 
 // Workspace of one pass at most (heads beyond it take another pass).
@@ -1489,11 +1510,13 @@ int chunk_passes(const DeltaArgs &a)
     const size_t each = gates + (GRAD ? 2 : 1) * (mm + st + row) + (GRAD ? row : 0);
     constexpr int kDirs = GRAD ? 2 : 1;
     // columns a workgroup of the chains: 128 share what they read of a chunk,
-    // narrower states leave half of those waves idle
-    const bool wide = !GRAD && p.dvp > 64;
+    // narrower states would leave waves idle
+    const bool wide = !GRAD && p.dvp > 64, slim = !GRAD && p.dvp <= 32;
     const int cols = wide ? 128 : 64, vb = (p.dvp + cols - 1) / cols, pb = (p.dvp + KD + cols - 1) / cols;
     const int nhk = static_cast<int>(std::max(1.0, std::min<double>(a.hk, kMostBytes / (static_cast<double>(each) * p.rep))));
-    plan_segments(p, seqs * p.rep * nhk, GRAD, vb, pb);
+    // (measured: a join takes 5.7 us of d_k' = 128, 0.6 us of 32, a step 5 and 3.3 us; two
+    // workgroups fit a compute unit where the state is small)
+    plan_segments(p, seqs * p.rep * nhk, GRAD, vb, pb, !GRAD && KD <= 64 ? 512 : 256, KD == 128 ? 1.0 : (KD == 64 ? 0.4 : 0.2));
     const size_t sa = static_cast<size_t>(p.nseg) * KD * KD * 4, ss = static_cast<size_t>(p.nseg) * KD * p.dvp * 4;
     const size_t seg_each = p.nseg > 1 ? static_cast<size_t>(seqs) * (sa + kDirs * ss) : 0;
     void *ws = nullptr;
@@ -1549,6 +1572,9 @@ int chunk_passes(const DeltaArgs &a)
         auto chains_of = [&](auto probe) -> int {
             if constexpr (!GRAD) {
                 if (wide) return run_chains(probe, std::integral_constant<int, 512>{});
+                if constexpr (!decltype(probe)::value) {
+                    if (slim) return run_chains(probe, std::integral_constant<int, 128>{});
+                }
             }
             return run_chains(probe, std::integral_constant<int, 256>{});
         };
