@@ -63,6 +63,8 @@ struct ChunkParams {
     // [KD][KD], its state from zero and then its first state (forward and
     // adjoint) [KD][dvp]
     float *seg_a, *seg_s, *seg_d;
+    float *sum;                         // dQ and dK of shared heads so far, by [slot][key head]
+    int turn;                           // which of the heads that share a key head (delta_local)
     int nseg, seg_len;                  // segments of the longest sequence, chunks a segment
     long batch, tokens, n_seq, slots, chunks_b;  // chunks_b: chunks of a batch entry
     int hk, h, rep, dk_, dv_, dvp;
@@ -1223,204 +1225,258 @@ struct LocalLds {
     static constexpr int kBytes = kMain + kSums * 4;
 };
 
-template <typename T, int KD>
-__global__ __launch_bounds__(512, 1) void delta_local(ChunkParams p)
+// Two or three sums whose terms take turns, so that none waits for itself.
+template <int NP>
+__device__ __forceinline__ void mma_turns(facc &q, const bfrag (&fq)[NP], facc &r, const bfrag (&fr)[3], const bfrag (&a)[3], facc &c,
+                                          const bfrag (&d)[3], const bfrag (&fc)[3])
+{
+#pragma unroll
+    for (int s = 2; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i <= s; ++i) {
+            r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], fr[s - i], r, 0, 0, 0);
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(d[i], fc[s - i], c, 0, 0, 0);
+            if (s - i < NP) q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], fq[s - i], q, 0, 0, 0);
+        }
+}
+template <int NA, int NB, int NC, int ND>
+__device__ __forceinline__ void mma_two(facc &x, const bfrag (&a)[NA], const bfrag (&b)[NB], facc &y, const bfrag (&c)[NC], const bfrag (&d)[ND])
+{
+    constexpr int kX = NA > NB ? NA : NB, kY = NC > ND ? NC : ND, kMax = kX > kY ? kX : kY;
+#pragma unroll
+    for (int s = kMax - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i <= s; ++i) {
+            if (s < kX && i < NA && s - i < NB) x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[s - i], x, 0, 0, 0);
+            if (s < kY && i < NC && s - i < ND) y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c[i], d[s - i], y, 0, 0, 0);
+        }
+}
+
+// Gradients of one chunk for head p.turn of those that share key head
+// hk0 + blockIdx.y: workgroup (slot, key head), a launch a turn, dQ and dK
+// summed from turn to turn. Wave w holds tokens 16 (w % 4) .. and, of eight
+// waves, half of the dims: the three d_k-wide sums of its tokens stay in
+// accumulators over all slices of 32 columns, the next slice's matrices are
+// read while this one's are multiplied. Four waves where that leaves two
+// workgroups a compute unit (d_k' <= 64): their phases overlap.
+template <typename T, int KD, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, WAVES == 4 ? 2 : 1) void delta_local(ChunkParams p)
 {
     using L = LocalLds<T, KD>;
-    constexpr int NP = L::NP, VS = L::VS, NT = KD / 32;  // NT: tiles of 16 dims a wave
+    constexpr int NP = L::NP, VS = L::VS, THREADS = WAVES * 64, HALVES = WAVES / 4, NT = KD / 16 / HALVES, JT = 4 / HALVES;
+    constexpr int kE = kC * VS / 4 / THREADS, kS = (KD * VS / 4 + THREADS - 1) / THREADS;
+    static_assert(KD * VS / 4 % THREADS == 0 || KD * VS / 4 < THREADS, "pieces of a slice");
     extern __shared__ __align__(16) uint16_t lds[];
     const long slot = blockIdx.x;
     const Place c = find_chunk(p, slot);
     if (c.len == 0) return;
-    const int hk = p.hk0 + blockIdx.y, wave = threadIdx.x / 64, l = threadIdx.x % 64, g4 = l / 16;
-    const int rt = wave % 4, half = wave / 4, i = 16 * rt + l % 16;  // this wave's tokens; its half of the dims and of the columns j
+    const int hk = p.hk0 + blockIdx.y, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64, g4 = l / 16;
+    const int rt = wave % 4, half = wave / 4, i = 16 * rt + l % 16;  // this wave's tokens; its part of the dims and of the columns j
     const typename L::OT ot{lds};
     const typename L::UT ut{lds + L::OT::kBytes / 2}, rt_{ut.p + L::UT::kBytes / 2};
     const typename L::ST st{rt_.p + L::UT::kBytes / 2}, dt{st.p + L::ST::kBytes / 2};
     const typename L::KT qt{lds}, kt{lds + L::KT::kBytes / 2};
     const typename L::PT pt{lds + L::KT::kBytes}, nt{pt.p + L::PT::kBytes / 2};
     float *gt = reinterpret_cast<float *>(lds + L::kMain / 2), *sg = gt + kGates, *sb = sg + 2 * kC, *sw = sb + 2 * kC;
-    facc dq[NT], dk[NT];  // rows 16 (half NT + t) + 4 g4 + r (dims), column i, over the heads of the group
+    const int hl = blockIdx.y * p.rep + p.turn, head = hk * p.rep + p.turn;
+    const long at = slot * p.nh + hl;
+    const T *op = static_cast<const T *>(p.dout) + c.b * p.os[0] + c.t0 * p.os[1] + head * p.os[2];
+    const float *e0 = p.e + at * kC * p.dvp, *r0 = p.dr + at * kC * p.dvp, *s0 = p.s0 + at * KD * p.dvp, *d0 = p.d1 + at * KD * p.dvp;
+    // one slice in registers
+    Stage<T, VS, THREADS> so;
+    facc xe[kE], xr[kE], xs[kS], xd[kS];
+    auto fetch = [&](int v0) __attribute__((always_inline)) {
+        so.load(op + v0, p.os[1], c.len, p.dv_ - v0, p.vec_do);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) dq[t] = dk[t] = facc{0, 0, 0, 0};
-    for (int r = 0; r < p.rep; ++r) {
-        const int hl = blockIdx.y * p.rep + r, head = hk * p.rep + r;
-        const long at = slot * p.nh + hl;
-        __syncthreads();
-        for (int w = threadIdx.x; w < kGates; w += 512) gt[w] = p.gates[at * kGates + w];
-        __syncthreads();
-        const T *op = static_cast<const T *>(p.dout) + c.b * p.os[0] + c.t0 * p.os[1] + head * p.os[2];
-        facc aq[NT], ar[NT], ac[NT], ap[2], an[2];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) aq[t] = ar[t] = ac[t] = facc{0, 0, 0, 0};
-#pragma unroll
-        for (int t = 0; t < 2; ++t) ap[t] = an[t] = facc{0, 0, 0, 0};
-        float sd = 0.0f;              // <S0, D1>, this thread's part
-        facc db = {0, 0, 0, 0};       // dR . E of this thread's four tokens and its columns
-        const int tok = 16 * (threadIdx.x / 64 % 4) + 4 * g4, pcol = 16 * (threadIdx.x / 256) + l % 16;
-        for (int v0 = 0; v0 < p.dvp; v0 += VS) {
-            {
-                Stage<T, VS, 512> so;
-                so.load(op + v0, p.os[1], c.len, p.dv_ - v0, p.vec_do);
-                so.put(ot);
-            }
-            {   // 64 x 32: one piece a thread, four tokens of a column
-                const facc x = *reinterpret_cast<const facc *>(p.e + at * kC * p.dvp + v0 * kC + threadIdx.x * 4);
-                const facc y = *reinterpret_cast<const facc *>(p.dr + at * kC * p.dvp + v0 * kC + threadIdx.x * 4);
-                const facc u = x * *reinterpret_cast<const facc *>(gt + 2 * kC + tok);
-                ut.put4(pcol, tok, u[0], u[1], u[2], u[3]);
-                rt_.put4(pcol, tok, y[0], y[1], y[2], y[3]);
-                db += x * y;
-            }
-#pragma unroll
-            for (int w = threadIdx.x; w < KD * VS / 4; w += 512) {
-                const facc x = *reinterpret_cast<const facc *>(p.s0 + at * KD * p.dvp + v0 * KD + w * 4);
-                const facc y = *reinterpret_cast<const facc *>(p.d1 + at * KD * p.dvp + v0 * KD + w * 4);
-                const int tile = w / 64, row = 16 * (tile % (KD / 16)) + 4 * (w % 64 / 16), col = 16 * (tile / (KD / 16)) + w % 16;
-                st.put4(col, row, x[0], x[1], x[2], x[3]);
-                dt.put4(col, row, y[0], y[1], y[2], y[3]);
-                sd += x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3];
-            }
-            __syncthreads();
-            bfrag fo[NP], fr[3], fu[3];
-            ot.rows(16 * rt, 0, fo);
-            rt_.cols(0, 16 * rt, fr);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int jt = 2 * half + t;
-                if (jt > rt) continue;
-                bfrag a[3];
-                ut.cols(0, 16 * jt, a);
-                mma<3, NP>(ap[t], a, fo);
-                mma<3, 3>(an[t], a, fr);
-            }
-            ut.cols(0, 16 * rt, fu);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                bfrag a[3];
-                st.cols(0, 16 * (half * NT + t), a);
-                mma<3, NP>(aq[t], a, fo);
-                mma<3, 3>(ar[t], a, fr);
-                dt.cols(0, 16 * (half * NT + t), a);
-                mma<3, 3>(ac[t], a, fu);
-            }
-            __syncthreads();
+        for (int k = 0; k < kE; ++k) {
+            xe[k] = *reinterpret_cast<const facc *>(e0 + v0 * kC + (k * THREADS + threadIdx.x) * 4);
+            xr[k] = *reinterpret_cast<const facc *>(r0 + v0 * kC + (k * THREADS + threadIdx.x) * 4);
         }
-        {   // rows' factors, and the triangular matrices into LDS
-            const float ga = gt[i], gl = gt[kC + i], be = gt[2 * kC + i];
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    aq[t][j] *= p.scale * ga;
-                    ar[t][j] *= -ga * be;
-                    ac[t][j] *= gl;
-                }
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int j0 = 16 * (2 * half + t) + 4 * g4;
-                float x[4], y[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float f = j0 + j <= i ? gam(gt, i, j0 + j) : 0.0f;
-                    x[j] = j0 + j <= i ? p.scale * f * ap[t][j] : 0.0f;
-                    y[j] = j0 + j < i ? -be * f * an[t][j] : 0.0f;
-                }
-                pt.put4(i, j0, x[0], x[1], x[2], x[3]);
-                nt.put4(i, j0, y[0], y[1], y[2], y[3]);
-            }
-            Stage<T, KD, 512> a, b;
-            a.load(static_cast<const T *>(p.q) + c.b * p.qs[0] + c.t0 * p.qs[1] + hk * p.qs[2], p.qs[1], c.len, p.dk_, p.vec_qk);
-            b.load(static_cast<const T *>(p.k) + c.b * p.ks[0] + c.t0 * p.ks[1] + hk * p.ks[2], p.ks[1], c.len, p.dk_, p.vec_qk);
-            a.put(qt);
-            b.put(kt);
+        for (int k = 0; k < kS; ++k) {
+            const int w = min(k * THREADS + static_cast<int>(threadIdx.x), KD * VS / 4 - 1);
+            xs[k] = *reinterpret_cast<const facc *>(s0 + v0 * KD + w * 4);
+            xd[k] = *reinterpret_cast<const facc *>(d0 + v0 * KD + w * 4);
         }
-        __syncthreads();
-        float end = 0.0f;  // sum over this lane's dims of k . (Gam_last U D1^T)
+    };
+    fetch(0);
+    for (int w = threadIdx.x; w < kGates; w += THREADS) gt[w] = p.gates[at * kGates + w];
+    __syncthreads();
+    facc aq[NT], ar[NT], ac[NT], ap[JT], an[JT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) aq[t] = ar[t] = ac[t] = facc{0, 0, 0, 0};
+#pragma unroll
+    for (int t = 0; t < JT; ++t) ap[t] = an[t] = facc{0, 0, 0, 0};
+    float sd = 0.0f;         // <S0, D1>, this thread's part
+    facc db = {0, 0, 0, 0};  // dR . E of this thread's four tokens and its columns
+    const int tok = 16 * rt + 4 * g4;
+    for (int v0 = 0; v0 < p.dvp; v0 += VS) {
+        so.put(ot);
+#pragma unroll
+        for (int k = 0; k < kE; ++k) {  // 64 x 32: a piece is four tokens of a column
+            const int pcol = 16 * ((k * THREADS + static_cast<int>(threadIdx.x)) / 256) + l % 16;
+            const facc u = xe[k] * *reinterpret_cast<const facc *>(gt + 2 * kC + tok);
+            ut.put4(pcol, tok, u[0], u[1], u[2], u[3]);
+            rt_.put4(pcol, tok, xr[k][0], xr[k][1], xr[k][2], xr[k][3]);
+            db += xe[k] * xr[k];
+        }
+#pragma unroll
+        for (int k = 0; k < kS; ++k) {
+            const int w = k * THREADS + threadIdx.x, tile = w / 64, row = 16 * (tile % (KD / 16)) + 4 * g4, col = 16 * (tile / (KD / 16)) + l % 16;
+            if (KD * VS / 4 % THREADS == 0 || w < KD * VS / 4) {
+                st.put4(col, row, xs[k][0], xs[k][1], xs[k][2], xs[k][3]);
+                dt.put4(col, row, xd[k][0], xd[k][1], xd[k][2], xd[k][3]);
+                const facc m = xs[k] * xd[k];
+                sd += (m[0] + m[1]) + (m[2] + m[3]);
+            }
+        }
+        lds_barrier();
+        if (v0 + VS < p.dvp) fetch(v0 + VS);
+        bfrag fo[NP], fr[3], fu[3];
+        ot.rows(16 * rt, 0, fo);
+        rt_.cols(0, 16 * rt, fr);
+        ut.cols(0, 16 * rt, fu);
+#pragma unroll
+        for (int t = 0; t < JT; ++t) {
+            const int jt = JT * half + t;
+            if (jt > rt) continue;
+            bfrag a[3];
+            ut.cols(0, 16 * jt, a);
+            mma_two<3, NP, 3, 3>(ap[t], a, fo, an[t], a, fr);
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            float x[4];
-            kt.get4(i, 16 * (half * NT + t) + 4 * g4, x);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) end += x[j] * ac[t][j];
+            bfrag a[3], d[3];
+            st.cols(0, 16 * (half * NT + t), a);
+            dt.cols(0, 16 * (half * NT + t), d);
+            mma_turns<NP>(aq[t], fo, ar[t], fr, a, ac[t], d, fu);
         }
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            if (32 * ks <= 16 * rt + 15) {  // j <= i
-                bfrag fp[3], fn[3];
-                pt.rows(16 * rt, 32 * ks, fp);
-                nt.rows(16 * rt, 32 * ks, fn);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    bfrag a[NP];
-                    kt.cols(32 * ks, 16 * (half * NT + t), a);
-                    mma<NP, 3>(aq[t], a, fp);
-                    mma<NP, 3>(ar[t], a, fn);
-                }
-            }
-            if (32 * ks + 31 >= 16 * rt) {  // this wave's tokens as j, i >= j
-                bfrag fp[3], fn[3];
-                pt.cols(32 * ks, 16 * rt, fp);
-                nt.cols(32 * ks, 16 * rt, fn);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    bfrag a[NP];
-                    qt.cols(32 * ks, 16 * (half * NT + t), a);
-                    mma<NP, 3>(ac[t], a, fp);
-                    kt.cols(32 * ks, 16 * (half * NT + t), a);
-                    mma<NP, 3>(ac[t], a, fn);
-                }
-            }
-        }
-        float dg = 0.0f;
+        lds_barrier();
+    }
+    {   // rows' factors, and the triangular matrices into LDS
+        Stage<T, KD, THREADS> a, b;
+        a.load(static_cast<const T *>(p.q) + c.b * p.qs[0] + c.t0 * p.qs[1] + hk * p.qs[2], p.qs[1], c.len, p.dk_, p.vec_qk);
+        b.load(static_cast<const T *>(p.k) + c.b * p.ks[0] + c.t0 * p.ks[1] + hk * p.ks[2], p.ks[1], c.len, p.dk_, p.vec_qk);
+        const float ga = gt[i], gl = gt[kC + i], be = gt[2 * kC + i];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
+            aq[t] *= p.scale * ga;
+            ar[t] *= -ga * be;
+            ac[t] *= gl;
+        }
+#pragma unroll
+        for (int t = 0; t < JT; ++t) {
+            const int j0 = 16 * (JT * half + t) + 4 * g4;
             float x[4], y[4];
-            qt.get4(i, 16 * (half * NT + t) + 4 * g4, x);
-            kt.get4(i, 16 * (half * NT + t) + 4 * g4, y);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                dg += x[j] * aq[t][j] + y[j] * (ar[t][j] - ac[t][j]);
-                dq[t][j] += aq[t][j];
-                dk[t][j] += ar[t][j] + ac[t][j];
+                const float f = j0 + j <= i ? gam(gt, i, j0 + j) : 0.0f;
+                x[j] = j0 + j <= i ? p.scale * f * ap[t][j] : 0.0f;
+                y[j] = j0 + j < i ? -be * f * an[t][j] : 0.0f;
+            }
+            pt.put4(i, j0, x[0], x[1], x[2], x[3]);
+            nt.put4(i, j0, y[0], y[1], y[2], y[3]);
+        }
+        a.put(qt);
+        b.put(kt);
+    }
+    lds_barrier();
+    float end = 0.0f;  // sum over this lane's dims of k . (Gam_last U D1^T)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        float x[4];
+        kt.get4(i, 16 * (half * NT + t) + 4 * g4, x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) end += x[j] * ac[t][j];
+    }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+        if (32 * ks <= 16 * rt + 15) {  // j <= i
+            bfrag fp[3], fn[3];
+            pt.rows(16 * rt, 32 * ks, fp);
+            nt.rows(16 * rt, 32 * ks, fn);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                bfrag a[NP];
+                kt.cols(32 * ks, 16 * (half * NT + t), a);
+                mma_two<NP, 3, NP, 3>(aq[t], a, fp, ar[t], a, fn);
             }
         }
-        dg += __shfl_xor(dg, 16, 64);
-        dg += __shfl_xor(dg, 32, 64);
-        if (g4 == 0) sg[half * kC + i] = dg;
+        if (32 * ks + 31 >= 16 * rt) {  // this wave's tokens as j, i >= j
+            bfrag fp[3], fn[3];
+            pt.cols(32 * ks, 16 * rt, fp);
+            nt.cols(32 * ks, 16 * rt, fn);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) db[j] = lane_sum<16>(db[j]);
-        if (l % 16 == 0) *reinterpret_cast<facc *>(sb + (threadIdx.x / 256) * kC + tok) = db;
-        end = lane_sum<64>(end);
-        sd = lane_sum<64>(sd);
-        if (l == 0) sw[wave] = end, sw[8 + wave] = sd;
-        __syncthreads();
-        if (threadIdx.x < kC) {
-            const int t = threadIdx.x;
-            float e = 0.0f, d = 0.0f;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) e += sw[w], d += sw[8 + w];
-            float s = sg[t] + sg[kC + t];
-#pragma unroll
-            for (int m = 1; m < 64; m *= 2) {
-                const float u = __shfl_down(s, m, 64);
-                if (t + m < 64) s += u;
+            for (int t = 0; t < NT; ++t) {
+                bfrag a[NP], d[NP];
+                facc x = {0, 0, 0, 0};
+                qt.cols(32 * ks, 16 * (half * NT + t), a);
+                kt.cols(32 * ks, 16 * (half * NT + t), d);
+                mma_two<NP, 3, NP, 3>(ac[t], a, fp, x, d, fn);
+                ac[t] += x;
             }
-            if (t < c.len) {
-                const long out = (c.b * p.tokens + c.t0 + t) * p.h + head;
-                p.dg[out] = s + e + gt[kC - 1] * d;
-                p.dbeta[out] = sb[t] + sb[kC + t];
-            }
+        }
+    }
+    float dg = 0.0f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        float x[4], y[4];
+        qt.get4(i, 16 * (half * NT + t) + 4 * g4, x);
+        kt.get4(i, 16 * (half * NT + t) + 4 * g4, y);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dg += x[j] * aq[t][j] + y[j] * (ar[t][j] - ac[t][j]);
+    }
+    dg += __shfl_xor(dg, 16, 64);
+    dg += __shfl_xor(dg, 32, 64);
+    if (g4 == 0) sg[half * kC + i] = dg;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) db[j] = lane_sum<16>(db[j]);
+    if (l % 16 == 0) *reinterpret_cast<facc *>(sb + half * kC + tok) = db;
+    end = lane_sum<64>(end);
+    sd = lane_sum<64>(sd);
+    if (l == 0) sw[wave] = end, sw[8 + wave] = sd;
+    lds_barrier();
+    if (threadIdx.x < kC) {
+        const int t = threadIdx.x;
+        float e = 0.0f, d = 0.0f, s = sg[t], be = sb[t];
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) e += sw[w], d += sw[8 + w];
+        if constexpr (HALVES == 2) s += sg[kC + t], be += sb[kC + t];
+#pragma unroll
+        for (int m = 1; m < 64; m *= 2) {
+            const float u = __shfl_down(s, m, 64);
+            if (t + m < 64) s += u;
+        }
+        if (t < c.len) {
+            const long out = (c.b * p.tokens + c.t0 + t) * p.h + head;
+            p.dg[out] = s + e + gt[kC - 1] * d;
+            p.dbeta[out] = be;
+        }
+    }
+    // dQ in aq, dK in ar: rows 16 (half NT + t) + 4 g4 + j (dims), column i
+#pragma unroll
+    for (int t = 0; t < NT; ++t) ar[t] += ac[t];
+    if (p.rep > 1) {
+        facc *sum = reinterpret_cast<facc *>(p.sum) + (slot * p.nhk + blockIdx.y) * (2 * NT * THREADS) + threadIdx.x;
+        if (p.turn > 0) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) aq[t] += sum[(2 * t) * THREADS], ar[t] += sum[(2 * t + 1) * THREADS];
+        }
+        if (p.turn + 1 < p.rep) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) sum[(2 * t) * THREADS] = aq[t], sum[(2 * t + 1) * THREADS] = ar[t];
+            return;
         }
     }
     if (i < c.len) {
         const long row = ((c.b * p.tokens + c.t0 + i) * p.hk + hk) * p.dk_;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
+            const facc vq = aq[t], vk = ar[t];
             const int d0 = 16 * (half * NT + t) + 4 * g4;
             T *a = static_cast<T *>(p.dq) + row + d0, *b = static_cast<T *>(p.dk) + row + d0;
             if (p.vec_dqk && d0 + 4 <= p.dk_) {
-                float x[4] = {dq[t][0], dq[t][1], dq[t][2], dq[t][3]}, y[4] = {dk[t][0], dk[t][1], dk[t][2], dk[t][3]};
+                float x[4] = {vq[0], vq[1], vq[2], vq[3]}, y[4] = {vk[0], vk[1], vk[2], vk[3]};
                 Raw<T, 4> w;
                 w.set(x);
                 w.store(a);
@@ -1429,7 +1485,7 @@ __global__ __launch_bounds__(512, 1) void delta_local(ChunkParams p)
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (d0 + j < p.dk_) store1(a + j, dq[t][j]), store1(b + j, dk[t][j]);
+                    if (d0 + j < p.dk_) store1(a + j, vq[j]), store1(b + j, vk[j]);
             }
         }
     }
@@ -1519,8 +1575,9 @@ int chunk_passes(const DeltaArgs &a)
     plan_segments(p, seqs * p.rep * nhk, GRAD, vb, pb, !GRAD && KD <= 64 ? 512 : 256, KD == 128 ? 1.0 : (KD == 64 ? 0.4 : 0.2));
     const size_t sa = static_cast<size_t>(p.nseg) * KD * KD * 4, ss = static_cast<size_t>(p.nseg) * KD * p.dvp * 4;
     const size_t seg_each = p.nseg > 1 ? static_cast<size_t>(seqs) * (sa + kDirs * ss) : 0;
+    const size_t sums = GRAD && p.rep > 1 ? n * 2 * kC * KD * 4 : 0;  // by key head
     void *ws = nullptr;
-    int rc = get_aux_ws(a.dev, a.stream, kSlotDelta, (each + seg_each) * p.rep * nhk, &ws);
+    int rc = get_aux_ws(a.dev, a.stream, kSlotDelta, ((each + seg_each) * p.rep + sums) * nhk, &ws);
     if (rc != SSM2D_OK) return rc;
     const hipStream_t s = static_cast<hipStream_t>(a.stream);
     for (p.hk0 = 0; p.hk0 < a.hk; p.hk0 += nhk) {
@@ -1547,6 +1604,7 @@ int chunk_passes(const DeltaArgs &a)
             p.seg_s = reinterpret_cast<float *>(take(seqs * ss));
             if (GRAD) p.seg_d = reinterpret_cast<float *>(take(seqs * ss));
         }
+        p.sum = reinterpret_cast<float *>(w);
         const unsigned slots = static_cast<unsigned>(p.slots), nk = static_cast<unsigned>(p.nhk), nh = static_cast<unsigned>(p.nh);
         delta_prep<T, KD, GRAD><<<dim3(slots, nk), dim3(256), 0, s>>>(p);
         if ((rc = launched()) != SSM2D_OK) return rc;
@@ -1593,15 +1651,18 @@ int chunk_passes(const DeltaArgs &a)
         }
         if ((rc = chains_of(std::false_type{})) != SSM2D_OK) return rc;
         if constexpr (GRAD) {
-            constexpr int kL = LocalLds<T, KD>::kBytes;
-            if ((rc = big_lds(delta_local<T, KD>, kL)) != SSM2D_OK) return rc;
-            delta_local<T, KD><<<dim3(slots, nk), dim3(512), kL, s>>>(p);
+            constexpr int kL = LocalLds<T, KD>::kBytes, kWaves = KD <= 64 ? 4 : 8;
+            if ((rc = big_lds(delta_local<T, KD, kWaves>, kL)) != SSM2D_OK) return rc;
+            for (p.turn = 0; p.turn < p.rep; ++p.turn) {
+                delta_local<T, KD, kWaves><<<dim3(slots, nk), dim3(kWaves * 64), kL, s>>>(p);
+                if ((rc = launched()) != SSM2D_OK) return rc;
+            }
         } else {
             constexpr int kO = OutLds<T, KD>::kBytes;
             if ((rc = big_lds(delta_out<T, KD>, kO)) != SSM2D_OK) return rc;
             delta_out<T, KD><<<dim3(slots, nh), dim3(256), kO, s>>>(p);
+            if ((rc = launched()) != SSM2D_OK) return rc;
         }
-        if ((rc = launched()) != SSM2D_OK) return rc;
     }
     return SSM2D_OK;
 }
