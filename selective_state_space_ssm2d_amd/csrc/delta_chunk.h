@@ -200,6 +200,33 @@ __device__ __forceinline__ void mma_each(facc (&acc)[NT], const bfrag (&a)[NT][N
         }
 }
 
+// Two or three sums whose terms take turns, so that none waits for itself.
+template <int NP>
+__device__ __forceinline__ void mma_turns(facc &q, const bfrag (&fq)[NP], facc &r, const bfrag (&fr)[3], const bfrag (&a)[3], facc &c,
+                                          const bfrag (&d)[3], const bfrag (&fc)[3])
+{
+#pragma unroll
+    for (int s = 2; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i <= s; ++i) {
+            r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], fr[s - i], r, 0, 0, 0);
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(d[i], fc[s - i], c, 0, 0, 0);
+            if (s - i < NP) q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], fq[s - i], q, 0, 0, 0);
+        }
+}
+template <int NA, int NB, int NC, int ND>
+__device__ __forceinline__ void mma_two(facc &x, const bfrag (&a)[NA], const bfrag (&b)[NB], facc &y, const bfrag (&c)[NC], const bfrag (&d)[ND])
+{
+    constexpr int kX = NA > NB ? NA : NB, kY = NC > ND ? NC : ND, kMax = kX > kY ? kX : kY;
+#pragma unroll
+    for (int s = kMax - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i <= s; ++i) {
+            if (s < kX && i < NA && s - i < NB) x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[s - i], x, 0, 0, 0);
+            if (s < kY && i < NC && s - i < ND) y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c[i], d[s - i], y, 0, 0, 0);
+        }
+}
+
 // A workgroup barrier for what goes through LDS alone: unlike __syncthreads it
 // does not wait for global loads and stores still in flight.
 __device__ __forceinline__ void lds_barrier()
@@ -540,85 +567,100 @@ __global__ __launch_bounds__(256, 3) void delta_prep(ChunkParams p)
 
 // ------------------------------------------------------------------ P
 
-// Rows 16 rt .. of scale Gam_ij q_i . k_j (j <= i) into `out`, by one wave:
-// lane token i = 16 rt + l % 16, four neighbouring j at a time.
-template <typename T, int KD, int NPP>
-__device__ __forceinline__ void make_p(const Tile<kParts<T>, kC, KD> &qt, const Tile<kParts<T>, kC, KD> &kt, const float *gt, float scale,
-                                       int rt, const Tile<NPP, kC, kC> &out)
+// Rows 16 rt .. of scale Gam_ij q_i . k_j (j <= i), by one wave: column (token)
+// i = 16 rt + l % 16, rows j; fq: the wave's rows of q.
+template <typename T, int KD>
+__device__ __forceinline__ void make_p(const bfrag (&fq)[KD / 32][kParts<T>], const Tile<kParts<T>, kC, KD> &kt, const float *gt, float scale,
+                                       int rt, facc (&out)[4])
 {
     constexpr int NP = kParts<T>;
     const int l = threadIdx.x % 64, i = 16 * rt + l % 16;
 #pragma unroll
     for (int jt = 0; jt < 4; ++jt) {
-        facc acc = {0, 0, 0, 0};
-        if (jt <= rt) {
+        out[jt] = facc{0, 0, 0, 0};
+        if (jt > rt) continue;
+        facc acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};  // two sums, so that a product does not wait for the one before
 #pragma unroll
-            for (int ks = 0; ks < KD / 32; ++ks) {
-                bfrag a[NP], b[NP];
-                kt.rows(16 * jt, 32 * ks, a);
-                qt.rows(16 * rt, 32 * ks, b);
-                mma<NP, NP>(acc, a, b);
-            }
+        for (int ks = 0; ks < KD / 32; ++ks) {
+            bfrag a[NP];
+            kt.rows(16 * jt, 32 * ks, a);
+            mma<NP, NP>(acc[ks % 2], a, fq[ks]);
         }
         const int j0 = 16 * jt + 4 * (l / 16);
-        float x[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = j0 + j <= i ? scale * gam(gt, i, j0 + j) * acc[j] : 0.0f;
-        out.put4(i, j0, x[0], x[1], x[2], x[3]);
+        for (int j = 0; j < 4; ++j) out[jt][j] = j0 + j <= i ? scale * gam(gt, i, j0 + j) * (acc[0][j] + acc[1][j]) : 0.0f;
     }
 }
-
-// Z = scale P^T dO of one chunk and head: workgroup (slot, head).
-template <typename T, int KD>
-__global__ __launch_bounds__(256) void delta_z(ChunkParams p)
+template <int NPP>
+__device__ __forceinline__ void put_p(const facc (&x)[4], int rt, const Tile<NPP, kC, kC> &out)
 {
-    constexpr int NP = kParts<T>, VS = 32;
+    const int l = threadIdx.x % 64;
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt) out.put4(16 * rt + l % 16, 16 * jt + 4 * (l / 16), x[jt][0], x[jt][1], x[jt][2], x[jt][3]);
+}
+
+// Z = scale P^T dO of one chunk and head: workgroup (slot, head). Q and K give
+// their place to P and dO.
+template <typename T, int KD>
+struct ZLds {
+    static constexpr int NP = kParts<T>, VS = 32;
     using KT = Tile<NP, kC, KD>;
     using PT = Tile<3, kC, kC>;
     using VT = Tile<NP, kC, VS>;
+    static constexpr int kAfter = PT::kBytes + VT::kBytes, kMain = 2 * KT::kBytes > kAfter ? 2 * KT::kBytes : kAfter;
+    static constexpr int kBytes = kMain + kGates * 4;
+};
+
+template <typename T, int KD>
+__global__ __launch_bounds__(256) void delta_z(ChunkParams p)
+{
+    using L = ZLds<T, KD>;
+    constexpr int NP = L::NP, VS = L::VS;
     extern __shared__ __align__(16) uint16_t lds[];
     const long slot = blockIdx.x;
     const Place c = find_chunk(p, slot);
     if (c.len == 0) return;
-    const int hl = blockIdx.y, head = p.hk0 * p.rep + hl, hk = head / p.rep, wave = threadIdx.x / 64, l = threadIdx.x % 64;
-    const KT qt{lds}, kt{lds + KT::kBytes / 2};
-    const PT pt{lds + KT::kBytes};
-    const VT ot{lds + KT::kBytes + PT::kBytes / 2};
-    float *gt = reinterpret_cast<float *>(lds + KT::kBytes + PT::kBytes / 2 + VT::kBytes / 2);
+    const int hl = blockIdx.y, head = p.hk0 * p.rep + hl, hk = head / p.rep, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64;
+    const typename L::KT qt{lds}, kt{lds + L::KT::kBytes / 2};
+    const typename L::PT pt{lds};
+    const typename L::VT ot{lds + L::PT::kBytes / 2};
+    float *gt = reinterpret_cast<float *>(lds + L::kMain / 2);
+    const T *op = static_cast<const T *>(p.dout) + c.b * p.os[0] + c.t0 * p.os[1] + head * p.os[2];
+    Stage<T, VS, 256> so;
+    facc x[4];
     {
         Stage<T, KD, 256> a, b;
         a.load(static_cast<const T *>(p.q) + c.b * p.qs[0] + c.t0 * p.qs[1] + hk * p.qs[2], p.qs[1], c.len, p.dk_, p.vec_qk);
         b.load(static_cast<const T *>(p.k) + c.b * p.ks[0] + c.t0 * p.ks[1] + hk * p.ks[2], p.ks[1], c.len, p.dk_, p.vec_qk);
+        so.load(op, p.os[1], c.len, p.dv_, p.vec_do);
         make_gates(p, c, head, gt);
         a.put(qt);
         b.put(kt);
+        lds_barrier();
+        bfrag fq[KD / 32][NP];
+#pragma unroll
+        for (int ks = 0; ks < KD / 32; ++ks) qt.rows(16 * wave, 32 * ks, fq[ks]);
+        make_p<T, KD>(fq, kt, gt, p.scale, wave, x);
     }
-    __syncthreads();
-    make_p<T, KD, 3>(qt, kt, gt, p.scale, wave, pt);
-    const T *op = static_cast<const T *>(p.dout) + c.b * p.os[0] + c.t0 * p.os[1] + head * p.os[2];
+    lds_barrier();
+    put_p<3>(x, wave, pt);
     float *zp = p.z + (slot * p.nh + hl) * kC * p.dvp;
     for (int v0 = 0; v0 < p.dvp; v0 += VS) {
-        __syncthreads();
-        {
-            Stage<T, VS, 256> st;
-            st.load(op + v0, p.os[1], c.len, p.dv_ - v0, p.vec_do);
-            st.put(ot);
-        }
-        __syncthreads();
+        so.put(ot);
+        lds_barrier();
+        if (v0 + VS < p.dvp) so.load(op + v0 + VS, p.os[1], c.len, p.dv_ - v0 - VS, p.vec_do);
         // rows tokens j = 16 wave .., columns v
         facc acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
             if (32 * ks + 31 < 16 * wave) continue;  // i >= j
-            bfrag a[3];
+            bfrag a[3], b[2][NP];
             pt.cols(32 * ks, 16 * wave, a);
 #pragma unroll
-            for (int vt = 0; vt < 2; ++vt) {
-                bfrag b[NP];
-                ot.cols(32 * ks, 16 * vt, b);
-                mma<3, NP>(acc[vt], a, b);
-            }
+            for (int vt = 0; vt < 2; ++vt) ot.cols(32 * ks, 16 * vt, b[vt]);
+            mma_two<3, NP, 3, NP>(acc[0], a, b[0], acc[1], a, b[1]);
         }
+        lds_barrier();
 #pragma unroll
         for (int vt = 0; vt < 2; ++vt) *reinterpret_cast<facc *>(zp + (v0 + 16 * vt) * kC + wave * 256 + l * 4) = acc[vt];
     }
@@ -1093,25 +1135,35 @@ __global__ __launch_bounds__(THREADS, 1) void delta_join(ChunkParams p)
 
 // ------------------------------------------------------------------ delta_out
 
-// 32 columns of a matrix of ROWS rows, as it lies in the workspace, into LDS
-// transposed (a piece is four neighbours of a column), times factor[row].
-template <int NP, int ROWS, int THREADS>
-__device__ __forceinline__ void put_slice(const Tile<NP, 32, ROWS> &to, const float *from, const float *factor)
-{
-    constexpr int kAll = ROWS * 32 / 4, kEach = (kAll + THREADS - 1) / THREADS;
+// 32 columns of a matrix of ROWS rows, as it lies in the workspace: to
+// registers, then into LDS transposed (a piece is four neighbours of a column),
+// times factor[row].
+template <int ROWS, int THREADS>
+struct Slice {
+    static constexpr int kAll = ROWS * 32 / 4, kEach = (kAll + THREADS - 1) / THREADS;
     facc x[kEach];
+    __device__ __forceinline__ void load(const float *from)
+    {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) x[i] = *reinterpret_cast<const facc *>(from + min(i * THREADS + static_cast<int>(threadIdx.x), kAll - 1) * 4);
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        const int w = i * THREADS + threadIdx.x, tile = w / 64, row = 16 * (tile % (ROWS / 16)) + 4 * (w % 64 / 16);
-        if (kAll % THREADS != 0 && w >= kAll) continue;
-        if (factor) x[i] *= *reinterpret_cast<const facc *>(factor + row);
-        to.put4(16 * (tile / (ROWS / 16)) + w % 16, row, x[i][0], x[i][1], x[i][2], x[i][3]);
+        for (int i = 0; i < kEach; ++i) x[i] = *reinterpret_cast<const facc *>(from + min(i * THREADS + static_cast<int>(threadIdx.x), kAll - 1) * 4);
     }
-}
+    template <int NP, bool SCALED>
+    __device__ __forceinline__ void put(const Tile<NP, 32, ROWS> &to, const float *factor)
+    {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int w = i * THREADS + threadIdx.x, tile = w / 64, row = 16 * (tile % (ROWS / 16)) + 4 * (w % 64 / 16);
+            if (kAll % THREADS != 0 && w >= kAll) continue;
+            if constexpr (SCALED) x[i] *= *reinterpret_cast<const facc *>(factor + row);
+            to.put4(16 * (tile / (ROWS / 16)) + w % 16, row, x[i][0], x[i][1], x[i][2], x[i][3]);
+        }
+    }
+};
 
-// O of one chunk and head: workgroup (slot, head), 32 columns at a time.
+// O of one chunk and head: workgroup (slot, head), 32 columns at a time, the
+// next ones read while these are multiplied. The wave's rows of Q stay in
+// registers; Q and K give their place to P and the slices, so that three
+// workgroups fit a compute unit (the phases of one wait for one another).
 template <typename T, int KD>
 struct OutLds {
     static constexpr int NP = kParts<T>, NPO = sizeof(T) == 2 ? 2 : 3, VS = 32;
@@ -1119,9 +1171,8 @@ struct OutLds {
     using PT = Tile<NPO, kC, kC>;
     using ST = Tile<NPO, VS, KD>;  // transposed
     using UT = Tile<NPO, VS, kC>;
-    // K is done with when the first slices come
-    static constexpr int kSlices = ST::kBytes + UT::kBytes, kShared = KT::kBytes > kSlices ? KT::kBytes : kSlices;
-    static constexpr int kBytes = KT::kBytes + PT::kBytes + kShared + kGates * 4;
+    static constexpr int kAfter = PT::kBytes + ST::kBytes + UT::kBytes, kMain = 2 * KT::kBytes > kAfter ? 2 * KT::kBytes : kAfter;
+    static constexpr int kBytes = kMain + kGates * 4;
 };
 
 template <typename T, int KD>
@@ -1133,68 +1184,76 @@ __global__ __launch_bounds__(256) void delta_out(ChunkParams p)
     const long slot = blockIdx.x;
     const Place c = find_chunk(p, slot);
     if (c.len == 0) return;
-    const int hl = blockIdx.y, head = p.hk0 * p.rep + hl, hk = head / p.rep, wave = threadIdx.x / 64, l = threadIdx.x % 64;
+    const int hl = blockIdx.y, head = p.hk0 * p.rep + hl, hk = head / p.rep, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64;
     const long at = slot * p.nh + hl;
-    const typename L::KT qt{lds}, kt{lds + L::KT::kBytes / 2 + L::PT::kBytes / 2};
-    const typename L::PT pt{lds + L::KT::kBytes / 2};
-    const typename L::ST st{kt.p};
-    const typename L::UT ut{kt.p + L::ST::kBytes / 2};
-    float *gt = reinterpret_cast<float *>(kt.p + L::kShared / 2);
+    const typename L::KT qt{lds}, kt{lds + L::KT::kBytes / 2};
+    const typename L::PT pt{lds};
+    const typename L::ST st{lds + L::PT::kBytes / 2};
+    const typename L::UT ut{st.p + L::ST::kBytes / 2};
+    float *gt = reinterpret_cast<float *>(lds + L::kMain / 2);
+    const float *s0 = p.s0 + at * KD * p.dvp, *e0 = p.e + at * kC * p.dvp;
+    Slice<KD, 256> ss;
+    Slice<kC, 256> su;
+    bfrag fq[KD / 32][NP];
+    facc x[4];
     {
         Stage<T, KD, 256> a, b;
         a.load(static_cast<const T *>(p.q) + c.b * p.qs[0] + c.t0 * p.qs[1] + hk * p.qs[2], p.qs[1], c.len, p.dk_, p.vec_qk);
         b.load(static_cast<const T *>(p.k) + c.b * p.ks[0] + c.t0 * p.ks[1] + hk * p.ks[2], p.ks[1], c.len, p.dk_, p.vec_qk);
-        for (int i = threadIdx.x; i < kGates; i += 256) gt[i] = p.gates[at * kGates + i];
+        const float g0 = p.gates[at * kGates + threadIdx.x], g1 = p.gates[at * kGates + 256 + threadIdx.x % 64];
+        ss.load(s0);
+        su.load(e0);
+        gt[threadIdx.x] = g0;
+        if (threadIdx.x < 64) gt[256 + threadIdx.x] = g1;
         a.put(qt);
         b.put(kt);
+        lds_barrier();
+#pragma unroll
+        for (int ks = 0; ks < KD / 32; ++ks) qt.rows(16 * wave, 32 * ks, fq[ks]);
+        make_p<T, KD>(fq, kt, gt, p.scale, wave, x);
     }
-    __syncthreads();
-    make_p<T, KD, NPO>(qt, kt, gt, p.scale, wave, pt);
+    lds_barrier();
+    put_p<NPO>(x, wave, pt);
     const int i = 16 * wave + l % 16;
     const float lead = p.scale * gt[i];
     T *op = static_cast<T *>(p.o) + ((c.b * p.tokens + c.t0 + i) * p.h + head) * p.dv_;
     for (int v0 = 0; v0 < p.dvp; v0 += VS) {
-        __syncthreads();
-        put_slice<NPO, KD, 256>(st, p.s0 + at * KD * p.dvp + v0 * KD, nullptr);
-        put_slice<NPO, kC, 256>(ut, p.e + at * kC * p.dvp + v0 * kC, gt + 2 * kC);
-        __syncthreads();
+        ss.template put<NPO, false>(st, nullptr);
+        su.template put<NPO, true>(ut, gt + 2 * kC);
+        lds_barrier();
+        if (v0 + VS < p.dvp) {
+            ss.load(s0 + (v0 + VS) * KD);
+            su.load(e0 + (v0 + VS) * kC);
+        }
         // rows v, columns tokens i: four neighbouring v a lane
         facc acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
         for (int ks = 0; ks < KD / 32; ++ks) {
-            bfrag b[NP];
-            qt.rows(16 * wave, 32 * ks, b);
+            bfrag a[2][NPO];
 #pragma unroll
-            for (int vt = 0; vt < 2; ++vt) {
-                bfrag a[NPO];
-                st.rows(16 * vt, 32 * ks, a);
-                mma<NPO, NP>(acc[vt], a, b);
-            }
+            for (int vt = 0; vt < 2; ++vt) st.rows(16 * vt, 32 * ks, a[vt]);
+            mma_two<NPO, NP, NPO, NP>(acc[0], a[0], fq[ks], acc[1], a[1], fq[ks]);
         }
 #pragma unroll
-        for (int vt = 0; vt < 2; ++vt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[vt][j] *= lead;
+        for (int vt = 0; vt < 2; ++vt) acc[vt] *= lead;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
             if (32 * ks > 16 * wave + 15) continue;  // j <= i
-            bfrag b[NPO];
+            bfrag b[NPO], a[2][NPO];
             pt.rows(16 * wave, 32 * ks, b);
 #pragma unroll
-            for (int vt = 0; vt < 2; ++vt) {
-                bfrag a[NPO];
-                ut.rows(16 * vt, 32 * ks, a);
-                mma<NPO, NPO>(acc[vt], a, b);
-            }
+            for (int vt = 0; vt < 2; ++vt) ut.rows(16 * vt, 32 * ks, a[vt]);
+            mma_two<NPO, NPO, NPO, NPO>(acc[0], a[0], b, acc[1], a[1], b);
         }
+        lds_barrier();
         if (i < c.len) {
 #pragma unroll
             for (int vt = 0; vt < 2; ++vt) {
                 const int v = v0 + 16 * vt + 4 * (l / 16);
                 if (p.vec_o && v + 4 <= p.dv_) {
                     Raw<T, 4> r;
-                    float x[4] = {acc[vt][0], acc[vt][1], acc[vt][2], acc[vt][3]};
-                    r.set(x);
+                    float y[4] = {acc[vt][0], acc[vt][1], acc[vt][2], acc[vt][3]};
+                    r.set(y);
                     r.store(op + v);
                 } else {
 #pragma unroll
@@ -1224,33 +1283,6 @@ struct LocalLds {
     static constexpr int kSums = kGates + 2 * kC + 2 * kC + 16;
     static constexpr int kBytes = kMain + kSums * 4;
 };
-
-// Two or three sums whose terms take turns, so that none waits for itself.
-template <int NP>
-__device__ __forceinline__ void mma_turns(facc &q, const bfrag (&fq)[NP], facc &r, const bfrag (&fr)[3], const bfrag (&a)[3], facc &c,
-                                          const bfrag (&d)[3], const bfrag (&fc)[3])
-{
-#pragma unroll
-    for (int s = 2; s >= 0; --s)
-#pragma unroll
-        for (int i = 0; i <= s; ++i) {
-            r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], fr[s - i], r, 0, 0, 0);
-            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(d[i], fc[s - i], c, 0, 0, 0);
-            if (s - i < NP) q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], fq[s - i], q, 0, 0, 0);
-        }
-}
-template <int NA, int NB, int NC, int ND>
-__device__ __forceinline__ void mma_two(facc &x, const bfrag (&a)[NA], const bfrag (&b)[NB], facc &y, const bfrag (&c)[NC], const bfrag (&d)[ND])
-{
-    constexpr int kX = NA > NB ? NA : NB, kY = NC > ND ? NC : ND, kMax = kX > kY ? kX : kY;
-#pragma unroll
-    for (int s = kMax - 1; s >= 0; --s)
-#pragma unroll
-        for (int i = 0; i <= s; ++i) {
-            if (s < kX && i < NA && s - i < NB) x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[s - i], x, 0, 0, 0);
-            if (s < kY && i < NC && s - i < ND) y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c[i], d[s - i], y, 0, 0, 0);
-        }
-}
 
 // Gradients of one chunk for head p.turn of those that share key head
 // hk0 + blockIdx.y: workgroup (slot, key head), a launch a turn, dQ and dK
@@ -1609,7 +1641,7 @@ int chunk_passes(const DeltaArgs &a)
         delta_prep<T, KD, GRAD><<<dim3(slots, nk), dim3(256), 0, s>>>(p);
         if ((rc = launched()) != SSM2D_OK) return rc;
         if constexpr (GRAD) {
-            constexpr int kZ = 2 * Tile<kParts<T>, kC, KD>::kBytes + Tile<3, kC, kC>::kBytes + Tile<kParts<T>, kC, 32>::kBytes + kGates * 4;
+            constexpr int kZ = ZLds<T, KD>::kBytes;
             if ((rc = big_lds(delta_z<T, KD>, kZ)) != SSM2D_OK) return rc;
             delta_z<T, KD><<<dim3(slots, nh), dim3(256), kZ, s>>>(p);
             if ((rc = launched()) != SSM2D_OK) return rc;
