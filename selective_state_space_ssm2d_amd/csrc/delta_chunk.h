@@ -482,16 +482,25 @@ __global__ __launch_bounds__(256, 3) void delta_prep(ChunkParams p)
                 const float x = sn[(o + i) * kLdM + o + l16];
                 m[i] = i > l16 ? x : 0.0f;
             }
-            __builtin_amdgcn_sched_barrier(0);
+            facc be[4], next[4];  // N below row i in column i, from its mirror image
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                be[k] = *reinterpret_cast<const facc *>(beta + o + 4 * k);
+                next[k] = *reinterpret_cast<const facc *>(sn + (o + 1) * kLdM + o + 4 * k);
+            }
 #pragma unroll
             for (int i = 1; i < 15; ++i) {
-                facc row[4];  // N below row i in column i, from its mirror image
+                facc row[4];
+                int zero = 0;
+                asm volatile("" : "+v"(zero) : "v"(m[i]));  // (the next row is read now: all rows at once would take 120 registers)
 #pragma unroll
-                for (int k = (i + 1) / 4; k < 4; ++k) row[k] = *reinterpret_cast<const facc *>(sn + (o + i) * kLdM + o + 4 * k);
-                const float x = beta[o + i] * m[i];
+                for (int k = i / 4; k < 4; ++k) {
+                    row[k] = next[k];
+                    if (i < 14) next[k] = *reinterpret_cast<const facc *>(sn + (o + i + 1) * kLdM + o + 4 * k + zero);
+                }
+                const float x = be[i / 4][i % 4] * m[i];
 #pragma unroll
                 for (int k = i + 1; k < 16; ++k) m[k] = fmaf(-row[k / 4][k % 4], x, m[k]);
-                if (i % 2 == 1) __builtin_amdgcn_sched_barrier(0);  // (else all rows are read at once, into 120 registers)
             }
             if (g4 == 0) {
 #pragma unroll
@@ -543,6 +552,7 @@ __global__ __launch_bounds__(256, 3) void delta_prep(ChunkParams p)
         }
         __syncthreads();
         // fragments of -M (and -M^T), three parts each
+#pragma unroll 1
         for (int f = wave; f < (BWD ? 2 : 1) * kMFrags; f += 4) {
             const bool tr = f >= kMFrags;
             const int n = tr ? f - kMFrags : f;
