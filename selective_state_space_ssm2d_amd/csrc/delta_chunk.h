@@ -1062,9 +1062,10 @@ template <typename T, int KD, bool GRAD, int THREADS>
 __global__ __launch_bounds__(THREADS, 1) void delta_join(ChunkParams p)
 {
     using AT = Tile<3, KD, KD>;
+    constexpr bool kTwo = KD <= 64;  // two buffers, so one barrier a step
+    constexpr int DEPTH = KD == 32 ? 8 : (KD == 64 ? 4 : 2);
     constexpr int NT = KD / 16, kAll = KD * KD / 4, kPieces = (kAll + THREADS - 1) / THREADS, kGroup = NT < 4 ? NT : 4;
     extern __shared__ __align__(16) uint16_t lds[];
-    const AT at{lds};
     const bool bwd = GRAD && blockIdx.z == 1;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64, g4 = l / 16, l16 = l % 16;
     const long s = blockIdx.x / p.nh;
@@ -1085,35 +1086,45 @@ __global__ __launch_bounds__(THREADS, 1) void delta_join(ChunkParams p)
             S[t][j] = init ? init[state + static_cast<long>(min(row, p.dk_ - 1)) * p.dv_ + min(col, p.dv_ - 1)] : 0.0f;
             S[t][j] = (live && row < p.dk_) ? S[t][j] : 0.0f;
         }
-    facc a[kPieces], b[NT];
+    // A and b of the next DEPTH segments, read that far ahead: another XCD wrote
+    // them, so they come from memory, later than a step or two
+    facc a[DEPTH][kPieces], b[DEPTH][NT];
     auto seg = [&](int i) { return static_cast<long>(blockIdx.x) * p.nseg + (bwd ? ns - 1 - i : i); };
     auto place = [&](int i) { return (bwd ? p.seg_d : p.seg_s) + seg(i) * KD * p.dvp + (act ? v0 : 0) * KD + l * 4; };
-    auto fetch = [&](int i) __attribute__((always_inline)) {  // (the last segment's A and b are not needed; nor, maybe, there)
+    auto fetch = [&](int i, int at) __attribute__((always_inline)) {  // (the last segment's A and b are not needed; nor, maybe, there)
         const float *src = p.seg_a + seg(i) * KD * KD;
 #pragma unroll
-        for (int k = 0; k < kPieces; ++k) a[k] = *reinterpret_cast<const facc *>(src + min(k * THREADS + static_cast<int>(threadIdx.x), kAll - 1) * 4);
+        for (int k = 0; k < kPieces; ++k) a[at][k] = *reinterpret_cast<const facc *>(src + min(k * THREADS + static_cast<int>(threadIdx.x), kAll - 1) * 4);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) b[t] = *reinterpret_cast<const facc *>(place(i) + t * 256);
+        for (int t = 0; t < NT; ++t) b[at][t] = *reinterpret_cast<const facc *>(place(i) + t * 256);
     };
-    if (ns > 1) fetch(0);
-    for (int i = 0; i + 1 < ns; ++i) {
-        lds_barrier();  // (the last A has been read)
 #pragma unroll
-        for (int k = 0; k < kPieces; ++k) {
-            const int w = k * THREADS + threadIdx.x, tile = w / 64;
-            if (kAll % THREADS == 0 || w < kAll)
-                at.put4(16 * (tile / NT) + w % 16, 16 * (tile % NT) + 4 * (w % 64 / 16), a[k][0], a[k][1], a[k][2], a[k][3]);
-        }
-        facc out[NT];
+    for (int u = 0; u < DEPTH; ++u)
+        if (u + 1 < ns) fetch(u, u);
+    for (int i0 = 0; i0 + 1 < ns; i0 += DEPTH) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            out[t] = S[t];
-            S[t] = b[t];
-        }
-        float *to = place(i);
-        lds_barrier();
-        if (i + 2 < ns) fetch(i + 1);
-        if (act) {
+        for (int u = 0; u < DEPTH; ++u) {
+            const int i = i0 + u;
+            if (i + 1 >= ns) break;
+            // (two buffers: the A before this one may still be in use)
+            const AT at{lds + (kTwo ? (i & 1) * (AT::kBytes / 2) : 0)};
+            if (!kTwo) lds_barrier();
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+                const int w = k * THREADS + threadIdx.x, tile = w / 64;
+                if (kAll % THREADS == 0 || w < kAll)
+                    at.put4(16 * (tile / NT) + w % 16, 16 * (tile % NT) + 4 * (w % 64 / 16), a[u][k][0], a[u][k][1], a[u][k][2], a[u][k][3]);
+            }
+            facc out[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                out[t] = S[t];
+                S[t] = b[u][t];
+            }
+            float *to = place(i);
+            lds_barrier();
+            if (i + DEPTH + 1 < ns) fetch(i + DEPTH, u);
+            if (!act) continue;
 #pragma unroll
             for (int ks = 0; ks < KD / 32; ++ks) {
                 bfrag f[3];
@@ -1123,14 +1134,14 @@ __global__ __launch_bounds__(THREADS, 1) void delta_join(ChunkParams p)
                     bfrag m[kGroup][3];
                     facc acc[kGroup];
 #pragma unroll
-                    for (int u = 0; u < kGroup; ++u) {
-                        if (bwd) at.rows(16 * (t + u), 32 * ks, m[u]);
-                        else at.cols(32 * ks, 16 * (t + u), m[u]);
-                        acc[u] = S[t + u];
+                    for (int g = 0; g < kGroup; ++g) {
+                        if (bwd) at.rows(16 * (t + g), 32 * ks, m[g]);
+                        else at.cols(32 * ks, 16 * (t + g), m[g]);
+                        acc[g] = S[t + g];
                     }
                     mma_each<3, 3, kGroup>(acc, m, f);
 #pragma unroll
-                    for (int u = 0; u < kGroup; ++u) S[t + u] = acc[u];
+                    for (int g = 0; g < kGroup; ++g) S[t + g] = acc[g];
                 }
             }
 #pragma unroll
@@ -1681,15 +1692,14 @@ int chunk_passes(const DeltaArgs &a)
         if (p.nseg > 1) {
             if ((rc = chains_of(std::true_type{})) != SSM2D_OK) return rc;
             auto join = [&](auto threads) -> int {
-                constexpr int THREADS = decltype(threads)::value, kJ = Tile<3, KD, KD>::kBytes;
+                constexpr int THREADS = decltype(threads)::value, kJ = (KD <= 64 ? 2 : 1) * Tile<3, KD, KD>::kBytes;
                 const int st2 = big_lds(delta_join<T, KD, GRAD, THREADS>, kJ);
                 if (st2 != SSM2D_OK) return st2;
                 delta_join<T, KD, GRAD, THREADS>
                     <<<dim3(chains, static_cast<unsigned>((p.dvp + THREADS / 4 - 1) / (THREADS / 4)), kDirs), dim3(THREADS), kJ, s>>>(p);
                 return launched();
             };
-            rc = p.dvp > 64 ? join(std::integral_constant<int, 512>{}) : join(std::integral_constant<int, 256>{});
-            if (rc != SSM2D_OK) return rc;
+            if ((rc = join(std::integral_constant<int, 256>{})) != SSM2D_OK) return rc;
         }
         if ((rc = chains_of(std::false_type{})) != SSM2D_OK) return rc;
         if constexpr (GRAD) {
