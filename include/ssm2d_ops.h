@@ -64,7 +64,7 @@ int ssm2d_layer_norm_fwd_bf16(const uint16_t *x, const float *weight, const floa
  *   dweight = sum dy xh,  dbias = sum dy   over batch and cells
  * (dweight, dbias: NULL = not computed). dx is dense like y, dy has strides
  * like x's. The sums go through per-workgroup partial sums in a workspace of
- * at most 8 KiB * n bytes, added in a fixed order. */
+ * at most 4 KiB * n bytes, added in a fixed order. */
 int ssm2d_layer_norm_bwd(const float *x, const float *weight, const float *mean, const float *rstd, const float *dy,
                          float *dx, float *dweight, float *dbias, int64_t batch, int64_t n, int64_t cells,
                          int64_t x_stride_b, int64_t x_stride_n, int64_t dy_stride_b, int64_t dy_stride_n, void *stream);

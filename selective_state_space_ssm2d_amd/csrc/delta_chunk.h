@@ -1479,8 +1479,7 @@ __global__ __launch_bounds__(WAVES * 64, WAVES == 4 ? 2 : 1) void delta_local(Ch
 #pragma unroll
         for (int j = 0; j < 4; ++j) dg += x[j] * aq[t][j] + y[j] * (ar[t][j] - ac[t][j]);
     }
-    dg += __shfl_xor(dg, 16, 64);
-    dg += __shfl_xor(dg, 32, 64);
+    dg = pair_sum<32>(pair_sum<16>(dg));
     if (g4 == 0) sg[half * kC + i] = dg;
 #pragma unroll
     for (int j = 0; j < 4; ++j) db[j] = lane_sum<16>(db[j]);

@@ -23,6 +23,16 @@ struct StepParams {
     float scale;
 };
 
+// Sum of a row's lanes VL, 2 VL .. apart (VL = 4: by two rotations of the row).
+template <int VL>
+__device__ __forceinline__ float row_turn(float v)
+{
+    static_assert(VL == 4, "rotations");
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xf, 0xf, true));  // row_ror:8
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x124, 0xf, 0xf, true));  // row_ror:4
+    return v;
+}
+
 template <typename T, int VS, int VEC>
 __global__ __launch_bounds__(256) void delta_step_kernel(StepParams p)
 {
@@ -76,11 +86,11 @@ __global__ __launch_bounds__(256) void delta_step_kernel(StepParams p)
         const float kq = lane_sum<64>(sk[tid % 64] * sq[tid % 64] + sk[64 + tid % 64] * sq[64 + tid % 64]);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-#pragma unroll
-            for (int m = VL; m < 64; m *= 2) {
-                ak[j] += __shfl_xor(ak[j], m, 64);
-                aq[j] += __shfl_xor(aq[j], m, 64);
-            }
+            // (rows of 16 lanes hold 16 / VL row groups of the same columns; mirror
+            // images would mix columns, so within them a rotation by VL)
+            if constexpr (VL == 4) ak[j] = row_turn<4>(ak[j]), aq[j] = row_turn<4>(aq[j]);
+            if constexpr (VL <= 16) ak[j] = pair_sum<16>(ak[j]), aq[j] = pair_sum<16>(aq[j]);
+            if constexpr (VL <= 32) ak[j] = pair_sum<32>(ak[j]), aq[j] = pair_sum<32>(aq[j]);
             if (kr % RW == 0) {
                 part[wave][vl * VEC + j][0] = ak[j];
                 part[wave][vl * VEC + j][1] = aq[j];

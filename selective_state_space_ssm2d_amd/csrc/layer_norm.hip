@@ -126,23 +126,37 @@ __global__ __launch_bounds__(WPR * 64 > 256 ? WPR * 64 : 256) void ln_row_bwd(co
         }
     }
     const float inv_n = 1.0f / static_cast<float>(n);
-    for (long r0 = static_cast<long>(blockIdx.x) * kRows; r0 < rows; r0 += static_cast<long>(gridDim.x) * kRows) {
-        const long row = r0 + (WPR >= 4 ? 0 : threadIdx.x / (WPR * 64));
-        const bool live = row < rows;
-        Raw<T, VEC> vx[NCH], vg[NCH];
-        float mu = 0.0f, rs = 0.0f;
-        if (live) mu = mean[row], rs = rstd[row];
+    // the next row is read while this one is worked on (where registers allow)
+    constexpr bool kAhead = NCH * VEC <= 16;
+    Raw<T, VEC> nx[NCH], ng[NCH];
+    float nmu = 0.0f, nrs = 0.0f;
+    auto fetch = [&](long row) __attribute__((always_inline)) {
+        const long at = row < rows ? row : rows - 1;  // (rows past the end read the last one, and are not used)
+        nmu = mean[at], nrs = rstd[at];
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
             const int col = (c * WPR * 64 + t) * VEC;
-            if (live && col < n) {
-                vx[c].load(x + row * ldx + col);
-                vg[c].load(dy + row * ldy + col);
+            if (col < n) {
+                nx[c].load(x + at * ldx + col);
+                ng[c].load(dy + at * ldy + col);
             } else {
-                vx[c].clear();
-                vg[c].clear();
+                nx[c].clear();
+                ng[c].clear();
             }
         }
+    };
+    const long first = static_cast<long>(blockIdx.x) * kRows, step = static_cast<long>(gridDim.x) * kRows;
+    const int sub = WPR >= 4 ? 0 : threadIdx.x / (WPR * 64);
+    if (kAhead) fetch(first + sub);
+    for (long r0 = first; r0 < rows; r0 += step) {
+        const long row = r0 + sub;
+        const bool live = row < rows;
+        if (!kAhead) fetch(row);
+        Raw<T, VEC> vx[NCH], vg[NCH];
+        const float mu = nmu, rs = nrs;
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) vx[c] = nx[c], vg[c] = ng[c];
+        if (kAhead && r0 + step < rows) fetch(row + step);
         // (columns past n: x = dy = 0, their terms of both sums are 0 * (-mu rs) = 0
         // unless the row's statistics are not finite, where dx is not either)
         float sa = 0.0f, sc = 0.0f;
@@ -217,24 +231,35 @@ __global__ __launch_bounds__(WPR * 64 > 256 ? WPR * 64 : 256) void ln_row_bwd(co
     }
 }
 
-// dweight (columns 0 .. n - 1 of the partial rows) and dbias (n .. 2n - 1):
-// 32 columns a workgroup, its 8 (32 with 1024 threads) row groups added in order.
+// dweight (columns 0 .. n - 1 of the partial rows) and dbias (n .. 2n - 1): 16
+// columns a workgroup, so that few columns still make several workgroups; 64
+// groups of rows, then the groups in order.
 __global__ __launch_bounds__(1024) void ln_fold(const float *part, int np, int n, float *dweight, float *dbias)
 {
-    __shared__ float s[32][33];
-    const int lx = threadIdx.x % 32, ly = threadIdx.x / 32;
-    const int col = static_cast<int>(blockIdx.x) * 32 + lx;
+    __shared__ float s[64][17];
+    const int lx = threadIdx.x % 16, ly = threadIdx.x / 16;
+    const int col = static_cast<int>(blockIdx.x) * 16 + lx, at = min(col, 2 * n - 1);
     float acc = 0.0f;
-    if (col < 2 * n)
-        for (int p = ly; p < np; p += 32) acc += part[static_cast<long>(p) * 2 * n + col];
+    int p = ly;
+    for (; p + 7 * 64 < np; p += 8 * 64) {
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = part[static_cast<long>(p + 64 * k) * 2 * n + at];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc += v[k];
+    }
+    for (; p < np; p += 64) acc += part[static_cast<long>(p) * 2 * n + at];
     s[ly][lx] = acc;
     __syncthreads();
-    if (ly == 0 && col < 2 * n) {
+    if (threadIdx.x < 64) {  // 16 columns by 4 groups of 16 rows
         float v = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) v += s[k][lx];
-        float *out = col < n ? dweight : dbias;
-        if (out) out[col < n ? col : col - n] = v;
+        for (int k = 0; k < 16; ++k) v += s[16 * ly + k][lx];
+        v = pair_sum<32>(pair_sum<16>(v));
+        if (ly == 0 && col < 2 * n) {
+            float *out = col < n ? dweight : dbias;
+            if (out) out[col < n ? col : col - n] = v;
+        }
     }
 }
 
@@ -248,9 +273,10 @@ __device__ __forceinline__ void tile_sum(float (&v)[VEC], float *buf)
     constexpr int kWaves = TX * TY / 64;
     const int tx = threadIdx.x % TX, wave = threadIdx.x / 64;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j)
-#pragma unroll
-        for (int m = TX; m < 64; m *= 2) v[j] += __shfl_xor(v[j], m, 64);
+    for (int j = 0; j < VEC; ++j) {
+        static_assert(TX == 16 || TX == 64, "lanes of a channel group");
+        if constexpr (TX == 16) v[j] = pair_sum<32>(pair_sum<16>(v[j]));
+    }
     __syncthreads();  // (the last use of buf has been read)
     if (threadIdx.x % 64 < TX) {
 #pragma unroll
@@ -263,6 +289,16 @@ __device__ __forceinline__ void tile_sum(float (&v)[VEC], float *buf)
     for (int u = 0; u < kWaves; ++u)
 #pragma unroll
         for (int j = 0; j < VEC; ++j) v[j] += buf[(u * VEC + j) * TX + tx];
+}
+
+// A lane's place within a workgroup's channels, beside a base the workgroup
+// shares. In 32 bits one register serves every channel group; strides of 2^26
+// elements or more take the kernels of single cells, which keep 64.
+template <int VEC>
+__device__ __forceinline__ auto lane_offset(int ty, int at, long stride)
+{
+    if constexpr (VEC == 1) return ty * stride + at;
+    else return static_cast<unsigned>(ty) * static_cast<unsigned>(stride) + static_cast<unsigned>(at);
 }
 
 // KEEP: the tile stays in registers (n <= TY * NCH); else it is read again for
@@ -279,22 +315,21 @@ __global__ __launch_bounds__(TX *TY) void ln_map_fwd(const T *x, const float *we
     const int nc = KEEP ? NCH : (n + TY - 1) / TY;
     for (long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const long b = tile / tiles_b;
-        const long cell = (tile - b * tiles_b) * (TX * VEC) + tx * VEC;
+        const long cell0 = (tile - b * tiles_b) * (TX * VEC), cell = cell0 + tx * VEC;
         const bool live = cell < cells;
-        const T *xb = x + b * sb + cell;
+        const T *xb = x + b * sb + cell0;
+        const auto lane = lane_offset<VEC>(ty, tx * VEC, sn);
         Raw<T, VEC> v[KEEP ? NCH : 1];
         auto get = [&](int c) -> const Raw<T, VEC> & {
             if constexpr (KEEP) return v[c];
-            const int ch = c * TY + ty;
-            if (live && ch < n) v[0].load(xb + ch * sn);
+            if (live && c * TY + ty < n) v[0].load(xb + c * TY * sn + lane);
             else v[0].clear();
             return v[0];
         };
         if constexpr (KEEP) {
 #pragma unroll
             for (int c = 0; c < NCH; ++c) {
-                const int ch = c * TY + ty;
-                if (live && ch < n) v[c].load(xb + ch * sn);
+                if (live && c * TY + ty < n) v[c].load(xb + c * TY * sn + lane);
                 else v[c].clear();
             }
         }
@@ -347,7 +382,7 @@ __global__ __launch_bounds__(TX *TY) void ln_map_fwd(const T *x, const float *we
             for (int j = 0; j < VEC; ++j) o[j] = (r.get(j) - mu[j]) * q[j] * w + bi;
             Raw<T, VEC> out;
             out.set(o);
-            out.store(y + (b * n + ch) * cells + cell);
+            out.store(y + (b * n + c * TY) * cells + cell0 + lane_offset<VEC>(ty, tx * VEC, cells));
         }
     }
 }
@@ -368,15 +403,16 @@ __global__ __launch_bounds__(TX *TY) void ln_map_bwd(const T *x, const float *we
     }
     for (long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const long b = tile / tiles_b;
-        const long cell = (tile - b * tiles_b) * (TX * VEC) + tx * VEC;
+        const long cell0 = (tile - b * tiles_b) * (TX * VEC), cell = cell0 + tx * VEC;
         const bool live = cell < cells;
-        const T *xb = x + b * sb + cell, *yb = dy + b * gb + cell;
+        const T *xb = x + b * sb + cell0, *yb = dy + b * gb + cell0;
+        const auto xl = lane_offset<VEC>(ty, tx * VEC, sn);
+        const auto yl = lane_offset<VEC>(ty, tx * VEC, gn);
         Raw<T, VEC> vx[KEEP ? NCH : 1], vg[KEEP ? NCH : 1];
         auto fetch = [&](int c, int k) {
-            const int ch = c * TY + ty;
-            if (live && ch < n) {
-                vx[k].load(xb + ch * sn);
-                vg[k].load(yb + ch * gn);
+            if (live && c * TY + ty < n) {
+                vx[k].load(xb + c * TY * sn + xl);
+                vg[k].load(yb + c * TY * gn + yl);
             } else {
                 vx[k].clear();
                 vg[k].clear();
@@ -431,7 +467,7 @@ __global__ __launch_bounds__(TX *TY) void ln_map_bwd(const T *x, const float *we
             }
             Raw<T, VEC> out;
             out.set(o);
-            out.store(dx + (b * n + ch) * cells + cell);
+            out.store(dx + (b * n + c * TY) * cells + cell0 + lane_offset<VEC>(ty, tx * VEC, cells));
         }
     }
     if constexpr (KEEP) {
@@ -491,8 +527,15 @@ struct NormArgs {
     hipStream_t s;
 };
 
-constexpr int kMaxParts = 1024;  // partial rows of dweight and dbias (the workgroups of a backward launch)
+constexpr int64_t kFar = int64_t{1} << 26;
+constexpr int kMaxParts = 512;  // partial rows of dweight and dbias (the workgroups of a backward launch)
 
+// Workgroups for `work` turns of a loop: at most `most`, all with as many turns (but the last).
+unsigned even_blocks(int64_t work, int64_t most)
+{
+    const int64_t turns = (work + most - 1) / most;
+    return static_cast<unsigned>(turns > 0 ? (work + turns - 1) / turns : 1);
+}
 unsigned blocks_for(int64_t work, int64_t most) { return static_cast<unsigned>(std::max<int64_t>(1, std::min(work, most))); }
 
 // The row kernels' variant: waves a row and pieces a lane, the fewest that
@@ -597,7 +640,7 @@ int norm_fwd(const T *x, const float *weight, const float *bias, T *y, float *me
             return launched();
         });
     };
-    auto fits = [&](int v) { return a.cells % v == 0 && aligned_to(x, a.batch > 1 ? a.sb : 0, a.n > 1 ? a.sn : 0, v) && !off_by(y, v * sizeof(T)); };
+    auto fits = [&](int v) { return a.cells < kFar && a.sn < kFar && a.cells % v == 0 && aligned_to(x, a.batch > 1 ? a.sb : 0, a.n > 1 ? a.sn : 0, v) && !off_by(y, v * sizeof(T)); };
     return pick_cells<V>(a.n, fits, go);
 }
 
@@ -621,7 +664,7 @@ int norm_bwd(const T *x, const float *weight, const float *mean, const float *rs
     };
     auto fold = [&](unsigned np) -> int {
         if (!sums) return SSM2D_OK;
-        ln_fold<<<dim3(static_cast<unsigned>((2 * n + 31) / 32)), dim3(1024), 0, a.s>>>(part, static_cast<int>(np), n, dweight, dbias);
+        ln_fold<<<dim3(static_cast<unsigned>((2 * n + 15) / 16)), dim3(1024), 0, a.s>>>(part, static_cast<int>(np), n, dweight, dbias);
         return launched();
     };
     if (a.cells == 1 && ((a.sn == 1 && a.gn == 1) || a.n == 1)) {
@@ -630,7 +673,7 @@ int norm_bwd(const T *x, const float *weight, const float *mean, const float *rs
             return pick_row<T, VEC>(a.n, [&](auto nch, auto wpr) {
                 constexpr int NCH = decltype(nch)::value, WPR = decltype(wpr)::value;
                 constexpr int kRows = WPR >= 4 ? 1 : 4 / WPR;
-                const unsigned grid = blocks_for((a.batch + kRows - 1) / kRows, WPR == 16 ? 256 : kMaxParts);
+                const unsigned grid = even_blocks((a.batch + kRows - 1) / kRows, WPR == 16 ? 256 : kMaxParts);
                 int st = parts(grid);
                 if (st != SSM2D_OK) return st;
                 ln_row_bwd<T, VEC, NCH, WPR><<<dim3(grid), dim3(WPR * 64 > 256 ? WPR * 64 : 256), 0, a.s>>>(
@@ -648,7 +691,7 @@ int norm_bwd(const T *x, const float *weight, const float *mean, const float *rs
             constexpr int TX = decltype(tx)::value, TY = decltype(ty)::value, NCH = decltype(nch)::value;
             constexpr bool KEEP = decltype(keep)::value;
             const int64_t tiles_b = (a.cells + TX * VEC - 1) / (TX * VEC), tiles = tiles_b * a.batch;
-            const unsigned grid = blocks_for(tiles, KEEP ? (TX * TY > 256 ? 256 : kMaxParts) : 1 << 20);
+            const unsigned grid = KEEP ? even_blocks(tiles, TX * TY > 256 ? 512 : kMaxParts) : blocks_for(tiles, 1 << 20);
             const unsigned slices = KEEP ? grid : blocks_for((a.batch * a.cells + 2047) / 2048, 64);
             int st = parts(slices);
             if (st != SSM2D_OK) return st;
@@ -667,7 +710,7 @@ int norm_bwd(const T *x, const float *weight, const float *mean, const float *rs
     };
     auto fits = [&](int v) {
         const int64_t b = a.batch > 1, c = a.n > 1;
-        return a.cells % v == 0 && aligned_to(x, b * a.sb, c * a.sn, v) && aligned_to(dy, b * a.gb, c * a.gn, v) &&
+        return a.cells < kFar && a.sn < kFar && a.gn < kFar && a.cells % v == 0 && aligned_to(x, b * a.sb, c * a.sn, v) && aligned_to(dy, b * a.gb, c * a.gn, v) &&
                !off_by(dx, v * sizeof(T));
     };
     return pick_cells<V>(a.n, fits, go);

@@ -103,12 +103,34 @@ struct Raw {
     }
 };
 
+// v + the value M lanes away, for lanes in pairs M apart: within rows of 16 by
+// DPP (M = 4 and 8 as mirror images, which needs groups of M lanes to hold
+// equal values, as in lane_sum), beyond by the row swaps. No LDS round trip.
+template <int M>
+__device__ __forceinline__ float pair_sum(float v)
+{
+    if constexpr (M < 16) {
+        constexpr int kCtrl = M == 1 ? 0xB1 : (M == 2 ? 0x4E : (M == 4 ? 0x141 : 0x140));  // quad_perm, row_half_mirror, row_mirror
+        return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, 0xf, 0xf, true));
+    } else if constexpr (M == 16) {
+        const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    } else {
+        const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    }
+}
+
 // Sum over aligned groups of W lanes; every lane gets it.
 template <int W>
 __device__ __forceinline__ float lane_sum(float v)
 {
-#pragma unroll
-    for (int m = 1; m < W; m *= 2) v += __shfl_xor(v, m, 64);
+    if constexpr (W > 1) v = pair_sum<1>(v);
+    if constexpr (W > 2) v = pair_sum<2>(v);
+    if constexpr (W > 4) v = pair_sum<4>(v);
+    if constexpr (W > 8) v = pair_sum<8>(v);
+    if constexpr (W > 16) v = pair_sum<16>(v);
+    if constexpr (W > 32) v = pair_sum<32>(v);
     return v;
 }
 

@@ -68,9 +68,13 @@ def _entry(name, dtype):
     return f
 
 
+# The current stream's handle: 0.1 us where torch offers it as an integer, 2 us through a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _run(fn, dev, stream, args):
     """Calls fn(*args, stream) with ``dev`` current; a status becomes an exception."""
-    handle = (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
+    handle = stream.cuda_stream if stream is not None else _raw_stream(dev.index)
     if dev.index == torch.cuda.current_device():
         s = fn(*args, handle)
     else:
@@ -104,6 +108,13 @@ def _f32(shape, **tensors):
     for name, t in tensors.items():
         if t is not None and (t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous()):
             raise ValueError(f"{name} must be contiguous float32 {list(shape)}")
+
+
+def _like(name, t, ref, stream):
+    """An output like a tensor of the call: given, or allocated."""
+    if t is None and stream is None and ref.is_contiguous():
+        return torch.empty_like(ref)
+    return _out(name, t, ref.shape, ref.dtype, ref.device, stream)
 
 
 def _out(name, t, shape, dtype, dev, stream):
@@ -149,7 +160,7 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, *, channels_first=False,
     batch, n, cells, sb, sn = _norm_layout(x, channels_first)
     _on_gpu(dev, weight=weight, bias=bias)
     _f32((n,), weight=weight, bias=bias)
-    y = _out("y", y, x.shape, x.dtype, dev, stream)
+    y = _like("y", y, x, stream)
     mean = rstd = None
     if return_stats:
         shape = x.shape[:1] + x.shape[2:] if channels_first else x.shape[:-1]
@@ -172,7 +183,7 @@ def layer_norm_bwd(x, weight, mean, rstd, dy, *, channels_first=False, out=None,
     _f32((n,), weight=weight)
     _f32(x.shape[:1] + x.shape[2:] if channels_first else x.shape[:-1], mean=mean, rstd=rstd)
     out = out or {}
-    r = {"dx": _out("dx", out.get("dx"), x.shape, x.dtype, dev, stream),
+    r = {"dx": _like("dx", out.get("dx"), x, stream),
          "dweight": _out("dweight", out.get("dweight"), (n,), torch.float32, dev, stream),
          "dbias": _out("dbias", out.get("dbias"), (n,), torch.float32, dev, stream)}
     _run(fn, dev, stream, (x.data_ptr(), _ptr(weight), mean.data_ptr(), rstd.data_ptr(), dy.data_ptr(), r["dx"].data_ptr(),
@@ -207,10 +218,10 @@ def _rope(q, k, positions, inv_freq, sections, interleaved, inverse, q_out, k_ou
         raise ValueError("the last dim of positions must be contiguous")
     _on_gpu(dev, k=k, positions=positions, inv_freq=inv_freq)
     _f32((sum(sections),), inv_freq=inv_freq)
-    q_out = _out("q_out", q_out, q.shape, q.dtype, dev, stream)
+    q_out = _like("q_out", q_out, q, stream)
     hk, ks = 0, (0, 0, 0)
     if k is not None:
-        k_out = _out("k_out", k_out, k.shape, k.dtype, dev, stream)
+        k_out = _like("k_out", k_out, k, stream)
         hk, ks = k.shape[2], _strides(k, "k")
     pos = (positions.stride(0), positions.stride(1) if positions.dim() == 3 else 0)
     shape = _rope_shape(B, T, hq, hk, d, _strides(q, "q"), ks, sections, pos)
@@ -287,7 +298,7 @@ def gated_delta_fwd(q, k, v, g, beta, *, scale=None, h_init=None, cu_seqlens=Non
     states = (seqs, v.shape[2], q.shape[3], v.shape[3])
     _on_gpu(dev, h_init=h_init)
     _f32(states, h_init=h_init)
-    o = _out("o", o, v.shape, v.dtype, dev, stream)
+    o = _like("o", o, v, stream)
     if return_last_state or h_last is not None:
         h_last = _out("h_last", h_last, states, torch.float32, dev, stream)
     _run(fn, dev, stream, (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(h_init), _ptr(cu_seqlens),
@@ -305,7 +316,7 @@ def gated_delta_bwd(q, k, v, g, beta, do, *, scale=None, h_init=None, dh_last=No
     _on_gpu(dev, h_init=h_init, dh_last=dh_last)
     _f32(states, h_init=h_init, dh_last=dh_last)
     out = out or {}
-    r = {n: _out(n, out.get(n), t.shape, t.dtype, dev, stream) for n, t in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta))}
+    r = {n: _like(n, out.get(n), t, stream) for n, t in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta))}
     if h_init is not None or dh_last is not None:
         r["dh_init"] = _out("dh_init", out.get("dh_init"), states, torch.float32, dev, stream)
     _run(fn, dev, stream, (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(h_init), _ptr(cu_seqlens),
@@ -320,16 +331,29 @@ def gated_delta_step(q, k, v, g, beta, state, *, scale=None, o=None, stream=None
     tokens, all with a token dim after the batch. state: float32 [batch, heads,
     d_k, d_v], updated in place. Returns o (v's shape and dtype)."""
     fn = _entry("ssm2d_gated_delta_step", q.dtype)
-    if q.dim() == 3:
-        q4, k4, v4, g3, b3 = q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1), g.unsqueeze(1), beta.unsqueeze(1)
-    else:
-        q4, k4, v4, g3, b3 = q, k, v, g, beta
-    dev, B, shape = _delta_check(q4, k4, v4, g3, b3, None)
-    _on_gpu(dev, state=state)
     if state is None:
         raise ValueError("state is required")
-    _f32((B, v4.shape[2], q4.shape[3], v4.shape[3]), state=state)
-    o = _out("o", o, v.shape, v.dtype, dev, stream)
+    if q.dim() == 3:  # one token: as [batch, 1, heads, d] without making the views
+        (B, hk, dk), (_, h, dv) = q.shape, v.shape if v.dim() == 3 else (0, 0, 0)
+        dev = q.device
+        if k.shape != q.shape or v.shape != (B, h, dv) or g.shape != (B, h) or beta.shape != (B, h) or (h % hk if hk else h) != 0:
+            raise ValueError("one token: q and k [batch, heads_qk, d_k], v [batch, heads, d_v], g and beta [batch, heads]")
+        if k.dtype != q.dtype or v.dtype != q.dtype:
+            raise TypeError("q, k and v must have one dtype")
+        if g.dtype != torch.float32 or beta.dtype != torch.float32:
+            raise ValueError("g and beta must be float32")
+        qs, ks, vs, gs, bs = q.stride(), k.stride(), v.stride(), g.stride(), beta.stride()
+        if (dk > 1 and (qs[2] != 1 or ks[2] != 1)) or (dv > 1 and vs[2] != 1):
+            raise ValueError("the last dims of q, k and v must be contiguous")
+        _on_gpu(dev, k=k, v=v, g=g, beta=beta, state=state)
+        shape = _delta_shape(B, 1, 0, hk, h, dk, dv, (qs[0], 0, qs[1]), (ks[0], 0, ks[1]), (vs[0], 0, vs[1]), (0, 0, 0),
+                             (gs[0], 0, gs[1]), (bs[0], 0, bs[1]))
+    else:
+        dev, B, shape = _delta_check(q, k, v, g, beta, None)
+        h, dk, dv = v.shape[2], q.shape[3], v.shape[3]
+        _on_gpu(dev, state=state)
+    _f32((B, h, dk, dv), state=state)
+    o = _like("o", o, v, stream)
     _run(fn, dev, stream, (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(), o.data_ptr(),
-                           shape, q4.shape[3] ** -0.5 if scale is None else float(scale)))
+                           shape, dk ** -0.5 if scale is None else float(scale)))
     return o
