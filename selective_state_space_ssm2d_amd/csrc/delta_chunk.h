@@ -54,7 +54,8 @@ struct ChunkParams {
     float *h_last, *dg, *dbeta, *dh_init;
     // workspace, by [slot][head of this pass]
     float *gates;                       // [5][kC]: gamma, Gam_last, beta, G and its rounding error
-    word4 *m, *mt;                      // -M, -M^T: 6 fragments x 3 parts
+    // -M, -M^T and P: their 10 tiles that are not zero, as operands: row lane % 16, columns 4 (lane / 16) + j
+    float *m, *mt, *pm;
     // (matrices as accumulator tiles: 16 columns after 16, of each 16 rows after
     // 16, of each the 64 lanes' four values: column lane % 16, rows 4 (lane / 16) + j)
     float *s0, *d1;                     // [KD][dvp]
@@ -197,6 +198,22 @@ __device__ __forceinline__ void mma_each(facc (&acc)[NT], const bfrag (&a)[NT][N
             if (j < 0 || j >= NB) continue;
 #pragma unroll
             for (int t = 0; t < NT; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[t][i], b[j], acc[t], 0, 0, 0);
+        }
+}
+
+// The same with the operands' sides changed: acc[t]^T += b^T a[t]^T.
+template <int NA, int NB, int NT>
+__device__ __forceinline__ void mma_each_t(facc (&acc)[NT], const bfrag (&a)[NT][NA], const bfrag (&b)[NB])
+{
+    constexpr int kMax = NA > NB ? NA : NB;
+#pragma unroll
+    for (int s = kMax - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            const int j = s - i;
+            if (j < 0 || j >= NB) continue;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], a[t][i], acc[t], 0, 0, 0);
         }
 }
 
@@ -392,9 +409,12 @@ __device__ __forceinline__ float gam(const float *gt, int i, int j)
 }
 
 constexpr int kGates = 5 * kC;
-constexpr int kMFrags = 6;             // fragments of M that are not zero
-constexpr int kMWords = kMFrags * 3 * 64;  // word4 of one head's M
-// fragment of M for rows 16 rt .., columns 32 ks .. (ks <= rt / 2)
+// The triangular matrices of a chunk are kept as 10 tiles of 16 x 16, tile
+// (a, b), a >= b, at a (a + 1) / 2 + b, and multiplied as 6 fragments of 16 x 32.
+constexpr int kTriTiles = 10, kTriFloats = kTriTiles * 256, kTriFrags = 6;
+__device__ __forceinline__ int tri_row(int tile) { return tile < 1 ? 0 : (tile < 3 ? 1 : (tile < 6 ? 2 : 3)); }
+__host__ __device__ constexpr int tri_tile(int a, int b) { return a * (a + 1) / 2 + b; }
+// fragment of M (P) for rows 16 rt .., columns 32 ks .. (ks <= rt / 2)
 __host__ __device__ constexpr int m_frag(int rt, int ks) { return rt < 2 ? rt : 2 * rt - 2 + ks; }
 // fragment of M^T for rows 16 rt .., columns 32 ks .. (ks >= rt / 2)
 __host__ __device__ constexpr int mt_frag(int rt, int ks) { return rt < 2 ? 2 * rt + ks : 2 + rt; }
@@ -403,16 +423,17 @@ __host__ __device__ constexpr int mt_frag(int rt, int ks) { return rt < 2 ? 2 * 
 
 __device__ __forceinline__ facc mfma4(float a, float b, facc c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 
-// Gates and M of one chunk for the heads that share key head hk0 + blockIdx.y.
-// M block by block: the 16 x 16 blocks on the diagonal by substitution, a
-// column a lane, then the blocks below by M21 = (I - M22 B2) N21 (I - B1 M11)
-// for halves of 32 and of 64, in fp32 matrix instructions (20 products of 16^3
-// a head: small beside the split products elsewhere).
+// Gates, M and (for the forward) P of one chunk for the heads that share key
+// head hk0 + blockIdx.y. M block by block: the 16 x 16 blocks on the diagonal by
+// substitution, a column a lane, then the blocks below by
+// M21 = (I - M22 B2) N21 (I - B1 M11) for halves of 32 and of 64, in fp32 matrix
+// instructions (20 products of 16^3 a head: small beside the split products
+// elsewhere).
 template <typename T, int KD, bool BWD>
 __global__ __launch_bounds__(256, 3) void delta_prep(ChunkParams p)
 {
-    // K is done with when N and M come: they share its place, so that four
-    // workgroups fit a compute unit (the phases below wait for one another)
+    // Q, then K, then N and M share one place, so that several workgroups fit a
+    // compute unit (the phases below wait for one another)
     constexpr int NP = kParts<T>, kLdM = 68, kNM = 2 * kC * kLdM * 4, kK = Tile<NP, kC, KD>::kBytes;
     __shared__ __align__(16) unsigned char buf[kK > kNM ? kK : kNM];
     __shared__ __align__(16) float gt[kGates];
@@ -424,23 +445,33 @@ __global__ __launch_bounds__(256, 3) void delta_prep(ChunkParams p)
     const int hk = p.hk0 + blockIdx.y, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64;
     int g4 = l / 16, l16 = l % 16;
     const Tile<NP, kC, KD> kt{kbuf};
+    facc kk[4], qk[4];  // K K^T: rows 16 wave + 4 g4 + r, columns 16 ct + l16; Q K^T transposed: rows 16 ct + .., columns 16 wave + ..
     {
-        Stage<T, KD, 256> st;
-        st.load(static_cast<const T *>(p.k) + c.b * p.ks[0] + c.t0 * p.ks[1] + hk * p.ks[2], p.ks[1], c.len, p.dk_, p.vec_qk);
-        st.put(kt);
-    }
-    __syncthreads();
-    facc kk[4];  // rows 16 wave + 4 g4 + r, columns 16 ct + l16
+        Stage<T, KD, 256> sq, sk;
+        bfrag fq[KD / 32][NP];
+        if constexpr (!BWD) sq.load(static_cast<const T *>(p.q) + c.b * p.qs[0] + c.t0 * p.qs[1] + hk * p.qs[2], p.qs[1], c.len, p.dk_, p.vec_qk);
+        sk.load(static_cast<const T *>(p.k) + c.b * p.ks[0] + c.t0 * p.ks[1] + hk * p.ks[2], p.ks[1], c.len, p.dk_, p.vec_qk);
+        if constexpr (!BWD) {
+            sq.put(kt);
+            lds_barrier();
 #pragma unroll
-    for (int ct = 0; ct < 4; ++ct) {
-        kk[ct] = facc{0, 0, 0, 0};
-        if (ct > wave) continue;
+            for (int ks = 0; ks < KD / 32; ++ks) kt.rows(16 * wave, 32 * ks, fq[ks]);
+            lds_barrier();
+        }
+        sk.put(kt);
+        lds_barrier();
 #pragma unroll
-        for (int ks = 0; ks < KD / 32; ++ks) {
-            bfrag a[NP], b[NP];
-            kt.rows(16 * wave, 32 * ks, a);
-            kt.rows(16 * ct, 32 * ks, b);
-            mma<NP, NP>(kk[ct], a, b);
+        for (int ct = 0; ct < 4; ++ct) {
+            kk[ct] = qk[ct] = facc{0, 0, 0, 0};
+            if (ct > wave) continue;
+#pragma unroll
+            for (int ks = 0; ks < KD / 32; ++ks) {
+                bfrag a[NP], b[NP];
+                kt.rows(16 * wave, 32 * ks, a);
+                kt.rows(16 * ct, 32 * ks, b);
+                if constexpr (BWD) mma<NP, NP>(kk[ct], a, b);
+                else mma_two<NP, NP, NP, NP>(kk[ct], a, b, qk[ct], b, fq[ks]);
+            }
         }
     }
     for (int r = 0; r < p.rep; ++r) {
@@ -451,6 +482,21 @@ __global__ __launch_bounds__(256, 3) void delta_prep(ChunkParams p)
         __syncthreads();
         const long at = slot * p.nh + hl;
         for (int i = threadIdx.x; i < kGates; i += 256) p.gates[at * kGates + i] = gt[i];
+        if constexpr (!BWD) {  // P: token i = 16 wave + l16, four neighbouring j a lane, which is an operand's layout
+            const int i = 16 * wave + l16;
+            const float hi = gt[3 * kC + i], lo = gt[4 * kC + i];
+#pragma unroll
+            for (int ct = 0; ct < 4; ++ct) {
+                if (ct > wave) continue;
+                const int j0 = 16 * ct + 4 * g4;
+                const facc jhi = *reinterpret_cast<const facc *>(gt + 3 * kC + j0), jlo = *reinterpret_cast<const facc *>(gt + 4 * kC + j0);
+                facc x;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    x[j] = j0 + j <= i ? p.scale * __builtin_amdgcn_exp2f((hi - jhi[j]) + (lo - jlo[j])) * qk[ct][j] : 0.0f;
+                *reinterpret_cast<facc *>(p.pm + at * kTriFloats + tri_tile(wave, ct) * 256 + l * 4) = x;
+            }
+        }
         {   // N (in the blocks on the diagonal with its mirror image, read below)
             const facc hi = *reinterpret_cast<const facc *>(gt + 3 * kC + 16 * wave + 4 * g4), lo = *reinterpret_cast<const facc *>(gt + 4 * kC + 16 * wave + 4 * g4);
 #pragma unroll
@@ -551,26 +597,17 @@ __global__ __launch_bounds__(256, 3) void delta_prep(ChunkParams p)
             for (int j = 0; j < 4; ++j) sm[(r0 + 4 * g4 + j) * kLdM + c0 + l16] = x[j];
         }
         __syncthreads();
-        // fragments of -M (and -M^T), three parts each
 #pragma unroll 1
-        for (int f = wave; f < (BWD ? 2 : 1) * kMFrags; f += 4) {
-            const bool tr = f >= kMFrags;
-            const int n = tr ? f - kMFrags : f;
-            int rt, ks;
-            if (!tr) rt = n < 2 ? n : 2 + (n - 2) / 2, ks = n < 2 ? 0 : (n - 2) % 2;
-            else rt = n < 4 ? n / 2 : n - 2, ks = n < 4 ? n % 2 : 1;
-            float x[8];
+        for (int t = wave; t < kTriTiles; t += 4) {
+            const int ra = tri_row(t), rb = t - tri_tile(ra, 0);
+            *reinterpret_cast<facc *>(p.m + at * kTriFloats + t * 256 + l * 4) =
+                -*reinterpret_cast<const facc *>(sm + (16 * ra + l16) * kLdM + 16 * rb + 4 * g4);
+            if constexpr (BWD) {
+                facc x;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int row = 16 * rt + l16, k = 32 * ks + 16 * (j / 4) + 4 * g4 + j % 4;
-                x[j] = -(tr ? sm[k * kLdM + row] : sm[row * kLdM + k]);
+                for (int j = 0; j < 4; ++j) x[j] = -sm[(16 * ra + 4 * g4 + j) * kLdM + 16 * rb + l16];
+                *reinterpret_cast<facc *>(p.mt + at * kTriFloats + t * 256 + l * 4) = x;
             }
-            unsigned w[4][3];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) split2<3>(x[2 * j], x[2 * j + 1], w[j]);
-            word4 *out = (tr ? p.mt : p.m) + at * kMWords + n * 3 * 64 + l;
-#pragma unroll
-            for (int q = 0; q < 3; ++q) out[q * 64] = word4{w[0][q], w[1][q], w[2][q], w[3][q]};
         }
     }
 }
@@ -678,81 +715,101 @@ __global__ __launch_bounds__(256) void delta_z(ChunkParams p)
 
 // ------------------------------------------------------------------ delta_seq
 
-// What a chunk's step reads from LDS: K (and Q in the backward), M's
-// fragments, the gates and, of bf16 inputs, the columns of v (dO).
-template <typename T, int KD, bool BWD, int THREADS>
+// What a chunk's step reads from LDS: K (and Q, but for the forward's chain of
+// a backward), M's fragments (and P's, for the outputs), the gates and, of bf16
+// inputs, the columns of v (dO).
+template <typename T, int KD, bool BWD, bool OUT, int THREADS>
 struct SeqBuf {
-    static constexpr int kCols = THREADS / 4;
-    static constexpr bool kStaged = sizeof(T) == 2;
+    static constexpr int kCols = THREADS / 4, NPO = sizeof(T) == 2 ? 2 : 3;
+    static constexpr bool kStaged = sizeof(T) == 2, kQ = BWD || OUT;
     static constexpr int kTile = Tile<kParts<T>, kC, KD>::kBytes;
-    static constexpr int kRest = kMWords * 16 + 4 * kC * 4, kV = kStaged ? Tile<1, kC, kCols>::kBytes : 0;
-    static constexpr int kBytes = (BWD ? 2 : 1) * kTile + kRest + kV;
-    // two buffers where they fit beside each other
-    static constexpr int kBufs = 2 * kBytes <= 160 * 1024 ? 2 : 1;
+    static constexpr int kTri = kTriFrags * 1024 * 3, kTriP = OUT ? kTriFrags * 1024 * NPO : 0;
+    static constexpr int kOne = (kQ ? 2 : 1) * kTile + kTri + kTriP + 3 * kC * 4;
+    static constexpr int kV = kStaged ? Tile<1, kC, kCols>::kBytes : 0;
+    // two buffers where that costs no second workgroup a compute unit: a large
+    // state fills its registers with one anyway
+    static constexpr int kBufs = (THREADS == 512 || KD == 128) && 2 * kOne + kV <= 160 * 1024 ? 2 : 1;
+    static constexpr int kBytes = kBufs * kOne + kV;
 };
 
-// 16 bytes a lane from global memory into LDS at `to` + 16 lane, without a
-// register in between. Done when vmcnt says so.
-__device__ __forceinline__ void load_to_lds(const word4 *from, void *to)
-{
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) unsigned *)from,
-                                     (__attribute__((address_space(3))) unsigned *)lds_offset(to), 16, 0, 0);
-}
-
-// The next step's inputs. With two buffers M and the gates go straight to
-// LDS; K and Q pass through registers, which pad and cut them.
-template <typename T, int KD, bool BWD, int THREADS>
+// The next step's inputs, on their way through registers into LDS.
+template <typename T, int KD, bool BWD, bool OUT, int THREADS>
 struct SeqStage {
-    using Buf = SeqBuf<T, KD, BWD, THREADS>;
-    static constexpr bool kDirect = Buf::kBufs == 2;
-    static constexpr int kLines = (kMWords + 3 * kC / 4) / 64 + 1, kEach = (kMWords + THREADS - 1) / THREADS;  // kLines: 1 KiB each
+    using Buf = SeqBuf<T, KD, BWD, OUT, THREADS>;
+    static constexpr int kTiles = OUT ? 2 * kTriTiles : kTriTiles, kWaves = THREADS / 64, kEach = (kTiles + kWaves - 1) / kWaves;
+    static constexpr int kGateEach = (3 * kC + THREADS - 1) / THREADS;
     Stage<T, KD, THREADS> k, q;
     Stage<T, Buf::kCols, THREADS> v;
-    word4 m[kDirect ? 1 : kEach];
-    float g;
-    __device__ __forceinline__ void load(const ChunkParams &p, long b, long t0, int len, int hk, long at, uint16_t *lds)
+    facc m[kEach];
+    float g[kGateEach];
+    __device__ __forceinline__ void load(const ChunkParams &p, long b, long t0, int len, int hk, long at)
     {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64;
         k.load(static_cast<const T *>(p.k) + b * p.ks[0] + t0 * p.ks[1] + hk * p.ks[2], p.ks[1], len, p.dk_, p.vec_qk);
-        if constexpr (BWD) q.load(static_cast<const T *>(p.q) + b * p.qs[0] + t0 * p.qs[1] + hk * p.qs[2], p.qs[1], len, p.dk_, p.vec_qk);
-        const word4 *src = (BWD ? p.mt : p.m) + at * kMWords;
-        if constexpr (kDirect) {
-            word4 *to = reinterpret_cast<word4 *>(lds + (BWD ? 2 : 1) * (Buf::kTile / 2));
-            const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64;
-            const word4 *gates = reinterpret_cast<const word4 *>(p.gates + at * kGates);
+        if constexpr (Buf::kQ) q.load(static_cast<const T *>(p.q) + b * p.qs[0] + t0 * p.qs[1] + hk * p.qs[2], p.qs[1], len, p.dk_, p.vec_qk);
 #pragma unroll
-            for (int i = 0; i < (kLines + THREADS / 64 - 1) / (THREADS / 64); ++i) {
-                const int line = i * (THREADS / 64) + wave;
-                if (line < kMWords / 64) load_to_lds(src + line * 64 + l, to + line * 64);
-                else if (line == kMWords / 64) load_to_lds(gates + l, to + kMWords);  // (gamma, Gam_last, beta, G: 1 KiB)
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) m[i] = src[min(i * THREADS + static_cast<int>(threadIdx.x), kMWords - 1)];
-            g = p.gates[at * kGates + min(static_cast<int>(threadIdx.x), 3 * kC - 1)];
+        for (int i = 0; i < kEach; ++i) {
+            const int t = min(i * kWaves + wave, kTiles - 1);
+            const float *src = (OUT && t >= kTriTiles ? p.pm - kTriFloats : (BWD ? p.mt : p.m)) + at * kTriFloats + t * 256;
+            m[i] = *reinterpret_cast<const facc *>(src + l * 4);
         }
+#pragma unroll
+        for (int i = 0; i < kGateEach; ++i) g[i] = p.gates[at * kGates + min(i * THREADS + static_cast<int>(threadIdx.x), 3 * kC - 1)];
     }
     // the workgroup's columns of v (dO) from c0 on: n of them
     __device__ __forceinline__ void load_v(const T *base, long stride, int len, int n, bool vec)
     {
         if constexpr (Buf::kStaged) v.load(base, stride, len, n, vec);
     }
-    __device__ __forceinline__ void put(uint16_t *lds) const
+    // a tile's four values into their fragment's parts
+    template <int NP>
+    static __device__ __forceinline__ void put_tile(uint16_t *area, int frag, int half, const facc &x)
+    {
+        const int l = threadIdx.x % 64;
+        unsigned a[NP], b[NP];
+        split2<NP>(x[0], x[1], a);
+        split2<NP>(x[2], x[3], b);
+#pragma unroll
+        for (int n = 0; n < NP; ++n) *reinterpret_cast<uint2 *>(area + ((frag * NP + n) * 64 + l) * 8 + half * 4) = make_uint2(a[n], b[n]);
+    }
+    __device__ __forceinline__ void put(uint16_t *one, uint16_t *vbuf) const
     {
         constexpr int kTile = Buf::kTile / 2;
-        if constexpr (Buf::kStaged) v.put(Tile<1, kC, Buf::kCols>{lds + (BWD ? 2 : 1) * kTile + Buf::kRest / 2});
-        k.put(Tile<kParts<T>, kC, KD>{lds});
-        if constexpr (BWD) q.put(Tile<kParts<T>, kC, KD>{lds + kTile});
-        if constexpr (kDirect) {
-            __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): what load() sent to LDS has arrived
-        } else {
-            uint16_t *rest = lds + (BWD ? 2 : 1) * kTile;
-            word4 *mm = reinterpret_cast<word4 *>(rest);
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+        if constexpr (Buf::kStaged) v.put(Tile<1, kC, Buf::kCols>{vbuf});
+        k.put(Tile<kParts<T>, kC, KD>{one});
+        if constexpr (Buf::kQ) q.put(Tile<kParts<T>, kC, KD>{one + kTile});
+        uint16_t *mm = one + (Buf::kQ ? 2 : 1) * kTile, *pp = mm + Buf::kTri / 2;
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                const int w = i * THREADS + threadIdx.x;
-                if (w < kMWords) mm[w] = m[i];
+        for (int i = 0; i < kEach; ++i) {
+            const int t = i * kWaves + wave;
+            if (t >= kTiles) break;
+            const int u = t < kTriTiles ? t : t - kTriTiles, a = tri_row(u), b = u - tri_tile(a, 0);
+            if (BWD) put_tile<3>(mm, mt_frag(b, a / 2), a % 2, m[i]);
+            else if (!OUT || t < kTriTiles) put_tile<3>(mm, m_frag(a, b / 2), b % 2, m[i]);
+            else put_tile<Buf::NPO>(pp, m_frag(a, b / 2), b % 2, m[i]);
+        }
+        float *gates = reinterpret_cast<float *>(pp + Buf::kTriP / 2);
+#pragma unroll
+        for (int i = 0; i < kGateEach; ++i)
+            if (i * THREADS + static_cast<int>(threadIdx.x) < 3 * kC) gates[i * THREADS + threadIdx.x] = g[i];
+    }
+    // the two halves of fragments that no tile fills, once
+    static __device__ __forceinline__ void clear(uint16_t *one)
+    {
+        uint16_t *mm = one + (Buf::kQ ? 2 : 1) * (Buf::kTile / 2), *pp = mm + Buf::kTri / 2;
+        const facc zero = {0, 0, 0, 0};
+        if (threadIdx.x >= 64) return;
+        if constexpr (BWD) {
+            put_tile<3>(mm, mt_frag(1, 0), 0, zero);
+            put_tile<3>(mm, mt_frag(3, 1), 0, zero);
+        } else {
+            put_tile<3>(mm, m_frag(0, 0), 1, zero);
+            put_tile<3>(mm, m_frag(2, 1), 1, zero);
+            if constexpr (OUT) {
+                put_tile<Buf::NPO>(pp, m_frag(0, 0), 1, zero);
+                put_tile<Buf::NPO>(pp, m_frag(2, 1), 1, zero);
             }
-            if (threadIdx.x < 3 * kC) reinterpret_cast<float *>(rest + kMWords * 8)[threadIdx.x] = g;
         }
     }
 };
@@ -767,11 +824,17 @@ struct SeqStage {
 // columns from the unit matrix and v = 0 (A); delta_join goes over the
 // segments; then they run at once from their true first states. The adjoint's
 // transition is A^T.
-template <typename T, int KD, bool BWD, bool PROBE, int THREADS>
+//
+// OUT: the outputs come from the same step, O = scale gamma Q S0 + P U, in
+// transposed tiles (the parts of S and U are operands as they are, and a lane
+// gets four neighbours of a token's row); else S0 and E are kept for
+// delta_local.
+template <typename T, int KD, bool BWD, bool PROBE, bool OUT, int THREADS>
 __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
 {
     constexpr int NP = kParts<T>, NT = KD / 16;
-    using Buf = SeqBuf<T, KD, BWD, THREADS>;
+    using Buf = SeqBuf<T, KD, BWD, OUT, THREADS>;
+    constexpr int NPO = Buf::NPO;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64, g4 = l / 16, l16 = l % 16;
     const long s = blockIdx.x / p.nh;
     const int hl = static_cast<int>(blockIdx.x - s * p.nh), head = p.hk0 * p.rep + hl, hk = head / p.rep;
@@ -818,7 +881,8 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
     facc x1[4];
     const T *vp = BWD ? static_cast<const T *>(p.dout) + q.b * p.os[0] + head * p.os[2] : static_cast<const T *>(p.v) + q.b * p.vs[0] + head * p.vs[2];
     const long vstep = BWD ? p.os[1] : p.vs[1];
-    SeqStage<T, KD, BWD, THREADS> st;
+    SeqStage<T, KD, BWD, OUT, THREADS> st;
+    uint16_t *vbuf = lds + Buf::kBufs * (Buf::kOne / 2);
     const int wg0 = min(static_cast<int>(blockIdx.y) * Buf::kCols, (p.dv_ - 1) / 16 * 16);  // (workgroups of the unit matrix alone read any)
     auto load_cols = [&](long c) __attribute__((always_inline)) {
         const int len = len_of(c);
@@ -839,9 +903,7 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
             for (int t = 0; t < 4; ++t) x1[t] = *reinterpret_cast<const facc *>(z + t * 256);
         }
     };
-    auto fetch = [&](long c, uint16_t *to) __attribute__((always_inline)) {
-        st.load(p, q.b, q.t0 + c * kC, len_of(c), hk, (q.slot0 + c) * p.nh + hl, to);
-    };
+    auto fetch = [&](long c) __attribute__((always_inline)) { st.load(p, q.b, q.t0 + c * kC, len_of(c), hk, (q.slot0 + c) * p.nh + hl); };
     facc y0[4], y1[4];  // the step's rows of v (dO) and Z
     auto take_cols = [&](long c) __attribute__((always_inline)) {
         const int len = len_of(c);
@@ -861,9 +923,9 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
         }
     };
     // (staged columns: 16 tokens of column l16 by a transposing read, which gives an accumulator's rows)
-    auto staged_cols = [&](uint16_t *buf) __attribute__((always_inline)) {
+    auto staged_cols = [&]() __attribute__((always_inline)) {
         if constexpr (Buf::kStaged) {
-            const Tile<1, kC, Buf::kCols> vt{buf + (BWD ? 2 : 1) * (Buf::kTile / 2) + Buf::kRest / 2};
+            const Tile<1, kC, Buf::kCols> vt{vbuf};
 #pragma unroll
             for (int t = 0; t < 4; t += 2) {
                 bfrag f[1];
@@ -884,11 +946,13 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
         for (int t = 0; t < NT; ++t) *reinterpret_cast<facc *>(keep + t * 256) = S[t];
     };
     if (n > 0) {
-        fetch(chunk(0), lds);
+        fetch(chunk(0));
         load_cols(chunk(0));
-        st.put(lds);
+        st.clear(lds);
+        if constexpr (Buf::kBufs == 2) st.clear(lds + Buf::kOne / 2);
+        st.put(lds, vbuf);
         take_cols(chunk(0));
-        if (!PROBE && act) keep_state(chunk(0));
+        if (!PROBE && !OUT && act) keep_state(chunk(0));
     }
     // One step: read the next chunk, compute this one, put what was read, store
     // this one's results. The stores come last: loads and stores share one
@@ -896,25 +960,26 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
     // and these get a whole step to finish.
     for (long i = 0; i < n; ++i) {
         const long c = chunk(i), at = (q.slot0 + c) * p.nh + hl;
-        uint16_t *buf = lds + (Buf::kBufs == 2 ? (i & 1) * (Buf::kBytes / 2) : 0);
-        uint16_t *next = lds + (Buf::kBufs == 2 ? ((i + 1) & 1) * (Buf::kBytes / 2) : 0);
+        uint16_t *buf = lds + (Buf::kBufs == 2 ? (i & 1) * (Buf::kOne / 2) : 0);
+        uint16_t *next = lds + (Buf::kBufs == 2 ? ((i + 1) & 1) * (Buf::kOne / 2) : 0);
         lds_barrier();
+        if (act) staged_cols();
+        if constexpr (Buf::kBufs == 2 && Buf::kStaged) lds_barrier();  // (there is one place for the columns)
         if (i + 1 < n) {
-            fetch(chunk(i + 1), next);
+            fetch(chunk(i + 1));
             load_cols(chunk(i + 1));
         }
-        facc X[4];
+        facc X[4], O[4];
         float o0[16];
         if (act) {
             const Tile<NP, kC, KD> kt{buf}, qt{buf + Buf::kTile / 2};
-            uint16_t *rest = buf + (BWD ? 2 : 1) * (Buf::kTile / 2);
-            const word4 *mm = reinterpret_cast<const word4 *>(rest);
-            const float *gt = reinterpret_cast<const float *>(rest + kMWords * 8);
-            staged_cols(buf);
+            uint16_t *rest = buf + (Buf::kQ ? 2 : 1) * (Buf::kTile / 2);
+            const word4 *mm = reinterpret_cast<const word4 *>(rest), *pp = reinterpret_cast<const word4 *>(rest + Buf::kTri / 2);
+            const float *gt = reinterpret_cast<const float *>(rest + (Buf::kTri + Buf::kTriP) / 2);
             // Y = K S, then the right-hand side: V - gamma Y, or Z + Gam_last Y
             facc Y[4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) Y[t] = facc{0, 0, 0, 0};
+            for (int t = 0; t < 4; ++t) Y[t] = O[t] = facc{0, 0, 0, 0};
 #pragma unroll
             for (int ks = 0; ks < KD / 32; ++ks) {
                 bfrag b[3], a[4][NP];
@@ -922,6 +987,14 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
                 for (int t = 0; t < 4; ++t) kt.rows(16 * t, 32 * ks, a[t]);
                 split_acc<3>(S[2 * ks], S[2 * ks + 1], b);
                 mma_each<NP, 3, 4>(Y, a, b);
+                if constexpr (OUT) {
+                    bfrag bo[NPO];
+#pragma unroll
+                    for (int n3 = 0; n3 < NPO; ++n3) bo[n3] = b[n3];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) qt.rows(16 * t, 32 * ks, a[t]);
+                    mma_each_t<NP, NPO, 4>(O, a, bo);
+                }
             }
             facc ga[4], gl[4], be[4], W[4];  // W: beta times the right-hand side
 #pragma unroll
@@ -958,6 +1031,34 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
                             if (BWD ? ks >= t / 2 : ks <= t / 2) X[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[t][u], b[sum - u], X[t], 0, 0, 0);
             }
             facc W2[4];
+            if constexpr (OUT) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    W2[t] = be[t] * X[t];              // U
+                    O[t] *= p.scale * gt[16 * t + l16];  // (this lane's token)
+                }
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    bfrag b[NPO], a[4][NPO];
+                    split_acc<NPO>(W2[2 * ks], W2[2 * ks + 1], b);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        if (ks <= t / 2)
+#pragma unroll
+                            for (int n3 = 0; n3 < NPO; ++n3) {
+                                FragBits fb;
+                                fb.q = pp[(m_frag(t, ks) * NPO + n3) * 64 + l];
+                                a[t][n3] = fb.f;
+                            }
+#pragma unroll
+                    for (int sum = NPO - 1; sum >= 0; --sum)
+#pragma unroll
+                        for (int u = 0; u <= sum; ++u)
+#pragma unroll
+                            for (int t = 0; t < 4; ++t)
+                                if (ks <= t / 2) O[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[sum - u], a[t][u], O[t], 0, 0, 0);
+                }
+            }
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -993,11 +1094,30 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
         }
         if (i + 1 < n) {
             if constexpr (Buf::kBufs == 1) lds_barrier();
-            st.put(next);
+            st.put(next, vbuf);
             take_cols(chunk(i + 1));
         }
         asm volatile("" ::: "memory");  // (no store goes up past the waits above)
-        if (!PROBE && act) {
+        if (OUT && act) {
+            const int len = len_of(c), v = v0 + 4 * g4;
+            T *op = static_cast<T *>(p.o) + ((q.b * p.tokens + q.t0 + c * kC + l16) * p.h + head) * p.dv_ + v;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                if (16 * t + l16 >= len) continue;
+                T *to = op + static_cast<long>(16 * t) * p.h * p.dv_;
+                if (p.vec_o && v + 4 <= p.dv_) {
+                    Raw<T, 4> r;
+                    float y[4] = {O[t][0], O[t][1], O[t][2], O[t][3]};
+                    r.set(y);
+                    r.store(to);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (v + j < p.dv_) store1(to + j, O[t][j]);
+                }
+            }
+        }
+        if (!PROBE && !OUT && act) {
             float *ep = (BWD ? p.dr : p.e) + at * kC * p.dvp + v0 * kC + l * 4;
 #pragma unroll
             for (int t = 0; t < 4; ++t) *reinterpret_cast<facc *>(ep + t * 256) = X[t];
@@ -1046,11 +1166,11 @@ __global__ __launch_bounds__(THREADS, 1) void delta_seq(ChunkParams p)
     extern __shared__ __align__(16) uint16_t lds[];
     if constexpr (GRAD) {
         if (static_cast<int>(blockIdx.z) >= p.nseg) {
-            seq_chain<T, KD, true, PROBE, THREADS>(p, lds);
+            seq_chain<T, KD, true, PROBE, false, THREADS>(p, lds);
             return;
         }
     }
-    seq_chain<T, KD, false, PROBE, THREADS>(p, lds);
+    seq_chain<T, KD, false, PROBE, !GRAD && !PROBE, THREADS>(p, lds);
 }
 
 // First states of the segments: S over a sequence's segments, S <- A S + b
@@ -1151,138 +1271,6 @@ __global__ __launch_bounds__(THREADS, 1) void delta_join(ChunkParams p)
     if (act) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) *reinterpret_cast<facc *>(place(ns - 1) + t * 256) = S[t];
-    }
-}
-
-// ------------------------------------------------------------------ delta_out
-
-// 32 columns of a matrix of ROWS rows, as it lies in the workspace: to
-// registers, then into LDS transposed (a piece is four neighbours of a column),
-// times factor[row].
-template <int ROWS, int THREADS>
-struct Slice {
-    static constexpr int kAll = ROWS * 32 / 4, kEach = (kAll + THREADS - 1) / THREADS;
-    facc x[kEach];
-    __device__ __forceinline__ void load(const float *from)
-    {
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) x[i] = *reinterpret_cast<const facc *>(from + min(i * THREADS + static_cast<int>(threadIdx.x), kAll - 1) * 4);
-    }
-    template <int NP, bool SCALED>
-    __device__ __forceinline__ void put(const Tile<NP, 32, ROWS> &to, const float *factor)
-    {
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const int w = i * THREADS + threadIdx.x, tile = w / 64, row = 16 * (tile % (ROWS / 16)) + 4 * (w % 64 / 16);
-            if (kAll % THREADS != 0 && w >= kAll) continue;
-            if constexpr (SCALED) x[i] *= *reinterpret_cast<const facc *>(factor + row);
-            to.put4(16 * (tile / (ROWS / 16)) + w % 16, row, x[i][0], x[i][1], x[i][2], x[i][3]);
-        }
-    }
-};
-
-// O of one chunk and head: workgroup (slot, head), 32 columns at a time, the
-// next ones read while these are multiplied. The wave's rows of Q stay in
-// registers; Q and K give their place to P and the slices, so that three
-// workgroups fit a compute unit (the phases of one wait for one another).
-template <typename T, int KD>
-struct OutLds {
-    static constexpr int NP = kParts<T>, NPO = sizeof(T) == 2 ? 2 : 3, VS = 32;
-    using KT = Tile<NP, kC, KD>;
-    using PT = Tile<NPO, kC, kC>;
-    using ST = Tile<NPO, VS, KD>;  // transposed
-    using UT = Tile<NPO, VS, kC>;
-    static constexpr int kAfter = PT::kBytes + ST::kBytes + UT::kBytes, kMain = 2 * KT::kBytes > kAfter ? 2 * KT::kBytes : kAfter;
-    static constexpr int kBytes = kMain + kGates * 4;
-};
-
-template <typename T, int KD>
-__global__ __launch_bounds__(256) void delta_out(ChunkParams p)
-{
-    using L = OutLds<T, KD>;
-    constexpr int NP = L::NP, NPO = L::NPO, VS = L::VS;
-    extern __shared__ __align__(16) uint16_t lds[];
-    const long slot = blockIdx.x;
-    const Place c = find_chunk(p, slot);
-    if (c.len == 0) return;
-    const int hl = blockIdx.y, head = p.hk0 * p.rep + hl, hk = head / p.rep, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64;
-    const long at = slot * p.nh + hl;
-    const typename L::KT qt{lds}, kt{lds + L::KT::kBytes / 2};
-    const typename L::PT pt{lds};
-    const typename L::ST st{lds + L::PT::kBytes / 2};
-    const typename L::UT ut{st.p + L::ST::kBytes / 2};
-    float *gt = reinterpret_cast<float *>(lds + L::kMain / 2);
-    const float *s0 = p.s0 + at * KD * p.dvp, *e0 = p.e + at * kC * p.dvp;
-    Slice<KD, 256> ss;
-    Slice<kC, 256> su;
-    bfrag fq[KD / 32][NP];
-    facc x[4];
-    {
-        Stage<T, KD, 256> a, b;
-        a.load(static_cast<const T *>(p.q) + c.b * p.qs[0] + c.t0 * p.qs[1] + hk * p.qs[2], p.qs[1], c.len, p.dk_, p.vec_qk);
-        b.load(static_cast<const T *>(p.k) + c.b * p.ks[0] + c.t0 * p.ks[1] + hk * p.ks[2], p.ks[1], c.len, p.dk_, p.vec_qk);
-        const float g0 = p.gates[at * kGates + threadIdx.x], g1 = p.gates[at * kGates + 256 + threadIdx.x % 64];
-        ss.load(s0);
-        su.load(e0);
-        gt[threadIdx.x] = g0;
-        if (threadIdx.x < 64) gt[256 + threadIdx.x] = g1;
-        a.put(qt);
-        b.put(kt);
-        lds_barrier();
-#pragma unroll
-        for (int ks = 0; ks < KD / 32; ++ks) qt.rows(16 * wave, 32 * ks, fq[ks]);
-        make_p<T, KD>(fq, kt, gt, p.scale, wave, x);
-    }
-    lds_barrier();
-    put_p<NPO>(x, wave, pt);
-    const int i = 16 * wave + l % 16;
-    const float lead = p.scale * gt[i];
-    T *op = static_cast<T *>(p.o) + ((c.b * p.tokens + c.t0 + i) * p.h + head) * p.dv_;
-    for (int v0 = 0; v0 < p.dvp; v0 += VS) {
-        ss.template put<NPO, false>(st, nullptr);
-        su.template put<NPO, true>(ut, gt + 2 * kC);
-        lds_barrier();
-        if (v0 + VS < p.dvp) {
-            ss.load(s0 + (v0 + VS) * KD);
-            su.load(e0 + (v0 + VS) * kC);
-        }
-        // rows v, columns tokens i: four neighbouring v a lane
-        facc acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-#pragma unroll
-        for (int ks = 0; ks < KD / 32; ++ks) {
-            bfrag a[2][NPO];
-#pragma unroll
-            for (int vt = 0; vt < 2; ++vt) st.rows(16 * vt, 32 * ks, a[vt]);
-            mma_two<NPO, NP, NPO, NP>(acc[0], a[0], fq[ks], acc[1], a[1], fq[ks]);
-        }
-#pragma unroll
-        for (int vt = 0; vt < 2; ++vt) acc[vt] *= lead;
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            if (32 * ks > 16 * wave + 15) continue;  // j <= i
-            bfrag b[NPO], a[2][NPO];
-            pt.rows(16 * wave, 32 * ks, b);
-#pragma unroll
-            for (int vt = 0; vt < 2; ++vt) ut.rows(16 * vt, 32 * ks, a[vt]);
-            mma_two<NPO, NPO, NPO, NPO>(acc[0], a[0], b, acc[1], a[1], b);
-        }
-        lds_barrier();
-        if (i < c.len) {
-#pragma unroll
-            for (int vt = 0; vt < 2; ++vt) {
-                const int v = v0 + 16 * vt + 4 * (l / 16);
-                if (p.vec_o && v + 4 <= p.dv_) {
-                    Raw<T, 4> r;
-                    float y[4] = {acc[vt][0], acc[vt][1], acc[vt][2], acc[vt][3]};
-                    r.set(y);
-                    r.store(op + v);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (v + j < p.dv_) store1(op + v + j, acc[vt][j]);
-                }
-            }
-        }
     }
 }
 
@@ -1614,8 +1602,8 @@ int chunk_passes(const DeltaArgs &a)
     const long seqs = a.n_seq > 0 ? a.n_seq : a.batch;
     // bytes of one head's chunks, in the order they are laid out
     const size_t n = static_cast<size_t>(p.slots);
-    const size_t gates = n * kGates * 4, mm = n * kMWords * 16, st = n * KD * p.dvp * 4, row = n * kC * p.dvp * 4;
-    const size_t each = gates + (GRAD ? 2 : 1) * (mm + st + row) + (GRAD ? row : 0);
+    const size_t gates = n * kGates * 4, mm = n * kTriFloats * 4, st = n * KD * p.dvp * 4, row = n * kC * p.dvp * 4;
+    const size_t each = gates + 2 * mm + (GRAD ? 2 * st + 3 * row : 0);
     constexpr int kDirs = GRAD ? 2 : 1;
     // columns a workgroup of the chains: 128 share what they read of a chunk,
     // narrower states would leave waves idle
@@ -1641,11 +1629,11 @@ int chunk_passes(const DeltaArgs &a)
             w += bytes * p.nh;
             return at;
         };
-        p.m = reinterpret_cast<word4 *>(take(mm));
-        p.s0 = reinterpret_cast<float *>(take(st));
-        p.e = reinterpret_cast<float *>(take(row));
+        p.m = reinterpret_cast<float *>(take(mm));
+        (GRAD ? p.mt : p.pm) = reinterpret_cast<float *>(take(mm));
         if (GRAD) {
-            p.mt = reinterpret_cast<word4 *>(take(mm));
+            p.s0 = reinterpret_cast<float *>(take(st));
+            p.e = reinterpret_cast<float *>(take(row));
             p.d1 = reinterpret_cast<float *>(take(st));
             p.dr = reinterpret_cast<float *>(take(row));
             p.z = reinterpret_cast<float *>(take(row));
@@ -1670,9 +1658,8 @@ int chunk_passes(const DeltaArgs &a)
         auto run_chains = [&](auto probe, auto threads) -> int {
             constexpr bool PROBE = decltype(probe)::value;
             constexpr int THREADS = decltype(threads)::value;
-            using F = SeqBuf<T, KD, false, THREADS>;
-            using B = SeqBuf<T, KD, true, THREADS>;
-            constexpr int kF = F::kBufs * F::kBytes, kB = B::kBufs * B::kBytes, kSeq = GRAD && kB > kF ? kB : kF;
+            constexpr int kF = SeqBuf<T, KD, false, !GRAD && !PROBE, THREADS>::kBytes, kB = SeqBuf<T, KD, true, false, THREADS>::kBytes;
+            constexpr int kSeq = GRAD && kB > kF ? kB : kF;
             const int st2 = big_lds(delta_seq<T, KD, GRAD, PROBE, THREADS>, kSeq);
             if (st2 != SSM2D_OK) return st2;
             delta_seq<T, KD, GRAD, PROBE, THREADS>
@@ -1708,11 +1695,6 @@ int chunk_passes(const DeltaArgs &a)
                 delta_local<T, KD, kWaves><<<dim3(slots, nk), dim3(kWaves * 64), kL, s>>>(p);
                 if ((rc = launched()) != SSM2D_OK) return rc;
             }
-        } else {
-            constexpr int kO = OutLds<T, KD>::kBytes;
-            if ((rc = big_lds(delta_out<T, KD>, kO)) != SSM2D_OK) return rc;
-            delta_out<T, KD><<<dim3(slots, nh), dim3(256), kO, s>>>(p);
-            if ((rc = launched()) != SSM2D_OK) return rc;
         }
     }
     return SSM2D_OK;
