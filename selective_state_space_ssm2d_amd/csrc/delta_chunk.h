@@ -430,7 +430,7 @@ __device__ __forceinline__ facc mfma4(float a, float b, facc c) { return __built
 // instructions (20 products of 16^3 a head: small beside the split products
 // elsewhere).
 template <typename T, int KD, bool BWD>
-__global__ __launch_bounds__(256, 3) void delta_prep(ChunkParams p)
+__global__ __launch_bounds__(256, KD == 128 && sizeof(T) == 4 ? 3 : 4) void delta_prep(ChunkParams p)
 {
     // Q, then K, then N and M share one place, so that several workgroups fit a
     // compute unit (the phases below wait for one another)
@@ -996,17 +996,15 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
                     mma_each_t<NP, NPO, 4>(O, a, bo);
                 }
             }
-            facc ga[4], gl[4], be[4], W[4];  // W: beta times the right-hand side
+            // (gamma, Gam_last and beta of the lane's tokens come from LDS at each use: kept, they take 48 registers)
+            auto gate = [&](int which, int t) { return *reinterpret_cast<const facc *>(gt + which * kC + 16 * t + 4 * g4); };
+            facc W[4];  // beta times the right-hand side
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                ga[t] = *reinterpret_cast<const facc *>(gt + 16 * t + 4 * g4);
-                gl[t] = *reinterpret_cast<const facc *>(gt + kC + 16 * t + 4 * g4);
-                be[t] = *reinterpret_cast<const facc *>(gt + 2 * kC + 16 * t + 4 * g4);
+                const facc f = gate(BWD ? 1 : 0, t);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    X[t][j] = BWD ? fmaf(gl[t][j], Y[t][j], y1[t][j]) : fmaf(-ga[t][j], Y[t][j], y0[t][j]);
-                    W[t][j] = be[t][j] * X[t][j];
-                }
+                for (int j = 0; j < 4; ++j) X[t][j] = BWD ? fmaf(f[j], Y[t][j], y1[t][j]) : fmaf(-f[j], Y[t][j], y0[t][j]);
+                W[t] = gate(2, t) * X[t];
             }
             // E = R - M (B R), or dR = dU - M^T (B dU)
 #pragma unroll
@@ -1034,7 +1032,7 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
             if constexpr (OUT) {
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    W2[t] = be[t] * X[t];              // U
+                    W2[t] = gate(2, t) * X[t];           // U
                     O[t] *= p.scale * gt[16 * t + l16];  // (this lane's token)
                 }
 #pragma unroll
@@ -1060,18 +1058,18 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
                 }
             }
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < 4; ++t) {
+                const facc bx = gate(2, t) * X[t];
+                if constexpr (BWD) {
+                    const facc ga = gate(0, t);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float bx = be[t][j] * X[t][j];
-                    if constexpr (BWD) {
-                        o0[4 * t + j] = bx;
-                        W[t][j] = -ga[t][j] * bx;
-                        W2[t][j] = p.scale * ga[t][j] * y0[t][j];
-                    } else {
-                        W[t][j] = gl[t][j] * bx;
-                    }
+                    for (int j = 0; j < 4; ++j) o0[4 * t + j] = bx[j];
+                    W[t] = -ga * bx;
+                    W2[t] = p.scale * ga * y0[t];
+                } else {
+                    W[t] = gate(1, t) * bx;
                 }
+            }
             const float last = gt[kC - 1];
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -1161,7 +1159,7 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
 // Workgroups (sequence and head, 64 or 128 columns, segment); with GRAD those of the
 // upper half of blockIdx.z run the adjoints' chain, at the same time.
 template <typename T, int KD, bool GRAD, bool PROBE, int THREADS>
-__global__ __launch_bounds__(THREADS, 1) void delta_seq(ChunkParams p)
+__global__ __launch_bounds__(THREADS, THREADS == 256 && KD <= 64 ? 2 : 1) void delta_seq(ChunkParams p)
 {
     extern __shared__ __align__(16) uint16_t lds[];
     if constexpr (GRAD) {
