@@ -127,7 +127,7 @@ __global__ __launch_bounds__(WPR * 64 > 256 ? WPR * 64 : 256) void ln_row_bwd(co
     }
     const float inv_n = 1.0f / static_cast<float>(n);
     // the next row is read while this one is worked on (where registers allow)
-    constexpr bool kAhead = NCH * VEC <= 16;
+    constexpr bool kAhead = NCH * VEC <= 16 && WPR < 16;
     Raw<T, VEC> nx[NCH], ng[NCH];
     float nmu = 0.0f, nrs = 0.0f;
     auto fetch = [&](long row) __attribute__((always_inline)) {
@@ -555,52 +555,86 @@ int pick_row(int64_t n, F &&f)
         if (n <= 64 * per) return SSM2D_ROW(4, 16);
         return SSM2D_ROW(16, 16);
     } else {
-        return SSM2D_ROW(4, 16);
+        return SSM2D_ROW(16 / VEC, 16);
     }
 #undef SSM2D_ROW
 }
 
-// The map kernels' variant: lanes over 16 pieces of VEC cells (64 cells one by
-// one where rows of cells are not aligned), channels over TY groups of at
-// most 16. A thread keeps NCH pieces (the backward two tensors' worth), so
-// 16-byte pieces go up to 384 channels (512 threads, 256 registers each) and
-// 8-byte ones up to 1024 (1024 threads, 128 registers); more channels are
-// read again each pass.
-template <int VEC, bool FULL, typename F>
+// The map kernels' variants. Lanes run over 16 pieces of VEC cells, or over 64
+// pieces of few cells where rows of cells are not aligned; channels over TY
+// groups of NCH at most, which a thread keeps (the backward those of two tensors
+// and two sums a channel). The widest piece is taken with which nothing spills:
+//   * forward: 16 bytes up to 384 channels, 8 up to 1024, single cells or 4
+//     bytes where rows allow no more; beyond, the tile is read again each pass
+//     (bf16, 21 x 1536 x 448: 36 us, 1.6 TB/s; 4 x 1024 x 3136 kept: 17 us, 3.1).
+//   * backward: 16 bytes up to 64 channels of bf16 and 128 of fp32 (bf16,
+//     4 x 96 x 50176: 45 us with 8-byte pieces, 71 with 16; fp32: 58 and 50),
+//     8 up to 512; beyond, read again (bf16, 4 x 768 x 3136: 37 us; 53 with
+//     4-byte pieces kept by 1024 threads, which spill).
+enum : int { kCells16 = 0, kCells8 = 1, kCells4 = 2, kCellsFew = 3 };
+
+template <int LEVEL, int VEC, bool BWD, typename F>
 int pick_map(int64_t n, F &&f)
 {
     using std::integral_constant;
 #define SSM2D_MAP(TX, TY, NCH, KEEP) \
     f(integral_constant<int, TX>{}, integral_constant<int, TY>{}, integral_constant<int, NCH>{}, std::bool_constant<KEEP>{})
-    if constexpr (VEC == 1) {
+    if constexpr (LEVEL == kCellsFew) {
         if (n <= 64) return SSM2D_MAP(64, 4, 16, true);
-        if (n <= 256) return SSM2D_MAP(64, 16, 16, true);
+        if constexpr (!BWD || VEC == 1) {
+            if (n <= 256) return SSM2D_MAP(64, 16, 16, true);
+        }
         return SSM2D_MAP(64, 16, 16, false);
-    } else {
-        if (n <= 64) return SSM2D_MAP(16, 16, 4, true);
+    } else if constexpr (LEVEL == kCells16) {
+        if (n <= 64 || (BWD && VEC == 8)) return SSM2D_MAP(16, 16, 4, true);
+        if constexpr (BWD && VEC == 4) return SSM2D_MAP(16, 16, 8, true);
+        if constexpr (!BWD) {
+            if (n <= 128) return SSM2D_MAP(16, 16, 8, true);
+            if (n <= 192) return SSM2D_MAP(16, 16, 12, true);
+            if (n <= 256) return SSM2D_MAP(16, 32, 8, true);
+            return SSM2D_MAP(16, 32, 12, true);
+        }
+    } else if constexpr (LEVEL == kCells8) {
+        if (n > (BWD ? 512 : 1024)) return SSM2D_MAP(16, 64, 16, false);
         if (n <= 128) return SSM2D_MAP(16, 16, 8, true);
         if (n <= 192) return SSM2D_MAP(16, 16, 12, true);
         if (n <= 256) return SSM2D_MAP(16, 32, 8, true);
         if (n <= 384) return SSM2D_MAP(16, 32, 12, true);
-        if constexpr (!FULL) {
+        if constexpr (BWD) {
+            return SSM2D_MAP(16, 32, 16, true);
+        } else {
+            if (n <= 512) return SSM2D_MAP(16, 32, 16, true);
             if (n <= 768) return SSM2D_MAP(16, 64, 12, true);
-            if (n <= 1024) return SSM2D_MAP(16, 64, 16, true);
+            return SSM2D_MAP(16, 64, 16, true);
         }
-        return SSM2D_MAP(16, 64, 16, false);
+    } else {
+        if (n <= 768) return SSM2D_MAP(16, 64, 12, true);
+        return SSM2D_MAP(16, 64, 16, true);
     }
 #undef SSM2D_MAP
 }
 
-// Cells a lane for `fits(v)`, whether v cells can be read at once everywhere:
-// 16 bytes, or 8 where that keeps more channels in registers.
-template <int V, typename P, typename F>
+// The piece for n channels; fits(v): v cells can be read at once everywhere.
+// Two cells of bf16 a lane spill for 65 to 256 channels of the backward (bf16,
+// 8 x 192 x 12546: 112 us, and 88 with one).
+template <int V, bool BWD, typename P, typename F>
 int pick_cells(int64_t n, P &&fits, F &&go)
 {
-    const bool half = fits(V / 2);
-    if (half && n > 384 && n <= 1024) return go(std::integral_constant<int, V / 2>{}, std::false_type{});
-    if (fits(V)) return go(std::integral_constant<int, V>{}, std::true_type{});
-    if (half) return go(std::integral_constant<int, V / 2>{}, std::false_type{});
-    return go(std::integral_constant<int, 1>{}, std::true_type{});
+    using std::integral_constant;
+    if (n <= (BWD ? 512 / V : 384) && fits(V)) return go(integral_constant<int, V>{}, integral_constant<int, kCells16>{});
+    if (fits(V / 2)) return go(integral_constant<int, V / 2>{}, integral_constant<int, kCells8>{});
+    const bool middle = n > 256 && n <= 1024;
+    if constexpr (V / 4 > 1) {
+        const bool few = BWD ? n <= 64 || n > 256 : !middle;
+        if (few && fits(V / 4)) return go(integral_constant<int, V / 4>{}, integral_constant<int, kCellsFew>{});
+        if constexpr (!BWD) {
+            if (middle && fits(V / 4)) return go(integral_constant<int, V / 4>{}, integral_constant<int, kCells4>{});
+        }
+    }
+    if constexpr (!BWD) {
+        if (middle) return go(integral_constant<int, 1>{}, integral_constant<int, kCells4>{});
+    }
+    return go(integral_constant<int, 1>{}, integral_constant<int, kCellsFew>{});
 }
 
 // Whether rows of `stride` elements from p can be read V elements at a time.
@@ -630,9 +664,9 @@ int norm_fwd(const T *x, const float *weight, const float *bias, T *y, float *me
         const bool wide = a.n % V == 0 && aligned_to(x, a.sb, 0, V) && !off_by(y, 16);
         return wide ? go(std::integral_constant<int, V>{}) : go(std::integral_constant<int, 1>{});
     }
-    auto go = [&](auto vec, auto full) {
+    auto go = [&](auto vec, auto level) {
         constexpr int VEC = decltype(vec)::value;
-        return pick_map<VEC, decltype(full)::value>(a.n, [&](auto tx, auto ty, auto nch, auto keep) {
+        return pick_map<decltype(level)::value, VEC, false>(a.n, [&](auto tx, auto ty, auto nch, auto keep) {
             constexpr int TX = decltype(tx)::value, TY = decltype(ty)::value, NCH = decltype(nch)::value;
             const int64_t tiles_b = (a.cells + TX * VEC - 1) / (TX * VEC), tiles = tiles_b * a.batch;
             ln_map_fwd<T, VEC, TX, TY, NCH, decltype(keep)::value><<<dim3(blocks_for(tiles, 1 << 20)), dim3(TX * TY), 0, a.s>>>(
@@ -641,7 +675,7 @@ int norm_fwd(const T *x, const float *weight, const float *bias, T *y, float *me
         });
     };
     auto fits = [&](int v) { return a.cells < kFar && a.sn < kFar && a.cells % v == 0 && aligned_to(x, a.batch > 1 ? a.sb : 0, a.n > 1 ? a.sn : 0, v) && !off_by(y, v * sizeof(T)); };
-    return pick_cells<V>(a.n, fits, go);
+    return pick_cells<V, false>(a.n, fits, go);
 }
 
 template <typename T>
@@ -685,9 +719,9 @@ int norm_bwd(const T *x, const float *weight, const float *mean, const float *rs
         const bool wide = a.n % V == 0 && aligned_to(x, a.sb, 0, V) && aligned_to(dy, a.gb, 0, V) && !off_by(dx, 16);
         return wide ? go(std::integral_constant<int, V>{}) : go(std::integral_constant<int, 1>{});
     }
-    auto go = [&](auto vec, auto full) {
+    auto go = [&](auto vec, auto level) {
         constexpr int VEC = decltype(vec)::value;
-        return pick_map<VEC, decltype(full)::value>(a.n, [&](auto tx, auto ty, auto nch, auto keep) {
+        return pick_map<decltype(level)::value, VEC, true>(a.n, [&](auto tx, auto ty, auto nch, auto keep) {
             constexpr int TX = decltype(tx)::value, TY = decltype(ty)::value, NCH = decltype(nch)::value;
             constexpr bool KEEP = decltype(keep)::value;
             const int64_t tiles_b = (a.cells + TX * VEC - 1) / (TX * VEC), tiles = tiles_b * a.batch;
@@ -713,7 +747,7 @@ int norm_bwd(const T *x, const float *weight, const float *mean, const float *rs
         return a.cells < kFar && a.sn < kFar && a.gn < kFar && a.cells % v == 0 && aligned_to(x, b * a.sb, c * a.sn, v) && aligned_to(dy, b * a.gb, c * a.gn, v) &&
                !off_by(dx, v * sizeof(T));
     };
-    return pick_cells<V>(a.n, fits, go);
+    return pick_cells<V, true>(a.n, fits, go);
 }
 
 int check_sizes(int64_t batch, int64_t n, int64_t cells)

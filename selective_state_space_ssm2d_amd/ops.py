@@ -183,9 +183,10 @@ def layer_norm_bwd(x, weight, mean, rstd, dy, *, channels_first=False, out=None,
     _f32((n,), weight=weight)
     _f32(x.shape[:1] + x.shape[2:] if channels_first else x.shape[:-1], mean=mean, rstd=rstd)
     out = out or {}
-    r = {"dx": _like("dx", out.get("dx"), x, stream),
-         "dweight": _out("dweight", out.get("dweight"), (n,), torch.float32, dev, stream),
-         "dbias": _out("dbias", out.get("dbias"), (n,), torch.float32, dev, stream)}
+    r = {"dx": _like("dx", out.get("dx"), x, stream)}
+    for name in ("dweight", "dbias"):
+        r[name] = (_out(name, out.get(name), (n,), torch.float32, dev, stream) if weight is None
+                   else _like(name, out.get(name), weight, stream))
     _run(fn, dev, stream, (x.data_ptr(), _ptr(weight), mean.data_ptr(), rstd.data_ptr(), dy.data_ptr(), r["dx"].data_ptr(),
                            r["dweight"].data_ptr(), r["dbias"].data_ptr(), batch, n, cells, sb, sn, gb, gn))
     return r
@@ -198,6 +199,15 @@ def _rope_shape(batch, tokens, hq, hk, d, qs, ks, sections, pos):
     return _RopeShape(batch, tokens, hq, hk, d, qs, ks, len(sections), sections + (0,) * (ROPE_MAX_AXES - len(sections)), pos)
 
 
+@functools.lru_cache(maxsize=64)
+def _sections(sections):
+    """(the sections as integers, the pairs they make)."""
+    if not 1 <= len(sections) <= ROPE_MAX_AXES:
+        raise ValueError(f"1 to {ROPE_MAX_AXES} sections")
+    sections = tuple(int(s) for s in sections)
+    return sections, sum(sections)
+
+
 def _strides(t, name):
     if t.shape[3] > 1 and t.stride(3) != 1:
         raise ValueError(f"the last dim of {name} must be contiguous")
@@ -206,28 +216,33 @@ def _strides(t, name):
 
 def _rope(q, k, positions, inv_freq, sections, interleaved, inverse, q_out, k_out, stream):
     fn, dev = _entry("ssm2d_rope", q.dtype), q.device
-    sections = tuple(int(s) for s in sections)
-    if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.dtype != q.dtype or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3])):
-        raise ValueError("q and k must be [batch, tokens, heads, d] of one dtype, alike but for their heads")
+    if q.dim() != 4:
+        raise ValueError("q must be [batch, tokens, heads, d]")
     B, T, hq, d = q.shape
-    if not 1 <= len(sections) <= ROPE_MAX_AXES:
-        raise ValueError(f"1 to {ROPE_MAX_AXES} sections")
-    if positions.dtype != torch.int32 or positions.shape not in ((len(sections), T), (len(sections), B, T)):
+    sections, pairs = _sections(tuple(sections))
+    axes = len(sections)
+    if positions.dtype != torch.int32 or positions.shape not in ((axes, T), (axes, B, T)):
         raise ValueError("positions must be int32 [axes, tokens] or [axes, batch, tokens]")
-    if T > 1 and positions.stride(-1) != 1:
+    ps = positions.stride()
+    if T > 1 and ps[-1] != 1:
         raise ValueError("the last dim of positions must be contiguous")
-    _on_gpu(dev, k=k, positions=positions, inv_freq=inv_freq)
-    _f32((sum(sections),), inv_freq=inv_freq)
-    q_out = _like("q_out", q_out, q, stream)
-    hk, ks = 0, (0, 0, 0)
+    if inv_freq.dtype != torch.float32 or inv_freq.shape != (pairs,) or not inv_freq.is_contiguous():
+        raise ValueError(f"inv_freq must be contiguous float32 [{pairs}]")
+    qs, ks, hk, kp, kop = q.stride(), (0, 0, 0), 0, None, None
+    if d > 1 and qs[3] != 1:
+        raise ValueError("the last dim of q must be contiguous")
     if k is not None:
-        k_out = _like("k_out", k_out, k, stream)
+        if k.dim() != 4 or k.dtype != q.dtype or k.shape[:2] != (B, T) or k.shape[3] != d:
+            raise ValueError("k must be [batch, tokens, heads, d] like q, but for the heads")
         hk, ks = k.shape[2], _strides(k, "k")
-    pos = (positions.stride(0), positions.stride(1) if positions.dim() == 3 else 0)
-    shape = _rope_shape(B, T, hq, hk, d, _strides(q, "q"), ks, sections, pos)
-    flags = (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0)
-    _run(fn, dev, stream, (q.data_ptr(), _ptr(k), positions.data_ptr(), inv_freq.data_ptr(), q_out.data_ptr(), _ptr(k_out) if hk else None,
-                           shape, flags))
+        k_out = _like("k_out", k_out, k, stream)
+        if hk:
+            kp, kop = k.data_ptr(), k_out.data_ptr()
+    _on_gpu(dev, k=k, positions=positions, inv_freq=inv_freq)
+    q_out = _like("q_out", q_out, q, stream)
+    shape = _rope_shape(B, T, hq, hk, d, qs[:3], ks, sections, (ps[0], ps[1] if len(ps) == 3 else 0))
+    _run(fn, dev, stream, (q.data_ptr(), kp, positions.data_ptr(), inv_freq.data_ptr(), q_out.data_ptr(), kop, shape,
+                           (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0)))
     return q_out, (k_out if k is not None else None)
 
 
