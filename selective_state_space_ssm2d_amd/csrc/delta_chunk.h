@@ -1608,9 +1608,10 @@ int chunk_passes(const DeltaArgs &a)
     const bool wide = !GRAD && p.dvp > 64, slim = !GRAD && p.dvp <= 32;
     const int cols = wide ? 128 : 64, vb = (p.dvp + cols - 1) / cols, pb = (p.dvp + KD + cols - 1) / cols;
     const int nhk = static_cast<int>(std::max(1.0, std::min<double>(a.hk, kMostBytes / (static_cast<double>(each) * p.rep))));
-    // (measured: a join takes 5.7 us of d_k' = 128, 0.6 us of 32, a step 5 and 3.3 us; two
-    // workgroups fit a compute unit where the state is small)
-    plan_segments(p, seqs * p.rep * nhk, GRAD, vb, pb, !GRAD && KD <= 64 ? 512 : 256, KD == 128 ? 1.0 : (KD == 64 ? 0.4 : 0.2));
+    // Measured: a join takes 5.7 us of d_k' = 128, 0.6 of 32, a step 5 and 3.3 us. Two
+    // workgroups fit a compute unit where the state is small (2 x 12 heads of 32 x 32,
+    // 12544 tokens, bf16 forward and backward: 440 us planned with one, 355 with two).
+    plan_segments(p, seqs * p.rep * nhk, GRAD, vb, pb, KD <= 64 ? 512 : 256, KD == 128 ? 1.0 : (KD == 64 ? 0.4 : 0.2));
     const size_t sa = static_cast<size_t>(p.nseg) * KD * KD * 4, ss = static_cast<size_t>(p.nseg) * KD * p.dvp * 4;
     const size_t seg_each = p.nseg > 1 ? static_cast<size_t>(seqs) * (sa + kDirs * ss) : 0;
     const size_t sums = GRAD && p.rep > 1 ? n * 2 * kC * KD * 4 : 0;  // by key head
