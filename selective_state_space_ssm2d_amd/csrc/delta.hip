@@ -54,6 +54,26 @@ int pass_states_on(const DeltaArgs &a, const float *in, float *out)
     return launched();
 }
 
+// Heads without keys or values leave nothing to sum: outputs that are not
+// empty themselves are zeros.
+template <typename T>
+__global__ void fill_zeros(T *out, long n)
+{
+    const long i = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (i < n) out[i] = 0;
+}
+
+template <typename T>
+int zeros(T *out, int64_t rows, int64_t d, void *stream)
+{
+    if (rows <= 0 || d <= 0) return SSM2D_OK;
+    if (rows * d > (int64_t{1} << 38)) return SSM2D_ERR_UNSUPPORTED;  // (a grid; far beyond memory)
+    if (!out) return SSM2D_ERR_NULLPTR;
+    if (off_by(out, sizeof(T))) return SSM2D_ERR_MISALIGNED;
+    fill_zeros<<<dim3(static_cast<unsigned>((rows * d + 255) / 256)), dim3(256), 0, static_cast<hipStream_t>(stream)>>>(out, rows * d);
+    return launched();
+}
+
 template <typename T>
 bool misaligned_in(const DeltaArgs &a)
 {
@@ -81,7 +101,8 @@ int fwd_entry(const T *q, const T *k, const T *v, const float *g, const float *b
     DeltaArgs a{};
     bool work = false;
     const int st = fill(&a, sh, scale, stream, &work);
-    if (st != SSM2D_OK || !work) return st;
+    if (st != SSM2D_OK) return st;
+    if (!work) return sh->d_k == 0 ? zeros(o, a.batch * a.tokens * a.h, a.dv_, stream) : SSM2D_OK;
     a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.h_init = h_init, a.cu = a.n_seq > 0 ? cu : nullptr, a.o = o, a.h_last = h_last;
     if (a.tokens > 0 && (!q || !k || !v || !g || !beta || !o || (a.n_seq > 0 && !cu))) return SSM2D_ERR_NULLPTR;
     if (misaligned_in<T>(a)) return SSM2D_ERR_MISALIGNED;
@@ -100,7 +121,17 @@ int bwd_entry(const T *q, const T *k, const T *v, const float *g, const float *b
     DeltaArgs a{};
     bool work = false;
     const int st = fill(&a, sh, scale, stream, &work);
-    if (st != SSM2D_OK || !work) return st;
+    if (st != SSM2D_OK) return st;
+    if (!work) {
+        const int64_t rows = a.batch * a.tokens;
+        int z = SSM2D_OK;
+        for (T *out : {dq, dk})
+            if (z == SSM2D_OK) z = zeros(out, rows * a.hk, a.dk_, stream);
+        if (z == SSM2D_OK) z = zeros(dv, rows * a.h, a.dv_, stream);
+        for (float *out : {dg, dbeta})
+            if (z == SSM2D_OK) z = zeros(out, rows * a.h, 1, stream);
+        return z;
+    }
     a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.h_init = h_init, a.cu = a.n_seq > 0 ? cu : nullptr, a.dout = dout, a.dh_last = dh_last;
     a.dq = dq, a.dk = dk, a.dv = dv, a.dg = dg, a.dbeta = dbeta, a.dh_init = dh_init;
     if (a.tokens > 0 && (!q || !k || !v || !g || !beta || !dout || !dq || !dk || !dv || !dg || !dbeta || (a.n_seq > 0 && !cu)))
@@ -120,7 +151,8 @@ int step_entry(const T *q, const T *k, const T *v, const float *g, const float *
     bool work = false;
     if (sh && sh->n_seq != 0) return SSM2D_ERR_BAD_FLAGS;
     const int st = fill(&a, sh, scale, stream, &work);
-    if (st != SSM2D_OK || !work || a.tokens == 0) return st;
+    if (st != SSM2D_OK || a.tokens == 0) return st;
+    if (!work) return sh->d_k == 0 ? zeros(o, a.batch * a.tokens * a.h, a.dv_, stream) : SSM2D_OK;
     a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.h_init = state, a.h_last = state, a.o = o;
     if (!q || !k || !v || !g || !beta || !state || !o) return SSM2D_ERR_NULLPTR;
     if (misaligned_in<T>(a)) return SSM2D_ERR_MISALIGNED;

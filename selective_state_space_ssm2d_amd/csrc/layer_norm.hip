@@ -528,6 +528,7 @@ struct NormArgs {
 };
 
 constexpr int64_t kFar = int64_t{1} << 26;
+inline bool near(int64_t stride) { return stride >= 0 && stride < kFar; }
 constexpr int kMaxParts = 512;  // partial rows of dweight and dbias (the workgroups of a backward launch)
 
 // Workgroups for `work` turns of a loop: at most `most`, all with as many turns (but the last).
@@ -674,7 +675,10 @@ int norm_fwd(const T *x, const float *weight, const float *bias, T *y, float *me
             return launched();
         });
     };
-    auto fits = [&](int v) { return a.cells < kFar && a.sn < kFar && a.cells % v == 0 && aligned_to(x, a.batch > 1 ? a.sb : 0, a.n > 1 ? a.sn : 0, v) && !off_by(y, v * sizeof(T)); };
+    auto fits = [&](int v) {
+        return a.cells < kFar && near(a.sn) && a.cells % v == 0 && aligned_to(x, a.batch > 1 ? a.sb : 0, a.n > 1 ? a.sn : 0, v) &&
+               !off_by(y, v * sizeof(T));
+    };
     return pick_cells<V, false>(a.n, fits, go);
 }
 
@@ -744,8 +748,8 @@ int norm_bwd(const T *x, const float *weight, const float *mean, const float *rs
     };
     auto fits = [&](int v) {
         const int64_t b = a.batch > 1, c = a.n > 1;
-        return a.cells < kFar && a.sn < kFar && a.gn < kFar && a.cells % v == 0 && aligned_to(x, b * a.sb, c * a.sn, v) && aligned_to(dy, b * a.gb, c * a.gn, v) &&
-               !off_by(dx, v * sizeof(T));
+        return a.cells < kFar && near(a.sn) && near(a.gn) && a.cells % v == 0 && aligned_to(x, b * a.sb, c * a.sn, v) &&
+               aligned_to(dy, b * a.gb, c * a.gn, v) && !off_by(dx, v * sizeof(T));
     };
     return pick_cells<V, true>(a.n, fits, go);
 }

@@ -269,6 +269,10 @@ def _delta_shape(batch, tokens, n_seq, hk, h, dk, dv, qs, ks, vs, os, gs, bs):
     return _DeltaShape(batch, tokens, n_seq, hk, h, dk, dv, qs, ks, vs, os, gs, bs)
 
 
+def _scale(scale, d_k):
+    return max(d_k, 1) ** -0.5 if scale is None else float(scale)
+
+
 def _delta_check(q, k, v, g, beta, cu_seqlens, do=None):
     """(device, sequences, the C shape) of one call's checked tensors [batch, tokens, heads, d]."""
     if q.dim() != 4 or k.shape != q.shape or v.dim() != 4 or v.shape[:2] != q.shape[:2]:
@@ -317,7 +321,7 @@ def gated_delta_fwd(q, k, v, g, beta, *, scale=None, h_init=None, cu_seqlens=Non
     if return_last_state or h_last is not None:
         h_last = _out("h_last", h_last, states, torch.float32, dev, stream)
     _run(fn, dev, stream, (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(h_init), _ptr(cu_seqlens),
-                           o.data_ptr(), _ptr(h_last), shape, q.shape[3] ** -0.5 if scale is None else float(scale)))
+                           o.data_ptr(), _ptr(h_last), shape, _scale(scale, q.shape[3])))
     return (o, h_last) if return_last_state else o
 
 
@@ -336,7 +340,7 @@ def gated_delta_bwd(q, k, v, g, beta, do, *, scale=None, h_init=None, dh_last=No
         r["dh_init"] = _out("dh_init", out.get("dh_init"), states, torch.float32, dev, stream)
     _run(fn, dev, stream, (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(h_init), _ptr(cu_seqlens),
                            do.data_ptr(), _ptr(dh_last), *(r[n].data_ptr() for n in ("dq", "dk", "dv", "dg", "dbeta")), _ptr(r.get("dh_init")),
-                           shape, q.shape[3] ** -0.5 if scale is None else float(scale)))
+                           shape, _scale(scale, q.shape[3])))
     return r
 
 
@@ -370,5 +374,5 @@ def gated_delta_step(q, k, v, g, beta, state, *, scale=None, o=None, stream=None
     _f32((B, h, dk, dv), state=state)
     o = _like("o", o, v, stream)
     _run(fn, dev, stream, (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(), o.data_ptr(),
-                           shape, dk ** -0.5 if scale is None else float(scale)))
+                           shape, _scale(scale, dk)))
     return o
