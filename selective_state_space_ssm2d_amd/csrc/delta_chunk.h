@@ -61,9 +61,9 @@ struct ChunkParams {
     float *s0, *d1;                     // [KD][dvp]
     float *e, *dr, *z;                  // [kC][dvp]
     // by [sequence][head of this pass][segment]: a segment's transition
-    // [KD][KD], its state from zero and then its first state (forward and
-    // adjoint) [KD][dvp]
-    float *seg_a, *seg_s, *seg_d;
+    // [KD][KD] (as tiles of its columns, for adjoints, and of its rows), its state
+    // from zero and then its first state (forward and adjoint) [KD][dvp]
+    float *seg_a, *seg_at, *seg_s, *seg_d;
     float *sum;                         // dQ and dK of shared heads so far, by [slot][key head]
     int turn;                           // which of the heads that share a key head (delta_local)
     int nseg, seg_len;                  // segments of the longest sequence, chunks a segment
@@ -1139,6 +1139,15 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
     }
     if constexpr (PROBE) {
         if (!act) return;
+        if (unit) {
+            // A for delta_join: as operands' tiles of its rows, and for the adjoint of its columns
+            float *at = p.seg_at + segs * KD + v0 * 16 + (4 * g4 + 16 * (l16 / 4)) * 4 + l16 % 4;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) at[t * (NT * 256) + j * 4] = S[t][j];
+            if (!p.seg_a) return;
+        }
         float *end = unit ? p.seg_a + segs * KD + v0 * KD + l * 4 : joined;
 #pragma unroll
         for (int t = 0; t < NT; ++t) *reinterpret_cast<facc *>(end + t * 256) = S[t];
@@ -1173,17 +1182,17 @@ __global__ __launch_bounds__(THREADS, THREADS == 256 && KD <= 64 ? 2 : 1) void d
 
 // First states of the segments: S over a sequence's segments, S <- A S + b
 // (adjoint: D <- A^T D + b from the last one), each stored in b's place.
-// Workgroup (sequence and head, 64 or 128 columns, forward or adjoint); A goes
-// through LDS in three parts (its transpose: a piece of A is four neighbours
-// of a column), 16 columns of the state a wave as in seq_chain.
-template <typename T, int KD, bool GRAD, int THREADS>
-__global__ __launch_bounds__(THREADS, 1) void delta_join(ChunkParams p)
+// Workgroup (sequence and head, 16 columns, forward or adjoint), a wave 16 rows
+// of the state: its rows of A come from memory as operands, and only the
+// state's parts pass through LDS, one barrier a segment. What a step waits for
+// is its own chain (parts, LDS, products), so few rows a wave: with 64 columns
+// a workgroup and all rows a wave, A through LDS, a step of 128 x 128 took 5.7
+// us.
+template <typename T, int KD, bool GRAD>
+__global__ __launch_bounds__(KD * 4, 1) void delta_join(ChunkParams p)
 {
-    using AT = Tile<3, KD, KD>;
-    constexpr bool kTwo = KD <= 64;  // two buffers, so one barrier a step
-    constexpr int DEPTH = KD == 32 ? 8 : (KD == 64 ? 4 : 2);
-    constexpr int NT = KD / 16, kAll = KD * KD / 4, kPieces = (kAll + THREADS - 1) / THREADS, kGroup = NT < 4 ? NT : 4;
-    extern __shared__ __align__(16) uint16_t lds[];
+    constexpr int NT = KD / 16, KS = KD / 32, DEPTH = KD == 128 ? 3 : (KD == 64 ? 6 : 8);
+    __shared__ __align__(16) word4 parts[2][3][KS][64];  // [turn][part]: two tiles' parts, a lane's 16 bytes
     const bool bwd = GRAD && blockIdx.z == 1;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64, g4 = l / 16, l16 = l % 16;
     const long s = blockIdx.x / p.nh;
@@ -1191,85 +1200,68 @@ __global__ __launch_bounds__(THREADS, 1) void delta_join(ChunkParams p)
     const Seq q = find_seq(p, s);
     const long n_all = (q.len + kC - 1) / kC;
     const int ns = n_all > 0 ? static_cast<int>((n_all + p.seg_len - 1) / p.seg_len) : 1;
-    const int v0 = blockIdx.y * (THREADS / 4) + wave * 16, col = v0 + l16;
-    const bool act = v0 < p.dvp, live = col < p.dv_;
+    const int v0 = blockIdx.y * 16, col = v0 + l16;
     const float *init = bwd ? p.dh_last : p.h_init;
     const long state = ((s * p.h + head) * p.dk_) * p.dv_;
-    facc S[NT];
+    facc S;
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int row = 16 * t + 4 * g4 + j;
-            S[t][j] = init ? init[state + static_cast<long>(min(row, p.dk_ - 1)) * p.dv_ + min(col, p.dv_ - 1)] : 0.0f;
-            S[t][j] = (live && row < p.dk_) ? S[t][j] : 0.0f;
-        }
+    for (int j = 0; j < 4; ++j) {
+        const int row = 16 * wave + 4 * g4 + j;
+        S[j] = init ? init[state + static_cast<long>(min(row, p.dk_ - 1)) * p.dv_ + min(col, p.dv_ - 1)] : 0.0f;
+        S[j] = (col < p.dv_ && row < p.dk_) ? S[j] : 0.0f;
+    }
     // A and b of the next DEPTH segments, read that far ahead: another XCD wrote
     // them, so they come from memory, later than a step or two
-    facc a[DEPTH][kPieces], b[DEPTH][NT];
+    facc a[DEPTH][NT], b[DEPTH];
     auto seg = [&](int i) { return static_cast<long>(blockIdx.x) * p.nseg + (bwd ? ns - 1 - i : i); };
-    auto place = [&](int i) { return (bwd ? p.seg_d : p.seg_s) + seg(i) * KD * p.dvp + (act ? v0 : 0) * KD + l * 4; };
-    auto fetch = [&](int i, int at) __attribute__((always_inline)) {  // (the last segment's A and b are not needed; nor, maybe, there)
-        const float *src = p.seg_a + seg(i) * KD * KD;
+    auto place = [&](int i) { return (bwd ? p.seg_d : p.seg_s) + seg(i) * KD * p.dvp + v0 * KD + wave * 256 + l * 4; };
+    auto fetch = [&](int i, int at) __attribute__((always_inline)) {  // (past the end the last segment's, which are not used)
+        i = min(i, ns - 1);
+        const float *src = (bwd ? p.seg_a : p.seg_at) + seg(i) * KD * KD + wave * (NT * 256) + l * 4;
 #pragma unroll
-        for (int k = 0; k < kPieces; ++k) a[at][k] = *reinterpret_cast<const facc *>(src + min(k * THREADS + static_cast<int>(threadIdx.x), kAll - 1) * 4);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) b[at][t] = *reinterpret_cast<const facc *>(place(i) + t * 256);
+        for (int t = 0; t < NT; ++t) a[at][t] = *reinterpret_cast<const facc *>(src + t * 256);
+        b[at] = *reinterpret_cast<const facc *>(place(i));
     };
+    if (ns > 1) {
 #pragma unroll
-    for (int u = 0; u < DEPTH; ++u)
-        if (u + 1 < ns) fetch(u, u);
-    for (int i0 = 0; i0 + 1 < ns; i0 += DEPTH) {
+        for (int u = 0; u < DEPTH; ++u) fetch(u, u);
+        for (int i0 = 0; i0 + 1 < ns; i0 += DEPTH) {
 #pragma unroll
-        for (int u = 0; u < DEPTH; ++u) {
-            const int i = i0 + u;
-            if (i + 1 >= ns) break;
-            // (two buffers: the A before this one may still be in use)
-            const AT at{lds + (kTwo ? (i & 1) * (AT::kBytes / 2) : 0)};
-            if (!kTwo) lds_barrier();
+            for (int u = 0; u < DEPTH; ++u) {
+                const int i = i0 + u;
+                if (i + 1 >= ns) break;
+                unsigned w0[3], w1[3];
+                split2<3>(S[0], S[1], w0);
+                split2<3>(S[2], S[3], w1);
+                const int turn = i & 1;
 #pragma unroll
-            for (int k = 0; k < kPieces; ++k) {
-                const int w = k * THREADS + threadIdx.x, tile = w / 64;
-                if (kAll % THREADS == 0 || w < kAll)
-                    at.put4(16 * (tile / NT) + w % 16, 16 * (tile % NT) + 4 * (w % 64 / 16), a[u][k][0], a[u][k][1], a[u][k][2], a[u][k][3]);
-            }
-            facc out[NT];
+                for (int n = 0; n < 3; ++n)
+                    reinterpret_cast<uint2 *>(&parts[turn][n][wave / 2][l])[wave % 2] = make_uint2(w0[n], w1[n]);
+                bfrag m[KS][3];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                out[t] = S[t];
-                S[t] = b[u][t];
-            }
-            float *to = place(i);
-            lds_barrier();
-            if (i + DEPTH + 1 < ns) fetch(i + DEPTH, u);
-            if (!act) continue;
+                for (int ks = 0; ks < KS; ++ks) split_acc<3>(a[u][2 * ks], a[u][2 * ks + 1], m[ks]);
+                facc x = b[u], y = {0.0f, 0.0f, 0.0f, 0.0f};
+                float *to = place(i);
+                const facc out = S;
+                fetch(i + DEPTH, u);
+                lds_barrier();
 #pragma unroll
-            for (int ks = 0; ks < KD / 32; ++ks) {
-                bfrag f[3];
-                split_acc<3>(out[2 * ks], out[2 * ks + 1], f);
+                for (int ks = 0; ks < KS; ++ks) {
+                    bfrag f[3];
 #pragma unroll
-                for (int t = 0; t < NT; t += kGroup) {
-                    bfrag m[kGroup][3];
-                    facc acc[kGroup];
-#pragma unroll
-                    for (int g = 0; g < kGroup; ++g) {
-                        if (bwd) at.rows(16 * (t + g), 32 * ks, m[g]);
-                        else at.cols(32 * ks, 16 * (t + g), m[g]);
-                        acc[g] = S[t + g];
+                    for (int n = 0; n < 3; ++n) {
+                        FragBits r;
+                        r.q = parts[turn][n][ks][l];
+                        f[n] = r.f;
                     }
-                    mma_each<3, 3, kGroup>(acc, m, f);
-#pragma unroll
-                    for (int g = 0; g < kGroup; ++g) S[t + g] = acc[g];
+                    mma<3, 3>(ks % 2 ? y : x, m[ks], f);
                 }
+                S = x + y;
+                *reinterpret_cast<facc *>(to) = out;
             }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) *reinterpret_cast<facc *>(to + t * 256) = out[t];
         }
     }
-    if (act) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) *reinterpret_cast<facc *>(place(ns - 1) + t * 256) = S[t];
-    }
+    *reinterpret_cast<facc *>(place(ns - 1)) = S;
 }
 
 // ------------------------------------------------------------------ delta_local
@@ -1613,7 +1605,7 @@ int chunk_passes(const DeltaArgs &a)
     // 12544 tokens, bf16 forward and backward: 440 us planned with one, 355 with two).
     plan_segments(p, seqs * p.rep * nhk, GRAD, vb, pb, KD <= 64 ? 512 : 256, KD == 128 ? 1.0 : (KD == 64 ? 0.4 : 0.2));
     const size_t sa = static_cast<size_t>(p.nseg) * KD * KD * 4, ss = static_cast<size_t>(p.nseg) * KD * p.dvp * 4;
-    const size_t seg_each = p.nseg > 1 ? static_cast<size_t>(seqs) * (sa + kDirs * ss) : 0;
+    const size_t seg_each = p.nseg > 1 ? static_cast<size_t>(seqs) * kDirs * (sa + ss) : 0;
     const size_t sums = GRAD && p.rep > 1 ? n * 2 * kC * KD * 4 : 0;  // by key head
     void *ws = nullptr;
     int rc = get_aux_ws(a.dev, a.stream, kSlotDelta, ((each + seg_each) * p.rep + sums) * nhk, &ws);
@@ -1639,7 +1631,8 @@ int chunk_passes(const DeltaArgs &a)
         }
         p.gates = reinterpret_cast<float *>(take(gates));
         if (p.nseg > 1) {
-            p.seg_a = reinterpret_cast<float *>(take(seqs * sa));
+            p.seg_at = reinterpret_cast<float *>(take(seqs * sa));
+            if (GRAD) p.seg_a = reinterpret_cast<float *>(take(seqs * sa));
             p.seg_s = reinterpret_cast<float *>(take(seqs * ss));
             if (GRAD) p.seg_d = reinterpret_cast<float *>(take(seqs * ss));
         }
@@ -1676,15 +1669,8 @@ int chunk_passes(const DeltaArgs &a)
         };
         if (p.nseg > 1) {
             if ((rc = chains_of(std::true_type{})) != SSM2D_OK) return rc;
-            auto join = [&](auto threads) -> int {
-                constexpr int THREADS = decltype(threads)::value, kJ = (KD <= 64 ? 2 : 1) * Tile<3, KD, KD>::kBytes;
-                const int st2 = big_lds(delta_join<T, KD, GRAD, THREADS>, kJ);
-                if (st2 != SSM2D_OK) return st2;
-                delta_join<T, KD, GRAD, THREADS>
-                    <<<dim3(chains, static_cast<unsigned>((p.dvp + THREADS / 4 - 1) / (THREADS / 4)), kDirs), dim3(THREADS), kJ, s>>>(p);
-                return launched();
-            };
-            if ((rc = join(std::integral_constant<int, 256>{})) != SSM2D_OK) return rc;
+            delta_join<T, KD, GRAD><<<dim3(chains, static_cast<unsigned>(p.dvp / 16), kDirs), dim3(KD * 4), 0, s>>>(p);
+            if ((rc = launched()) != SSM2D_OK) return rc;
         }
         if ((rc = chains_of(std::false_type{})) != SSM2D_OK) return rc;
         if constexpr (GRAD) {
