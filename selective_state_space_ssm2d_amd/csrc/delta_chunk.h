@@ -61,9 +61,11 @@ struct ChunkParams {
     float *s0, *d1;                     // [KD][dvp]
     float *e, *dr, *z;                  // [kC][dvp]
     // by [sequence][head of this pass][segment]: a segment's transition
-    // [KD][KD] (as tiles of its columns, for adjoints, and of its rows), its state
-    // from zero and then its first state (forward and adjoint) [KD][dvp]
-    float *seg_a, *seg_at, *seg_s, *seg_d;
+    // [KD][KD] (as operands of its columns, for adjoints, and of its rows, in three
+    // parts), its state from zero and then its first state (forward and adjoint)
+    // [KD][dvp]
+    word4 *seg_a, *seg_at;
+    float *seg_s, *seg_d;
     float *sum;                         // dQ and dK of shared heads so far, by [slot][key head]
     int turn;                           // which of the heads that share a key head (delta_local)
     int nseg, seg_len;                  // segments of the longest sequence, chunks a segment
@@ -75,6 +77,10 @@ struct ChunkParams {
     int vec_qk, vec_do, vec_v;          // rows of q and k, of dout, of v can be read 16 bytes at a time
     int vec_o, vec_dqk;                 // rows of o, of dq and dk can be written four elements at a time
 };
+
+// 16-byte words of 16 rows (columns) of a segment's transition
+template <int KD>
+constexpr int kSegTile = KD / 32 * 3 * 64;
 
 using bfrag = __bf16 __attribute__((ext_vector_type(8)));
 using facc = float __attribute__((ext_vector_type(4)));
@@ -168,6 +174,24 @@ __device__ __forceinline__ void split_acc(const facc &lo, const facc &hi, bfrag 
     }
 #pragma unroll
     for (int n = 0; n < N; ++n) f[n] = b[n].f;
+}
+
+// 4 x 4 values of four neighbouring lanes, turned: lane b's j-th was lane j's b-th.
+__device__ __forceinline__ facc turn4(facc v)
+{
+    const int b = threadIdx.x % 4;
+    auto swap = [&](int i, int j, bool high, auto ctrl) __attribute__((always_inline)) {
+        const float r = __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(high ? v[i] : v[j]), decltype(ctrl)::value, 0xf, 0xf, true));
+        if (high) v[i] = r;
+        else v[j] = r;
+    };
+    constexpr std::integral_constant<int, 0xb1> one{};  // lanes 1 apart
+    constexpr std::integral_constant<int, 0x4e> two{};  // lanes 2 apart
+    swap(0, 1, b & 1, one);
+    swap(2, 3, b & 1, one);
+    swap(0, 2, b & 2, two);
+    swap(1, 3, b & 2, two);
+    return v;
 }
 
 // acc += a b over the parts whose product reaches the last place kept.
@@ -1140,17 +1164,31 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
     if constexpr (PROBE) {
         if (!act) return;
         if (unit) {
-            // A for delta_join: as operands' tiles of its rows, and for the adjoint of its columns
-            float *at = p.seg_at + segs * KD + v0 * 16 + (4 * g4 + 16 * (l16 / 4)) * 4 + l16 % 4;
+            // A for delta_join, in parts: its rows' operands (four columns of a row
+            // a lane), and for the adjoint its columns'
+            const long at = segs / KD * (kSegTile<KD> * NT);
+            uint2 *rows = reinterpret_cast<uint2 *>(p.seg_at + at + v0 / 32 * 3 * 64 + 4 * g4 + l16 % 4 + 16 * (l16 / 4)) + v0 / 16 % 2;
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < NT; ++t) {
+                const facc r = turn4(S[t]);
+                unsigned w0[3], w1[3];
+                split2<3>(r[0], r[1], w0);
+                split2<3>(r[2], r[3], w1);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) at[t * (NT * 256) + j * 4] = S[t][j];
+                for (int n = 0; n < 3; ++n) rows[2 * (t * kSegTile<KD> + n * 64)] = make_uint2(w0[n], w1[n]);
+            }
             if (!p.seg_a) return;
-        }
-        float *end = unit ? p.seg_a + segs * KD + v0 * KD + l * 4 : joined;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) *reinterpret_cast<facc *>(end + t * 256) = S[t];
+            for (int ks = 0; ks < NT / 2; ++ks) {
+                bfrag f[3];
+                split_acc<3>(S[2 * ks], S[2 * ks + 1], f);
+#pragma unroll
+                for (int n = 0; n < 3; ++n) p.seg_a[at + v0 / 16 * kSegTile<KD> + (ks * 3 + n) * 64 + l] = FragBits{.f = f[n]}.q;
+            }
+            return;
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) *reinterpret_cast<facc *>(joined + t * 256) = S[t];
         return;
     }
     float *out = BWD ? p.dh_init : p.h_last;
@@ -1182,16 +1220,16 @@ __global__ __launch_bounds__(THREADS, THREADS == 256 && KD <= 64 ? 2 : 1) void d
 
 // First states of the segments: S over a sequence's segments, S <- A S + b
 // (adjoint: D <- A^T D + b from the last one), each stored in b's place.
-// Workgroup (sequence and head, 16 columns, forward or adjoint), a wave 16 rows
-// of the state: its rows of A come from memory as operands, and only the
-// state's parts pass through LDS, one barrier a segment. What a step waits for
-// is its own chain (parts, LDS, products), so few rows a wave: with 64 columns
-// a workgroup and all rows a wave, A through LDS, a step of 128 x 128 took 5.7
-// us.
+// Workgroup (sequence and head, 16 columns, forward or adjoint). What a step
+// waits for is its own chain (the state's parts, products), so a wave has few
+// rows: 16, with the state's parts through LDS and one barrier a segment, or a
+// small state's 32, whose parts stay in registers. A comes as operands, split
+// by the probe. (With 64 columns a workgroup, all rows a wave and A through
+// LDS a step of 128 x 128 took 5.7 us.)
 template <typename T, int KD, bool GRAD>
-__global__ __launch_bounds__(KD * 4, 1) void delta_join(ChunkParams p)
+__global__ __launch_bounds__(KD == 32 ? 64 : KD * 4, 1) void delta_join(ChunkParams p)
 {
-    constexpr int NT = KD / 16, KS = KD / 32, DEPTH = KD == 128 ? 3 : (KD == 64 ? 6 : 8);
+    constexpr int NT = KD / 16, KS = KD / 32, WT = KD == 32 ? 2 : 1, DEPTH = KD == 128 ? 2 : (KD == 64 ? 4 : 6);
     __shared__ __align__(16) word4 parts[2][3][KS][64];  // [turn][part]: two tiles' parts, a lane's 16 bytes
     const bool bwd = GRAD && blockIdx.z == 1;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64, g4 = l / 16, l16 = l % 16;
@@ -1203,24 +1241,32 @@ __global__ __launch_bounds__(KD * 4, 1) void delta_join(ChunkParams p)
     const int v0 = blockIdx.y * 16, col = v0 + l16;
     const float *init = bwd ? p.dh_last : p.h_init;
     const long state = ((s * p.h + head) * p.dk_) * p.dv_;
-    facc S;
+    facc S[WT];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int row = 16 * wave + 4 * g4 + j;
-        S[j] = init ? init[state + static_cast<long>(min(row, p.dk_ - 1)) * p.dv_ + min(col, p.dv_ - 1)] : 0.0f;
-        S[j] = (col < p.dv_ && row < p.dk_) ? S[j] : 0.0f;
-    }
+    for (int t = 0; t < WT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int row = 16 * (wave * WT + t) + 4 * g4 + j;
+            S[t][j] = init ? init[state + static_cast<long>(min(row, p.dk_ - 1)) * p.dv_ + min(col, p.dv_ - 1)] : 0.0f;
+            S[t][j] = (col < p.dv_ && row < p.dk_) ? S[t][j] : 0.0f;
+        }
     // A and b of the next DEPTH segments, read that far ahead: another XCD wrote
     // them, so they come from memory, later than a step or two
-    facc a[DEPTH][NT], b[DEPTH];
+    word4 a[DEPTH][WT][KS][3];
+    facc b[DEPTH][WT];
     auto seg = [&](int i) { return static_cast<long>(blockIdx.x) * p.nseg + (bwd ? ns - 1 - i : i); };
-    auto place = [&](int i) { return (bwd ? p.seg_d : p.seg_s) + seg(i) * KD * p.dvp + v0 * KD + wave * 256 + l * 4; };
+    auto place = [&](int i) { return (bwd ? p.seg_d : p.seg_s) + seg(i) * KD * p.dvp + v0 * KD + wave * WT * 256 + l * 4; };
     auto fetch = [&](int i, int at) __attribute__((always_inline)) {  // (past the end the last segment's, which are not used)
         i = min(i, ns - 1);
-        const float *src = (bwd ? p.seg_a : p.seg_at) + seg(i) * KD * KD + wave * (NT * 256) + l * 4;
+        const word4 *src = (bwd ? p.seg_a : p.seg_at) + seg(i) * kSegTile<KD> * NT + wave * WT * kSegTile<KD> + l;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) a[at][t] = *reinterpret_cast<const facc *>(src + t * 256);
-        b[at] = *reinterpret_cast<const facc *>(place(i));
+        for (int t = 0; t < WT; ++t) {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int n = 0; n < 3; ++n) a[at][t][ks][n] = src[t * kSegTile<KD> + (ks * 3 + n) * 64];
+            b[at][t] = *reinterpret_cast<const facc *>(place(i) + t * 256);
+        }
     };
     if (ns > 1) {
 #pragma unroll
@@ -1230,38 +1276,48 @@ __global__ __launch_bounds__(KD * 4, 1) void delta_join(ChunkParams p)
             for (int u = 0; u < DEPTH; ++u) {
                 const int i = i0 + u;
                 if (i + 1 >= ns) break;
-                unsigned w0[3], w1[3];
-                split2<3>(S[0], S[1], w0);
-                split2<3>(S[2], S[3], w1);
                 const int turn = i & 1;
+                bfrag f[KS][3];
+                if constexpr (WT == NT) {
+                    split_acc<3>(S[0], S[1], f[0]);
+                } else {
+                    unsigned w0[3], w1[3];
+                    split2<3>(S[0][0], S[0][1], w0);
+                    split2<3>(S[0][2], S[0][3], w1);
 #pragma unroll
-                for (int n = 0; n < 3; ++n)
-                    reinterpret_cast<uint2 *>(&parts[turn][n][wave / 2][l])[wave % 2] = make_uint2(w0[n], w1[n]);
-                bfrag m[KS][3];
+                    for (int n = 0; n < 3; ++n)
+                        reinterpret_cast<uint2 *>(&parts[turn][n][wave / 2][l])[wave % 2] = make_uint2(w0[n], w1[n]);
+                    lds_barrier();
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) split_acc<3>(a[u][2 * ks], a[u][2 * ks + 1], m[ks]);
-                facc x = b[u], y = {0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                        for (int n = 0; n < 3; ++n) f[ks][n] = FragBits{.q = parts[turn][n][ks][l]}.f;
+                }
                 float *to = place(i);
-                const facc out = S;
-                fetch(i + DEPTH, u);
-                lds_barrier();
+                facc out[WT], x[WT], y[WT];
+#pragma unroll
+                for (int t = 0; t < WT; ++t) out[t] = S[t], x[t] = b[u][t], y[t] = facc{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
-                    bfrag f[3];
+                    bfrag m[WT][3];
 #pragma unroll
-                    for (int n = 0; n < 3; ++n) {
-                        FragBits r;
-                        r.q = parts[turn][n][ks][l];
-                        f[n] = r.f;
-                    }
-                    mma<3, 3>(ks % 2 ? y : x, m[ks], f);
+                    for (int t = 0; t < WT; ++t)
+#pragma unroll
+                        for (int n = 0; n < 3; ++n) m[t][n] = FragBits{.q = a[u][t][ks][n]}.f;
+                    if (ks % 2) mma_each<3, 3, WT>(y, m, f[ks]);
+                    else mma_each<3, 3, WT>(x, m, f[ks]);
                 }
-                S = x + y;
-                *reinterpret_cast<facc *>(to) = out;
+                fetch(i + DEPTH, u);
+#pragma unroll
+                for (int t = 0; t < WT; ++t) {
+                    S[t] = KS > 1 ? x[t] + y[t] : x[t];
+                    *reinterpret_cast<facc *>(to + t * 256) = out[t];
+                }
             }
         }
     }
-    *reinterpret_cast<facc *>(place(ns - 1)) = S;
+#pragma unroll
+    for (int t = 0; t < WT; ++t) *reinterpret_cast<facc *>(place(ns - 1) + t * 256) = S[t];
 }
 
 // ------------------------------------------------------------------ delta_local
@@ -1600,11 +1656,11 @@ int chunk_passes(const DeltaArgs &a)
     const bool wide = !GRAD && p.dvp > 64, slim = !GRAD && p.dvp <= 32;
     const int cols = wide ? 128 : 64, vb = (p.dvp + cols - 1) / cols, pb = (p.dvp + KD + cols - 1) / cols;
     const int nhk = static_cast<int>(std::max(1.0, std::min<double>(a.hk, kMostBytes / (static_cast<double>(each) * p.rep))));
-    // Measured: a join takes 5.7 us of d_k' = 128, 0.6 of 32, a step 5 and 3.3 us. Two
+    // Measured: a join takes 2 us of d_k' = 128, 0.3 of 32, a step 5 and 3.3 us. Two
     // workgroups fit a compute unit where the state is small (2 x 12 heads of 32 x 32,
     // 12544 tokens, bf16 forward and backward: 440 us planned with one, 355 with two).
-    plan_segments(p, seqs * p.rep * nhk, GRAD, vb, pb, KD <= 64 ? 512 : 256, KD == 128 ? 1.0 : (KD == 64 ? 0.4 : 0.2));
-    const size_t sa = static_cast<size_t>(p.nseg) * KD * KD * 4, ss = static_cast<size_t>(p.nseg) * KD * p.dvp * 4;
+    plan_segments(p, seqs * p.rep * nhk, GRAD, vb, pb, KD <= 64 ? 512 : 256, KD == 128 ? 0.4 : (KD == 64 ? 0.3 : 0.1));
+    const size_t sa = static_cast<size_t>(p.nseg) * KD * KD * 6, ss = static_cast<size_t>(p.nseg) * KD * p.dvp * 4;
     const size_t seg_each = p.nseg > 1 ? static_cast<size_t>(seqs) * kDirs * (sa + ss) : 0;
     const size_t sums = GRAD && p.rep > 1 ? n * 2 * kC * KD * 4 : 0;  // by key head
     void *ws = nullptr;
@@ -1631,8 +1687,8 @@ int chunk_passes(const DeltaArgs &a)
         }
         p.gates = reinterpret_cast<float *>(take(gates));
         if (p.nseg > 1) {
-            p.seg_at = reinterpret_cast<float *>(take(seqs * sa));
-            if (GRAD) p.seg_a = reinterpret_cast<float *>(take(seqs * sa));
+            p.seg_at = reinterpret_cast<word4 *>(take(seqs * sa));
+            if (GRAD) p.seg_a = reinterpret_cast<word4 *>(take(seqs * sa));
             p.seg_s = reinterpret_cast<float *>(take(seqs * ss));
             if (GRAD) p.seg_d = reinterpret_cast<float *>(take(seqs * ss));
         }
@@ -1669,7 +1725,7 @@ int chunk_passes(const DeltaArgs &a)
         };
         if (p.nseg > 1) {
             if ((rc = chains_of(std::true_type{})) != SSM2D_OK) return rc;
-            delta_join<T, KD, GRAD><<<dim3(chains, static_cast<unsigned>(p.dvp / 16), kDirs), dim3(KD * 4), 0, s>>>(p);
+            delta_join<T, KD, GRAD><<<dim3(chains, static_cast<unsigned>(p.dvp / 16), kDirs), dim3(KD == 32 ? 64 : KD * 4), 0, s>>>(p);
             if ((rc = launched()) != SSM2D_OK) return rc;
         }
         if ((rc = chains_of(std::false_type{})) != SSM2D_OK) return rc;
