@@ -10,6 +10,10 @@
 // sine are as exact at an angle of 2^20 as at 1; on [-pi/4, pi/4] they are
 // their Taylor polynomials (the first term left out is below 2^-36). Angles
 // beyond 2^20 go through fp64.
+// Measured: q and k of 32 maps of 56 x 56 with 6 heads of 32 each, bf16: 27 us,
+// 5.8 TB/s; 5 and 1 heads of 72 at 27918 positions, fp32, interleaved: 22 us, 4.4
+// TB/s (d of 18 16-byte pieces, so a wave's pieces cross heads).
+// A bf16 output is rounded once, from the fp32 turn.
 #include "ops_common.h"
 
 namespace ssm2d_impl {
@@ -188,8 +192,9 @@ int rope_entry(const T *q, const T *k, const int32_t *pos, const float *freq, T 
     for (int i = 0; i < 3; ++i) p.qs[i] = sh->q_stride[i], p.ks[i] = sh->k_stride[i];
     p.pos_axis = sh->pos_stride[0], p.pos_batch = sh->pos_stride[1];
     p.sign = (flags & SSM2D_ROPE_INVERSE) ? -1.0f : 1.0f;
-    // tokens a workgroup: about 64 KiB of reads and writes, within the table,
-    // fewer where that would leave compute units without one
+    // Tokens a workgroup: about 64 KiB of reads and writes (the maps above: 27 us, 31
+    // with 16 KiB, 29 with 256), within the table, fewer where that would leave
+    // compute units without one.
     const int64_t row = (sh->heads_q + sh->heads_k) * sh->d * static_cast<int64_t>(sizeof(T)) * 2;
     int64_t tok = std::max<int64_t>(1, 65536 / row);
     if (pairs > 0) tok = std::min<int64_t>(tok, kMaxTable / pairs);
@@ -201,7 +206,8 @@ int rope_entry(const T *q, const T *k, const int32_t *pos, const float *freq, T 
     const hipStream_t s = static_cast<hipStream_t>(stream);
     const bool inter = flags & SSM2D_ROPE_INTERLEAVED;
     // V elements at a time: pieces must not cross the halves of a head, and
-    // every row of both tensors must start at a multiple of V
+    // every row of both tensors must start at a multiple of V. (Element by element
+    // the same sizes reach half the bandwidth: bf16 heads of 50, 2.5 TB/s.)
     auto fits = [&](int v) {
         if (sh->d % v || (inter ? 2 * pairs : pairs) % v) return false;
         auto rows = [&](const T *in, const T *out, const int64_t (&st)[3]) {
