@@ -317,6 +317,14 @@ __device__ __forceinline__ auto lane_offset(int ty, int at, long stride)
     else return static_cast<unsigned>(ty) * static_cast<unsigned>(stride) + static_cast<unsigned>(at);
 }
 
+// The channels' weights or biases in LDS (a load each where they are used would
+// be waited for one by one); a barrier comes before their use.
+template <int THREADS>
+__device__ __forceinline__ void map_params(const float *src, int n, float missing, float *out)
+{
+    for (int i = threadIdx.x; i < n; i += THREADS) out[i] = src ? src[i] : missing;
+}
+
 // KEEP: the tile stays in registers (n <= TY * NCH); else it is read again for
 // each pass (from cache: a tile is TX * VEC * n elements) and dweight and
 // dbias are left to ln_map_sums.
@@ -328,6 +336,11 @@ __global__ __launch_bounds__(TX *TY) void ln_map_fwd(const T *x, const float *we
     __shared__ float buf[TX * TY / 64 * VEC * TX];
     const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
     const float inv_n = 1.0f / static_cast<float>(n);
+    __shared__ float ws[KEEP ? TY * NCH : 1], bs[KEEP ? TY * NCH : 1];
+    if constexpr (KEEP) {
+        map_params<TX * TY>(weight, n, 1.0f, ws);
+        map_params<TX * TY>(bias, n, 0.0f, bs);
+    }
     const int nc = KEEP ? NCH : (n + TY - 1) / TY;
     for (long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const long b = tile / tiles_b;
@@ -392,7 +405,7 @@ __global__ __launch_bounds__(TX *TY) void ln_map_fwd(const T *x, const float *we
             const int ch = c * TY + ty;
             const Raw<T, VEC> &r = get(c);
             if (ch >= n) continue;
-            const float w = weight ? weight[ch] : 1.0f, bi = bias ? bias[ch] : 0.0f;
+            const float w = KEEP ? ws[ch] : (weight ? weight[ch] : 1.0f), bi = KEEP ? bs[ch] : (bias ? bias[ch] : 0.0f);
             float o[VEC];
 #pragma unroll
             for (int j = 0; j < VEC; ++j) o[j] = (r.get(j) - mu[j]) * q[j] * w + bi;
@@ -412,8 +425,11 @@ __global__ __launch_bounds__(TX *TY) void ln_map_bwd(const T *x, const float *we
     const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
     const float inv_n = 1.0f / static_cast<float>(n);
     const int nc = KEEP ? NCH : (n + TY - 1) / TY;
+    __shared__ float ws[KEEP ? TY * NCH : 1];
     float dw[KEEP ? NCH : 1], db[KEEP ? NCH : 1];
     if constexpr (KEEP) {
+        map_params<TX * TY>(weight, n, 1.0f, ws);
+        __syncthreads();
 #pragma unroll
         for (int c = 0; c < NCH; ++c) dw[c] = db[c] = 0.0f;
     }
@@ -439,17 +455,20 @@ __global__ __launch_bounds__(TX *TY) void ln_map_bwd(const T *x, const float *we
             for (int c = 0; c < NCH; ++c) fetch(c, c);
         }
         float mu[VEC], rs[VEC], a[VEC], cc[VEC];
+        const long stat = b * cells + (live ? cell : cell0);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-            mu[j] = live ? mean[b * cells + cell + j] : 0.0f;
-            rs[j] = live ? rstd[b * cells + cell + j] : 0.0f;
+            mu[j] = mean[stat + j];
+            rs[j] = rstd[stat + j];
             a[j] = cc[j] = 0.0f;
         }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) mu[j] = live ? mu[j] : 0.0f, rs[j] = live ? rs[j] : 0.0f;
 #pragma unroll(KEEP ? NCH : 1)
         for (int c = 0; c < nc; ++c) {
             const int k = KEEP ? c : 0, ch = c * TY + ty;
             if constexpr (!KEEP) fetch(c, 0);
-            const float w = (weight && ch < n) ? weight[ch] : 1.0f;
+            const float w = KEEP ? ws[min(ch, n - 1)] : (weight ? weight[min(ch, n - 1)] : 1.0f);
             float sw = 0.0f, sg = 0.0f;
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
@@ -474,7 +493,7 @@ __global__ __launch_bounds__(TX *TY) void ln_map_bwd(const T *x, const float *we
             const int k = KEEP ? c : 0, ch = c * TY + ty;
             if constexpr (!KEEP) fetch(c, 0);
             if (ch >= n) continue;
-            const float w = weight ? weight[ch] : 1.0f;
+            const float w = KEEP ? ws[ch] : (weight ? weight[ch] : 1.0f);
             float o[VEC];
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
@@ -587,11 +606,13 @@ int pick_row(int64_t n, F &&f)
 // and two sums a channel). The widest piece is taken with which nothing spills:
 //   * forward: 16 bytes up to 384 channels, 8 up to 1024, single cells or 4
 //     bytes where rows allow no more; beyond, the tile is read again each pass
-//     (bf16, 21 x 1536 x 448: 36 us, 1.6 TB/s; 4 x 1024 x 3136 kept: 17 us, 3.1).
+//     (bf16, 21 x 1536 x 448: 36 us, 1.6 TB/s; 4 x 1024 x 3136 kept: 15 us, 3.5).
 //   * backward: 16 bytes up to 64 channels of bf16 and 128 of fp32 (bf16,
 //     4 x 96 x 50176: 45 us with 8-byte pieces, 71 with 16; fp32: 58 and 50),
-//     8 up to 512; beyond, read again (bf16, 4 x 768 x 3136: 37 us; 53 with
-//     4-byte pieces kept by 1024 threads, which spill).
+//     8 up to 384 and 512, single cells up to 128 (4 x 96 x 50175, bf16: 61 us, and
+//     136 with 1024 threads of 128 registers, which spill); beyond, read again
+//     (bf16, 4 x 768 x 3136: 37 us; 53 with 4-byte pieces kept by 1024 threads;
+//     8 x 512 x 3136: 43 us).
 enum : int { kCells16 = 0, kCells8 = 1, kCells4 = 2, kCellsFew = 3 };
 
 template <int LEVEL, int VEC, bool BWD, typename F>
@@ -602,7 +623,10 @@ int pick_map(int64_t n, F &&f)
     f(integral_constant<int, TX>{}, integral_constant<int, TY>{}, integral_constant<int, NCH>{}, std::bool_constant<KEEP>{})
     if constexpr (LEVEL == kCellsFew) {
         if (n <= 64) return SSM2D_MAP(64, 4, 16, true);
-        if constexpr (!BWD || VEC == 1) {
+        if constexpr (BWD && VEC == 1) {
+            if (n <= 128) return SSM2D_MAP(64, 8, 16, true);
+        }
+        if constexpr (!BWD) {
             if (n <= 256) return SSM2D_MAP(64, 16, 16, true);
         }
         return SSM2D_MAP(64, 16, 16, false);
@@ -616,13 +640,13 @@ int pick_map(int64_t n, F &&f)
             return SSM2D_MAP(16, 32, 12, true);
         }
     } else if constexpr (LEVEL == kCells8) {
-        if (n > (BWD ? 512 : 1024)) return SSM2D_MAP(16, 64, 16, false);
+        if (n > (BWD ? (VEC == 2 ? 512 : 384) : 1024)) return SSM2D_MAP(16, 64, 16, false);
         if (n <= 128) return SSM2D_MAP(16, 16, 8, true);
         if (n <= 192) return SSM2D_MAP(16, 16, 12, true);
         if (n <= 256) return SSM2D_MAP(16, 32, 8, true);
         if (n <= 384) return SSM2D_MAP(16, 32, 12, true);
         if constexpr (BWD) {
-            return SSM2D_MAP(16, 32, 16, true);
+            return SSM2D_MAP(16, 32, VEC == 2 ? 16 : 12, true);
         } else {
             if (n <= 512) return SSM2D_MAP(16, 32, 16, true);
             if (n <= 768) return SSM2D_MAP(16, 64, 12, true);
@@ -636,8 +660,8 @@ int pick_map(int64_t n, F &&f)
 }
 
 // The piece for n channels; fits(v): v cells can be read at once everywhere.
-// Two cells of bf16 a lane spill for 65 to 256 channels of the backward (bf16,
-// 8 x 192 x 12546: 112 us, and 88 with one).
+// Two cells of bf16 a lane are kept for up to 64 channels of the backward (more
+// spill: 8 x 192 x 12546 took 112 us, and 88 with one cell).
 template <int V, bool BWD, typename P, typename F>
 int pick_cells(int64_t n, P &&fits, F &&go)
 {
@@ -646,7 +670,7 @@ int pick_cells(int64_t n, P &&fits, F &&go)
     if (fits(V / 2)) return go(integral_constant<int, V / 2>{}, integral_constant<int, kCells8>{});
     const bool middle = n > 256 && n <= 1024;
     if constexpr (V / 4 > 1) {
-        const bool few = BWD ? n <= 64 || n > 256 : !middle;
+        const bool few = BWD ? n <= 64 || n > 128 : !middle;
         if (few && fits(V / 4)) return go(integral_constant<int, V / 4>{}, integral_constant<int, kCellsFew>{});
         if constexpr (!BWD) {
             if (middle && fits(V / 4)) return go(integral_constant<int, V / 4>{}, integral_constant<int, kCells4>{});
