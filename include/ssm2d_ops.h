@@ -137,8 +137,11 @@ int ssm2d_rope_bf16(const uint16_t *q, const uint16_t *k, const int32_t *positio
  *
  * The forward and backward work on chunks of 64 tokens with matrix
  * instructions: products of fp32 operands split into three bf16 parts each, so
- * that nothing between inputs and outputs is held in fewer bits. A NaN or Inf
- * at a token therefore may reach the other tokens of its chunk. */
+ * that states and sums keep fp32's precision; what makes a bf16 o has two parts
+ * (2^-16 of the terms, before o's own rounding of 2^-9). A NaN or Inf at a token
+ * may reach the other tokens of its chunk, but no chunk before. Up to 8 tokens
+ * (bf16; 16 of float32) go through the recurrence itself.
+ * Heads of no keys or no values give zeros. */
 #define SSM2D_DELTA_MAX_DK 128
 #define SSM2D_DELTA_MAX_DV 1024
 
@@ -163,9 +166,12 @@ int ssm2d_gated_delta_fwd_bf16(const uint16_t *q, const uint16_t *k, const uint1
  * (NULL: not stored; like h_init, may be dh_last). The forward's chunk states
  * are computed again. Workspaces: per head and chunk of 64 tokens, with
  * d_k' = d_k rounded up to 32, 64 or 128 and d_v' = d_v to a multiple of 32,
- * 19712 + 4 (d_k' + 64) d_v' bytes for the forward and 38144 + 4 (2 d_k' +
- * 192) d_v' for the backward; heads are taken in passes that keep this within
- * 16 GiB where one key head's share allows. */
+ * 21760 bytes for the forward and 21760 + 4 (2 d_k' + 192) d_v' for the backward,
+ * and 512 d_k' per chunk and key head that several heads share (backward). Where
+ * few long sequences are cut into segments (at most one for every 4 chunks, 256
+ * in all), per head, sequence and segment d_k' (6 d_k' + 4 d_v') bytes, twice that
+ * for the backward. Heads are taken in passes that keep the chunks' share within
+ * 16 GiB where one key head's allows. */
 int ssm2d_gated_delta_bwd(const float *q, const float *k, const float *v, const float *g, const float *beta,
                           const float *h_init, const int32_t *cu_seqlens, const float *dout, const float *dh_last,
                           float *dq, float *dk, float *dv, float *dg, float *dbeta, float *dh_init,

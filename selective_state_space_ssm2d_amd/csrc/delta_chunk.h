@@ -19,17 +19,25 @@
 //   dG_i = q_i . dQ_i + k_i . Rk_i - k_i . Ck_i, and at the chunk's end
 //   also gamma_last <S0, D1> + sum_j k_j . (Gam_last U D1^T)_j;  dg = suffix sums of dG.
 //
-// Kernels: delta_prep (per chunk: the gates and M), delta_z (scale P^T dO),
-// delta_seq (the chain over chunks, S0 and E, and in the backward at the same
-// time the chain of adjoints, D1 and dR), delta_out (O) and delta_local (the
-// gradients of a chunk). Only delta_seq is sequential.
+// Kernels: delta_prep (per chunk: the gates, M and for the forward P), delta_z
+// (scale P^T dO), delta_seq (the chain over chunks: in the forward O as it goes,
+// in the backward S0 and E, and at the same time the chain of adjoints, D1 and
+// dR), delta_join (first states of the chains' segments) and delta_local (the
+// gradients of a chunk). Only delta_seq and delta_join are sequential.
+//
+// What bounds them is not memory (4 heads of 32 x 32 over 196608 tokens, fp32, have
+// 409 MB to move, 80 us, and take 436): a chunk's step is a chain of products of
+// one wave's 16 columns, each waiting for the one before, and cutting operands
+// into parts takes twice the issue cycles of the matrix instructions (SQ
+// counters: of delta_seq's wave cycles 25 to 43 % issue vector instructions, 14 to 21
+// matrix ones, 27 to 42 wait).
 //
 // Precision: an fp32 operand goes through the matrix cores as the sum of
 // three bf16 parts, cut off exactly (8 + 8 + 8 bits); products keep the six
 // terms down to 2^-24 of the largest, so every product is as exact as in fp32
 // at 6/16 of its matrix instructions' time. bf16 inputs are one part (three
-// terms against an fp32 operand). Only delta_out of a bf16 result uses two
-// parts (2^-16, against the 2^-9 of the result's own rounding).
+// terms against an fp32 operand). Only the products that make a bf16 output use
+// two parts of S, U and P (2^-16, against the 2^-9 of the result's own rounding).
 //
 // Fragments: v_mfma_f32_16x16x32_bf16 with lane l holding row (column) l % 16
 // and, of the 32 summed indices, 4 (l / 16) + j and 16 + 4 (l / 16) + j, j < 4.
@@ -452,7 +460,10 @@ __device__ __forceinline__ facc mfma4(float a, float b, facc c) { return __built
 // substitution, a column a lane, then the blocks below by
 // M21 = (I - M22 B2) N21 (I - B1 M11) for halves of 32 and of 64, in fp32 matrix
 // instructions (20 products of 16^3 a head: small beside the split products
-// elsewhere).
+// elsewhere). Bound by the substitution's 14 dependent steps and the barriers
+// between the phases, so by workgroups a compute unit. 12288 chunks and heads of d_k
+// 32, fp32: 138 us (172 with the rows below read all at once, in registers that
+// halve the workgroups); 2508 of d_k 128, bf16: 36 us.
 template <typename T, int KD, bool BWD>
 __global__ __launch_bounds__(256, KD == 128 && sizeof(T) == 4 ? 3 : 4) void delta_prep(ChunkParams p)
 {
@@ -671,7 +682,9 @@ __device__ __forceinline__ void put_p(const facc (&x)[4], int rt, const Tile<NPP
 }
 
 // Z = scale P^T dO of one chunk and head: workgroup (slot, head). Q and K give
-// their place to P and dO.
+// their place to P and dO. Its own kernel, since it needs no state: 3072 chunks
+// and heads of 64 x 64, bf16, take 31 us, bound by the latency of one chunk's
+// phases (58 % of its wave cycles wait).
 template <typename T, int KD>
 struct ZLds {
     static constexpr int NP = kParts<T>, VS = 32;
@@ -853,6 +866,13 @@ struct SeqStage {
 // transposed tiles (the parts of S and U are operands as they are, and a lane
 // gets four neighbours of a token's row); else S0 and E are kept for
 // delta_local.
+//
+// Measured: 8 heads of 128 x 128, bf16, 20034 packed tokens: probe 140 us, outputs
+// 107 us (443 us for the whole forward with 64 columns a workgroup, 283 with 128,
+// which read a chunk's K, Q and M once for 8 waves); 4 heads of 32 x 32, fp32, 196608
+// tokens: 111 and 187 us (290 with four waves, two of them idle). With 128 columns
+// the backward's chains took 147 and 130 us instead of 137 and 113 (2 x 4099
+// tokens, 8 heads of 128 x 128).
 template <typename T, int KD, bool BWD, bool PROBE, bool OUT, int THREADS>
 __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
 {
@@ -1224,8 +1244,8 @@ __global__ __launch_bounds__(THREADS, THREADS == 256 && KD <= 64 ? 2 : 1) void d
 // waits for is its own chain (the state's parts, products), so a wave has few
 // rows: 16, with the state's parts through LDS and one barrier a segment, or a
 // small state's 32, whose parts stay in registers. A comes as operands, split
-// by the probe. (With 64 columns a workgroup, all rows a wave and A through
-// LDS a step of 128 x 128 took 5.7 us.)
+// by the probe. A step takes 2 us of 128 x 128, 0.3 of 32 x 32; with 64 columns a
+// workgroup, all rows a wave and A through LDS 5.7 and 0.6.
 template <typename T, int KD, bool GRAD>
 __global__ __launch_bounds__(KD == 32 ? 64 : KD * 4, 1) void delta_join(ChunkParams p)
 {
@@ -1345,7 +1365,10 @@ struct LocalLds {
 // waves, half of the dims: the three d_k-wide sums of its tokens stay in
 // accumulators over all slices of 32 columns, the next slice's matrices are
 // read while this one's are multiplied. Four waves where that leaves two
-// workgroups a compute unit (d_k' <= 64): their phases overlap.
+// workgroups a compute unit (d_k' <= 64): their phases overlap. Bound by the
+// waits between its phases (43 % of wave cycles) and the splits (23 %): 3072
+// chunks and heads of 64 x 64, bf16: 107 us; 520 chunks and key heads of 128 x 128:
+// 65 us a turn.
 template <typename T, int KD, int WAVES>
 __global__ __launch_bounds__(WAVES * 64, WAVES == 4 ? 2 : 1) void delta_local(ChunkParams p)
 {
@@ -1652,7 +1675,7 @@ int chunk_passes(const DeltaArgs &a)
     const size_t each = gates + 2 * mm + (GRAD ? 2 * st + 3 * row : 0);
     constexpr int kDirs = GRAD ? 2 : 1;
     // columns a workgroup of the chains: 128 share what they read of a chunk,
-    // narrower states would leave waves idle
+    // narrower states would leave waves idle (both measured at seq_chain)
     const bool wide = !GRAD && p.dvp > 64, slim = !GRAD && p.dvp <= 32;
     const int cols = wide ? 128 : 64, vb = (p.dvp + cols - 1) / cols, pb = (p.dvp + KD + cols - 1) / cols;
     const int nhk = static_cast<int>(std::max(1.0, std::min<double>(a.hk, kMostBytes / (static_cast<double>(each) * p.rep))));

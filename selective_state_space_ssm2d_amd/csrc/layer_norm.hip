@@ -15,10 +15,11 @@
 //     sums of its channels in registers, writes one partial row a workgroup,
 //     and a second kernel adds the partial rows in a fixed order.
 // Only y and dx of bf16 tensors are rounded to fewer bits, once each.
-// Measured: forward of 32 x 192 x 56 x 56 maps, bf16: 17 us, 4.5 TB/s (a copy of
-// that size runs at 5.1); backward of 12544 rows of 768, bf16: 16 us and 3 us of
-// ln_fold, 3.1 TB/s together; of a 128 x 384 x 512 map, fp32: 72 and 4 us, 4.0
-// TB/s. One row of 768 takes 4.3 us, a launch.
+// Measured, inputs from memory (a large copy runs at 5.1 TB/s): forward of 32 x
+// 192 x 56 x 56 maps, bf16: 17 us, 4.6 TB/s; backward of 12544 rows of 768, bf16:
+// 18 us, 3.3 TB/s, 4 of them ln_fold; of a 128 x 384 x 512 map, fp32: 71 us, 4.3
+// TB/s. One row of 768 takes 2.2 us. What bounds the smaller ones is the start
+// and the end of a launch, then the fold.
 #include "ops_common.h"
 
 namespace ssm2d_impl {
@@ -577,9 +578,11 @@ unsigned even_blocks(int64_t work, int64_t most)
 unsigned blocks_for(int64_t work, int64_t most) { return static_cast<unsigned>(std::max<int64_t>(1, std::min(work, most))); }
 
 // The row kernels' variant: waves a row and pieces a lane, the fewest that
-// hold n channels with VEC channels a piece. (A wave a row needs no barrier: at
-// 768 channels of bf16 the backward runs at 3.1 TB/s; rows of single elements,
-// where they are not aligned, at a third of that.)
+// hold n channels with VEC channels a piece. A wave a row needs no barrier: the
+// backward of 12544 x 768 (bf16) takes 21 us with one, 32 with four. Four from
+// 2048 channels of bf16 on: 4096 x 4096 takes 36 us with four, 60 with one. Rows
+// that are not aligned are read by single elements (12544 x 767: 14 us forward and
+// 31 backward; 9.7 and 19 of 768).
 template <typename T, int VEC, typename F>
 int pick_row(int64_t n, F &&f)
 {

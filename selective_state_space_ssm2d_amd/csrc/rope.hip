@@ -11,8 +11,8 @@
 // their Taylor polynomials (the first term left out is below 2^-36). Angles
 // beyond 2^20 go through fp64.
 // Measured: q and k of 32 maps of 56 x 56 with 6 heads of 32 each, bf16: 27 us,
-// 5.8 TB/s; 5 and 1 heads of 72 at 27918 positions, fp32, interleaved: 22 us, 4.4
-// TB/s (d of 18 16-byte pieces, so a wave's pieces cross heads).
+// 32 from memory (4.8 TB/s); 5 heads and 1 of 72 at 27918 positions, fp32,
+// interleaved: 22 us, 4.4 TB/s.
 // A bf16 output is rounded once, from the fp32 turn.
 #include "ops_common.h"
 
