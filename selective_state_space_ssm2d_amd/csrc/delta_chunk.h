@@ -26,7 +26,7 @@
 // gradients of a chunk). Only delta_seq and delta_join are sequential.
 //
 // What bounds them is not memory (4 heads of 32 x 32 over 196608 tokens, fp32, have
-// 409 MB to move, 80 us, and take 436): a chunk's step is a chain of products of
+// 409 MB to move, 80 us, and take 430): a chunk's step is a chain of products of
 // one wave's 16 columns, each waiting for the one before, and cutting operands
 // into parts takes twice the issue cycles of the matrix instructions (SQ
 // counters: of delta_seq's wave cycles 25 to 43 % issue vector instructions, 14 to 21
@@ -411,16 +411,22 @@ struct Stage {
 // hardware's exponential, exact to a unit of the last place, takes powers of
 // two), so that differences of large sums stay exact. Below -1e4 a decay is 0 in any sum: held there,
 // so that -inf gives 0 and not inf - inf.
-__device__ __forceinline__ void make_gates(const ChunkParams &p, const Place &c, int head, float *out)
+// g and beta of the chunk's tokens, one a lane of the first wave (clamped reads;
+// tokens past the end count as g = beta = 0).
+struct GateIn {
+    float g, b;
+    __device__ __forceinline__ void load(const ChunkParams &p, const Place &c, int head)
+    {
+        const long t = c.t0 + min(static_cast<int>(threadIdx.x), c.len - 1);
+        g = p.g[c.b * p.gs[0] + t * p.gs[1] + head * p.gs[2]];
+        b = p.beta[c.b * p.bs[0] + t * p.bs[1] + head * p.bs[2]];
+    }
+};
+__device__ __forceinline__ void make_gates(const Place &c, const GateIn &in, float *out)
 {
     const int i = threadIdx.x;
     if (i >= kC) return;
-    float g = 0.0f, b = 0.0f;
-    if (i < c.len) {
-        g = p.g[c.b * p.gs[0] + (c.t0 + i) * p.gs[1] + head * p.gs[2]];
-        g = g < -1e4f ? -1e4f : g;
-        b = p.beta[c.b * p.bs[0] + (c.t0 + i) * p.bs[1] + head * p.bs[2]];
-    }
+    const float g = i < c.len ? (in.g < -1e4f ? -1e4f : in.g) : 0.0f, b = i < c.len ? in.b : 0.0f;
     double s = g * 1.4426950408889634;
 #pragma unroll
     for (int m = 1; m < 64; m *= 2) {
@@ -462,7 +468,7 @@ __device__ __forceinline__ facc mfma4(float a, float b, facc c) { return __built
 // instructions (20 products of 16^3 a head: small beside the split products
 // elsewhere). Bound by the substitution's 14 dependent steps and the barriers
 // between the phases, so by workgroups a compute unit. 12288 chunks and heads of d_k
-// 32, fp32: 138 us (172 with the rows below read all at once, in registers that
+// 32, fp32: 133 us (172 with the rows below read all at once, in registers that
 // halve the workgroups); 2508 of d_k 128, bf16: 36 us.
 template <typename T, int KD, bool BWD>
 __global__ __launch_bounds__(256, KD == 128 && sizeof(T) == 4 ? 3 : 4) void delta_prep(ChunkParams p)
@@ -481,11 +487,16 @@ __global__ __launch_bounds__(256, KD == 128 && sizeof(T) == 4 ? 3 : 4) void delt
     int g4 = l / 16, l16 = l % 16;
     const Tile<NP, kC, KD> kt{kbuf};
     facc kk[4], qk[4];  // K K^T: rows 16 wave + 4 g4 + r, columns 16 ct + l16; Q K^T transposed: rows 16 ct + .., columns 16 wave + ..
+    // (the gates' inputs are read first, and for the next head a head ahead: their
+    // sums over the chunk go on while the rows of q and k come)
+    GateIn gates;
+    gates.load(p, c, hk * p.rep);
     {
         Stage<T, KD, 256> sq, sk;
         bfrag fq[KD / 32][NP];
         if constexpr (!BWD) sq.load(static_cast<const T *>(p.q) + c.b * p.qs[0] + c.t0 * p.qs[1] + hk * p.qs[2], p.qs[1], c.len, p.dk_, p.vec_qk);
         sk.load(static_cast<const T *>(p.k) + c.b * p.ks[0] + c.t0 * p.ks[1] + hk * p.ks[2], p.ks[1], c.len, p.dk_, p.vec_qk);
+        make_gates(c, gates, gt);
         if constexpr (!BWD) {
             sq.put(kt);
             lds_barrier();
@@ -512,9 +523,12 @@ __global__ __launch_bounds__(256, KD == 128 && sizeof(T) == 4 ? 3 : 4) void delt
     for (int r = 0; r < p.rep; ++r) {
         const int hl = blockIdx.y * p.rep + r;  // head of this pass
         asm volatile("" : "+v"(g4), "+v"(l16));  // (else the addresses of the whole body are kept across heads, in 200 registers)
-        __syncthreads();
-        make_gates(p, c, hk * p.rep + r, gt);
-        __syncthreads();
+        lds_barrier();
+        if (r > 0) {
+            make_gates(c, gates, gt);
+            lds_barrier();
+        }
+        if (r + 1 < p.rep) gates.load(p, c, hk * p.rep + r + 1);
         const long at = slot * p.nh + hl;
         for (int i = threadIdx.x; i < kGates; i += 256) p.gates[at * kGates + i] = gt[i];
         if constexpr (!BWD) {  // P: token i = 16 wave + l16, four neighbouring j a lane, which is an operand's layout
@@ -714,10 +728,15 @@ __global__ __launch_bounds__(256) void delta_z(ChunkParams p)
     facc x[4];
     {
         Stage<T, KD, 256> a, b;
+        float gates[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) gates[i] = p.gates[(slot * p.nh + hl) * kGates + min(i * 256 + static_cast<int>(threadIdx.x), kGates - 1)];
         a.load(static_cast<const T *>(p.q) + c.b * p.qs[0] + c.t0 * p.qs[1] + hk * p.qs[2], p.qs[1], c.len, p.dk_, p.vec_qk);
         b.load(static_cast<const T *>(p.k) + c.b * p.ks[0] + c.t0 * p.ks[1] + hk * p.ks[2], p.ks[1], c.len, p.dk_, p.vec_qk);
         so.load(op, p.os[1], c.len, p.dv_, p.vec_do);
-        make_gates(p, c, head, gt);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (i * 256 + static_cast<int>(threadIdx.x) < kGates) gt[i * 256 + threadIdx.x] = gates[i];
         a.put(qt);
         b.put(kt);
         lds_barrier();
