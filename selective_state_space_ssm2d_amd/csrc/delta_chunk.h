@@ -468,7 +468,7 @@ __device__ __forceinline__ facc mfma4(float a, float b, facc c) { return __built
 // instructions (20 products of 16^3 a head: small beside the split products
 // elsewhere). Bound by the substitution's 14 dependent steps and the barriers
 // between the phases, so by workgroups a compute unit. 12288 chunks and heads of d_k
-// 32, fp32: 133 us (172 with the rows below read all at once, in registers that
+// 32, fp32: 130 us (172 with the rows below read all at once, in registers that
 // halve the workgroups); 2508 of d_k 128, bf16: 36 us.
 template <typename T, int KD, bool BWD>
 __global__ __launch_bounds__(256, KD == 128 && sizeof(T) == 4 ? 3 : 4) void delta_prep(ChunkParams p)
@@ -697,7 +697,7 @@ __device__ __forceinline__ void put_p(const facc (&x)[4], int rt, const Tile<NPP
 
 // Z = scale P^T dO of one chunk and head: workgroup (slot, head). Q and K give
 // their place to P and dO. Its own kernel, since it needs no state: 3072 chunks
-// and heads of 64 x 64, bf16, take 31 us, bound by the latency of one chunk's
+// and heads of 64 x 64, bf16, take 29 us, bound by the latency of one chunk's
 // phases (58 % of its wave cycles wait).
 template <typename T, int KD>
 struct ZLds {
@@ -886,10 +886,10 @@ struct SeqStage {
 // gets four neighbours of a token's row); else S0 and E are kept for
 // delta_local.
 //
-// Measured: 8 heads of 128 x 128, bf16, 20034 packed tokens: probe 140 us, outputs
+// Measured: 8 heads of 128 x 128, bf16, 20034 packed tokens: probe 139 us, outputs
 // 107 us (443 us for the whole forward with 64 columns a workgroup, 283 with 128,
 // which read a chunk's K, Q and M once for 8 waves); 4 heads of 32 x 32, fp32, 196608
-// tokens: 111 and 187 us (290 with four waves, two of them idle). With 128 columns
+// tokens: 107 and 181 us (290 with four waves, two of them idle). With 128 columns
 // the backward's chains took 147 and 130 us instead of 137 and 113 (2 x 4099
 // tokens, 8 heads of 128 x 128).
 template <typename T, int KD, bool BWD, bool PROBE, bool OUT, int THREADS>
@@ -1386,7 +1386,7 @@ struct LocalLds {
 // read while this one's are multiplied. Four waves where that leaves two
 // workgroups a compute unit (d_k' <= 64): their phases overlap. Bound by the
 // waits between its phases (43 % of wave cycles) and the splits (23 %): 3072
-// chunks and heads of 64 x 64, bf16: 107 us; 520 chunks and key heads of 128 x 128:
+// chunks and heads of 64 x 64, bf16: 104 us; 520 chunks and key heads of 128 x 128:
 // 65 us a turn.
 template <typename T, int KD, int WAVES>
 __global__ __launch_bounds__(WAVES * 64, WAVES == 4 ? 2 : 1) void delta_local(ChunkParams p)
