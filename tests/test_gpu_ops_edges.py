@@ -139,6 +139,52 @@ def test_delta_heads_of_no_dims(dk, dv, dtype):
     assert bool((o == 0).all())
 
 
+@pytest.fixture
+def large():
+    """Room for tens of GB, given back afterwards."""
+    free, _ = torch.cuda.mem_get_info()
+    if free < 100 << 30:
+        pytest.skip("needs 100 GB of free GPU memory")
+    yield
+    pkg.release_workspaces()
+    torch.cuda.empty_cache()
+
+
+def _some_heads(x, hk, rep):
+    """One key head's inputs and the heads that share it."""
+    q, k, v, g, beta = x
+    own = slice(hk * rep, (hk + 1) * rep)
+    return tuple(t.contiguous() for t in (q[:, :, hk:hk + 1], k[:, :, hk:hk + 1], v[:, :, own], g[:, :, own], beta[:, :, own])), own
+
+
+def test_delta_fwd_in_passes(large):
+    """Workspaces beyond 16 GiB: heads go in passes, each head as by itself (cut into other
+    segments, so with other roundings; two roundings of a bf16 output)."""
+    T = 65536
+    x = D.make(16, T, 64, 64, 32, 32, "bf16", 70)
+    o, last = pkg.gated_delta_fwd(*x, return_last_state=True)
+    for head in (0, 31, 63):
+        one, own = _some_heads(x, head, 1)
+        want, S = pkg.gated_delta_fwd(*one, return_last_state=True)
+        ref, top = want.double(), float(S.abs().amax())
+        D._close(o[:, :, own], ref, 2 * D._bar(T, 32, top, ref, "bf16"), f"head {head}")
+        D._close(last[:, own], S.double(), 2 * D._bar(T, 32, top, S.double(), "f32"), f"state {head}")
+
+
+def test_delta_bwd_in_passes(large):
+    T = 32768
+    x = D.make(4, T, 20, 40, 128, 128, "bf16", 71)
+    do = torch.randn(4, T, 40, 128, generator=D._gen(72), device="cuda").to(torch.bfloat16)
+    r = pkg.gated_delta_bwd(*x, do)
+    for hk in (0, 15, 16, 19):
+        one, own = _some_heads(x, hk, 2)
+        want = pkg.gated_delta_bwd(*one, do[:, :, own].contiguous())
+        for n, t in want.items():
+            got = r[n][:, :, hk:hk + 1] if n in ("dq", "dk") else r[n][:, :, own]
+            ref = t.double()
+            D._close(got, ref, 2 * D._bar(T, 128, ref.abs().amax(), ref, "bf16" if n in ("dq", "dk", "dv") else "f32", 32), f"{n} {hk}")
+
+
 # ------------------------------------------------------------------ streams
 
 def test_operators_on_other_streams():
