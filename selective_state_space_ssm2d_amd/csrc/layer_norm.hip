@@ -567,7 +567,11 @@ struct NormArgs {
 
 constexpr int64_t kFar = int64_t{1} << 26;
 inline bool near(int64_t stride) { return stride >= 0 && stride < kFar; }
-constexpr int kMaxParts = 512;  // partial rows of dweight and dbias (the workgroups of a backward launch)
+// Partial rows of dweight and dbias: the workgroups of a backward launch, two a
+// compute unit. Fewer leave the reads short (bf16, 8 x 192 x 12544: 42 us with 256,
+// 33 with 512, 34 with 1024), more make the fold longer (bf16 rows, 8192 x 2048: 25,
+// 26 and 31 us).
+constexpr int kMaxParts = 512;
 
 // Workgroups for `work` turns of a loop: at most `most`, all with as many turns (but the last).
 unsigned even_blocks(int64_t work, int64_t most)
@@ -703,6 +707,7 @@ int norm_fwd(const T *x, const float *weight, const float *bias, T *y, float *me
             return pick_row<T, VEC>(a.n, [&](auto nch, auto wpr) {
                 constexpr int NCH = decltype(nch)::value, WPR = decltype(wpr)::value;
                 constexpr int kRows = WPR >= 4 ? 1 : 4 / WPR;
+                // (enough to fill the chip; a workgroup reads the weights once for its rows)
                 const unsigned grid = blocks_for((a.batch + kRows - 1) / kRows, WPR == 16 ? 1024 : 4096);
                 ln_row_fwd<T, VEC, NCH, WPR><<<dim3(grid), dim3(WPR * 64 > 256 ? WPR * 64 : 256), 0, a.s>>>(
                     x, weight, bias, y, mean, rstd, a.batch, n, a.sb, eps);
@@ -758,6 +763,7 @@ int norm_bwd(const T *x, const float *weight, const float *mean, const float *rs
             return pick_row<T, VEC>(a.n, [&](auto nch, auto wpr) {
                 constexpr int NCH = decltype(nch)::value, WPR = decltype(wpr)::value;
                 constexpr int kRows = WPR >= 4 ? 1 : 4 / WPR;
+                // (of 16 waves one workgroup fits a compute unit)
                 const unsigned grid = even_blocks((a.batch + kRows - 1) / kRows, WPR == 16 ? 256 : kMaxParts);
                 int st = parts(grid);
                 if (st != SSM2D_OK) return st;
@@ -776,7 +782,7 @@ int norm_bwd(const T *x, const float *weight, const float *mean, const float *rs
             constexpr int TX = decltype(tx)::value, TY = decltype(ty)::value, NCH = decltype(nch)::value;
             constexpr bool KEEP = decltype(keep)::value;
             const int64_t tiles_b = (a.cells + TX * VEC - 1) / (TX * VEC), tiles = tiles_b * a.batch;
-            const unsigned grid = KEEP ? even_blocks(tiles, TX * TY > 256 ? 512 : kMaxParts) : blocks_for(tiles, 1 << 20);
+            const unsigned grid = KEEP ? even_blocks(tiles, kMaxParts) : blocks_for(tiles, 1 << 20);
             const unsigned slices = KEEP ? grid : blocks_for((a.batch * a.cells + 2047) / 2048, 64);
             int st = parts(slices);
             if (st != SSM2D_OK) return st;
