@@ -24,8 +24,6 @@ int get_aux_ws(int dev, void *stream, int slot, size_t bytes, void **out);
 // Scratch slots (0 .. 37 are the scan's).
 enum : int { kSlotNorm = 64, kSlotDelta = 65 };
 
-template <int N>
-using fvec = float __attribute__((ext_vector_type(N)));
 using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
 using f32x2 = float __attribute__((ext_vector_type(2)));
 

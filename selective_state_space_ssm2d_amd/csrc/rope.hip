@@ -27,7 +27,7 @@ struct RopeParams {
     const float *freq;
     void *qo, *ko;
     long batch, tokens;
-    int hq, hk, d, pairs, sec_end[SSM2D_ROPE_MAX_AXES], n_axes;
+    int hq, hk, d, pairs, sec_end[SSM2D_ROPE_MAX_AXES];
     long qs[3], ks[3], pos_axis, pos_batch;
     float sign;
     int tok;  // tokens a workgroup
@@ -188,7 +188,7 @@ int rope_entry(const T *q, const T *k, const int32_t *pos, const float *freq, T 
     p.q = q, p.k = k, p.pos = pos, p.freq = freq, p.qo = qo, p.ko = ko;
     p.batch = sh->batch, p.tokens = sh->tokens;
     p.hq = static_cast<int>(sh->heads_q), p.hk = static_cast<int>(sh->heads_k), p.d = static_cast<int>(sh->d);
-    p.pairs = static_cast<int>(pairs), p.n_axes = static_cast<int>(sh->n_axes);
+    p.pairs = static_cast<int>(pairs);
     for (int i = 0; i < 3; ++i) p.qs[i] = sh->q_stride[i], p.ks[i] = sh->k_stride[i];
     p.pos_axis = sh->pos_stride[0], p.pos_batch = sh->pos_stride[1];
     p.sign = (flags & SSM2D_ROPE_INVERSE) ? -1.0f : 1.0f;
