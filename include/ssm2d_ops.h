@@ -137,9 +137,9 @@ int ssm2d_rope_bf16(const uint16_t *q, const uint16_t *k, const int32_t *positio
  *
  * The forward and backward work on chunks of 64 tokens with matrix
  * instructions: products of fp32 operands split into three bf16 parts each, so
- * that states and sums keep fp32's precision; what makes a bf16 o has two parts
- * (2^-16 of the terms, before o's own rounding of 2^-9). A NaN or Inf at a token
- * may reach the other tokens of its chunk, but no chunk before. Up to 8 tokens
+ * that states and sums keep fp32's precision, those that make a bf16 output
+ * too. A NaN or Inf at a token may reach the other tokens of its chunk, but no
+ * chunk before. Up to 8 tokens
  * (bf16; 16 of float32) go through the recurrence itself.
  * Heads of no keys or no values give zeros. */
 #define SSM2D_DELTA_MAX_DK 128

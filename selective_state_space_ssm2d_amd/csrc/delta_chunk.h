@@ -36,8 +36,7 @@
 // three bf16 parts, cut off exactly (8 + 8 + 8 bits); products keep the six
 // terms down to 2^-24 of the largest, so every product is as exact as in fp32
 // at 6/16 of its matrix instructions' time. bf16 inputs are one part (three
-// terms against an fp32 operand). Only the products that make a bf16 output use
-// two parts of S, U and P (2^-16, against the 2^-9 of the result's own rounding).
+// terms against an fp32 operand). Outputs are rounded once, from sums like these.
 //
 // Fragments: v_mfma_f32_16x16x32_bf16 with lane l holding row (column) l % 16
 // and, of the 32 summed indices, 4 (l / 16) + j and 16 + 4 (l / 16) + j, j < 4.
@@ -776,10 +775,10 @@ __global__ __launch_bounds__(256) void delta_z(ChunkParams p)
 // inputs, the columns of v (dO).
 template <typename T, int KD, bool BWD, bool OUT, int THREADS>
 struct SeqBuf {
-    static constexpr int kCols = THREADS / 4, NPO = sizeof(T) == 2 ? 2 : 3;
+    static constexpr int kCols = THREADS / 4;
     static constexpr bool kStaged = sizeof(T) == 2, kQ = BWD || OUT;
     static constexpr int kTile = Tile<kParts<T>, kC, KD>::kBytes;
-    static constexpr int kTri = kTriFrags * 1024 * 3, kTriP = OUT ? kTriFrags * 1024 * NPO : 0;
+    static constexpr int kTri = kTriFrags * 1024 * 3, kTriP = OUT ? kTri : 0;
     static constexpr int kOne = (kQ ? 2 : 1) * kTile + kTri + kTriP + 3 * kC * 4;
     static constexpr int kV = kStaged ? Tile<1, kC, kCols>::kBytes : 0;
     // two buffers where that costs no second workgroup a compute unit: a large
@@ -818,15 +817,14 @@ struct SeqStage {
         if constexpr (Buf::kStaged) v.load(base, stride, len, n, vec);
     }
     // a tile's four values into their fragment's parts
-    template <int NP>
     static __device__ __forceinline__ void put_tile(uint16_t *area, int frag, int half, const facc &x)
     {
         const int l = threadIdx.x % 64;
-        unsigned a[NP], b[NP];
-        split2<NP>(x[0], x[1], a);
-        split2<NP>(x[2], x[3], b);
+        unsigned a[3], b[3];
+        split2<3>(x[0], x[1], a);
+        split2<3>(x[2], x[3], b);
 #pragma unroll
-        for (int n = 0; n < NP; ++n) *reinterpret_cast<uint2 *>(area + ((frag * NP + n) * 64 + l) * 8 + half * 4) = make_uint2(a[n], b[n]);
+        for (int n = 0; n < 3; ++n) *reinterpret_cast<uint2 *>(area + ((frag * 3 + n) * 64 + l) * 8 + half * 4) = make_uint2(a[n], b[n]);
     }
     __device__ __forceinline__ void put(uint16_t *one, uint16_t *vbuf) const
     {
@@ -841,9 +839,8 @@ struct SeqStage {
             const int t = i * kWaves + wave;
             if (t >= kTiles) break;
             const int u = t < kTriTiles ? t : t - kTriTiles, a = tri_row(u), b = u - tri_tile(a, 0);
-            if (BWD) put_tile<3>(mm, mt_frag(b, a / 2), a % 2, m[i]);
-            else if (!OUT || t < kTriTiles) put_tile<3>(mm, m_frag(a, b / 2), b % 2, m[i]);
-            else put_tile<Buf::NPO>(pp, m_frag(a, b / 2), b % 2, m[i]);
+            if (BWD) put_tile(mm, mt_frag(b, a / 2), a % 2, m[i]);
+            else put_tile(OUT && t >= kTriTiles ? pp : mm, m_frag(a, b / 2), b % 2, m[i]);
         }
         float *gates = reinterpret_cast<float *>(pp + Buf::kTriP / 2);
 #pragma unroll
@@ -857,14 +854,14 @@ struct SeqStage {
         const facc zero = {0, 0, 0, 0};
         if (threadIdx.x >= 64) return;
         if constexpr (BWD) {
-            put_tile<3>(mm, mt_frag(1, 0), 0, zero);
-            put_tile<3>(mm, mt_frag(3, 1), 0, zero);
+            put_tile(mm, mt_frag(1, 0), 0, zero);
+            put_tile(mm, mt_frag(3, 1), 0, zero);
         } else {
-            put_tile<3>(mm, m_frag(0, 0), 1, zero);
-            put_tile<3>(mm, m_frag(2, 1), 1, zero);
+            put_tile(mm, m_frag(0, 0), 1, zero);
+            put_tile(mm, m_frag(2, 1), 1, zero);
             if constexpr (OUT) {
-                put_tile<Buf::NPO>(pp, m_frag(0, 0), 1, zero);
-                put_tile<Buf::NPO>(pp, m_frag(2, 1), 1, zero);
+                put_tile(pp, m_frag(0, 0), 1, zero);
+                put_tile(pp, m_frag(2, 1), 1, zero);
             }
         }
     }
@@ -897,7 +894,6 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
 {
     constexpr int NP = kParts<T>, NT = KD / 16;
     using Buf = SeqBuf<T, KD, BWD, OUT, THREADS>;
-    constexpr int NPO = Buf::NPO;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64, g4 = l / 16, l16 = l % 16;
     const long s = blockIdx.x / p.nh;
     const int hl = static_cast<int>(blockIdx.x - s * p.nh), head = p.hk0 * p.rep + hl, hk = head / p.rep;
@@ -1051,12 +1047,9 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
                 split_acc<3>(S[2 * ks], S[2 * ks + 1], b);
                 mma_each<NP, 3, 4>(Y, a, b);
                 if constexpr (OUT) {
-                    bfrag bo[NPO];
-#pragma unroll
-                    for (int n3 = 0; n3 < NPO; ++n3) bo[n3] = b[n3];
 #pragma unroll
                     for (int t = 0; t < 4; ++t) qt.rows(16 * t, 32 * ks, a[t]);
-                    mma_each_t<NP, NPO, 4>(O, a, bo);
+                    mma_each_t<NP, 3, 4>(O, a, b);
                 }
             }
             // (gamma, Gam_last and beta of the lane's tokens come from LDS at each use: kept, they take 48 registers)
@@ -1100,19 +1093,19 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
                 }
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
-                    bfrag b[NPO], a[4][NPO];
-                    split_acc<NPO>(W2[2 * ks], W2[2 * ks + 1], b);
+                    bfrag b[3], a[4][3];
+                    split_acc<3>(W2[2 * ks], W2[2 * ks + 1], b);
 #pragma unroll
                     for (int t = 0; t < 4; ++t)
                         if (ks <= t / 2)
 #pragma unroll
-                            for (int n3 = 0; n3 < NPO; ++n3) {
+                            for (int n3 = 0; n3 < 3; ++n3) {
                                 FragBits fb;
-                                fb.q = pp[(m_frag(t, ks) * NPO + n3) * 64 + l];
+                                fb.q = pp[(m_frag(t, ks) * 3 + n3) * 64 + l];
                                 a[t][n3] = fb.f;
                             }
 #pragma unroll
-                    for (int sum = NPO - 1; sum >= 0; --sum)
+                    for (int sum = 2; sum >= 0; --sum)
 #pragma unroll
                         for (int u = 0; u <= sum; ++u)
 #pragma unroll
