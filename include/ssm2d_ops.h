@@ -167,11 +167,12 @@ int ssm2d_gated_delta_fwd_bf16(const uint16_t *q, const uint16_t *k, const uint1
  * are computed again. Workspaces: per head and chunk of 64 tokens, with
  * d_k' = d_k rounded up to 32, 64 or 128 and d_v' = d_v to a multiple of 32,
  * 21760 bytes for the forward and 21760 + 4 (2 d_k' + 192) d_v' for the backward,
- * and 512 d_k' per chunk and key head that several heads share (backward). Where
- * few long sequences are cut into segments (at most one for every 4 chunks, 256
- * in all), per head, sequence and segment d_k' (6 d_k' + 4 d_v') bytes, twice that
- * for the backward. Heads are taken in passes that keep the chunks' share within
- * 16 GiB where one key head's allows. */
+ * and 512 d_k' per chunk and key head that several heads share (backward); packed
+ * sequences count as tokens / 64 + n_seq chunks. Where few or long sequences are
+ * cut into segments, per head and segment d_k' (6 d_k' + 4 d_v') bytes, twice that
+ * for the backward: at most one segment for every 4 chunks and 256 in all for a
+ * sequence, at most 512 for all of a packed batch. Heads are taken in passes that
+ * keep all of this within 16 GiB where one key head's allows. */
 int ssm2d_gated_delta_bwd(const float *q, const float *k, const float *v, const float *g, const float *beta,
                           const float *h_init, const int32_t *cu_seqlens, const float *dout, const float *dh_last,
                           float *dq, float *dk, float *dv, float *dg, float *dbeta, float *dh_init,

@@ -46,17 +46,15 @@
 #pragma once
 
 #include "delta.h"
+#include "delta_plan.h"
 
 namespace ssm2d_impl {
 
-constexpr int kC = 64;  // tokens a chunk
-
 using word4 = unsigned __attribute__((ext_vector_type(4)));  // (a register value; the uint4 struct is copied through memory)
 
-struct ChunkParams {
+struct ChunkParams : Cuts {
     const void *q, *k, *v, *dout;
     const float *g, *beta, *h_init, *dh_last;
-    const int *cu;
     void *o, *dq, *dk, *dv;
     float *h_last, *dg, *dbeta, *dh_init;
     // workspace, by [slot][head of this pass]
@@ -67,7 +65,7 @@ struct ChunkParams {
     // 16, of each the 64 lanes' four values: column lane % 16, rows 4 (lane / 16) + j)
     float *s0, *d1;                     // [KD][dvp]
     float *e, *dr, *z;                  // [kC][dvp]
-    // by [sequence][head of this pass][segment]: a segment's transition
+    // by [place of a segment][head of this pass]: a segment's transition
     // [KD][KD] (as operands of its columns, for adjoints, and of its rows, in three
     // parts), its state from zero and then its first state (forward and adjoint)
     // [KD][dvp]
@@ -75,8 +73,6 @@ struct ChunkParams {
     float *seg_s, *seg_d;
     float *sum;                         // dQ and dK of shared heads so far, by [slot][key head]
     int turn;                           // which of the heads that share a key head (delta_local)
-    int nseg, seg_len;                  // segments of the longest sequence, chunks a segment
-    long batch, tokens, n_seq, slots, chunks_b;  // chunks_b: chunks of a batch entry
     int hk, h, rep, dk_, dv_, dvp;
     int hk0, nhk, nh;                   // this pass: key heads hk0 .. hk0 + nhk - 1, nh = nhk * rep heads
     long qs[3], ks[3], vs[3], os[3], gs[3], bs[3];
@@ -92,51 +88,6 @@ constexpr int kSegTile = KD / 32 * 3 * 64;
 using bfrag = __bf16 __attribute__((ext_vector_type(8)));
 using facc = float __attribute__((ext_vector_type(4)));
 using half4 = short __attribute__((ext_vector_type(4)));
-
-// Where a chunk lies.
-struct Place {
-    long b;   // batch entry (addresses)
-    long t0;  // its first token there
-    int len;  // tokens, 1 .. kC (0: no such chunk)
-};
-
-struct Seq {
-    long b, t0, len, slot0;  // slot0: the slot of its first chunk
-};
-
-__device__ __forceinline__ long packed_at(const ChunkParams &p, long s)
-{
-    const long c = p.cu[s];
-    return c < 0 ? 0 : (c > p.tokens ? p.tokens : c);
-}
-
-// Sequence s. Packed sequences' chunks get slots from cu / 64 + s on: at
-// least as many as they need before the next sequence's, without a table.
-__device__ __forceinline__ Seq find_seq(const ChunkParams &p, long s)
-{
-    if (p.n_seq == 0) return {s, 0, p.tokens, s * p.chunks_b};
-    const long a = packed_at(p, s), e = packed_at(p, s + 1);
-    return {0, a, e > a ? e - a : 0, a / kC + s};
-}
-
-__device__ __forceinline__ Place find_chunk(const ChunkParams &p, long slot)
-{
-    Seq q;
-    if (p.n_seq == 0) {
-        q = find_seq(p, slot / p.chunks_b);
-    } else {
-        long lo = 0, hi = p.n_seq - 1;  // the last sequence whose slots start at or before this one
-        while (lo < hi) {
-            const long mid = (lo + hi + 1) / 2;
-            if (packed_at(p, mid) / kC + mid <= slot) lo = mid;
-            else hi = mid - 1;
-        }
-        q = find_seq(p, lo);
-    }
-    const long at = (slot - q.slot0) * kC;
-    if (at < 0 || at >= q.len) return {0, 0, 0};
-    return {q.b, q.t0 + at, static_cast<int>(q.len - at < kC ? q.len - at : kC)};
-}
 
 // ------------------------------------------------------------------ parts
 
@@ -445,10 +396,6 @@ __device__ __forceinline__ float gam(const float *gt, int i, int j)
     return __builtin_amdgcn_exp2f((gt[3 * kC + i] - gt[3 * kC + j]) + (gt[4 * kC + i] - gt[4 * kC + j]));
 }
 
-constexpr int kGates = 5 * kC;
-// The triangular matrices of a chunk are kept as 10 tiles of 16 x 16, tile
-// (a, b), a >= b, at a (a + 1) / 2 + b, and multiplied as 6 fragments of 16 x 32.
-constexpr int kTriTiles = 10, kTriFloats = kTriTiles * 256, kTriFrags = 6;
 __device__ __forceinline__ int tri_row(int tile) { return tile < 1 ? 0 : (tile < 3 ? 1 : (tile < 6 ? 2 : 3)); }
 __host__ __device__ constexpr int tri_tile(int a, int b) { return a * (a + 1) / 2 + b; }
 // fragment of M (P) for rows 16 rt .., columns 32 ks .. (ks <= rt / 2)
@@ -895,14 +842,13 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
     constexpr int NP = kParts<T>, NT = KD / 16;
     using Buf = SeqBuf<T, KD, BWD, OUT, THREADS>;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64, g4 = l / 16, l16 = l % 16;
-    const long s = blockIdx.x / p.nh;
-    const int hl = static_cast<int>(blockIdx.x - s * p.nh), head = p.hk0 * p.rep + hl, hk = head / p.rep;
-    const int seg = blockIdx.z % p.nseg;
-    const Seq q = find_seq(p, s);
-    const long n_all = (q.len + kC - 1) / kC;
-    const int ns = n_all > 0 ? static_cast<int>((n_all + p.seg_len - 1) / p.seg_len) : 1;  // of this sequence
-    if (seg >= ns || (PROBE && ns == 1)) return;
-    const long c0 = static_cast<long>(seg) * p.seg_len, c1 = min(n_all, c0 + p.seg_len), n = c1 - c0;
+    const long x = blockIdx.x / p.nh;
+    const int hl = static_cast<int>(blockIdx.x - x * p.nh), head = p.hk0 * p.rep + hl, hk = head / p.rep;
+    const Segment sg = find_segment<PROBE>(p, x);
+    if (sg.of == 0) return;
+    const Seq q = sg.q;
+    const long s = sg.s, n_all = (q.len + kC - 1) / kC;
+    const long c0 = static_cast<long>(sg.at) * p.seg_len, c1 = min(n_all, c0 + p.seg_len), n = c1 - c0;
     int v0 = blockIdx.y * (THREADS / 4) + wave * 16;
     const bool unit = PROBE && !BWD && v0 >= p.dvp;  // this wave's columns are the unit matrix's
     if (unit) v0 -= p.dvp;
@@ -913,12 +859,12 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
     const int colv = min(col, p.dv_ - 1);  // (where lanes without a column read)
     const long state = ((s * p.h + head) * p.dk_) * p.dv_;
     const float *init = BWD ? p.dh_last : p.h_init;
-    const long segs = (static_cast<long>(blockIdx.x) * p.nseg + seg) * KD;
-    float *joined = (BWD ? p.seg_d : p.seg_s) + segs * p.dvp + v0 * KD + l * 4;
+    const long place = sg.place * p.nh + hl;
+    float *joined = (BWD ? p.seg_d : p.seg_s) + place * KD * p.dvp + v0 * KD + l * 4;
     facc S[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        if (!PROBE && p.nseg > 1) {
+        if (!PROBE && sg.of > 1) {
             S[t] = act ? *reinterpret_cast<const facc *>(joined + t * 256) : facc{0, 0, 0, 0};
             continue;
         }
@@ -1198,7 +1144,7 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
         if (unit) {
             // A for delta_join, in parts: its rows' operands (four columns of a row
             // a lane), and for the adjoint its columns'
-            const long at = segs / KD * (kSegTile<KD> * NT);
+            const long at = place * (kSegTile<KD> * NT);
             uint2 *rows = reinterpret_cast<uint2 *>(p.seg_at + at + v0 / 32 * 3 * 64 + 4 * g4 + l16 % 4 + 16 * (l16 / 4)) + v0 / 16 % 2;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
@@ -1224,7 +1170,7 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
         return;
     }
     float *out = BWD ? p.dh_init : p.h_last;
-    if (out && live && seg == (BWD ? 0 : ns - 1)) {
+    if (out && live && sg.at == (BWD ? 0 : sg.of - 1)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -1235,14 +1181,14 @@ __device__ __forceinline__ void seq_chain(const ChunkParams &p, uint16_t *lds)
     }
 }
 
-// Workgroups (sequence and head, 64 or 128 columns, segment); with GRAD those of the
-// upper half of blockIdx.z run the adjoints' chain, at the same time.
+// Workgroups (segment and head, 32, 64 or 128 columns); with GRAD those of blockIdx.z
+// = 1 run the adjoints' chain, at the same time.
 template <typename T, int KD, bool GRAD, bool PROBE, int THREADS>
 __global__ __launch_bounds__(THREADS, THREADS == 256 && KD <= 64 ? 2 : 1) void delta_seq(ChunkParams p)
 {
     extern __shared__ __align__(16) uint16_t lds[];
     if constexpr (GRAD) {
-        if (static_cast<int>(blockIdx.z) >= p.nseg) {
+        if (blockIdx.z == 1) {
             seq_chain<T, KD, true, PROBE, false, THREADS>(p, lds);
             return;
         }
@@ -1252,7 +1198,8 @@ __global__ __launch_bounds__(THREADS, THREADS == 256 && KD <= 64 ? 2 : 1) void d
 
 // First states of the segments: S over a sequence's segments, S <- A S + b
 // (adjoint: D <- A^T D + b from the last one), each stored in b's place.
-// Workgroup (sequence and head, 16 columns, forward or adjoint). What a step
+// Workgroup (sequence, or the place of its first segment, and head; 16 columns; forward
+// or adjoint). What a step
 // waits for is its own chain (the state's parts, products), so a wave has few
 // rows: 16, with the state's parts through LDS and one barrier a segment, or a
 // small state's 32, whose parts stay in registers. A comes as operands, split
@@ -1265,11 +1212,12 @@ __global__ __launch_bounds__(KD == 32 ? 64 : KD * 4, 1) void delta_join(ChunkPar
     __shared__ __align__(16) word4 parts[2][3][KS][64];  // [turn][part]: two tiles' parts, a lane's 16 bytes
     const bool bwd = GRAD && blockIdx.z == 1;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64, g4 = l / 16, l16 = l % 16;
-    const long s = blockIdx.x / p.nh;
-    const int hl = static_cast<int>(blockIdx.x - s * p.nh), head = p.hk0 * p.rep + hl;
-    const Seq q = find_seq(p, s);
-    const long n_all = (q.len + kC - 1) / kC;
-    const int ns = n_all > 0 ? static_cast<int>((n_all + p.seg_len - 1) / p.seg_len) : 1;
+    const long x = blockIdx.x / p.nh;
+    const int hl = static_cast<int>(blockIdx.x - x * p.nh), head = p.hk0 * p.rep + hl;
+    const Segment sg = find_joined(p, x);
+    if (sg.of == 0) return;
+    const long s = sg.s;
+    const int ns = sg.of;
     const int v0 = blockIdx.y * 16, col = v0 + l16;
     const float *init = bwd ? p.dh_last : p.h_init;
     const long state = ((s * p.h + head) * p.dk_) * p.dv_;
@@ -1286,7 +1234,7 @@ __global__ __launch_bounds__(KD == 32 ? 64 : KD * 4, 1) void delta_join(ChunkPar
     // them, so they come from memory, later than a step or two
     word4 a[DEPTH][WT][KS][3];
     facc b[DEPTH][WT];
-    auto seg = [&](int i) { return static_cast<long>(blockIdx.x) * p.nseg + (bwd ? ns - 1 - i : i); };
+    auto seg = [&](int i) { return (sg.place + (bwd ? ns - 1 - i : i)) * p.nh + hl; };
     auto place = [&](int i) { return (bwd ? p.seg_d : p.seg_s) + seg(i) * KD * p.dvp + v0 * KD + wave * WT * 256 + l * 4; };
     auto fetch = [&](int i, int at) __attribute__((always_inline)) {  // (past the end the last segment's, which are not used)
         i = min(i, ns - 1);
@@ -1300,7 +1248,7 @@ __global__ __launch_bounds__(KD == 32 ? 64 : KD * 4, 1) void delta_join(ChunkPar
             b[at][t] = *reinterpret_cast<const facc *>(place(i) + t * 256);
         }
     };
-    if (ns > 1) {
+    {
 #pragma unroll
         for (int u = 0; u < DEPTH; ++u) fetch(u, u);
         for (int i0 = 0; i0 + 1 < ns; i0 += DEPTH) {
@@ -1629,47 +1577,16 @@ int big_lds(F *kernel, int bytes)
     return e == hipSuccess ? SSM2D_OK : hip_fail(e);
 }
 
-// Segments of the chains. Whole, a chain of n chunks takes n steps, and the
-// `chains` * vb workgroups of all chains (twice that with the adjoints') may
-// leave compute units idle. In P segments: ceil(n / P) steps of the probes
-// (pb blocks of columns a chain), `join` of a step a segment to join them, and
-// ceil(n / P) steps again. The P with the fewest steps is taken, counting
-// rounds of `units` workgroups. Packed sequences' lengths are on the device:
-// there the counts are bounds (at most total / len + n_seq segments hold
-// tokens, at most total / len of one sequence), and a sequence no longer than
-// a segment is not cut.
-inline void plan_segments(ChunkParams &p, long chains, bool grad, int vb, int pb, long units, double join)
-{
-    const bool packed = p.n_seq > 0;
-    const long n = packed ? p.tokens / kC + 1 : p.chunks_b, dirs = grad ? 2 : 1;
-    const long heads = packed ? chains / p.n_seq : chains, extra = packed ? p.n_seq : 0;
-    auto rounds = [&](long workgroups) { return (workgroups + units - 1) / units; };
-    p.nseg = 1;
-    p.seg_len = static_cast<int>(n);
-    if (chains * vb * dirs >= 4 * units) return;
-    double best = static_cast<double>(n * rounds(chains * vb * dirs));
-    for (long k = 2; k <= std::min<long>(n / 4, 256); ++k) {
-        const long len = (n + k - 1) / k, segs = (k + extra) * heads;
-        const double steps = static_cast<double>(len * (rounds(segs * (pb + (grad ? vb : 0))) + rounds(segs * vb * dirs))) + join * static_cast<double>(k);
-        if (steps < best) best = steps, p.seg_len = static_cast<int>(len), p.nseg = static_cast<int>((n + len - 1) / len);
-    }
-}
-
-// Workspace of one pass at most (heads beyond it take another pass).
-constexpr double kMostBytes = 16.0 * (1u << 30);
-
 template <typename T, int KD, bool GRAD>
 int chunk_passes(const DeltaArgs &a)
 {
     ChunkParams p{};
     p.q = a.q, p.k = a.k, p.v = a.v, p.dout = a.dout, p.g = a.g, p.beta = a.beta, p.h_init = a.h_init, p.dh_last = a.dh_last, p.cu = a.cu;
     p.o = a.o, p.dq = a.dq, p.dk = a.dk, p.dv = a.dv, p.h_last = a.h_last, p.dg = a.dg, p.dbeta = a.dbeta, p.dh_init = a.dh_init;
-    p.batch = a.batch, p.tokens = a.tokens, p.n_seq = a.n_seq;
-    p.chunks_b = (a.tokens + kC - 1) / kC;
-    p.slots = a.n_seq > 0 ? a.tokens / kC + a.n_seq : a.batch * p.chunks_b;
+    p.batch = a.batch, p.tokens = a.tokens, p.n_seq = a.n_seq, p.chunks_b = (a.tokens + kC - 1) / kC;
     // (a lane's offset in a chunk's rows of v and dout is kept in 32 bits)
     if (a.tokens > 1 && (a.vs[1] < 0 || a.vs[1] >= (1 << 26) || (GRAD && (a.os[1] < 0 || a.os[1] >= (1 << 26))))) return SSM2D_ERR_UNSUPPORTED;
-    if (p.slots >= (1 << 22)) return SSM2D_ERR_UNSUPPORTED;  // (grids; far beyond memory but for tiny heads)
+    if (chunk_slots(p) >= (1 << 22)) return SSM2D_ERR_UNSUPPORTED;  // (grids; far beyond memory but for tiny heads)
     p.hk = a.hk, p.h = a.h, p.rep = a.h / a.hk, p.dk_ = a.dk_, p.dv_ = a.dv_, p.dvp = (a.dv_ + 31) / 32 * 32;
     for (int i = 0; i < 3; ++i) {
         p.qs[i] = a.qs[i], p.ks[i] = a.ks[i], p.vs[i] = a.vs[i], p.os[i] = a.os[i], p.gs[i] = a.gs[i], p.bs[i] = a.bs[i];
@@ -1680,30 +1597,24 @@ int chunk_passes(const DeltaArgs &a)
     p.vec_v = rows_aligned<T>(a.v, a.vs, a.dv_);
     p.vec_o = !GRAD && a.dv_ % 4 == 0 && !off_by(a.o, 4 * sizeof(T));
     p.vec_dqk = GRAD && a.dk_ % 4 == 0 && !off_by(a.dq, 4 * sizeof(T)) && !off_by(a.dk, 4 * sizeof(T));
-    const long seqs = a.n_seq > 0 ? a.n_seq : a.batch;
-    // bytes of one head's chunks, in the order they are laid out
-    const size_t n = static_cast<size_t>(p.slots);
-    const size_t gates = n * kGates * 4, mm = n * kTriFloats * 4, st = n * KD * p.dvp * 4, row = n * kC * p.dvp * 4;
-    const size_t each = gates + 2 * mm + (GRAD ? 2 * st + 3 * row : 0);
     constexpr int kDirs = GRAD ? 2 : 1;
     // columns a workgroup of the chains: 128 share what they read of a chunk,
     // narrower states would leave waves idle (both measured at seq_chain)
     const bool wide = !GRAD && p.dvp > 64, slim = !GRAD && p.dvp <= 32;
     const int cols = wide ? 128 : 64, vb = (p.dvp + cols - 1) / cols, pb = (p.dvp + KD + cols - 1) / cols;
-    const int nhk = static_cast<int>(std::max(1.0, std::min<double>(a.hk, kMostBytes / (static_cast<double>(each) * p.rep))));
     // Measured: a join takes 2 us of d_k' = 128, 0.3 of 32, a step 5 and 3.3 us. Two
     // workgroups fit a compute unit where the state is small (2 x 12 heads of 32 x 32,
     // 12544 tokens, bf16 forward and backward: 440 us planned with one, 355 with two).
-    plan_segments(p, seqs * p.rep * nhk, GRAD, vb, pb, KD <= 64 ? 512 : 256, KD == 128 ? 0.4 : (KD == 64 ? 0.3 : 0.1));
-    const size_t sa = static_cast<size_t>(p.nseg) * KD * KD * 6, ss = static_cast<size_t>(p.nseg) * KD * p.dvp * 4;
-    const size_t seg_each = p.nseg > 1 ? static_cast<size_t>(seqs) * kDirs * (sa + ss) : 0;
-    const size_t sums = GRAD && p.rep > 1 ? n * 2 * kC * KD * 4 : 0;  // by key head
+    const Extent x{a.batch, a.tokens, a.n_seq, a.hk, p.rep, KD, p.dvp, cols, GRAD, KD <= 64 ? 512 : 256, KD == 128 ? 0.4 : (KD == 64 ? 0.3 : 0.1)};
+    const Passes plan = plan_passes(x);
+    const Share &share = plan.share;
+    p.nseg = plan.cuts.nseg, p.seg_len = plan.cuts.seg_len;
     void *ws = nullptr;
-    int rc = get_aux_ws(a.dev, a.stream, kSlotDelta, ((each + seg_each) * p.rep + sums) * nhk, &ws);
+    int rc = get_aux_ws(a.dev, a.stream, kSlotDelta, plan.bytes(x), &ws);
     if (rc != SSM2D_OK) return rc;
     const hipStream_t s = static_cast<hipStream_t>(a.stream);
-    for (p.hk0 = 0; p.hk0 < a.hk; p.hk0 += nhk) {
-        p.nhk = std::min(nhk, a.hk - p.hk0);
+    for (p.hk0 = 0; p.hk0 < a.hk; p.hk0 += plan.nhk) {
+        p.nhk = std::min(plan.nhk, a.hk - p.hk0);
         p.nh = p.nhk * p.rep;
         unsigned char *w = static_cast<unsigned char *>(ws);
         auto take = [&](size_t bytes) {
@@ -1711,24 +1622,24 @@ int chunk_passes(const DeltaArgs &a)
             w += bytes * p.nh;
             return at;
         };
-        p.m = reinterpret_cast<float *>(take(mm));
-        (GRAD ? p.mt : p.pm) = reinterpret_cast<float *>(take(mm));
+        p.m = reinterpret_cast<float *>(take(share.tri));
+        (GRAD ? p.mt : p.pm) = reinterpret_cast<float *>(take(share.tri));
         if (GRAD) {
-            p.s0 = reinterpret_cast<float *>(take(st));
-            p.e = reinterpret_cast<float *>(take(row));
-            p.d1 = reinterpret_cast<float *>(take(st));
-            p.dr = reinterpret_cast<float *>(take(row));
-            p.z = reinterpret_cast<float *>(take(row));
+            p.s0 = reinterpret_cast<float *>(take(share.state));
+            p.e = reinterpret_cast<float *>(take(share.row));
+            p.d1 = reinterpret_cast<float *>(take(share.state));
+            p.dr = reinterpret_cast<float *>(take(share.row));
+            p.z = reinterpret_cast<float *>(take(share.row));
         }
-        p.gates = reinterpret_cast<float *>(take(gates));
+        p.gates = reinterpret_cast<float *>(take(share.gates));
         if (p.nseg > 1) {
-            p.seg_at = reinterpret_cast<word4 *>(take(seqs * sa));
-            if (GRAD) p.seg_a = reinterpret_cast<word4 *>(take(seqs * sa));
-            p.seg_s = reinterpret_cast<float *>(take(seqs * ss));
-            if (GRAD) p.seg_d = reinterpret_cast<float *>(take(seqs * ss));
+            p.seg_at = reinterpret_cast<word4 *>(take(share.seg_a));
+            if (GRAD) p.seg_a = reinterpret_cast<word4 *>(take(share.seg_a));
+            p.seg_s = reinterpret_cast<float *>(take(share.seg_s));
+            if (GRAD) p.seg_d = reinterpret_cast<float *>(take(share.seg_s));
         }
         p.sum = reinterpret_cast<float *>(w);
-        const unsigned slots = static_cast<unsigned>(p.slots), nk = static_cast<unsigned>(p.nhk), nh = static_cast<unsigned>(p.nh);
+        const unsigned slots = static_cast<unsigned>(chunk_slots(p)), nk = static_cast<unsigned>(p.nhk), nh = static_cast<unsigned>(p.nh);
         delta_prep<T, KD, GRAD><<<dim3(slots, nk), dim3(256), 0, s>>>(p);
         if ((rc = launched()) != SSM2D_OK) return rc;
         if constexpr (GRAD) {
@@ -1737,7 +1648,6 @@ int chunk_passes(const DeltaArgs &a)
             delta_z<T, KD><<<dim3(slots, nh), dim3(256), kZ, s>>>(p);
             if ((rc = launched()) != SSM2D_OK) return rc;
         }
-        const unsigned chains = static_cast<unsigned>(seqs * p.nh);
         auto run_chains = [&](auto probe, auto threads) -> int {
             constexpr bool PROBE = decltype(probe)::value;
             constexpr int THREADS = decltype(threads)::value;
@@ -1745,8 +1655,8 @@ int chunk_passes(const DeltaArgs &a)
             constexpr int kSeq = GRAD && kB > kF ? kB : kF;
             const int st2 = big_lds(delta_seq<T, KD, GRAD, PROBE, THREADS>, kSeq);
             if (st2 != SSM2D_OK) return st2;
-            delta_seq<T, KD, GRAD, PROBE, THREADS>
-                <<<dim3(chains, static_cast<unsigned>(PROBE ? pb : vb), kDirs * p.nseg), dim3(THREADS), kSeq, s>>>(p);
+            const unsigned groups = static_cast<unsigned>((PROBE ? seg_places(p) : seg_count(p)) * p.nh);
+            delta_seq<T, KD, GRAD, PROBE, THREADS><<<dim3(groups, static_cast<unsigned>(PROBE ? pb : vb), kDirs), dim3(THREADS), kSeq, s>>>(p);
             return launched();
         };
         auto chains_of = [&](auto probe) -> int {
@@ -1760,7 +1670,8 @@ int chunk_passes(const DeltaArgs &a)
         };
         if (p.nseg > 1) {
             if ((rc = chains_of(std::true_type{})) != SSM2D_OK) return rc;
-            delta_join<T, KD, GRAD><<<dim3(chains, static_cast<unsigned>(p.dvp / 16), kDirs), dim3(KD == 32 ? 64 : KD * 4), 0, s>>>(p);
+            const unsigned joins = static_cast<unsigned>(join_count(p) * p.nh);
+            delta_join<T, KD, GRAD><<<dim3(joins, static_cast<unsigned>(p.dvp / 16), kDirs), dim3(KD == 32 ? 64 : KD * 4), 0, s>>>(p);
             if ((rc = launched()) != SSM2D_OK) return rc;
         }
         if ((rc = chains_of(std::false_type{})) != SSM2D_OK) return rc;

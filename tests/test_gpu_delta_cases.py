@@ -50,3 +50,80 @@ def test_bf16_outputs_are_rounded_once(case):
     other = int((o != want).sum())
     print(f"{case}: {other} of {o.numel()} on the other side, {allowed:.0f} allowed")
     assert other <= allowed + 5 * math.sqrt(allowed), (other, allowed, o.numel())
+
+
+# ------------------------------------------------------------------ many packed sequences
+
+def _lens(kind):
+    g = torch.Generator().manual_seed(len(kind))
+    if kind == "short":  # a few hundred, some empty
+        return torch.randint(0, 131, (300,), generator=g).tolist()
+    if kind == "one long":  # among many short ones
+        return torch.randint(0, 40, (150,), generator=g).tolist() + [2300] + torch.randint(0, 40, (100,), generator=g).tolist()
+    return [196] * 64  # "equal"
+
+
+def _padded(x, lens):
+    """Packed tensors as a batch of the longest length; what is past a sequence's end is zero, which leaves a state as it is."""
+    out = []
+    for t in x:
+        p = torch.zeros(len(lens), max(lens), *t.shape[2:], dtype=t.dtype, device=t.device)
+        at = 0
+        for i, n in enumerate(lens):
+            p[i, :n] = t[0, at:at + n]
+            at += n
+        out.append(p)
+    return out
+
+
+def _unpadded(t, lens):
+    return torch.cat([t[i, :n] for i, n in enumerate(lens)])[None]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind,dk,dv", [("short", 32, 32), ("one long", 32, 40), ("one long", 128, 96), ("equal", 64, 64)])
+def test_many_packed_sequences(kind, dk, dv, dtype):
+    lens, hk, h = _lens(kind), 1, 2
+    x, cu, h0 = D._packed(lens, hk, h, dk, dv, dtype, 35)
+    pad, T = _padded(x, lens), max(lens)
+    ref, S, top = D.reference(*pad, dk ** -0.5, h0)
+    ref = _unpadded(ref, lens)
+    o, last = pkg.gated_delta_fwd(*x, h_init=h0, cu_seqlens=cu, return_last_state=True)
+    D._close(o, ref, D._bar(T, dk, top, ref, dtype), "o")
+    D._close(last, S, D._bar(T, dk, top, S, "f32"), "h_last")
+    # gradients: those of the batch, one sequence an entry, which other tests hold against 64 bits (both within the bar)
+    do = torch.randn(1, sum(lens), h, dv, generator=D._gen(36), device="cuda").to(DT[dtype])
+    dh = torch.randn(h0.shape, generator=D._gen(37), device="cuda")
+    r = pkg.gated_delta_bwd(*x, do, h_init=h0, dh_last=dh, cu_seqlens=cu)
+    e = pkg.gated_delta_bwd(*pad, _padded([do], lens)[0], h_init=h0, dh_last=dh)
+    terms = ((x[0].double() * r["dq"].double()).abs().sum(-1) + (x[1].double() * r["dk"].double()).abs().sum(-1)).max() * (h // hk)
+    for n, t in e.items():
+        want = (t if n == "dh_init" else _unpadded(t, lens)).double()
+        size = float(want.abs().max())
+        size = max(size, float(terms)) if n == "dg" else size
+        D._close(r[n], want, 2 * D._bar(T, dk + dv, size, want, dtype if n in ("dq", "dk", "dv") else "f32", 32), n)
+
+
+def _workspace(call):
+    """What a first call takes besides its outputs."""
+    torch.cuda.synchronize()
+    pkg.release_workspaces()
+    torch.cuda.empty_cache()
+    before = torch.cuda.mem_get_info()[0]
+    call()
+    torch.cuda.synchronize()
+    used = before - torch.cuda.mem_get_info()[0]
+    pkg.release_workspaces()
+    return used
+
+
+@pytest.mark.parametrize("n_seq,tokens,h,dk,dv", [(64, 512, 8, 128, 128), (1000, 66, 1, 128, 128), (64, 196, 12, 64, 64)])
+def test_packed_workspaces(n_seq, tokens, h, dk, dv):
+    """Many short sequences take what their tokens need (a chunk's 21760 bytes a head, one more chunk a sequence) and at
+    most 512 segments' transitions and states: below 1 GiB for each of these."""
+    x = D.make(1, n_seq * tokens, h, h, dk, dv, "bf16", 38)
+    cu = torch.arange(0, n_seq * tokens + 1, tokens, dtype=torch.int32, device="cuda")
+    o = torch.empty_like(x[2])
+    used = _workspace(lambda: pkg.gated_delta_fwd(*x, cu_seqlens=cu, o=o))
+    most = ((n_seq * tokens // 64 + n_seq) * 21760 + 512 * dk * (6 * dk + 4 * dv)) * h
+    assert used <= most + (64 << 20) and used < 1 << 30, (used, most)  # (an allocation is rounded up to whole MB)
