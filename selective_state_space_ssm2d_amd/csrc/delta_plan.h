@@ -67,12 +67,12 @@ __host__ __device__ inline Place find_chunk(const Cuts &p, long slot)
     return {q.b, q.t0 + at, static_cast<int>(q.len - at < kC ? q.len - at : kC)};
 }
 
-// Segments. Those of packed sequences get their numbers as chunks do, with W
-// tokens a segment: from cu / W + s on for the chains (a sequence of one
-// segment, or of no tokens, has one). Where a segment's transition and states
-// are kept (its place), only sequences of several have any, from 2 cu / W on: a
-// sequence of len > W tokens needs ceil(len / W) places, and 2 len / W or more lie
-// before the next one's.
+// Segments. Packed sequences' first ones are numbered as the sequences are; the
+// others, with W tokens a segment, from n_seq + offset / W on: of a sequence of len
+// tokens there are ceil(len / W) - 1 more, and len / W or more numbers before the next
+// one's. Where a segment's transition and states are kept (its place), only
+// sequences of several have any, from 2 offset / W on: a sequence of len > W tokens
+// needs ceil(len / W) places, and 2 len / W or more lie before the next one's.
 struct Segment {
     Seq q;
     long s;
@@ -85,18 +85,18 @@ __host__ __device__ inline long seg_places(const Cuts &p) { return p.n_seq > 0 ?
 __host__ __device__ inline long seg_count(const Cuts &p) { return p.n_seq > 0 ? p.tokens / seg_tokens(p) + p.n_seq : p.batch * p.nseg; }
 // (32-bit divisions: there are less than 2^22 chunks)
 __host__ __device__ inline long first_place(const Cuts &p, long s) { return 2 * static_cast<unsigned>(packed_at(p, s)) / seg_tokens(p); }
-__host__ __device__ inline long first_segment(const Cuts &p, long s) { return static_cast<unsigned>(packed_at(p, s)) / seg_tokens(p) + s; }
+__host__ __device__ inline long next_segment(const Cuts &p, long s) { return static_cast<unsigned>(packed_at(p, s)) / seg_tokens(p); }
 
-// Segment x of all, or (CUT) that of place x, if it is packed sequence s's.
+// Segment `at` of packed sequence s; CUT: of sequences of several.
 template <bool CUT>
-__host__ __device__ inline Segment packed_segment(const Cuts &p, long s, long x)
+__host__ __device__ inline Segment packed_segment(const Cuts &p, long s, long at)
 {
     const Seq q = find_seq(p, s);
     const long of = q.len > 0 ? (static_cast<unsigned>(q.len) + seg_tokens(p) - 1) / seg_tokens(p) : 1;
-    const long at = x - (CUT ? first_place(p, s) : first_segment(p, s));
     const bool is = at >= 0 && at < of && !(CUT && of == 1);
     return {q, s, static_cast<int>(at), is ? static_cast<int>(of) : 0, first_place(p, s) + at};
 }
+// Segment x of all, or (CUT) that of place x.
 template <bool CUT>
 __host__ __device__ inline Segment find_segment(const Cuts &p, long x)
 {
@@ -104,8 +104,16 @@ __host__ __device__ inline Segment find_segment(const Cuts &p, long x)
         const long s = static_cast<unsigned>(x) / static_cast<unsigned>(p.nseg);
         return {find_seq(p, s), s, static_cast<int>(x - s * p.nseg), p.nseg, x};
     }
-    if (!CUT && p.nseg == 1) return {find_seq(p, x), x, 0, 1, 0};
-    return packed_segment<CUT>(p, last_at(p, x, [&](long s) { return CUT ? first_place(p, s) : first_segment(p, s); }), x);
+    if constexpr (CUT) {
+        const long s = last_at(p, x, [&](long i) { return first_place(p, i); });
+        return packed_segment<true>(p, s, x - first_place(p, s));
+    } else {
+        if (x < p.n_seq) return packed_segment<false>(p, x, 0);
+        x -= p.n_seq;
+        const long s = last_at(p, x, [&](long i) { return next_segment(p, i); });
+        const Segment g = packed_segment<false>(p, s, x - next_segment(p, s) + 1);
+        return g.at > 0 ? g : Segment{g.q, g.s, 0, 0, 0};
+    }
 }
 
 // Workgroups of the join go by sequence, or by place where that makes fewer (only a
@@ -115,7 +123,7 @@ __host__ __device__ inline long join_count(const Cuts &p) { return p.n_seq > 0 ?
 __host__ __device__ inline Segment find_joined(const Cuts &p, long x)
 {
     if (p.n_seq == 0) return find_segment<true>(p, x * p.nseg);
-    const Segment g = p.n_seq < seg_places(p) ? packed_segment<true>(p, x, first_place(p, x)) : find_segment<true>(p, x);
+    const Segment g = p.n_seq < seg_places(p) ? packed_segment<true>(p, x, 0) : find_segment<true>(p, x);
     return g.at == 0 ? g : Segment{g.q, g.s, 0, 0, 0};
 }
 
@@ -136,16 +144,20 @@ struct Extent {
 // (pb blocks of columns a chain), `join` of a step a segment to join them, and
 // ceil(n / P) steps again. The P with the fewest steps is taken, counting
 // rounds of `units` workgroups. Packed sequences' lengths are on the device:
-// there the counts are bounds (at most total / len + n_seq segments hold
-// tokens, at most total / len of one sequence), and a sequence no longer than
-// a segment is not cut.
+// there it is planned for one that holds all tokens, since any number of short ones
+// may lie beside a long one, whose chain alone then bounds the call (127 sequences of
+// 500 tokens and one of 200000, 8 heads of 128 x 128, bf16 forward: 3.3 ms, 22.3 when
+// that many chains count as filling the chip; 1000 of 66 tokens, which nothing cuts,
+// pay 844 us instead of 806 for a probe and a join without work). A sequence no longer
+// than a segment is not cut; those that are may end in a part of one, which is
+// counted for half as many as there are segments.
 inline Cuts plan_segments(const Extent &x, long heads)
 {
     Cuts p{};
     p.batch = x.batch, p.tokens = x.tokens, p.n_seq = x.n_seq, p.chunks_b = (x.tokens + kC - 1) / kC;
     const bool packed = x.n_seq > 0;
-    const long n = packed ? x.tokens / kC + 1 : p.chunks_b, dirs = x.grad ? 2 : 1, extra = packed ? x.n_seq : 0;
-    const long chains = (packed ? x.n_seq : x.batch) * heads, each = packed ? heads : chains;
+    const long n = packed ? x.tokens / kC + 1 : p.chunks_b, dirs = x.grad ? 2 : 1;
+    const long chains = packed ? heads : x.batch * heads;
     const long vb = (x.dvp + x.cols - 1) / x.cols, pb = (x.dvp + x.kd + x.cols - 1) / x.cols;
     auto rounds = [&](long workgroups) { return (workgroups + x.units - 1) / x.units; };
     p.nseg = 1;
@@ -153,7 +165,7 @@ inline Cuts plan_segments(const Extent &x, long heads)
     if (chains * vb * dirs >= 4 * x.units) return p;
     double best = static_cast<double>(n * rounds(chains * vb * dirs));
     for (long k = 2; k <= std::min<long>(n / 4, 256); ++k) {
-        const long len = (n + k - 1) / k, segs = (k + extra) * each;
+        const long len = (n + k - 1) / k, segs = (k + std::min(x.n_seq, k / 2)) * chains;
         const double steps =
             static_cast<double>(len * (rounds(segs * (pb + (x.grad ? vb : 0))) + rounds(segs * vb * dirs))) + x.join * static_cast<double>(k);
         if (steps < best) best = steps, p.seg_len = static_cast<int>(len), p.nseg = static_cast<int>((n + len - 1) / len);

@@ -157,3 +157,24 @@ def test_packed_workspaces_follow_the_tokens(lib, grad):
         assert p["groups"] <= n_seq + 256, p
         if not grad and n_seq in (64, 1000) and tokens < 100000:
             assert p["bytes"] < 1 << 30, p
+
+
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("tokens,hk,kd", [(32768, 8, 128), (263500, 8, 128), (1 << 20, 4, 64), (100000, 24, 32)])
+def test_short_sequences_beside_a_long_one_do_not_keep_it_whole(lib, tokens, hk, kd, grad):
+    """The host does not know the lengths: whatever their number, one sequence may hold nearly all tokens. Its chains
+    (rounds of a segment's chunks, twice, and the join) take at most twice the steps that they are planned to take alone."""
+    join, units, dirs = {128: 0.4, 64: 0.3, 32: 0.1}[kd], (512 if kd <= 64 else 256), 1 + grad
+    cols = 128 if not grad and kd > 64 else 64
+    vb, pb = -(-kd // cols), -(-2 * kd // cols)
+
+    def steps(n_seq):
+        p = _plan(lib, tokens, n_seq, hk, kd=kd, dv=kd, grad=grad)
+        groups = p["nseg"] * hk
+        main = p["seg_len"] * -(-groups * vb * dirs // units)
+        probe = p["seg_len"] * -(-groups * (pb + (vb if grad else 0)) // units) + join * p["nseg"]
+        return main + (probe if p["nseg"] > 1 else 0)
+
+    alone = steps(1)
+    for n_seq in (2, 7, 64, 127, 128, 129, 500, 1000):
+        assert steps(n_seq) <= 2 * alone, (n_seq, steps(n_seq), alone)
