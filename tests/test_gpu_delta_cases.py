@@ -127,3 +127,45 @@ def test_packed_workspaces(n_seq, tokens, h, dk, dv):
     used = _workspace(lambda: pkg.gated_delta_fwd(*x, cu_seqlens=cu, o=o))
     most = ((n_seq * tokens // 64 + n_seq) * 21760 + 512 * dk * (6 * dk + 4 * dv)) * h
     assert used <= most + (64 << 20) and used < 1 << 30, (used, most)  # (an allocation is rounded up to whole MB)
+
+
+# ------------------------------------------------------------------ wide values, segments of every width
+
+# (batch, tokens, hk, h, dk, dv): probes whose workgroups hold columns of values and of the unit matrix, several blocks of columns
+WIDE = [(1, 1500, 1, 1, 32, 96), (1, 1500, 1, 2, 64, 128), (1, 1300, 1, 1, 128, 260), (1, 600, 1, 1, 24, 1024), (2, 150, 1, 2, 64, 1000)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", WIDE, ids=str)
+def test_wide_values(case, dtype):
+    B, T, hk, h, dk, dv = case
+    x = D.make(B, T, hk, h, dk, dv, dtype, T + dv)
+    g = D._gen(39)
+    h0, dh = torch.randn(B, h, dk, dv, generator=g, device="cuda"), torch.randn(B, h, dk, dv, generator=g, device="cuda")
+    do = torch.randn(B, T, h, dv, generator=g, device="cuda").to(DT[dtype])
+    ref, S, top = D.reference(*x, dk ** -0.5, h0)
+    o, last = pkg.gated_delta_fwd(*x, h_init=h0, return_last_state=True)
+    D._close(o, ref, D._bar(T, dk, top, ref, dtype), f"o {case}")
+    D._close(last, S, D._bar(T, dk, top, S, "f32"), f"h_last {case}")
+    D._check_bwd(x, do, h0, dh, dtype, f"{case}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dk,dv", [(64, 128), (32, 200)])
+def test_wide_values_packed(dk, dv, dtype):
+    lens, hk, h = [1200, 3, 0, 700, 64, 129], 1, 2
+    x, cu, h0 = D._packed(lens, hk, h, dk, dv, dtype, 43)
+    do = torch.randn(1, sum(lens), h, dv, generator=D._gen(44), device="cuda").to(DT[dtype])
+    dh = torch.randn(h0.shape, generator=D._gen(45), device="cuda")
+    o, last = pkg.gated_delta_fwd(*x, h_init=h0, cu_seqlens=cu, return_last_state=True)
+    r = pkg.gated_delta_bwd(*x, do, h_init=h0, dh_last=dh, cu_seqlens=cu)
+    at = 0
+    for i, t in enumerate(lens):
+        sl, one = slice(at, at + t), slice(i, i + 1)
+        ref, S, top = D.reference(*(y[:, sl] for y in x), dk ** -0.5, h0[one])
+        D._close(o[:, sl], ref, D._bar(t, dk, top, ref, dtype), f"o {i}")
+        D._close(last[one], S, D._bar(t, dk, top, S, "f32"), f"h_last {i}")
+        if t:
+            got = {n: r[n][:, sl] for n in ("dq", "dk", "dv", "dg", "dbeta")} | {"dh_init": r["dh_init"][one]}
+            D._check_bwd([y[:, sl] for y in x], do[:, sl], h0[one], dh[one], dtype, f"{i}", got=got)
+        at += t
