@@ -132,7 +132,7 @@ int ssm2d_rope_bf16(const uint16_t *q, const uint16_t *k, const int32_t *positio
  * [sequences][heads][d_k][d_v], the state before the first and after the last
  * token; an empty sequence passes its state on. h_last may be h_init.
  * Limits: d_k <= SSM2D_DELTA_MAX_DK, d_v <= SSM2D_DELTA_MAX_DV, sequences *
- * heads < 2^24, heads < 2^15, tokens < 2^31 - 64, chunks of 64 tokens < 2^22, and
+ * heads < 2^24 (2^23 beyond the few tokens below), heads < 2^15, tokens < 2^31 - 64, chunks of 64 tokens < 2^22, and
  * token strides of v and dout in 0 .. 2^26 - 1.
  *
  * The forward and backward work on chunks of 64 tokens with matrix

@@ -42,15 +42,18 @@ int fill(DeltaArgs *a, const ssm2d_delta_shape *sh, float scale, void *stream, b
 
 __global__ void pass_states(const float *in, float *out, long n)
 {
-    const long i = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (i < n) out[i] = in ? in[i] : 0.0f;
+    const long step = static_cast<long>(gridDim.x) * blockDim.x;
+    for (long i = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) out[i] = in ? in[i] : 0.0f;
 }
+
+// Workgroups of 256 for n elements (any number beyond these takes more turns).
+unsigned blocks_of(long n) { return static_cast<unsigned>(std::min<long>((n + 255) / 256, 1 << 20)); }
 
 int pass_states_on(const DeltaArgs &a, const float *in, float *out)
 {
     const long n = (a.n_seq > 0 ? a.n_seq : a.batch) * a.h * a.dk_ * a.dv_;
     if (!out || out == in || n == 0) return SSM2D_OK;
-    pass_states<<<dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, static_cast<hipStream_t>(a.stream)>>>(in, out, n);
+    pass_states<<<dim3(blocks_of(n)), dim3(256), 0, static_cast<hipStream_t>(a.stream)>>>(in, out, n);
     return launched();
 }
 
@@ -59,18 +62,18 @@ int pass_states_on(const DeltaArgs &a, const float *in, float *out)
 template <typename T>
 __global__ void fill_zeros(T *out, long n)
 {
-    const long i = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (i < n) out[i] = 0;
+    const long step = static_cast<long>(gridDim.x) * blockDim.x;
+    for (long i = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) out[i] = 0;
 }
 
 template <typename T>
 int zeros(T *out, int64_t rows, int64_t d, void *stream)
 {
     if (rows <= 0 || d <= 0) return SSM2D_OK;
-    if (rows * d > (int64_t{1} << 38)) return SSM2D_ERR_UNSUPPORTED;  // (a grid; far beyond memory)
+    if (rows > (int64_t{1} << 45) / d) return SSM2D_ERR_UNSUPPORTED;  // (far beyond memory; rows are below 2^55)
     if (!out) return SSM2D_ERR_NULLPTR;
     if (off_by(out, sizeof(T))) return SSM2D_ERR_MISALIGNED;
-    fill_zeros<<<dim3(static_cast<unsigned>((rows * d + 255) / 256)), dim3(256), 0, static_cast<hipStream_t>(stream)>>>(out, rows * d);
+    fill_zeros<<<dim3(blocks_of(rows * d)), dim3(256), 0, static_cast<hipStream_t>(stream)>>>(out, rows * d);
     return launched();
 }
 

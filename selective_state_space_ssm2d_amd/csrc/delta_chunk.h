@@ -1609,6 +1609,8 @@ int chunk_passes(const DeltaArgs &a)
     const Passes plan = plan_passes(x);
     const Share &share = plan.share;
     p.nseg = plan.cuts.nseg, p.seg_len = plan.cuts.seg_len;
+    // (so many chains at once take a workspace of 170 GiB and more)
+    if (seg_count(p) * plan.nhk * p.rep > most_groups(512)) return SSM2D_ERR_UNSUPPORTED;
     void *ws = nullptr;
     int rc = get_aux_ws(a.dev, a.stream, kSlotDelta, plan.bytes(x), &ws);
     if (rc != SSM2D_OK) return rc;

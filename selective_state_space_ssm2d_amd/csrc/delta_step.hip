@@ -22,7 +22,7 @@ struct StepParams {
     const float *g, *beta, *h_init;
     float *h_last;
     void *o;
-    long tokens;
+    long tokens, first;  // first: the launch's first head of all batch entries'
     int hk, h, dk, dv, slices;
     long qs[3], ks[3], vs[3], gs[3], bs[3];
     float scale;
@@ -45,8 +45,9 @@ __global__ __launch_bounds__(256) void delta_step_kernel(StepParams p)
     __shared__ float sk[SSM2D_DELTA_MAX_DK], sq[SSM2D_DELTA_MAX_DK];
     __shared__ float part[4][VS][2];
     const int tid = threadIdx.x, vl = tid % VL, kr = tid / VL, wave = tid / 64;
-    const long bh = blockIdx.x / p.slices;
-    const int slice = static_cast<int>(blockIdx.x - bh * p.slices);
+    const unsigned own = blockIdx.x / static_cast<unsigned>(p.slices);
+    const int slice = static_cast<int>(blockIdx.x - own * p.slices);
+    const long bh = p.first + own;
     const long b = bh / p.h;
     const int h = static_cast<int>(bh - b * p.h), hq = h / (p.h / p.hk);
     const int col = slice * VS + vl * VEC;
@@ -141,11 +142,16 @@ int delta_step(const DeltaArgs &a)
     }
     const hipStream_t s = static_cast<hipStream_t>(a.stream);
     const long heads = a.batch * a.h;
-    auto go = [&](auto vs, auto vec) {
+    auto go = [&](auto vs, auto vec) -> int {
         constexpr int VS = decltype(vs)::value, VEC = decltype(vec)::value;
         p.slices = (a.dv_ + VS - 1) / VS;
-        delta_step_kernel<T, VS, VEC><<<dim3(static_cast<unsigned>(heads * p.slices)), dim3(256), 0, s>>>(p);
-        return launched();
+        const long most = most_groups(256) / p.slices;
+        for (p.first = 0; p.first < heads; p.first += most) {
+            delta_step_kernel<T, VS, VEC><<<dim3(static_cast<unsigned>(std::min(heads - p.first, most) * p.slices)), dim3(256), 0, s>>>(p);
+            const int st = launched();
+            if (st != SSM2D_OK) return st;
+        }
+        return SSM2D_OK;
     };
     using std::integral_constant;
     if (a.dv_ % 4 != 0 || off_by(a.h_init, 16) || off_by(a.h_last, 16))

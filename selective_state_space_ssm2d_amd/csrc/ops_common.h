@@ -132,6 +132,10 @@ __device__ __forceinline__ float lane_sum(float v)
     return v;
 }
 
+// Workgroups of so many threads that one launch takes: HIP's grids have less
+// than 2^32 threads along a dimension.
+constexpr long most_groups(int threads) { return ((1L << 32) - 1) / threads; }
+
 inline bool off_by(const void *p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
 inline int launched()

@@ -169,3 +169,51 @@ def test_wide_values_packed(dk, dv, dtype):
             got = {n: r[n][:, sl] for n in ("dq", "dk", "dv", "dg", "dbeta")} | {"dh_init": r["dh_init"][one]}
             D._check_bwd([y[:, sl] for y in x], do[:, sl], h0[one], dh[one], dtype, f"{i}", got=got)
         at += t
+
+
+# ------------------------------------------------------------------ beyond the threads of one launch
+
+@pytest.fixture
+def large():
+    """Room for tens of GB, given back afterwards."""
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GB of free GPU memory")
+    yield
+    pkg.release_workspaces()
+    torch.cuda.empty_cache()
+
+
+def test_step_of_2_to_the_23_heads(large):
+    """Two blocks of columns a head: 2^24 workgroups of 256 threads, which HIP does not take at once. Heads of one key are
+    formulas of one element, each rounding a few times in fp32."""
+    B, h, dv = 1 << 20, 8, 128
+    g = D._gen(46)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    q, k, gate, beta = rn(B, h, 1), rn(B, h, 1).clamp_(-1, 1), -torch.rand(B, h, generator=g, device="cuda"), torch.rand(B, h, generator=g, device="cuda")
+    v, state = rn(B, h, dv), rn(B, h, 1, dv)
+    parts = [slice(i, i + (B >> 3)) for i in range(0, B, B >> 3)]
+    first = state.clone()
+    o = pkg.gated_delta_step(q, k, v, gate, beta, state, scale=0.5)
+    for p in parts:
+        S = torch.exp(gate[p])[..., None] * first[p, :, 0]
+        S = S + k[p] * (beta[p][..., None] * (v[p] - S * k[p]))
+        size = first[p, :, 0].abs() + v[p].abs()  # (|k| <= 1: what is added up is no larger)
+        assert bool(((state[p, :, 0] - S).abs() <= 16 * U * size).all()), p
+        assert bool(((o[p] - 0.5 * q[p] * S).abs() <= 16 * U * size * (1 + q[p].abs())).all()), p
+
+
+def test_no_tokens_of_2_to_the_32_state_elements(large):
+    h0 = torch.empty(1 << 15, 1, 128, 1024, device="cuda")
+    h0.view(-1)[::12345] = 1.0
+    none = [torch.empty(1 << 15, 0, 1, d, device="cuda") for d in (128, 128, 1024)] + [torch.empty(1 << 15, 0, 1, device="cuda")] * 2
+    _, last = pkg.gated_delta_fwd(*none, h_init=h0, return_last_state=True)
+    assert all(torch.equal(last[i:i + 4096].view(torch.int32), h0[i:i + 4096].view(torch.int32)) for i in range(0, 1 << 15, 4096))
+
+
+def test_no_keys_of_2_to_the_32_outputs(large):
+    B, T, dv = 1 << 12, 1 << 10, 1024
+    v = torch.empty(B, T, 1, dv, dtype=torch.bfloat16, device="cuda")
+    q, g = torch.empty(B, T, 1, 0, dtype=torch.bfloat16, device="cuda"), torch.zeros(B, T, 1, device="cuda")
+    o = torch.full_like(v, 3.0)
+    pkg.gated_delta_fwd(q, q, v, g, g, o=o)
+    assert not any(bool(o[i:i + 512].any()) for i in range(0, B, 512))
