@@ -132,6 +132,8 @@ def _norm_layout(x, channels_first, name="x"):
     if channels_first:
         if x.dim() < 2:
             raise ValueError(f"{name} must be [batch, channels, ...]")
+        if 0 in x.shape[2:]:
+            return x.shape[0], x.shape[1], 0, x.stride(0), x.stride(1)
         cells = 1
         for size, stride in zip(reversed(x.shape[2:]), reversed(x.stride()[2:])):
             if size != 1 and stride != cells:

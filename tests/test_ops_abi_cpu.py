@@ -169,3 +169,13 @@ def test_binding_refuses_tensors_off_the_gpu():
             call()
     with pytest.raises(TypeError):
         pkg.layer_norm_fwd(x.double())
+
+
+def test_norm_layout_of_empty_maps():
+    """Maps without cells lie anyhow: their strides say nothing."""
+    for shape in ((2, 3, 4, 0), (2, 3, 0, 4), (2, 3, 0, 0), (0, 3, 4, 4), (2, 0, 4, 4)):
+        x = torch.empty(shape)
+        b, n, cells, _, _ = ops._norm_layout(x, True)
+        assert (b, n, cells) == (shape[0], shape[1], shape[2] * shape[3]), shape
+    with pytest.raises(ValueError):
+        ops._norm_layout(torch.empty(2, 3, 4, 5).transpose(2, 3), True)
