@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 
 import torch
 
@@ -201,12 +202,11 @@ def _rope_shape(batch, tokens, hq, hk, d, qs, ks, sections, pos):
     return _RopeShape(batch, tokens, hq, hk, d, qs, ks, len(sections), sections + (0,) * (ROPE_MAX_AXES - len(sections)), pos)
 
 
-@functools.lru_cache(maxsize=64)
 def _sections(sections):
     """(the sections as integers, the pairs they make)."""
     if not 1 <= len(sections) <= ROPE_MAX_AXES:
         raise ValueError(f"1 to {ROPE_MAX_AXES} sections")
-    sections = tuple(int(s) for s in sections)
+    sections = tuple(map(operator.index, sections))
     return sections, sum(sections)
 
 

@@ -179,3 +179,13 @@ def test_norm_layout_of_empty_maps():
         assert (b, n, cells) == (shape[0], shape[1], shape[2] * shape[3]), shape
     with pytest.raises(ValueError):
         ops._norm_layout(torch.empty(2, 3, 4, 5).transpose(2, 3), True)
+
+
+def test_rope_sections_are_read_at_each_call():
+    """Sections held in tensors that change are not answered from an earlier call; halves of a pair are refused."""
+    sections = [torch.tensor(2), torch.tensor(3)]
+    assert ops._sections(tuple(sections)) == ((2, 3), 5)
+    sections[0].fill_(1)
+    assert ops._sections(tuple(sections)) == ((1, 3), 4)
+    with pytest.raises(TypeError):
+        ops._sections((2.5, 1))
