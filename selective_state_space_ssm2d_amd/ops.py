@@ -181,6 +181,8 @@ def layer_norm_bwd(x, weight, mean, rstd, dy, *, channels_first=False, out=None,
     batch, n, cells, sb, sn = _norm_layout(x, channels_first)
     if dy.shape != x.shape or dy.dtype != x.dtype:
         raise ValueError("dy must match x in shape and dtype")
+    if mean is None or rstd is None:
+        raise ValueError("mean and rstd are required")
     _, _, _, gb, gn = _norm_layout(dy, channels_first, "dy")
     _on_gpu(dev, weight=weight, mean=mean, rstd=rstd, dy=dy)
     _f32((n,), weight=weight)

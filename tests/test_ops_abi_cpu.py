@@ -189,3 +189,10 @@ def test_rope_sections_are_read_at_each_call():
     assert ops._sections(tuple(sections)) == ((1, 3), 4)
     with pytest.raises(TypeError):
         ops._sections((2.5, 1))
+
+
+def test_norm_bwd_needs_the_statistics():
+    x = torch.zeros(2, 8)
+    for mean, rstd in ((None, x[:, 0]), (x[:, 0], None), (None, None)):
+        with pytest.raises(ValueError, match="mean and rstd"):
+            pkg.layer_norm_bwd(x, None, mean, rstd, x)
