@@ -332,7 +332,7 @@ def gated_delta_fwd(q, k, v, g, beta, *, scale=None, h_init=None, cu_seqlens=Non
 def gated_delta_bwd(q, k, v, g, beta, do, *, scale=None, h_init=None, dh_last=None, cu_seqlens=None, out=None, stream=None):
     """Gradients of gated_delta_fwd for do = dL/do and dh_last = dL/dh_last
     (None: zeros): a dict dq, dk, dv (their inputs' dtype), dg, dbeta (float32),
-    and dh_init when h_init or dh_last is given. ``out`` may supply any of them."""
+    and dh_init when h_init or dh_last is given or ``out`` holds it. ``out`` may supply any of them."""
     fn = _entry("ssm2d_gated_delta_bwd", q.dtype)
     dev, seqs, shape = _delta_check(q, k, v, g, beta, cu_seqlens, do)
     states = (seqs, v.shape[2], q.shape[3], v.shape[3])
@@ -340,7 +340,7 @@ def gated_delta_bwd(q, k, v, g, beta, do, *, scale=None, h_init=None, dh_last=No
     _f32(states, h_init=h_init, dh_last=dh_last)
     out = out or {}
     r = {n: _like(n, out.get(n), t, stream) for n, t in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta))}
-    if h_init is not None or dh_last is not None:
+    if h_init is not None or dh_last is not None or out.get("dh_init") is not None:
         r["dh_init"] = _out("dh_init", out.get("dh_init"), states, torch.float32, dev, stream)
     _run(fn, dev, stream, (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(h_init), _ptr(cu_seqlens),
                            do.data_ptr(), _ptr(dh_last), *(r[n].data_ptr() for n in ("dq", "dk", "dv", "dg", "dbeta")), _ptr(r.get("dh_init")),

@@ -217,3 +217,16 @@ def test_no_keys_of_2_to_the_32_outputs(large):
     o = torch.full_like(v, 3.0)
     pkg.gated_delta_fwd(q, q, v, g, g, o=o)
     assert not any(bool(o[i:i + 512].any()) for i in range(0, B, 512))
+
+
+# ------------------------------------------------------------------ gradients of a state that is not given
+
+def test_bwd_writes_the_state_gradient_it_is_given():
+    """dh_init in ``out`` is asked for, also where the forward started from zeros."""
+    x = D.make(2, 70, 1, 2, 32, 32, "f32", 47)
+    do = torch.randn(2, 70, 2, 32, generator=D._gen(48), device="cuda")
+    want = pkg.gated_delta_bwd(*x, do, h_init=torch.zeros(2, 2, 32, 32, device="cuda"))["dh_init"]
+    into = torch.full((2, 2, 32, 32), 3.0, device="cuda")
+    r = pkg.gated_delta_bwd(*x, do, out={"dh_init": into})
+    assert r["dh_init"] is into and torch.equal(into, want)
+    assert "dh_init" not in pkg.gated_delta_bwd(*x, do)
