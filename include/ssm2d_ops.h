@@ -47,7 +47,8 @@ extern "C" {
  * scan's own layout, with cells = H * W and x_stride_n = H * W. y is dense
  * [batch][n][cells]; weight, bias float32 [n] (NULL: ones, zeros); mean, rstd
  * float32 [batch][cells] (NULL: not stored). The variance is the mean of
- * squared differences from the mean, not a difference of moments.
+ * squared differences from the mean, not a difference of moments. Of no channels
+ * the mean is 0 and rstd 1 / sqrt(eps).
  * Limit: n <= SSM2D_LN_MAX_N. */
 #define SSM2D_LN_MAX_N 16384
 

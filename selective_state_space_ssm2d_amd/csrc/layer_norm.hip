@@ -558,6 +558,16 @@ __global__ void ln_zero(float *a, float *b, int n)
     if (b) b[i] = 0.0f;
 }
 
+// The statistics of no channels: sums over nothing are zeros.
+__global__ void ln_no_channels(float *mean, float *rstd, long rows, float eps)
+{
+    const long step = static_cast<long>(gridDim.x) * blockDim.x;
+    for (long i = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x; i < rows; i += step) {
+        if (mean) mean[i] = 0.0f;
+        if (rstd) rstd[i] = 1.0f / sqrtf(eps);
+    }
+}
+
 // ------------------------------------------------------------------ host
 
 struct NormArgs {
@@ -825,8 +835,14 @@ int norm_fwd_entry(const T *x, const float *weight, const float *bias, T *y, flo
 {
     int st = check_sizes(batch, n, cells);
     if (st != SSM2D_OK) return st;
-    if (batch == 0 || n == 0 || cells == 0) return SSM2D_OK;
+    if (batch == 0 || cells == 0 || (n == 0 && !mean && !rstd)) return SSM2D_OK;
     if (beyond(batch, n, cells)) return SSM2D_ERR_UNSUPPORTED;
+    if (n == 0) {
+        if (off_by(mean, 4) || off_by(rstd, 4)) return SSM2D_ERR_MISALIGNED;
+        ln_no_channels<<<dim3(blocks_for((batch * cells + 255) / 256, 1 << 20)), dim3(256), 0, static_cast<hipStream_t>(stream)>>>(
+            mean, rstd, batch * cells, eps);
+        return launched();
+    }
     if (!x || !y) return SSM2D_ERR_NULLPTR;
     if (off_by(x, sizeof(T)) || off_by(y, sizeof(T)) || off_by(weight, 4) || off_by(bias, 4) || off_by(mean, 4) || off_by(rstd, 4))
         return SSM2D_ERR_MISALIGNED;

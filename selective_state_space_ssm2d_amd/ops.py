@@ -144,9 +144,11 @@ def _norm_layout(x, channels_first, name="x"):
     if x.dim() < 1:
         raise ValueError(f"{name} must be [..., channels]")
     n = x.shape[-1]
+    if n == 0:
+        return x.shape[:-1].numel(), 0, 1, 0, 1
     if x.dim() != 2:
         try:
-            x = x.view(-1, n) if n else x.reshape(0, 0)
+            x = x.view(-1, n)
         except RuntimeError:
             raise ValueError(f"the rows of {name} must lie at one stride") from None
     if n > 1 and x.shape[0] and x.stride(1) != 1:

@@ -290,3 +290,19 @@ def test_example_serves_what_it_trains(example, dtype):
         want = m(x).double()
     bar = 64 * U * math.sqrt(120 * 32) + (4 * 2.0 ** -7 if dtype == "bf16" else 0)
     D._close(m.serve(x, 7), want, bar * want.abs().max(), "served")
+
+
+# ------------------------------------------------------------------ rows of no channels
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape,cf", [((5, 0), False), ((2, 7, 0), False), ((2, 0, 7), True)])
+def test_norm_of_no_channels(shape, cf, dtype):
+    """Sums over nothing are zeros: the mean 0, the variance 0, so rstd = 1 / sqrt(eps)."""
+    x = torch.empty(shape, dtype=DT[dtype], device="cuda")
+    stale = [torch.full((s,), 3.0, device="cuda") for s in (5, 14) for _ in range(64)]  # (what an allocation without writing would show)
+    del stale
+    y, mean, rstd = pkg.layer_norm_fwd(x, eps=0.25, channels_first=cf, return_stats=True)
+    assert y.shape == x.shape and mean.shape == (shape[:1] + shape[2:] if cf else shape[:-1])
+    assert bool((mean == 0).all()) and bool((rstd == 2).all())
+    r = pkg.layer_norm_bwd(x, None, mean, rstd, x, channels_first=cf)
+    assert r["dx"].shape == x.shape and r["dweight"].shape == (0,)
