@@ -116,14 +116,16 @@ __host__ __device__ inline Segment find_segment(const Cuts &p, long x)
     }
 }
 
-// Workgroups of the join go by sequence, or by place where that makes fewer (only a
-// sequence's first place does anything: of 7 sequences with 49 places, 8 heads of
-// 128 x 128, 22 us by sequence and 47 by place).
-__host__ __device__ inline long join_count(const Cuts &p) { return p.n_seq > 0 ? (p.n_seq < seg_places(p) ? p.n_seq : seg_places(p)) : p.batch; }
+// Workgroups of the join go by sequence, or by place where that makes far fewer (only
+// a sequence's first place does anything, and finding it takes a search, which empty
+// workgroups wait for: of 7 sequences with 49 places, 8 heads of 128 x 128, 22 us by
+// sequence and 47 by place).
+__host__ __device__ inline bool join_by_place(const Cuts &p) { return p.n_seq > 4 * seg_places(p); }
+__host__ __device__ inline long join_count(const Cuts &p) { return p.n_seq == 0 ? p.batch : (join_by_place(p) ? seg_places(p) : p.n_seq); }
 __host__ __device__ inline Segment find_joined(const Cuts &p, long x)
 {
     if (p.n_seq == 0) return find_segment<true>(p, x * p.nseg);
-    const Segment g = p.n_seq < seg_places(p) ? packed_segment<true>(p, x, 0) : find_segment<true>(p, x);
+    const Segment g = join_by_place(p) ? find_segment<true>(p, x) : packed_segment<true>(p, x, 0);
     return g.at == 0 ? g : Segment{g.q, g.s, 0, 0, 0};
 }
 
