@@ -230,3 +230,19 @@ def test_bwd_writes_the_state_gradient_it_is_given():
     r = pkg.gated_delta_bwd(*x, do, out={"dh_init": into})
     assert r["dh_init"] is into and torch.equal(into, want)
     assert "dh_init" not in pkg.gated_delta_bwd(*x, do)
+
+
+# ------------------------------------------------------------------ many segments
+
+@pytest.mark.parametrize("T,dk,dv,dtype", [(12000, 32, 32, "f32"), (9000, 64, 48, "bf16"), (9000, 128, 64, "bf16")])
+def test_long_chains(T, dk, dv, dtype):
+    """One sequence in as many segments as the plan makes of it, against the recurrence over all of its tokens."""
+    x = D.make(1, T, 1, 1, dk, dv, dtype, T + dk)
+    h0 = torch.randn(1, 1, dk, dv, generator=D._gen(49), device="cuda")
+    ref, S, top = D.reference(*x, dk ** -0.5, h0)
+    o, last = pkg.gated_delta_fwd(*x, h_init=h0, return_last_state=True)
+    D._close(o, ref, D._bar(T, dk, top, ref, dtype), "o")
+    D._close(last, S, D._bar(T, dk, top, S, "f32"), "h_last")
+    x, T = tuple(t[:, :4500] for t in x), 4500
+    do = torch.randn(1, T, 1, dv, generator=D._gen(50), device="cuda").to(DT[dtype])
+    D._check_bwd(x, do, h0, torch.randn(h0.shape, generator=D._gen(51), device="cuda"), dtype, "long")
