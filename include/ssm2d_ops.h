@@ -140,8 +140,8 @@ int ssm2d_rope_bf16(const uint16_t *q, const uint16_t *k, const int32_t *positio
  * instructions: products of fp32 operands split into three bf16 parts each, so
  * that states and sums keep fp32's precision, those that make a bf16 output
  * too. A NaN or Inf at a token may reach the other tokens of its chunk, but no
- * chunk before. Up to 8 tokens
- * (bf16; 16 of float32) go through the recurrence itself.
+ * chunk before. Up to 8 tokens (bf16; 16 of float32) go through the recurrence
+ * itself.
  * Heads of no keys or no values give zeros. */
 #define SSM2D_DELTA_MAX_DK 128
 #define SSM2D_DELTA_MAX_DV 1024

@@ -814,7 +814,7 @@ struct SeqStage {
     }
 };
 
-// The chain over a sequence's chunks for 16 columns of the state a wave (64 or
+// The chain over a sequence's chunks for 16 columns of the state a wave (32, 64 or
 // 128 a workgroup). Columns are independent, so waves only share what they read.
 // The state [KD][16] stays in accumulators, from which it is cut into operands.
 //
@@ -830,10 +830,10 @@ struct SeqStage {
 // gets four neighbours of a token's row); else S0 and E are kept for
 // delta_local.
 //
-// Measured: 8 heads of 128 x 128, bf16, 20034 packed tokens: probe 139 us, outputs
-// 107 us (443 us for the whole forward with 64 columns a workgroup, 283 with 128,
+// Measured: 8 heads of 128 x 128, bf16, 20034 packed tokens: probe 138 us, outputs
+// 113 us (443 us for the whole forward with 64 columns a workgroup, 283 with 128,
 // which read a chunk's K, Q and M once for 8 waves); 4 heads of 32 x 32, fp32, 196608
-// tokens: 107 and 181 us (290 with four waves, two of them idle). With 128 columns
+// tokens: 109 and 184 us (290 with four waves, two of them idle). With 128 columns
 // the backward's chains took 147 and 130 us instead of 137 and 113 (2 x 4099
 // tokens, 8 heads of 128 x 128).
 template <typename T, int KD, bool BWD, bool PROBE, bool OUT, int THREADS>

@@ -19,7 +19,10 @@
 // 192 x 56 x 56 maps, bf16: 17 us, 4.6 TB/s; backward of 12544 rows of 768, bf16:
 // 18 us, 3.3 TB/s, 4 of them ln_fold; of a 128 x 384 x 512 map, fp32: 71 us, 4.3
 // TB/s. One row of 768 takes 2.2 us. What bounds the smaller ones is the start
-// and the end of a launch, then the fold.
+// and the end of a launch, then the fold. Far from memory's rate, warm inputs: 64 x
+// 768 x 196 maps backward (read again: 53 us bf16, 74 fp32, 1.1 and 1.6 TB/s), 64 x 768 x
+// 49 (odd rows of cells: 10 and 13 us forward, 42 and 44 backward), 4 x 96 x 50175 (56 us
+// forward; 64 and 70 backward, 1.8 and 3.3 TB/s).
 #include "ops_common.h"
 
 namespace ssm2d_impl {

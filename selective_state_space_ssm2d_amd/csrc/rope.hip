@@ -38,7 +38,7 @@ __device__ __forceinline__ float2 cos_sin(int pos, float freq)
 {
     // (the sums of parts below rely on every operation rounding by itself)
 #pragma clang fp contract(off)
-    // pos in two parts of at most 16 bits, exact in fp32; the products' errors by fma
+    // pos in two parts, of 20 bits (with the sign) and 12, exact in fp32; the products' errors by fma
     const float ph = static_cast<float>(pos >> 12) * 4096.0f, pl = static_cast<float>(pos & 4095);
     const float a = ph * freq, ae = fmaf(ph, freq, -a);
     const float b = pl * freq, be = fmaf(pl, freq, -b);

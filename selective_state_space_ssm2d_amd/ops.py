@@ -13,7 +13,8 @@ the HIP stream to libssm2d.so; every operator runs in the library's kernels.
 
 x, q, k, v and gradients of them: float32 or bfloat16; weights, statistics, g,
 beta and states: float32. Inputs may be strided views (inner dim contiguous);
-outputs are dense. Without ``stream`` a call runs on the current stream of its
+outputs are dense, and take no part in autograd: gradients come from the _bwd
+entries (examples/map_mixer.py wraps them). Without ``stream`` a call runs on the current stream of its
 tensors' device; with one, its outputs are allocated on that stream too, and
 ordering the inputs' producers before it is the caller's.
 """
