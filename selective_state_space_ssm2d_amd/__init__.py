@@ -19,7 +19,9 @@ tensors on the current CUDA (HIP) device, contiguous. ``scan_fwd_ex`` selects
 the scan direction and order, and multi-direction sums (SSM2D_* flags).
 
 The operators around the scan (layer norm, rotary positions with several axes,
-the gated delta rule) are in ``ops``, and reached from here too.
+the gated delta rule) are in ``ops``, those of a recurrent block (projections,
+its norms with gate and residual, the gated linear recurrence) in ``block``; all
+are reached from here too.
 """
 from __future__ import annotations
 
@@ -34,6 +36,7 @@ __all__ = [
     "sync_check", "set_spin_limit", "release_workspaces", "set_epoch_for_test", "fwd_kernels", "exported_names",
     "Ssm2dError",
     "layer_norm_fwd", "layer_norm_bwd", "rope_fwd", "rope_bwd", "gated_delta_fwd", "gated_delta_bwd", "gated_delta_step",
+    "linear_fwd", "linear_bwd", "block_norm_fwd", "block_norm_bwd", "recurrence_fwd", "recurrence_bwd", "recurrence_step",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -387,11 +390,19 @@ def scan_bwd_mamba(x, delta, A, B, C, D, dy, z=None, delta_bias=None, *, delta_s
 _OPS = ("layer_norm_fwd", "layer_norm_bwd", "rope_fwd", "rope_bwd", "gated_delta_fwd", "gated_delta_bwd", "gated_delta_step")
 
 
+_BLOCK = ("linear_fwd", "linear_bwd", "block_norm_fwd", "block_norm_bwd", "recurrence_fwd", "recurrence_bwd", "recurrence_step")
+
+
 def __getattr__(name):
-    """The operators of ``ops``, imported with their first use (they need torch at import; this module does not)."""
+    """The operators of ``ops`` and ``block``, imported with their first use (they need torch at import; this module does not)."""
     if name in _OPS:
         from . import ops
 
         globals().update({n: getattr(ops, n) for n in _OPS})
+        return globals()[name]
+    if name in _BLOCK:
+        from . import block
+
+        globals().update({n: getattr(block, n) for n in _BLOCK})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,425 @@
+// libssm2d: linear's entries: checks, the products behind the forward and the
+// gradients, and the pass that makes dz and dbias (linear.h has the products).
+//
+// With rows as token rows [r][channel] and maps [channel][r], all of them are
+// C = A B^T with C's n contiguous:
+//   forward    y rows: m = r, n = j, A = x, B = weight;    y maps: m = j, n = r, A = weight, B = x
+//   dx         x rows: m = r, n = i, A = dz, B = weight^T;  x maps: m = i, n = r, A = weight^T, B = dz
+//   dweight    m = j, n = i, A = dz^T, B = x^T, the sum over r and the batch
+// and each operand has its summed index contiguous or the other one.
+#include "linear.h"
+
+namespace ssm2d_impl {
+namespace gemm {
+
+template <>
+int run_gemm<uint16_t>(GemmParams p, bool a_kc, bool b_kc, void *ws, hipStream_t s);
+template <>
+int run_gemm<float>(GemmParams p, bool a_kc, bool b_kc, void *ws, hipStream_t s);
+
+}  // namespace gemm
+
+namespace {
+
+using namespace gemm;
+
+// ------------------------------------------------------------------ dz and dbias
+
+struct SlopeParams {
+    const void *dy, *pre;
+    void *dz;        // NULL: not stored
+    float *part;     // [slice][n] sums; NULL: not wanted
+    long batch, rows, n;
+    long d_b, d_s;   // dy: batch; row, or channel of maps
+    int act, slices; // slices of the rows (of each batch entry)
+    long each;       // rows of a slice
+    long first;
+};
+
+template <typename T, int V>
+__device__ __forceinline__ void slope_of(const SlopeParams &p, const T *dy, const T *pre, T *dz, float (&v)[V])
+{
+    Raw<T, V> d;
+    d.load(dy);
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = d.get(j);
+    if (p.act != SSM2D_ACT_NONE) {
+        Raw<T, V> z;
+        z.load(pre);
+        switch (p.act) {
+        case SSM2D_ACT_RELU:
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] = z.get(j) > 0.0f ? v[j] : 0.0f;
+            break;
+        case SSM2D_ACT_SILU:
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] *= act_slope<T, SSM2D_ACT_SILU>(z.get(j));
+            break;
+        default:
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] *= act_slope<T, SSM2D_ACT_GELU>(z.get(j));
+            break;
+        }
+        if (dz) {
+            Raw<T, V> o;
+            o.set(v);
+            o.store(dz);
+        }
+    }
+}
+
+// Token rows: 32 lanes of V channels by 8 rows; a slice of rows a workgroup.
+template <typename T, int V>
+__global__ __launch_bounds__(256) void slope_rows(const SlopeParams p)
+{
+    __shared__ float sum[8][32 * V + 1];
+    const int cx = threadIdx.x % 32, ry = threadIdx.x / 32;
+    const long tiles = (p.n + 32 * V - 1) / (32 * V), id = p.first + blockIdx.x;
+    const long c = (id % tiles * 32 + cx) * V, slice = id / tiles, b = slice / p.slices;
+    const long r1 = slice % p.slices * p.each, r2 = min(r1 + p.each, p.rows);
+    float s[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) s[j] = 0.0f;
+    if (c < p.n) {
+#pragma unroll 4
+        for (long r = r1 + ry; r < r2; r += 8) {
+            float v[V];
+            const long at = (b * p.rows + r) * p.n + c;
+            slope_of<T, V>(p, static_cast<const T *>(p.dy) + b * p.d_b + r * p.d_s + c, static_cast<const T *>(p.pre) + at,
+                           p.dz ? static_cast<T *>(p.dz) + at : nullptr, v);
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[j] += v[j];
+        }
+    }
+    if (!p.part) return;
+#pragma unroll
+    for (int j = 0; j < V; ++j) sum[ry][cx * V + j] = s[j];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * V; i += 256) {
+        const long col = id % tiles * 32 * V + i;
+        if (col >= p.n) continue;
+        float t = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t += sum[k][i];
+        p.part[slice * p.n + col] = t;
+    }
+}
+
+// Maps: a slice of one channel's cells a workgroup.
+template <typename T, int V>
+__global__ __launch_bounds__(256) void slope_maps(const SlopeParams p)
+{
+    __shared__ float sum[4];
+    const long id = p.first + blockIdx.x, c = id % p.n, slice = id / p.n, b = slice / p.slices;
+    const long r1 = slice % p.slices * p.each, r2 = min(r1 + p.each, p.rows);
+    float s = 0.0f;
+#pragma unroll 2
+    for (long r = r1 + threadIdx.x * V; r < r2; r += 256 * V) {
+        float v[V];
+        const long at = (b * p.n + c) * p.rows + r;
+        slope_of<T, V>(p, static_cast<const T *>(p.dy) + b * p.d_b + c * p.d_s + r, static_cast<const T *>(p.pre) + at,
+                       p.dz ? static_cast<T *>(p.dz) + at : nullptr, v);
+#pragma unroll
+        for (int j = 0; j < V; ++j) s += v[j];
+    }
+    if (!p.part) return;
+    s = lane_sum<64>(s);
+    if (threadIdx.x % 64 == 0) sum[threadIdx.x / 64] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) p.part[slice * p.n + c] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+}
+
+// Slices of a batch entry's rows: enough workgroups to fill the chip, and whole
+// vectors. At most 512 partial rows where the batch allows.
+void slope_slices(const ssm2d_linear_shape &a, bool maps, int *slices, long *each)
+{
+    const long tiles = maps ? a.n : (a.n + 127) / 128, unit = maps ? 2048 : 32;
+    long want = std::max(1L, std::min(2048 / std::max(1L, std::min<long>(tiles * a.batch, 2048)), std::max(1L, 512 / static_cast<long>(a.batch))));
+    want = std::min(want, static_cast<long>((a.rows + unit - 1) / unit));
+    *each = round_up_to((a.rows + want - 1) / std::max(want, 1L), 8);
+    *slices = static_cast<int>((a.rows + *each - 1) / std::max(*each, 1L));
+}
+
+template <typename T>
+int run_slope(SlopeParams p, bool maps, hipStream_t s)
+{
+    constexpr int V = 16 / static_cast<int>(sizeof(T));
+    const long inner = maps ? p.rows : p.n;
+    auto fits = [&](int v) {
+        const size_t to = v * sizeof(T);
+        return inner % v == 0 && !off_by(p.dy, to) && !off_by(p.pre, to) && !off_by(p.dz, to) && p.d_b % v == 0 && p.d_s % v == 0;
+    };
+    auto go = [&](auto vec) {
+        constexpr int W = decltype(vec)::value;
+        const long groups = p.slices * p.batch * (maps ? p.n : (p.n + 32 * W - 1) / (32 * W)), most = most_groups(256);
+        for (p.first = 0; p.first < groups; p.first += most) {
+            const dim3 grid(static_cast<unsigned>(std::min(groups - p.first, most)));
+            if (maps) slope_maps<T, W><<<grid, dim3(256), 0, s>>>(p);
+            else slope_rows<T, W><<<grid, dim3(256), 0, s>>>(p);
+            const int st = launched();
+            if (st != SSM2D_OK) return st;
+        }
+        return static_cast<int>(SSM2D_OK);
+    };
+    if (fits(V)) return go(std::integral_constant<int, V>{});
+    if constexpr (V == 8) {
+        if (fits(4)) return go(std::integral_constant<int, 4>{});
+    }
+    return go(std::integral_constant<int, 1>{});
+}
+
+// ------------------------------------------------------------------ checks
+
+constexpr uint32_t kLinearFlags = SSM2D_LINEAR_X_MAPS | SSM2D_LINEAR_Y_MAPS;
+
+int check_linear(const ssm2d_linear_shape *a, int act, uint32_t flags)
+{
+    if ((flags & ~kLinearFlags) || act < SSM2D_ACT_NONE || act > SSM2D_ACT_GELU) return SSM2D_ERR_BAD_FLAGS;
+    if (!a) return SSM2D_ERR_NULLPTR;
+    if (a->batch < 0 || a->rows < 0 || a->n < 0 || a->k < 0) return SSM2D_ERR_BAD_DIM;
+    for (const int64_t st : {a->x_stride[0], a->x_stride[1], a->r_stride[0], a->r_stride[1], a->w_stride}) {
+        if (st < 0) return SSM2D_ERR_BAD_DIM;
+        if (st >= (int64_t{1} << 40)) return SSM2D_ERR_UNSUPPORTED;
+    }
+    const int64_t most = (int64_t{1} << 31) - 256;
+    if (a->rows >= most || a->n >= most || a->k >= most || a->batch >= most) return SSM2D_ERR_UNSUPPORTED;
+    const double b = static_cast<double>(a->batch), r = static_cast<double>(a->rows), n = static_cast<double>(a->n), k = static_cast<double>(a->k);
+    for (const double t : {b * (r / 64 + 1) * (n / 64 + 1), b * (r / 64 + 1) * (k / 64 + 1), (k / 64 + 1) * (n / 64 + 1)})
+        if (t >= 2147483648.0) return SSM2D_ERR_UNSUPPORTED;
+    return SSM2D_OK;
+}
+
+// Elements of rows of `len` at strides s0 and s1 that can be read at once.
+template <typename T>
+int readable(const void *p, long len, long s0, long s1)
+{
+    for (const int v : {8, 4})
+        if (len % v == 0 && s0 % v == 0 && s1 % v == 0 && !off_by(p, std::min<size_t>(v * sizeof(T), 16))) return v;
+    return 1;
+}
+// Whether four neighbours can be accessed at once in rows of n.
+template <typename T>
+bool quads(const void *p, long n, long ld, long bs)
+{
+    return !p || (n % 4 == 0 && ld % 4 == 0 && bs % 4 == 0 && !off_by(p, 4 * sizeof(T)));
+}
+
+// The operand with index pairs (rows, len) at p, `ld` between rows, contiguous along len.
+struct Side {
+    const void *p;
+    long ld, bs;
+    bool kc;
+};
+
+template <typename T>
+int product(GemmParams &g, const Side &a, const Side &b, void *ws, hipStream_t s)
+{
+    const long kb = g.kb > 1 ? g.kb : g.batch;
+    g.a = a.p, g.a_ld = a.ld, g.a_bs = a.bs, g.b = b.p, g.b_ld = b.ld, g.b_bs = b.bs;
+    g.a_vec = readable<T>(a.p, a.kc ? g.K : g.M, a.ld, kb > 1 ? a.bs : 0);
+    g.b_vec = readable<T>(b.p, b.kc ? g.K : g.N, b.ld, kb > 1 ? b.bs : 0);
+    g.c_vec = quads<T>(g.c, g.N, g.c_ld, g.c_bs) && quads<T>(g.pre, g.N, 0, 0) && quads<T>(g.res, g.N, g.r_ld, g.batch > 1 ? g.r_bs : 0) ? 4 : 1;
+    // (a tile's offsets within 31 bits, and rows that do not lie over each other)
+    auto straight = [&](const Side &x, int vec, long len) { return vec == 8 && x.ld >= len && x.ld < (1L << 22); };
+    g.straight = sizeof(T) == 2 && straight(a, g.a_vec, a.kc ? g.K : g.M) && straight(b, g.b_vec, b.kc ? g.K : g.N);
+    return run_gemm<T>(g, a.kc, b.kc, ws, s);
+}
+
+template <typename T>
+GemmPlan plan_fwd(const ssm2d_linear_shape &a, uint32_t flags)
+{
+    return flags & SSM2D_LINEAR_Y_MAPS ? plan_gemm<T>(a.batch, a.n, a.rows, a.k, 1) : plan_gemm<T>(a.batch, a.rows, a.n, a.k, 1);
+}
+
+template <typename T>
+int64_t fwd_workspace(const ssm2d_linear_shape *a, uint32_t flags)
+{
+    const int st = check_linear(a, 0, flags);
+    if (st != SSM2D_OK) return -st;
+    if (a->batch == 0 || a->rows == 0 || a->n == 0) return 0;
+    return plan_fwd<T>(*a, flags).bytes;
+}
+
+template <typename T>
+int linear_fwd(const T *x, const T *weight, const float *bias, const T *res, T *y, T *pre, const ssm2d_linear_shape *a, int act, uint32_t flags,
+               void *ws, int64_t ws_bytes, void *stream)
+{
+    const int st = check_linear(a, act, flags);
+    if (st != SSM2D_OK) return st;
+    if (a->batch == 0 || a->rows == 0 || a->n == 0) return SSM2D_OK;
+    if ((a->k > 0 && (!x || !weight)) || !y) return SSM2D_ERR_NULLPTR;
+    if (off_by(x, sizeof(T)) || off_by(weight, sizeof(T)) || off_by(res, sizeof(T)) || off_by(y, sizeof(T)) || off_by(pre, sizeof(T)) ||
+        off_by(bias, 4) || off_by(ws, 16))
+        return SSM2D_ERR_MISALIGNED;
+    const int64_t need = plan_fwd<T>(*a, flags).bytes;
+    if (need > 0 && (!ws || ws_bytes < need)) return SSM2D_ERR_NOMEM;
+    const bool xm = flags & SSM2D_LINEAR_X_MAPS, ym = flags & SSM2D_LINEAR_Y_MAPS;
+    GemmParams g{};
+    g.batch = a->batch, g.kb = 1, g.K = static_cast<int>(a->k);
+    g.bias = bias, g.bias_m = ym, g.act = act, g.res = res, g.c = y, g.pre = pre;
+    g.r_bs = a->r_stride[0], g.r_ld = a->r_stride[1], g.c_bs = a->rows * a->n;
+    const Side w{weight, a->w_stride, 0, true}, in{x, a->x_stride[1], a->x_stride[0], !xm};
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (ym) {
+        g.M = static_cast<int>(a->n), g.N = static_cast<int>(a->rows), g.c_ld = a->rows;
+        return product<T>(g, w, in, ws, s);
+    }
+    g.M = static_cast<int>(a->rows), g.N = static_cast<int>(a->n), g.c_ld = a->n;
+    return product<T>(g, in, w, ws, s);
+}
+
+// The backward's workspace: dz, then the slices' sums or (later) the splits'.
+struct BwdPlan {
+    int slices;
+    long each;
+    int64_t dz, rest;
+    GemmPlan dx, dw;
+};
+template <typename T>
+BwdPlan plan_bwd(const ssm2d_linear_shape &a, int act, uint32_t flags)
+{
+    BwdPlan p{};
+    slope_slices(a, flags & SSM2D_LINEAR_Y_MAPS, &p.slices, &p.each);
+    p.dz = act != SSM2D_ACT_NONE ? round_up_to(a.batch * a.rows * a.n * static_cast<int64_t>(sizeof(T)), 256) : 0;
+    p.dx = flags & SSM2D_LINEAR_X_MAPS ? plan_gemm<T>(a.batch, a.k, a.rows, a.n, 1) : plan_gemm<T>(a.batch, a.rows, a.k, a.n, 1);
+    p.dw = plan_gemm<T>(1, a.n, a.k, a.rows, a.batch);
+    p.rest = std::max<int64_t>({p.dx.bytes, p.dw.bytes, p.slices * a.batch * a.n * 4});
+    return p;
+}
+
+template <typename T>
+int64_t bwd_workspace(const ssm2d_linear_shape *a, int act, uint32_t flags)
+{
+    const int st = check_linear(a, act, flags);
+    if (st != SSM2D_OK) return -st;
+    if (a->batch == 0 || a->rows == 0 || a->n == 0) return 0;
+    const BwdPlan p = plan_bwd<T>(*a, act, flags);
+    return p.dz + p.rest;
+}
+
+template <typename T>
+__global__ void clear_all(T *p, long n)
+{
+    const long i = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (i < n) p[i] = T{0};
+}
+template <typename T>
+int clear(T *p, long n, hipStream_t s)
+{
+    if (!p || n == 0) return SSM2D_OK;
+    const long most = most_groups(256) * 256;
+    for (long at = 0; at < n; at += most) {
+        const long m = std::min(most, n - at);
+        clear_all<T><<<dim3(static_cast<unsigned>((m + 255) / 256)), dim3(256), 0, s>>>(p + at, m);
+        const int st = launched();
+        if (st != SSM2D_OK) return st;
+    }
+    return SSM2D_OK;
+}
+
+template <typename T>
+int linear_bwd(const T *x, const T *weight, const T *pre, const T *dy, T *dx, T *dweight, float *dbias, const ssm2d_linear_shape *a, int act,
+               uint32_t flags, void *ws, int64_t ws_bytes, void *stream)
+{
+    int st = check_linear(a, act, flags);
+    if (st != SSM2D_OK) return st;
+    if (off_by(x, sizeof(T)) || off_by(weight, sizeof(T)) || off_by(pre, sizeof(T)) || off_by(dy, sizeof(T)) || off_by(dx, sizeof(T)) ||
+        off_by(dweight, sizeof(T)) || off_by(dbias, 4) || off_by(ws, 16))
+        return SSM2D_ERR_MISALIGNED;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const long B = a->batch, R = a->rows, n = a->n, k = a->k;
+    if (B == 0 || R == 0 || n == 0) {  // sums over nothing
+        if ((st = clear(dx, B * R * k, s)) != SSM2D_OK || (st = clear(dweight, n * k, s)) != SSM2D_OK) return st;
+        return clear(dbias, n, s);
+    }
+    if (k == 0) dx = nullptr, dweight = nullptr;
+    if (!dx && !dweight && !dbias) return SSM2D_OK;
+    if (!dy || (act != SSM2D_ACT_NONE && !pre) || (dx && !weight) || (dweight && !x)) return SSM2D_ERR_NULLPTR;
+    const BwdPlan plan = plan_bwd<T>(*a, act, flags);
+    if (!ws || ws_bytes < plan.dz + plan.rest) return SSM2D_ERR_NOMEM;
+    const bool xm = flags & SSM2D_LINEAR_X_MAPS, ym = flags & SSM2D_LINEAR_Y_MAPS;
+    void *rest = static_cast<char *>(ws) + plan.dz;
+    Side dz{dy, a->r_stride[1], a->r_stride[0], true};  // (contiguous: channels of rows, cells of maps)
+    if (act != SSM2D_ACT_NONE || dbias) {
+        SlopeParams p{};
+        p.dy = dy, p.pre = pre, p.dz = act != SSM2D_ACT_NONE && (dx || dweight) ? ws : nullptr, p.part = dbias ? static_cast<float *>(rest) : nullptr;
+        p.batch = B, p.rows = R, p.n = n, p.d_b = a->r_stride[0], p.d_s = a->r_stride[1], p.act = act, p.slices = plan.slices, p.each = plan.each;
+        if ((st = run_slope<T>(p, ym, s)) != SSM2D_OK) return st;
+        if (dbias) {
+            fold_rows<<<dim3(fold_blocks(n)), dim3(kFoldThreads), 0, s>>>(p.part, static_cast<int>(plan.slices * B), n, n, dbias);
+            if ((st = launched()) != SSM2D_OK) return st;
+        }
+        if (act != SSM2D_ACT_NONE) dz = Side{ws, ym ? R : n, R * n, true};
+    }
+    const Side in{x, a->x_stride[1], a->x_stride[0], true};
+    auto along = [](Side side, bool kc) {
+        side.kc = kc;
+        return side;
+    };
+    if (dx) {
+        GemmParams g{};
+        g.batch = B, g.kb = 1, g.K = static_cast<int>(n), g.c = dx, g.c_bs = R * k;
+        const Side w{weight, a->w_stride, 0, false};
+        if (xm) {
+            g.M = static_cast<int>(k), g.N = static_cast<int>(R), g.c_ld = R;
+            st = product<T>(g, w, along(dz, !ym), rest, s);
+        } else {
+            g.M = static_cast<int>(R), g.N = static_cast<int>(k), g.c_ld = k;
+            st = product<T>(g, along(dz, !ym), w, rest, s);
+        }
+        if (st != SSM2D_OK) return st;
+    }
+    if (dweight) {
+        GemmParams g{};
+        g.batch = 1, g.kb = static_cast<int>(B), g.K = static_cast<int>(R), g.M = static_cast<int>(n), g.N = static_cast<int>(k);
+        g.c = dweight, g.c_ld = k;
+        st = product<T>(g, along(dz, ym), along(in, xm), rest, s);
+    }
+    return st;
+}
+
+}  // namespace
+}  // namespace ssm2d_impl
+
+extern "C" {
+
+int64_t ssm2d_linear_fwd_workspace(const ssm2d_linear_shape *shape, uint32_t flags) { return ssm2d_impl::fwd_workspace<float>(shape, flags); }
+int64_t ssm2d_linear_fwd_workspace_bf16(const ssm2d_linear_shape *shape, uint32_t flags)
+{
+    return ssm2d_impl::fwd_workspace<uint16_t>(shape, flags);
+}
+int64_t ssm2d_linear_bwd_workspace(const ssm2d_linear_shape *shape, int act, uint32_t flags)
+{
+    return ssm2d_impl::bwd_workspace<float>(shape, act, flags);
+}
+int64_t ssm2d_linear_bwd_workspace_bf16(const ssm2d_linear_shape *shape, int act, uint32_t flags)
+{
+    return ssm2d_impl::bwd_workspace<uint16_t>(shape, act, flags);
+}
+
+int ssm2d_linear_fwd(const float *x, const float *weight, const float *bias, const float *residual, float *y, float *pre,
+                     const ssm2d_linear_shape *shape, int act, uint32_t flags, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    return ssm2d_impl::linear_fwd<float>(x, weight, bias, residual, y, pre, shape, act, flags, workspace, workspace_bytes, stream);
+}
+
+int ssm2d_linear_fwd_bf16(const uint16_t *x, const uint16_t *weight, const float *bias, const uint16_t *residual, uint16_t *y, uint16_t *pre,
+                          const ssm2d_linear_shape *shape, int act, uint32_t flags, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    return ssm2d_impl::linear_fwd<uint16_t>(x, weight, bias, residual, y, pre, shape, act, flags, workspace, workspace_bytes, stream);
+}
+
+int ssm2d_linear_bwd(const float *x, const float *weight, const float *pre, const float *dy, float *dx, float *dweight, float *dbias,
+                     const ssm2d_linear_shape *shape, int act, uint32_t flags, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    return ssm2d_impl::linear_bwd<float>(x, weight, pre, dy, dx, dweight, dbias, shape, act, flags, workspace, workspace_bytes, stream);
+}
+
+int ssm2d_linear_bwd_bf16(const uint16_t *x, const uint16_t *weight, const uint16_t *pre, const uint16_t *dy, uint16_t *dx, uint16_t *dweight,
+                          float *dbias, const ssm2d_linear_shape *shape, int act, uint32_t flags, void *workspace, int64_t workspace_bytes,
+                          void *stream)
+{
+    return ssm2d_impl::linear_bwd<uint16_t>(x, weight, pre, dy, dx, dweight, dbias, shape, act, flags, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -40,7 +40,7 @@ __device__ __forceinline__ float widen1(uint16_t v) { return __uint_as_float(sta
 __device__ __forceinline__ void store1(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint16_t *p, float v) { *p = static_cast<uint16_t>(bf16_pack(v, 0.0f) & 0xffffu); }
 
-// N elements of T as they lie in memory (N * sizeof(T) bytes, so aligned).
+// N elements of T as they lie in memory (N * sizeof(T) bytes, so aligned; 32 of them to 16).
 template <typename T, int N>
 struct Raw {
     static constexpr int kWords = (N * static_cast<int>(sizeof(T)) + 3) / 4;
@@ -48,7 +48,11 @@ struct Raw {
     __device__ __forceinline__ void load(const T *p)
     {
         constexpr int B = N * static_cast<int>(sizeof(T));
-        if constexpr (B == 16) {
+        if constexpr (B == 32) {
+            const uint4 t = *reinterpret_cast<const uint4 *>(p), u = *(reinterpret_cast<const uint4 *>(p) + 1);
+            w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
+            w[4] = u.x, w[5] = u.y, w[6] = u.z, w[7] = u.w;
+        } else if constexpr (B == 16) {
             const uint4 t = *reinterpret_cast<const uint4 *>(p);
             w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
         } else if constexpr (B == 8) {
@@ -64,7 +68,10 @@ struct Raw {
     __device__ __forceinline__ void store(T *p) const
     {
         constexpr int B = N * static_cast<int>(sizeof(T));
-        if constexpr (B == 16) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        if constexpr (B == 32) {
+            *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+            *(reinterpret_cast<uint4 *>(p) + 1) = make_uint4(w[4], w[5], w[6], w[7]);
+        } else if constexpr (B == 16) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
         else if constexpr (B == 8) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
         else if constexpr (B == 4) *reinterpret_cast<unsigned *>(p) = w[0];
         else *reinterpret_cast<uint16_t *>(p) = static_cast<uint16_t>(w[0]);

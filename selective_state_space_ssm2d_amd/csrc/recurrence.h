@@ -1,0 +1,770 @@
+// libssm2d: the gated linear recurrence h[t] = a[t] h[t - 1] + w[t] x[t]
+// (include/ssm2d_block.h), forward and backward, for token rows and for
+// channels-first maps.
+//
+// Memory-bound. A stretch of tokens maps a state h to P h + c, with P the
+// product of its a's, so stretches are worked on at once and joined in a fixed
+// order: a thread takes neighbouring tokens of its channels one after the other,
+// threads are joined within a wave and over the workgroup's waves, workgroups
+// through a small workspace (rec_join). A workgroup holds a chunk of tokens in
+// registers as it was read: it needs each input once where it can walk over all
+// tokens of its channels, and where there are too few channels for that (the
+// host's choice) a first launch reads the inputs for P and c alone.
+// The backward joins both ways: e[t] = dh[t] + a[t + 1] e[t + 1] is the same
+// recurrence from the end, and what flows out of a stretch, f = a e, is P f' + c'.
+// States are fp32 throughout, also in the backward, which computes them again.
+//
+// Packed sequences: a first token of a sequence does not see the one before. Its
+// stretch has P = -0: a product with it stays -0 until another cut, and joins
+// select instead of multiply there, so that no Inf or NaN of one sequence
+// reaches another.
+#pragma once
+
+#include "block_common.h"
+
+namespace ssm2d_impl {
+
+struct RecParams {
+    const void *x, *g, *dh;        // at the first token in the order of the recurrence
+    const float *h_init, *dh_last;
+    const int *cu;
+    void *h, *dx, *dg;
+    float *h_last, *dh_init;
+    float *P, *H, *F;              // [batch][segment][channel]: a segment's product and sums, then what enters it
+    long T;                        // tokens
+    long seg;                      // tokens of a segment
+    int S;                         // segments
+    long first;                    // the launch's first workgroup (a grid has less than 2^32 threads)
+    int n, n_seq, tiles;
+    long x_b, g_b, d_b, x_t, g_t, d_t;  // strides of batch and token (rows; token strides signed) or channel (maps)
+    long o_t;                      // token stride of the outputs (rows)
+};
+
+constexpr float kCut = -0.0f;
+template <bool PACKED>
+__device__ __forceinline__ bool is_cut(float p)
+{
+    return PACKED && __float_as_uint(p) == 0x80000000u;
+}
+// The stretch (P, c) after (p0, c0).
+template <bool PACKED>
+__device__ __forceinline__ void join(float p0, float c0, float &P, float &c)
+{
+    if (is_cut<PACKED>(P)) return;
+    c = fmaf(P, c0, c);
+    P = is_cut<PACKED>(p0) ? p0 : P * p0;
+}
+// The state after a stretch (P, c) entered with h.
+template <bool PACKED>
+__device__ __forceinline__ float pass(float P, float c, float h)
+{
+    return is_cut<PACKED>(P) ? c : fmaf(P, h, c);
+}
+
+// a and w of a gate; for bf16 the sigmoid's two sides share their exponential.
+template <typename T, bool SIG>
+__device__ __forceinline__ void gates(float g, float &a, float &w)
+{
+    if constexpr (SIG) {
+        // of e = exp(-|g|): 1 / (1 + e) and e / (1 + e), neither a difference
+        const float e = exp_for<T>(-fabsf(g)), r = inverse_for<T>(1.0f + e), s = e * r;
+        a = g < 0.0f ? s : r, w = g < 0.0f ? r : s;
+    } else {
+        a = exp_for<T>(g), w = 1.0f;
+    }
+}
+
+// ------------------------------------------------------------------ packed sequences
+
+// Where a token stands: its sequence (-1: none), whether it is its first, and
+// the next token at which that changes.
+struct Place {
+    int seq;
+    bool first;
+    long end, next;
+};
+__device__ __forceinline__ long cu_at(const RecParams &p, int i)
+{
+    const long v = p.cu[i];
+    return v < 0 ? 0 : (v > p.T ? p.T : v);
+}
+// (by halves at each change: any contents end, and stay within the tokens)
+__device__ __forceinline__ Place locate(const RecParams &p, long t)
+{
+    int lo = -1, hi = p.n_seq;  // cu[lo] <= t < cu[hi], as far as they ascend
+    while (hi - lo > 1) {
+        const int m = (lo + hi) / 2;
+        if (cu_at(p, m) <= t) lo = m;
+        else hi = m;
+    }
+    Place w{-1, false, -1, 0x7fffffffffffffffL};
+    if (lo < 0) {
+        w.next = cu_at(p, 0);
+    } else {
+        const long end = cu_at(p, lo + 1);
+        if (t < end) w = Place{lo, cu_at(p, lo) == t, end, end};
+    }
+    return w;
+}
+
+// ------------------------------------------------------------------ token rows
+
+template <typename T, int V, bool BWD>
+struct RowDims {
+    // 16 lanes of 4 channels (128-byte runs in bf16) by 16 (backward 32) lots of tokens; single channels where rows are odd
+    static constexpr int kBX = V == 4 ? 16 : 32, kBY = (BWD ? 512 : 256) / kBX, kThreads = kBX * kBY, kWaves = kThreads / 64;
+    static constexpr int kL = BWD ? 8 : (sizeof(T) == 2 || V == 1 ? 16 : 8), kChunk = kBY * kL;
+};
+
+// What one thread holds of a chunk: kL tokens of V channels.
+template <typename T, int V, int L>
+struct Lot {
+    Raw<T, V> x[L], g[L];
+};
+
+// Joins the threads' stretches (P, c) of a workgroup in token order: *in gets
+// the state before each thread's stretch given `carry` before the workgroup's,
+// and carry (with carryP, the product so far) moves to its end. DOWN: in reverse
+// token order. tot: LDS for this use alone until the next barrier but one.
+template <int V, int BX, int WAVES, bool PACKED, bool DOWN>
+__device__ __forceinline__ void join_lots(float (&P)[V], float (&c)[V], float (&carry)[V], float (&carryP)[V], float (&in)[V],
+                                          float (*tot)[BX * V][2])
+{
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, cx = lane % BX, sub = lane / BX;
+    constexpr int kSubs = 64 / BX;
+#pragma unroll
+    for (int d = 1; d < kSubs; d *= 2)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float p0 = DOWN ? __shfl_down(P[j], d * BX) : __shfl_up(P[j], d * BX);
+            const float c0 = DOWN ? __shfl_down(c[j], d * BX) : __shfl_up(c[j], d * BX);
+            if (DOWN ? sub + d < kSubs : sub >= d) join<PACKED>(p0, c0, P[j], c[j]);
+        }
+    if (sub == (DOWN ? 0 : kSubs - 1)) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) tot[wave][cx * V + j][0] = P[j], tot[wave][cx * V + j][1] = c[j];
+    }
+    float eP[V], ec[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        eP[j] = DOWN ? __shfl_down(P[j], BX) : __shfl_up(P[j], BX);
+        ec[j] = DOWN ? __shfl_down(c[j], BX) : __shfl_up(c[j], BX);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        float h = carry[j];
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) {
+            const int w = DOWN ? WAVES - 1 - i : i;
+            const float wP = tot[w][cx * V + j][0], wc = tot[w][cx * V + j][1];
+            if (w == wave) in[j] = h;
+            h = pass<PACKED>(wP, wc, h);
+            float p = wP, q = 0.0f;
+            join<PACKED>(carryP[j], 0.0f, p, q);
+            carryP[j] = p;
+        }
+        carry[j] = h;
+        if (sub != (DOWN ? kSubs - 1 : 0)) in[j] = pass<PACKED>(eP[j], ec[j], in[j]);
+    }
+}
+
+// What a packed token's place adds to the recurrence, for walks over a thread's tokens.
+template <bool PACKED>
+struct Walk {
+    Place at;
+    __device__ __forceinline__ void begin(const RecParams &p, long t)
+    {
+        if constexpr (PACKED) at = locate(p, t);
+    }
+    // moves on to token t (the one after the last)
+    __device__ __forceinline__ void to(const RecParams &p, long t)
+    {
+        if constexpr (PACKED) {
+            if (t >= at.next) at = locate(p, t);
+            else at.first = false;
+        }
+    }
+};
+
+// AGG: only the segment's product and state from zero, into P and H.
+template <typename T, int V, bool PACKED, bool SIG, bool AGG>
+__global__ __launch_bounds__(256) void rec_rows_fwd(const RecParams p)
+{
+    using D = RowDims<T, V, false>;
+    __shared__ float tot[2][D::kWaves][D::kBX * V][2];
+    const int cx = threadIdx.x % D::kBX, ty = threadIdx.x / D::kBX;
+    const int tile = static_cast<int>((p.first + blockIdx.x) % p.tiles);
+    const long rest = (p.first + blockIdx.x) / p.tiles;
+    const int seg = static_cast<int>(rest % p.S);
+    const long b = rest / p.S;
+    const int c0 = (tile * D::kBX + cx) * V;
+    const bool live = c0 < p.n;
+    const int c = live ? c0 : p.n - V;
+    const T *x = static_cast<const T *>(p.x) + b * p.x_b + c, *g = static_cast<const T *>(p.g) + b * p.g_b + c;
+    T *h_out = static_cast<T *>(p.h) + b * p.T * p.n + c;
+    const long t1 = static_cast<long>(seg) * p.seg, t2 = min(t1 + p.seg, p.T);
+    const long place = (b * p.S + seg) * p.n + c;
+    float carry[V], carryP[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        carryP[j] = 1.0f, carry[j] = 0.0f;
+        if (!AGG) {
+            if (p.S > 1) carry[j] = p.H[place + j];
+            else if (!PACKED && p.h_init) carry[j] = p.h_init[b * p.n + c + j];
+        }
+    }
+    Walk<PACKED> walk;
+    int buf = 0;
+    for (long t0 = t1; t0 < t2; t0 += D::kChunk, buf ^= 1) {
+        const long mine = t0 + ty * D::kL;
+        const int cnt = static_cast<int>(max(0L, min(t2 - mine, static_cast<long>(D::kL))));
+        Lot<T, V, D::kL> lot;
+#pragma unroll
+        for (int i = 0; i < D::kL; ++i) {
+            const long t = min(mine + i, t2 - 1);  // (tokens past the segment read its last, and are not used)
+            lot.x[i].load(x + t * p.x_t);
+            lot.g[i].load(g + t * p.g_t);
+        }
+        float P[V], h[V], in[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) P[j] = 1.0f, h[j] = 0.0f;
+        walk.begin(p, mine);
+        // one token on: FINAL with the true states, stored
+        auto step = [&](int i, bool final) __attribute__((always_inline)) {
+            const long t = mine + i;
+            if (i > 0) walk.to(p, t);
+            const bool out = PACKED && walk.at.seq < 0;
+            float o[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float a, w;
+                gates<T, SIG>(lot.g[i].get(j), a, w);
+                const float wx = SIG ? w * lot.x[i].get(j) : lot.x[i].get(j);
+                if (PACKED && (out || walk.at.first)) {
+                    P[j] = kCut;
+                    h[j] = out ? 0.0f : (p.h_init ? fmaf(a, p.h_init[static_cast<long>(walk.at.seq) * p.n + c + j], wx) : wx);
+                } else {
+                    if (!final && !is_cut<PACKED>(P[j])) P[j] *= a;
+                    h[j] = fmaf(a, h[j], wx);
+                }
+                o[j] = h[j];
+            }
+            if (!final || !live || out) return;
+            Raw<T, V> v;
+            v.set(o);
+            v.store(h_out + t * p.o_t);
+            if (p.h_last && (PACKED ? t + 1 == walk.at.end : t + 1 == p.T)) {
+                const long s = PACKED ? walk.at.seq : b;
+#pragma unroll
+                for (int j = 0; j < V; ++j) p.h_last[s * p.n + c + j] = o[j];
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < D::kL; ++i)
+            if (i < cnt) step(i, false);
+        join_lots<V, D::kBX, D::kWaves, PACKED, false>(P, h, carry, carryP, in, tot[buf]);
+        if (AGG) continue;
+#pragma unroll
+        for (int i = 0; i < D::kL; ++i) lot.g[i].forget();
+#pragma unroll
+        for (int j = 0; j < V; ++j) h[j] = in[j];
+        walk.begin(p, mine);
+#pragma unroll
+        for (int i = 0; i < D::kL; ++i)
+            if (i < cnt) step(i, true);
+    }
+    if (AGG && live && ty == 0) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) p.P[place + j] = carryP[j], p.H[place + j] = carry[j];
+    }
+}
+
+// A workgroup's chunk is a segment. AGG: its product, state from zero and flow from zero, into P, H and F.
+template <typename T, int V, bool PACKED, bool SIG, bool AGG>
+__global__ __launch_bounds__(512) void rec_rows_bwd(const RecParams p)
+{
+    using D = RowDims<T, V, true>;
+    constexpr int L = D::kL;
+    __shared__ float tot[2][D::kWaves][D::kBX * V][2];
+    const int cx = threadIdx.x % D::kBX, ty = threadIdx.x / D::kBX;
+    const int tile = static_cast<int>((p.first + blockIdx.x) % p.tiles);
+    const long rest = (p.first + blockIdx.x) / p.tiles;
+    const int seg = static_cast<int>(rest % p.S);
+    const long b = rest / p.S;
+    const int c0 = (tile * D::kBX + cx) * V;
+    const bool live = c0 < p.n;
+    const int c = live ? c0 : p.n - V;
+    const T *x = static_cast<const T *>(p.x) + b * p.x_b + c, *g = static_cast<const T *>(p.g) + b * p.g_b + c;
+    const T *d = static_cast<const T *>(p.dh) + b * p.d_b + c;
+    const long t1 = static_cast<long>(seg) * p.seg, t2 = min(t1 + p.seg, p.T);
+    const long place = (b * p.S + seg) * p.n + c;
+    const long mine = t1 + ty * L;
+    const int cnt = static_cast<int>(max(0L, min(t2 - mine, static_cast<long>(L))));
+    Raw<T, V> rx[L], rg[L], rd[L];
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        const long t = min(mine + i, t2 - 1);
+        rx[i].load(x + t * p.x_t);
+        rg[i].load(g + t * p.g_t);
+        rd[i].load(d + t * p.d_t);
+    }
+    float enter[V], flow[V], one[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        enter[j] = flow[j] = 0.0f;
+        if (AGG) continue;
+        if (p.S > 1) {
+            enter[j] = p.H[place + j], flow[j] = p.F[place + j];
+        } else if (!PACKED) {
+            if (p.h_init) enter[j] = p.h_init[b * p.n + c + j];
+            if (p.dh_last) flow[j] = p.dh_last[b * p.n + c + j];
+        }
+    }
+    // first tokens and last tokens of sequences among this thread's, and which are in one
+    unsigned firsts = 0, ends = 0, outs = 0;
+    int seq[L];
+    if constexpr (PACKED) {
+        Place w = locate(p, mine);
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            if (i > 0) {
+                if (mine + i >= w.next) w = locate(p, mine + i);
+                else w.first = false;
+            }
+            seq[i] = w.seq < 0 ? 0 : w.seq;
+            firsts |= (w.seq >= 0 && w.first ? 1u : 0u) << i;
+            ends |= (w.seq >= 0 && mine + i + 1 == w.end ? 1u : 0u) << i;
+            outs |= (w.seq < 0 ? 1u : 0u) << i;
+        }
+    }
+    auto first = [&](int i) { return PACKED && ((firsts >> i) & 1u); };
+    auto end = [&](int i) { return PACKED && ((ends >> i) & 1u); };
+    auto none = [&](int i) { return PACKED && ((outs >> i) & 1u); };
+    auto init_of = [&](int i, int j) { return p.h_init ? p.h_init[static_cast<long>(seq[i]) * p.n + c + j] : 0.0f; };
+    auto last_of = [&](int i, int j) { return p.dh_last ? p.dh_last[static_cast<long>(seq[i]) * p.n + c + j] : 0.0f; };
+    // the thread's stretch, forward and (f) backward
+    float P[V], h[V], f[V], in[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) P[j] = 1.0f, h[j] = 0.0f, f[j] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        if (i >= cnt) continue;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float a, w;
+            gates<T, SIG>(rg[i].get(j), a, w);
+            const float wx = SIG ? w * rx[i].get(j) : rx[i].get(j);
+            if (first(i) || none(i)) {
+                h[j] = none(i) ? 0.0f : fmaf(a, init_of(i, j), wx);
+                P[j] = kCut;
+            } else {
+                h[j] = fmaf(a, h[j], wx);
+                if (!is_cut<PACKED>(P[j])) P[j] *= a;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = L - 1; i >= 0; --i) {
+        if (i >= cnt) continue;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float a, w;
+            gates<T, SIG>(rg[i].get(j), a, w);
+            const float e = rd[i].get(j) + (end(i) ? last_of(i, j) : f[j]);
+            f[j] = first(i) || none(i) ? 0.0f : a * e;
+        }
+    }
+    float P2[V], out[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) P2[j] = P[j], one[j] = 1.0f;
+    join_lots<V, D::kBX, D::kWaves, PACKED, false>(P, h, enter, one, in, tot[0]);
+    if (AGG && live && ty == 0) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) p.P[place + j] = one[j], p.H[place + j] = enter[j];
+    }
+    join_lots<V, D::kBX, D::kWaves, PACKED, true>(P2, f, flow, one, out, tot[1]);
+    if (AGG) {
+        if (live && ty == 0) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) p.F[place + j] = flow[j];
+        }
+        return;
+    }
+    if (!live) return;
+#pragma unroll
+    for (int i = 0; i < L; ++i) rg[i].forget(), rx[i].forget();
+    // what e is to be multiplied by for dg, of each token
+    float q[L][V];
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        if (i >= cnt) continue;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float a, w;
+            gates<T, SIG>(rg[i].get(j), a, w);
+            const float xv = rx[i].get(j), before = first(i) ? init_of(i, j) : in[j];
+            q[i][j] = SIG ? a * w * (before - xv) : a * before;
+            in[j] = fmaf(a, before, SIG ? w * xv : xv);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < L; ++i) rg[i].forget();
+#pragma unroll
+    for (int i = L - 1; i >= 0; --i) {
+        if (i >= cnt) continue;
+        float dx[V], dg[V], fl[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float a, w;
+            gates<T, SIG>(rg[i].get(j), a, w);
+            const float e = rd[i].get(j) + (end(i) ? last_of(i, j) : out[j]);
+            dx[j] = SIG ? w * e : e;
+            dg[j] = q[i][j] * e;
+            fl[j] = a * e;
+            out[j] = first(i) || none(i) ? 0.0f : fl[j];
+        }
+        if (none(i)) continue;
+        const long t = mine + i, at = b * p.T * p.n + t * p.o_t + c;
+        Raw<T, V> v;
+        v.set(dx);
+        v.store(static_cast<T *>(p.dx) + at);
+        v.set(dg);
+        v.store(static_cast<T *>(p.dg) + at);
+        if (p.dh_init && (PACKED ? first(i) : t == 0)) {
+            const long s = PACKED ? seq[i] : b;
+#pragma unroll
+            for (int j = 0; j < V; ++j) p.dh_init[s * p.n + c + j] = fl[j];
+        }
+    }
+}
+
+// ------------------------------------------------------------------ maps
+
+template <typename T, int V>
+constexpr int kMapU = V == 1 ? 8 : 2;  // vectors of V tokens a lane holds
+template <typename T, int V, int WPR>
+constexpr int kMapChunk = WPR * 64 * V * kMapU<T, V>;
+
+// Inclusive join over the wave's lanes.
+__device__ __forceinline__ void wave_join(float &P, float &c)
+{
+    auto step = [&](auto ctrl, auto rows) __attribute__((always_inline)) {
+        constexpr int kCtrl = decltype(ctrl)::value, kRowMask = decltype(rows)::value;
+        const float p0 = __int_as_float(__builtin_amdgcn_update_dpp(0x3f800000, __float_as_int(P), kCtrl, kRowMask, 0xf, false));
+        const float c0 = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(c), kCtrl, kRowMask, 0xf, false));
+        c = fmaf(P, c0, c);
+        P *= p0;
+    };
+    using std::integral_constant;
+    step(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});  // row_shr:1, 2, 4, 8
+    step(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
+    step(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
+    step(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
+    step(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});  // the rows' last lanes to the next row, and to the second half
+    step(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});
+}
+__device__ __forceinline__ float lane_before(float v, float none)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(none), __float_as_int(v), 0x138, 0xf, 0xf, false));  // wave_shr:1
+}
+__device__ __forceinline__ float last_lane(float v) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63)); }
+
+// The states before each of a lane's U stretches (in token order: all lanes'
+// first, then all lanes' second) given h before the wave's; h moves to the end.
+// P, c: the stretches; they become the joined ones up to each lane.
+template <int U>
+__device__ __forceinline__ void wave_total(float (&P)[U], float (&c)[U], float &wP, float &wc)
+{
+    wP = 1.0f, wc = 0.0f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        wave_join(P[u], c[u]);
+        const float lP = last_lane(P[u]), lc = last_lane(c[u]);
+        wc = fmaf(lP, wc, lc);
+        wP *= lP;
+    }
+}
+template <int U>
+__device__ __forceinline__ void wave_states(const float (&P)[U], const float (&c)[U], float h, float (&in)[U])
+{
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const float eP = lane_before(P[u], 1.0f), ec = lane_before(c[u], 0.0f);
+        in[u] = fmaf(eP, h, ec);
+        h = fmaf(last_lane(P[u]), h, last_lane(c[u]));
+    }
+}
+
+// V tokens from place i in the order of the recurrence.
+template <typename T, int V, bool REV>
+struct Run {
+    Raw<T, V> r;
+    __device__ __forceinline__ void load(const T *row, long i, long n) { r.load(row + (REV ? n - V - i : i)); }
+    __device__ __forceinline__ float get(int j) const { return r.get(REV ? V - 1 - j : j); }
+    __device__ __forceinline__ void forget() { r.forget(); }
+};
+template <typename T, int V, bool REV>
+__device__ __forceinline__ void store_run(T *row, long i, long n, const float (&v)[V])
+{
+    float o[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) o[j] = v[REV ? V - 1 - j : j];
+    Raw<T, V> r;
+    r.set(o);
+    r.store(row + (REV ? n - V - i : i));
+}
+
+// Over the workgroup's WPR waves of one row: the state before this wave given
+// `carry` before the first; carry and its product move to the end. Every wave
+// of the workgroup calls it. DOWN: from the last wave to the first.
+template <int WPR, bool DOWN>
+__device__ __forceinline__ float join_waves(float wP, float wc, float &carry, float &carryP, float (*tot)[2])
+{
+    float in = carry;
+    if constexpr (WPR > 1) {
+        const int wave = threadIdx.x / 64;
+        if (threadIdx.x % 64 == 0) tot[wave][0] = wP, tot[wave][1] = wc;
+        __syncthreads();
+        float h = carry;
+#pragma unroll
+        for (int i = 0; i < WPR; ++i) {
+            const int w = DOWN ? WPR - 1 - i : i;
+            if (w == wave) in = h;
+            h = fmaf(tot[w][0], h, tot[w][1]);
+            carryP *= tot[w][0];
+        }
+        carry = h;
+    } else {
+        carry = fmaf(wP, carry, wc);
+        carryP *= wP;
+    }
+    return in;
+}
+
+template <typename T, int V, int WPR, bool REV, bool SIG, bool AGG>
+__global__ __launch_bounds__(256) void rec_maps_fwd(const RecParams p, long units)
+{
+    constexpr int U = kMapU<T, V>, kRowsOf = 4 / WPR, kChunk = kMapChunk<T, V, WPR>;
+    __shared__ float tot[2][4][2];
+    const int lane = threadIdx.x % 64, wave = WPR == 1 ? 0 : threadIdx.x / 64;
+    const long unit = (p.first + blockIdx.x) * kRowsOf + (WPR == 1 ? threadIdx.x / 64 : 0);
+    if (WPR == 1 && unit >= units) return;  // (whole waves, and no barrier follows)
+    const int seg = static_cast<int>(unit % p.S);
+    const long row = unit / p.S, b = row / p.n, c = row % p.n;
+    const T *x = static_cast<const T *>(p.x) + b * p.x_b + c * p.x_t, *g = static_cast<const T *>(p.g) + b * p.g_b + c * p.g_t;
+    T *h_out = static_cast<T *>(p.h) + row * p.T;
+    const long t1 = static_cast<long>(seg) * p.seg, t2 = min(t1 + p.seg, p.T);
+    const long place = (b * p.S + seg) * p.n + c;
+    float carry = 0.0f, carryP = 1.0f;
+    if (!AGG) carry = p.S > 1 ? p.H[place] : (p.h_init ? p.h_init[row] : 0.0f);
+    int buf = 0;
+    for (long t0 = t1; t0 < t2; t0 += kChunk, buf ^= 1) {
+        Run<T, V, REV> rx[U], rg[U];
+        float P[U], h[U], in[U];
+        auto at = [&](int u) { return t0 + (static_cast<long>(wave * U + u) * 64 + lane) * V; };
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long t = min(at(u), p.T - V);  // (segments end at whole vectors: V divides T or is 1)
+            rx[u].load(x, t, p.T);
+            rg[u].load(g, t, p.T);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            P[u] = 1.0f, h[u] = 0.0f;
+            if (at(u) < t2) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    float a, w;
+                    gates<T, SIG>(rg[u].get(j), a, w);
+                    h[u] = fmaf(a, h[u], SIG ? w * rx[u].get(j) : rx[u].get(j));
+                    P[u] *= a;
+                }
+            }
+        }
+        float wP, wc;
+        wave_total<U>(P, h, wP, wc);
+        const float enter = join_waves<WPR, false>(wP, wc, carry, carryP, tot[buf]);
+        if (AGG) continue;
+        wave_states<U>(P, h, enter, in);
+#pragma unroll
+        for (int u = 0; u < U; ++u) rg[u].forget();
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (at(u) >= t2) continue;
+            float o[V], v = in[u];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float a, w;
+                gates<T, SIG>(rg[u].get(j), a, w);
+                o[j] = v = fmaf(a, v, SIG ? w * rx[u].get(j) : rx[u].get(j));
+            }
+            store_run<T, V, REV>(h_out, at(u), p.T, o);
+            if (p.h_last && at(u) + V == p.T) p.h_last[row] = v;
+        }
+    }
+    if (AGG && lane == 0 && wave == 0) p.P[place] = carryP, p.H[place] = carry;
+}
+
+template <typename T, int V, int WPR, bool REV, bool SIG, bool AGG>
+__global__ __launch_bounds__(256) void rec_maps_bwd(const RecParams p, long units)
+{
+    constexpr int U = kMapU<T, V>, kRowsOf = 4 / WPR;
+    __shared__ float tot[2][4][2];
+    const int lane = threadIdx.x % 64, wave = WPR == 1 ? 0 : threadIdx.x / 64;
+    const long unit = (p.first + blockIdx.x) * kRowsOf + (WPR == 1 ? threadIdx.x / 64 : 0);
+    if (WPR == 1 && unit >= units) return;
+    const int seg = static_cast<int>(unit % p.S);
+    const long row = unit / p.S, b = row / p.n, c = row % p.n;
+    const T *x = static_cast<const T *>(p.x) + b * p.x_b + c * p.x_t, *g = static_cast<const T *>(p.g) + b * p.g_b + c * p.g_t;
+    const T *d = static_cast<const T *>(p.dh) + b * p.d_b + c * p.d_t;
+    const long t1 = static_cast<long>(seg) * p.seg, t2 = min(t1 + p.seg, p.T);
+    const long place = (b * p.S + seg) * p.n + c;
+    auto at = [&](int u) { return t1 + (static_cast<long>(wave * U + u) * 64 + lane) * V; };
+    Run<T, V, REV> rx[U], rg[U], rd[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const long t = min(at(u), p.T - V);
+        rx[u].load(x, t, p.T);
+        rg[u].load(g, t, p.T);
+        rd[u].load(d, t, p.T);
+    }
+    float enter = 0.0f, flow = 0.0f, product = 1.0f, unused = 1.0f;
+    if (!AGG) {
+        if (p.S > 1) enter = p.H[place], flow = p.F[place];
+        else enter = p.h_init ? p.h_init[row] : 0.0f, flow = p.dh_last ? p.dh_last[row] : 0.0f;
+    }
+    // each lane's stretches, forward, and backward with the lanes and stretches mirrored
+    float P[U], h[U], Q[U], f[U], in[U], out[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        P[u] = 1.0f, h[u] = 0.0f, f[u] = 0.0f;
+        if (at(u) < t2) {
+            float a[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float w;
+                gates<T, SIG>(rg[u].get(j), a[j], w);
+                h[u] = fmaf(a[j], h[u], SIG ? w * rx[u].get(j) : rx[u].get(j));
+                P[u] *= a[j];
+            }
+#pragma unroll
+            for (int j = V - 1; j >= 0; --j) f[u] = a[j] * (rd[u].get(j) + f[u]);
+        }
+    }
+    float G[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) Q[u] = __shfl(P[U - 1 - u], 63 - lane), G[u] = __shfl(f[U - 1 - u], 63 - lane);
+    float wP, wc;
+    wave_total<U>(P, h, wP, wc);
+    const float enter_w = join_waves<WPR, false>(wP, wc, enter, product, tot[0]);
+    wave_total<U>(Q, G, wP, wc);
+    const float flow_w = join_waves<WPR, true>(wP, wc, flow, unused, tot[1]);
+    if (AGG) {
+        if (lane == 0 && wave == 0) p.P[place] = product, p.H[place] = enter, p.F[place] = flow;
+        return;
+    }
+    wave_states<U>(P, h, enter_w, in);
+    wave_states<U>(Q, G, flow_w, f);
+#pragma unroll
+    for (int u = 0; u < U; ++u) out[u] = __shfl(f[U - 1 - u], 63 - lane);
+#pragma unroll
+    for (int u = 0; u < U; ++u) rg[u].forget();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (at(u) >= t2) continue;
+        float a[V], w[V], q[V], dx[V], dg[V], v = in[u], e = out[u];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            gates<T, SIG>(rg[u].get(j), a[j], w[j]);
+            const float xv = rx[u].get(j);
+            q[j] = SIG ? a[j] * w[j] * (v - xv) : a[j] * v;
+            v = fmaf(a[j], v, SIG ? w[j] * xv : xv);
+        }
+#pragma unroll
+        for (int j = V - 1; j >= 0; --j) {
+            e += rd[u].get(j);
+            dx[j] = SIG ? w[j] * e : e;
+            dg[j] = q[j] * e;
+            e *= a[j];
+        }
+        store_run<T, V, REV>(static_cast<T *>(p.dx) + row * p.T, at(u), p.T, dx);
+        store_run<T, V, REV>(static_cast<T *>(p.dg) + row * p.T, at(u), p.T, dg);
+        if (p.dh_init && at(u) == 0) p.dh_init[row] = e;
+    }
+}
+
+// ------------------------------------------------------------------ launches
+
+// How a call is cut, and which kernels run it.
+struct RecPlan {
+    bool maps, packed, sig, rev;
+    int v;    // elements read at once
+    int wpr;  // maps: waves a row
+};
+
+template <typename F>
+int rec_launch(RecParams p, long groups, int threads, F &&f)
+{
+    const long most = most_groups(threads);
+    for (p.first = 0; p.first < groups; p.first += most) {
+        f(p, dim3(static_cast<unsigned>(std::min(groups - p.first, most))));
+        const int st = launched();
+        if (st != SSM2D_OK) return st;
+    }
+    return SSM2D_OK;
+}
+
+// f(bool_constant...) for the values of some flags.
+template <typename F>
+int with_flags(F &&f)
+{
+    return f();
+}
+template <typename F, typename... B>
+int with_flags(F &&f, bool first, B... rest)
+{
+    if (first) return with_flags([&](auto... r) { return f(std::true_type{}, r...); }, rest...);
+    return with_flags([&](auto... r) { return f(std::false_type{}, r...); }, rest...);
+}
+
+template <typename T, bool BWD>
+int rec_run(const RecParams &p, const RecPlan &plan, long batch, bool agg, hipStream_t s)
+{
+    if (!plan.maps) {
+        auto go = [&](auto vec) {
+            constexpr int V = decltype(vec)::value;
+            return with_flags(
+                [&](auto packed, auto sig, auto only) {
+                    constexpr bool K = decltype(packed)::value, G = decltype(sig)::value, A = decltype(only)::value;
+                    constexpr int kThreads = RowDims<T, V, BWD>::kThreads;
+                    return rec_launch(p, batch * p.S * p.tiles, kThreads, [&](const RecParams &q, dim3 grid) {
+                        if constexpr (BWD) rec_rows_bwd<T, V, K, G, A><<<grid, dim3(kThreads), 0, s>>>(q);
+                        else rec_rows_fwd<T, V, K, G, A><<<grid, dim3(kThreads), 0, s>>>(q);
+                    });
+                },
+                plan.packed, plan.sig, agg);
+        };
+        return plan.v == 4 ? go(std::integral_constant<int, 4>{}) : go(std::integral_constant<int, 1>{});
+    }
+    const long units = batch * p.n * p.S;
+    auto go = [&](auto vec) {
+        constexpr int V = decltype(vec)::value;
+        return with_flags(
+            [&](auto wide, auto rev, auto sig, auto only) {
+                constexpr int W = decltype(wide)::value ? 4 : 1;
+                constexpr bool R = decltype(rev)::value, G = decltype(sig)::value, A = decltype(only)::value;
+                return rec_launch(p, (units * W + 3) / 4, 256, [&](const RecParams &q, dim3 grid) {
+                    if constexpr (BWD) rec_maps_bwd<T, V, W, R, G, A><<<grid, dim3(256), 0, s>>>(q, units);
+                    else rec_maps_fwd<T, V, W, R, G, A><<<grid, dim3(256), 0, s>>>(q, units);
+                });
+            },
+            plan.wpr == 4, plan.rev, plan.sig, agg);
+    };
+    if constexpr (sizeof(T) == 2) {
+        if (plan.v == 8) return go(std::integral_constant<int, 8>{});
+    }
+    return plan.v == 4 ? go(std::integral_constant<int, 4>{}) : go(std::integral_constant<int, 1>{});
+}
+
+}  // namespace ssm2d_impl

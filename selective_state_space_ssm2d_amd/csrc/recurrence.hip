@@ -1,0 +1,269 @@
+// libssm2d: the gated linear recurrence's entries: checks, how tokens are cut
+// into segments, and the join between the launches (recurrence.h has the kernels).
+#include "recurrence.h"
+
+namespace ssm2d_impl {
+
+extern template int rec_run<uint16_t, false>(const RecParams &, const RecPlan &, long, bool, hipStream_t);
+extern template int rec_run<uint16_t, true>(const RecParams &, const RecPlan &, long, bool, hipStream_t);
+extern template int rec_run<float, false>(const RecParams &, const RecPlan &, long, bool, hipStream_t);
+extern template int rec_run<float, true>(const RecParams &, const RecPlan &, long, bool, hipStream_t);
+
+namespace {
+
+// Per channel: what enters each segment, from the segments' products and sums
+// (H, and F from the last segment to the first), in place. 16 threads a channel
+// take as many segments each, then join.
+template <bool PACKED>
+__global__ __launch_bounds__(256) void rec_join(const RecParams p)
+{
+    __shared__ float sP[16][17], sc[16][17];
+    const int cx = threadIdx.x % 16, k = threadIdx.x / 16;
+    const long chan = static_cast<long>(blockIdx.x % p.tiles) * 16 + cx, b = p.first + blockIdx.x / p.tiles;
+    const bool live = chan < p.n;
+    const long base = b * p.S * p.n + (live ? chan : 0);
+    const int each = (p.S + 15) / 16, s0 = min(k * each, p.S), s1 = min(s0 + each, p.S);
+    auto at = [&](int s) { return base + static_cast<long>(s) * p.n; };
+    auto both = [&](float *buf, bool down, float enter) {
+        float P = 1.0f, c = 0.0f;
+        for (int i = s0; i < s1; ++i) {
+            const int s = down ? s1 - 1 - (i - s0) : i;
+            float q = p.P[at(s)], d = buf[at(s)];
+            join<PACKED>(P, c, q, d);
+            P = q, c = d;
+        }
+        sP[k][cx] = P, sc[k][cx] = c;
+        __syncthreads();
+        float h = enter;
+        for (int i = 0; i < (down ? 15 - k : k); ++i) h = pass<PACKED>(sP[down ? 15 - i : i][cx], sc[down ? 15 - i : i][cx], h);
+        for (int i = s0; i < s1; ++i) {
+            const int s = down ? s1 - 1 - (i - s0) : i;
+            const float q = p.P[at(s)], d = buf[at(s)];
+            if (live) buf[at(s)] = h;
+            h = pass<PACKED>(q, d, h);
+        }
+        __syncthreads();
+    };
+    both(p.H, false, !PACKED && p.h_init && live ? p.h_init[b * p.n + chan] : 0.0f);
+    if (p.F) both(p.F, true, !PACKED && p.dh_last && live ? p.dh_last[b * p.n + chan] : 0.0f);
+}
+
+// Sequences without tokens pass their state on: dst = src (NULL: zeros) for them.
+__global__ void rec_empty(const RecParams p, const float *src, float *dst)
+{
+    const long i = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (i >= static_cast<long>(p.n_seq) * p.n) return;
+    const int s = static_cast<int>(i / p.n);
+    if (cu_at(p, s + 1) <= cu_at(p, s)) dst[i] = src ? src[i] : 0.0f;
+}
+
+__global__ void copy_floats(const float *src, float *dst, long n)
+{
+    const long i = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (i < n) dst[i] = src[i];
+}
+
+constexpr uint32_t kRecFlags = SSM2D_RECUR_SIGMOID | SSM2D_RECUR_MAPS | SSM2D_RECUR_REVERSE;
+
+int check_rec(const ssm2d_recurrence_shape *a, uint32_t flags)
+{
+    if (flags & ~kRecFlags) return SSM2D_ERR_BAD_FLAGS;
+    if (!a) return SSM2D_ERR_NULLPTR;
+    if (a->n_seq > 0 && (flags & (SSM2D_RECUR_MAPS | SSM2D_RECUR_REVERSE))) return SSM2D_ERR_BAD_FLAGS;
+    if (a->batch < 0 || a->tokens < 0 || a->channels < 0 || a->n_seq < 0 || (a->n_seq > 0 && a->batch != 1)) return SSM2D_ERR_BAD_DIM;
+    for (const auto &st : {a->x_stride, a->g_stride, a->dh_stride})
+        if (st[0] < 0 || st[1] < 0) return SSM2D_ERR_BAD_DIM;
+    const int64_t most = (int64_t{1} << 31) - 65536;
+    if (a->batch >= most || a->tokens >= most || a->channels >= most || a->n_seq >= most) return SSM2D_ERR_UNSUPPORTED;
+    if (a->batch * a->channels >= (int64_t{1} << 31) || a->n_seq * a->channels >= (int64_t{1} << 38)) return SSM2D_ERR_UNSUPPORTED;
+    if (static_cast<double>(a->batch) * static_cast<double>(a->tokens) * static_cast<double>(a->channels) > 1e14) return SSM2D_ERR_UNSUPPORTED;
+    return SSM2D_OK;
+}
+
+// How many tokens a segment has (whole chunks), for vectors of v elements.
+struct Cut {
+    long seg;
+    int S, tiles, wpr;
+};
+Cut cut_tokens(const ssm2d_recurrence_shape &a, uint32_t flags, bool bf16, bool bwd, int v)
+{
+    Cut c{};
+    long chunk, groups;
+    if (flags & SSM2D_RECUR_MAPS) {
+        const long one = 64L * v * (v == 1 ? 8 : 2);  // (kMapChunk)
+        c.wpr = a.tokens <= one ? 1 : 4;
+        chunk = one * c.wpr;
+        groups = (a.batch * a.channels * c.wpr + 3) / 4;
+    } else {
+        const int bx = v == 4 ? 16 : 32, by = (bwd ? 512 : 256) / bx;  // (RowDims)
+        chunk = by * (bwd ? 8 : (bf16 || v == 1 ? 16 : 8));
+        c.tiles = static_cast<int>((a.channels + bx * v - 1) / (bx * v));
+        groups = a.batch * c.tiles;
+    }
+    const long chunks = (a.tokens + chunk - 1) / chunk;
+    // The backward has to hold what it walks over twice: a segment is a chunk.
+    // The forward walks where its channels alone make enough workgroups.
+    long segs = bwd ? chunks : (groups >= 512 ? 1 : std::min(chunks, (1024 + groups - 1) / std::max(groups, 1L)));
+    segs = std::max(segs, 1L);
+    c.seg = (chunks + segs - 1) / segs * chunk;
+    c.S = static_cast<int>((a.tokens + c.seg - 1) / std::max(c.seg, 1L));
+    return c;
+}
+
+constexpr int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+int64_t rec_workspace(const ssm2d_recurrence_shape *a, uint32_t flags, bool bf16, bool bwd)
+{
+    const int st = check_rec(a, flags);
+    if (st != SSM2D_OK) return -st;
+    if (a->batch == 0 || a->tokens == 0 || a->channels == 0) return 0;
+    int64_t bytes = 0;
+    for (const int v : {8, 4, 1}) {
+        if (v == 8 && !(bf16 && (flags & SSM2D_RECUR_MAPS))) continue;
+        const int64_t S = cut_tokens(*a, flags, bf16, bwd, v).S;
+        if (S > 1) bytes = std::max(bytes, (bwd ? 3 : 2) * a->batch * S * a->channels * 4);
+    }
+    if (a->n_seq > 0) bytes = round_up(bytes, 16) + a->n_seq * a->channels * 4;  // (a copy of a state that is written in place)
+    return bytes;
+}
+
+bool rows_by(const void *ptr, int64_t s0, int64_t s1, int v, size_t size) { return !off_by(ptr, v * size) && s0 % v == 0 && s1 % v == 0; }
+
+template <typename T, bool BWD>
+int rec_entry(const T *x, const T *g, const float *h_init, const int32_t *cu, const T *dh, const float *dh_last, T *out, T *dg, float *last,
+              const ssm2d_recurrence_shape *a, uint32_t flags, void *ws, int64_t ws_bytes, void *stream)
+{
+    // (`last`: h_last of the forward, dh_init of the backward; `state`: what an empty sequence passes on)
+    int st = check_rec(a, flags);
+    if (st != SSM2D_OK) return st;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const long B = a->batch, T_ = a->tokens, n = a->channels, states = (a->n_seq > 0 ? a->n_seq : B) * n;
+    const float *state = BWD ? dh_last : h_init;
+    if (states == 0 || (T_ == 0 && !last)) return SSM2D_OK;
+    if (off_by(h_init, 4) || off_by(dh_last, 4) || off_by(last, 4)) return SSM2D_ERR_MISALIGNED;
+    auto blocks = [](long m) { return dim3(static_cast<unsigned>((m + 255) / 256)); };
+    if ((states + 255) / 256 > most_groups(256)) return SSM2D_ERR_UNSUPPORTED;
+    if (T_ == 0) {
+        if (last == state) return SSM2D_OK;
+        if (state) copy_floats<<<blocks(states), dim3(256), 0, s>>>(state, last, states);
+        else clear_floats<<<blocks(states), dim3(256), 0, s>>>(last, states);
+        return launched();
+    }
+    if (!x || !g || !out || (BWD && (!dh || !dg)) || (a->n_seq > 0 && !cu)) return SSM2D_ERR_NULLPTR;
+    if (off_by(x, sizeof(T)) || off_by(g, sizeof(T)) || off_by(out, sizeof(T)) || off_by(dh, sizeof(T)) || off_by(dg, sizeof(T)) ||
+        off_by(ws, 16) || (a->n_seq > 0 && off_by(cu, 4)))
+        return SSM2D_ERR_MISALIGNED;
+    const int64_t need = rec_workspace(a, flags, sizeof(T) == 2, BWD);
+    if (need > 0 && (!ws || ws_bytes < need)) return SSM2D_ERR_NOMEM;
+    RecPlan plan{};
+    plan.maps = flags & SSM2D_RECUR_MAPS, plan.packed = a->n_seq > 0, plan.sig = flags & SSM2D_RECUR_SIGMOID;
+    plan.rev = flags & SSM2D_RECUR_REVERSE;
+    plan.v = 1;
+    for (const int v : {8, 4}) {
+        if (v == 8 && !(sizeof(T) == 2 && plan.maps)) continue;
+        const bool fits = (plan.maps ? T_ : n) % v == 0 && rows_by(x, a->x_stride[0], a->x_stride[1], v, sizeof(T)) &&
+                          rows_by(g, a->g_stride[0], a->g_stride[1], v, sizeof(T)) && rows_by(out, 0, 0, v, sizeof(T)) &&
+                          (!BWD || (rows_by(dh, a->dh_stride[0], a->dh_stride[1], v, sizeof(T)) && rows_by(dg, 0, 0, v, sizeof(T))));
+        if (fits) {
+            plan.v = v;
+            break;
+        }
+    }
+    const Cut c = cut_tokens(*a, flags, sizeof(T) == 2, BWD, plan.v);
+    plan.wpr = c.wpr;
+    RecParams p{};
+    p.x = x, p.g = g, p.dh = dh, p.h_init = h_init, p.dh_last = dh_last, p.cu = cu;
+    p.T = T_, p.seg = c.seg, p.S = c.S, p.n = static_cast<int>(n), p.n_seq = static_cast<int>(a->n_seq), p.tiles = c.tiles;
+    p.x_b = a->x_stride[0], p.g_b = a->g_stride[0], p.d_b = a->dh_stride[0];
+    p.x_t = a->x_stride[1], p.g_t = a->g_stride[1], p.d_t = a->dh_stride[1], p.o_t = n;
+    T *o = out, *o2 = dg;
+    if (plan.rev && !plan.maps) {  // (from the last token on)
+        p.x = x + (T_ - 1) * p.x_t, p.g = g + (T_ - 1) * p.g_t;
+        if (BWD) p.dh = dh + (T_ - 1) * p.d_t, o2 += (T_ - 1) * n;
+        o += (T_ - 1) * n;
+        p.x_t = -p.x_t, p.g_t = -p.g_t, p.d_t = -p.d_t, p.o_t = -n;
+    }
+    if (BWD) p.dx = o, p.dg = o2, p.dh_init = last;
+    else p.h = o, p.h_last = last;
+    const long plane = B * p.S * n;
+    p.P = static_cast<float *>(ws), p.H = p.P + plane, p.F = BWD ? p.H + plane : nullptr;
+    if (plan.packed && last) {
+        if (last == state) {  // other workgroups read what one writes: from a copy
+            float *copy = reinterpret_cast<float *>(static_cast<char *>(ws) + (need - states * 4));
+            copy_floats<<<blocks(states), dim3(256), 0, s>>>(state, copy, states);
+            if ((st = launched()) != SSM2D_OK) return st;
+            (BWD ? p.dh_last : p.h_init) = copy;
+        } else {
+            rec_empty<<<blocks(states), dim3(256), 0, s>>>(p, state, last);
+            if ((st = launched()) != SSM2D_OK) return st;
+        }
+    }
+    if (p.S > 1) {
+        if ((st = rec_run<T, BWD>(p, plan, B, true, s)) != SSM2D_OK) return st;
+        RecParams q = p;
+        q.tiles = static_cast<int>((n + 15) / 16);
+        const long most = std::max(1L, most_groups(256) / q.tiles);
+        for (q.first = 0; q.first < B; q.first += most) {
+            const dim3 grid(static_cast<unsigned>(std::min(B - q.first, most) * q.tiles));
+            if (plan.packed) rec_join<true><<<grid, dim3(256), 0, s>>>(q);
+            else rec_join<false><<<grid, dim3(256), 0, s>>>(q);
+            if ((st = launched()) != SSM2D_OK) return st;
+        }
+    }
+    return rec_run<T, BWD>(p, plan, B, false, s);
+}
+
+}  // namespace
+}  // namespace ssm2d_impl
+
+extern "C" {
+
+int64_t ssm2d_recurrence_fwd_workspace(const ssm2d_recurrence_shape *shape, uint32_t flags)
+{
+    return ssm2d_impl::rec_workspace(shape, flags, false, false);
+}
+int64_t ssm2d_recurrence_fwd_workspace_bf16(const ssm2d_recurrence_shape *shape, uint32_t flags)
+{
+    return ssm2d_impl::rec_workspace(shape, flags, true, false);
+}
+int64_t ssm2d_recurrence_bwd_workspace(const ssm2d_recurrence_shape *shape, uint32_t flags)
+{
+    return ssm2d_impl::rec_workspace(shape, flags, false, true);
+}
+int64_t ssm2d_recurrence_bwd_workspace_bf16(const ssm2d_recurrence_shape *shape, uint32_t flags)
+{
+    return ssm2d_impl::rec_workspace(shape, flags, true, true);
+}
+
+int ssm2d_recurrence_fwd(const float *x, const float *g, const float *h_init, const int32_t *cu_seqlens, float *h, float *h_last,
+                         const ssm2d_recurrence_shape *shape, uint32_t flags, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    return ssm2d_impl::rec_entry<float, false>(x, g, h_init, cu_seqlens, nullptr, nullptr, h, nullptr, h_last, shape, flags, workspace,
+                                               workspace_bytes, stream);
+}
+
+int ssm2d_recurrence_fwd_bf16(const uint16_t *x, const uint16_t *g, const float *h_init, const int32_t *cu_seqlens, uint16_t *h,
+                              float *h_last, const ssm2d_recurrence_shape *shape, uint32_t flags, void *workspace, int64_t workspace_bytes,
+                              void *stream)
+{
+    return ssm2d_impl::rec_entry<uint16_t, false>(x, g, h_init, cu_seqlens, nullptr, nullptr, h, nullptr, h_last, shape, flags, workspace,
+                                                  workspace_bytes, stream);
+}
+
+int ssm2d_recurrence_bwd(const float *x, const float *g, const float *h_init, const int32_t *cu_seqlens, const float *dh,
+                         const float *dh_last, float *dx, float *dg, float *dh_init, const ssm2d_recurrence_shape *shape, uint32_t flags,
+                         void *workspace, int64_t workspace_bytes, void *stream)
+{
+    return ssm2d_impl::rec_entry<float, true>(x, g, h_init, cu_seqlens, dh, dh_last, dx, dg, dh_init, shape, flags, workspace,
+                                              workspace_bytes, stream);
+}
+
+int ssm2d_recurrence_bwd_bf16(const uint16_t *x, const uint16_t *g, const float *h_init, const int32_t *cu_seqlens, const uint16_t *dh,
+                              const float *dh_last, uint16_t *dx, uint16_t *dg, float *dh_init, const ssm2d_recurrence_shape *shape,
+                              uint32_t flags, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    return ssm2d_impl::rec_entry<uint16_t, true>(x, g, h_init, cu_seqlens, dh, dh_last, dx, dg, dh_init, shape, flags, workspace,
+                                                 workspace_bytes, stream);
+}
+
+}  // extern "C"

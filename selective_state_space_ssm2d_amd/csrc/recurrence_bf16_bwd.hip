@@ -1,0 +1,8 @@
+// libssm2d: the gated linear recurrence, backward, bf16.
+#include "recurrence.h"
+
+namespace ssm2d_impl {
+
+template int rec_run<uint16_t, true>(const RecParams &, const RecPlan &, long, bool, hipStream_t);
+
+}  // namespace ssm2d_impl

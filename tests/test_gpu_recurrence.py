@@ -1,0 +1,314 @@
+"""GPU tests of the gated linear recurrence (include/ssm2d_block.h) against 64
+bits, token by token.
+
+Bars. With every term by its magnitude the recurrence gives H[t] = a H[t-1] + |w x|
+(and E the adjoint's). A gate a errs by at most (6 + 2 |g|) 2^-24 of itself (exp's
+argument rounds, then exp, a sum and an inverse), w alike; a step rounds twice;
+joins over lanes, waves and segments (at most 6 + 8 + 32 levels) round H once
+more each, and a stretch's product carries its a's errors and roundings beside
+its sum's. So the error follows e[t] = a e[t-1] + (12 + 4 |g|) 2^-24 (a H[t-1] + |w x|), and the
+joins add 64 2^-24 H. dg = a h e (w) multiplies two such. bf16 outputs round once, 2^-8."""
+import pytest
+
+import selective_state_space_ssm2d_amd as pkg
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _randn(shape, dtype, seed):
+    return torch.randn(*shape, generator=_gen(seed), device="cuda").to(DT[dtype])
+
+
+def _half(v, dtype):
+    return v.abs() * (2.0 ** -8 if dtype == torch.bfloat16 else U)
+
+
+def _near(got, want, bar, what):
+    bad = ~((got.double() - want).abs() <= bar + 1e-30)
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()}, worst {((got.double() - want).abs() / (bar + 1e-30)).max().item():.2f} bars"
+
+
+def make(batch, tokens, n, dtype, seed, maps=False, sig=False, lens=None, state=True):
+    shape = (batch, n, tokens) if maps else (batch, tokens, n)
+    z = 2 * torch.randn(*shape, generator=_gen(seed), device="cuda") + 2
+    g = (z if sig else -torch.nn.functional.softplus(-z)).to(DT[dtype])
+    seqs = len(lens) if lens else batch
+    cu = None
+    if lens:
+        cu = torch.tensor([sum(lens[:i]) for i in range(len(lens) + 1)], dtype=torch.int32, device="cuda")
+    s = {"x": _randn(shape, dtype, seed + 1), "g": g, "dh": _randn(shape, dtype, seed + 2), "cu": cu, "lens": lens}
+    s["h_init"], s["dh_last"] = (_randn((seqs, n), "f32", seed + i) if state else None for i in (3, 4))
+    return s
+
+
+def reference(s, sig, maps, rev):
+    """{output: (values, bar without the rounding)}, the loop over tokens in 64 bits on the CPU."""
+    order = lambda t: (t.transpose(1, 2) if maps else t).double().cpu()  # noqa: E731  [batch, tokens, n]
+    x, g, d = (order(s[k]) for k in ("x", "g", "dh"))
+    if rev:
+        x, g, d = (t.flip(1) for t in (x, g, d))
+    a, w = (torch.sigmoid(g), torch.sigmoid(-g)) if sig else (torch.exp(g), torch.ones_like(g))
+    B, T, n = x.shape
+    zero = torch.zeros(len(s["lens"]) if s["lens"] else B, n, dtype=torch.float64)
+    h0 = s["h_init"].double().cpu() if s["h_init"] is not None else zero
+    f0 = s["dh_last"].double().cpu() if s["dh_last"] is not None else zero
+    rel = (12 + 4 * g.abs().nan_to_num(0, 0, 0)) * U
+    out = {k: torch.zeros_like(x) for k in ("h", "H", "hb", "prev", "Prev", "pb", "e", "E", "eb")}
+    h_last, H_last, hb_last, f_first, F_first, fb_first = (torch.zeros_like(zero) for _ in range(6))
+    parts = [(j, slice(j, j + 1), range(B)[0:1], lo, lo + t) for j, (lo, t) in enumerate(zip([sum(s["lens"][:i]) for i in range(len(s["lens"]))], s["lens"]))] \
+        if s["lens"] else [(slice(0, B), slice(0, B), None, 0, T)]
+    for which, st, _, lo, hi in parts:
+        rows = slice(0, B)
+        h, H, hb = h0[st], h0[st].abs(), torch.zeros_like(h0[st])
+        for t in range(lo, hi):
+            at, wx, r = a[rows, t], w[rows, t] * x[rows, t], rel[rows, t]
+            out["prev"][rows, t], out["Prev"][rows, t], out["pb"][rows, t] = h, H, hb
+            hb = at * hb + r * (at * H + wx.abs())
+            h, H = at * h + wx, at * H + wx.abs()
+            out["h"][rows, t], out["H"][rows, t], out["hb"][rows, t] = h, H, hb
+        h_last[st], H_last[st], hb_last[st] = h, H, hb
+        f, F, fb = f0[st], f0[st].abs(), torch.zeros_like(f0[st])
+        for t in reversed(range(lo, hi)):
+            at, r = a[rows, t], rel[rows, t]
+            e, E, eb = d[rows, t] + f, d[rows, t].abs() + F, fb + U * (d[rows, t].abs() + F)
+            out["e"][rows, t], out["E"][rows, t], out["eb"][rows, t] = e, E, eb
+            f, F, fb = at * e, at * E, at * eb + r * at * E
+        f_first[st], F_first[st], fb_first[st] = f, F, fb
+    o = out
+    hb, eb, pb = o["hb"] + 64 * U * o["H"], o["eb"] + 64 * U * o["E"], o["pb"] + 64 * U * o["Prev"]
+    inner, Inner, ib = (w * (o["prev"] - x), w * (o["Prev"] + x.abs()), w * (pb + U * (o["Prev"] + x.abs()))) if sig else (o["prev"], o["Prev"], pb)
+    back = lambda t: ((t.flip(1) if rev else t).transpose(1, 2) if maps else (t.flip(1) if rev else t)).cuda()  # noqa: E731
+    res = {"h": (back(o["h"]), back(hb)), "dx": (back(w * o["e"]), back(w * (eb + rel * o["E"]))),
+           "dg": (back(a * inner * o["e"]), back(a * (ib * o["E"] + Inner * eb + 4 * rel * Inner * o["E"]))),
+           "h_last": (h_last.cuda(), (hb_last + 64 * U * H_last).cuda()), "dh_init": (f_first.cuda(), (fb_first + 64 * U * F_first).cuda())}
+    return res
+
+
+def check(s, sig=False, maps=False, rev=False, what=""):
+    args = dict(gates="sigmoid" if sig else "decay", h_init=s["h_init"], cu_seqlens=s["cu"], channels_first=maps, reverse=rev)
+    h, last = pkg.recurrence_fwd(s["x"], s["g"], return_last_state=True, **args)
+    got = {"h": h, "h_last": last, **pkg.recurrence_bwd(s["x"], s["g"], s["dh"], dh_last=s["dh_last"], **args)}
+    want = reference(s, sig, maps, rev)
+    assert s["h_init"] is None or "dh_init" in got
+    for name, t in got.items():
+        v, bar = want[name]
+        _near(t, v, bar + _half(v, t.dtype), f"{what} {name}")
+    return got
+
+
+TOKENS = [1, 2, 7, 8, 9, 15, 16, 17, 63, 64, 65, 127, 128, 129, 255, 256, 257, 300, 511, 513, 1000]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("sig", [False, True])
+@pytest.mark.parametrize("tokens", TOKENS)
+def test_rows(tokens, sig, dtype):
+    check(make(2, tokens, 72, dtype, tokens, sig=sig), sig, what=f"{tokens} tokens")
+    check(make(1, tokens, 37, dtype, tokens, sig=sig, state=False), sig, rev=True, what=f"{tokens} tokens reversed")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("sig", [False, True])
+@pytest.mark.parametrize("tokens", [1, 3, 4, 8, 49, 64, 196, 200, 256, 511, 512, 513, 1023, 1024, 1028, 2048, 2052, 4096, 4104, 5000, 5001])
+def test_maps(tokens, sig, dtype):
+    check(make(2, tokens, 3, dtype, tokens, maps=True, sig=sig), sig, True, what=f"{tokens} cells")
+    check(make(1, tokens, 5, dtype, tokens, maps=True, sig=sig, state=False), sig, True, rev=True, what=f"{tokens} cells reversed")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 31, 32, 33, 63, 64, 65, 100, 128, 200])
+def test_channels(n, dtype):
+    check(make(3, 150, n, dtype, n), what=f"{n} channels")
+    check(make(3, 150, n, dtype, n, maps=True), maps=True, what=f"{n} channels of maps")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("sig", [False, True])
+def test_walks_over_chunks(sig, dtype):
+    """So many channels that a workgroup walks over all tokens of its own."""
+    check(make(70, 700, 512, dtype, 1, sig=sig), sig, what="rows")
+    check(make(6, 9000, 100, dtype, 2, maps=True, sig=sig), sig, True, what="maps")
+    check(make(6, 9001, 100, dtype, 2, maps=True, sig=sig), sig, True, rev=True, what="odd maps reversed")
+    check(make(33, 400, 520, dtype, 3, sig=sig), sig, rev=True, what="rows reversed")
+
+
+PACKED = [[1], [5, 0, 3], [0, 0, 7, 1, 0], [64, 64, 64], [100, 1, 1, 1, 500, 0, 33], [256, 256, 1], [1] * 40, [700, 0, 900], [16] * 20, [15, 17, 16, 1, 128, 129]]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [72, 37])
+@pytest.mark.parametrize("lens", PACKED, ids=lambda v: f"{len(v)}of{sum(v)}")
+def test_packed(lens, n, dtype):
+    check(make(1, sum(lens), n, dtype, sum(lens), lens=lens, sig=n == 72), n == 72, what=str(lens))
+    check(make(1, sum(lens), n, dtype, sum(lens), lens=lens, state=False), what=str(lens))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_packed_equals_each_alone(dtype):
+    """What one sequence holds, Inf and NaN too, says nothing to another."""
+    lens = [300, 1, 0, 270, 45]
+    s = make(1, sum(lens), 64, dtype, 3, lens=lens)
+    clean = check(s)
+    for at, v in ((299, float("nan")), (10, float("inf")), (300, float("-inf"))):
+        t = dict(s, x=s["x"].clone(), dh=s["dh"].clone())
+        t["x"][0, at] = v
+        t["dh"][0, at] = v
+        args = dict(cu_seqlens=s["cu"], h_init=s["h_init"])
+        h, last = pkg.recurrence_fwd(t["x"], t["g"], return_last_state=True, **args)
+        got = {"h": h, **pkg.recurrence_bwd(t["x"], t["g"], t["dh"], dh_last=s["dh_last"], **args)}
+        j = 0 if at < 300 else 1
+        other = torch.ones(sum(lens), dtype=torch.bool, device="cuda")
+        other[(0, 300)[j]:(300, 301)[j]] = False
+        for name in ("h", "dx", "dg"):
+            assert torch.equal(got[name][0, other], clean[name][0, other]), (name, at)
+        keep = [i for i in range(5) if i != j]
+        assert torch.equal(last[keep], clean["h_last"][keep]) and torch.equal(got["dh_init"][keep], clean["dh_init"][keep])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_behind_the_last_sequence_are_left(dtype):
+    lens = [40, 0, 300]
+    s = make(1, 600, 64, dtype, 4, lens=lens)
+    for t in (s["x"], s["g"], s["dh"]):
+        t[0, 340:] = float("nan")
+    s["cu"] = torch.tensor([0, 40, 40, 340], dtype=torch.int32, device="cuda")
+    short = dict(s, **{k: s[k][:, :340].contiguous() for k in ("x", "g", "dh")})
+    args = dict(cu_seqlens=s["cu"], h_init=s["h_init"])
+    h = torch.full_like(s["x"], 7)
+    out = {k: torch.full_like(s["x"], 7) for k in ("dx", "dg")}
+    _, last = pkg.recurrence_fwd(s["x"], s["g"], h=h, return_last_state=True, **args)
+    g = pkg.recurrence_bwd(s["x"], s["g"], s["dh"], dh_last=s["dh_last"], out=out, **args)
+    want = check(short)
+    _near(last, want["h_last"].double(), 1e-4 * (1 + want["h_last"].double().abs()), "last")  # (another cut of the same sums)
+    for t, name in ((h, "h"), (g["dx"], "dx"), (g["dg"], "dg")):
+        assert (t[0, 340:] == 7).all(), name
+        assert torch.isfinite(t[0, :340]).all(), name
+    # offsets that start late
+    s["cu"] = torch.tensor([100, 340], dtype=torch.int32, device="cuda")
+    h.fill_(7)
+    pkg.recurrence_fwd(s["x"], s["g"], h=h, cu_seqlens=s["cu"], h_init=s["h_init"][:1])
+    assert (h[0, :100] == 7).all() and (h[0, 340:] == 7).all() and torch.isfinite(h[0, 100:340]).all()
+
+
+def test_any_offsets_are_safe():
+    """Offsets out of range or out of order give some result, within the tensors."""
+    s = make(1, 500, 48, "f32", 5, lens=[500])
+    guard = torch.full((3, 500, 48), 7.0, device="cuda")
+    for cu in ([-5, 200, 900], [300, 100, 400], [500, 0, 500], [0, 2 ** 31 - 1, -2 ** 31], [0, 0, 0], [500, 500, 500], [7, 7, 7]):
+        c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        st = _randn((2, 48), "f32", 6)
+        pkg.recurrence_fwd(s["x"], s["g"], cu_seqlens=c, h_init=st, h=guard[1:2], return_last_state=True)
+        pkg.recurrence_bwd(s["x"], s["g"], s["dh"], cu_seqlens=c, h_init=st, dh_last=st, out={"dx": guard[1:2]})
+        torch.cuda.synchronize()
+        assert (guard[0] == 7).all() and (guard[2] == 7).all(), cu
+    a = pkg.recurrence_fwd(s["x"], s["g"], cu_seqlens=torch.tensor([-9, 200, 1 << 30], dtype=torch.int32, device="cuda"))
+    b = pkg.recurrence_fwd(s["x"], s["g"], cu_seqlens=torch.tensor([0, 200, 500], dtype=torch.int32, device="cuda"))
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("maps", [False, True])
+@pytest.mark.parametrize("sig", [False, True])
+def test_gates_at_their_ends(sig, maps, dtype):
+    """Decays of 0 (which clear the state) and of 1, and gates beyond exp's range."""
+    s = make(2, 300, 8, dtype, 6, maps=maps, sig=sig)
+    inf = float("inf")
+    vals = [-inf, -100.0, -88.0, 0.0] + ([inf, 100.0, 30.0] if sig else [0.01])
+    flat = s["g"].view(-1)
+    flat[:: 13] = torch.tensor(vals, device="cuda").to(DT[dtype])[torch.arange(flat[::13].numel(), device="cuda") % len(vals)]
+    check(s, sig, maps, what="ends")
+    check(s, sig, maps, rev=True, what="ends reversed")
+    # a decay of 0 takes an Inf to NaN, and then stays; what comes before is not touched
+    t = dict(s, x=s["x"].clone())
+    (t["x"][0, 2] if maps else t["x"][0, :, 2])[150] = float("nan")
+    args = dict(gates="sigmoid" if sig else "decay", channels_first=maps)
+    a, b = pkg.recurrence_fwd(s["x"], s["g"], **args), pkg.recurrence_fwd(t["x"], s["g"], **args)
+    a, b = (v[0, 2] if maps else v[0, :, 2] for v in (a, b))
+    assert torch.equal(a[:150], b[:150]) and torch.isnan(b[150:]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_strides(dtype):
+    big = make(4, 320, 200, dtype, 7, sig=True)
+    for lo, n in ((0, 64), (8, 100), (3, 50), (4, 96)):
+        cut = {k: big[k][:, :, lo:lo + n] for k in ("x", "g", "dh")}
+        st = {k: big[k][:, lo:lo + n].contiguous() for k in ("h_init", "dh_last")}
+        check(dict(big, **cut, **st), True, what=f"from {lo}")
+        every = {k: v[::2, ::3] for k, v in cut.items()}
+        check(dict(big, **every, **{k: v[::2].contiguous() for k, v in st.items()}), True, rev=True, what=f"every third token from {lo}")
+    maps = make(4, 320, 20, dtype, 8, maps=True)
+    check(dict(maps, **{k: maps[k][1:3, 2:13] for k in ("x", "g", "dh")}, **{k: maps[k][1:3, 2:13].contiguous() for k in ("h_init", "dh_last")}), maps=True,
+          what="channels of maps")
+    one = dict(big, g=big["g"][:1].expand(4, 320, 200))
+    check(one, True, what="gates shared by the batch")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("gates", ["decay", "sigmoid"])
+@pytest.mark.parametrize("batch,n", [(1, 1), (1, 768), (3, 37), (128, 1536), (257, 40)])
+def test_step_is_the_recurrence(batch, n, gates, dtype):
+    s = make(batch, 5, n, dtype, 9, sig=gates == "sigmoid")
+    h, last = pkg.recurrence_fwd(s["x"], s["g"], gates=gates, h_init=s["h_init"], return_last_state=True)
+    state = s["h_init"].clone()
+    for t in range(5):
+        o = pkg.recurrence_step(s["x"][:, t], s["g"][:, t], state, gates=gates)
+        _near(o, h[:, t].double(), 1e-5 * (1 + h[:, t].double().abs()) + 2 * _half(h[:, t].double(), o.dtype), "step")
+    _near(state, last.double(), 1e-5 * (1 + last.double().abs()), "state")
+
+
+def test_states_in_place():
+    for lens, b, t in ((None, 2, 900), (None, 2, 60), ([400, 0, 500, 1], 1, 901), ([20, 0, 30], 1, 50)):
+        s = make(b, t, 64, "f32", 10, lens=lens)
+        h, last = pkg.recurrence_fwd(s["x"], s["g"], h_init=s["h_init"], cu_seqlens=s["cu"], return_last_state=True)
+        st = s["h_init"].clone()
+        h2 = pkg.recurrence_fwd(s["x"], s["g"], h_init=st, cu_seqlens=s["cu"], h_last=st)
+        assert torch.equal(h, h2) and torch.equal(st, last)
+        g = pkg.recurrence_bwd(s["x"], s["g"], s["dh"], h_init=s["h_init"], dh_last=s["dh_last"], cu_seqlens=s["cu"])
+        st = s["dh_last"].clone()
+        g2 = pkg.recurrence_bwd(s["x"], s["g"], s["dh"], h_init=s["h_init"], dh_last=st, cu_seqlens=s["cu"], out={"dh_init": st})
+        assert all(torch.equal(g[k], g2[k]) for k in g) and g2["dh_init"] is st
+
+
+def test_empty():
+    x = torch.zeros(2, 0, 5, device="cuda")
+    st = torch.randn(2, 5, device="cuda")
+    h, last = pkg.recurrence_fwd(x, x, h_init=st, return_last_state=True)
+    assert h.shape == x.shape and torch.equal(last, st)
+    assert not pkg.recurrence_fwd(x, x, return_last_state=True, h_last=torch.ones_like(st))[1].any()
+    assert torch.equal(pkg.recurrence_bwd(x, x, x, dh_last=st)["dh_init"], st)
+    assert pkg.recurrence_fwd(torch.zeros(0, 4, 5, device="cuda"), torch.zeros(0, 4, 5, device="cuda")).shape == (0, 4, 5)
+    assert pkg.recurrence_fwd(torch.zeros(2, 0, 5, device="cuda"), torch.zeros(2, 0, 5, device="cuda"), channels_first=True).shape == (2, 0, 5)
+    y = torch.zeros(1, 0, 5, device="cuda")
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    assert torch.equal(pkg.recurrence_fwd(y, y, cu_seqlens=cu, h_init=st, return_last_state=True)[1], st)
+
+
+@pytest.mark.parametrize("sig", [False, True])
+@pytest.mark.parametrize("maps", [False, True])
+def test_gradients_against_differences(maps, sig):
+    s = make(2, 6, 3, "f32", 11, maps=maps, sig=sig)
+    g = pkg.recurrence_bwd(s["x"], s["g"], s["dh"], gates="sigmoid" if sig else "decay", h_init=s["h_init"], dh_last=s["dh_last"], channels_first=maps)
+
+    def loss(v):
+        t = {**s, **v}
+        r = reference({**t, "x": t["x"], "g": t["g"]}, sig, maps, False)
+        return (r["h"][0] * s["dh"].double()).sum() + (r["h_last"][0] * s["dh_last"].double()).sum()
+
+    for k, name in (("x", "dx"), ("g", "dg"), ("h_init", "dh_init")):
+        d, h = torch.randn(s[k].shape, generator=_gen(12), device="cuda").double(), 1e-6
+        slope = (loss({k: s[k].double() + h * d}) - loss({k: s[k].double() - h * d})) / (2 * h)
+        got = g[name].double() * d
+        assert abs(got.sum() - slope) <= 1e-5 * got.abs().sum() + 1e-7, name
+
+
+def test_deterministic():
+    s = make(1, 20000, 96, "bf16", 13)
+    a, b = (pkg.recurrence_bwd(s["x"], s["g"], s["dh"]) for _ in range(2))
+    assert all(torch.equal(a[k], b[k]) for k in a)
