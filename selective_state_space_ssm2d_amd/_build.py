@@ -23,7 +23,8 @@ SOURCES = ["ssm2d.hip"] + [f"scan2d_{t}_{v}.hip" for t in ("f32", "bf16") for v 
 SOURCES += ["layer_norm.hip", "rope.hip", "delta.hip", "delta_step.hip",
             "delta_chunk_bf16.hip", "delta_chunk_bf16_bwd.hip", "delta_chunk_f32.hip", "delta_chunk_f32_bwd.hip"]
 # the operators of a recurrent block
-SOURCES += ["block_norm.hip", "linear.hip", "linear_bf16.hip", "linear_f32.hip", "recurrence.hip", "recurrence_bf16.hip",
+SOURCES += ["block_norm.hip", "block_norm_f32.hip", "block_norm_f32_bwd.hip", "block_norm_bf16.hip", "block_norm_bf16_bwd.hip",
+            "block_norm_bf16_f32.hip", "block_norm_bf16_f32_bwd.hip", "linear.hip", "linear_bf16.hip", "linear_f32.hip", "recurrence.hip", "recurrence_bf16.hip",
             "recurrence_bf16_bwd.hip", "recurrence_f32.hip", "recurrence_f32_bwd.hip"]
 LIB = os.path.join(PKG, "libssm2d.so")
 INCLUDE = os.path.join(ROOT, "include")

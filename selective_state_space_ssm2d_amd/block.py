@@ -26,12 +26,12 @@ before it is the caller's.
 from __future__ import annotations
 
 import ctypes
-import functools
+import operator
 
 import torch
 
-from . import OK, Ssm2dError, load_library
-from .ops import _f32, _like, _new, _norm_layout, _on_gpu, _out, _ptr, _run
+from . import ERR_HIP, OK, Ssm2dError, load_library
+from .ops import _f32, _new, _norm_layout, _on_gpu, _out, _raw_stream
 
 __all__ = ["linear_fwd", "linear_bwd", "block_norm_fwd", "block_norm_bwd", "recurrence_fwd", "recurrence_bwd", "recurrence_step"]
 
@@ -102,10 +102,6 @@ def _bytes(name, dtype, *args):
     return n
 
 
-def _workspace(n, dev, stream):
-    return _new((n,), torch.uint8, dev, stream) if n else None
-
-
 def _gpu(t, name="x"):
     if t.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"{name} must be float32 or bfloat16")
@@ -114,16 +110,56 @@ def _gpu(t, name="x"):
     return t.device
 
 
+# What a call's checks come to depends on its tensors' shapes, strides, types and
+# devices alone: it is kept by those, and the next call of the kind pays for
+# reading them (half of one token's call otherwise: 12 of 22 us of host time).
+_plans = {}
+
+
+def _meta(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+def _keep(key, plan):
+    if len(_plans) >= 4096:
+        _plans.clear()
+    _plans[key] = plan
+    return plan
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _launch(fn, index, stream, args):
+    """Calls fn(*args, stream) with device ``index`` current; a status becomes an exception."""
+    handle = stream.cuda_stream if stream is not None else _raw_stream(index)
+    if _current_device() == index:
+        s = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            s = fn(*args, handle)
+    if s != OK:
+        raise Ssm2dError(s, fn.__name__ + (f" ({load_library().ssm2d_last_hip_error().decode()})" if s == ERR_HIP else ""))
+
+
+def _make(name, t, shape, dtype, like, stream):
+    """An output: given, or allocated on the device of ``like``."""
+    if t is None and stream is None:
+        return torch.empty_like(like) if dtype is like.dtype and like.shape == shape and like.is_contiguous() else like.new_empty(shape, dtype=dtype)
+    return _out(name, t, shape, dtype, like.device, stream)
+
+
+def _workspace(n, like, stream):
+    if not n:
+        return None
+    return like.new_empty(n, dtype=torch.uint8) if stream is None else _new((n,), torch.uint8, like.device, stream)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
 # ------------------------------------------------------------------ linear
-
-@functools.lru_cache(maxsize=256)
-def _linear_shape(batch, rows, n, k, xs, rs, ws, dtype, act, flags, bwd):
-    """(the C shape, the workspace's bytes)"""
-    s = _LinearShape(batch, rows, n, k, xs, rs, ws)
-    if bwd:
-        return s, _bytes("ssm2d_linear_bwd_workspace", dtype, s, act, flags)
-    return s, _bytes("ssm2d_linear_fwd_workspace", dtype, s, flags)
-
 
 def _linear_layout(t, maps, by_batch, name):
     """(batch, rows, channels, (batch stride, row or channel stride)) of rows or maps."""
@@ -140,34 +176,47 @@ def _linear_layout(t, maps, by_batch, name):
     return 1, rows, c, (0, sr)
 
 
-def _linear(x, weight, act, channels_first, out_channels_first):
-    """Checks shared by both directions: (device, act, flags, layout of x, n, weight's stride, shape of y, layout of a tensor like y)."""
-    dev = _gpu(x)
-    if act not in ACTS:
+def _act(act):
+    if act is not None and not isinstance(act, str) or act not in ACTS:
         raise ValueError(f"act must be one of {[a for a in ACTS if a]} or None")
-    if out_channels_first is None:
-        out_channels_first = channels_first
+    return ACTS[act]
+
+
+def _linear_plan(bwd, x, weight, bias, res, pre, a, cf, ocf):
+    """(C entry, device index, C shape, flags, workspace bytes, n, y's shape) of a call's checked tensors; res: the residual, or dy."""
+    dev = _gpu(x)
     if weight.dim() != 2 or weight.dtype != x.dtype:
         raise ValueError("weight must be [n, k] of x's dtype")
     if weight.shape[1] > 1 and weight.stride(1) != 1:
         raise ValueError("the rows of weight must be contiguous")
-    mixed = channels_first or out_channels_first
-    batch, rows, k, xs = _linear_layout(x, channels_first, mixed, "x")
+    batch, rows, k, xs = _linear_layout(x, cf, cf or ocf, "x")
     n = weight.shape[0]
     if weight.shape[1] != k:
         raise ValueError(f"x has {k} channels, weight takes {weight.shape[1]}")
-    if channels_first:
-        shape = (batch, n) + tuple(x.shape[2:]) if out_channels_first else (batch, rows, n)
+    if cf:
+        shape = (batch, n) + tuple(x.shape[2:]) if ocf else (batch, rows, n)
     else:
-        shape = (batch, n, rows) if out_channels_first else tuple(x.shape[:-1]) + (n,)
-    flags = (LINEAR_X_MAPS if channels_first else 0) | (LINEAR_Y_MAPS if out_channels_first else 0)
-
-    def like_y(t, name):
-        if tuple(t.shape) != shape or t.dtype != x.dtype:
+        shape = (batch, n, rows) if ocf else tuple(x.shape[:-1]) + (n,)
+    shape, rs = torch.Size(shape), (0, 0)
+    if res is not None:
+        name = "dy" if bwd else "residual"
+        if res.shape != shape or res.dtype != x.dtype:
             raise ValueError(f"{name} must be {x.dtype} {list(shape)}")
-        return _linear_layout(t, out_channels_first, mixed, name)[3]
-
-    return dev, ACTS[act], flags, (batch, rows, k, xs), n, weight.stride(0), shape, like_y
+        rs = _linear_layout(res, ocf, cf or ocf, name)[3]
+    if bwd and a:
+        if pre is None:
+            raise ValueError("pre is required with an activation")
+        if pre.shape != shape or pre.dtype != x.dtype or not pre.is_contiguous():
+            raise ValueError(f"pre must be contiguous {x.dtype} {list(shape)}")
+    _on_gpu(dev, weight=weight, bias=bias, residual=res, pre=pre)
+    _f32((n,), bias=bias)
+    flags = (LINEAR_X_MAPS if cf else 0) | (LINEAR_Y_MAPS if ocf else 0)
+    s = _LinearShape(batch, rows, n, k, xs, rs, weight.stride(0))
+    if bwd:
+        need = _bytes("ssm2d_linear_bwd_workspace", x.dtype, s, a, flags)
+    else:
+        need = _bytes("ssm2d_linear_fwd_workspace", x.dtype, s, flags)
+    return _entry("ssm2d_linear_bwd" if bwd else "ssm2d_linear_fwd", x.dtype), dev.index, s, flags, need, n, shape
 
 
 def linear_fwd(x, weight, bias=None, residual=None, *, act=None, channels_first=False, out_channels_first=None, return_pre=False, y=None,
@@ -179,17 +228,15 @@ def linear_fwd(x, weight, bias=None, residual=None, *, act=None, channels_first=
     [batch, cells, k] to maps [batch, n, cells], or from maps to rows [batch,
     cells, n]. residual: y's shape and dtype. Returns y, or with ``return_pre``
     (y, pre): what act was applied to, for linear_bwd. ``y`` may be the residual."""
-    dev, a, flags, (batch, rows, k, xs), n, ws, shape, like_y = _linear(x, weight, act, channels_first, out_channels_first)
-    fn = _entry("ssm2d_linear_fwd", x.dtype)
-    _on_gpu(dev, weight=weight, bias=bias, residual=residual)
-    if bias is not None:
-        _f32((n,), bias=bias)
-    rs = like_y(residual, "residual") if residual is not None else (0, 0)
-    s, need = _linear_shape(batch, rows, n, k, xs, rs, ws, x.dtype, a, flags, False)
-    y = _out("y", y, shape, x.dtype, dev, stream)
-    pre = _new(shape, x.dtype, dev, stream) if return_pre else None
-    work = _workspace(need, dev, stream)
-    _run(fn, dev, stream, (x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), _ptr(pre), s, a, flags, _ptr(work), need))
+    a, cf = _act(act), bool(channels_first)
+    ocf = cf if out_channels_first is None else bool(out_channels_first)
+    key = ("linear", _meta(x), _meta(weight), _meta(bias), _meta(residual), a, cf, ocf)
+    fn, index, s, flags, need, _, shape = _plans.get(key) or _keep(key, _linear_plan(False, x, weight, bias, residual, None, a, cf, ocf))
+    dt = x.dtype
+    y = _make("y", y, shape, dt, x, stream)
+    pre = _make("pre", None, shape, dt, x, stream) if return_pre else None
+    work = _workspace(need, x, stream)
+    _launch(fn, index, stream, (x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), _ptr(pre), s, a, flags, _ptr(work), need))
     return (y, pre) if return_pre else y
 
 
@@ -197,34 +244,23 @@ def linear_bwd(x, weight, dy, pre=None, *, act=None, bias=True, channels_first=F
     """Gradients of linear_fwd for dy, with the pre that it returned (needed with
     an activation): a dict dx, dweight (x's dtype) and, with ``bias``, dbias (float32
     [n]). The residual's gradient is dy. ``out`` may supply any of them."""
-    dev, a, flags, (batch, rows, k, xs), n, ws, shape, like_y = _linear(x, weight, act, channels_first, out_channels_first)
-    fn = _entry("ssm2d_linear_bwd", x.dtype)
-    _on_gpu(dev, weight=weight, dy=dy, pre=pre)
-    rs = like_y(dy, "dy")
-    if a:
-        if pre is None:
-            raise ValueError("pre is required with an activation")
-        if tuple(pre.shape) != shape or pre.dtype != x.dtype or not pre.is_contiguous():
-            raise ValueError(f"pre must be contiguous {x.dtype} {list(shape)}")
-    out = out or {}
-    r = {"dx": _out("dx", out.get("dx"), tuple(x.shape), x.dtype, dev, stream),
-         "dweight": _out("dweight", out.get("dweight"), (n, k), x.dtype, dev, stream)}
+    a, cf = _act(act), bool(channels_first)
+    ocf = cf if out_channels_first is None else bool(out_channels_first)
+    if not a:
+        pre = None
+    key = ("linear_bwd", _meta(x), _meta(weight), _meta(dy), _meta(pre), a, cf, ocf)
+    fn, index, s, flags, need, n, _ = _plans.get(key) or _keep(key, _linear_plan(True, x, weight, None, dy, pre, a, cf, ocf))
+    out, dt = out or {}, x.dtype
+    r = {"dx": _make("dx", out.get("dx"), x.shape, dt, x, stream), "dweight": _make("dweight", out.get("dweight"), weight.shape, dt, weight, stream)}
     if bias:
-        r["dbias"] = _out("dbias", out.get("dbias"), (n,), torch.float32, dev, stream)
-    s, need = _linear_shape(batch, rows, n, k, xs, rs, ws, x.dtype, a, flags, True)
-    work = _workspace(need, dev, stream)
-    _run(fn, dev, stream, (x.data_ptr(), weight.data_ptr(), _ptr(pre) if a else None, dy.data_ptr(), r["dx"].data_ptr(), r["dweight"].data_ptr(),
-                           _ptr(r.get("dbias")), s, a, flags, _ptr(work), need))
+        r["dbias"] = _make("dbias", out.get("dbias"), (n,), torch.float32, x, stream)
+    work = _workspace(need, x, stream)
+    _launch(fn, index, stream, (x.data_ptr(), weight.data_ptr(), _ptr(pre), dy.data_ptr(), r["dx"].data_ptr(), r["dweight"].data_ptr(),
+                                _ptr(r.get("dbias")), s, a, flags, _ptr(work), need))
     return r
 
 
 # ------------------------------------------------------------------ block norm
-
-@functools.lru_cache(maxsize=256)
-def _norm_shape(rows, n, groups, xs, gs, rs, os, ys, flags, bwd):
-    s = _NormShape(rows, n, groups, xs, gs, rs, os, ys)
-    return s, _bytes("ssm2d_block_norm_bwd_workspace", torch.float32, s, flags) if bwd else 0
-
 
 def _rows_like(t, x, name, dtypes):
     """The row stride of an optional tensor of x's shape."""
@@ -235,21 +271,45 @@ def _rows_like(t, x, name, dtypes):
     return _norm_layout(t, False, name)[3]
 
 
-def _block_norm(x, weight, gate, residual, scale, next_weight, norm, groups, gate_act, gate_first):
+def _norm_plan(bwd, x, weight, gate, residual, scale, next_weight, norm, groups, sigmoid, first, dout, dy):
+    """(C entry, device index, C shape, flags, workspace bytes, n, dtype of out) of a call's checked tensors. dout: in the forward out's dtype."""
     dev = _gpu(x)
     rows, n, _, xs, _ = _norm_layout(x, False)
     if not 0 < groups or n % groups:
         raise ValueError("the channels must be a multiple of groups")
-    if gate_act not in ("silu", "sigmoid"):
-        raise ValueError('gate_act must be "silu" or "sigmoid"')
     if weight is not None and not norm:
         raise ValueError("weight belongs to the norm")
     _on_gpu(dev, weight=weight, gate=gate, residual=residual, scale=scale, next_weight=next_weight)
     _f32((n,), weight=weight, scale=scale, next_weight=next_weight)
     gs = _rows_like(gate, x, "gate", (x.dtype,))
     rs = _rows_like(residual, x, "residual", (x.dtype, torch.float32) if x.dtype != torch.float32 else (x.dtype,))
-    flags = (NORM_ON if norm else 0) | (NORM_GATE_SIGMOID if gate_act == "sigmoid" else 0) | (NORM_GATE_FIRST if gate_first else 0)
-    return dev, rows, n, xs, gs, rs, flags
+    os, ys = 0, 0
+    rt = residual.dtype if residual is not None else None
+    if bwd:
+        if dy is not None and next_weight is None:
+            raise ValueError("dy needs next_weight")
+        if dout is None and dy is None:
+            raise ValueError("dout or dy is required")
+        rt = rt or (dout.dtype if dout is not None else x.dtype)
+        if rt not in (x.dtype, torch.float32):
+            raise ValueError("dout must have out's dtype")
+        _on_gpu(dev, dout=dout, dy=dy)
+        os, ys = _rows_like(dout, x, "dout", (rt,)), _rows_like(dy, x, "dy", (x.dtype,))
+    else:
+        rt = rt or dout or x.dtype
+        if dout not in (None, rt) or rt not in (x.dtype, torch.float32):
+            raise ValueError("out_dtype must be the residual's dtype, or x's or float32 without one")
+    flags = ((NORM_ON if norm else 0) | (NORM_GATE_SIGMOID if sigmoid else 0) | (NORM_GATE_FIRST if first else 0)
+             | (NORM_RESIDUAL_F32 if rt != x.dtype else 0))
+    s = _NormShape(rows, n, groups, xs, gs, rs, os, ys)
+    need = _bytes("ssm2d_block_norm_bwd_workspace", torch.float32, s, flags) if bwd else 0
+    return _entry("ssm2d_block_norm_bwd" if bwd else "ssm2d_block_norm_fwd", x.dtype), dev.index, s, flags, need, n, rt
+
+
+def _gate_act(act):
+    if act not in ("silu", "sigmoid"):
+        raise ValueError('gate_act must be "silu" or "sigmoid"')
+    return act == "sigmoid"
 
 
 def block_norm_fwd(x, weight=None, *, gate=None, residual=None, scale=None, next_weight=None, norm=True, groups=1, gate_act="silu",
@@ -265,22 +325,18 @@ def block_norm_fwd(x, weight=None, *, gate=None, residual=None, scale=None, next
     weight, scale, next_weight: float32 [n]; all but x may be None. out has the
     residual's dtype (``out_dtype``, x's dtype or float32, where there is none).
     Returns out, or (out, y) with next_weight. ``out`` may be the residual."""
-    dev, rows, n, xs, gs, rs, flags = _block_norm(x, weight, gate, residual, scale, next_weight, norm, groups, gate_act, gate_first)
-    fn = _entry("ssm2d_block_norm_fwd", x.dtype)
-    if out_dtype is None:
-        out_dtype = residual.dtype if residual is not None else x.dtype
-    elif out_dtype not in (x.dtype, torch.float32) or (residual is not None and out_dtype != residual.dtype):
-        raise ValueError("out_dtype must be the residual's dtype, or x's or float32 without one")
-    if out_dtype != x.dtype:
-        flags |= NORM_RESIDUAL_F32
-    out = _out("out", out, x.shape, out_dtype, dev, stream)
+    sig, norm, first, groups = _gate_act(gate_act), bool(norm), bool(gate_first), operator.index(groups)
+    key = ("norm", _meta(x), _meta(weight), _meta(gate), _meta(residual), _meta(scale), _meta(next_weight), norm, groups, sig, first, out_dtype)
+    fn, index, s, flags, _, _, rt = _plans.get(key) or _keep(key, _norm_plan(False, x, weight, gate, residual, scale, next_weight, norm, groups, sig,
+                                                                           first, out_dtype, None))
+    shape = x.shape
+    out = _make("out", out, shape, rt, residual if residual is not None else x, stream)
     if next_weight is not None:
-        y = _out("y", y, x.shape, x.dtype, dev, stream)
+        y = _make("y", y, shape, x.dtype, x, stream)
     elif y is not None:
         raise ValueError("y needs next_weight")
-    s, _ = _norm_shape(rows, n, groups, xs, gs, rs, 0, 0, flags, False)
-    _run(fn, dev, stream, (x.data_ptr(), _ptr(gate), _ptr(residual), _ptr(weight), _ptr(scale), _ptr(next_weight), out.data_ptr(), _ptr(y), s,
-                           float(eps), flags))
+    _launch(fn, index, stream, (x.data_ptr(), _ptr(gate), _ptr(residual), _ptr(weight), _ptr(scale), _ptr(next_weight), out.data_ptr(), _ptr(y), s,
+                                float(eps), flags))
     return (out, y) if next_weight is not None else out
 
 
@@ -291,46 +347,28 @@ def block_norm_bwd(x, dout, dy=None, weight=None, *, gate=None, residual=None, s
     dy (None: none): a dict of dx and, of what was given, dgate, dresidual, and
     dweight, dscale, dnext_weight (float32 [n]). Nothing of the forward but its
     inputs is needed. ``out`` may supply any of them."""
-    dev, rows, n, xs, gs, rs, flags = _block_norm(x, weight, gate, residual, scale, next_weight, norm, groups, gate_act, gate_first)
-    fn = _entry("ssm2d_block_norm_bwd", x.dtype)
-    if dy is not None and next_weight is None:
-        raise ValueError("dy needs next_weight")
-    if dout is None and dy is None:
-        raise ValueError("dout or dy is required")
-    rt = residual.dtype if residual is not None else (dout.dtype if dout is not None else x.dtype)
-    _on_gpu(dev, dout=dout, dy=dy)
-    if rt not in (x.dtype, torch.float32):
-        raise ValueError("dout must have out's dtype")
-    os, ys = _rows_like(dout, x, "dout", (rt,)), _rows_like(dy, x, "dy", (x.dtype,))
-    if rt != x.dtype:
-        flags |= NORM_RESIDUAL_F32
-    out, r = out or {}, {}
-
-    def result(name, given, shape, dtype):
-        if given is not None:
-            r[name] = _out(name, out.get(name), shape, dtype, dev, stream)
-
-    result("dx", x, x.shape, x.dtype)
-    result("dgate", gate, x.shape, x.dtype)
-    result("dresidual", residual, x.shape, rt)
-    result("dweight", weight, (n,), torch.float32)
-    result("dscale", scale, (n,), torch.float32)
-    result("dnext_weight", next_weight, (n,), torch.float32)
-    s, need = _norm_shape(rows, n, groups, xs, gs, rs, os, ys, flags, True)
-    work = _workspace(need, dev, stream)
-    _run(fn, dev, stream, (x.data_ptr(), _ptr(gate), _ptr(residual), _ptr(weight), _ptr(scale), _ptr(next_weight), _ptr(dout), _ptr(dy),
-                           r["dx"].data_ptr(), *(_ptr(r.get(k)) for k in ("dgate", "dresidual", "dweight", "dscale", "dnext_weight")), s,
-                           float(eps), flags, _ptr(work), need))
+    sig, norm, first, groups = _gate_act(gate_act), bool(norm), bool(gate_first), operator.index(groups)
+    key = ("norm_bwd", _meta(x), _meta(weight), _meta(gate), _meta(residual), _meta(scale), _meta(next_weight), norm, groups, sig, first,
+           _meta(dout), _meta(dy))
+    fn, index, s, flags, need, n, rt = _plans.get(key) or _keep(key, _norm_plan(True, x, weight, gate, residual, scale, next_weight, norm, groups,
+                                                                              sig, first, dout, dy))
+    out, shape = out or {}, x.shape
+    r = {"dx": _make("dx", out.get("dx"), shape, x.dtype, x, stream)}
+    if gate is not None:
+        r["dgate"] = _make("dgate", out.get("dgate"), shape, x.dtype, gate, stream)
+    if residual is not None:
+        r["dresidual"] = _make("dresidual", out.get("dresidual"), shape, rt, residual, stream)
+    for name, t in (("dweight", weight), ("dscale", scale), ("dnext_weight", next_weight)):
+        if t is not None:
+            r[name] = _make(name, out.get(name), t.shape, torch.float32, t, stream)
+    work = _workspace(need, x, stream)
+    _launch(fn, index, stream, (x.data_ptr(), _ptr(gate), _ptr(residual), _ptr(weight), _ptr(scale), _ptr(next_weight), _ptr(dout), _ptr(dy),
+                                r["dx"].data_ptr(), *(_ptr(r.get(k)) for k in ("dgate", "dresidual", "dweight", "dscale", "dnext_weight")), s,
+                                float(eps), flags, _ptr(work), need))
     return r
 
 
 # ------------------------------------------------------------------ recurrence
-
-@functools.lru_cache(maxsize=256)
-def _recurrence_shape(batch, tokens, channels, n_seq, xs, gs, ds, dtype, flags, bwd):
-    s = _RecurrenceShape(batch, tokens, channels, n_seq, xs, gs, ds)
-    return s, _bytes("ssm2d_recurrence_bwd_workspace" if bwd else "ssm2d_recurrence_fwd_workspace", dtype, s, flags)
-
 
 def _sequence_layout(t, maps, name):
     """(batch, tokens, channels, (batch stride, token or channel stride))"""
@@ -340,29 +378,43 @@ def _sequence_layout(t, maps, name):
     return _linear_layout(t, False, True, name)
 
 
-def _recurrence(x, g, gates, cu_seqlens, channels_first, reverse, dh=None):
-    dev = _gpu(x)
+def _gates(gates):
     if gates not in ("decay", "sigmoid"):
         raise ValueError('gates must be "decay" or "sigmoid"')
+    return gates == "sigmoid"
+
+
+def _recurrence_plan(bwd, x, g, sig, cu_seqlens, maps, rev, dh, states, step=False):
+    """(C entry, device index, C shape, flags, workspace bytes, the states' shape) of a call's checked tensors."""
+    dev = _gpu(x)
     if g.shape != x.shape or g.dtype != x.dtype:
         raise ValueError("g must match x in shape and dtype")
-    batch, tokens, channels, xs = _sequence_layout(x, channels_first, "x")
-    gs = _sequence_layout(g, channels_first, "g")[3]
-    ds = (0, 0)
-    if dh is not None:
+    if step:
+        batch, channels = x.shape
+        if channels > 1 and (x.stride(1) != 1 or g.stride(1) != 1):
+            raise ValueError("the channels of x and g must be contiguous")
+        tokens, xs, gs = 1, (x.stride(0), 0), (g.stride(0), 0)
+    else:
+        batch, tokens, channels, xs = _sequence_layout(x, maps, "x")
+        gs = _sequence_layout(g, maps, "g")[3]
+    ds, n_seq = (0, 0), 0
+    if bwd:
         if dh.shape != x.shape or dh.dtype != x.dtype:
             raise ValueError("dh must match x in shape and dtype")
-        ds = _sequence_layout(dh, channels_first, "dh")[3]
-    n_seq = 0
+        ds = _sequence_layout(dh, maps, "dh")[3]
     if cu_seqlens is not None:
         if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or not cu_seqlens.is_contiguous():
             raise ValueError("cu_seqlens must be contiguous int32 [sequences + 1], at least one sequence")
-        if batch != 1 or channels_first or reverse:
+        if batch != 1 or maps or rev:
             raise ValueError("packed sequences need batch 1, and go neither channels first nor in reverse")
         n_seq = cu_seqlens.numel() - 1
-    _on_gpu(dev, g=g, cu_seqlens=cu_seqlens, dh=dh)
-    flags = (RECUR_SIGMOID if gates == "sigmoid" else 0) | (RECUR_MAPS if channels_first else 0) | (RECUR_REVERSE if reverse else 0)
-    return dev, flags, (n_seq or batch, channels), _recurrence_shape(batch, tokens, channels, n_seq, xs, gs, ds, x.dtype, flags, dh is not None)
+    shape = torch.Size((n_seq or batch, channels))
+    _on_gpu(dev, g=g, cu_seqlens=cu_seqlens, dh=dh, **states)
+    _f32(shape, **states)
+    flags = (RECUR_SIGMOID if sig else 0) | (RECUR_MAPS if maps else 0) | (RECUR_REVERSE if rev else 0)
+    s = _RecurrenceShape(batch, tokens, channels, n_seq, xs, gs, ds)
+    need = _bytes("ssm2d_recurrence_bwd_workspace" if bwd else "ssm2d_recurrence_fwd_workspace", x.dtype, s, flags)
+    return _entry("ssm2d_recurrence_bwd" if bwd else "ssm2d_recurrence_fwd", x.dtype), dev.index, s, flags, need, shape
 
 
 def recurrence_fwd(x, g, *, gates="decay", h_init=None, cu_seqlens=None, channels_first=False, reverse=False, return_last_state=False, h=None,
@@ -375,15 +427,15 @@ def recurrence_fwd(x, g, *, gates="decay", h_init=None, cu_seqlens=None, channel
     tokens hold packed sequences; tokens behind the last one are left as they
     were. h_init: float32 [sequences, channels] or None (zeros). Returns h (x's
     shape and dtype), or (h, h_last)."""
-    dev, flags, states, (shape, need) = _recurrence(x, g, gates, cu_seqlens, channels_first, reverse)
-    fn = _entry("ssm2d_recurrence_fwd", x.dtype)
-    _on_gpu(dev, h_init=h_init)
-    _f32(states, h_init=h_init)
-    h = _like("h", h, x, stream)
+    sig, maps, rev = _gates(gates), bool(channels_first), bool(reverse)
+    key = ("recurrence", _meta(x), _meta(g), _meta(h_init), _meta(cu_seqlens), sig, maps, rev)
+    fn, index, s, flags, need, states = _plans.get(key) or _keep(key, _recurrence_plan(False, x, g, sig, cu_seqlens, maps, rev, None,
+                                                                                     {"h_init": h_init}))
+    h = _make("h", h, x.shape, x.dtype, x, stream)
     if return_last_state or h_last is not None:
-        h_last = _out("h_last", h_last, states, torch.float32, dev, stream)
-    work = _workspace(need, dev, stream)
-    _run(fn, dev, stream, (x.data_ptr(), g.data_ptr(), _ptr(h_init), _ptr(cu_seqlens), h.data_ptr(), _ptr(h_last), shape, flags, _ptr(work), need))
+        h_last = _make("h_last", h_last, states, torch.float32, x, stream)
+    work = _workspace(need, x, stream)
+    _launch(fn, index, stream, (x.data_ptr(), g.data_ptr(), _ptr(h_init), _ptr(cu_seqlens), h.data_ptr(), _ptr(h_last), s, flags, _ptr(work), need))
     return (h, h_last) if return_last_state else h
 
 
@@ -392,17 +444,17 @@ def recurrence_bwd(x, g, dh, *, gates="decay", h_init=None, dh_last=None, cu_seq
     """Gradients of recurrence_fwd for dh = dL/dh and dh_last = dL/dh_last (None:
     zeros): a dict dx, dg (x's dtype), and dh_init (float32) when h_init or
     dh_last is given or ``out`` holds it. ``out`` may supply any of them."""
-    dev, flags, states, (shape, need) = _recurrence(x, g, gates, cu_seqlens, channels_first, reverse, dh)
-    fn = _entry("ssm2d_recurrence_bwd", x.dtype)
-    _on_gpu(dev, h_init=h_init, dh_last=dh_last)
-    _f32(states, h_init=h_init, dh_last=dh_last)
+    sig, maps, rev = _gates(gates), bool(channels_first), bool(reverse)
+    key = ("recurrence_bwd", _meta(x), _meta(g), _meta(h_init), _meta(dh_last), _meta(cu_seqlens), _meta(dh), sig, maps, rev)
+    fn, index, s, flags, need, states = _plans.get(key) or _keep(key, _recurrence_plan(True, x, g, sig, cu_seqlens, maps, rev, dh,
+                                                                                     {"h_init": h_init, "dh_last": dh_last}))
     out = out or {}
-    r = {n: _like(n, out.get(n), x, stream) for n in ("dx", "dg")}
+    r = {n: _make(n, out.get(n), x.shape, x.dtype, x, stream) for n in ("dx", "dg")}
     if h_init is not None or dh_last is not None or out.get("dh_init") is not None:
-        r["dh_init"] = _out("dh_init", out.get("dh_init"), states, torch.float32, dev, stream)
-    work = _workspace(need, dev, stream)
-    _run(fn, dev, stream, (x.data_ptr(), g.data_ptr(), _ptr(h_init), _ptr(cu_seqlens), dh.data_ptr(), _ptr(dh_last), r["dx"].data_ptr(),
-                           r["dg"].data_ptr(), _ptr(r.get("dh_init")), shape, flags, _ptr(work), need))
+        r["dh_init"] = _make("dh_init", out.get("dh_init"), states, torch.float32, x, stream)
+    work = _workspace(need, x, stream)
+    _launch(fn, index, stream, (x.data_ptr(), g.data_ptr(), _ptr(h_init), _ptr(cu_seqlens), dh.data_ptr(), _ptr(dh_last), r["dx"].data_ptr(),
+                                r["dg"].data_ptr(), _ptr(r.get("dh_init")), s, flags, _ptr(work), need))
     return r
 
 
@@ -414,20 +466,10 @@ def recurrence_step(x, g, state, *, gates="decay", h=None, stream=None):
         raise ValueError("x and g must be [batch, channels]")
     if state is None:
         raise ValueError("state is required")
-    dev = _gpu(x)
-    batch, channels = x.shape
-    if gates not in ("decay", "sigmoid"):
-        raise ValueError('gates must be "decay" or "sigmoid"')
-    if g.shape != x.shape or g.dtype != x.dtype:
-        raise ValueError("g must match x in shape and dtype")
-    if channels > 1 and (x.stride(1) != 1 or g.stride(1) != 1):
-        raise ValueError("the channels of x and g must be contiguous")
-    fn = _entry("ssm2d_recurrence_fwd", x.dtype)
-    _on_gpu(dev, g=g, state=state)
-    _f32((batch, channels), state=state)
-    flags = RECUR_SIGMOID if gates == "sigmoid" else 0
-    shape, need = _recurrence_shape(batch, 1, channels, 0, (x.stride(0), 0), (g.stride(0), 0), (0, 0), x.dtype, flags, False)
-    h = _like("h", h, x, stream)
-    work = _workspace(need, dev, stream)
-    _run(fn, dev, stream, (x.data_ptr(), g.data_ptr(), state.data_ptr(), None, h.data_ptr(), state.data_ptr(), shape, flags, _ptr(work), need))
+    sig = _gates(gates)
+    key = ("step", _meta(x), _meta(g), _meta(state), sig)
+    fn, index, s, flags, need, _ = _plans.get(key) or _keep(key, _recurrence_plan(False, x, g, sig, None, False, False, None, {"state": state}, True))
+    h = _make("h", h, x.shape, x.dtype, x, stream)
+    at = state.data_ptr()
+    _launch(fn, index, stream, (x.data_ptr(), g.data_ptr(), at, None, h.data_ptr(), at, s, flags, None, need))
     return h

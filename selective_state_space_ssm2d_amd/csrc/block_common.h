@@ -73,7 +73,7 @@ __device__ __forceinline__ float act_slope(float z)
 // columns a workgroup, 64 rows at a time, then over the 64.
 constexpr int kFoldThreads = 1024;
 inline unsigned fold_blocks(long n) { return static_cast<unsigned>((n + 15) / 16); }
-static __global__ __launch_bounds__(kFoldThreads) void fold_rows(const float *part, int np, long n, long ld, float *dst)
+__device__ __forceinline__ void fold_columns(const float *part, int np, long n, long ld, float *dst)
 {
     __shared__ float s[64][17];
     const int cx = threadIdx.x % 16, ry = threadIdx.x / 16;
@@ -88,6 +88,16 @@ static __global__ __launch_bounds__(kFoldThreads) void fold_rows(const float *pa
         for (int r = 0; r < 64; ++r) t += s[r][cx];
         dst[c] = t;
     }
+}
+static __global__ __launch_bounds__(kFoldThreads) void fold_rows(const float *part, int np, long n, float *dst)
+{
+    fold_columns(part, np, n, n, dst);
+}
+// Of partial rows [np][3][n], each of the three that is wanted.
+static __global__ __launch_bounds__(kFoldThreads) void fold_three(const float *part, int np, long n, float *d0, float *d1, float *d2)
+{
+    float *dst = blockIdx.y == 0 ? d0 : (blockIdx.y == 1 ? d1 : d2);
+    if (dst) fold_columns(part + blockIdx.y * n, np, n, 3 * n, dst);
 }
 
 // Clears n floats (a kernel: memset nodes of captured graphs have been misapplied).

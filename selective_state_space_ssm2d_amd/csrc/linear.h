@@ -24,7 +24,6 @@ struct GemmParams {
     long batch;
     int splits;       // parts of the sum, each by workgroups of its own
     long steps, per;  // steps of BK in all stretches, and of one split
-    int a_vec, b_vec; // elements that can be read at once (8, 4 or 1)
     // epilogue
     const float *bias;  // along n, or with bias_m along m
     int bias_m, act;
@@ -32,7 +31,6 @@ struct GemmParams {
     long r_ld, r_bs;
     void *c, *pre;
     long c_ld, c_bs;
-    int c_vec;        // rows of c, pre and res can be accessed 4 elements at a time
     int straight;     // bf16 operands can be loaded straight to LDS
     float *part;      // splits > 1: [split][batch][M][N rounded up to 4]
     long first;       // the launch's first workgroup
@@ -63,11 +61,12 @@ __device__ __forceinline__ void finish4(const GemmParams &p, long b, int m, int 
     }
     const long at = b * p.c_bs + static_cast<long>(m) * p.c_ld + n;
     T *c = static_cast<T *>(p.c) + at;
+    const bool four = n + 4 <= p.N;
     auto put = [&](T *dst) __attribute__((always_inline)) {
-        if (p.c_vec == 4) {
+        if (four) {
             Raw<T, 4> r;
             r.set(v);
-            r.store(dst);
+            r.store_any(dst);
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -83,9 +82,9 @@ __device__ __forceinline__ void finish4(const GemmParams &p, long b, int m, int 
     }
     if (p.res) {
         const T *r = static_cast<const T *>(p.res) + b * p.r_bs + static_cast<long>(m) * p.r_ld + n;
-        if (p.c_vec == 4) {
+        if (four) {
             Raw<T, 4> w;
-            w.load(r);
+            w.load_any(r);
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] += w.get(j);
         } else {
@@ -142,45 +141,33 @@ struct OperandTile {
 // Eight elements of an operand on their way from memory to LDS.
 template <typename T>
 struct Chunk {
-    Raw<T, 4> h[2];
-    // the first `count` of the 8 at p (0 or less: none), the others 0; vec: as GemmParams
-    __device__ __forceinline__ void load(const T *p, long count, int vec)
+    Raw<T, 8> r;
+    // the first `count` of the 8 at p (0 or less: none), the others 0
+    __device__ __forceinline__ void load(const T *p, long count)
     {
-        if (vec >= 4) {  // (count is a multiple of vec)
-            if (count >= 8) {
-                if (sizeof(T) == 2 && vec == 8) {
-                    const uint4 t = *reinterpret_cast<const uint4 *>(p);
-                    h[0].w[0] = t.x, h[0].w[1] = t.y, h[1].w[0] = t.z, h[1].w[1] = t.w;
-                } else {
-                    h[0].load(p);
-                    h[1].load(p + 4);
-                }
-                return;
-            }
-            h[0].clear();
-            h[1].clear();
-            if (count >= 4) h[0].load(p);
-            return;
-        }
-        h[0].clear();
-        h[1].clear();
+        if (count >= 8) {
+            r.load_any(p);
+        } else if (count > 0) {
+            float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (i >= count) continue;
-            if constexpr (sizeof(T) == 2) h[i / 4].w[i % 4 / 2] |= static_cast<unsigned>(p[i]) << (16 * (i & 1));
-            else h[i / 4].w[i % 4] = __float_as_uint(p[i]);
+            for (int i = 0; i < 8; ++i) v[i] = widen1(p[min(i, static_cast<int>(count) - 1)]);
+#pragma unroll
+            for (int i = 1; i < 8; ++i) v[i] = i < count ? v[i] : 0.0f;
+            r.set(v);
+        } else {
+            r.clear();
         }
     }
     // as NP parts, kPart elements apart
     __device__ __forceinline__ void store(uint16_t *dst, int part) const
     {
         if constexpr (sizeof(T) == 2) {
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(h[0].w[0], h[0].w[1], h[1].w[0], h[1].w[1]);
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
         } else {
             // three parts of 8 bits each, cut off: exact
             float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = h[i / 4].get(i % 4);
+            for (int i = 0; i < 8; ++i) v[i] = r.get(i);
 #pragma unroll
             for (int n = 0; n < 3; ++n) {
                 unsigned w[4];
@@ -270,23 +257,23 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmParams p)
         const long kb = p.kb == 1 ? 0 : s / each, k0 = (s - kb * each) * BK;
         const T *ap = A + kb * p.a_bs, *bp = B + kb * p.b_bs;
         if (p.kb == 1) ap = A, bp = B;
-        auto side = [&](auto kc, const T *src, long ld, int vec, int r0, int rows, auto &reg, auto row_len) __attribute__((always_inline)) {
+        auto side = [&](auto kc, const T *src, long ld, int r0, int rows, auto &reg, auto row_len) __attribute__((always_inline)) {
             constexpr int kChunks = decltype(row_len)::value / 8;
 #pragma unroll
             for (int i = 0; i < static_cast<int>(sizeof(reg) / sizeof(reg[0])); ++i) {
                 const int id = i * 256 + threadIdx.x, row = id / kChunks, col = id % kChunks * 8;
                 if constexpr (decltype(kc)::value) {
                     const long m = r0 + row, k = k0 + col;
-                    reg[i].load(src + m * ld + k, m < rows ? p.K - k : 0, vec);
+                    reg[i].load(src + m * ld + k, m < rows ? p.K - k : 0);
                 } else {
                     const long k = k0 + row, m = r0 + col;
-                    reg[i].load(src + k * ld + m, k < p.K ? rows - m : 0, vec);
+                    reg[i].load(src + k * ld + m, k < p.K ? rows - m : 0);
                 }
             }
         };
         using std::integral_constant;
-        side(integral_constant<bool, A_KC>{}, ap, p.a_ld, p.a_vec, t.m0, p.M, ra, integral_constant<int, TA::kRow>{});
-        side(integral_constant<bool, B_KC>{}, bp, p.b_ld, p.b_vec, t.n0, p.N, rb, integral_constant<int, TB::kRow>{});
+        side(integral_constant<bool, A_KC>{}, ap, p.a_ld, t.m0, p.M, ra, integral_constant<int, TA::kRow>{});
+        side(integral_constant<bool, B_KC>{}, bp, p.b_ld, t.n0, p.N, rb, integral_constant<int, TB::kRow>{});
     };
     facc acc[WM / 16][WN / 16];
 #pragma unroll

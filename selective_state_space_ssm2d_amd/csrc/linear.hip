@@ -40,12 +40,12 @@ template <typename T, int V>
 __device__ __forceinline__ void slope_of(const SlopeParams &p, const T *dy, const T *pre, T *dz, float (&v)[V])
 {
     Raw<T, V> d;
-    d.load(dy);
+    d.load_any(dy);
 #pragma unroll
     for (int j = 0; j < V; ++j) v[j] = d.get(j);
     if (p.act != SSM2D_ACT_NONE) {
         Raw<T, V> z;
-        z.load(pre);
+        z.load_any(pre);
         switch (p.act) {
         case SSM2D_ACT_RELU:
 #pragma unroll
@@ -63,24 +63,25 @@ __device__ __forceinline__ void slope_of(const SlopeParams &p, const T *dy, cons
         if (dz) {
             Raw<T, V> o;
             o.set(v);
-            o.store(dz);
+            o.store_any(dz);
         }
     }
 }
 
-// Token rows: 32 lanes of V channels by 8 rows; a slice of rows a workgroup.
+// Token rows: 32 lanes of V channels by 8 rows; a slice of rows a workgroup. The
+// last lane of a row reaches back over the one before, and counts what is its own.
 template <typename T, int V>
 __global__ __launch_bounds__(256) void slope_rows(const SlopeParams p)
 {
     __shared__ float sum[8][32 * V + 1];
     const int cx = threadIdx.x % 32, ry = threadIdx.x / 32;
     const long tiles = (p.n + 32 * V - 1) / (32 * V), id = p.first + blockIdx.x;
-    const long c = (id % tiles * 32 + cx) * V, slice = id / tiles, b = slice / p.slices;
+    const long c0 = (id % tiles * 32 + cx) * V, c = min(c0, p.n - V), slice = id / tiles, b = slice / p.slices;
     const long r1 = slice % p.slices * p.each, r2 = min(r1 + p.each, p.rows);
     float s[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) s[j] = 0.0f;
-    if (c < p.n) {
+    if (c0 < p.n) {
 #pragma unroll 4
         for (long r = r1 + ry; r < r2; r += 8) {
             float v[V];
@@ -92,8 +93,12 @@ __global__ __launch_bounds__(256) void slope_rows(const SlopeParams p)
         }
     }
     if (!p.part) return;
+    const int back = static_cast<int>(c0 - c);
+    if (c0 < p.n) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) sum[ry][cx * V + j] = s[j];
+        for (int j = 0; j < V; ++j)
+            if (j >= back) sum[ry][cx * V + j - back] = s[j];
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < 32 * V; i += 256) {
         const long col = id % tiles * 32 * V + i;
@@ -111,16 +116,22 @@ __global__ __launch_bounds__(256) void slope_maps(const SlopeParams p)
 {
     __shared__ float sum[4];
     const long id = p.first + blockIdx.x, c = id % p.n, slice = id / p.n, b = slice / p.slices;
-    const long r1 = slice % p.slices * p.each, r2 = min(r1 + p.each, p.rows);
+    const long r1 = slice % p.slices * p.each, r2 = min(r1 + p.each, p.rows), at = (b * p.n + c) * p.rows;
+    const T *dy = static_cast<const T *>(p.dy) + b * p.d_b + c * p.d_s, *pre = static_cast<const T *>(p.pre) + at;
+    T *dz = p.dz ? static_cast<T *>(p.dz) + at : nullptr;
     float s = 0.0f;
+    long r = r1 + threadIdx.x * V;
 #pragma unroll 2
-    for (long r = r1 + threadIdx.x * V; r < r2; r += 256 * V) {
+    for (; r + V <= r2; r += 256 * V) {
         float v[V];
-        const long at = (b * p.n + c) * p.rows + r;
-        slope_of<T, V>(p, static_cast<const T *>(p.dy) + b * p.d_b + c * p.d_s + r, static_cast<const T *>(p.pre) + at,
-                       p.dz ? static_cast<T *>(p.dz) + at : nullptr, v);
+        slope_of<T, V>(p, dy + r, pre + r, dz ? dz + r : nullptr, v);
 #pragma unroll
         for (int j = 0; j < V; ++j) s += v[j];
+    }
+    for (const long end = min(r + V, r2); r < end; ++r) {  // (one thread's, at the end of the row)
+        float v[1];
+        slope_of<T, 1>(p, dy + r, pre + r, dz ? dz + r : nullptr, v);
+        s += v[0];
     }
     if (!p.part) return;
     s = lane_sum<64>(s);
@@ -144,11 +155,6 @@ template <typename T>
 int run_slope(SlopeParams p, bool maps, hipStream_t s)
 {
     constexpr int V = 16 / static_cast<int>(sizeof(T));
-    const long inner = maps ? p.rows : p.n;
-    auto fits = [&](int v) {
-        const size_t to = v * sizeof(T);
-        return inner % v == 0 && !off_by(p.dy, to) && !off_by(p.pre, to) && !off_by(p.dz, to) && p.d_b % v == 0 && p.d_s % v == 0;
-    };
     auto go = [&](auto vec) {
         constexpr int W = decltype(vec)::value;
         const long groups = p.slices * p.batch * (maps ? p.n : (p.n + 32 * W - 1) / (32 * W)), most = most_groups(256);
@@ -161,11 +167,7 @@ int run_slope(SlopeParams p, bool maps, hipStream_t s)
         }
         return static_cast<int>(SSM2D_OK);
     };
-    if (fits(V)) return go(std::integral_constant<int, V>{});
-    if constexpr (V == 8) {
-        if (fits(4)) return go(std::integral_constant<int, 4>{});
-    }
-    return go(std::integral_constant<int, 1>{});
+    return maps || p.n >= V ? go(std::integral_constant<int, V>{}) : go(std::integral_constant<int, 1>{});
 }
 
 // ------------------------------------------------------------------ checks
@@ -189,19 +191,11 @@ int check_linear(const ssm2d_linear_shape *a, int act, uint32_t flags)
     return SSM2D_OK;
 }
 
-// Elements of rows of `len` at strides s0 and s1 that can be read at once.
-template <typename T>
-int readable(const void *p, long len, long s0, long s1)
+// Whether rows of `len` at strides s0 and s1 are whole 16-byte words.
+bool in_words(const void *p, long len, long s0, long s1, size_t size)
 {
-    for (const int v : {8, 4})
-        if (len % v == 0 && s0 % v == 0 && s1 % v == 0 && !off_by(p, std::min<size_t>(v * sizeof(T), 16))) return v;
-    return 1;
-}
-// Whether four neighbours can be accessed at once in rows of n.
-template <typename T>
-bool quads(const void *p, long n, long ld, long bs)
-{
-    return !p || (n % 4 == 0 && ld % 4 == 0 && bs % 4 == 0 && !off_by(p, 4 * sizeof(T)));
+    const long v = 16 / static_cast<long>(size);
+    return len % v == 0 && s0 % v == 0 && s1 % v == 0 && !off_by(p, 16);
 }
 
 // The operand with index pairs (rows, len) at p, `ld` between rows, contiguous along len.
@@ -216,12 +210,11 @@ int product(GemmParams &g, const Side &a, const Side &b, void *ws, hipStream_t s
 {
     const long kb = g.kb > 1 ? g.kb : g.batch;
     g.a = a.p, g.a_ld = a.ld, g.a_bs = a.bs, g.b = b.p, g.b_ld = b.ld, g.b_bs = b.bs;
-    g.a_vec = readable<T>(a.p, a.kc ? g.K : g.M, a.ld, kb > 1 ? a.bs : 0);
-    g.b_vec = readable<T>(b.p, b.kc ? g.K : g.N, b.ld, kb > 1 ? b.bs : 0);
-    g.c_vec = quads<T>(g.c, g.N, g.c_ld, g.c_bs) && quads<T>(g.pre, g.N, 0, 0) && quads<T>(g.res, g.N, g.r_ld, g.batch > 1 ? g.r_bs : 0) ? 4 : 1;
     // (a tile's offsets within 31 bits, and rows that do not lie over each other)
-    auto straight = [&](const Side &x, int vec, long len) { return vec == 8 && x.ld >= len && x.ld < (1L << 22); };
-    g.straight = sizeof(T) == 2 && straight(a, g.a_vec, a.kc ? g.K : g.M) && straight(b, g.b_vec, b.kc ? g.K : g.N);
+    auto straight = [&](const Side &x, long len) {
+        return in_words(x.p, len, x.ld, kb > 1 ? x.bs : 0, sizeof(T)) && x.ld >= len && x.ld < (1L << 22);
+    };
+    g.straight = sizeof(T) == 2 && straight(a, a.kc ? g.K : g.M) && straight(b, b.kc ? g.K : g.N);
     return run_gemm<T>(g, a.kc, b.kc, ws, s);
 }
 
@@ -346,7 +339,7 @@ int linear_bwd(const T *x, const T *weight, const T *pre, const T *dy, T *dx, T 
         p.batch = B, p.rows = R, p.n = n, p.d_b = a->r_stride[0], p.d_s = a->r_stride[1], p.act = act, p.slices = plan.slices, p.each = plan.each;
         if ((st = run_slope<T>(p, ym, s)) != SSM2D_OK) return st;
         if (dbias) {
-            fold_rows<<<dim3(fold_blocks(n)), dim3(kFoldThreads), 0, s>>>(p.part, static_cast<int>(plan.slices * B), n, n, dbias);
+            fold_rows<<<dim3(fold_blocks(n)), dim3(kFoldThreads), 0, s>>>(p.part, static_cast<int>(plan.slices * B), n, dbias);
             if ((st = launched()) != SSM2D_OK) return st;
         }
         if (act != SSM2D_ACT_NONE) dz = Side{ws, ym ? R : n, R * n, true};

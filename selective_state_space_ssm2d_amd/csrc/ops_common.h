@@ -76,6 +76,42 @@ struct Raw {
         else if constexpr (B == 4) *reinterpret_cast<unsigned *>(p) = w[0];
         else *reinterpret_cast<uint16_t *>(p) = static_cast<uint16_t>(w[0]);
     }
+    // The same at any element's address: memory accesses of any width take any
+    // (a copy of 128 MB in 16-byte words 2 bytes off runs at 97 % of an aligned one).
+    __device__ __forceinline__ void load_any(const T *p)
+    {
+        constexpr int B = N * static_cast<int>(sizeof(T));
+        if constexpr (B >= 16) {
+#pragma unroll
+            for (int i = 0; i < B / 16; ++i) {
+                const Words<4> t = reinterpret_cast<const Loose<4> *>(p)[i].v;
+                w[4 * i] = t[0], w[4 * i + 1] = t[1], w[4 * i + 2] = t[2], w[4 * i + 3] = t[3];
+            }
+        } else if constexpr (B == 8) {
+            const Words<2> t = reinterpret_cast<const Loose<2> *>(p)->v;
+            w[0] = t[0], w[1] = t[1];
+        } else {
+            load(p);
+        }
+    }
+    __device__ __forceinline__ void store_any(T *p) const
+    {
+        constexpr int B = N * static_cast<int>(sizeof(T));
+        if constexpr (B >= 16) {
+#pragma unroll
+            for (int i = 0; i < B / 16; ++i) reinterpret_cast<Loose<4> *>(p)[i].v = Words<4>{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+        } else if constexpr (B == 8) {
+            reinterpret_cast<Loose<2> *>(p)->v = Words<2>{w[0], w[1]};
+        } else {
+            store(p);
+        }
+    }
+    template <int W>
+    using Words = unsigned __attribute__((ext_vector_type(W)));
+    template <int W>
+    struct __attribute__((packed, aligned(alignof(T)))) Loose {
+        Words<W> v;
+    };
     __device__ __forceinline__ void clear()
     {
 #pragma unroll

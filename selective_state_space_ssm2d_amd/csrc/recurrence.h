@@ -25,7 +25,7 @@
 namespace ssm2d_impl {
 
 struct RecParams {
-    const void *x, *g, *dh;        // at the first token in the order of the recurrence
+    const void *x, *g, *dh;
     const float *h_init, *dh_last;
     const int *cu;
     void *h, *dx, *dg;
@@ -36,8 +36,8 @@ struct RecParams {
     int S;                         // segments
     long first;                    // the launch's first workgroup (a grid has less than 2^32 threads)
     int n, n_seq, tiles;
-    long x_b, g_b, d_b, x_t, g_t, d_t;  // strides of batch and token (rows; token strides signed) or channel (maps)
-    long o_t;                      // token stride of the outputs (rows)
+    long x_b, g_b, d_b, x_t, g_t, d_t;  // strides of batch and token (rows) or channel (maps)
+    int rev;                       // rows: from the last token to the first
 };
 
 constexpr float kCut = -0.0f;
@@ -73,6 +73,10 @@ __device__ __forceinline__ void gates(float g, float &a, float &w)
         a = exp_for<T>(g), w = 1.0f;
     }
 }
+
+// A gate that leaves the state as it is, where x is 0: for tokens past the last.
+template <typename T, bool SIG>
+__device__ __forceinline__ float idle() { return SIG ? INFINITY : 0.0f; }
 
 // ------------------------------------------------------------------ packed sequences
 
@@ -111,15 +115,30 @@ __device__ __forceinline__ Place locate(const RecParams &p, long t)
 
 template <typename T, int V, bool BWD>
 struct RowDims {
-    // 16 lanes of 4 channels (128-byte runs in bf16) by 16 (backward 32) lots of tokens; single channels where rows are odd
-    static constexpr int kBX = V == 4 ? 16 : 32, kBY = (BWD ? 512 : 256) / kBX, kThreads = kBX * kBY, kWaves = kThreads / 64;
-    static constexpr int kL = BWD ? 8 : (sizeof(T) == 2 || V == 1 ? 16 : 8), kChunk = kBY * kL;
+    // 16 lanes of 8 bytes (128-byte runs) by 16 (backward 32) lots of 8 tokens; single channels where there are fewer or rows are far apart
+    static constexpr int kBX = V > 1 ? 16 : 32, kBY = (BWD ? 512 : 256) / kBX, kThreads = kBX * kBY, kWaves = kThreads / 64;
+    static constexpr int kL = 8, kChunk = kBY * kL;
 };
 
-// What one thread holds of a chunk: kL tokens of V channels.
-template <typename T, int V, int L>
-struct Lot {
-    Raw<T, V> x[L], g[L];
+template <typename T>
+constexpr int kRowV = 8 / static_cast<int>(sizeof(T));  // channels a lane holds
+
+// Where a thread's tokens of a chunk lie in a tensor: token `k` of the chunk, in
+// the order of the recurrence, at base + offset. Offsets are 32 bits where
+// channels are read together (the host sees to it that a chunk spans less).
+template <int V>
+struct Line {
+    using Offset = std::conditional_t<V == 1, unsigned long, unsigned>;
+    long base;            // elements from the tensor's start, the same for the workgroup
+    Offset first, step;   // of token `lot` of the chunk (or the last there is), and to the next one
+    // tokens t1 .. t1 + last; the thread's first is `lot`
+    __device__ __forceinline__ void begin(const RecParams &p, long batch, long stride, long t1, int last, int lot, int channel)
+    {
+        base = batch + (p.rev ? p.T - 1 - t1 - last : t1) * stride;
+        const int k = min(lot, last);
+        first = static_cast<Offset>(p.rev ? last - k : k) * static_cast<Offset>(stride) + channel;
+        step = p.rev ? -static_cast<Offset>(stride) : static_cast<Offset>(stride);
+    }
 };
 
 // Joins the threads' stretches (P, c) of a workgroup in token order: *in gets
@@ -151,45 +170,120 @@ __device__ __forceinline__ void join_lots(float (&P)[V], float (&c)[V], float (&
         ec[j] = DOWN ? __shfl_down(c[j], BX) : __shfl_up(c[j], BX);
     }
     __syncthreads();
+    // (two waves at a time: all at once would take the registers of the lots)
+    float h[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        float h = carry[j];
+    for (int j = 0; j < V; ++j) h[j] = carry[j];
+#pragma unroll 2
+    for (int i = 0; i < WAVES; ++i) {
+        const int w = DOWN ? WAVES - 1 - i : i;
 #pragma unroll
-        for (int i = 0; i < WAVES; ++i) {
-            const int w = DOWN ? WAVES - 1 - i : i;
+        for (int j = 0; j < V; ++j) {
             const float wP = tot[w][cx * V + j][0], wc = tot[w][cx * V + j][1];
-            if (w == wave) in[j] = h;
-            h = pass<PACKED>(wP, wc, h);
+            if (w == wave) in[j] = h[j];
+            h[j] = pass<PACKED>(wP, wc, h[j]);
             float p = wP, q = 0.0f;
             join<PACKED>(carryP[j], 0.0f, p, q);
             carryP[j] = p;
         }
-        carry[j] = h;
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        carry[j] = h[j];
         if (sub != (DOWN ? kSubs - 1 : 0)) in[j] = pass<PACKED>(eP[j], ec[j], in[j]);
     }
 }
 
-// What a packed token's place adds to the recurrence, for walks over a thread's tokens.
-template <bool PACKED>
-struct Walk {
-    Place at;
-    __device__ __forceinline__ void begin(const RecParams &p, long t)
+// Which of a thread's L tokens from t on are the first or the last of a packed
+// sequence, and which are in none.
+template <int L>
+struct Marks {
+    unsigned firsts, ends, outs;
+    // t0: the workgroup's first token, of `chunk`
+    __device__ __forceinline__ void find(const RecParams &p, long t0, int chunk, long t)
     {
-        if constexpr (PACKED) at = locate(p, t);
-    }
-    // moves on to token t (the one after the last)
-    __device__ __forceinline__ void to(const RecParams &p, long t)
-    {
-        if constexpr (PACKED) {
-            if (t >= at.next) at = locate(p, t);
-            else at.first = false;
+        firsts = ends = outs = 0;
+        Place w = locate(p, t0);  // (by scalar loads)
+        if (w.seq >= 0 && !w.first && w.end > t0 + chunk) return;  // (most: inside one sequence)
+        w = locate(p, t);
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            if (i > 0) {
+                if (t + i >= w.next) w = locate(p, t + i);
+                else w.first = false;
+            }
+            firsts |= (w.seq >= 0 && w.first ? 1u : 0u) << i;
+            ends |= (w.seq >= 0 && t + i + 1 == w.end ? 1u : 0u) << i;
+            outs |= (w.seq < 0 ? 1u : 0u) << i;
         }
     }
+    __device__ __forceinline__ bool first(int i) const { return (firsts >> i) & 1u; }
+    __device__ __forceinline__ bool end(int i) const { return (ends >> i) & 1u; }
+    __device__ __forceinline__ bool none(int i) const { return (outs >> i) & 1u; }
+    __device__ __forceinline__ bool any() const { return (firsts | ends | outs) != 0; }
 };
+// A state of the sequence that token t belongs to (NULL: zeros).
+__device__ __forceinline__ float state_at(const RecParams &p, const float *state, long t, long c)
+{
+    return state ? state[static_cast<long>(locate(p, t).seq) * p.n + c] : 0.0f;
+}
+
+// A few tokens (serving: one): a thread walks over them all for V channels (the
+// last one of a row for those that are left: the state may be written in place,
+// so that no two threads may share one).
+template <typename T, int V, bool SIG>
+__global__ __launch_bounds__(256) void rec_few(const RecParams p, long threads)
+{
+    const long id = (p.first + blockIdx.x) * 256 + threadIdx.x;
+    if (id >= threads) return;
+    const long b = id / p.tiles;
+    const int c = static_cast<int>(id % p.tiles) * V, left = min(p.n - c, V);
+    const T *x = static_cast<const T *>(p.x) + b * p.x_b + c, *g = static_cast<const T *>(p.g) + b * p.g_b + c;
+    T *out = static_cast<T *>(p.h) + b * p.T * p.n + c;
+    const long at = b * p.n + c;
+    float h[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) h[j] = p.h_init && j < left ? p.h_init[at + j] : 0.0f;
+    for (long i = 0; i < p.T; ++i) {
+        const long t = p.rev ? p.T - 1 - i : i;
+        Raw<T, V> vx, vg, o;
+        if (left == V) {
+            vx.load_any(x + t * p.x_t);
+            vg.load_any(g + t * p.g_t);
+        } else {
+            float fx[V], fg[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                fx[j] = j < left ? widen1(x[t * p.x_t + j]) : 0.0f;
+                fg[j] = j < left ? widen1(g[t * p.g_t + j]) : 0.0f;
+            }
+            vx.set(fx);
+            vg.set(fg);
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float a, w;
+            gates<T, SIG>(vg.get(j), a, w);
+            h[j] = fmaf(a, h[j], SIG ? w * vx.get(j) : vx.get(j));
+        }
+        if (left == V) {
+            o.set(h);
+            o.store_any(out + t * p.n);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (j < left) store1(out + t * p.n + j, h[j]);
+        }
+    }
+    if (!p.h_last) return;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        if (j < left) p.h_last[at + j] = h[j];
+}
 
 // AGG: only the segment's product and state from zero, into P and H.
 template <typename T, int V, bool PACKED, bool SIG, bool AGG>
-__global__ __launch_bounds__(256) void rec_rows_fwd(const RecParams p)
+__global__ __launch_bounds__(256, 4) void rec_rows_fwd(const RecParams p)
 {
     using D = RowDims<T, V, false>;
     __shared__ float tot[2][D::kWaves][D::kBX * V][2];
@@ -200,9 +294,10 @@ __global__ __launch_bounds__(256) void rec_rows_fwd(const RecParams p)
     const long b = rest / p.S;
     const int c0 = (tile * D::kBX + cx) * V;
     const bool live = c0 < p.n;
-    const int c = live ? c0 : p.n - V;
-    const T *x = static_cast<const T *>(p.x) + b * p.x_b + c, *g = static_cast<const T *>(p.g) + b * p.g_b + c;
-    T *h_out = static_cast<T *>(p.h) + b * p.T * p.n + c;
+    // (the last lane of a row reaches back over the one before: both get the same values)
+    const int c = min(c0, p.n - V);
+    const T *x = static_cast<const T *>(p.x), *g = static_cast<const T *>(p.g);
+    T *h_out = static_cast<T *>(p.h);
     const long t1 = static_cast<long>(seg) * p.seg, t2 = min(t1 + p.seg, p.T);
     const long place = (b * p.S + seg) * p.n + c;
     float carry[V], carryP[V];
@@ -214,65 +309,85 @@ __global__ __launch_bounds__(256) void rec_rows_fwd(const RecParams p)
             else if (!PACKED && p.h_init) carry[j] = p.h_init[b * p.n + c + j];
         }
     }
-    Walk<PACKED> walk;
     int buf = 0;
     for (long t0 = t1; t0 < t2; t0 += D::kChunk, buf ^= 1) {
         const long mine = t0 + ty * D::kL;
-        const int cnt = static_cast<int>(max(0L, min(t2 - mine, static_cast<long>(D::kL))));
-        Lot<T, V, D::kL> lot;
+        const int last = static_cast<int>(min(t2 - t0, static_cast<long>(D::kChunk))) - 1, cnt = min(last + 1 - ty * D::kL, D::kL);
+        Raw<T, V> rx[D::kL], rg[D::kL];
+        Line<V> lx, lg, lo;
+        lx.begin(p, b * p.x_b, p.x_t, t0, last, ty * D::kL, c);
+        lg.begin(p, b * p.g_b, p.g_t, t0, last, ty * D::kL, c);
+        lo.begin(p, b * p.T * p.n, p.n, t0, last, ty * D::kL, c);
 #pragma unroll
-        for (int i = 0; i < D::kL; ++i) {
-            const long t = min(mine + i, t2 - 1);  // (tokens past the segment read its last, and are not used)
-            lot.x[i].load(x + t * p.x_t);
-            lot.g[i].load(g + t * p.g_t);
+        for (int i = 0; i < D::kL; ++i) {  // (tokens past the segment read its last, and are not used)
+            rx[i].load_any(x + lx.base + lx.first);
+            rg[i].load_any(g + lg.base + lg.first);
+            if (i + 1 < cnt) lx.first += lx.step, lg.first += lg.step;
         }
+        Marks<D::kL> marks;
+        if constexpr (PACKED) marks.find(p, t0, D::kChunk, mine);
         float P[V], h[V], in[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) P[j] = 1.0f, h[j] = 0.0f;
-        walk.begin(p, mine);
-        // one token on: FINAL with the true states, stored
-        auto step = [&](int i, bool final) __attribute__((always_inline)) {
-            const long t = mine + i;
-            if (i > 0) walk.to(p, t);
-            const bool out = PACKED && walk.at.seq < 0;
-            float o[V];
+        // One token on, of the product too until the true states are known.
+        auto step = [&](int i, bool product, bool cut) __attribute__((always_inline)) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 float a, w;
-                gates<T, SIG>(lot.g[i].get(j), a, w);
-                const float wx = SIG ? w * lot.x[i].get(j) : lot.x[i].get(j);
-                if (PACKED && (out || walk.at.first)) {
-                    P[j] = kCut;
-                    h[j] = out ? 0.0f : (p.h_init ? fmaf(a, p.h_init[static_cast<long>(walk.at.seq) * p.n + c + j], wx) : wx);
+                gates<T, SIG>(rg[i].get(j), a, w);
+                const float wx = SIG ? w * rx[i].get(j) : rx[i].get(j);
+                if (PACKED && cut && marks.none(i)) {
+                    P[j] = kCut, h[j] = 0.0f;
+                } else if (PACKED && cut && marks.first(i)) {
+                    P[j] = kCut, h[j] = fmaf(a, state_at(p, p.h_init, mine + i, c + j), wx);
                 } else {
-                    if (!final && !is_cut<PACKED>(P[j])) P[j] *= a;
+                    if (product && !(cut && is_cut<PACKED>(P[j]))) P[j] *= a;
                     h[j] = fmaf(a, h[j], wx);
                 }
-                o[j] = h[j];
-            }
-            if (!final || !live || out) return;
-            Raw<T, V> v;
-            v.set(o);
-            v.store(h_out + t * p.o_t);
-            if (p.h_last && (PACKED ? t + 1 == walk.at.end : t + 1 == p.T)) {
-                const long s = PACKED ? walk.at.seq : b;
-#pragma unroll
-                for (int j = 0; j < V; ++j) p.h_last[s * p.n + c + j] = o[j];
             }
         };
+        // (whole lots inside one sequence, which are most, go without a branch)
+        const bool whole = cnt == D::kL && !(PACKED && marks.any());
+        if (whole) {
 #pragma unroll
-        for (int i = 0; i < D::kL; ++i)
-            if (i < cnt) step(i, false);
+            for (int i = 0; i < D::kL; ++i) step(i, true, false);
+        } else {
+#pragma unroll
+            for (int i = 0; i < D::kL; ++i)
+                if (i < cnt) step(i, true, true);
+        }
         join_lots<V, D::kBX, D::kWaves, PACKED, false>(P, h, carry, carryP, in, tot[buf]);
         if (AGG) continue;
 #pragma unroll
-        for (int i = 0; i < D::kL; ++i) lot.g[i].forget();
+        for (int i = 0; i < D::kL; ++i) rg[i].forget(), rx[i].forget();
 #pragma unroll
         for (int j = 0; j < V; ++j) h[j] = in[j];
-        walk.begin(p, mine);
+        auto put = [&](int i) __attribute__((always_inline)) {
+            Raw<T, V> v;
+            v.set(h);
+            v.store_any(h_out + lo.base + (lo.first + i * lo.step));
+        };
+        auto keep = [&](long s) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < D::kL; ++i)
-            if (i < cnt) step(i, true);
+            for (int j = 0; j < V; ++j) p.h_last[s * p.n + c + j] = h[j];
+        };
+        if (whole) {
+#pragma unroll
+            for (int i = 0; i < D::kL; ++i) {
+                step(i, false, false);
+                if (live) put(i);
+            }
+            if (!PACKED && p.h_last && live && mine + D::kL == p.T) keep(b);
+        } else {
+#pragma unroll
+            for (int i = 0; i < D::kL; ++i) {
+                if (i >= cnt) continue;
+                step(i, false, true);
+                if (!live || (PACKED && marks.none(i))) continue;
+                put(i);
+                if (p.h_last && (PACKED ? marks.end(i) : mine + i + 1 == p.T)) keep(PACKED ? locate(p, mine + i).seq : b);
+            }
+        }
     }
     if (AGG && live && ty == 0) {
 #pragma unroll
@@ -282,7 +397,7 @@ __global__ __launch_bounds__(256) void rec_rows_fwd(const RecParams p)
 
 // A workgroup's chunk is a segment. AGG: its product, state from zero and flow from zero, into P, H and F.
 template <typename T, int V, bool PACKED, bool SIG, bool AGG>
-__global__ __launch_bounds__(512) void rec_rows_bwd(const RecParams p)
+__global__ __launch_bounds__(512, 4) void rec_rows_bwd(const RecParams p)
 {
     using D = RowDims<T, V, true>;
     constexpr int L = D::kL;
@@ -294,20 +409,25 @@ __global__ __launch_bounds__(512) void rec_rows_bwd(const RecParams p)
     const long b = rest / p.S;
     const int c0 = (tile * D::kBX + cx) * V;
     const bool live = c0 < p.n;
-    const int c = live ? c0 : p.n - V;
-    const T *x = static_cast<const T *>(p.x) + b * p.x_b + c, *g = static_cast<const T *>(p.g) + b * p.g_b + c;
-    const T *d = static_cast<const T *>(p.dh) + b * p.d_b + c;
+    // (the last lane of a row reaches back over the one before: both get the same values)
+    const int c = min(c0, p.n - V);
+    const T *x = static_cast<const T *>(p.x), *g = static_cast<const T *>(p.g), *d = static_cast<const T *>(p.dh);
     const long t1 = static_cast<long>(seg) * p.seg, t2 = min(t1 + p.seg, p.T);
     const long place = (b * p.S + seg) * p.n + c;
     const long mine = t1 + ty * L;
-    const int cnt = static_cast<int>(max(0L, min(t2 - mine, static_cast<long>(L))));
+    const int last = static_cast<int>(t2 - t1) - 1, cnt = min(last + 1 - ty * L, L);
     Raw<T, V> rx[L], rg[L], rd[L];
+    Line<V> lx, lg, ld, lo;
+    lx.begin(p, b * p.x_b, p.x_t, t1, last, ty * L, c);
+    lg.begin(p, b * p.g_b, p.g_t, t1, last, ty * L, c);
+    ld.begin(p, b * p.d_b, p.d_t, t1, last, ty * L, c);
+    lo.begin(p, b * p.T * p.n, p.n, t1, last, ty * L, c);
 #pragma unroll
     for (int i = 0; i < L; ++i) {
-        const long t = min(mine + i, t2 - 1);
-        rx[i].load(x + t * p.x_t);
-        rg[i].load(g + t * p.g_t);
-        rd[i].load(d + t * p.d_t);
+        rx[i].load_any(x + lx.base + lx.first);
+        rg[i].load_any(g + lg.base + lg.first);
+        rd[i].load_any(d + ld.base + ld.first);
+        if (i + 1 < cnt) lx.first += lx.step, lg.first += lg.step, ld.first += ld.step;
     }
     float enter[V], flow[V], one[V];
 #pragma unroll
@@ -321,60 +441,46 @@ __global__ __launch_bounds__(512) void rec_rows_bwd(const RecParams p)
             if (p.dh_last) flow[j] = p.dh_last[b * p.n + c + j];
         }
     }
-    // first tokens and last tokens of sequences among this thread's, and which are in one
-    unsigned firsts = 0, ends = 0, outs = 0;
-    int seq[L];
-    if constexpr (PACKED) {
-        Place w = locate(p, mine);
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            if (i > 0) {
-                if (mine + i >= w.next) w = locate(p, mine + i);
-                else w.first = false;
-            }
-            seq[i] = w.seq < 0 ? 0 : w.seq;
-            firsts |= (w.seq >= 0 && w.first ? 1u : 0u) << i;
-            ends |= (w.seq >= 0 && mine + i + 1 == w.end ? 1u : 0u) << i;
-            outs |= (w.seq < 0 ? 1u : 0u) << i;
-        }
-    }
-    auto first = [&](int i) { return PACKED && ((firsts >> i) & 1u); };
-    auto end = [&](int i) { return PACKED && ((ends >> i) & 1u); };
-    auto none = [&](int i) { return PACKED && ((outs >> i) & 1u); };
-    auto init_of = [&](int i, int j) { return p.h_init ? p.h_init[static_cast<long>(seq[i]) * p.n + c + j] : 0.0f; };
-    auto last_of = [&](int i, int j) { return p.dh_last ? p.dh_last[static_cast<long>(seq[i]) * p.n + c + j] : 0.0f; };
-    // the thread's stretch, forward and (f) backward
+    Marks<L> marks;
+    if constexpr (PACKED) marks.find(p, t1, D::kChunk, mine);
+    const bool whole = cnt == L && !(PACKED && marks.any());
+    // the thread's stretch, forward and (f) backward; CUT: with what a lot that is not whole has to look at
     float P[V], h[V], f[V], in[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) P[j] = 1.0f, h[j] = 0.0f, f[j] = 0.0f;
+    auto stretch = [&](auto cut) __attribute__((always_inline)) {
+        constexpr bool CUT = decltype(cut)::value;
 #pragma unroll
-    for (int i = 0; i < L; ++i) {
-        if (i >= cnt) continue;
+        for (int i = 0; i < L; ++i) {
+            if (CUT && i >= cnt) continue;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float a, w;
-            gates<T, SIG>(rg[i].get(j), a, w);
-            const float wx = SIG ? w * rx[i].get(j) : rx[i].get(j);
-            if (first(i) || none(i)) {
-                h[j] = none(i) ? 0.0f : fmaf(a, init_of(i, j), wx);
-                P[j] = kCut;
-            } else {
-                h[j] = fmaf(a, h[j], wx);
-                if (!is_cut<PACKED>(P[j])) P[j] *= a;
+            for (int j = 0; j < V; ++j) {
+                float a, w;
+                gates<T, SIG>(rg[i].get(j), a, w);
+                const float wx = SIG ? w * rx[i].get(j) : rx[i].get(j);
+                if (PACKED && CUT && (marks.first(i) || marks.none(i))) {
+                    h[j] = marks.none(i) ? 0.0f : fmaf(a, state_at(p, p.h_init, mine + i, c + j), wx);
+                    P[j] = kCut;
+                } else {
+                    h[j] = fmaf(a, h[j], wx);
+                    if (!(CUT && is_cut<PACKED>(P[j]))) P[j] *= a;
+                }
             }
         }
-    }
 #pragma unroll
-    for (int i = L - 1; i >= 0; --i) {
-        if (i >= cnt) continue;
+        for (int i = L - 1; i >= 0; --i) {
+            if (CUT && i >= cnt) continue;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float a, w;
-            gates<T, SIG>(rg[i].get(j), a, w);
-            const float e = rd[i].get(j) + (end(i) ? last_of(i, j) : f[j]);
-            f[j] = first(i) || none(i) ? 0.0f : a * e;
+            for (int j = 0; j < V; ++j) {
+                float a, w;
+                gates<T, SIG>(rg[i].get(j), a, w);
+                const float after = PACKED && CUT && marks.end(i) ? state_at(p, p.dh_last, mine + i, c + j) : f[j];
+                f[j] = PACKED && CUT && (marks.first(i) || marks.none(i)) ? 0.0f : a * (rd[i].get(j) + after);
+            }
         }
-    }
+    };
+    if (whole) stretch(std::false_type{});
+    else stretch(std::true_type{});
     float P2[V], out[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) P2[j] = P[j], one[j] = 1.0f;
@@ -393,58 +499,64 @@ __global__ __launch_bounds__(512) void rec_rows_bwd(const RecParams p)
     }
     if (!live) return;
 #pragma unroll
-    for (int i = 0; i < L; ++i) rg[i].forget(), rx[i].forget();
-    // what e is to be multiplied by for dg, of each token
-    float q[L][V];
+    for (int i = 0; i < L; ++i) rg[i].forget(), rx[i].forget(), rd[i].forget();
+    auto finish = [&](auto cut) __attribute__((always_inline)) {
+        constexpr bool CUT = decltype(cut)::value;
+        // what e is to be multiplied by for dg, of each token
+        float q[L][V];
 #pragma unroll
-    for (int i = 0; i < L; ++i) {
-        if (i >= cnt) continue;
+        for (int i = 0; i < L; ++i) {
+            if (CUT && i >= cnt) continue;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float a, w;
-            gates<T, SIG>(rg[i].get(j), a, w);
-            const float xv = rx[i].get(j), before = first(i) ? init_of(i, j) : in[j];
-            q[i][j] = SIG ? a * w * (before - xv) : a * before;
-            in[j] = fmaf(a, before, SIG ? w * xv : xv);
+            for (int j = 0; j < V; ++j) {
+                float a, w;
+                gates<T, SIG>(rg[i].get(j), a, w);
+                const float xv = rx[i].get(j), before = PACKED && CUT && marks.first(i) ? state_at(p, p.h_init, mine + i, c + j) : in[j];
+                q[i][j] = SIG ? a * w * (before - xv) : a * before;
+                in[j] = fmaf(a, before, SIG ? w * xv : xv);
+            }
         }
-    }
 #pragma unroll
-    for (int i = 0; i < L; ++i) rg[i].forget();
+        for (int i = 0; i < L; ++i) rg[i].forget();
 #pragma unroll
-    for (int i = L - 1; i >= 0; --i) {
-        if (i >= cnt) continue;
-        float dx[V], dg[V], fl[V];
+        for (int i = L - 1; i >= 0; --i) {
+            if (CUT && i >= cnt) continue;
+            float dx[V], dg[V], fl[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float a, w;
-            gates<T, SIG>(rg[i].get(j), a, w);
-            const float e = rd[i].get(j) + (end(i) ? last_of(i, j) : out[j]);
-            dx[j] = SIG ? w * e : e;
-            dg[j] = q[i][j] * e;
-            fl[j] = a * e;
-            out[j] = first(i) || none(i) ? 0.0f : fl[j];
+            for (int j = 0; j < V; ++j) {
+                float a, w;
+                gates<T, SIG>(rg[i].get(j), a, w);
+                const float e = rd[i].get(j) + (PACKED && CUT && marks.end(i) ? state_at(p, p.dh_last, mine + i, c + j) : out[j]);
+                dx[j] = SIG ? w * e : e;
+                dg[j] = q[i][j] * e;
+                fl[j] = a * e;
+                out[j] = PACKED && CUT && (marks.first(i) || marks.none(i)) ? 0.0f : fl[j];
+            }
+            if (PACKED && CUT && marks.none(i)) continue;
+            const auto at = lo.first + i * lo.step;
+            Raw<T, V> v;
+            v.set(dx);
+            v.store_any(static_cast<T *>(p.dx) + lo.base + at);
+            v.set(dg);
+            v.store_any(static_cast<T *>(p.dg) + lo.base + at);
+            if ((PACKED ? CUT : i == 0) && p.dh_init && (PACKED ? marks.first(i) : mine == 0)) {
+                const long s = PACKED ? locate(p, mine + i).seq : b;
+#pragma unroll
+                for (int j = 0; j < V; ++j) p.dh_init[s * p.n + c + j] = fl[j];
+            }
         }
-        if (none(i)) continue;
-        const long t = mine + i, at = b * p.T * p.n + t * p.o_t + c;
-        Raw<T, V> v;
-        v.set(dx);
-        v.store(static_cast<T *>(p.dx) + at);
-        v.set(dg);
-        v.store(static_cast<T *>(p.dg) + at);
-        if (p.dh_init && (PACKED ? first(i) : t == 0)) {
-            const long s = PACKED ? seq[i] : b;
-#pragma unroll
-            for (int j = 0; j < V; ++j) p.dh_init[s * p.n + c + j] = fl[j];
-        }
-    }
+    };
+    if (whole) finish(std::false_type{});
+    else finish(std::true_type{});
 }
 
 // ------------------------------------------------------------------ maps
 
-template <typename T, int V>
-constexpr int kMapU = V == 1 ? 8 : 2;  // vectors of V tokens a lane holds
-template <typename T, int V, int WPR>
-constexpr int kMapChunk = WPR * 64 * V * kMapU<T, V>;
+template <typename T>
+constexpr int kMapV = 16 / static_cast<int>(sizeof(T));  // tokens of a vector
+constexpr int kMapU = 2;                                 // vectors a lane holds
+template <typename T, int WPR>
+constexpr int kMapChunk = WPR * 64 * kMapV<T> * kMapU;
 
 // Inclusive join over the wave's lanes.
 __device__ __forceinline__ void wave_join(float &P, float &c)
@@ -496,23 +608,40 @@ __device__ __forceinline__ void wave_states(const float (&P)[U], const float (&c
     }
 }
 
-// V tokens from place i in the order of the recurrence.
+// V tokens from place i in the order of the recurrence, at any alignment; `fill`
+// past the last of the row's n.
 template <typename T, int V, bool REV>
 struct Run {
     Raw<T, V> r;
-    __device__ __forceinline__ void load(const T *row, long i, long n) { r.load(row + (REV ? n - V - i : i)); }
+    __device__ __forceinline__ void load(const T *row, long i, long n, float fill)
+    {
+        if (i + V <= n) {
+            r.load_any(row + (REV ? n - V - i : i));
+            return;
+        }
+        float f[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[REV ? V - 1 - j : j] = i + j < n ? widen1(row[REV ? n - 1 - i - j : i + j]) : fill;
+        r.set(f);
+    }
     __device__ __forceinline__ float get(int j) const { return r.get(REV ? V - 1 - j : j); }
     __device__ __forceinline__ void forget() { r.forget(); }
 };
 template <typename T, int V, bool REV>
 __device__ __forceinline__ void store_run(T *row, long i, long n, const float (&v)[V])
 {
+    if (i + V > n) {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (i + j < n) store1(row + (REV ? n - 1 - i - j : i + j), v[j]);
+        return;
+    }
     float o[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) o[j] = v[REV ? V - 1 - j : j];
     Raw<T, V> r;
     r.set(o);
-    r.store(row + (REV ? n - V - i : i));
+    r.store_any(row + (REV ? n - V - i : i));
 }
 
 // Over the workgroup's WPR waves of one row: the state before this wave given
@@ -542,10 +671,10 @@ __device__ __forceinline__ float join_waves(float wP, float wc, float &carry, fl
     return in;
 }
 
-template <typename T, int V, int WPR, bool REV, bool SIG, bool AGG>
+template <typename T, int WPR, bool REV, bool SIG, bool AGG>
 __global__ __launch_bounds__(256) void rec_maps_fwd(const RecParams p, long units)
 {
-    constexpr int U = kMapU<T, V>, kRowsOf = 4 / WPR, kChunk = kMapChunk<T, V, WPR>;
+    constexpr int V = kMapV<T>, U = kMapU, kRowsOf = 4 / WPR, kChunk = kMapChunk<T, WPR>;
     __shared__ float tot[2][4][2];
     const int lane = threadIdx.x % 64, wave = WPR == 1 ? 0 : threadIdx.x / 64;
     const long unit = (p.first + blockIdx.x) * kRowsOf + (WPR == 1 ? threadIdx.x / 64 : 0);
@@ -565,21 +694,19 @@ __global__ __launch_bounds__(256) void rec_maps_fwd(const RecParams p, long unit
         auto at = [&](int u) { return t0 + (static_cast<long>(wave * U + u) * 64 + lane) * V; };
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const long t = min(at(u), p.T - V);  // (segments end at whole vectors: V divides T or is 1)
-            rx[u].load(x, t, p.T);
-            rg[u].load(g, t, p.T);
+            // (segments end with whole chunks or with the row)
+            rx[u].load(x, at(u), p.T, 0.0f);
+            rg[u].load(g, at(u), p.T, idle<T, SIG>());
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             P[u] = 1.0f, h[u] = 0.0f;
-            if (at(u) < t2) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    float a, w;
-                    gates<T, SIG>(rg[u].get(j), a, w);
-                    h[u] = fmaf(a, h[u], SIG ? w * rx[u].get(j) : rx[u].get(j));
-                    P[u] *= a;
-                }
+            for (int j = 0; j < V; ++j) {
+                float a, w;
+                gates<T, SIG>(rg[u].get(j), a, w);
+                h[u] = fmaf(a, h[u], SIG ? w * rx[u].get(j) : rx[u].get(j));
+                P[u] *= a;
             }
         }
         float wP, wc;
@@ -591,7 +718,6 @@ __global__ __launch_bounds__(256) void rec_maps_fwd(const RecParams p, long unit
         for (int u = 0; u < U; ++u) rg[u].forget();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (at(u) >= t2) continue;
             float o[V], v = in[u];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
@@ -600,16 +726,16 @@ __global__ __launch_bounds__(256) void rec_maps_fwd(const RecParams p, long unit
                 o[j] = v = fmaf(a, v, SIG ? w * rx[u].get(j) : rx[u].get(j));
             }
             store_run<T, V, REV>(h_out, at(u), p.T, o);
-            if (p.h_last && at(u) + V == p.T) p.h_last[row] = v;
+            if (p.h_last && at(u) < p.T && at(u) + V >= p.T) p.h_last[row] = v;  // (past the last token it stays)
         }
     }
     if (AGG && lane == 0 && wave == 0) p.P[place] = carryP, p.H[place] = carry;
 }
 
-template <typename T, int V, int WPR, bool REV, bool SIG, bool AGG>
+template <typename T, int WPR, bool REV, bool SIG, bool AGG>
 __global__ __launch_bounds__(256) void rec_maps_bwd(const RecParams p, long units)
 {
-    constexpr int U = kMapU<T, V>, kRowsOf = 4 / WPR;
+    constexpr int V = kMapV<T>, U = kMapU, kRowsOf = 4 / WPR;
     __shared__ float tot[2][4][2];
     const int lane = threadIdx.x % 64, wave = WPR == 1 ? 0 : threadIdx.x / 64;
     const long unit = (p.first + blockIdx.x) * kRowsOf + (WPR == 1 ? threadIdx.x / 64 : 0);
@@ -618,16 +744,14 @@ __global__ __launch_bounds__(256) void rec_maps_bwd(const RecParams p, long unit
     const long row = unit / p.S, b = row / p.n, c = row % p.n;
     const T *x = static_cast<const T *>(p.x) + b * p.x_b + c * p.x_t, *g = static_cast<const T *>(p.g) + b * p.g_b + c * p.g_t;
     const T *d = static_cast<const T *>(p.dh) + b * p.d_b + c * p.d_t;
-    const long t1 = static_cast<long>(seg) * p.seg, t2 = min(t1 + p.seg, p.T);
-    const long place = (b * p.S + seg) * p.n + c;
+    const long t1 = static_cast<long>(seg) * p.seg, place = (b * p.S + seg) * p.n + c;
     auto at = [&](int u) { return t1 + (static_cast<long>(wave * U + u) * 64 + lane) * V; };
     Run<T, V, REV> rx[U], rg[U], rd[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const long t = min(at(u), p.T - V);
-        rx[u].load(x, t, p.T);
-        rg[u].load(g, t, p.T);
-        rd[u].load(d, t, p.T);
+        rx[u].load(x, at(u), p.T, 0.0f);
+        rg[u].load(g, at(u), p.T, idle<T, SIG>());
+        rd[u].load(d, at(u), p.T, 0.0f);
     }
     float enter = 0.0f, flow = 0.0f, product = 1.0f, unused = 1.0f;
     if (!AGG) {
@@ -639,18 +763,16 @@ __global__ __launch_bounds__(256) void rec_maps_bwd(const RecParams p, long unit
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         P[u] = 1.0f, h[u] = 0.0f, f[u] = 0.0f;
-        if (at(u) < t2) {
-            float a[V];
+        float a[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float w;
-                gates<T, SIG>(rg[u].get(j), a[j], w);
-                h[u] = fmaf(a[j], h[u], SIG ? w * rx[u].get(j) : rx[u].get(j));
-                P[u] *= a[j];
-            }
-#pragma unroll
-            for (int j = V - 1; j >= 0; --j) f[u] = a[j] * (rd[u].get(j) + f[u]);
+        for (int j = 0; j < V; ++j) {
+            float w;
+            gates<T, SIG>(rg[u].get(j), a[j], w);
+            h[u] = fmaf(a[j], h[u], SIG ? w * rx[u].get(j) : rx[u].get(j));
+            P[u] *= a[j];
         }
+#pragma unroll
+        for (int j = V - 1; j >= 0; --j) f[u] = a[j] * (rd[u].get(j) + f[u]);
     }
     float G[U];
 #pragma unroll
@@ -672,7 +794,6 @@ __global__ __launch_bounds__(256) void rec_maps_bwd(const RecParams p, long unit
     for (int u = 0; u < U; ++u) rg[u].forget();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        if (at(u) >= t2) continue;
         float a[V], w[V], q[V], dx[V], dg[V], v = in[u], e = out[u];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -699,7 +820,8 @@ __global__ __launch_bounds__(256) void rec_maps_bwd(const RecParams p, long unit
 // How a call is cut, and which kernels run it.
 struct RecPlan {
     bool maps, packed, sig, rev;
-    int v;    // elements read at once
+    bool few;  // forward of few tokens: a thread walks over them
+    int v;    // token rows: channels a lane holds
     int wpr;  // maps: waves a row
 };
 
@@ -728,9 +850,27 @@ int with_flags(F &&f, bool first, B... rest)
     return with_flags([&](auto... r) { return f(std::false_type{}, r...); }, rest...);
 }
 
+template <typename T>
+int rec_run_few(RecParams p, const RecPlan &plan, long batch, hipStream_t s)
+{
+    auto go = [&](auto vec) {
+        constexpr int V = decltype(vec)::value;
+        p.tiles = (p.n + V - 1) / V;
+        const long threads = batch * p.tiles;
+        return rec_launch(p, (threads + 255) / 256, 256, [&](const RecParams &q, dim3 grid) {
+            if (plan.sig) rec_few<T, V, true><<<grid, dim3(256), 0, s>>>(q, threads);
+            else rec_few<T, V, false><<<grid, dim3(256), 0, s>>>(q, threads);
+        });
+    };
+    return plan.v > 1 ? go(std::integral_constant<int, kRowV<T>>{}) : go(std::integral_constant<int, 1>{});
+}
+
 template <typename T, bool BWD>
 int rec_run(const RecParams &p, const RecPlan &plan, long batch, bool agg, hipStream_t s)
 {
+    if constexpr (!BWD) {
+        if (plan.few) return rec_run_few<T>(p, plan, batch, s);
+    }
     if (!plan.maps) {
         auto go = [&](auto vec) {
             constexpr int V = decltype(vec)::value;
@@ -745,26 +885,19 @@ int rec_run(const RecParams &p, const RecPlan &plan, long batch, bool agg, hipSt
                 },
                 plan.packed, plan.sig, agg);
         };
-        return plan.v == 4 ? go(std::integral_constant<int, 4>{}) : go(std::integral_constant<int, 1>{});
+        return plan.v > 1 ? go(std::integral_constant<int, kRowV<T>>{}) : go(std::integral_constant<int, 1>{});
     }
     const long units = batch * p.n * p.S;
-    auto go = [&](auto vec) {
-        constexpr int V = decltype(vec)::value;
-        return with_flags(
-            [&](auto wide, auto rev, auto sig, auto only) {
-                constexpr int W = decltype(wide)::value ? 4 : 1;
-                constexpr bool R = decltype(rev)::value, G = decltype(sig)::value, A = decltype(only)::value;
-                return rec_launch(p, (units * W + 3) / 4, 256, [&](const RecParams &q, dim3 grid) {
-                    if constexpr (BWD) rec_maps_bwd<T, V, W, R, G, A><<<grid, dim3(256), 0, s>>>(q, units);
-                    else rec_maps_fwd<T, V, W, R, G, A><<<grid, dim3(256), 0, s>>>(q, units);
-                });
-            },
-            plan.wpr == 4, plan.rev, plan.sig, agg);
-    };
-    if constexpr (sizeof(T) == 2) {
-        if (plan.v == 8) return go(std::integral_constant<int, 8>{});
-    }
-    return plan.v == 4 ? go(std::integral_constant<int, 4>{}) : go(std::integral_constant<int, 1>{});
+    return with_flags(
+        [&](auto wide, auto rev, auto sig, auto only) {
+            constexpr int W = decltype(wide)::value ? 4 : 1;
+            constexpr bool R = decltype(rev)::value, G = decltype(sig)::value, A = decltype(only)::value;
+            return rec_launch(p, (units * W + 3) / 4, 256, [&](const RecParams &q, dim3 grid) {
+                if constexpr (BWD) rec_maps_bwd<T, W, R, G, A><<<grid, dim3(256), 0, s>>>(q, units);
+                else rec_maps_fwd<T, W, R, G, A><<<grid, dim3(256), 0, s>>>(q, units);
+            });
+        },
+        plan.wpr == 4, plan.rev, plan.sig, agg);
 }
 
 }  // namespace ssm2d_impl

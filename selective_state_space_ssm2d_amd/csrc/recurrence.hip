@@ -80,30 +80,33 @@ int check_rec(const ssm2d_recurrence_shape *a, uint32_t flags)
     return SSM2D_OK;
 }
 
-// How many tokens a segment has (whole chunks), for vectors of v elements.
+// Token rows that are walked over by a thread for each few channels.
+bool few_tokens(const ssm2d_recurrence_shape &a, uint32_t flags) { return a.tokens <= 8 && a.n_seq == 0 && !(flags & SSM2D_RECUR_MAPS); }
+
+// How many tokens a segment has (whole chunks); token rows: for v channels a lane.
 struct Cut {
     long seg;
     int S, tiles, wpr;
 };
-Cut cut_tokens(const ssm2d_recurrence_shape &a, uint32_t flags, bool bf16, bool bwd, int v)
+template <typename T, bool BWD>
+Cut cut_tokens(const ssm2d_recurrence_shape &a, uint32_t flags, int v)
 {
     Cut c{};
     long chunk, groups;
     if (flags & SSM2D_RECUR_MAPS) {
-        const long one = 64L * v * (v == 1 ? 8 : 2);  // (kMapChunk)
-        c.wpr = a.tokens <= one ? 1 : 4;
-        chunk = one * c.wpr;
+        c.wpr = a.tokens <= kMapChunk<T, 1> ? 1 : 4;
+        chunk = c.wpr == 1 ? kMapChunk<T, 1> : kMapChunk<T, 4>;
         groups = (a.batch * a.channels * c.wpr + 3) / 4;
     } else {
-        const int bx = v == 4 ? 16 : 32, by = (bwd ? 512 : 256) / bx;  // (RowDims)
-        chunk = by * (bwd ? 8 : (bf16 || v == 1 ? 16 : 8));
+        const int bx = v > 1 ? RowDims<T, kRowV<T>, BWD>::kBX : RowDims<T, 1, BWD>::kBX;
+        chunk = v > 1 ? RowDims<T, kRowV<T>, BWD>::kChunk : RowDims<T, 1, BWD>::kChunk;
         c.tiles = static_cast<int>((a.channels + bx * v - 1) / (bx * v));
         groups = a.batch * c.tiles;
     }
     const long chunks = (a.tokens + chunk - 1) / chunk;
     // The backward has to hold what it walks over twice: a segment is a chunk.
     // The forward walks where its channels alone make enough workgroups.
-    long segs = bwd ? chunks : (groups >= 512 ? 1 : std::min(chunks, (1024 + groups - 1) / std::max(groups, 1L)));
+    long segs = BWD ? chunks : (groups >= 512 ? 1 : std::min(chunks, (2048 + groups - 1) / std::max(groups, 1L)));
     segs = std::max(segs, 1L);
     c.seg = (chunks + segs - 1) / segs * chunk;
     c.S = static_cast<int>((a.tokens + c.seg - 1) / std::max(c.seg, 1L));
@@ -112,22 +115,29 @@ Cut cut_tokens(const ssm2d_recurrence_shape &a, uint32_t flags, bool bf16, bool 
 
 constexpr int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
-int64_t rec_workspace(const ssm2d_recurrence_shape *a, uint32_t flags, bool bf16, bool bwd)
+// Whether workgroups read states that another one writes, so that one written in
+// place is read from a copy: packed sequences begin and end anywhere, and the
+// last lane of a row reaches back over channels of other lanes.
+template <typename T>
+bool shares_states(const ssm2d_recurrence_shape &a, uint32_t flags)
+{
+    return a.n_seq > 0 || (!(flags & SSM2D_RECUR_MAPS) && a.channels % kRowV<T> != 0);
+}
+
+template <typename T, bool BWD>
+int64_t rec_workspace(const ssm2d_recurrence_shape *a, uint32_t flags)
 {
     const int st = check_rec(a, flags);
     if (st != SSM2D_OK) return -st;
     if (a->batch == 0 || a->tokens == 0 || a->channels == 0) return 0;
     int64_t bytes = 0;
-    for (const int v : {8, 4, 1}) {
-        if (v == 8 && !(bf16 && (flags & SSM2D_RECUR_MAPS))) continue;
-        const int64_t S = cut_tokens(*a, flags, bf16, bwd, v).S;
-        if (S > 1) bytes = std::max(bytes, (bwd ? 3 : 2) * a->batch * S * a->channels * 4);
+    for (const int v : {kRowV<T>, 1}) {
+        const int64_t S = cut_tokens<T, BWD>(*a, flags, v).S;
+        if (S > 1) bytes = std::max(bytes, (BWD ? 3 : 2) * a->batch * S * a->channels * 4);
     }
-    if (a->n_seq > 0) bytes = round_up(bytes, 16) + a->n_seq * a->channels * 4;  // (a copy of a state that is written in place)
+    if (shares_states<T>(*a, flags) && (BWD || !few_tokens(*a, flags))) bytes = round_up(bytes, 16) + std::max(a->n_seq, a->batch) * a->channels * 4;
     return bytes;
 }
-
-bool rows_by(const void *ptr, int64_t s0, int64_t s1, int v, size_t size) { return !off_by(ptr, v * size) && s0 % v == 0 && s1 % v == 0; }
 
 template <typename T, bool BWD>
 int rec_entry(const T *x, const T *g, const float *h_init, const int32_t *cu, const T *dh, const float *dh_last, T *out, T *dg, float *last,
@@ -153,50 +163,36 @@ int rec_entry(const T *x, const T *g, const float *h_init, const int32_t *cu, co
     if (off_by(x, sizeof(T)) || off_by(g, sizeof(T)) || off_by(out, sizeof(T)) || off_by(dh, sizeof(T)) || off_by(dg, sizeof(T)) ||
         off_by(ws, 16) || (a->n_seq > 0 && off_by(cu, 4)))
         return SSM2D_ERR_MISALIGNED;
-    const int64_t need = rec_workspace(a, flags, sizeof(T) == 2, BWD);
+    const int64_t need = rec_workspace<T, BWD>(a, flags);
     if (need > 0 && (!ws || ws_bytes < need)) return SSM2D_ERR_NOMEM;
     RecPlan plan{};
     plan.maps = flags & SSM2D_RECUR_MAPS, plan.packed = a->n_seq > 0, plan.sig = flags & SSM2D_RECUR_SIGMOID;
     plan.rev = flags & SSM2D_RECUR_REVERSE;
-    plan.v = 1;
-    for (const int v : {8, 4}) {
-        if (v == 8 && !(sizeof(T) == 2 && plan.maps)) continue;
-        const bool fits = (plan.maps ? T_ : n) % v == 0 && rows_by(x, a->x_stride[0], a->x_stride[1], v, sizeof(T)) &&
-                          rows_by(g, a->g_stride[0], a->g_stride[1], v, sizeof(T)) && rows_by(out, 0, 0, v, sizeof(T)) &&
-                          (!BWD || (rows_by(dh, a->dh_stride[0], a->dh_stride[1], v, sizeof(T)) && rows_by(dg, 0, 0, v, sizeof(T))));
-        if (fits) {
-            plan.v = v;
-            break;
-        }
-    }
-    const Cut c = cut_tokens(*a, flags, sizeof(T) == 2, BWD, plan.v);
+    // (a chunk of tokens spans less than 2^31 bytes)
+    const int64_t far = std::max({a->x_stride[1], a->g_stride[1], a->dh_stride[1], a->channels});
+    plan.v = n >= kRowV<T> && far < (int64_t{1} << 20) ? kRowV<T> : 1;
+    plan.few = !BWD && few_tokens(*a, flags);
+    const Cut c = cut_tokens<T, BWD>(*a, flags, plan.v);
     plan.wpr = c.wpr;
     RecParams p{};
     p.x = x, p.g = g, p.dh = dh, p.h_init = h_init, p.dh_last = dh_last, p.cu = cu;
     p.T = T_, p.seg = c.seg, p.S = c.S, p.n = static_cast<int>(n), p.n_seq = static_cast<int>(a->n_seq), p.tiles = c.tiles;
     p.x_b = a->x_stride[0], p.g_b = a->g_stride[0], p.d_b = a->dh_stride[0];
-    p.x_t = a->x_stride[1], p.g_t = a->g_stride[1], p.d_t = a->dh_stride[1], p.o_t = n;
-    T *o = out, *o2 = dg;
-    if (plan.rev && !plan.maps) {  // (from the last token on)
-        p.x = x + (T_ - 1) * p.x_t, p.g = g + (T_ - 1) * p.g_t;
-        if (BWD) p.dh = dh + (T_ - 1) * p.d_t, o2 += (T_ - 1) * n;
-        o += (T_ - 1) * n;
-        p.x_t = -p.x_t, p.g_t = -p.g_t, p.d_t = -p.d_t, p.o_t = -n;
-    }
-    if (BWD) p.dx = o, p.dg = o2, p.dh_init = last;
-    else p.h = o, p.h_last = last;
+    p.x_t = a->x_stride[1], p.g_t = a->g_stride[1], p.d_t = a->dh_stride[1], p.rev = plan.rev;
+    if (BWD) p.dx = out, p.dg = dg, p.dh_init = last;
+    else p.h = out, p.h_last = last;
     const long plane = B * p.S * n;
     p.P = static_cast<float *>(ws), p.H = p.P + plane, p.F = BWD ? p.H + plane : nullptr;
-    if (plan.packed && last) {
-        if (last == state) {  // other workgroups read what one writes: from a copy
+    if (last && last == state) {
+        if (shares_states<T>(*a, flags) && !plan.few) {
             float *copy = reinterpret_cast<float *>(static_cast<char *>(ws) + (need - states * 4));
             copy_floats<<<blocks(states), dim3(256), 0, s>>>(state, copy, states);
             if ((st = launched()) != SSM2D_OK) return st;
             (BWD ? p.dh_last : p.h_init) = copy;
-        } else {
-            rec_empty<<<blocks(states), dim3(256), 0, s>>>(p, state, last);
-            if ((st = launched()) != SSM2D_OK) return st;
         }
+    } else if (plan.packed && last) {
+        rec_empty<<<blocks(states), dim3(256), 0, s>>>(p, state, last);
+        if ((st = launched()) != SSM2D_OK) return st;
     }
     if (p.S > 1) {
         if ((st = rec_run<T, BWD>(p, plan, B, true, s)) != SSM2D_OK) return st;
@@ -220,19 +216,19 @@ extern "C" {
 
 int64_t ssm2d_recurrence_fwd_workspace(const ssm2d_recurrence_shape *shape, uint32_t flags)
 {
-    return ssm2d_impl::rec_workspace(shape, flags, false, false);
+    return ssm2d_impl::rec_workspace<float, false>(shape, flags);
 }
 int64_t ssm2d_recurrence_fwd_workspace_bf16(const ssm2d_recurrence_shape *shape, uint32_t flags)
 {
-    return ssm2d_impl::rec_workspace(shape, flags, true, false);
+    return ssm2d_impl::rec_workspace<uint16_t, false>(shape, flags);
 }
 int64_t ssm2d_recurrence_bwd_workspace(const ssm2d_recurrence_shape *shape, uint32_t flags)
 {
-    return ssm2d_impl::rec_workspace(shape, flags, false, true);
+    return ssm2d_impl::rec_workspace<float, true>(shape, flags);
 }
 int64_t ssm2d_recurrence_bwd_workspace_bf16(const ssm2d_recurrence_shape *shape, uint32_t flags)
 {
-    return ssm2d_impl::rec_workspace(shape, flags, true, true);
+    return ssm2d_impl::rec_workspace<uint16_t, true>(shape, flags);
 }
 
 int ssm2d_recurrence_fwd(const float *x, const float *g, const float *h_init, const int32_t *cu_seqlens, float *h, float *h_last,

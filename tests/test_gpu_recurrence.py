@@ -264,8 +264,9 @@ def test_step_is_the_recurrence(batch, n, gates, dtype):
 
 
 def test_states_in_place():
-    for lens, b, t in ((None, 2, 900), (None, 2, 60), ([400, 0, 500, 1], 1, 901), ([20, 0, 30], 1, 50)):
-        s = make(b, t, 64, "f32", 10, lens=lens)
+    for lens, b, t, n in ((None, 2, 900, 64), (None, 2, 60, 64), ([400, 0, 500, 1], 1, 901, 64), ([20, 0, 30], 1, 50, 64), (None, 2, 60, 65), (None, 90, 300, 527),
+                          (None, 3, 900, 67), ([20, 0, 30], 1, 50, 37), (None, 3, 1, 37), (None, 3, 5, 2)):
+        s = make(b, t, n, "f32", 10, lens=lens)
         h, last = pkg.recurrence_fwd(s["x"], s["g"], h_init=s["h_init"], cu_seqlens=s["cu"], return_last_state=True)
         st = s["h_init"].clone()
         h2 = pkg.recurrence_fwd(s["x"], s["g"], h_init=st, cu_seqlens=s["cu"], h_last=st)
