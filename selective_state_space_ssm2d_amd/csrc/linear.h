@@ -20,10 +20,10 @@ struct GemmParams {
     long a_bs, b_bs;  // stride of the batch, or of the stretches of k that are summed (kb > 1)
     int M, N, K;
     int kb;           // stretches of K
-    int tiles_m, tiles_n;
+    unsigned tiles_m, tiles_n, total;  // total: of all splits and batch entries
     long batch;
-    int splits;       // parts of the sum, each by workgroups of its own
-    long steps, per;  // steps of BK in all stretches, and of one split
+    unsigned splits;  // parts of the sum, each by workgroups of its own
+    int steps, per;   // steps of BK in all stretches, and of one split
     // epilogue
     const float *bias;  // along n, or with bias_m along m
     int bias_m, act;
@@ -33,7 +33,7 @@ struct GemmParams {
     long c_ld, c_bs;
     int straight;     // bf16 operands can be loaded straight to LDS
     float *part;      // splits > 1: [split][batch][M][N rounded up to 4]
-    long first;       // the launch's first workgroup
+    unsigned first;   // the launch's first workgroup
 };
 
 template <typename T>
@@ -43,57 +43,68 @@ constexpr int kStep = sizeof(T) == 2 ? 64 : 32;  // k of a step
 
 // ------------------------------------------------------------------ epilogue
 
+template <typename T>
+constexpr int kWide = 16 / static_cast<int>(sizeof(T));  // elements of C that a lane finishes at once
+
 template <typename T, int ACT>
-__device__ __forceinline__ void act4(float (&v)[4])
+__device__ __forceinline__ void act_all(float (&v)[kWide<T>])
 {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = activate<T, ACT>(v[j]);
+    for (int j = 0; j < kWide<T>; ++j) v[j] = activate<T, ACT>(v[j]);
 }
 
-// Four neighbours of row m from column n on.
+// The bias of columns n .. n + kWide - 1.
 template <typename T>
-__device__ __forceinline__ void finish4(const GemmParams &p, long b, int m, int n, float (&v)[4])
+__device__ __forceinline__ void column_bias(const GemmParams &p, int n, float (&b)[kWide<T>])
 {
-    if (m >= p.M || n >= p.N) return;
-    if (p.bias) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] += p.bias[p.bias_m ? m : min(n + j, p.N - 1)];
-    }
+    for (int j = 0; j < kWide<T>; ++j) b[j] = p.bias && !p.bias_m && n < p.N ? p.bias[min(n + j, p.N - 1)] : 0.0f;
+}
+
+// Neighbours of row m from column n on, `bias` their columns'.
+template <typename T>
+__device__ __forceinline__ void finish(const GemmParams &p, long b, int m, int n, float (&v)[kWide<T>], const float (&bias)[kWide<T>])
+{
+    constexpr int V = kWide<T>;
+    if (m >= p.M || n >= p.N) return;
+    const float row = p.bias && p.bias_m ? p.bias[m] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] += p.bias_m ? row : bias[j];
     const long at = b * p.c_bs + static_cast<long>(m) * p.c_ld + n;
-    T *c = static_cast<T *>(p.c) + at;
-    const bool four = n + 4 <= p.N;
-    auto put = [&](T *dst) __attribute__((always_inline)) {
-        if (four) {
-            Raw<T, 4> r;
+    const bool whole = n + V <= p.N;
+    auto put = [&](void *c) __attribute__((always_inline)) {
+        T *dst = static_cast<T *>(c) + at;
+        if (whole) {
+            Raw<T, V> r;
             r.set(v);
             r.store_any(dst);
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < V; ++j)
                 if (n + j < p.N) store1(dst + j, v[j]);
         }
     };
-    if (p.pre) put(static_cast<T *>(p.pre) + at);
+    if (p.pre) put(p.pre);
     switch (p.act) {
-    case SSM2D_ACT_RELU: act4<T, SSM2D_ACT_RELU>(v); break;
-    case SSM2D_ACT_SILU: act4<T, SSM2D_ACT_SILU>(v); break;
-    case SSM2D_ACT_GELU: act4<T, SSM2D_ACT_GELU>(v); break;
+    case SSM2D_ACT_RELU: act_all<T, SSM2D_ACT_RELU>(v); break;
+    case SSM2D_ACT_SILU: act_all<T, SSM2D_ACT_SILU>(v); break;
+    case SSM2D_ACT_GELU: act_all<T, SSM2D_ACT_GELU>(v); break;
     default: break;
     }
     if (p.res) {
         const T *r = static_cast<const T *>(p.res) + b * p.r_bs + static_cast<long>(m) * p.r_ld + n;
-        if (four) {
-            Raw<T, 4> w;
+        if (whole) {
+            Raw<T, V> w;
             w.load_any(r);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] += w.get(j);
+            for (int j = 0; j < V; ++j) v[j] += w.get(j);
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < V; ++j)
                 if (n + j < p.N) v[j] += widen1(r[j]);
         }
     }
-    put(c);
+    put(p.c);
 }
 
 // ------------------------------------------------------------------ operands
@@ -203,9 +214,9 @@ struct TilePlace {
 template <int BM, int BN>
 __device__ __forceinline__ TilePlace tile_place(const GemmParams &p)
 {
-    const long total = static_cast<long>(p.tiles_m) * p.tiles_n * p.batch * p.splits;
-    long id = p.first + blockIdx.x;
-    const long each = total / 8, more = total % 8, die = id % 8;
+    const unsigned total = p.total, each = total / 8, more = total % 8;
+    unsigned id = p.first + blockIdx.x;
+    const unsigned die = id % 8;
     id = die * each + min(die, more) + id / 8;
     TilePlace t;
     t.n0 = static_cast<int>(id % p.tiles_n) * BN;
@@ -217,25 +228,49 @@ __device__ __forceinline__ TilePlace tile_place(const GemmParams &p)
     return t;
 }
 
+// A wave's accumulators to memory, by way of LDS: there its lanes hold 16 rows by
+// four columns each, and whole runs of rows go out (four times fewer requests).
+// Every wave of the workgroup calls it, when none reads the operands' tiles any more.
 template <typename T, int BM, int BN, int WM, int WN>
-__device__ __forceinline__ void finish_tile(const GemmParams &p, const TilePlace &t, facc (&acc)[WM / 16][WN / 16])
+__device__ __forceinline__ void finish_tile(const GemmParams &p, const TilePlace &t, facc (&acc)[WM / 16][WN / 16], void *lds, int slot)
 {
+    constexpr int V = kWide<T>, kLd = WN + 4, kLanes = WN / V, kRowsOnce = 64 / kLanes;
     const int l = threadIdx.x % 64, wave = threadIdx.x / 64;
-    const int m0 = t.m0 + wave / (BN / WN) * WM + l % 16, n0 = t.n0 + wave % (BN / WN) * WN + 4 * (l / 16);
+    const int m0 = t.m0 + wave / (BN / WN) * WM, n = t.n0 + wave % (BN / WN) * WN + l % kLanes * V;
+    float *mine = static_cast<float *>(lds) + slot * 32 * kLd;  // 32 rows at a time
     const long ldp = (p.N + 3) / 4 * 4;
+    float bias[V];
+    column_bias<T>(p, n, bias);
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < WM / 16; ++i)
+    for (int half = 0; half < WM / 32; ++half) {
 #pragma unroll
-        for (int j = 0; j < WN / 16; ++j) {
-            const int m = m0 + i * 16, n = n0 + j * 16;
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < WN / 16; ++j)
+                *reinterpret_cast<facc *>(mine + (i * 16 + l % 16) * kLd + j * 16 + 4 * (l / 16)) = acc[half * 2 + i][j];
+        // (its own lanes' writes, in order before its reads: no barrier)
+#pragma unroll 2
+        for (int r = l / kLanes; r < 32; r += kRowsOnce) {
+            const int m = m0 + half * 32 + r;
+            float v[V];
+#pragma unroll
+            for (int k = 0; k < V / 4; ++k) {
+                const facc f = *reinterpret_cast<const facc *>(mine + r * kLd + l % kLanes * V + 4 * k);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[4 * k + j] = f[j];
+            }
             if (p.splits > 1) {
-                if (m < p.M && n < p.N)
-                    *reinterpret_cast<facc *>(p.part + ((t.split * p.batch + t.b) * p.M + m) * ldp + n) = acc[i][j];
+                if (m >= p.M) continue;
+                float *part = p.part + ((static_cast<long>(t.split) * p.batch + t.b) * p.M + m) * ldp + n;
+#pragma unroll
+                for (int k = 0; k < V / 4; ++k)
+                    if (n + 4 * k < p.N) *reinterpret_cast<facc *>(part + 4 * k) = facc{v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]};
             } else {
-                float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                finish4<T>(p, t.b, m, n, v);
+                finish<T>(p, t.b, m, n, v, bias);
             }
         }
+    }
 }
 
 // Any alignment: operands go through registers to LDS, the next step's read
@@ -246,15 +281,17 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmParams p)
     constexpr int NP = kParts<T>, BK = kStep<T>, WM = BM / 2, WN = BN / 2;
     using TA = OperandTile<A_KC, BM, BK, NP>;
     using TB = OperandTile<B_KC, BN, BK, NP>;
-    __shared__ __align__(16) uint16_t sa[TA::kElems], sb[TB::kElems];
+    // (the epilogue's place too)
+    __shared__ __align__(16) uint16_t tiles[std::max(TA::kElems + TB::kElems, 4 * 32 * (WN + 4) * 2)];
+    uint16_t *const sa = tiles, *const sb = tiles + TA::kElems;
     const TilePlace t = tile_place<BM, BN>(p);
     const T *A = static_cast<const T *>(p.a), *B = static_cast<const T *>(p.b);
     if (p.kb == 1) A += t.b * p.a_bs, B += t.b * p.b_bs;
-    const long s1 = t.split * p.per, s2 = min(s1 + p.per, p.steps), each = (p.K + BK - 1) / BK;
+    const int s1 = t.split * p.per, s2 = min(s1 + p.per, p.steps), each = (p.K + BK - 1) / BK;
     constexpr int CA = BM * BK / 8 / 256, CB = BN * BK / 8 / 256;
     Chunk<T> ra[CA], rb[CB];
-    auto fetch = [&](long s) __attribute__((always_inline)) {
-        const long kb = p.kb == 1 ? 0 : s / each, k0 = (s - kb * each) * BK;
+    auto fetch = [&](int s) __attribute__((always_inline)) {
+        const int kb = p.kb == 1 ? 0 : s / each, k0 = (s - kb * each) * BK;
         const T *ap = A + kb * p.a_bs, *bp = B + kb * p.b_bs;
         if (p.kb == 1) ap = A, bp = B;
         auto side = [&](auto kc, const T *src, long ld, int r0, int rows, auto &reg, auto row_len) __attribute__((always_inline)) {
@@ -282,7 +319,7 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmParams p)
         for (auto &v : r) v = facc{0.0f, 0.0f, 0.0f, 0.0f};
     const int wave = threadIdx.x / 64, wm = wave / 2 * WM, wn = wave % 2 * WN;
     if (s1 < s2) fetch(s1);
-    for (long s = s1; s < s2; ++s) {
+    for (int s = s1; s < s2; ++s) {
         __syncthreads();  // (the last step's tiles have been read)
 #pragma unroll
         for (int i = 0; i < CA; ++i) {
@@ -313,82 +350,93 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmParams p)
             }
         }
     }
-    finish_tile<T, BM, BN, WM, WN>(p, t, acc);
+    finish_tile<T, BM, BN, WM, WN>(p, t, acc, tiles, wave);
 }
 
 // ------------------------------------------------------------------ straight to LDS
 
 constexpr unsigned kNowhere = 0x80000000u;  // an offset behind every buffer: its load gives zeros
 
-// One operand's loads of a step, from memory straight to LDS: 16 bytes a lane,
-// 64 lanes a kilobyte of the tile in the order of its places. The turn of a
-// chunk (OperandTile) is in which chunk a lane asks for.
-template <bool KC, int R>
+// One operand's loads, step after step, from memory straight to LDS: 16 bytes a
+// lane, 64 lanes a kilobyte of the tile in the order of its places. The turn of
+// a chunk (OperandTile) is in which chunk a lane asks for.
+template <bool KC, int R, int BK>
 struct StraightLoads {
-    using Tile = OperandTile<KC, R, 64, 1>;
-    static constexpr int kLoads = R * 8 / 256;               // a thread's, of a step of 64
+    using Tile = OperandTile<KC, R, BK, 1>;
+    static constexpr int kLoads = R * BK / 8 / 256;          // a thread's, of a step
     static constexpr int kRowsEach = 256 / Tile::kChunks;    // rows of the tile that 256 lanes cover
-    const uint16_t *base;                                    // the tile's first row (KC) or column
-    long ld;
-    int K;
+    const uint16_t *src;                                     // of the next step: the tile's first row (KC) or column
+    long ld, stride;                                         // stride: between stretches of k
     unsigned off[KC ? kLoads : 1];
     int col;                                                 // KC: the lane's first k
-    __device__ __forceinline__ void begin(const uint16_t *src, long ld_, int r0, int rows, int K_)
+    __device__ __forceinline__ void begin(const uint16_t *p, long ld_, long stride_, int r0, int rows, long kb, int k0)
     {
-        ld = ld_, K = K_;
+        ld = ld_, stride = stride_;
         const int row = threadIdx.x / Tile::kChunks, c = (threadIdx.x % Tile::kChunks) ^ Tile::turn(row);
+        src = p + kb * stride + (KC ? r0 * ld + k0 : r0 + k0 * ld);
         if constexpr (KC) {
-            base = src + r0 * ld, col = c * 8;
+            col = c * 8;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i)
                 off[i] = r0 + i * kRowsEach + row < rows ? static_cast<unsigned>(i * kRowsEach + row) * static_cast<unsigned>(ld * 2) + c * 16 : kNowhere;
         } else {
-            base = src + r0, col = 0;
+            col = 0;
             off[0] = r0 + c * 8 < rows ? static_cast<unsigned>(row) * static_cast<unsigned>(ld * 2) + c * 16 : kNowhere;
         }
     }
-    // k0 .. k0 + 63 of the stretch that lies `at` elements on
-    __device__ __forceinline__ void issue(uint16_t *tile, long at, int k0) const
+    // `left` of k: all BK, or what is left of a stretch, zeros past it (0: all zeros)
+    __device__ __forceinline__ void issue(uint16_t *tile, int left) const
     {
         using lds = __attribute__((address_space(3))) void;
-        const int left = K - k0;
-        const uint16_t *src = base + at + (KC ? static_cast<long>(k0) : k0 * ld);
-        // (of the last rows of k no more than there are)
-        const unsigned bytes = KC || left >= 64 ? 0x7fffffffu : static_cast<unsigned>(left) * static_cast<unsigned>(ld * 2);
+        const unsigned bytes = KC || left >= BK ? 0x7fffffffu : static_cast<unsigned>(left) * static_cast<unsigned>(ld * 2);
         const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(src), 0, static_cast<int>(bytes), 0x00020000);
         uint16_t *dst = tile + threadIdx.x / 64 * 512;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const unsigned o = KC ? (left >= 64 || col < left ? off[i] : kNowhere) : off[0];
+            const unsigned o = KC ? (col < left ? off[i] : kNowhere) : off[0];
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds *)(dst + i * 2048), 16, static_cast<int>(o),
                                                      KC ? 0 : static_cast<int>(i * kRowsEach * ld * 2), 0, 0);
         }
+    }
+    // to the next step, from the last of a stretch (it began `back` of k ago) to the next stretch
+    __device__ __forceinline__ void next(bool over, int back)
+    {
+        if (over) src += stride - (KC ? static_cast<long>(back) : back * ld);
+        else src += KC ? static_cast<long>(BK) : BK * ld;
     }
 };
 
 // bf16 operands whose rows are whole 16-byte chunks: two stages of tiles in LDS,
 // one filled by loads that pass the registers by while the other is used.
-template <bool A_KC, bool B_KC, int BM, int BN>
-__global__ __launch_bounds__(256) void gemm_straight(const GemmParams p)
+template <bool A_KC, bool B_KC, int BM, int BN, int BK>
+__global__ __launch_bounds__(256, 2) void gemm_straight(const GemmParams p)
 {
     constexpr int WM = BM / 2, WN = BN / 2;
-    using TA = OperandTile<A_KC, BM, 64, 1>;
-    using TB = OperandTile<B_KC, BN, 64, 1>;
+    using TA = OperandTile<A_KC, BM, BK, 1>;
+    using TB = OperandTile<B_KC, BN, BK, 1>;
+    using LA = StraightLoads<A_KC, BM, BK>;
+    using LB = StraightLoads<B_KC, BN, BK>;
     // (variables of their own, so that a read waits for its own stage's loads alone)
-    __shared__ __align__(16) uint16_t a0[TA::kElems], b0[TB::kElems], a1[TA::kElems], b1[TB::kElems];
+    __shared__ __align__(16) uint16_t ring0[TA::kElems + TB::kElems], ring1[TA::kElems + TB::kElems];
     const TilePlace t = tile_place<BM, BN>(p);
     const uint16_t *A = static_cast<const uint16_t *>(p.a), *B = static_cast<const uint16_t *>(p.b);
     if (p.kb == 1) A += t.b * p.a_bs, B += t.b * p.b_bs;
-    StraightLoads<A_KC, BM> la;
-    StraightLoads<B_KC, BN> lb;
-    la.begin(A, p.a_ld, t.m0, p.M, p.K);
-    lb.begin(B, p.b_ld, t.n0, p.N, p.K);
-    const long s1 = t.split * p.per, s2 = min(s1 + p.per, p.steps), each = (p.K + 63) / 64;
-    auto issue = [&](long s, uint16_t *a, uint16_t *b) __attribute__((always_inline)) {
-        const long kb = p.kb == 1 ? 0 : s / each;
-        const int k0 = static_cast<int>((s - kb * each) * 64);
-        la.issue(a, kb * p.a_bs, k0);
-        lb.issue(b, kb * p.b_bs, k0);
+    LA la;
+    LB lb;
+    const int s1 = t.split * p.per, s2 = min(s1 + p.per, p.steps), each = (p.K + BK - 1) / BK, kb = p.kb == 1 ? 0 : s1 / each;
+    int k0 = (s1 - kb * each) * BK;
+    la.begin(A, p.a_ld, p.kb == 1 ? 0 : p.a_bs, t.m0, p.M, kb, k0);
+    lb.begin(B, p.b_ld, p.kb == 1 ? 0 : p.b_bs, t.n0, p.N, kb, k0);
+    int ahead = s2 - s1;  // steps whose loads have not begun
+    auto issue = [&](uint16_t *ring) __attribute__((always_inline)) {
+        const int left = p.K - k0;
+        la.issue(ring, left);
+        lb.issue(ring + TA::kElems, left);
+        const bool over = left <= BK;
+        la.next(over, k0);
+        lb.next(over, k0);
+        k0 = over ? 0 : k0 + BK;
+        --ahead;
     };
     facc acc[WM / 16][WN / 16];
 #pragma unroll
@@ -396,44 +444,60 @@ __global__ __launch_bounds__(256) void gemm_straight(const GemmParams p)
 #pragma unroll
         for (auto &v : r) v = facc{0.0f, 0.0f, 0.0f, 0.0f};
     const int wave = threadIdx.x / 64, wm = wave / 2 * WM, wn = wave % 2 * WN;
-    auto step = [&](const uint16_t *a, const uint16_t *b) __attribute__((always_inline)) {
+    auto step = [&](const uint16_t *ring) __attribute__((always_inline)) {
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
+        for (int ks = 0; ks < BK / 32; ++ks) {
             bfrag fb[WN / 16], fa[WM / 16];
 #pragma unroll
-            for (int j = 0; j < WN / 16; ++j) fb[j] = TB::frag(b, 0, wn + j * 16, ks);
+            for (int j = 0; j < WN / 16; ++j) fb[j] = TB::frag(ring + TA::kElems, 0, wn + j * 16, ks);
 #pragma unroll
-            for (int i = 0; i < WM / 16; ++i) fa[i] = TA::frag(a, 0, wm + i * 16, ks);
+            for (int i = 0; i < WM / 16; ++i) fa[i] = TA::frag(ring, 0, wm + i * 16, ks);
 #pragma unroll
             for (int i = 0; i < WM / 16; ++i)
 #pragma unroll
                 for (int j = 0; j < WN / 16; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
         }
     };
-    if (s1 < s2) issue(s1, a0, b0);
-    for (long s = s1; s < s2; s += 2) {
+    if (ahead > 0) issue(ring0);
+    for (int left = s2 - s1; left > 0; left -= 2) {
         __syncthreads();  // (stage 0 is there, and stage 1 has been read)
-        if (s + 1 < s2) issue(s + 1, a1, b1);
-        step(a0, b0);
+        if (ahead > 0) issue(ring1);
+        step(ring0);
+        if (left == 1) break;
         __syncthreads();
-        if (s + 2 < s2) issue(s + 2, a0, b0);
-        if (s + 1 < s2) step(a1, b1);
+        if (ahead > 0) issue(ring0);
+        step(ring1);
     }
-    finish_tile<uint16_t, BM, BN, WM, WN>(p, t, acc);
+    static_assert(sizeof(ring0) >= 2 * 32 * (WN + 4) * sizeof(float), "the epilogue's place");
+    finish_tile<uint16_t, BM, BN, WM, WN>(p, t, acc, wave < 2 ? ring0 : ring1, wave % 2);
 }
 
 // Adds the splits' sums in order, then the epilogue.
 template <typename T>
 __global__ __launch_bounds__(256) void gemm_join(const GemmParams p)
 {
-    const long ldp = (p.N + 3) / 4 * 4, quads = ldp / 4;
-    const long i = (p.first + blockIdx.x) * 256 + threadIdx.x;
-    if (i >= p.batch * p.M * quads) return;
-    const long row = i / quads;
-    facc sum = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; s < p.splits; ++s) sum += *reinterpret_cast<const facc *>(p.part + (s * p.batch * p.M + row) * ldp + i % quads * 4);
-    float v[4] = {sum[0], sum[1], sum[2], sum[3]};
-    finish4<T>(p, row / p.M, static_cast<int>(row % p.M), static_cast<int>(i % quads) * 4, v);
+    constexpr int V = kWide<T>;
+    const long ldp = (p.N + 3) / 4 * 4, runs = (p.N + V - 1) / V;
+    const long i = static_cast<long>(p.first + blockIdx.x) * 256 + threadIdx.x;
+    if (i >= p.batch * p.M * runs) return;
+    const long row = i / runs;
+    const int n = static_cast<int>(i % runs) * V;
+    float v[V], bias[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = 0.0f;
+#pragma unroll 4
+    for (unsigned s = 0; s < p.splits; ++s) {
+        const float *part = p.part + (s * p.batch * p.M + row) * ldp + n;
+#pragma unroll
+        for (int k = 0; k < V / 4; ++k) {
+            if (n + 4 * k >= p.N) continue;
+            const facc f = *reinterpret_cast<const facc *>(part + 4 * k);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[4 * k + j] += f[j];
+        }
+    }
+    column_bias<T>(p, n, bias);
+    finish<T>(p, row / p.M, static_cast<int>(row % p.M), n, v, bias);
 }
 
 // ------------------------------------------------------------------ launches
@@ -443,7 +507,7 @@ constexpr long round_up_to(long v, long to) { return (v + to - 1) / to * to; }
 // How a product is cut. From its sizes alone, so that the workspace is known without the pointers.
 struct GemmPlan {
     int bm, splits;
-    long steps, per;
+    int steps, per;
     int64_t bytes;  // of the splits' sums
 };
 template <typename T>
@@ -451,14 +515,14 @@ GemmPlan plan_gemm(long batch, long M, long N, long K, long kb)
 {
     GemmPlan g{};
     auto tiles = [&](long t) { return static_cast<double>((M + t - 1) / t) * static_cast<double>((N + t - 1) / t) * static_cast<double>(batch); };
-    g.steps = (K + kStep<T> - 1) / kStep<T> * kb;
+    g.steps = static_cast<int>((K + kStep<T> - 1) / kStep<T> * kb);  // (less than 2^31: checked at the entries)
     g.bm = tiles(128) >= 256 ? 128 : 64;
     g.splits = 1;
     const double have = tiles(g.bm);
-    if (have < 384 && g.steps >= 8) g.splits = static_cast<int>(std::min<double>(std::min<long>(g.steps / 4, 64), 768.0 / std::max(have, 1.0)));
+    if (have < 384 && g.steps >= 8) g.splits = static_cast<int>(std::min<double>(std::min(g.steps / 4, 64), 768.0 / std::max(have, 1.0)));
     g.splits = std::max(g.splits, 1);
     g.per = (g.steps + g.splits - 1) / g.splits;
-    g.splits = static_cast<int>(std::max<long>((g.steps + g.per - 1) / std::max<long>(g.per, 1), 1));
+    g.splits = std::max((g.steps + g.per - 1) / std::max(g.per, 1), 1);
     g.bytes = g.splits > 1 ? static_cast<int64_t>(g.splits) * batch * M * round_up_to(N, 4) * 4 : 0;
     return g;
 }
@@ -470,8 +534,9 @@ template <typename F>
 int gemm_launch(GemmParams &p, long groups, F &&f)
 {
     const long most = most_groups(256) / 8 * 8;
-    for (p.first = 0; p.first < groups; p.first += most) {
-        f(dim3(static_cast<unsigned>(std::min(groups - p.first, most))));
+    for (long first = 0; first < groups; first += most) {
+        p.first = static_cast<unsigned>(first);
+        f(dim3(static_cast<unsigned>(std::min(groups - first, most))));
         const int st = launched();
         if (st != SSM2D_OK) return st;
     }
@@ -491,15 +556,16 @@ int run_gemm_of(GemmParams p, bool a_kc, bool b_kc, void *ws, hipStream_t s)
     const GemmPlan g = plan_gemm<T>(p.batch, p.M, p.N, p.K, p.kb);
     p.splits = g.splits, p.steps = g.steps, p.per = g.per, p.part = static_cast<float *>(ws);
     auto go = [&](auto size) {
-        constexpr int BM = decltype(size)::value;
+        constexpr int BM = decltype(size)::value, kBK = kStep<uint16_t>;
         p.tiles_m = (p.M + BM - 1) / BM, p.tiles_n = (p.N + BM - 1) / BM;
-        return gemm_launch(p, static_cast<long>(p.tiles_m) * p.tiles_n * p.batch * p.splits, [&](dim3 grid) {
+        p.total = p.tiles_m * p.tiles_n * static_cast<unsigned>(p.batch) * p.splits;
+        return gemm_launch(p, p.total, [&](dim3 grid) {
             if constexpr (sizeof(T) == 2) {
                 if (p.straight) {
-                    if (a_kc && b_kc) gemm_straight<true, true, BM, BM><<<grid, dim3(256), 0, s>>>(p);
-                    else if (a_kc) gemm_straight<true, false, BM, BM><<<grid, dim3(256), 0, s>>>(p);
-                    else if (b_kc) gemm_straight<false, true, BM, BM><<<grid, dim3(256), 0, s>>>(p);
-                    else gemm_straight<false, false, BM, BM><<<grid, dim3(256), 0, s>>>(p);
+                    if (a_kc && b_kc) gemm_straight<true, true, BM, BM, kBK><<<grid, dim3(256), 0, s>>>(p);
+                    else if (a_kc) gemm_straight<true, false, BM, BM, kBK><<<grid, dim3(256), 0, s>>>(p);
+                    else if (b_kc) gemm_straight<false, true, BM, BM, kBK><<<grid, dim3(256), 0, s>>>(p);
+                    else gemm_straight<false, false, BM, BM, kBK><<<grid, dim3(256), 0, s>>>(p);
                     return;
                 }
             }
@@ -511,8 +577,8 @@ int run_gemm_of(GemmParams p, bool a_kc, bool b_kc, void *ws, hipStream_t s)
     };
     int st = g.bm == 128 ? go(std::integral_constant<int, 128>{}) : go(std::integral_constant<int, 64>{});
     if (st == SSM2D_OK && p.splits > 1) {
-        const long quads = p.batch * p.M * (round_up_to(p.N, 4) / 4);
-        st = gemm_launch(p, (quads + 255) / 256, [&](dim3 grid) { gemm_join<T><<<grid, dim3(256), 0, s>>>(p); });
+        const long runs = p.batch * p.M * ((p.N + kWide<T> - 1) / kWide<T>);
+        st = gemm_launch(p, (runs + 255) / 256, [&](dim3 grid) { gemm_join<T><<<grid, dim3(256), 0, s>>>(p); });
     }
     return st;
 }

@@ -188,6 +188,7 @@ int check_linear(const ssm2d_linear_shape *a, int act, uint32_t flags)
     const double b = static_cast<double>(a->batch), r = static_cast<double>(a->rows), n = static_cast<double>(a->n), k = static_cast<double>(a->k);
     for (const double t : {b * (r / 64 + 1) * (n / 64 + 1), b * (r / 64 + 1) * (k / 64 + 1), (k / 64 + 1) * (n / 64 + 1)})
         if (t >= 2147483648.0) return SSM2D_ERR_UNSUPPORTED;
+    if (b * (r / 32 + 1) >= 2147483648.0) return SSM2D_ERR_UNSUPPORTED;  // (steps of dweight's sum)
     return SSM2D_OK;
 }
 
