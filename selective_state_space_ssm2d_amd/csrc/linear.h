@@ -61,13 +61,31 @@ __device__ __forceinline__ void column_bias(const GemmParams &p, int n, float (&
     for (int j = 0; j < kWide<T>; ++j) b[j] = p.bias && !p.bias_m && n < p.N ? p.bias[min(n + j, p.N - 1)] : 0.0f;
 }
 
-// Neighbours of row m from column n on, `bias` their columns'.
+// The residual of row m from column n on, zeros where there is none.
 template <typename T>
-__device__ __forceinline__ void finish(const GemmParams &p, long b, int m, int n, float (&v)[kWide<T>], const float (&bias)[kWide<T>])
+__device__ __forceinline__ void read_residual(const GemmParams &p, long b, int m, int n, Raw<T, kWide<T>> &w)
+{
+    constexpr int V = kWide<T>;
+    w.clear();
+    if (!p.res || m >= p.M || n >= p.N) return;
+    const T *r = static_cast<const T *>(p.res) + b * p.r_bs + static_cast<long>(m) * p.r_ld + n;
+    if (n + V <= p.N) {
+        w.load_any(r);
+    } else {
+        float v[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = n + j < p.N ? widen1(r[j]) : 0.0f;
+        w.set(v);
+    }
+}
+
+// Neighbours of row m from column n on; bias: their columns', or the row's; RES: with a residual.
+template <typename T, bool RES>
+__device__ __forceinline__ void finish(const GemmParams &p, long b, int m, int n, float (&v)[kWide<T>], const float (&bias)[kWide<T>], float row,
+                                       const Raw<T, kWide<T>> &res)
 {
     constexpr int V = kWide<T>;
     if (m >= p.M || n >= p.N) return;
-    const float row = p.bias && p.bias_m ? p.bias[m] : 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) v[j] += p.bias_m ? row : bias[j];
     const long at = b * p.c_bs + static_cast<long>(m) * p.c_ld + n;
@@ -91,18 +109,9 @@ __device__ __forceinline__ void finish(const GemmParams &p, long b, int m, int n
     case SSM2D_ACT_GELU: act_all<T, SSM2D_ACT_GELU>(v); break;
     default: break;
     }
-    if (p.res) {
-        const T *r = static_cast<const T *>(p.res) + b * p.r_bs + static_cast<long>(m) * p.r_ld + n;
-        if (whole) {
-            Raw<T, V> w;
-            w.load_any(r);
+    if constexpr (RES) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) v[j] += w.get(j);
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (n + j < p.N) v[j] += widen1(r[j]);
-        }
+        for (int j = 0; j < V; ++j) v[j] += res.get(j);
     }
     put(p.c);
 }
@@ -149,47 +158,52 @@ struct OperandTile {
     }
 };
 
-// Eight elements of an operand on their way from memory to LDS.
+// 16 bytes of an operand on their way from memory to LDS (neighbouring lanes take
+// neighbouring ones: two loads into the same line that is still under way
+// would wait for each other).
 template <typename T>
 struct Chunk {
-    Raw<T, 8> r;
-    // the first `count` of the 8 at p (0 or less: none), the others 0
+    static constexpr int kN = 16 / static_cast<int>(sizeof(T));
+    Raw<T, kN> r;
+    // the first `count` of the kN elements at p (0 or less: none), the others 0
     __device__ __forceinline__ void load(const T *p, long count)
     {
-        if (count >= 8) {
+        if (count >= kN) {
             r.load_any(p);
         } else if (count > 0) {
-            float v[8];
+            float v[kN];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = widen1(p[min(i, static_cast<int>(count) - 1)]);
+            for (int i = 0; i < kN; ++i) v[i] = widen1(p[min(i, static_cast<int>(count) - 1)]);
 #pragma unroll
-            for (int i = 1; i < 8; ++i) v[i] = i < count ? v[i] : 0.0f;
+            for (int i = 1; i < kN; ++i) v[i] = i < count ? v[i] : 0.0f;
             r.set(v);
         } else {
             r.clear();
         }
     }
-    // as NP parts, kPart elements apart
-    __device__ __forceinline__ void store(uint16_t *dst, int part) const
+    // to place c (in chunks) of a row of the tile, as NP parts
+    template <typename Tile>
+    __device__ __forceinline__ void store(uint16_t *tile, int row, int c) const
     {
         if constexpr (sizeof(T) == 2) {
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+            *reinterpret_cast<uint4 *>(tile + Tile::at(row, c)) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
         } else {
+            uint16_t *dst = tile + Tile::at(row, c / 2) + c % 2 * 4;
             // three parts of 8 bits each, cut off: exact
-            float v[8];
+            float v[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = r.get(i);
+            for (int i = 0; i < 4; ++i) v[i] = r.get(i);
 #pragma unroll
             for (int n = 0; n < 3; ++n) {
-                unsigned w[4];
+                unsigned w[2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 2; ++i) {
                     const unsigned lo = __float_as_uint(v[2 * i]), hi = __float_as_uint(v[2 * i + 1]);
                     w[i] = top_halves(hi, lo);
                     v[2 * i] -= __uint_as_float(lo & 0xffff0000u);
                     v[2 * i + 1] -= __uint_as_float(hi & 0xffff0000u);
                 }
-                *reinterpret_cast<uint4 *>(dst + n * part) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint2 *>(dst + n * Tile::kPart) = make_uint2(w[0], w[1]);
             }
         }
     }
@@ -239,44 +253,63 @@ __device__ __forceinline__ void finish_tile(const GemmParams &p, const TilePlace
     const int m0 = t.m0 + wave / (BN / WN) * WM, n = t.n0 + wave % (BN / WN) * WN + l % kLanes * V;
     float *mine = static_cast<float *>(lds) + slot * 32 * kLd;  // 32 rows at a time
     const long ldp = (p.N + 3) / 4 * 4;
+    constexpr int kPasses = 32 / kRowsOnce;
     float bias[V];
     column_bias<T>(p, n, bias);
     __syncthreads();
+    auto all = [&](auto with_res) __attribute__((always_inline)) {
+        constexpr bool RES = decltype(with_res)::value;
 #pragma unroll
-    for (int half = 0; half < WM / 32; ++half) {
+        for (int half = 0; half < WM / 32; ++half) {
+            const int r0 = m0 + half * 32 + l / kLanes;
+            // (all that is read, before anything is written that it might be)
+            Raw<T, V> res[RES ? kPasses : 1];
+            if constexpr (RES) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < WN / 16; ++j)
-                *reinterpret_cast<facc *>(mine + (i * 16 + l % 16) * kLd + j * 16 + 4 * (l / 16)) = acc[half * 2 + i][j];
-        // (its own lanes' writes, in order before its reads: no barrier)
-#pragma unroll 2
-        for (int r = l / kLanes; r < 32; r += kRowsOnce) {
-            const int m = m0 + half * 32 + r;
-            float v[V];
-#pragma unroll
-            for (int k = 0; k < V / 4; ++k) {
-                const facc f = *reinterpret_cast<const facc *>(mine + r * kLd + l % kLanes * V + 4 * k);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[4 * k + j] = f[j];
+                for (int k = 0; k < kPasses; ++k) read_residual<T>(p, t.b, r0 + k * kRowsOnce, n, res[k]);
             }
-            if (p.splits > 1) {
-                if (m >= p.M) continue;
-                float *part = p.part + ((static_cast<long>(t.split) * p.batch + t.b) * p.M + m) * ldp + n;
 #pragma unroll
-                for (int k = 0; k < V / 4; ++k)
-                    if (n + 4 * k < p.N) *reinterpret_cast<facc *>(part + 4 * k) = facc{v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]};
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < WN / 16; ++j)
+                    *reinterpret_cast<facc *>(mine + (i * 16 + l % 16) * kLd + j * 16 + 4 * (l / 16)) = acc[half * 2 + i][j];
+            // (its own lanes' writes, in order before its reads: no barrier)
+            auto pass = [&](int k, const Raw<T, V> &w) __attribute__((always_inline)) {
+                const int m = r0 + k * kRowsOnce;
+                float v[V];
+#pragma unroll
+                for (int q = 0; q < V / 4; ++q) {
+                    const facc f = *reinterpret_cast<const facc *>(mine + (l / kLanes + k * kRowsOnce) * kLd + l % kLanes * V + 4 * q);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[4 * q + j] = f[j];
+                }
+                if (p.splits > 1) {
+                    if (m >= p.M) return;
+                    float *part = p.part + ((static_cast<long>(t.split) * p.batch + t.b) * p.M + m) * ldp + n;
+#pragma unroll
+                    for (int q = 0; q < V / 4; ++q)
+                        if (n + 4 * q < p.N) *reinterpret_cast<facc *>(part + 4 * q) = facc{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+                } else {
+                    finish<T, RES>(p, t.b, m, n, v, bias, p.bias && p.bias_m && m < p.M ? p.bias[m] : 0.0f, w);
+                }
+            };
+            if constexpr (RES) {
+#pragma unroll
+                for (int k = 0; k < kPasses; ++k) pass(k, res[k]);
             } else {
-                finish<T>(p, t.b, m, n, v, bias);
+#pragma unroll 2
+                for (int k = 0; k < kPasses; ++k) pass(k, res[0]);
             }
         }
-    }
+    };
+    if (p.res && p.splits == 1) all(std::true_type{});
+    else all(std::false_type{});
 }
 
 // Any alignment: operands go through registers to LDS, the next step's read
 // while this one's products run.
 template <typename T, bool A_KC, bool B_KC, int BM, int BN>
-__global__ __launch_bounds__(256) void gemm_kernel(const GemmParams p)
+__global__ __launch_bounds__(256, 2) void gemm_kernel(const GemmParams p)
 {
     constexpr int NP = kParts<T>, BK = kStep<T>, WM = BM / 2, WN = BN / 2;
     using TA = OperandTile<A_KC, BM, BK, NP>;
@@ -288,17 +321,17 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmParams p)
     const T *A = static_cast<const T *>(p.a), *B = static_cast<const T *>(p.b);
     if (p.kb == 1) A += t.b * p.a_bs, B += t.b * p.b_bs;
     const int s1 = t.split * p.per, s2 = min(s1 + p.per, p.steps), each = (p.K + BK - 1) / BK;
-    constexpr int CA = BM * BK / 8 / 256, CB = BN * BK / 8 / 256;
+    constexpr int W = Chunk<T>::kN, CA = BM * BK / W / 256, CB = BN * BK / W / 256;
     Chunk<T> ra[CA], rb[CB];
     auto fetch = [&](int s) __attribute__((always_inline)) {
         const int kb = p.kb == 1 ? 0 : s / each, k0 = (s - kb * each) * BK;
         const T *ap = A + kb * p.a_bs, *bp = B + kb * p.b_bs;
         if (p.kb == 1) ap = A, bp = B;
         auto side = [&](auto kc, const T *src, long ld, int r0, int rows, auto &reg, auto row_len) __attribute__((always_inline)) {
-            constexpr int kChunks = decltype(row_len)::value / 8;
+            constexpr int kChunks = decltype(row_len)::value / W;
 #pragma unroll
             for (int i = 0; i < static_cast<int>(sizeof(reg) / sizeof(reg[0])); ++i) {
-                const int id = i * 256 + threadIdx.x, row = id / kChunks, col = id % kChunks * 8;
+                const int id = i * 256 + threadIdx.x, row = id / kChunks, col = id % kChunks * W;
                 if constexpr (decltype(kc)::value) {
                     const long m = r0 + row, k = k0 + col;
                     reg[i].load(src + m * ld + k, m < rows ? p.K - k : 0);
@@ -324,12 +357,12 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmParams p)
 #pragma unroll
         for (int i = 0; i < CA; ++i) {
             const int id = i * 256 + threadIdx.x;
-            ra[i].store(sa + TA::at(id / TA::kChunks, id % TA::kChunks), TA::kPart);
+            ra[i].template store<TA>(sa, id / (TA::kRow / W), id % (TA::kRow / W));
         }
 #pragma unroll
         for (int i = 0; i < CB; ++i) {
             const int id = i * 256 + threadIdx.x;
-            rb[i].store(sb + TB::at(id / TB::kChunks, id % TB::kChunks), TB::kPart);
+            rb[i].template store<TB>(sb, id / (TB::kRow / W), id % (TB::kRow / W));
         }
         __syncthreads();
         if (s + 1 < s2) fetch(s + 1);
@@ -472,57 +505,91 @@ __global__ __launch_bounds__(256, 2) void gemm_straight(const GemmParams p)
     finish_tile<uint16_t, BM, BN, WM, WN>(p, t, acc, wave < 2 ? ring0 : ring1, wave % 2);
 }
 
-// Adds the splits' sums in order, then the epilogue.
+// Adds the splits' sums, four threads a run of columns each every fourth, then
+// those in order; then the epilogue.
 template <typename T>
 __global__ __launch_bounds__(256) void gemm_join(const GemmParams p)
 {
     constexpr int V = kWide<T>;
+    __shared__ float sums[4][64][V + 1];
     const long ldp = (p.N + 3) / 4 * 4, runs = (p.N + V - 1) / V;
-    const long i = static_cast<long>(p.first + blockIdx.x) * 256 + threadIdx.x;
-    if (i >= p.batch * p.M * runs) return;
+    const long i = static_cast<long>(p.first + blockIdx.x) * 64 + threadIdx.x % 64;
+    const unsigned turn = threadIdx.x / 64;
+    const bool live = i < p.batch * p.M * runs;
     const long row = i / runs;
-    const int n = static_cast<int>(i % runs) * V;
+    const int n = static_cast<int>(i % runs) * V, m = static_cast<int>(row % p.M);
     float v[V], bias[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) v[j] = 0.0f;
-#pragma unroll 4
-    for (unsigned s = 0; s < p.splits; ++s) {
-        const float *part = p.part + (s * p.batch * p.M + row) * ldp + n;
+    Raw<T, V> res;
+    res.clear();
+    if (live) {
+#pragma unroll 8
+        for (unsigned s = turn; s < p.splits; s += 4) {
+            const float *part = p.part + (s * p.batch * p.M + row) * ldp + n;
 #pragma unroll
-        for (int k = 0; k < V / 4; ++k) {
-            if (n + 4 * k >= p.N) continue;
-            const facc f = *reinterpret_cast<const facc *>(part + 4 * k);
+            for (int k = 0; k < V / 4; ++k) {
+                if (n + 4 * k >= p.N) continue;
+                const facc f = *reinterpret_cast<const facc *>(part + 4 * k);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[4 * k + j] += f[j];
+                for (int j = 0; j < 4; ++j) v[4 * k + j] += f[j];
+            }
         }
+        if (turn == 0) read_residual<T>(p, row / p.M, m, n, res);
     }
+#pragma unroll
+    for (int j = 0; j < V; ++j) sums[turn][threadIdx.x % 64][j] = v[j];
+    __syncthreads();
+    if (turn != 0 || !live) return;
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = (v[j] + sums[1][threadIdx.x][j]) + (sums[2][threadIdx.x][j] + sums[3][threadIdx.x][j]);
     column_bias<T>(p, n, bias);
-    finish<T>(p, row / p.M, static_cast<int>(row % p.M), n, v, bias);
+    finish<T, true>(p, row / p.M, m, n, v, bias, p.bias && p.bias_m ? p.bias[m] : 0.0f, res);
 }
 
 // ------------------------------------------------------------------ launches
 
 constexpr long round_up_to(long v, long to) { return (v + to - 1) / to * to; }
 
-// How a product is cut. From its sizes alone, so that the workspace is known without the pointers.
+// How a product is cut: the side of its tiles, and the parts of its sum. From its
+// sizes alone, so that the workspace is known without the pointers.
 struct GemmPlan {
     int bm, splits;
     int steps, per;
     int64_t bytes;  // of the splits' sums
 };
+
+// The choice with the least time by this count, in us, of what was measured (bf16;
+// float32): a workgroup alone takes 0.4 (1.1) a step of 64 x 64 and 0.8 (2.0) of
+// 128 x 128, a compute unit full of them 0.22 (0.48) and 0.5 (1.4) for each; and parts
+// cost 4 for the launch that joins them and their sums' way to memory and back.
+// 768 x 768 over 12544 rows: 33 to 34 us of bf16 in 7 parts of 64 x 64 or 14 of 128 x 128, 115 and
+// 193 undivided; 196 x 768 of 768: 7.4 us undivided, 11.5 in two parts. Short float32 sums of
+// few steps are taken in tiles of 64, whose loads more workgroups keep under way
+// (128 of 128 channels by 196608 cells: 84 us, 93 in tiles of 128).
 template <typename T>
 GemmPlan plan_gemm(long batch, long M, long N, long K, long kb)
 {
+    constexpr bool kHalf = sizeof(T) == 2;
     GemmPlan g{};
-    auto tiles = [&](long t) { return static_cast<double>((M + t - 1) / t) * static_cast<double>((N + t - 1) / t) * static_cast<double>(batch); };
     g.steps = static_cast<int>((K + kStep<T> - 1) / kStep<T> * kb);  // (less than 2^31: checked at the entries)
-    g.bm = tiles(128) >= 256 ? 128 : 64;
-    g.splits = 1;
-    const double have = tiles(g.bm);
-    if (have < 384 && g.steps >= 8) g.splits = static_cast<int>(std::min<double>(std::min(g.steps / 4, 64), 768.0 / std::max(have, 1.0)));
-    g.splits = std::max(g.splits, 1);
-    g.per = (g.steps + g.splits - 1) / g.splits;
-    g.splits = std::max((g.steps + g.per - 1) / std::max(g.per, 1), 1);
+    g.bm = 64, g.splits = 1;
+    double best = 0.0;
+    for (const int bm : {64, 128}) {
+        if (bm == 128 && !kHalf && K <= 256 && kb == 1) continue;
+        const double tiles = static_cast<double>((M + bm - 1) / bm) * static_cast<double>((N + bm - 1) / bm) * static_cast<double>(batch);
+        const double alone = bm == 64 ? (kHalf ? 0.4 : 1.1) : (kHalf ? 0.8 : 2.0), full = bm == 64 ? (kHalf ? 0.22 : 0.48) : (kHalf ? 0.5 : 1.4);
+        for (const int parts : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+            const int per = (g.steps + parts - 1) / parts;
+            if (parts > 1 && (per < 4 || tiles * parts > 2048.0)) continue;
+            const double rounds = tiles * parts / 256.0;
+            double us = per * std::max(alone, rounds * full);
+            if (parts > 1) us += 4.0 + parts * static_cast<double>(batch) * static_cast<double>(M) * static_cast<double>(N) * 8.0 / 4e6;
+            if (best == 0.0 || us < best) best = us, g.bm = bm, g.splits = parts;
+        }
+    }
+    g.per = std::max((g.steps + g.splits - 1) / g.splits, 1);
+    g.splits = std::max((g.steps + g.per - 1) / g.per, 1);
     g.bytes = g.splits > 1 ? static_cast<int64_t>(g.splits) * batch * M * round_up_to(N, 4) * 4 : 0;
     return g;
 }
@@ -578,7 +645,7 @@ int run_gemm_of(GemmParams p, bool a_kc, bool b_kc, void *ws, hipStream_t s)
     int st = g.bm == 128 ? go(std::integral_constant<int, 128>{}) : go(std::integral_constant<int, 64>{});
     if (st == SSM2D_OK && p.splits > 1) {
         const long runs = p.batch * p.M * ((p.N + kWide<T> - 1) / kWide<T>);
-        st = gemm_launch(p, (runs + 255) / 256, [&](dim3 grid) { gemm_join<T><<<grid, dim3(256), 0, s>>>(p); });
+        st = gemm_launch(p, (runs + 63) / 64, [&](dim3 grid) { gemm_join<T><<<grid, dim3(256), 0, s>>>(p); });
     }
     return st;
 }
