@@ -38,6 +38,7 @@ struct RecParams {
     int n, n_seq, tiles;
     long x_b, g_b, d_b, x_t, g_t, d_t;  // strides of batch and token (rows) or channel (maps)
     int rev;                       // rows: from the last token to the first
+    int pass_on;                   // packed: empty sequences' states are to be written
 };
 
 constexpr float kCut = -0.0f;
@@ -87,28 +88,37 @@ struct Place {
     bool first;
     long end, next;
 };
-__device__ __forceinline__ long cu_at(const RecParams &p, int i)
-{
-    const long v = p.cu[i];
-    return v < 0 ? 0 : (v > p.T ? p.T : v);
-}
+__device__ __forceinline__ long in_tokens(const RecParams &p, long v) { return v < 0 ? 0 : (v > p.T ? p.T : v); }
+__device__ __forceinline__ long cu_at(const RecParams &p, int i) { return in_tokens(p, p.cu[i]); }
 // (by halves at each change: any contents end, and stay within the tokens)
-__device__ __forceinline__ Place locate(const RecParams &p, long t)
+template <typename F>
+__device__ __forceinline__ Place locate_by(const RecParams &p, long t, F &&at)
 {
-    int lo = -1, hi = p.n_seq;  // cu[lo] <= t < cu[hi], as far as they ascend
+    int lo = -1, hi = p.n_seq;  // at(lo) <= t < at(hi), as far as they ascend
     while (hi - lo > 1) {
         const int m = (lo + hi) / 2;
-        if (cu_at(p, m) <= t) lo = m;
+        if (at(m) <= t) lo = m;
         else hi = m;
     }
     Place w{-1, false, -1, 0x7fffffffffffffffL};
     if (lo < 0) {
-        w.next = cu_at(p, 0);
+        w.next = at(0);
     } else {
-        const long end = cu_at(p, lo + 1);
-        if (t < end) w = Place{lo, cu_at(p, lo) == t, end, end};
+        const long end = at(lo + 1);
+        if (t < end) w = Place{lo, at(lo) == t, end, end};
     }
     return w;
+}
+__device__ __forceinline__ Place locate(const RecParams &p, long t)
+{
+    return locate_by(p, t, [&](int i) { return cu_at(p, i); });
+}
+// Of the workgroup's first token, by scalar loads (nothing writes the offsets
+// meanwhile): vector loads would wait for all that were asked for before.
+__device__ __forceinline__ Place locate_first(const RecParams &p, long t)
+{
+    const auto *cu = reinterpret_cast<const __attribute__((address_space(4))) int *>(reinterpret_cast<uintptr_t>(p.cu));
+    return locate_by(p, t, [&](int i) { return in_tokens(p, cu[i]); });
 }
 
 // ------------------------------------------------------------------ token rows
@@ -203,7 +213,7 @@ struct Marks {
     __device__ __forceinline__ void find(const RecParams &p, long t0, int chunk, long t)
     {
         firsts = ends = outs = 0;
-        Place w = locate(p, t0);  // (by scalar loads)
+        Place w = locate_first(p, t0);
         if (w.seq >= 0 && !w.first && w.end > t0 + chunk) return;  // (most: inside one sequence)
         w = locate(p, t);
 #pragma unroll
@@ -281,6 +291,19 @@ __global__ __launch_bounds__(256) void rec_few(const RecParams p, long threads)
         if (j < left) p.h_last[at + j] = h[j];
 }
 
+// Sequences without tokens pass their state on (NULL: zeros): for V channels, a
+// share of the sequences each.
+template <int V>
+__device__ __forceinline__ void pass_on(const RecParams &p, const float *src, float *dst, int c, int first, int step)
+{
+    for (int s = first; s < p.n_seq; s += step) {
+        if (cu_at(p, s + 1) > cu_at(p, s)) continue;
+        const long at = static_cast<long>(s) * p.n + c;
+#pragma unroll
+        for (int j = 0; j < V; ++j) dst[at + j] = src ? src[at + j] : 0.0f;
+    }
+}
+
 // AGG: only the segment's product and state from zero, into P and H.
 template <typename T, int V, bool PACKED, bool SIG, bool AGG>
 __global__ __launch_bounds__(256, 4) void rec_rows_fwd(const RecParams p)
@@ -309,6 +332,7 @@ __global__ __launch_bounds__(256, 4) void rec_rows_fwd(const RecParams p)
             else if (!PACKED && p.h_init) carry[j] = p.h_init[b * p.n + c + j];
         }
     }
+    if (PACKED && !AGG && p.pass_on && live) pass_on<V>(p, p.h_init, p.h_last, c, seg * D::kBY + ty, p.S * D::kBY);
     int buf = 0;
     for (long t0 = t1; t0 < t2; t0 += D::kChunk, buf ^= 1) {
         const long mine = t0 + ty * D::kL;
@@ -429,6 +453,7 @@ __global__ __launch_bounds__(512, 4) void rec_rows_bwd(const RecParams p)
         rd[i].load_any(d + ld.base + ld.first);
         if (i + 1 < cnt) lx.first += lx.step, lg.first += lg.step, ld.first += ld.step;
     }
+    if (PACKED && !AGG && p.pass_on && live) pass_on<V>(p, p.dh_last, p.dh_init, c, seg * D::kBY + ty, p.S * D::kBY);
     float enter[V], flow[V], one[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -554,11 +579,16 @@ __global__ __launch_bounds__(512, 4) void rec_rows_bwd(const RecParams p)
 
 template <typename T>
 constexpr int kMapV = 16 / static_cast<int>(sizeof(T));  // tokens of a vector
-constexpr int kMapU = 2;                                 // vectors a lane holds
-template <typename T, int WPR>
-constexpr int kMapChunk = WPR * 64 * kMapV<T> * kMapU;
+// How a row of cells is held: LPR lanes (16 .. 256: four waves) with U vectors each.
+template <int LPR_, int U_>
+struct MapDims {
+    static constexpr int kLpr = LPR_, kU = U_, kWaves = LPR_ > 64 ? LPR_ / 64 : 1, kWidth = LPR_ > 64 ? 64 : LPR_, kRows = 256 / LPR_;
+    template <typename T>
+    static constexpr int kChunk = LPR_ * kMapV<T> * U_;
+};
 
-// Inclusive join over the wave's lanes.
+// Inclusive join over aligned groups of W lanes.
+template <int W>
 __device__ __forceinline__ void wave_join(float &P, float &c)
 {
     auto step = [&](auto ctrl, auto rows) __attribute__((always_inline)) {
@@ -573,38 +603,48 @@ __device__ __forceinline__ void wave_join(float &P, float &c)
     step(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
     step(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
     step(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
-    step(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});  // the rows' last lanes to the next row, and to the second half
-    step(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});
+    // the rows' last lanes to the next row, and to the second half
+    if constexpr (W > 16) step(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});
+    if constexpr (W > 32) step(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});
 }
+// The value of the lane before, `none` for the first of a group.
+template <int W>
 __device__ __forceinline__ float lane_before(float v, float none)
 {
-    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(none), __float_as_int(v), 0x138, 0xf, 0xf, false));  // wave_shr:1
+    constexpr int kCtrl = W == 16 ? 0x111 : 0x138;  // row_shr:1, wave_shr:1
+    const float r = __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(none), __float_as_int(v), kCtrl, 0xf, 0xf, false));
+    return W == 32 && threadIdx.x % 32 == 0 ? none : r;
 }
-__device__ __forceinline__ float last_lane(float v) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63)); }
+template <int W>
+__device__ __forceinline__ float last_lane(float v)
+{
+    if constexpr (W == 64) return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+    else return __shfl(v, W - 1, W);
+}
 
-// The states before each of a lane's U stretches (in token order: all lanes'
-// first, then all lanes' second) given h before the wave's; h moves to the end.
-// P, c: the stretches; they become the joined ones up to each lane.
-template <int U>
+// The product and sum of U stretches of each lane of a group (in token order: all
+// lanes' first, then all lanes' second); P, c become the joined ones up to each lane.
+template <int W, int U>
 __device__ __forceinline__ void wave_total(float (&P)[U], float (&c)[U], float &wP, float &wc)
 {
     wP = 1.0f, wc = 0.0f;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        wave_join(P[u], c[u]);
-        const float lP = last_lane(P[u]), lc = last_lane(c[u]);
+        wave_join<W>(P[u], c[u]);
+        const float lP = last_lane<W>(P[u]), lc = last_lane<W>(c[u]);
         wc = fmaf(lP, wc, lc);
         wP *= lP;
     }
 }
-template <int U>
+// The states before each of a lane's stretches given h before the group's.
+template <int W, int U>
 __device__ __forceinline__ void wave_states(const float (&P)[U], const float (&c)[U], float h, float (&in)[U])
 {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const float eP = lane_before(P[u], 1.0f), ec = lane_before(c[u], 0.0f);
+        const float eP = lane_before<W>(P[u], 1.0f), ec = lane_before<W>(c[u], 0.0f);
         in[u] = fmaf(eP, h, ec);
-        h = fmaf(last_lane(P[u]), h, last_lane(c[u]));
+        h = fmaf(last_lane<W>(P[u]), h, last_lane<W>(c[u]));
     }
 }
 
@@ -671,14 +711,15 @@ __device__ __forceinline__ float join_waves(float wP, float wc, float &carry, fl
     return in;
 }
 
-template <typename T, int WPR, bool REV, bool SIG, bool AGG>
+template <typename T, typename DIMS, bool REV, bool SIG, bool AGG>
 __global__ __launch_bounds__(256) void rec_maps_fwd(const RecParams p, long units)
 {
-    constexpr int V = kMapV<T>, U = kMapU, kRowsOf = 4 / WPR, kChunk = kMapChunk<T, WPR>;
+    constexpr int V = kMapV<T>, U = DIMS::kU, W = DIMS::kWidth, kWaves = DIMS::kWaves, kChunk = DIMS::template kChunk<T>;
     __shared__ float tot[2][4][2];
-    const int lane = threadIdx.x % 64, wave = WPR == 1 ? 0 : threadIdx.x / 64;
-    const long unit = (p.first + blockIdx.x) * kRowsOf + (WPR == 1 ? threadIdx.x / 64 : 0);
-    if (WPR == 1 && unit >= units) return;  // (whole waves, and no barrier follows)
+    const int place_in = threadIdx.x % DIMS::kLpr, wave = place_in / 64, lane = place_in % 64;  // of the row
+    const long unit = (p.first + blockIdx.x) * DIMS::kRows + threadIdx.x / DIMS::kLpr;
+    // (rows past the last: whole waves or parts of them, and no barrier follows)
+    if (DIMS::kRows > 1 && unit >= units) return;
     const int seg = static_cast<int>(unit % p.S);
     const long row = unit / p.S, b = row / p.n, c = row % p.n;
     const T *x = static_cast<const T *>(p.x) + b * p.x_b + c * p.x_t, *g = static_cast<const T *>(p.g) + b * p.g_b + c * p.g_t;
@@ -691,7 +732,7 @@ __global__ __launch_bounds__(256) void rec_maps_fwd(const RecParams p, long unit
     for (long t0 = t1; t0 < t2; t0 += kChunk, buf ^= 1) {
         Run<T, V, REV> rx[U], rg[U];
         float P[U], h[U], in[U];
-        auto at = [&](int u) { return t0 + (static_cast<long>(wave * U + u) * 64 + lane) * V; };
+        auto at = [&](int u) { return t0 + (static_cast<long>(wave * U + u) * W + lane) * V; };
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             // (segments end with whole chunks or with the row)
@@ -710,10 +751,10 @@ __global__ __launch_bounds__(256) void rec_maps_fwd(const RecParams p, long unit
             }
         }
         float wP, wc;
-        wave_total<U>(P, h, wP, wc);
-        const float enter = join_waves<WPR, false>(wP, wc, carry, carryP, tot[buf]);
+        wave_total<W, U>(P, h, wP, wc);
+        const float enter = join_waves<kWaves, false>(wP, wc, carry, carryP, tot[buf]);
         if (AGG) continue;
-        wave_states<U>(P, h, enter, in);
+        wave_states<W, U>(P, h, enter, in);
 #pragma unroll
         for (int u = 0; u < U; ++u) rg[u].forget();
 #pragma unroll
@@ -732,20 +773,21 @@ __global__ __launch_bounds__(256) void rec_maps_fwd(const RecParams p, long unit
     if (AGG && lane == 0 && wave == 0) p.P[place] = carryP, p.H[place] = carry;
 }
 
-template <typename T, int WPR, bool REV, bool SIG, bool AGG>
+template <typename T, typename DIMS, bool REV, bool SIG, bool AGG>
 __global__ __launch_bounds__(256) void rec_maps_bwd(const RecParams p, long units)
 {
-    constexpr int V = kMapV<T>, U = kMapU, kRowsOf = 4 / WPR;
+    constexpr int V = kMapV<T>, U = DIMS::kU, W = DIMS::kWidth, kWaves = DIMS::kWaves;
     __shared__ float tot[2][4][2];
-    const int lane = threadIdx.x % 64, wave = WPR == 1 ? 0 : threadIdx.x / 64;
-    const long unit = (p.first + blockIdx.x) * kRowsOf + (WPR == 1 ? threadIdx.x / 64 : 0);
-    if (WPR == 1 && unit >= units) return;
+    const int place_in = threadIdx.x % DIMS::kLpr, wave = place_in / 64, lane = place_in % 64;  // of the row
+    const long unit = (p.first + blockIdx.x) * DIMS::kRows + threadIdx.x / DIMS::kLpr;
+    // (rows past the last: whole waves or parts of them, and no barrier follows)
+    if (DIMS::kRows > 1 && unit >= units) return;
     const int seg = static_cast<int>(unit % p.S);
     const long row = unit / p.S, b = row / p.n, c = row % p.n;
     const T *x = static_cast<const T *>(p.x) + b * p.x_b + c * p.x_t, *g = static_cast<const T *>(p.g) + b * p.g_b + c * p.g_t;
     const T *d = static_cast<const T *>(p.dh) + b * p.d_b + c * p.d_t;
     const long t1 = static_cast<long>(seg) * p.seg, place = (b * p.S + seg) * p.n + c;
-    auto at = [&](int u) { return t1 + (static_cast<long>(wave * U + u) * 64 + lane) * V; };
+    auto at = [&](int u) { return t1 + (static_cast<long>(wave * U + u) * W + lane) * V; };
     Run<T, V, REV> rx[U], rg[U], rd[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -776,20 +818,20 @@ __global__ __launch_bounds__(256) void rec_maps_bwd(const RecParams p, long unit
     }
     float G[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) Q[u] = __shfl(P[U - 1 - u], 63 - lane), G[u] = __shfl(f[U - 1 - u], 63 - lane);
+    for (int u = 0; u < U; ++u) Q[u] = __shfl(P[U - 1 - u], W - 1 - lane, W), G[u] = __shfl(f[U - 1 - u], W - 1 - lane, W);
     float wP, wc;
-    wave_total<U>(P, h, wP, wc);
-    const float enter_w = join_waves<WPR, false>(wP, wc, enter, product, tot[0]);
-    wave_total<U>(Q, G, wP, wc);
-    const float flow_w = join_waves<WPR, true>(wP, wc, flow, unused, tot[1]);
+    wave_total<W, U>(P, h, wP, wc);
+    const float enter_w = join_waves<kWaves, false>(wP, wc, enter, product, tot[0]);
+    wave_total<W, U>(Q, G, wP, wc);
+    const float flow_w = join_waves<kWaves, true>(wP, wc, flow, unused, tot[1]);
     if (AGG) {
         if (lane == 0 && wave == 0) p.P[place] = product, p.H[place] = enter, p.F[place] = flow;
         return;
     }
-    wave_states<U>(P, h, enter_w, in);
-    wave_states<U>(Q, G, flow_w, f);
+    wave_states<W, U>(P, h, enter_w, in);
+    wave_states<W, U>(Q, G, flow_w, f);
 #pragma unroll
-    for (int u = 0; u < U; ++u) out[u] = __shfl(f[U - 1 - u], 63 - lane);
+    for (int u = 0; u < U; ++u) out[u] = __shfl(f[U - 1 - u], W - 1 - lane, W);
 #pragma unroll
     for (int u = 0; u < U; ++u) rg[u].forget();
 #pragma unroll
@@ -821,8 +863,8 @@ __global__ __launch_bounds__(256) void rec_maps_bwd(const RecParams p, long unit
 struct RecPlan {
     bool maps, packed, sig, rev;
     bool few;  // forward of few tokens: a thread walks over them
-    int v;    // token rows: channels a lane holds
-    int wpr;  // maps: waves a row
+    int v;       // token rows: channels a lane holds
+    long cells;  // maps: tokens of a row
 };
 
 template <typename F>
@@ -848,6 +890,19 @@ int with_flags(F &&f, bool first, B... rest)
 {
     if (first) return with_flags([&](auto... r) { return f(std::true_type{}, r...); }, rest...);
     return with_flags([&](auto... r) { return f(std::false_type{}, r...); }, rest...);
+}
+
+// Calls f with how rows of so many cells are held: as few lanes as hold them, so
+// that a wave has several short rows (64 maps of 768 channels, bf16, 14 x 14 cells: 22 us
+// from 62 with a wave a row, 7 x 7: 10 from 56).
+template <typename T, typename F>
+auto with_map_dims(long cells, F &&f)
+{
+    if (cells <= MapDims<16, 1>::kChunk<T>) return f(MapDims<16, 1>{});
+    if (cells <= MapDims<32, 1>::kChunk<T>) return f(MapDims<32, 1>{});
+    if (cells <= MapDims<64, 1>::kChunk<T>) return f(MapDims<64, 1>{});
+    if (cells <= MapDims<64, 2>::kChunk<T>) return f(MapDims<64, 2>{});
+    return f(MapDims<256, 2>{});
 }
 
 template <typename T>
@@ -888,16 +943,22 @@ int rec_run(const RecParams &p, const RecPlan &plan, long batch, bool agg, hipSt
         return plan.v > 1 ? go(std::integral_constant<int, kRowV<T>>{}) : go(std::integral_constant<int, 1>{});
     }
     const long units = batch * p.n * p.S;
-    return with_flags(
-        [&](auto wide, auto rev, auto sig, auto only) {
-            constexpr int W = decltype(wide)::value ? 4 : 1;
-            constexpr bool R = decltype(rev)::value, G = decltype(sig)::value, A = decltype(only)::value;
-            return rec_launch(p, (units * W + 3) / 4, 256, [&](const RecParams &q, dim3 grid) {
-                if constexpr (BWD) rec_maps_bwd<T, W, R, G, A><<<grid, dim3(256), 0, s>>>(q, units);
-                else rec_maps_fwd<T, W, R, G, A><<<grid, dim3(256), 0, s>>>(q, units);
-            });
-        },
-        plan.wpr == 4, plan.rev, plan.sig, agg);
+    return with_map_dims<T>(plan.cells, [&](auto dims) {
+        using D = decltype(dims);
+        return with_flags(
+            [&](auto rev, auto sig, auto only) {
+                constexpr bool R = decltype(rev)::value, G = decltype(sig)::value, A = decltype(only)::value;
+                if constexpr (A && D::kWaves == 1) {  // (rows of a wave or less are one chunk)
+                    return static_cast<int>(SSM2D_ERR_UNSUPPORTED);
+                } else {
+                    return rec_launch(p, (units + D::kRows - 1) / D::kRows, 256, [&](const RecParams &q, dim3 grid) {
+                        if constexpr (BWD) rec_maps_bwd<T, D, R, G, A><<<grid, dim3(256), 0, s>>>(q, units);
+                        else rec_maps_fwd<T, D, R, G, A><<<grid, dim3(256), 0, s>>>(q, units);
+                    });
+                }
+            },
+            plan.rev, plan.sig, agg);
+    });
 }
 
 }  // namespace ssm2d_impl
