@@ -24,7 +24,8 @@ SOURCES += ["layer_norm.hip", "rope.hip", "delta.hip", "delta_step.hip",
             "delta_chunk_bf16.hip", "delta_chunk_bf16_bwd.hip", "delta_chunk_f32.hip", "delta_chunk_f32_bwd.hip"]
 # the operators of a recurrent block
 SOURCES += ["block_norm.hip", "block_norm_f32.hip", "block_norm_f32_bwd.hip", "block_norm_bf16.hip", "block_norm_bf16_bwd.hip",
-            "block_norm_bf16_f32.hip", "block_norm_bf16_f32_bwd.hip", "linear.hip", "linear_bf16.hip", "linear_f32.hip", "recurrence.hip", "recurrence_bf16.hip",
+            "block_norm_bf16_f32.hip", "block_norm_bf16_f32_bwd.hip", "linear.hip", "linear_bf16.hip", "linear_bf16_bwd.hip", "linear_f32.hip",
+            "linear_f32_bwd.hip", "recurrence.hip", "recurrence_bf16.hip",
             "recurrence_bf16_bwd.hip", "recurrence_f32.hip", "recurrence_f32_bwd.hip"]
 LIB = os.path.join(PKG, "libssm2d.so")
 INCLUDE = os.path.join(ROOT, "include")

@@ -33,7 +33,13 @@ struct GemmParams {
     long c_ld, c_bs;
     int straight;     // bf16 operands can be loaded straight to LDS
     float *part;      // splits > 1: [split][batch][M][N rounded up to 4]
+    float *sums;      // [split][M] sums of A's rows over k (NULL: not wanted; batch 1)
     unsigned first;   // the launch's first workgroup
+    // columns that the launch which joins the parts sums as well: [rows][n]
+    const float *fold;
+    float *fold_to;
+    int fold_rows, fold_n;
+    unsigned join_blocks;
 };
 
 template <typename T>
@@ -226,10 +232,9 @@ struct TilePlace {
     long b;
 };
 template <int BM, int BN>
-__device__ __forceinline__ TilePlace tile_place(const GemmParams &p)
+__device__ __forceinline__ TilePlace tile_place(const GemmParams &p, unsigned id)
 {
     const unsigned total = p.total, each = total / 8, more = total % 8;
-    unsigned id = p.first + blockIdx.x;
     const unsigned die = id % 8;
     id = die * each + min(die, more) + id / 8;
     TilePlace t;
@@ -306,18 +311,49 @@ __device__ __forceinline__ void finish_tile(const GemmParams &p, const TilePlace
     else all(std::false_type{});
 }
 
-// Any alignment: operands go through registers to LDS, the next step's read
-// while this one's products run.
+// Sums of A's rows, by products with ones (the first column of tiles has them; a
+// lane's all four are one row's), a wave's rows.
+template <int WM>
+struct RowSums {
+    facc v[WM / 16];
+    bool on;
+    __device__ __forceinline__ void begin(bool wanted)
+    {
+        on = wanted;
+#pragma unroll
+        for (auto &f : v) f = facc{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    __device__ __forceinline__ void add(int i, const bfrag &a)
+    {
+        const __bf16 one = static_cast<__bf16>(1.0f);
+        const bfrag ones = {one, one, one, one, one, one, one, one};
+        v[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, a, v[i], 0, 0, 0);
+    }
+    __device__ __forceinline__ void put(const GemmParams &p, const TilePlace &t, int wm) const
+    {
+        if (!on || threadIdx.x % 64 >= 16) return;
+#pragma unroll
+        for (int i = 0; i < WM / 16; ++i) {
+            const int m = t.m0 + wm + i * 16 + static_cast<int>(threadIdx.x % 16);
+            if (m < p.M) p.sums[static_cast<long>(t.split) * p.M + m] = v[i][0];
+        }
+    }
+};
+
+// Elements of LDS: both operands' tiles, the epilogue's place too.
 template <typename T, bool A_KC, bool B_KC, int BM, int BN>
-__global__ __launch_bounds__(256, 2) void gemm_kernel(const GemmParams p)
+constexpr int kTileElems = std::max((BM + BN) * kStep<T> * kParts<T>, 4 * 32 * (BN / 2 + 4) * 2);
+
+// Any alignment: operands go through registers to LDS, the next step's read
+// while this one's products run. SUMS: A's row sums too.
+template <typename T, bool A_KC, bool B_KC, int BM, int BN, bool SUMS>
+__device__ __forceinline__ void gemm_by_registers(const GemmParams &p, unsigned id, uint16_t *tiles)
 {
     constexpr int NP = kParts<T>, BK = kStep<T>, WM = BM / 2, WN = BN / 2;
     using TA = OperandTile<A_KC, BM, BK, NP>;
     using TB = OperandTile<B_KC, BN, BK, NP>;
-    // (the epilogue's place too)
-    __shared__ __align__(16) uint16_t tiles[std::max(TA::kElems + TB::kElems, 4 * 32 * (WN + 4) * 2)];
     uint16_t *const sa = tiles, *const sb = tiles + TA::kElems;
-    const TilePlace t = tile_place<BM, BN>(p);
+    const TilePlace t = tile_place<BM, BN>(p, id);
     const T *A = static_cast<const T *>(p.a), *B = static_cast<const T *>(p.b);
     if (p.kb == 1) A += t.b * p.a_bs, B += t.b * p.b_bs;
     const int s1 = t.split * p.per, s2 = min(s1 + p.per, p.steps), each = (p.K + BK - 1) / BK;
@@ -351,6 +387,8 @@ __global__ __launch_bounds__(256, 2) void gemm_kernel(const GemmParams p)
 #pragma unroll
         for (auto &v : r) v = facc{0.0f, 0.0f, 0.0f, 0.0f};
     const int wave = threadIdx.x / 64, wm = wave / 2 * WM, wn = wave % 2 * WN;
+    RowSums<WM> sums;
+    if constexpr (SUMS) sums.begin(p.sums && t.n0 == 0 && wave % 2 == 0);
     if (s1 < s2) fetch(s1);
     for (int s = s1; s < s2; ++s) {
         __syncthreads();  // (the last step's tiles have been read)
@@ -380,10 +418,23 @@ __global__ __launch_bounds__(256, 2) void gemm_kernel(const GemmParams p)
                 for (int n = 0; n < NP; ++n) fa[n] = TA::frag(sa, n, wm + i * 16, ks);
 #pragma unroll
                 for (int j = 0; j < WN / 16; ++j) mma<NP>(acc[i][j], fb[j], fa);  // (D's rows, a lane's registers, are n)
+                if constexpr (SUMS) {
+                    if (sums.on) {
+#pragma unroll
+                        for (int n = NP - 1; n >= 0; --n) sums.add(i, fa[n]);
+                    }
+                }
             }
         }
     }
+    if constexpr (SUMS) sums.put(p, t, wm);
     finish_tile<T, BM, BN, WM, WN>(p, t, acc, tiles, wave);
+}
+template <typename T, bool A_KC, bool B_KC, int BM, int BN>
+__global__ __launch_bounds__(256, 2) void gemm_kernel(const GemmParams p)
+{
+    __shared__ __align__(16) uint16_t tiles[kTileElems<T, A_KC, B_KC, BM, BN>];
+    gemm_by_registers<T, A_KC, B_KC, BM, BN, false>(p, p.first + blockIdx.x, tiles);
 }
 
 // ------------------------------------------------------------------ straight to LDS
@@ -440,18 +491,17 @@ struct StraightLoads {
 };
 
 // bf16 operands whose rows are whole 16-byte chunks: two stages of tiles in LDS,
-// one filled by loads that pass the registers by while the other is used.
-template <bool A_KC, bool B_KC, int BM, int BN, int BK>
-__global__ __launch_bounds__(256, 2) void gemm_straight(const GemmParams p)
+// one filled by loads that pass the registers by while the other is used (arrays
+// of their own, so that a read waits for its own stage's loads alone).
+template <bool A_KC, bool B_KC, int BM, int BN, bool SUMS>
+__device__ __forceinline__ void gemm_by_lds(const GemmParams &p, unsigned id, uint16_t *ring0, uint16_t *ring1)
 {
-    constexpr int WM = BM / 2, WN = BN / 2;
+    constexpr int WM = BM / 2, WN = BN / 2, BK = kStep<uint16_t>;
     using TA = OperandTile<A_KC, BM, BK, 1>;
     using TB = OperandTile<B_KC, BN, BK, 1>;
     using LA = StraightLoads<A_KC, BM, BK>;
     using LB = StraightLoads<B_KC, BN, BK>;
-    // (variables of their own, so that a read waits for its own stage's loads alone)
-    __shared__ __align__(16) uint16_t ring0[TA::kElems + TB::kElems], ring1[TA::kElems + TB::kElems];
-    const TilePlace t = tile_place<BM, BN>(p);
+    const TilePlace t = tile_place<BM, BN>(p, id);
     const uint16_t *A = static_cast<const uint16_t *>(p.a), *B = static_cast<const uint16_t *>(p.b);
     if (p.kb == 1) A += t.b * p.a_bs, B += t.b * p.b_bs;
     LA la;
@@ -477,6 +527,8 @@ __global__ __launch_bounds__(256, 2) void gemm_straight(const GemmParams p)
 #pragma unroll
         for (auto &v : r) v = facc{0.0f, 0.0f, 0.0f, 0.0f};
     const int wave = threadIdx.x / 64, wm = wave / 2 * WM, wn = wave % 2 * WN;
+    RowSums<WM> sums;
+    if constexpr (SUMS) sums.begin(p.sums && t.n0 == 0 && wave % 2 == 0);
     auto step = [&](const uint16_t *ring) __attribute__((always_inline)) {
 #pragma unroll
         for (int ks = 0; ks < BK / 32; ++ks) {
@@ -489,6 +541,12 @@ __global__ __launch_bounds__(256, 2) void gemm_straight(const GemmParams p)
             for (int i = 0; i < WM / 16; ++i)
 #pragma unroll
                 for (int j = 0; j < WN / 16; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+            if constexpr (SUMS) {
+                if (sums.on) {
+#pragma unroll
+                    for (int i = 0; i < WM / 16; ++i) sums.add(i, fa[i]);
+                }
+            }
         }
     };
     if (ahead > 0) issue(ring0);
@@ -501,17 +559,68 @@ __global__ __launch_bounds__(256, 2) void gemm_straight(const GemmParams p)
         if (ahead > 0) issue(ring0);
         step(ring1);
     }
-    static_assert(sizeof(ring0) >= 2 * 32 * (WN + 4) * sizeof(float), "the epilogue's place");
+    if constexpr (SUMS) sums.put(p, t, wm);
+    static_assert((BM + BN) * BK * 2 >= 2 * 32 * (WN + 4) * 4, "the epilogue's place");
     finish_tile<uint16_t, BM, BN, WM, WN>(p, t, acc, wave < 2 ? ring0 : ring1, wave % 2);
+}
+template <int BM, int BN>
+constexpr int kRingElems = (BM + BN) * kStep<uint16_t>;
+template <bool A_KC, bool B_KC, int BM, int BN>
+__global__ __launch_bounds__(256, 2) void gemm_straight(const GemmParams p)
+{
+    __shared__ __align__(16) uint16_t ring0[kRingElems<BM, BN>], ring1[kRingElems<BM, BN>];
+    gemm_by_lds<A_KC, B_KC, BM, BN, false>(p, p.first + blockIdx.x, ring0, ring1);
+}
+
+// Both gradients of a projection in one launch: dweight's workgroups, then dx's (up
+// to a whole round of the dies), so that the last ones of either share the chip
+(12544 x 768 by 768, bf16: 56 us, 37 + 32 one after the other; float32, 7755 x 200 by
+97 maps: 17, 12 + 11).
+struct PairParams {
+    GemmParams dx, dw;
+    unsigned first, dw_room;  // dw's total, rounded up to the 8 dies
+};
+template <typename T, bool X_MAPS, bool Y_MAPS, int BM, bool STRAIGHT>
+__global__ __launch_bounds__(256, 2) void gemm_pair(const PairParams p)
+{
+    constexpr bool A_KC = !X_MAPS && !Y_MAPS, B_KC = X_MAPS && !Y_MAPS;  // (dx: dz by weight^T, of maps weight^T by dz)
+    const unsigned id = p.first + blockIdx.x;
+    if (id >= p.dw.total && id < p.dw_room) return;
+    if constexpr (STRAIGHT) {
+        __shared__ __align__(16) uint16_t ring0[kRingElems<BM, BM>], ring1[kRingElems<BM, BM>];
+        if (id < p.dw.total) gemm_by_lds<Y_MAPS, X_MAPS, BM, BM, true>(p.dw, id, ring0, ring1);
+        else gemm_by_lds<A_KC, B_KC, BM, BM, false>(p.dx, id - p.dw_room, ring0, ring1);
+    } else {
+        __shared__ __align__(16) uint16_t tiles[kTileElems<T, A_KC, B_KC, BM, BM>];
+        if (id < p.dw.total) gemm_by_registers<T, Y_MAPS, X_MAPS, BM, BM, true>(p.dw, id, tiles);
+        else gemm_by_registers<T, A_KC, B_KC, BM, BM, false>(p.dx, id - p.dw_room, tiles);
+    }
 }
 
 // Adds the splits' sums, four threads a run of columns each every fourth, then
-// those in order; then the epilogue.
+// those in order; then the epilogue. Workgroups behind them: sums of columns.
 template <typename T>
 __global__ __launch_bounds__(256) void gemm_join(const GemmParams p)
 {
     constexpr int V = kWide<T>;
     __shared__ float sums[4][64][V + 1];
+    if (p.first + blockIdx.x >= p.join_blocks) {
+        float(&s)[16][17] = *reinterpret_cast<float(*)[16][17]>(sums);
+        const int cx = threadIdx.x % 16, ry = threadIdx.x / 16, c = static_cast<int>(p.first + blockIdx.x - p.join_blocks) * 16 + cx;
+        float v = 0.0f;
+        if (c < p.fold_n) {
+#pragma unroll 8
+            for (int r = ry; r < p.fold_rows; r += 16) v += p.fold[static_cast<long>(r) * p.fold_n + c];
+        }
+        s[ry][cx] = v;
+        __syncthreads();
+        if (ry != 0 || c >= p.fold_n) return;
+        v = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v += s[r][cx];
+        p.fold_to[c] = v;
+        return;
+    }
     const long ldp = (p.N + 3) / 4 * 4, runs = (p.N + V - 1) / V;
     const long i = static_cast<long>(p.first + blockIdx.x) * 64 + threadIdx.x % 64;
     const unsigned turn = threadIdx.x / 64;
@@ -557,6 +666,7 @@ struct GemmPlan {
     int bm, splits;
     int steps, per;
     int64_t bytes;  // of the splits' sums
+    double us;      // as counted
 };
 
 // The choice with the least time by this count, in us, of what was measured (bf16;
@@ -567,42 +677,91 @@ struct GemmPlan {
 // 193 undivided; 196 x 768 of 768: 7.4 us undivided, 11.5 in two parts. Short float32 sums of
 // few steps are taken in tiles of 64, whose loads more workgroups keep under way
 // (128 of 128 channels by 196608 cells: 84 us, 93 in tiles of 128).
+struct GemmCost {
+    double alone, full;  // of a workgroup alone, of the chip full of them
+};
 template <typename T>
-GemmPlan plan_gemm(long batch, long M, long N, long K, long kb)
+GemmCost gemm_cost(const GemmPlan &g, long batch, long M, long N, int bm, int parts)
 {
     constexpr bool kHalf = sizeof(T) == 2;
-    GemmPlan g{};
-    g.steps = static_cast<int>((K + kStep<T> - 1) / kStep<T> * kb);  // (less than 2^31: checked at the entries)
-    g.bm = 64, g.splits = 1;
-    double best = 0.0;
-    for (const int bm : {64, 128}) {
-        if (bm == 128 && !kHalf && K <= 256 && kb == 1) continue;
-        const double tiles = static_cast<double>((M + bm - 1) / bm) * static_cast<double>((N + bm - 1) / bm) * static_cast<double>(batch);
-        const double alone = bm == 64 ? (kHalf ? 0.4 : 1.1) : (kHalf ? 0.8 : 2.0), full = bm == 64 ? (kHalf ? 0.22 : 0.48) : (kHalf ? 0.5 : 1.4);
-        for (const int parts : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
-            const int per = (g.steps + parts - 1) / parts;
-            if (parts > 1 && (per < 4 || tiles * parts > 2048.0)) continue;
-            const double rounds = tiles * parts / 256.0;
-            double us = per * std::max(alone, rounds * full);
-            if (parts > 1) us += 4.0 + parts * static_cast<double>(batch) * static_cast<double>(M) * static_cast<double>(N) * 8.0 / 4e6;
-            if (best == 0.0 || us < best) best = us, g.bm = bm, g.splits = parts;
-        }
-    }
-    g.per = std::max((g.steps + g.splits - 1) / g.splits, 1);
+    const double tiles = static_cast<double>((M + bm - 1) / bm) * static_cast<double>((N + bm - 1) / bm) * static_cast<double>(batch);
+    const double per = (g.steps + parts - 1) / parts;
+    return {per * (bm == 64 ? (kHalf ? 0.4 : 1.1) : (kHalf ? 0.8 : 2.0)), per * tiles * parts / 256.0 * (bm == 64 ? (kHalf ? 0.22 : 0.48) : (kHalf ? 0.5 : 1.4))};
+}
+// What parts cost, or 0 of one; less than 0: not taken.
+inline double parts_cost(const GemmPlan &g, long batch, long M, long N, int bm, int parts)
+{
+    if (parts == 1) return 0.0;
+    const double tiles = static_cast<double>((M + bm - 1) / bm) * static_cast<double>((N + bm - 1) / bm) * static_cast<double>(batch);
+    if ((g.steps + parts - 1) / parts < 4 || tiles * parts > 2048.0) return -1.0;
+    return 4.0 + parts * static_cast<double>(batch) * static_cast<double>(M) * static_cast<double>(N) * 8.0 / 4e6;
+}
+constexpr int kGemmParts[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
+
+inline void cut_plan(GemmPlan &g, long batch, long M, long N, int bm, int parts)
+{
+    g.bm = bm;
+    g.per = std::max((g.steps + parts - 1) / parts, 1);
     g.splits = std::max((g.steps + g.per - 1) / g.per, 1);
     g.bytes = g.splits > 1 ? static_cast<int64_t>(g.splits) * batch * M * round_up_to(N, 4) * 4 : 0;
-    return g;
 }
 
 template <typename T>
-int run_gemm(GemmParams p, bool a_kc, bool b_kc, void *ws, hipStream_t s);
+GemmPlan plan_gemm(long batch, long M, long N, long K, long kb)
+{
+    GemmPlan g{};
+    g.steps = static_cast<int>((K + kStep<T> - 1) / kStep<T> * kb);  // (less than 2^31: checked at the entries)
+    int side = 64, cuts = 1;
+    g.us = -1.0;
+    for (const int bm : {64, 128}) {
+        if (bm == 128 && sizeof(T) == 4 && K <= 256 && kb == 1) continue;
+        for (const int parts : kGemmParts) {
+            const double extra = parts_cost(g, batch, M, N, bm, parts);
+            if (extra < 0.0) continue;
+            const GemmCost c = gemm_cost<T>(g, batch, M, N, bm, parts);
+            const double us = std::max(c.alone, c.full) + extra;
+            if (g.us < 0.0 || us < g.us) g.us = us, side = bm, cuts = parts;
+        }
+    }
+    cut_plan(g, batch, M, N, side, cuts);
+    return g;
+}
+
+// Both of a projection's gradients in one launch with tiles of one size, where
+// that is counted to take less than one after the other (a launch is 3).
+template <typename T>
+bool plan_pair(GemmPlan &dx, GemmPlan &dw, long batch, long M, long N, long n, long k)
+{
+    double best = dx.us + dw.us + 3.0;
+    bool pair = false;
+    const GemmPlan x = dx, w = dw;
+    for (const int bm : {64, 128})
+        for (const int parts : kGemmParts) {
+            const double extra = parts_cost(w, 1, n, k, bm, parts);
+            if (extra < 0.0) continue;
+            const GemmCost a = gemm_cost<T>(x, batch, M, N, bm, 1), b = gemm_cost<T>(w, 1, n, k, bm, parts);
+            const double us = std::max({a.alone, b.alone, a.full + b.full}) + extra;
+            if (us >= best) continue;
+            best = us, pair = true;
+            cut_plan(dx, batch, M, N, bm, 1);
+            cut_plan(dw, 1, n, k, bm, parts);
+        }
+    return pair;
+}
+
+// A product as planned; ws: its parts' sums. Columns that p.fold names are summed too, in the joining launch or one more.
+template <typename T>
+int run_gemm(GemmParams p, const GemmPlan &g, bool a_kc, bool b_kc, void *ws, hipStream_t s);
+// dx (undivided) and dw as planned together, in tiles of one size.
+template <typename T>
+int run_pair(GemmParams dx, const GemmPlan &gx, GemmParams dw, const GemmPlan &gw, bool x_maps, bool y_maps, void *ws, hipStream_t s);
 
 template <typename F>
-int gemm_launch(GemmParams &p, long groups, F &&f)
+int gemm_launch(unsigned &at, long groups, F &&f)
 {
     const long most = most_groups(256) / 8 * 8;
     for (long first = 0; first < groups; first += most) {
-        p.first = static_cast<unsigned>(first);
+        at = static_cast<unsigned>(first);
         f(dim3(static_cast<unsigned>(std::min(groups - first, most))));
         const int st = launched();
         if (st != SSM2D_OK) return st;
@@ -610,29 +769,35 @@ int gemm_launch(GemmParams &p, long groups, F &&f)
     return SSM2D_OK;
 }
 
-#define SSM2D_DEFINE_RUN_GEMM(T)                                                                                     \
-    template <>                                                                                                      \
-    int run_gemm<T>(GemmParams p, bool a_kc, bool b_kc, void *ws, hipStream_t s)                                     \
-    {                                                                                                                \
-        return run_gemm_of<T>(p, a_kc, b_kc, ws, s);                                                                 \
-    }
+inline void lay_out(GemmParams &p, const GemmPlan &g, void *ws)
+{
+    p.splits = g.splits, p.steps = g.steps, p.per = g.per, p.part = static_cast<float *>(ws);
+    p.tiles_m = (p.M + g.bm - 1) / g.bm, p.tiles_n = (p.N + g.bm - 1) / g.bm;
+    p.total = p.tiles_m * p.tiles_n * static_cast<unsigned>(p.batch) * p.splits;
+}
 
 template <typename T>
-int run_gemm_of(GemmParams p, bool a_kc, bool b_kc, void *ws, hipStream_t s)
+int run_join(GemmParams &p, hipStream_t s)
 {
-    const GemmPlan g = plan_gemm<T>(p.batch, p.M, p.N, p.K, p.kb);
-    p.splits = g.splits, p.steps = g.steps, p.per = g.per, p.part = static_cast<float *>(ws);
+    if (p.splits == 1 && !p.fold) return SSM2D_OK;
+    const long blocks = p.splits == 1 ? 0 : (p.batch * p.M * ((p.N + kWide<T> - 1) / kWide<T>) + 63) / 64;
+    p.join_blocks = static_cast<unsigned>(blocks);
+    return gemm_launch(p.first, blocks + (p.fold ? (p.fold_n + 15) / 16 : 0), [&](dim3 grid) { gemm_join<T><<<grid, dim3(256), 0, s>>>(p); });
+}
+
+template <typename T>
+int run_gemm_of(GemmParams p, const GemmPlan &g, bool a_kc, bool b_kc, void *ws, hipStream_t s)
+{
+    lay_out(p, g, ws);
     auto go = [&](auto size) {
-        constexpr int BM = decltype(size)::value, kBK = kStep<uint16_t>;
-        p.tiles_m = (p.M + BM - 1) / BM, p.tiles_n = (p.N + BM - 1) / BM;
-        p.total = p.tiles_m * p.tiles_n * static_cast<unsigned>(p.batch) * p.splits;
-        return gemm_launch(p, p.total, [&](dim3 grid) {
+        constexpr int BM = decltype(size)::value;
+        return gemm_launch(p.first, p.total, [&](dim3 grid) {
             if constexpr (sizeof(T) == 2) {
                 if (p.straight) {
-                    if (a_kc && b_kc) gemm_straight<true, true, BM, BM, kBK><<<grid, dim3(256), 0, s>>>(p);
-                    else if (a_kc) gemm_straight<true, false, BM, BM, kBK><<<grid, dim3(256), 0, s>>>(p);
-                    else if (b_kc) gemm_straight<false, true, BM, BM, kBK><<<grid, dim3(256), 0, s>>>(p);
-                    else gemm_straight<false, false, BM, BM, kBK><<<grid, dim3(256), 0, s>>>(p);
+                    if (a_kc && b_kc) gemm_straight<true, true, BM, BM><<<grid, dim3(256), 0, s>>>(p);
+                    else if (a_kc) gemm_straight<true, false, BM, BM><<<grid, dim3(256), 0, s>>>(p);
+                    else if (b_kc) gemm_straight<false, true, BM, BM><<<grid, dim3(256), 0, s>>>(p);
+                    else gemm_straight<false, false, BM, BM><<<grid, dim3(256), 0, s>>>(p);
                     return;
                 }
             }
@@ -642,12 +807,33 @@ int run_gemm_of(GemmParams p, bool a_kc, bool b_kc, void *ws, hipStream_t s)
             else gemm_kernel<T, false, false, BM, BM><<<grid, dim3(256), 0, s>>>(p);
         });
     };
-    int st = g.bm == 128 ? go(std::integral_constant<int, 128>{}) : go(std::integral_constant<int, 64>{});
-    if (st == SSM2D_OK && p.splits > 1) {
-        const long runs = p.batch * p.M * ((p.N + kWide<T> - 1) / kWide<T>);
-        st = gemm_launch(p, (runs + 63) / 64, [&](dim3 grid) { gemm_join<T><<<grid, dim3(256), 0, s>>>(p); });
-    }
-    return st;
+    const int st = g.bm == 128 ? go(std::integral_constant<int, 128>{}) : go(std::integral_constant<int, 64>{});
+    return st == SSM2D_OK ? run_join<T>(p, s) : st;
+}
+
+template <typename T>
+int run_pair_of(GemmParams dx, const GemmPlan &gx, GemmParams dw, const GemmPlan &gw, bool x_maps, bool y_maps, void *ws, hipStream_t s)
+{
+    lay_out(dx, gx, nullptr);
+    lay_out(dw, gw, ws);
+    PairParams p{dx, dw, 0, static_cast<unsigned>(round_up_to(dw.total, 8))};
+    auto go = [&](auto size, auto straight) {
+        constexpr int BM = decltype(size)::value;
+        constexpr bool L = decltype(straight)::value;
+        return gemm_launch(p.first, static_cast<long>(p.dw_room) + dx.total, [&](dim3 grid) {
+            if (x_maps && y_maps) gemm_pair<T, true, true, BM, L><<<grid, dim3(256), 0, s>>>(p);
+            else if (x_maps) gemm_pair<T, true, false, BM, L><<<grid, dim3(256), 0, s>>>(p);
+            else if (y_maps) gemm_pair<T, false, true, BM, L><<<grid, dim3(256), 0, s>>>(p);
+            else gemm_pair<T, false, false, BM, L><<<grid, dim3(256), 0, s>>>(p);
+        });
+    };
+    auto sized = [&](auto straight) {
+        return gw.bm == 128 ? go(std::integral_constant<int, 128>{}, straight) : go(std::integral_constant<int, 64>{}, straight);
+    };
+    int st;
+    if constexpr (sizeof(T) == 2) st = dx.straight && dw.straight ? sized(std::true_type{}) : sized(std::false_type{});
+    else st = sized(std::false_type{});
+    return st == SSM2D_OK ? run_join<T>(dw, s) : st;
 }
 
 }  // namespace gemm

@@ -13,9 +13,13 @@ namespace ssm2d_impl {
 namespace gemm {
 
 template <>
-int run_gemm<uint16_t>(GemmParams p, bool a_kc, bool b_kc, void *ws, hipStream_t s);
+int run_gemm<uint16_t>(GemmParams p, const GemmPlan &g, bool a_kc, bool b_kc, void *ws, hipStream_t s);
 template <>
-int run_gemm<float>(GemmParams p, bool a_kc, bool b_kc, void *ws, hipStream_t s);
+int run_gemm<float>(GemmParams p, const GemmPlan &g, bool a_kc, bool b_kc, void *ws, hipStream_t s);
+template <>
+int run_pair<uint16_t>(GemmParams dx, const GemmPlan &gx, GemmParams dw, const GemmPlan &gw, bool x_maps, bool y_maps, void *ws, hipStream_t s);
+template <>
+int run_pair<float>(GemmParams dx, const GemmPlan &gx, GemmParams dw, const GemmPlan &gw, bool x_maps, bool y_maps, void *ws, hipStream_t s);
 
 }  // namespace gemm
 
@@ -207,7 +211,7 @@ struct Side {
 };
 
 template <typename T>
-int product(GemmParams &g, const Side &a, const Side &b, void *ws, hipStream_t s)
+void sides(GemmParams &g, const Side &a, const Side &b)
 {
     const long kb = g.kb > 1 ? g.kb : g.batch;
     g.a = a.p, g.a_ld = a.ld, g.a_bs = a.bs, g.b = b.p, g.b_ld = b.ld, g.b_bs = b.bs;
@@ -216,7 +220,6 @@ int product(GemmParams &g, const Side &a, const Side &b, void *ws, hipStream_t s
         return in_words(x.p, len, x.ld, kb > 1 ? x.bs : 0, sizeof(T)) && x.ld >= len && x.ld < (1L << 22);
     };
     g.straight = sizeof(T) == 2 && straight(a, a.kc ? g.K : g.M) && straight(b, b.kc ? g.K : g.N);
-    return run_gemm<T>(g, a.kc, b.kc, ws, s);
 }
 
 template <typename T>
@@ -245,8 +248,8 @@ int linear_fwd(const T *x, const T *weight, const float *bias, const T *res, T *
     if (off_by(x, sizeof(T)) || off_by(weight, sizeof(T)) || off_by(res, sizeof(T)) || off_by(y, sizeof(T)) || off_by(pre, sizeof(T)) ||
         off_by(bias, 4) || off_by(ws, 16))
         return SSM2D_ERR_MISALIGNED;
-    const int64_t need = plan_fwd<T>(*a, flags).bytes;
-    if (need > 0 && (!ws || ws_bytes < need)) return SSM2D_ERR_NOMEM;
+    const GemmPlan plan = plan_fwd<T>(*a, flags);
+    if (plan.bytes > 0 && (!ws || ws_bytes < plan.bytes)) return SSM2D_ERR_NOMEM;
     const bool xm = flags & SSM2D_LINEAR_X_MAPS, ym = flags & SSM2D_LINEAR_Y_MAPS;
     GemmParams g{};
     g.batch = a->batch, g.kb = 1, g.K = static_cast<int>(a->k);
@@ -256,18 +259,22 @@ int linear_fwd(const T *x, const T *weight, const float *bias, const T *res, T *
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (ym) {
         g.M = static_cast<int>(a->n), g.N = static_cast<int>(a->rows), g.c_ld = a->rows;
-        return product<T>(g, w, in, ws, s);
+        sides<T>(g, w, in);
+    } else {
+        g.M = static_cast<int>(a->rows), g.N = static_cast<int>(a->n), g.c_ld = a->n;
+        sides<T>(g, in, w);
     }
-    g.M = static_cast<int>(a->rows), g.N = static_cast<int>(a->n), g.c_ld = a->n;
-    return product<T>(g, in, w, ws, s);
+    return run_gemm<T>(g, plan, ym || !xm, !ym || !xm, ws, s);
 }
 
-// The backward's workspace: dz, then the slices' sums or (later) the splits'.
+// The backward's workspace: dz, the slices' sums (or those of dweight's parts: not
+// both), and the parts' sums.
 struct BwdPlan {
     int slices;
     long each;
-    int64_t dz, rest;
-    GemmPlan dx, dw;
+    int64_t dz, sums, parts;
+    GemmPlan dx, dw, pair_dx, pair_dw;
+    bool pair;
 };
 template <typename T>
 BwdPlan plan_bwd(const ssm2d_linear_shape &a, int act, uint32_t flags)
@@ -275,9 +282,12 @@ BwdPlan plan_bwd(const ssm2d_linear_shape &a, int act, uint32_t flags)
     BwdPlan p{};
     slope_slices(a, flags & SSM2D_LINEAR_Y_MAPS, &p.slices, &p.each);
     p.dz = act != SSM2D_ACT_NONE ? round_up_to(a.batch * a.rows * a.n * static_cast<int64_t>(sizeof(T)), 256) : 0;
-    p.dx = flags & SSM2D_LINEAR_X_MAPS ? plan_gemm<T>(a.batch, a.k, a.rows, a.n, 1) : plan_gemm<T>(a.batch, a.rows, a.k, a.n, 1);
-    p.dw = plan_gemm<T>(1, a.n, a.k, a.rows, a.batch);
-    p.rest = std::max<int64_t>({p.dx.bytes, p.dw.bytes, p.slices * a.batch * a.n * 4});
+    const long M = flags & SSM2D_LINEAR_X_MAPS ? a.k : a.rows, N = flags & SSM2D_LINEAR_X_MAPS ? a.rows : a.k;
+    p.pair_dx = p.dx = plan_gemm<T>(a.batch, M, N, a.n, 1);
+    p.pair_dw = p.dw = plan_gemm<T>(1, a.n, a.k, a.rows, a.batch);
+    p.pair = a.k > 0 && plan_pair<T>(p.pair_dx, p.pair_dw, a.batch, M, N, a.n, a.k);
+    p.sums = round_up_to(std::max<int64_t>(p.slices * a.batch, std::max(p.dw.splits, p.pair_dw.splits)) * a.n * 4, 16);
+    p.parts = std::max({p.dx.bytes, p.dw.bytes, p.pair_dw.bytes});
     return p;
 }
 
@@ -288,7 +298,7 @@ int64_t bwd_workspace(const ssm2d_linear_shape *a, int act, uint32_t flags)
     if (st != SSM2D_OK) return -st;
     if (a->batch == 0 || a->rows == 0 || a->n == 0) return 0;
     const BwdPlan p = plan_bwd<T>(*a, act, flags);
-    return p.dz + p.rest;
+    return p.dz + p.sums + p.parts;
 }
 
 template <typename T>
@@ -330,44 +340,55 @@ int linear_bwd(const T *x, const T *weight, const T *pre, const T *dy, T *dx, T 
     if (!dx && !dweight && !dbias) return SSM2D_OK;
     if (!dy || (act != SSM2D_ACT_NONE && !pre) || (dx && !weight) || (dweight && !x)) return SSM2D_ERR_NULLPTR;
     const BwdPlan plan = plan_bwd<T>(*a, act, flags);
-    if (!ws || ws_bytes < plan.dz + plan.rest) return SSM2D_ERR_NOMEM;
+    if (!ws || ws_bytes < plan.dz + plan.sums + plan.parts) return SSM2D_ERR_NOMEM;
     const bool xm = flags & SSM2D_LINEAR_X_MAPS, ym = flags & SSM2D_LINEAR_Y_MAPS;
-    void *rest = static_cast<char *>(ws) + plan.dz;
+    float *sums = reinterpret_cast<float *>(static_cast<char *>(ws) + plan.dz);
+    void *parts = static_cast<char *>(ws) + plan.dz + plan.sums;
+    const bool pair = plan.pair && dx && dweight;
+    // dbias without an activation: dweight's product sums dy's rows with the rest
+    // (with one, its slopes are summed as they were before dz was rounded).
+    const bool by_product = pair && dbias && act == SSM2D_ACT_NONE;
     Side dz{dy, a->r_stride[1], a->r_stride[0], true};  // (contiguous: channels of rows, cells of maps)
-    if (act != SSM2D_ACT_NONE || dbias) {
+    int sum_rows = 0;
+    if (act != SSM2D_ACT_NONE || (dbias && !by_product)) {
         SlopeParams p{};
-        p.dy = dy, p.pre = pre, p.dz = act != SSM2D_ACT_NONE && (dx || dweight) ? ws : nullptr, p.part = dbias ? static_cast<float *>(rest) : nullptr;
+        p.dy = dy, p.pre = pre, p.dz = act != SSM2D_ACT_NONE && (dx || dweight) ? ws : nullptr, p.part = dbias ? sums : nullptr;
         p.batch = B, p.rows = R, p.n = n, p.d_b = a->r_stride[0], p.d_s = a->r_stride[1], p.act = act, p.slices = plan.slices, p.each = plan.each;
         if ((st = run_slope<T>(p, ym, s)) != SSM2D_OK) return st;
-        if (dbias) {
-            fold_rows<<<dim3(fold_blocks(n)), dim3(kFoldThreads), 0, s>>>(p.part, static_cast<int>(plan.slices * B), n, dbias);
-            if ((st = launched()) != SSM2D_OK) return st;
-        }
+        if (dbias) sum_rows = static_cast<int>(plan.slices * B);
         if (act != SSM2D_ACT_NONE) dz = Side{ws, ym ? R : n, R * n, true};
     }
-    const Side in{x, a->x_stride[1], a->x_stride[0], true};
+    if (dbias && !dweight) {
+        fold_rows<<<dim3(fold_blocks(n)), dim3(kFoldThreads), 0, s>>>(sums, sum_rows, n, dbias);
+        if ((st = launched()) != SSM2D_OK) return st;
+    }
     auto along = [](Side side, bool kc) {
         side.kc = kc;
         return side;
     };
+    GemmParams gx{}, gw{};
     if (dx) {
-        GemmParams g{};
-        g.batch = B, g.kb = 1, g.K = static_cast<int>(n), g.c = dx, g.c_bs = R * k;
+        gx.batch = B, gx.kb = 1, gx.K = static_cast<int>(n), gx.c = dx, gx.c_bs = R * k;
         const Side w{weight, a->w_stride, 0, false};
         if (xm) {
-            g.M = static_cast<int>(k), g.N = static_cast<int>(R), g.c_ld = R;
-            st = product<T>(g, w, along(dz, !ym), rest, s);
+            gx.M = static_cast<int>(k), gx.N = static_cast<int>(R), gx.c_ld = R;
+            sides<T>(gx, w, along(dz, !ym));
         } else {
-            g.M = static_cast<int>(R), g.N = static_cast<int>(k), g.c_ld = k;
-            st = product<T>(g, along(dz, !ym), w, rest, s);
+            gx.M = static_cast<int>(R), gx.N = static_cast<int>(k), gx.c_ld = k;
+            sides<T>(gx, along(dz, !ym), w);
         }
-        if (st != SSM2D_OK) return st;
+        if (!pair && (st = run_gemm<T>(gx, plan.dx, !xm && !ym, xm && !ym, parts, s)) != SSM2D_OK) return st;
     }
     if (dweight) {
-        GemmParams g{};
-        g.batch = 1, g.kb = static_cast<int>(B), g.K = static_cast<int>(R), g.M = static_cast<int>(n), g.N = static_cast<int>(k);
-        g.c = dweight, g.c_ld = k;
-        st = product<T>(g, along(dz, ym), along(in, xm), rest, s);
+        gw.batch = 1, gw.kb = static_cast<int>(B), gw.K = static_cast<int>(R), gw.M = static_cast<int>(n), gw.N = static_cast<int>(k);
+        gw.c = dweight, gw.c_ld = k;
+        sides<T>(gw, along(dz, ym), Side{x, a->x_stride[1], a->x_stride[0], xm});
+        if (by_product) {
+            gw.sums = plan.pair_dw.splits > 1 ? sums : dbias;
+            sum_rows = plan.pair_dw.splits > 1 ? plan.pair_dw.splits : 0;
+        }
+        if (dbias && sum_rows > 0) gw.fold = sums, gw.fold_to = dbias, gw.fold_rows = sum_rows, gw.fold_n = static_cast<int>(n);
+        st = pair ? run_pair<T>(gx, plan.pair_dx, gw, plan.pair_dw, xm, ym, parts, s) : run_gemm<T>(gw, plan.dw, ym, xm, parts, s);
     }
     return st;
 }

@@ -4,7 +4,11 @@
 namespace ssm2d_impl {
 namespace gemm {
 
-SSM2D_DEFINE_RUN_GEMM(uint16_t)
+template <>
+int run_gemm<uint16_t>(GemmParams p, const GemmPlan &g, bool a_kc, bool b_kc, void *ws, hipStream_t s)
+{
+    return run_gemm_of<uint16_t>(p, g, a_kc, b_kc, ws, s);
+}
 
 }  // namespace gemm
 }  // namespace ssm2d_impl
