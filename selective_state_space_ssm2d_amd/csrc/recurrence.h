@@ -6,11 +6,12 @@
 // product of its a's, so stretches are worked on at once and joined in a fixed
 // order: a thread takes neighbouring tokens of its channels one after the other,
 // threads are joined within a wave and over the workgroup's waves, workgroups
-// through a small workspace (rec_join). A workgroup holds a chunk of tokens in
-// registers as it was read: it needs each input once where it can walk over all
-// tokens of its channels, and where there are too few channels for that (the
-// host's choice) a first launch reads the inputs for P and c alone.
-// The backward joins both ways: e[t] = dh[t] + a[t + 1] e[t + 1] is the same
+// through a small workspace. A workgroup holds a chunk of tokens in registers and
+// needs each input once. The forward walks over all tokens of its channels, or
+// where there are too few channels for that (the host's choice) chunks go to
+// workgroups of their own, which hand the state on (Relay). The backward, which
+// goes both ways, has a first launch that reads the inputs for P and c alone.
+// It joins both ways: e[t] = dh[t] + a[t + 1] e[t + 1] is the same
 // recurrence from the end, and what flows out of a stretch, f = a e, is P f' + c'.
 // States are fp32 throughout, also in the backward, which computes them again.
 //
@@ -30,7 +31,10 @@ struct RecParams {
     const int *cu;
     void *h, *dx, *dg;
     float *h_last, *dh_init;
-    float *P, *H, *F;              // [batch][segment][channel]: a segment's product and sums, then what enters it
+    float *P, *H, *F;              // backward, [batch][segment][channel]: a segment's product and sums, then what enters it
+    unsigned long *parts;          // forward, from workgroup to workgroup
+    unsigned *tickets, *enter;
+    long chains;                   // rows of maps, or tiles of channels, of the batch
     long T;                        // tokens
     long seg;                      // tokens of a segment
     int S;                         // segments
@@ -121,12 +125,69 @@ __device__ __forceinline__ Place locate_first(const RecParams &p, long t)
     return locate_by(p, t, [&](int i) { return in_tokens(p, cu[i]); });
 }
 
+// ------------------------------------------------------------------ from workgroup to workgroup
+
+// A forward in segments of one chunk. Each workgroup puts down its segment's
+// product and sum, and takes what enters it from those before it in its group of
+// segments and from what enters the group, which the last segment of the group
+// before puts down. So sums are taken in one order whatever comes first, the
+// inputs are read once, and only groups wait for each other.
+// Every wait ends: a channel's segments are taken by tickets in their order, so all
+// that a workgroup waits for belongs to workgroups that run already; they put their
+// products down before they wait, and the first of those that wait has all it
+// needs. (A counter for each row of maps or tile of channels: all workgroups at one
+// counter took 13 ns each, 175 us for the 73 below.) (196608 cells of 128 channels, float32: 73 us; 95 with a launch for the products,
+// one that joins them and one for the states. 16698 packed tokens of 1024, bf16: 45, 69 so.)
+// Words say for themselves that they are there: all bits set, a NaN that nothing
+// else is put down as, they are not. No order between them is needed.
+constexpr unsigned long kNotYet = ~0ul;
+constexpr int kMostPolls = 1 << 22;  // (seconds, before it goes on with a NaN rather than never)
+
+__device__ __forceinline__ void put_down(unsigned long *to, float P, float c)
+{
+    unsigned long w = static_cast<unsigned long>(__float_as_uint(P)) << 32 | __float_as_uint(c);
+    if (w == kNotYet) w = 0x7fc000007fc00000ul;
+    __hip_atomic_store(to, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ unsigned state_word(float h)
+{
+    const unsigned w = __float_as_uint(h);
+    return w == ~0u ? 0x7fc00000u : w;
+}
+__device__ __forceinline__ void put_down(unsigned *to, float h) { __hip_atomic_store(to, state_word(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+// Waits for the first `count` of V words.
+template <int V, typename W>
+__device__ __forceinline__ void take_up(const W *from, long step, int count, W (&w)[V])
+{
+    for (int polls = 0; polls < kMostPolls; ++polls) {
+        bool there = true;
+#pragma unroll
+        for (int j = 0; j < V; ++j) w[j] = __hip_atomic_load(from + min(j, count - 1) * step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+        for (int j = 0; j < V; ++j) there = there && w[j] != static_cast<W>(kNotYet);
+        if (there) return;
+        __builtin_amdgcn_s_sleep(2);
+    }
+}
+// The workgroup's segment of a row of maps or tile of channels.
+constexpr int kTicketWords = 32;  // from counter to counter, a line of their own
+__device__ __forceinline__ int draw_ticket(const RecParams &p, long chain)
+{
+    __shared__ unsigned drawn;
+    if (threadIdx.x == 0) drawn = __hip_atomic_fetch_add(p.tickets + chain * kTicketWords, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(static_cast<int>(drawn));
+}
+
 // ------------------------------------------------------------------ token rows
 
-template <typename T, int V, bool BWD>
+// How a workgroup holds token rows: 16 lanes of 8 bytes (128-byte runs; single channels
+// by 32 lanes, where there are fewer or rows are far apart) by 16 lots of 8 tokens, WIDE 32,
+// where a workgroup has one chunk. (Relays of 16384 x 1024, bf16: 35 us; lots of 4
+// tokens, more workgroups that each wait: 60, when those of 8 took 49.)
+template <typename T, int V, bool WIDE>
 struct RowDims {
-    // 16 lanes of 8 bytes (128-byte runs) by 16 (backward 32) lots of 8 tokens; single channels where there are fewer or rows are far apart
-    static constexpr int kBX = V > 1 ? 16 : 32, kBY = (BWD ? 512 : 256) / kBX, kThreads = kBX * kBY, kWaves = kThreads / 64;
+    static constexpr int kBX = V > 1 ? 16 : 32, kBY = (WIDE ? 512 : 256) / kBX, kThreads = kBX * kBY, kWaves = kThreads / 64;
     static constexpr int kL = 8, kChunk = kBY * kL;
 };
 
@@ -151,13 +212,13 @@ struct Line {
     }
 };
 
-// Joins the threads' stretches (P, c) of a workgroup in token order: *in gets
-// the state before each thread's stretch given `carry` before the workgroup's,
-// and carry (with carryP, the product so far) moves to its end. DOWN: in reverse
-// token order. tot: LDS for this use alone until the next barrier but one.
-template <int V, int BX, int WAVES, bool PACKED, bool DOWN>
-__device__ __forceinline__ void join_lots(float (&P)[V], float (&c)[V], float (&carry)[V], float (&carryP)[V], float (&in)[V],
-                                          float (*tot)[BX * V][2])
+// Joins the threads' stretches (P, c) of a workgroup in token order. lots_up: within
+// the waves, whose totals go to `tot`; eP, ec: what is before a thread's in its wave.
+// lots_in: `in` gets the state before each thread's stretch given `carry` before
+// the workgroup's, and carry (with carryP, the product so far) moves to its end. DOWN:
+// in reverse token order. tot: LDS for this use alone until the next barrier but one.
+template <int V, int BX, bool PACKED, bool DOWN>
+__device__ __forceinline__ void lots_up(float (&P)[V], float (&c)[V], float (&eP)[V], float (&ec)[V], float (*tot)[BX * V][2])
 {
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, cx = lane % BX, sub = lane / BX;
     constexpr int kSubs = 64 / BX;
@@ -173,13 +234,19 @@ __device__ __forceinline__ void join_lots(float (&P)[V], float (&c)[V], float (&
 #pragma unroll
         for (int j = 0; j < V; ++j) tot[wave][cx * V + j][0] = P[j], tot[wave][cx * V + j][1] = c[j];
     }
-    float eP[V], ec[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         eP[j] = DOWN ? __shfl_down(P[j], BX) : __shfl_up(P[j], BX);
         ec[j] = DOWN ? __shfl_down(c[j], BX) : __shfl_up(c[j], BX);
     }
     __syncthreads();
+}
+template <int V, int BX, int WAVES, bool PACKED, bool DOWN>
+__device__ __forceinline__ void lots_in(const float (&eP)[V], const float (&ec)[V], float (&carry)[V], float (&carryP)[V], float (&in)[V],
+                                        const float (*tot)[BX * V][2])
+{
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, cx = lane % BX, sub = lane / BX;
+    constexpr int kSubs = 64 / BX;
     // (two waves at a time: all at once would take the registers of the lots)
     float h[V];
 #pragma unroll
@@ -202,6 +269,14 @@ __device__ __forceinline__ void join_lots(float (&P)[V], float (&c)[V], float (&
         carry[j] = h[j];
         if (sub != (DOWN ? kSubs - 1 : 0)) in[j] = pass<PACKED>(eP[j], ec[j], in[j]);
     }
+}
+template <int V, int BX, int WAVES, bool PACKED, bool DOWN>
+__device__ __forceinline__ void join_lots(float (&P)[V], float (&c)[V], float (&carry)[V], float (&carryP)[V], float (&in)[V],
+                                          float (*tot)[BX * V][2])
+{
+    float eP[V], ec[V];
+    lots_up<V, BX, PACKED, DOWN>(P, c, eP, ec, tot);
+    lots_in<V, BX, WAVES, PACKED, DOWN>(eP, ec, carry, carryP, in, tot);
 }
 
 // Which of a thread's L tokens from t on are the first or the last of a packed
@@ -304,17 +379,15 @@ __device__ __forceinline__ void pass_on(const RecParams &p, const float *src, fl
     }
 }
 
-// AGG: only the segment's product and state from zero, into P and H.
-template <typename T, int V, bool PACKED, bool SIG, bool AGG>
-__global__ __launch_bounds__(256, 4) void rec_rows_fwd(const RecParams p)
+// RELAY: a segment a workgroup, of one chunk. Otherwise all tokens.
+template <typename T, int V, bool PACKED, bool SIG, bool RELAY>
+__global__ __launch_bounds__(RELAY ? 512 : 256, 4) void rec_rows_fwd(const RecParams p)
 {
-    using D = RowDims<T, V, false>;
+    using D = RowDims<T, V, RELAY>;
     __shared__ float tot[2][D::kWaves][D::kBX * V][2];
     const int cx = threadIdx.x % D::kBX, ty = threadIdx.x / D::kBX;
-    const int tile = static_cast<int>((p.first + blockIdx.x) % p.tiles);
-    const long rest = (p.first + blockIdx.x) / p.tiles;
-    const int seg = static_cast<int>(rest % p.S);
-    const long b = rest / p.S;
+    const long id = p.first + blockIdx.x, chain = RELAY ? id % p.chains : id, b = chain / p.tiles;
+    const int tile = static_cast<int>(chain % p.tiles), seg = RELAY ? draw_ticket(p, chain) : 0;
     const int c0 = (tile * D::kBX + cx) * V;
     const bool live = c0 < p.n;
     // (the last lane of a row reaches back over the one before: both get the same values)
@@ -322,17 +395,13 @@ __global__ __launch_bounds__(256, 4) void rec_rows_fwd(const RecParams p)
     const T *x = static_cast<const T *>(p.x), *g = static_cast<const T *>(p.g);
     T *h_out = static_cast<T *>(p.h);
     const long t1 = static_cast<long>(seg) * p.seg, t2 = min(t1 + p.seg, p.T);
-    const long place = (b * p.S + seg) * p.n + c;
     float carry[V], carryP[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         carryP[j] = 1.0f, carry[j] = 0.0f;
-        if (!AGG) {
-            if (p.S > 1) carry[j] = p.H[place + j];
-            else if (!PACKED && p.h_init) carry[j] = p.h_init[b * p.n + c + j];
-        }
+        if (!RELAY && !PACKED && p.h_init) carry[j] = p.h_init[b * p.n + c + j];
     }
-    if (PACKED && !AGG && p.pass_on && live) pass_on<V>(p, p.h_init, p.h_last, c, seg * D::kBY + ty, p.S * D::kBY);
+    if (PACKED && p.pass_on && live) pass_on<V>(p, p.h_init, p.h_last, c, seg * D::kBY + ty, p.S * D::kBY);
     int buf = 0;
     for (long t0 = t1; t0 < t2; t0 += D::kChunk, buf ^= 1) {
         const long mine = t0 + ty * D::kL;
@@ -350,40 +419,95 @@ __global__ __launch_bounds__(256, 4) void rec_rows_fwd(const RecParams p)
         }
         Marks<D::kL> marks;
         if constexpr (PACKED) marks.find(p, t0, D::kChunk, mine);
-        float P[V], h[V], in[V];
+        // what each token does to the state: h = a h + wx (a first one of a sequence: h = wx)
+        float a[D::kL][V], wx[D::kL][V], P[V], h[V], in[V], eP[V], ec[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) P[j] = 1.0f, h[j] = 0.0f;
-        // One token on, of the product too until the true states are known.
-        auto step = [&](int i, bool product, bool cut) __attribute__((always_inline)) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float a, w;
-                gates<T, SIG>(rg[i].get(j), a, w);
-                const float wx = SIG ? w * rx[i].get(j) : rx[i].get(j);
-                if (PACKED && cut && marks.none(i)) {
-                    P[j] = kCut, h[j] = 0.0f;
-                } else if (PACKED && cut && marks.first(i)) {
-                    P[j] = kCut, h[j] = fmaf(a, state_at(p, p.h_init, mine + i, c + j), wx);
-                } else {
-                    if (product && !(cut && is_cut<PACKED>(P[j]))) P[j] *= a;
-                    h[j] = fmaf(a, h[j], wx);
-                }
-            }
-        };
         // (whole lots inside one sequence, which are most, go without a branch)
         const bool whole = cnt == D::kL && !(PACKED && marks.any());
+#pragma unroll
+        for (int i = 0; i < D::kL; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float w;
+                gates<T, SIG>(rg[i].get(j), a[i][j], w);
+                wx[i][j] = SIG ? w * rx[i].get(j) : rx[i].get(j);
+            }
         if (whole) {
 #pragma unroll
-            for (int i = 0; i < D::kL; ++i) step(i, true, false);
+            for (int i = 0; i < D::kL; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) P[j] *= a[i][j], h[j] = fmaf(a[i][j], h[j], wx[i][j]);
         } else {
 #pragma unroll
-            for (int i = 0; i < D::kL; ++i)
-                if (i < cnt) step(i, true, true);
-        }
-        join_lots<V, D::kBX, D::kWaves, PACKED, false>(P, h, carry, carryP, in, tot[buf]);
-        if (AGG) continue;
+            for (int i = 0; i < D::kL; ++i) {
+                if (i >= cnt) continue;
+                const bool cut = PACKED && (marks.first(i) || marks.none(i));
 #pragma unroll
-        for (int i = 0; i < D::kL; ++i) rg[i].forget(), rx[i].forget();
+                for (int j = 0; j < V; ++j) {
+                    if (cut) {
+                        if (marks.none(i)) wx[i][j] = 0.0f;
+                        else wx[i][j] = fmaf(a[i][j], state_at(p, p.h_init, mine + i, c + j), wx[i][j]);
+                        P[j] = kCut, h[j] = wx[i][j];
+                    } else {
+                        if (!is_cut<PACKED>(P[j])) P[j] *= a[i][j];
+                        h[j] = fmaf(a[i][j], h[j], wx[i][j]);
+                    }
+                }
+            }
+        }
+        lots_up<V, D::kBX, PACKED, false>(P, h, eP, ec, tot[buf]);
+        if constexpr (RELAY) {
+            // A lane a channel here, so that words are asked for in whole lines and few
+            // registers are held beside the tokens' (lanes of V channels, 4 times the
+            // requests past the caches, and spills: 71 us for those 45).
+            constexpr int C = D::kBX * V, kShares = D::kThreads / C, kGroup = 4 * kShares;  // segments of a group
+            __shared__ float before[kShares][C][2], into[D::kWaves][C];
+            const int l = threadIdx.x % C, share = threadIdx.x / C, first = (tile * D::kBX + l / V) * V;
+            const bool here = first < p.n;
+            const int ch = min(first, p.n - V) + l % V;
+            const int k = seg % kGroup, group = seg / kGroup, groups = (p.S + kGroup - 1) / kGroup;
+            unsigned *enter = p.enter + (b * groups + group) * p.n + ch;
+            float q = 1.0f, d = 0.0f;
+            auto also = [&](const float(&w)[2]) __attribute__((always_inline)) {
+                float P1 = w[0], c1 = w[1];
+                join<PACKED>(q, d, P1, c1);
+                q = P1, d = c1;
+            };
+            if (share == 0 && here && seg + 1 < p.S) {
+                for (int w = 0; w < D::kWaves; ++w) also(tot[buf][w][l]);
+                put_down(p.parts + (b * p.S + seg) * p.n + ch, q, d);
+                q = 1.0f, d = 0.0f;
+            }
+            if (here && share * 4 < k) {
+                unsigned long w[4];
+                take_up<4>(p.parts + (b * p.S + seg - k + share * 4) * p.n + ch, static_cast<long>(p.n), min(k - share * 4, 4), w);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (share * 4 + i < k) also({__uint_as_float(static_cast<unsigned>(w[i] >> 32)), __uint_as_float(static_cast<unsigned>(w[i]))});
+            }
+            before[share][l][0] = q, before[share][l][1] = d;
+            unsigned w[1] = {0u};
+            if (share == 0 && here) take_up<1>(enter, 0, 1, w);
+            __syncthreads();
+            if (share == 0 && here) {
+                float state = __uint_as_float(w[0]);
+                for (int i = 0; i * 4 < k; ++i) state = pass<PACKED>(before[i][l][0], before[i][l][1], state);
+                for (int i = 0; i < D::kWaves; ++i) {
+                    into[i][l] = state;
+                    state = pass<PACKED>(tot[buf][i][l][0], tot[buf][i][l][1], state);
+                }
+                if (k + 1 == kGroup && seg + 1 < p.S) put_down(enter + p.n, state);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                in[j] = into[threadIdx.x / 64][cx * V + j];
+                if (threadIdx.x % 64 >= D::kBX) in[j] = pass<PACKED>(eP[j], ec[j], in[j]);
+            }
+        } else {
+            lots_in<V, D::kBX, D::kWaves, PACKED, false>(eP, ec, carry, carryP, in, tot[buf]);
+        }
 #pragma unroll
         for (int j = 0; j < V; ++j) h[j] = in[j];
         auto put = [&](int i) __attribute__((always_inline)) {
@@ -398,7 +522,8 @@ __global__ __launch_bounds__(256, 4) void rec_rows_fwd(const RecParams p)
         if (whole) {
 #pragma unroll
             for (int i = 0; i < D::kL; ++i) {
-                step(i, false, false);
+#pragma unroll
+                for (int j = 0; j < V; ++j) h[j] = fmaf(a[i][j], h[j], wx[i][j]);
                 if (live) put(i);
             }
             if (!PACKED && p.h_last && live && mine + D::kL == p.T) keep(b);
@@ -406,16 +531,14 @@ __global__ __launch_bounds__(256, 4) void rec_rows_fwd(const RecParams p)
 #pragma unroll
             for (int i = 0; i < D::kL; ++i) {
                 if (i >= cnt) continue;
-                step(i, false, true);
+                const bool cut = PACKED && (marks.first(i) || marks.none(i));
+#pragma unroll
+                for (int j = 0; j < V; ++j) h[j] = cut ? wx[i][j] : fmaf(a[i][j], h[j], wx[i][j]);
                 if (!live || (PACKED && marks.none(i))) continue;
                 put(i);
                 if (p.h_last && (PACKED ? marks.end(i) : mine + i + 1 == p.T)) keep(PACKED ? locate(p, mine + i).seq : b);
             }
         }
-    }
-    if (AGG && live && ty == 0) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) p.P[place + j] = carryP[j], p.H[place + j] = carry[j];
     }
 }
 
@@ -711,7 +834,8 @@ __device__ __forceinline__ float join_waves(float wP, float wc, float &carry, fl
     return in;
 }
 
-template <typename T, typename DIMS, bool REV, bool SIG, bool AGG>
+// RELAY: a segment a workgroup, of one chunk. Otherwise all tokens.
+template <typename T, typename DIMS, bool REV, bool SIG, bool RELAY>
 __global__ __launch_bounds__(256) void rec_maps_fwd(const RecParams p, long units)
 {
     constexpr int V = kMapV<T>, U = DIMS::kU, W = DIMS::kWidth, kWaves = DIMS::kWaves, kChunk = DIMS::template kChunk<T>;
@@ -720,18 +844,16 @@ __global__ __launch_bounds__(256) void rec_maps_fwd(const RecParams p, long unit
     const long unit = (p.first + blockIdx.x) * DIMS::kRows + threadIdx.x / DIMS::kLpr;
     // (rows past the last: whole waves or parts of them, and no barrier follows)
     if (DIMS::kRows > 1 && unit >= units) return;
-    const int seg = static_cast<int>(unit % p.S);
-    const long row = unit / p.S, b = row / p.n, c = row % p.n;
+    const long row = RELAY ? unit % p.chains : unit, b = row / p.n, c = row % p.n;
+    const int seg = RELAY ? draw_ticket(p, row) : 0;
     const T *x = static_cast<const T *>(p.x) + b * p.x_b + c * p.x_t, *g = static_cast<const T *>(p.g) + b * p.g_b + c * p.g_t;
     T *h_out = static_cast<T *>(p.h) + row * p.T;
     const long t1 = static_cast<long>(seg) * p.seg, t2 = min(t1 + p.seg, p.T);
-    const long place = (b * p.S + seg) * p.n + c;
-    float carry = 0.0f, carryP = 1.0f;
-    if (!AGG) carry = p.S > 1 ? p.H[place] : (p.h_init ? p.h_init[row] : 0.0f);
+    float carry = !RELAY && p.h_init ? p.h_init[row] : 0.0f, carryP = 1.0f;
     int buf = 0;
     for (long t0 = t1; t0 < t2; t0 += kChunk, buf ^= 1) {
         Run<T, V, REV> rx[U], rg[U];
-        float P[U], h[U], in[U];
+        float a[U][V], wx[U][V], P[U], h[U], in[U];
         auto at = [&](int u) { return t0 + (static_cast<long>(wave * U + u) * W + lane) * V; };
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -744,33 +866,60 @@ __global__ __launch_bounds__(256) void rec_maps_fwd(const RecParams p, long unit
             P[u] = 1.0f, h[u] = 0.0f;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                float a, w;
-                gates<T, SIG>(rg[u].get(j), a, w);
-                h[u] = fmaf(a, h[u], SIG ? w * rx[u].get(j) : rx[u].get(j));
-                P[u] *= a;
+                float w;
+                gates<T, SIG>(rg[u].get(j), a[u][j], w);
+                wx[u][j] = SIG ? w * rx[u].get(j) : rx[u].get(j);
+                h[u] = fmaf(a[u][j], h[u], wx[u][j]);
+                P[u] *= a[u][j];
             }
         }
         float wP, wc;
         wave_total<W, U>(P, h, wP, wc);
-        const float enter = join_waves<kWaves, false>(wP, wc, carry, carryP, tot[buf]);
-        if (AGG) continue;
-        wave_states<W, U>(P, h, enter, in);
+        float enter;
+        if constexpr (RELAY) {
+            __shared__ float entering;
+            constexpr int kGroup = 64;  // segments of a group: a lane each
+            const int k = seg % kGroup, group = seg / kGroup, groups = (p.S + kGroup - 1) / kGroup;
+            if (lane == 0) tot[0][wave][0] = wP, tot[0][wave][1] = wc;
+            __syncthreads();
+            if (wave == 0) {
+                float sP = 1.0f, sc = 0.0f;
 #pragma unroll
-        for (int u = 0; u < U; ++u) rg[u].forget();
+                for (int i = 0; i < kWaves; ++i) sc = fmaf(tot[0][i][0], sc, tot[0][i][1]), sP *= tot[0][i][0];
+                if (lane == 0 && seg + 1 < p.S) put_down(p.parts + row * p.S + seg, sP, sc);
+                float pP = 1.0f, pc = 0.0f;
+                if (lane < k) {
+                    unsigned long w[1];
+                    take_up<1>(p.parts + row * p.S + seg - k + lane, 0, 1, w);
+                    pP = __uint_as_float(static_cast<unsigned>(w[0] >> 32)), pc = __uint_as_float(static_cast<unsigned>(w[0]));
+                }
+                unsigned w[1];
+                take_up<1>(p.enter + row * groups + group, 0, 1, w);
+                wave_join<64>(pP, pc);
+                const float into = fmaf(last_lane<64>(pP), __uint_as_float(w[0]), last_lane<64>(pc));
+                if (lane == 0) {
+                    entering = into;
+                    if (k + 1 == kGroup && seg + 1 < p.S) put_down(p.enter + row * groups + group + 1, fmaf(sP, into, sc));
+                }
+            }
+            __syncthreads();
+            enter = entering;
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i)
+                if (i < wave) enter = fmaf(tot[0][i][0], enter, tot[0][i][1]);
+        } else {
+            enter = join_waves<kWaves, false>(wP, wc, carry, carryP, tot[buf]);
+        }
+        wave_states<W, U>(P, h, enter, in);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float o[V], v = in[u];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float a, w;
-                gates<T, SIG>(rg[u].get(j), a, w);
-                o[j] = v = fmaf(a, v, SIG ? w * rx[u].get(j) : rx[u].get(j));
-            }
+            for (int j = 0; j < V; ++j) o[j] = v = fmaf(a[u][j], v, wx[u][j]);
             store_run<T, V, REV>(h_out, at(u), p.T, o);
             if (p.h_last && at(u) < p.T && at(u) + V >= p.T) p.h_last[row] = v;  // (past the last token it stays)
         }
     }
-    if (AGG && lane == 0 && wave == 0) p.P[place] = carryP, p.H[place] = carry;
 }
 
 template <typename T, typename DIMS, bool REV, bool SIG, bool AGG>
@@ -932,7 +1081,7 @@ int rec_run(const RecParams &p, const RecPlan &plan, long batch, bool agg, hipSt
             return with_flags(
                 [&](auto packed, auto sig, auto only) {
                     constexpr bool K = decltype(packed)::value, G = decltype(sig)::value, A = decltype(only)::value;
-                    constexpr int kThreads = RowDims<T, V, BWD>::kThreads;
+                    constexpr int kThreads = RowDims<T, V, BWD || A>::kThreads;
                     return rec_launch(p, batch * p.S * p.tiles, kThreads, [&](const RecParams &q, dim3 grid) {
                         if constexpr (BWD) rec_rows_bwd<T, V, K, G, A><<<grid, dim3(kThreads), 0, s>>>(q);
                         else rec_rows_fwd<T, V, K, G, A><<<grid, dim3(kThreads), 0, s>>>(q);

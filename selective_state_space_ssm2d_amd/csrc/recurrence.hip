@@ -47,7 +47,21 @@ __global__ __launch_bounds__(256) void rec_join(const RecParams p)
         __syncthreads();
     };
     both(p.H, false, !PACKED && p.h_init && live ? p.h_init[b * p.n + chan] : 0.0f);
-    if (p.F) both(p.F, true, !PACKED && p.dh_last && live ? p.dh_last[b * p.n + chan] : 0.0f);
+    both(p.F, true, !PACKED && p.dh_last && live ? p.dh_last[b * p.n + chan] : 0.0f);
+}
+
+// Before a relay: nothing is there but what enters the first segments (rows:
+// [batch][group][channel], maps: [batch][channel][group]).
+__global__ __launch_bounds__(256) void relay_open(const RecParams p, long parts, long enters, int groups, int maps)
+{
+    const long i = (p.first + blockIdx.x) * 256 + threadIdx.x;
+    if (i < p.chains) p.tickets[i * kTicketWords] = 0u;
+    if (i < parts) p.parts[i] = kNotYet;
+    if (i >= enters) return;
+    const long b = i / (static_cast<long>(groups) * p.n), at = i % (static_cast<long>(groups) * p.n);
+    const bool first = maps ? at % groups == 0 : at < p.n;
+    const long c = maps ? at / groups : at;
+    p.enter[i] = first ? (p.h_init && p.n_seq == 0 ? state_word(p.h_init[b * p.n + c]) : 0u) : ~0u;
 }
 
 __global__ void copy_floats(const float *src, float *dst, long n)
@@ -80,41 +94,46 @@ bool few_tokens(const ssm2d_recurrence_shape &a, uint32_t flags) { return a.toke
 struct Cut {
     long seg;
     int S, tiles;
+    int groups;    // forward: of the relay
+    int64_t chains;
 };
 template <typename T, bool BWD>
 Cut cut_tokens(const ssm2d_recurrence_shape &a, uint32_t flags, int v)
 {
     Cut c{};
-    long chunk, groups;
+    // A workgroup's chunk: of one that walks over them, and of a relay or the backward's.
+    long chunk, wide, groups;
+    int relay = 64;  // segments of a group
+    double fit;      // workgroups that the chip takes at once, of those that walk
     if (flags & SSM2D_RECUR_MAPS) {
         int rows = 1;
-        chunk = with_map_dims<T>(a.tokens, [&](auto dims) {
+        chunk = wide = with_map_dims<T>(a.tokens, [&](auto dims) {
             rows = decltype(dims)::kRows;
             return static_cast<long>(decltype(dims)::template kChunk<T>);
         });
         groups = (a.batch * a.channels + rows - 1) / rows;
+        fit = 2048.0;
     } else {
-        const int bx = v > 1 ? RowDims<T, kRowV<T>, BWD>::kBX : RowDims<T, 1, BWD>::kBX;
-        chunk = v > 1 ? RowDims<T, kRowV<T>, BWD>::kChunk : RowDims<T, 1, BWD>::kChunk;
-        c.tiles = static_cast<int>((a.channels + bx * v - 1) / (bx * v));
+        auto dims = [&](auto vec) {
+            using N = RowDims<T, decltype(vec)::value, false>;
+            using W = RowDims<T, decltype(vec)::value, true>;
+            chunk = N::kChunk, wide = W::kChunk, relay = 4 * W::kThreads / (W::kBX * v);
+            c.tiles = static_cast<int>((a.channels + N::kBX * v - 1) / (N::kBX * v));
+        };
+        if (v > 1) dims(std::integral_constant<int, kRowV<T>>{});
+        else dims(std::integral_constant<int, 1>{});
         groups = a.batch * c.tiles;
+        fit = 1024.0;
     }
+    // Segments of one chunk, or of all tokens: the forward walks over all chunks where
+    // its channels make workgroups enough, by what rounds of as many workgroups as
+    // fit the chip take. (A relay's start and its waits are as long as two rounds.)
     const long chunks = (a.tokens + chunk - 1) / chunk;
-    // The backward has to hold what it walks over twice: a segment is a chunk. The
-    // forward walks over all chunks where its channels make workgroups enough,
-    // else it takes segments in two passes: by what full rounds of as many
-    // workgroups as fit the chip take. (Each pass's last round is seldom full:
-    // segments of one chunk, as long as their number does not make the join long.
-    // 16698 packed tokens of 1024 channels, bf16: 69 us in 131 segments, 73 in 66.)
-    long segs = chunks;
-    if (!BWD) {
-        const double fit = flags & SSM2D_RECUR_MAPS ? 2048.0 : 1024.0;
-        const double walk = std::ceil(groups / fit) * chunks, cut = 2.0 * std::ceil(static_cast<double>(groups) * chunks / fit) + 2.0;
-        if (walk <= cut) segs = 1;
-    }
-    segs = std::max(std::min(segs, 512L), 1L);
-    c.seg = (chunks + segs - 1) / segs * chunk;
-    c.S = static_cast<int>((a.tokens + c.seg - 1) / std::max(c.seg, 1L));
+    const double walk = std::ceil(groups / fit) * chunks, cut = std::ceil(static_cast<double>(groups) * chunks / fit) + 2.0;
+    c.seg = BWD || walk > cut ? wide : std::max(chunks, 1L) * chunk;
+    c.S = static_cast<int>((a.tokens + c.seg - 1) / c.seg);
+    c.groups = (c.S + relay - 1) / relay;
+    c.chains = a.batch * (flags & SSM2D_RECUR_MAPS ? a.channels : c.tiles);
     return c;
 }
 
@@ -137,8 +156,9 @@ int64_t rec_workspace(const ssm2d_recurrence_shape *a, uint32_t flags)
     if (a->batch == 0 || a->tokens == 0 || a->channels == 0) return 0;
     int64_t bytes = 0;
     for (const int v : {kRowV<T>, 1}) {
-        const int64_t S = cut_tokens<T, BWD>(*a, flags, v).S;
-        if (S > 1) bytes = std::max(bytes, (BWD ? 3 : 2) * a->batch * S * a->channels * 4);
+        const Cut c = cut_tokens<T, BWD>(*a, flags, v);
+        const int64_t lines = a->batch * a->channels;
+        if (c.S > 1) bytes = std::max(bytes, BWD ? 3 * lines * c.S * 4 : lines * (int64_t{8} * c.S + int64_t{4} * c.groups) + c.chains * kTicketWords * 4);
     }
     if (shares_states<T>(*a, flags) && (BWD || !few_tokens(*a, flags))) bytes = round_up(bytes, 16) + std::max(a->n_seq, a->batch) * a->channels * 4;
     return bytes;
@@ -187,7 +207,12 @@ int rec_entry(const T *x, const T *g, const float *h_init, const int32_t *cu, co
     if (BWD) p.dx = out, p.dg = dg, p.dh_init = last;
     else p.h = out, p.h_last = last;
     const long plane = B * p.S * n;
-    p.P = static_cast<float *>(ws), p.H = p.P + plane, p.F = BWD ? p.H + plane : nullptr;
+    if (BWD) {
+        p.P = static_cast<float *>(ws), p.H = p.P + plane, p.F = p.H + plane;
+    } else {
+        p.parts = static_cast<unsigned long *>(ws), p.enter = reinterpret_cast<unsigned *>(p.parts + plane);
+        p.tickets = p.enter + B * n * c.groups, p.chains = c.chains;
+    }
     if (last && last == state) {
         if (shares_states<T>(*a, flags) && !plan.few) {
             float *copy = reinterpret_cast<float *>(static_cast<char *>(ws) + (need - states * 4));
@@ -197,6 +222,16 @@ int rec_entry(const T *x, const T *g, const float *h_init, const int32_t *cu, co
         }
     } else {
         p.pass_on = plan.packed && last;
+    }
+    if (!BWD) {
+        if (p.S > 1) {
+            const long enters = B * n * c.groups;
+            const int opened = rec_launch(p, (std::max(plane, enters) + 255) / 256, 256, [&](const RecParams &q, dim3 grid) {
+                relay_open<<<grid, dim3(256), 0, s>>>(q, plane, enters, c.groups, plan.maps);
+            });
+            if (opened != SSM2D_OK) return opened;
+        }
+        return rec_run<T, BWD>(p, plan, B, p.S > 1, s);
     }
     if (p.S > 1) {
         if ((st = rec_run<T, BWD>(p, plan, B, true, s)) != SSM2D_OK) return st;

@@ -313,3 +313,63 @@ def test_deterministic():
     s = make(1, 20000, 96, "bf16", 13)
     a, b = (pkg.recurrence_bwd(s["x"], s["g"], s["dh"]) for _ in range(2))
     assert all(torch.equal(a[k], b[k]) for k in a)
+
+
+# ------------------------------------------------------------------ many segments
+
+def _scan(a, c):
+    """h[t] = a[t] h[t - 1] + c[t] along the last dim in 64 bits, by doubling."""
+    a, c, d = a.clone(), c.clone(), 1
+    while d < a.shape[-1]:
+        c[..., d:] = a[..., d:] * c[..., :-d] + c[..., d:]
+        a[..., d:] = a[..., d:] * a[..., :-d]
+        d *= 2
+    return c
+
+
+# A workgroup's chunk has 128 tokens (64 where channels are taken one by one), and 2048 or 4096
+# cells of maps; groups of 16, 8 and 64 chunks hand the state on. Each group and each
+# chunk after the first rounds a state of what was before once: at most 2 U times the number of
+# groups (here 10 at most) beside the joins within them.
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("batch,tokens,n", [(1, 2048, 64), (1, 2049, 64), (1, 4501, 70), (3, 2300, 5), (2, 1100, 1), (1, 64 * 32 + 1, 3)])
+def test_many_segments(batch, tokens, n, dtype):
+    check(make(batch, tokens, n, dtype, tokens, sig=True), True, what=f"{tokens} tokens")
+    check(make(batch, tokens, n, dtype, tokens + 1, state=False), rev=True, what=f"{tokens} tokens reversed")
+
+
+@pytest.mark.parametrize("maps", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_groups(dtype, maps):
+    tokens, n = (64 * 4096 + 5 if dtype == "bf16" else 64 * 2048 * 2 + 2048, 3) if maps else (9000, 40)
+    s = make(2, tokens, n, dtype, 5, maps=maps)
+    order = lambda t: t.double() if maps else t.double().transpose(1, 2)  # noqa: E731
+    x, g, h0 = order(s["x"]), order(s["g"]), s["h_init"].double()
+    a = torch.exp(g)
+    first = torch.zeros_like(x)
+    first[..., 0] = a[..., 0] * h0
+    want = _scan(a, x + first)
+    H = _scan(a, x.abs() + first.abs())
+    prev = torch.cat([h0.abs()[..., None], H[..., :-1]], -1)
+    bar = _scan(a, (12 + 4 * g.abs()) * U * (a * prev + x.abs())) + 64 * U * H
+    for _ in range(3):
+        h, last = pkg.recurrence_fwd(s["x"], s["g"], gates="decay", h_init=s["h_init"], channels_first=maps, return_last_state=True)
+        _near(order(h), want, bar + _half(want, DT[dtype]), "h")
+        _near(last, want[..., -1], bar[..., -1] + _half(want[..., -1], torch.float32), "h_last")
+
+
+@pytest.mark.parametrize("maps", [True, False])
+def test_any_nan_is_handed_on(maps):
+    """A NaN of any bits reaches all later tokens of its channel and no other channel."""
+    shape, at = ((1, 4, 9000), (0, 2, 100)) if maps else ((1, 5000, 40), (0, 100, 2))
+    for bits in (-1, 0x7fc00000, 0x7f800001):
+        x, g = torch.ones(shape, device="cuda"), torch.full(shape, -0.5, device="cuda")
+        h0 = torch.zeros(1, shape[1] if maps else shape[2], device="cuda")
+        clean = pkg.recurrence_fwd(x, g, gates="decay", h_init=h0, channels_first=maps)
+        x[at] = torch.tensor([bits], dtype=torch.int32, device="cuda").view(torch.float32)[0]
+        h0[0, 1] = x[at]
+        h = pkg.recurrence_fwd(x, g, gates="decay", h_init=h0, channels_first=maps)
+        rows = (lambda t: t[0]) if maps else (lambda t: t[0].t())
+        assert rows(h)[1].isnan().all() and rows(h)[2, 100:].isnan().all()
+        keep = [i for i in range(h0.shape[1]) if i not in (1, 2)]
+        assert torch.equal(rows(h)[keep], rows(clean)[keep]) and torch.equal(rows(h)[2, :100], rows(clean)[2, :100])
