@@ -228,3 +228,39 @@ def test_many_batches_and_deterministic():
     x, w, dy = _randn((9000, 64), "bf16", 1), _randn((96, 64), "bf16", 2), _randn((9000, 96), "bf16", 3)
     a, b = (pkg.linear_bwd(x, w, dy) for _ in range(2))
     assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cf,ocf", [(False, False), (False, True), (True, False), (True, True)])
+def test_each_gradient_alone(cf, ocf, dtype):
+    """The C entry leaves out the gradients it has no pointer for; the others are right in any company."""
+    from selective_state_space_ssm2d_amd import block
+
+    B, R, k, n = 2, 1500, 72, 40
+    x, w, dy = _randn((B, k, R) if cf else (B, R, k), dtype, 1), _randn((n, k), dtype, 2), _randn((B, n, R) if ocf else (B, R, n), dtype, 3)
+    fn, _, s, flags, need, _, _ = block._linear_plan(True, x, w, None, dy, None, 0, cf, ocf)
+    up, xr = _rows(dy, ocf).double(), _rows(x, cf).double()
+    flat, fx = up.reshape(-1, n), xr.reshape(-1, k)
+    dx, dw, db = up @ w.double(), flat.t() @ fx, flat.sum(0)
+    bars = {"dx": _sum_bar(n, dtype) * (up.abs() @ w.double().abs()) + _half(dx, dtype),
+            "dweight": _sum_bar(B * R, dtype) * (flat.abs().t() @ fx.abs()) + _half(dw, dtype),
+            "dbias": (3 * B * R + 2) * U * flat.abs().sum(0)}  # (float32 as three parts: additions of each)
+    for wanted in range(1, 8):
+        out = {"dx": torch.full_like(x, 7.0), "dweight": torch.full_like(w, 7.0), "dbias": torch.full((n,), 7.0, device="cuda")}
+        work = torch.empty(need, dtype=torch.uint8, device="cuda")
+        ptr = [t.data_ptr() if wanted >> i & 1 else None for i, t in enumerate(out.values())]
+        assert fn(x.data_ptr(), w.data_ptr(), None, dy.data_ptr(), *ptr, s, 0, flags, work.data_ptr(), need, torch.cuda.current_stream().cuda_stream) == 0
+        for i, (name, want) in enumerate(zip(out, (dx, dw, db))):
+            got = _rows(out[name], cf) if name == "dx" else out[name]
+            if wanted >> i & 1:
+                _near(got, want, bars[name], f"{name} of {wanted}")
+            else:
+                assert (got == 7.0).all(), (name, wanted)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,k,n,act", [(2, 16, 16, "silu"), (3, 2000, 5, None), (40000, 16, 24, None), (40000, 20, 9, "gelu"), (12544, 136, 264, None)])
+def test_gradients_of_few_and_many_rows(rows, k, n, act, dtype):
+    """Sums undivided and in parts, one gradient's workgroups few beside the other's."""
+    x, w = _randn((rows, k), dtype, rows), _randn((n, k), dtype, 1, k ** -0.5)
+    check(x, w, torch.zeros(n, device="cuda"), None, act, dtype=dtype, dy=_randn((rows, n), dtype, 2), what=f"{rows} rows")

@@ -373,3 +373,36 @@ def test_any_nan_is_handed_on(maps):
         assert rows(h)[1].isnan().all() and rows(h)[2, 100:].isnan().all()
         keep = [i for i in range(h0.shape[1]) if i not in (1, 2)]
         assert torch.equal(rows(h)[keep], rows(clean)[keep]) and torch.equal(rows(h)[2, :100], rows(clean)[2, :100])
+
+
+@pytest.mark.parametrize("kind", ["rows", "maps", "packed"])
+def test_relays_at_once(kind):
+    """Chunks that hand the state on, in three streams at once and in two graphs replayed in turn: the same bits each time."""
+    maps, lens = kind == "maps", [3000, 0, 1, 4999] if kind == "packed" else None
+    s = make(1, 300000 if maps else 8000, 2 if maps else 40, "f32", 3, maps=maps, sig=True, lens=lens)
+
+    def run():
+        return pkg.recurrence_fwd(s["x"], s["g"], gates="sigmoid", h_init=s["h_init"], cu_seqlens=s["cu"], channels_first=maps, return_last_state=True)
+
+    want = run()
+    torch.cuda.synchronize()
+    streams, got, graphs = [torch.cuda.Stream() for _ in range(3)], [], []
+    for _ in range(4):
+        for st in streams:
+            with torch.cuda.stream(st):
+                got.append(run())
+    torch.cuda.synchronize()
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = run()
+        graphs.append((g, out))
+    for _ in range(3):
+        for g, out in graphs:
+            out[0].zero_()
+            g.replay()
+        got.append(run())
+        torch.cuda.synchronize()
+        got += [tuple(t.clone() for t in out) for _, out in graphs]
+    for h, last in got:
+        assert torch.equal(h, want[0]) and torch.equal(last, want[1])
