@@ -574,8 +574,8 @@ __global__ __launch_bounds__(256, 2) void gemm_straight(const GemmParams p)
 
 // Both gradients of a projection in one launch: dweight's workgroups, then dx's (up
 // to a whole round of the dies), so that the last ones of either share the chip
-(12544 x 768 by 768, bf16: 56 us, 37 + 32 one after the other; float32, 7755 x 200 by
-97 maps: 17, 12 + 11).
+// (12544 x 768 by 768, bf16: 56 us, 37 + 32 one after the other; float32, 7755 x 200 by
+// 97 maps: 17, 12 + 11).
 struct PairParams {
     GemmParams dx, dw;
     unsigned first, dw_room;  // dw's total, rounded up to the 8 dies
