@@ -8,10 +8,11 @@
  * its kernels on `stream` and returns a status without waiting; it never throws
  * or aborts. All pointers are DEVICE pointers on the current HIP device, aligned
  * to their element. Strides count elements and are not negative unless said so.
- * Outputs are dense and must not alias an input unless said so. A `_bf16` entry takes bfloat16 bits (uint16_t) where the plain one takes
- * the same tensor in float32; sums, statistics and states are fp32, and each
- * bf16 output is rounded once (nearest even). No result depends on the order of
- * atomics: there are none, and every output is deterministic.
+ * Outputs are dense and must not alias an input unless said so. A `_bf16` entry
+ * takes bfloat16 bits (uint16_t) where the plain one takes the same tensor in
+ * float32; sums, statistics and states are fp32, and each bf16 output is rounded
+ * once (nearest even). Sums are taken in one order whichever workgroup comes
+ * first: every output is deterministic.
  *
  * Workspaces are the caller's: a call that needs one takes `workspace`
  * (16-byte aligned, at least as many bytes as the entry's _workspace function
@@ -51,9 +52,10 @@ extern "C" {
  * bf16 products are exact and summed in fp32. float32 operands go through the
  * bf16 matrix instructions in three exact parts and six products, which keeps
  * an error of about 2^-24 of the largest term; an operand that is Inf or NaN
- * gives Inf or NaN in the outputs that it enters, not always the one fp32
- * arithmetic would give.
- * Limits: rows, n, k < 2^31 - 256, batch < 2^31, strides < 2^40, fewer than 2^31 tiles of 64 x 64 in y.
+ * gives Inf or NaN in the outputs that it enters (dbias too), not always the one
+ * fp32 arithmetic would give.
+ * Limits: rows, n, k, batch < 2^31 - 256, strides < 2^40, fewer than 2^31 tiles of
+ * 64 x 64 in y and in x, and fewer than 2^31 steps of 32 rows in the batch.
  * k = 0 gives z = bias. */
 #define SSM2D_ACT_NONE 0
 #define SSM2D_ACT_RELU 1
