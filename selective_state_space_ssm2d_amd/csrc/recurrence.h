@@ -149,12 +149,11 @@ __device__ __forceinline__ void put_down(unsigned long *to, float P, float c)
     if (w == kNotYet) w = 0x7fc000007fc00000ul;
     __hip_atomic_store(to, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ unsigned state_word(float h)
+__device__ __forceinline__ void put_down(unsigned *to, float h)
 {
     const unsigned w = __float_as_uint(h);
-    return w == ~0u ? 0x7fc00000u : w;
+    __hip_atomic_store(to, w == ~0u ? 0x7fc00000u : w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ void put_down(unsigned *to, float h) { __hip_atomic_store(to, state_word(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 // Waits for the first `count` of V words.
 template <int V, typename W>
 __device__ __forceinline__ void take_up(const W *from, long step, int count, W (&w)[V])
@@ -488,7 +487,10 @@ __global__ __launch_bounds__(RELAY ? 512 : 256, 4) void rec_rows_fwd(const RecPa
             }
             before[share][l][0] = q, before[share][l][1] = d;
             unsigned w[1] = {0u};
-            if (share == 0 && here) take_up<1>(enter, 0, 1, w);
+            if (share == 0 && here) {
+                if (group > 0) take_up<1>(enter, 0, 1, w);
+                else if (!PACKED && p.h_init) w[0] = __float_as_uint(p.h_init[b * p.n + ch]);
+            }
             __syncthreads();
             if (share == 0 && here) {
                 float state = __uint_as_float(w[0]);
@@ -893,8 +895,9 @@ __global__ __launch_bounds__(256) void rec_maps_fwd(const RecParams p, long unit
                     take_up<1>(p.parts + row * p.S + seg - k + lane, 0, 1, w);
                     pP = __uint_as_float(static_cast<unsigned>(w[0] >> 32)), pc = __uint_as_float(static_cast<unsigned>(w[0]));
                 }
-                unsigned w[1];
-                take_up<1>(p.enter + row * groups + group, 0, 1, w);
+                unsigned w[1] = {0u};
+                if (group > 0) take_up<1>(p.enter + row * groups + group, 0, 1, w);
+                else if (p.h_init) w[0] = __float_as_uint(p.h_init[row]);
                 wave_join<64>(pP, pc);
                 const float into = fmaf(last_lane<64>(pP), __uint_as_float(w[0]), last_lane<64>(pc));
                 if (lane == 0) {

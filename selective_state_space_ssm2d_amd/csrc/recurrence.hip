@@ -50,18 +50,12 @@ __global__ __launch_bounds__(256) void rec_join(const RecParams p)
     both(p.F, true, !PACKED && p.dh_last && live ? p.dh_last[b * p.n + chan] : 0.0f);
 }
 
-// Before a relay: nothing is there but what enters the first segments (rows:
-// [batch][group][channel], maps: [batch][channel][group]).
-__global__ __launch_bounds__(256) void relay_open(const RecParams p, long parts, long enters, int groups, int maps)
+// Before a relay: no word is there, and no ticket drawn.
+__global__ __launch_bounds__(256) void relay_open(uint4 *words, long quads, unsigned *tickets, long chains, long first)
 {
-    const long i = (p.first + blockIdx.x) * 256 + threadIdx.x;
-    if (i < p.chains) p.tickets[i * kTicketWords] = 0u;
-    if (i < parts) p.parts[i] = kNotYet;
-    if (i >= enters) return;
-    const long b = i / (static_cast<long>(groups) * p.n), at = i % (static_cast<long>(groups) * p.n);
-    const bool first = maps ? at % groups == 0 : at < p.n;
-    const long c = maps ? at / groups : at;
-    p.enter[i] = first ? (p.h_init && p.n_seq == 0 ? state_word(p.h_init[b * p.n + c]) : 0u) : ~0u;
+    const long i = (first + blockIdx.x) * 256 + threadIdx.x;
+    if (i < quads) words[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+    if (i < chains) tickets[i * kTicketWords] = 0u;
 }
 
 __global__ void copy_floats(const float *src, float *dst, long n)
@@ -140,13 +134,16 @@ Cut cut_tokens(const ssm2d_recurrence_shape &a, uint32_t flags, int v)
 constexpr int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 // Whether workgroups read states that another one writes, so that one written in
-// place is read from a copy: packed sequences begin and end anywhere, and the
-// last lane of a row reaches back over channels of other lanes.
+// place is read from a copy: packed sequences begin and end anywhere, the last
+// lane of a row reaches back over channels of other lanes, and all of a relay's
+// first group read what enters it.
 template <typename T>
-bool shares_states(const ssm2d_recurrence_shape &a, uint32_t flags)
+bool shares_states(const ssm2d_recurrence_shape &a, uint32_t flags, bool relay)
 {
-    return a.n_seq > 0 || (!(flags & SSM2D_RECUR_MAPS) && a.channels % kRowV<T> != 0);
+    return a.n_seq > 0 || relay || (!(flags & SSM2D_RECUR_MAPS) && a.channels % kRowV<T> != 0);
 }
+// Bytes of a relay's words: products and sums, then states, in whole 16 bytes; behind them the counters.
+int64_t relay_words(const Cut &c, int64_t lines) { return round_up(lines * (int64_t{8} * c.S + int64_t{4} * c.groups), 16); }
 
 template <typename T, bool BWD>
 int64_t rec_workspace(const ssm2d_recurrence_shape *a, uint32_t flags)
@@ -155,12 +152,14 @@ int64_t rec_workspace(const ssm2d_recurrence_shape *a, uint32_t flags)
     if (st != SSM2D_OK) return -st;
     if (a->batch == 0 || a->tokens == 0 || a->channels == 0) return 0;
     int64_t bytes = 0;
+    bool relay = false;
     for (const int v : {kRowV<T>, 1}) {
         const Cut c = cut_tokens<T, BWD>(*a, flags, v);
         const int64_t lines = a->batch * a->channels;
-        if (c.S > 1) bytes = std::max(bytes, BWD ? 3 * lines * c.S * 4 : lines * (int64_t{8} * c.S + int64_t{4} * c.groups) + c.chains * kTicketWords * 4);
+        if (c.S > 1) bytes = std::max(bytes, BWD ? 3 * lines * c.S * 4 : relay_words(c, lines) + c.chains * kTicketWords * 4);
+        relay = relay || (!BWD && c.S > 1);
     }
-    if (shares_states<T>(*a, flags) && (BWD || !few_tokens(*a, flags))) bytes = round_up(bytes, 16) + std::max(a->n_seq, a->batch) * a->channels * 4;
+    if (shares_states<T>(*a, flags, relay) && (BWD || !few_tokens(*a, flags))) bytes = round_up(bytes, 16) + std::max(a->n_seq, a->batch) * a->channels * 4;
     return bytes;
 }
 
@@ -211,10 +210,10 @@ int rec_entry(const T *x, const T *g, const float *h_init, const int32_t *cu, co
         p.P = static_cast<float *>(ws), p.H = p.P + plane, p.F = p.H + plane;
     } else {
         p.parts = static_cast<unsigned long *>(ws), p.enter = reinterpret_cast<unsigned *>(p.parts + plane);
-        p.tickets = p.enter + B * n * c.groups, p.chains = c.chains;
+        p.tickets = reinterpret_cast<unsigned *>(static_cast<char *>(ws) + relay_words(c, B * n)), p.chains = c.chains;
     }
     if (last && last == state) {
-        if (shares_states<T>(*a, flags) && !plan.few) {
+        if (shares_states<T>(*a, flags, !BWD && p.S > 1) && !plan.few) {
             float *copy = reinterpret_cast<float *>(static_cast<char *>(ws) + (need - states * 4));
             copy_floats<<<blocks(states), dim3(256), 0, s>>>(state, copy, states);
             if ((st = launched()) != SSM2D_OK) return st;
@@ -225,9 +224,9 @@ int rec_entry(const T *x, const T *g, const float *h_init, const int32_t *cu, co
     }
     if (!BWD) {
         if (p.S > 1) {
-            const long enters = B * n * c.groups;
-            const int opened = rec_launch(p, (std::max(plane, enters) + 255) / 256, 256, [&](const RecParams &q, dim3 grid) {
-                relay_open<<<grid, dim3(256), 0, s>>>(q, plane, enters, c.groups, plan.maps);
+            const long quads = relay_words(c, B * n) / 16;
+            const int opened = rec_launch(p, (std::max<long>(quads, c.chains) + 255) / 256, 256, [&](const RecParams &q, dim3 grid) {
+                relay_open<<<grid, dim3(256), 0, s>>>(static_cast<uint4 *>(ws), quads, p.tickets, c.chains, q.first);
             });
             if (opened != SSM2D_OK) return opened;
         }

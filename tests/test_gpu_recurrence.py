@@ -406,3 +406,13 @@ def test_relays_at_once(kind):
         got += [tuple(t.clone() for t in out) for _, out in graphs]
     for h, last in got:
         assert torch.equal(h, want[0]) and torch.equal(last, want[1])
+
+
+@pytest.mark.parametrize("tokens", [100, 9000, 300000])
+def test_states_of_maps_in_place(tokens):
+    s = make(1, tokens, 2, "f32", 11, maps=True)
+    for _ in range(3):
+        h, last = pkg.recurrence_fwd(s["x"], s["g"], h_init=s["h_init"], channels_first=True, return_last_state=True)
+        st = s["h_init"].clone()
+        h2 = pkg.recurrence_fwd(s["x"], s["g"], h_init=st, h_last=st, channels_first=True)
+        assert torch.equal(h, h2) and torch.equal(st, last)
