@@ -5,6 +5,8 @@
 // with the sides chosen (linear.hip).
 #pragma once
 
+#include <cmath>
+
 #include "block_common.h"
 
 namespace ssm2d_impl {
@@ -572,6 +574,111 @@ __global__ __launch_bounds__(256, 2) void gemm_straight(const GemmParams p)
     gemm_by_lds<A_KC, B_KC, BM, BN, false>(p, p.first + blockIdx.x, ring0, ring1);
 }
 
+// ------------------------------------------------------------------ few rows
+
+// NP bf16 parts of 8 neighbours of k, as a fragment holds them.
+template <typename T>
+__device__ __forceinline__ void to_parts(const Raw<T, 8> &r, bfrag (&f)[kParts<T>])
+{
+    union {
+        unsigned w[4];
+        bfrag f;
+    } u;
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u.w[i] = r.w[i];
+        f[0] = u.f;
+    } else {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = r.get(i);
+#pragma unroll
+        for (int n = 0; n < 3; ++n) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const unsigned lo = __float_as_uint(v[2 * i]), hi = __float_as_uint(v[2 * i + 1]);
+                u.w[i] = top_halves(hi, lo);
+                v[2 * i] -= __uint_as_float(lo & 0xffff0000u);
+                v[2 * i + 1] -= __uint_as_float(hi & 0xffff0000u);
+            }
+            f[n] = u.f;
+        }
+    }
+}
+
+// Few rows (serving): 16 rows by 16 columns a workgroup, the sum over k shared by its
+// 8 waves, each with four (float32: two) steps of 32 under way from memory to registers:
+// no LDS and no barrier until the waves' sums are added, and little code, whose way
+// to the compute units counts here. Bound by the latencies of a launch and of a
+// read. 768 to 1536 channels, one row, in a graph: 3.0 us, float32 4.2; by tiles of 64 6.1 and 9.1.
+template <typename T>
+__global__ __launch_bounds__(512) void gemm_few(const GemmParams p)
+{
+    constexpr int NP = kParts<T>, kWaves = 8, kAhead = sizeof(T) == 2 ? 4 : 2, kLd = 20;
+    __shared__ float sums[kWaves][16 * kLd];
+    const unsigned id = p.first + blockIdx.x;
+    const int l = threadIdx.x % 64, wave = threadIdx.x / 64, n0 = static_cast<int>(id % p.tiles_n) * 16, m0 = static_cast<int>(id / p.tiles_n) * 16;
+    const int k0 = l / 16 * 8;
+    // (rows and columns past the last read it, and go nowhere)
+    const T *a = static_cast<const T *>(p.a) + min(m0 + l % 16, p.M - 1) * p.a_ld + k0;
+    const T *b = static_cast<const T *>(p.b) + static_cast<long>(min(n0 + l % 16, p.N - 1)) * p.b_ld + k0;
+    facc acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int steps = (p.K + 31) / 32;
+    for (int s = wave; s < steps; s += kWaves * kAhead) {
+        Raw<T, 8> ra[kAhead], rb[kAhead];
+        if ((s + kWaves * (kAhead - 1) + 1) * 32L <= p.K) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int k = (s + i * kWaves) * 32;
+                ra[i].load_any(a + k);
+                rb[i].load_any(b + k);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const long k = (s + i * kWaves) * 32L;
+                const long left = p.K - k - k0;
+                ra[i].clear();
+                rb[i].clear();
+                if (left >= 8) {
+                    ra[i].load_any(a + k);
+                    rb[i].load_any(b + k);
+                } else if (left > 0) {
+                    float x[8], y[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = j < left ? widen1(a[k + j]) : 0.0f, y[j] = j < left ? widen1(b[k + j]) : 0.0f;
+                    ra[i].set(x);
+                    rb[i].set(y);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            bfrag fa[NP], fb[NP];
+            to_parts<T>(ra[i], fa);
+            to_parts<T>(rb[i], fb);
+            mma<NP>(acc, fb, fa);
+        }
+    }
+    *reinterpret_cast<facc *>(&sums[wave][l % 16 * kLd + l / 16 * 4]) = acc;
+    __syncthreads();
+    // (an element a thread: little code, whose way to the compute units counts here)
+    const int r = threadIdx.x / 16, c = threadIdx.x % 16, n = n0 + c;
+    const long m = m0 + r;
+    if (r >= 16 || m >= p.M || n >= p.N) return;
+    float v = p.bias ? p.bias[n] : 0.0f, sum = 0.0f;
+    const float res = p.res ? widen1(static_cast<const T *>(p.res)[m * p.r_ld + n]) : 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) sum += sums[w][r * kLd + c];
+    v += sum;
+    const long at = m * p.c_ld + n;
+    if (p.pre) store1(static_cast<T *>(p.pre) + at, v);
+    if (p.act == SSM2D_ACT_RELU) v = activate<T, SSM2D_ACT_RELU>(v);
+    else if (p.act == SSM2D_ACT_SILU) v = activate<T, SSM2D_ACT_SILU>(v);
+    else if (p.act == SSM2D_ACT_GELU) v = activate<T, SSM2D_ACT_GELU>(v);
+    store1(static_cast<T *>(p.c) + at, v + res);
+}
+
 // Both gradients of a projection in one launch: dweight's workgroups, then dx's (up
 // to a whole round of the dies), so that the last ones of either share the chip
 // (12544 x 768 by 768, bf16: 56 us, 37 + 32 one after the other; float32, 7755 x 200 by
@@ -667,6 +774,7 @@ struct GemmPlan {
     int steps, per;
     int64_t bytes;  // of the splits' sums
     double us;      // as counted
+    bool few;       // gemm_few
 };
 
 // The choice with the least time by this count, in us, of what was measured (bf16;
@@ -725,6 +833,17 @@ GemmPlan plan_gemm(long batch, long M, long N, long K, long kb)
     }
     cut_plan(g, batch, M, N, side, cuts);
     return g;
+}
+
+// Whether rows are few, by the time gemm_few is counted to take (us): 2.4 and for each
+// round of 256 workgroups 1.6 (float32 3.5) a thousand of k; the count of tiles is
+// without their launch, 2.3 (1.5). (One row of 2048 to 8192 channels,
+// bf16: 7.4 us, 10.8 by tiles; 32 rows: 17 and 12; 64 of 768 to 1536: 5.0 and 6.6.)
+template <typename T>
+bool few_rows(const GemmPlan &g, long M, long N, long K)
+{
+    const double rounds = std::ceil(static_cast<double>((M + 15) / 16) * static_cast<double>((N + 15) / 16) / 256.0);
+    return 2.4 + rounds * static_cast<double>(K) * (sizeof(T) == 2 ? 0.0016 : 0.0035) < g.us + (sizeof(T) == 2 ? 2.3 : 1.5);
 }
 
 // Both of a projection's gradients in one launch with tiles of one size, where
@@ -788,6 +907,10 @@ int run_join(GemmParams &p, hipStream_t s)
 template <typename T>
 int run_gemm_of(GemmParams p, const GemmPlan &g, bool a_kc, bool b_kc, void *ws, hipStream_t s)
 {
+    if (g.few) {
+        p.tiles_n = (p.N + 15) / 16;
+        return gemm_launch(p.first, static_cast<long>(p.tiles_n) * ((p.M + 15) / 16), [&](dim3 grid) { gemm_few<T><<<grid, dim3(512), 0, s>>>(p); });
+    }
     lay_out(p, g, ws);
     auto go = [&](auto size) {
         constexpr int BM = decltype(size)::value;

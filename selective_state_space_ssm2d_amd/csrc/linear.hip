@@ -225,7 +225,10 @@ void sides(GemmParams &g, const Side &a, const Side &b)
 template <typename T>
 GemmPlan plan_fwd(const ssm2d_linear_shape &a, uint32_t flags)
 {
-    return flags & SSM2D_LINEAR_Y_MAPS ? plan_gemm<T>(a.batch, a.n, a.rows, a.k, 1) : plan_gemm<T>(a.batch, a.rows, a.n, a.k, 1);
+    GemmPlan g = flags & SSM2D_LINEAR_Y_MAPS ? plan_gemm<T>(a.batch, a.n, a.rows, a.k, 1) : plan_gemm<T>(a.batch, a.rows, a.n, a.k, 1);
+    g.few = !flags && a.batch == 1 && few_rows<T>(g, a.rows, a.n, a.k);
+    if (g.few) g.bytes = 0;
+    return g;
 }
 
 template <typename T>

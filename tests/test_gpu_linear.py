@@ -264,3 +264,20 @@ def test_gradients_of_few_and_many_rows(rows, k, n, act, dtype):
     """Sums undivided and in parts, one gradient's workgroups few beside the other's."""
     x, w = _randn((rows, k), dtype, rows), _randn((n, k), dtype, 1, k ** -0.5)
     check(x, w, torch.zeros(n, device="cuda"), None, act, dtype=dtype, dy=_randn((rows, n), dtype, 2), what=f"{rows} rows")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("k,n", [(768, 1536), (1, 3), (31, 17), (32, 16), (33, 15), (1000, 100), (1031, 33), (2047, 8)])
+def test_few_rows(k, n, dtype):
+    """Tiles of 16 rows and one row more, with the epilogue's parts, at strides, and into the residual."""
+    for i, rows in enumerate((1, 2, 5, 15, 16, 17, 33, 64)):
+        act = (None, "silu", "gelu", "relu")[i % 4]
+        case(1, rows, k, n, False, False, act, i % 2 == 0, dtype, rows + k, bias=i % 3 != 0)
+    wide, w = _randn((8, k + 5), dtype, 1), _randn((n + 2, k + 3), dtype, 2, k ** -0.5)
+    check(wide[::2, 3:3 + k], w[1:1 + n, 1:1 + k], None, None, "silu", dtype=dtype, what="strides")
+    x, r = wide[:3, :k], _randn((3, n), dtype, 3)
+    want = pkg.linear_fwd(x, w[:n, :k], None, r, act="gelu")
+    y = r.clone()
+    assert pkg.linear_fwd(x, w[:n, :k], None, y, act="gelu", y=y) is y and torch.equal(y, want)
+    # (both are few rows) a row alone, and with others: the same bits
+    assert torch.equal(pkg.linear_fwd(x[1:2], w[:n, :k]), pkg.linear_fwd(x, w[:n, :k])[1:2])
