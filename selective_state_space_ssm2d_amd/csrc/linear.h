@@ -835,15 +835,15 @@ GemmPlan plan_gemm(long batch, long M, long N, long K, long kb)
     return g;
 }
 
-// Whether rows are few, by the time gemm_few is counted to take (us): 2.4 and for each
-// round of 256 workgroups 1.6 (float32 3.5) a thousand of k; the count of tiles is
+// Whether rows are few, by the time gemm_few is counted to take (us): 2.1 and for each
+// round of 256 workgroups 0.3 and 1.6 (float32 3.5) a thousand of k; the count of tiles is
 // without their launch, 2.3 (1.5). (One row of 2048 to 8192 channels,
 // bf16: 7.4 us, 10.8 by tiles; 32 rows: 17 and 12; 64 of 768 to 1536: 5.0 and 6.6.)
 template <typename T>
 bool few_rows(const GemmPlan &g, long M, long N, long K)
 {
     const double rounds = std::ceil(static_cast<double>((M + 15) / 16) * static_cast<double>((N + 15) / 16) / 256.0);
-    return 2.4 + rounds * static_cast<double>(K) * (sizeof(T) == 2 ? 0.0016 : 0.0035) < g.us + (sizeof(T) == 2 ? 2.3 : 1.5);
+    return 2.1 + rounds * (0.3 + static_cast<double>(K) * (sizeof(T) == 2 ? 0.0016 : 0.0035)) < g.us + (sizeof(T) == 2 ? 2.3 : 1.5);
 }
 
 // Both of a projection's gradients in one launch with tiles of one size, where
