@@ -72,7 +72,8 @@ __device__ __forceinline__ void slope_of(const SlopeParams &p, const T *dy, cons
     }
 }
 
-// Token rows: 32 lanes of V channels by 8 rows; a slice of rows a workgroup. The
+// Token rows: 32 lanes of V channels by 8 rows; a slice of rows a workgroup (12544 x 768,
+// bf16, with SiLU: 14.6 us, memory). The
 // last lane of a row reaches back over the one before, and counts what is its own.
 template <typename T, int V>
 __global__ __launch_bounds__(256) void slope_rows(const SlopeParams p)

@@ -545,6 +545,8 @@ __global__ __launch_bounds__(RELAY ? 512 : 256, 4) void rec_rows_fwd(const RecPa
 }
 
 // A workgroup's chunk is a segment. AGG: its product, state from zero and flow from zero, into P, H and F.
+// (64 x 196 tokens of 768, bf16: 28 us, 3.4 TB/s, 64 x 256 4.0; bound by what two workgroups a
+// compute unit, as many as the registers allow, ask for, and by the gates' exponentials.)
 template <typename T, int V, bool PACKED, bool SIG, bool AGG>
 __global__ __launch_bounds__(512, 4) void rec_rows_bwd(const RecParams p)
 {
