@@ -108,7 +108,7 @@ int ssm2d_linear_bwd_bf16(const uint16_t *x, const uint16_t *weight, const uint1
  *   y = out / sqrt(mean of out^2 over the row + eps) next_weight
  * `groups` equal groups of neighbouring channels (heads) are normed each by
  * itself. Without SSM2D_NORM_ON rms and weight are left out (the norm before a
- * block alone: out = residual + x, y its norm). gate NULL: no gate; act is SiLU,
+ * block alone: out = residual + x, y its norm; dweight is zeros). gate NULL: no gate; act is SiLU,
  * or the sigmoid with SSM2D_NORM_GATE_SIGMOID. residual NULL: zeros. weight,
  * scale, next_weight: float32 [n], NULL: ones. y NULL: not computed; y comes from
  * out before it is rounded. With SSM2D_NORM_RESIDUAL_F32 residual, out, dout

@@ -59,7 +59,7 @@ int norm_fwd(const T *x, const T *gate, const void *res, const float *weight, co
         off_by(scale, 4) || off_by(next, 4))
         return SSM2D_ERR_MISALIGNED;
     NormParams p = norm_params(*a, eps, flags);
-    p.x = x, p.gate = gate, p.res = res, p.weight = weight, p.scale = scale, p.next = next, p.out = out, p.y = y;
+    p.x = x, p.gate = gate, p.res = res, p.weight = p.on ? weight : nullptr, p.scale = scale, p.next = next, p.out = out, p.y = y;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     return f32 ? launch_norm<T, float, false>(p, nullptr, nullptr, nullptr, s) : launch_norm<T, T, false>(p, nullptr, nullptr, nullptr, s);
 }
@@ -82,13 +82,16 @@ int norm_bwd(const T *x, const T *gate, const void *res, const float *weight, co
     if (st != SSM2D_OK) return st;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (off_by(dweight, 4) || off_by(dscale, 4) || off_by(dnext, 4)) return SSM2D_ERR_MISALIGNED;
+    auto clear = [&](float *d) {
+        if (!d || a->n == 0) return static_cast<int>(SSM2D_OK);
+        clear_floats<<<dim3(static_cast<unsigned>((a->n + 255) / 256)), dim3(256), 0, s>>>(d, a->n);
+        return launched();
+    };
     if (!work) {  // (sums over no rows)
-        for (float *d : {dweight, dscale, dnext})
-            if (d && a->n > 0) {
-                clear_floats<<<dim3(static_cast<unsigned>((a->n + 255) / 256)), dim3(256), 0, s>>>(d, a->n);
-                const int e = launched();
-                if (e != SSM2D_OK) return e;
-            }
+        for (float *d : {dweight, dscale, dnext}) {
+            const int e = clear(d);
+            if (e != SSM2D_OK) return e;
+        }
         return SSM2D_OK;
     }
     if (!x) return SSM2D_ERR_NULLPTR;
@@ -98,9 +101,14 @@ int norm_bwd(const T *x, const T *gate, const void *res, const float *weight, co
         off_by(res, tr) || off_by(dout, tr) || off_by(dres, tr) || off_by(weight, 4) || off_by(scale, 4) || off_by(next, 4) || off_by(ws, 16))
         return SSM2D_ERR_MISALIGNED;
     NormParams p = norm_params(*a, eps, flags);
-    p.x = x, p.gate = gate, p.res = res, p.weight = weight, p.scale = scale, p.next = next, p.dout = dout, p.dy = dy;
+    p.x = x, p.gate = gate, p.res = res, p.weight = p.on ? weight : nullptr, p.scale = scale, p.next = next, p.dout = dout, p.dy = dy;
     p.dx = dx, p.dgate = dgate, p.dres = dres, p.sums = dweight || dscale || dnext;
     if (p.sums && (!ws || ws_bytes < norm_workspace(a, flags))) return SSM2D_ERR_NOMEM;
+    if (!p.on) {  // (a weight that is left out has no gradient)
+        const int e = clear(dweight);
+        if (e != SSM2D_OK) return e;
+        dweight = nullptr, p.sums = dscale || dnext;
+    }
     p.part = static_cast<float *>(ws);
     return f32 ? launch_norm<T, float, true>(p, dweight, dscale, dnext, s) : launch_norm<T, T, true>(p, dweight, dscale, dnext, s);
 }

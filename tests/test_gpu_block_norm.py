@@ -238,3 +238,31 @@ def test_deterministic():
     args = {k: t[k] for k in ("weight", "gate", "residual", "scale", "next_weight")}
     a, b = (pkg.block_norm_bwd(t["x"], t["dout"], t["dy"], **args) for _ in range(2))
     assert all(torch.equal(a[k], b[k]) for k in a)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("gate", [False, True])
+def test_weight_without_the_norm_is_left_out(gate, dtype):
+    """The C entries, given a weight without SSM2D_NORM_ON: as without the weight, whose gradient is zeros."""
+    from selective_state_space_ssm2d_amd import block
+
+    t = make(9, 200, dtype, 1, gate=gate)
+    stream = torch.cuda.current_stream().cuda_stream
+    ptr = lambda k: t[k].data_ptr() if t[k] is not None else None  # noqa: E731
+    args = (False, 1, False, False)
+    fn, _, s, flags, _, _, _ = block._norm_plan(False, t["x"], None, t["gate"], t["residual"], t["scale"], t["next_weight"], *args, None, None)
+    want = pkg.block_norm_fwd(t["x"], gate=t["gate"], residual=t["residual"], scale=t["scale"], next_weight=t["next_weight"], norm=False)
+    out, y = torch.empty_like(t["residual"]), torch.empty_like(t["x"])
+    assert fn(t["x"].data_ptr(), ptr("gate"), ptr("residual"), ptr("weight"), ptr("scale"), ptr("next_weight"), out.data_ptr(), y.data_ptr(), s, EPS, flags,
+              stream) == 0
+    assert torch.equal(out, want[0]) and torch.equal(y, want[1])
+    fn, _, s, flags, need, _, _ = block._norm_plan(True, t["x"], None, t["gate"], t["residual"], t["scale"], t["next_weight"], *args, t["dout"], t["dy"])
+    want = pkg.block_norm_bwd(t["x"], t["dout"], t["dy"], gate=t["gate"], residual=t["residual"], scale=t["scale"], next_weight=t["next_weight"], norm=False)
+    like = {"dx": t["x"], "dgate": t["gate"], "dresidual": t["residual"], "dweight": t["weight"], "dscale": t["scale"], "dnext_weight": t["next_weight"]}
+    got = {k: torch.full_like(v, 7.0) if v is not None else None for k, v in like.items()}
+    work = torch.empty(need, dtype=torch.uint8, device="cuda")
+    assert fn(t["x"].data_ptr(), ptr("gate"), ptr("residual"), ptr("weight"), ptr("scale"), ptr("next_weight"), ptr("dout"), ptr("dy"),
+              *(v.data_ptr() if v is not None else None for v in got.values()), s, EPS, flags, work.data_ptr(), need, stream) == 0
+    for k, v in want.items():
+        assert torch.equal(got[k], v), k
+    assert not got["dweight"].any()
