@@ -213,7 +213,7 @@ __global__ __launch_bounds__(kThreads<LPR>) void block_norm_fwd_kernel(const Nor
         if (p.on) {
             group_sums<NCH, LPR>(s, p, red[0], pieces);
 #pragma unroll
-            for (int c = 0; c < NCH; ++c) s[c] = 1.0f / sqrtf(s[c] * p.inv_g + p.eps);
+            for (int c = 0; c < NCH; ++c) s[c] = lay.in(c) ? 1.0f / sqrtf(s[c] * p.inv_g + p.eps) : 0.0f;  // (past the row: of an empty group)
         } else {
 #pragma unroll
             for (int c = 0; c < NCH; ++c) s[c] = 1.0f;
@@ -319,7 +319,7 @@ __global__ __launch_bounds__(kThreads<LPR>) void block_norm_bwd_kernel(const Nor
         if (p.on) {
             group_sums<NCH, LPR>(r, p, red[0], pieces);
 #pragma unroll
-            for (int c = 0; c < NCH; ++c) r[c] = 1.0f / sqrtf(r[c] * p.inv_g + p.eps);
+            for (int c = 0; c < NCH; ++c) r[c] = lay.in(c) ? 1.0f / sqrtf(r[c] * p.inv_g + p.eps) : 0.0f;  // (as in the forward)
         } else {
 #pragma unroll
             for (int c = 0; c < NCH; ++c) r[c] = 1.0f;

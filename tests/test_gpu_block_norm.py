@@ -266,3 +266,13 @@ def test_weight_without_the_norm_is_left_out(gate, dtype):
     for k, v in want.items():
         assert torch.equal(got[k], v), k
     assert not got["dweight"].any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,groups", [(768, 12), (768, 6), (96, 3), (40, 5), (200, 25), (1536, 24), (4096, 64), (100, 1), (771, 3)])
+def test_eps_of_zero(n, groups, dtype, monkeypatch):
+    """No eps: lanes that hold nothing of the row (pieces behind it) do not reach what the row sums."""
+    monkeypatch.setitem(globals(), "EPS", 0.0)
+    for nxt in (True, False):
+        check(make(7, n, dtype, n + groups, nxt=nxt), groups=groups, what=f"{n}/{groups}")
+        check(make(5, n, dtype, n + groups, nxt=nxt, rf32=True), groups=groups, first=True, act="sigmoid", what=f"{n}/{groups} first")
