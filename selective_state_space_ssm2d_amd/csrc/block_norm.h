@@ -355,8 +355,10 @@ __global__ __launch_bounds__(kThreads<LPR>) void block_norm_bwd_kernel(const Nor
             float d[VEC];
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                const float m = m_of(c, j), dy = vy[c].get(j), xh = (m * sc[c][j] + vr[c].get(j)) * r2;
-                d[j] = vo[c].get(j) + r2 * (dy * nw[c][j] - xh * mean);
+                // (without dy nothing of out enters: a 0 by it would be NaN where out is not finite)
+                const float m = m_of(c, j), dy = vy[c].get(j), xh = p.dy ? (m * sc[c][j] + vr[c].get(j)) * r2 : 0.0f;
+                d[j] = vo[c].get(j);
+                if (p.dy) d[j] += r2 * (dy * nw[c][j] - xh * mean);
                 const float e = d[j] * sc[c][j], g = GATE == kGateAfter ? e * act(c, j) : e;
                 D[c][j] = e;
                 k[c] += g * w[c][j] * u[c][j] * lay.count(c, j);
@@ -383,7 +385,7 @@ __global__ __launch_bounds__(kThreads<LPR>) void block_norm_bwd_kernel(const Nor
             for (int j = 0; j < VEC; ++j) {
                 float d = D[c][j], da = 0.0f;
                 if (GATE == kGateAfter) da = d * u[c][j] * w[c][j], d *= act(c, j);
-                d = r[c] * (d * w[c][j] - u[c][j] * kk);
+                if (p.on) d = r[c] * (d * w[c][j] - u[c][j] * kk);
                 if (GATE == kGateFirst) da = d * vx[c].get(j), d *= act(c, j);
                 dx[j] = d;
                 if (GATE != kNoGate) {

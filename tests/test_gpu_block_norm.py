@@ -276,3 +276,20 @@ def test_eps_of_zero(n, groups, dtype, monkeypatch):
     for nxt in (True, False):
         check(make(7, n, dtype, n + groups, nxt=nxt), groups=groups, what=f"{n}/{groups}")
         check(make(5, n, dtype, n + groups, nxt=nxt, rf32=True), groups=groups, first=True, act="sigmoid", what=f"{n}/{groups} first")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [96, 771, 2048])
+def test_gradients_of_values_that_are_not_finite(n, dtype):
+    """Without the norm a gradient is dout by the scale, whatever x holds; and
+    without dy nothing is taken from the norm before the next block."""
+    t = make(6, n, dtype, 2, gate=False, weight=False)
+    t["x"][1, 3], t["x"][2, n - 1], t["x"][4, 0] = float("nan"), float("inf"), float("-inf")
+    g = pkg.block_norm_bwd(t["x"], t["dout"], None, residual=t["residual"], scale=t["scale"], next_weight=t["next_weight"], norm=False)
+    want = t["dout"].double() * t["scale"].double()
+    _near(g["dx"], want, U * want.abs() + _half(want, g["dx"].dtype), "dx")
+    assert torch.equal(g["dresidual"], t["dout"]) and not g["dnext_weight"].any()
+    # through y rows that hold such a value are lost, the others are not
+    g = pkg.block_norm_bwd(t["x"], t["dout"], t["dy"], residual=t["residual"], scale=t["scale"], next_weight=t["next_weight"], norm=False)
+    keep = torch.tensor([0, 3, 5], device="cuda")
+    assert all(torch.isfinite(g[k][keep]).all() for k in ("dx", "dresidual"))
