@@ -173,6 +173,11 @@ int ssm2d_block_norm_bwd_bf16(const uint16_t *x, const uint16_t *gate, const voi
  * h_init (NULL: zeros), h_last (NULL: not stored): float32
  * [sequences][channels]; h_last may be h_init. An empty sequence passes its
  * state on. One token with h_last = h_init = the state is the step of serving.
+ * Growing gates (0 < g < 88): a state of 0 stays 0 until x is not. Through any run of
+ * tokens that another state passes, the product of the a's has to be a float (a sum
+ * of g under 88; for the gradients the flow e likewise, from the last token on):
+ * tokens are joined in stretches, and where a stretch's product overflows h may be
+ * Inf or NaN from there on though a[t] h[t - 1], token by token, would not be.
  * Limits: batch, channels and tokens < 2^31 - 65536, channels * batch < 2^31. */
 #define SSM2D_RECUR_SIGMOID 1u
 #define SSM2D_RECUR_MAPS 2u

@@ -51,19 +51,34 @@ __device__ __forceinline__ bool is_cut(float p)
 {
     return PACKED && __float_as_uint(p) == 0x80000000u;
 }
+// Gates that grow (g > 0) may multiply to Inf where the state is 0 and stays 0,
+// token by token: c is then what is left, not the NaN of Inf by 0. Products of
+// gates, none of which is negative, are 0 where one of them is, not that NaN (where a
+// gate is NaN, c has it). GROW: gates may; a sigmoid's do not (64 x 196 tokens of 768,
+// backward: 28.4 us, 29.8 with what growing takes).
+template <bool GROW>
+__device__ __forceinline__ float state_after(float P, float c, float h)
+{
+    return GROW && h == 0.0f ? c : fmaf(P, h, c);
+}
+template <bool GROW>
+__device__ __forceinline__ float no_nan(float P)
+{
+    return GROW ? fmaxf(P, 0.0f) : P;
+}
 // The stretch (P, c) after (p0, c0).
-template <bool PACKED>
+template <bool PACKED, bool GROW>
 __device__ __forceinline__ void join(float p0, float c0, float &P, float &c)
 {
     if (is_cut<PACKED>(P)) return;
-    c = fmaf(P, c0, c);
-    P = is_cut<PACKED>(p0) ? p0 : P * p0;
+    c = state_after<GROW>(P, c, c0);
+    P = is_cut<PACKED>(p0) ? p0 : no_nan<GROW>(P * p0);
 }
 // The state after a stretch (P, c) entered with h.
-template <bool PACKED>
+template <bool PACKED, bool GROW>
 __device__ __forceinline__ float pass(float P, float c, float h)
 {
-    return is_cut<PACKED>(P) ? c : fmaf(P, h, c);
+    return is_cut<PACKED>(P) ? c : state_after<GROW>(P, c, h);
 }
 
 // a and w of a gate; for bf16 the sigmoid's two sides share their exponential.
@@ -216,7 +231,7 @@ struct Line {
 // lots_in: `in` gets the state before each thread's stretch given `carry` before
 // the workgroup's, and carry (with carryP, the product so far) moves to its end. DOWN:
 // in reverse token order. tot: LDS for this use alone until the next barrier but one.
-template <int V, int BX, bool PACKED, bool DOWN>
+template <int V, int BX, bool PACKED, bool GROW, bool DOWN>
 __device__ __forceinline__ void lots_up(float (&P)[V], float (&c)[V], float (&eP)[V], float (&ec)[V], float (*tot)[BX * V][2])
 {
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, cx = lane % BX, sub = lane / BX;
@@ -227,7 +242,7 @@ __device__ __forceinline__ void lots_up(float (&P)[V], float (&c)[V], float (&eP
         for (int j = 0; j < V; ++j) {
             const float p0 = DOWN ? __shfl_down(P[j], d * BX) : __shfl_up(P[j], d * BX);
             const float c0 = DOWN ? __shfl_down(c[j], d * BX) : __shfl_up(c[j], d * BX);
-            if (DOWN ? sub + d < kSubs : sub >= d) join<PACKED>(p0, c0, P[j], c[j]);
+            if (DOWN ? sub + d < kSubs : sub >= d) join<PACKED, GROW>(p0, c0, P[j], c[j]);
         }
     if (sub == (DOWN ? 0 : kSubs - 1)) {
 #pragma unroll
@@ -240,7 +255,7 @@ __device__ __forceinline__ void lots_up(float (&P)[V], float (&c)[V], float (&eP
     }
     __syncthreads();
 }
-template <int V, int BX, int WAVES, bool PACKED, bool DOWN>
+template <int V, int BX, int WAVES, bool PACKED, bool GROW, bool DOWN>
 __device__ __forceinline__ void lots_in(const float (&eP)[V], const float (&ec)[V], float (&carry)[V], float (&carryP)[V], float (&in)[V],
                                         const float (*tot)[BX * V][2])
 {
@@ -257,25 +272,25 @@ __device__ __forceinline__ void lots_in(const float (&eP)[V], const float (&ec)[
         for (int j = 0; j < V; ++j) {
             const float wP = tot[w][cx * V + j][0], wc = tot[w][cx * V + j][1];
             if (w == wave) in[j] = h[j];
-            h[j] = pass<PACKED>(wP, wc, h[j]);
+            h[j] = pass<PACKED, GROW>(wP, wc, h[j]);
             float p = wP, q = 0.0f;
-            join<PACKED>(carryP[j], 0.0f, p, q);
+            join<PACKED, GROW>(carryP[j], 0.0f, p, q);
             carryP[j] = p;
         }
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         carry[j] = h[j];
-        if (sub != (DOWN ? kSubs - 1 : 0)) in[j] = pass<PACKED>(eP[j], ec[j], in[j]);
+        if (sub != (DOWN ? kSubs - 1 : 0)) in[j] = pass<PACKED, GROW>(eP[j], ec[j], in[j]);
     }
 }
-template <int V, int BX, int WAVES, bool PACKED, bool DOWN>
+template <int V, int BX, int WAVES, bool PACKED, bool GROW, bool DOWN>
 __device__ __forceinline__ void join_lots(float (&P)[V], float (&c)[V], float (&carry)[V], float (&carryP)[V], float (&in)[V],
                                           float (*tot)[BX * V][2])
 {
     float eP[V], ec[V];
-    lots_up<V, BX, PACKED, DOWN>(P, c, eP, ec, tot);
-    lots_in<V, BX, WAVES, PACKED, DOWN>(eP, ec, carry, carryP, in, tot);
+    lots_up<V, BX, PACKED, GROW, DOWN>(P, c, eP, ec, tot);
+    lots_in<V, BX, WAVES, PACKED, GROW, DOWN>(eP, ec, carry, carryP, in, tot);
 }
 
 // Which of a thread's L tokens from t on are the first or the last of a packed
@@ -383,6 +398,7 @@ template <typename T, int V, bool PACKED, bool SIG, bool RELAY>
 __global__ __launch_bounds__(RELAY ? 512 : 256, 4) void rec_rows_fwd(const RecParams p)
 {
     using D = RowDims<T, V, RELAY>;
+    constexpr bool GROW = !SIG;
     __shared__ float tot[2][D::kWaves][D::kBX * V][2];
     const int cx = threadIdx.x % D::kBX, ty = threadIdx.x / D::kBX;
     const long id = p.first + blockIdx.x, chain = RELAY ? id % p.chains : id, b = chain / p.tiles;
@@ -437,6 +453,8 @@ __global__ __launch_bounds__(RELAY ? 512 : 256, 4) void rec_rows_fwd(const RecPa
             for (int i = 0; i < D::kL; ++i)
 #pragma unroll
                 for (int j = 0; j < V; ++j) P[j] *= a[i][j], h[j] = fmaf(a[i][j], h[j], wx[i][j]);
+#pragma unroll
+            for (int j = 0; j < V; ++j) P[j] = no_nan<GROW>(P[j]);
         } else {
 #pragma unroll
             for (int i = 0; i < D::kL; ++i) {
@@ -449,13 +467,13 @@ __global__ __launch_bounds__(RELAY ? 512 : 256, 4) void rec_rows_fwd(const RecPa
                         else wx[i][j] = fmaf(a[i][j], state_at(p, p.h_init, mine + i, c + j), wx[i][j]);
                         P[j] = kCut, h[j] = wx[i][j];
                     } else {
-                        if (!is_cut<PACKED>(P[j])) P[j] *= a[i][j];
+                        if (!is_cut<PACKED>(P[j])) P[j] = no_nan<GROW>(P[j] * a[i][j]);
                         h[j] = fmaf(a[i][j], h[j], wx[i][j]);
                     }
                 }
             }
         }
-        lots_up<V, D::kBX, PACKED, false>(P, h, eP, ec, tot[buf]);
+        lots_up<V, D::kBX, PACKED, GROW, false>(P, h, eP, ec, tot[buf]);
         if constexpr (RELAY) {
             // A lane a channel here, so that words are asked for in whole lines and few
             // registers are held beside the tokens' (lanes of V channels, 4 times the
@@ -470,7 +488,7 @@ __global__ __launch_bounds__(RELAY ? 512 : 256, 4) void rec_rows_fwd(const RecPa
             float q = 1.0f, d = 0.0f;
             auto also = [&](const float(&w)[2]) __attribute__((always_inline)) {
                 float P1 = w[0], c1 = w[1];
-                join<PACKED>(q, d, P1, c1);
+                join<PACKED, GROW>(q, d, P1, c1);
                 q = P1, d = c1;
             };
             if (share == 0 && here && seg + 1 < p.S) {
@@ -494,10 +512,10 @@ __global__ __launch_bounds__(RELAY ? 512 : 256, 4) void rec_rows_fwd(const RecPa
             __syncthreads();
             if (share == 0 && here) {
                 float state = __uint_as_float(w[0]);
-                for (int i = 0; i * 4 < k; ++i) state = pass<PACKED>(before[i][l][0], before[i][l][1], state);
+                for (int i = 0; i * 4 < k; ++i) state = pass<PACKED, GROW>(before[i][l][0], before[i][l][1], state);
                 for (int i = 0; i < D::kWaves; ++i) {
                     into[i][l] = state;
-                    state = pass<PACKED>(tot[buf][i][l][0], tot[buf][i][l][1], state);
+                    state = pass<PACKED, GROW>(tot[buf][i][l][0], tot[buf][i][l][1], state);
                 }
                 if (k + 1 == kGroup && seg + 1 < p.S) put_down(enter + p.n, state);
             }
@@ -505,10 +523,10 @@ __global__ __launch_bounds__(RELAY ? 512 : 256, 4) void rec_rows_fwd(const RecPa
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 in[j] = into[threadIdx.x / 64][cx * V + j];
-                if (threadIdx.x % 64 >= D::kBX) in[j] = pass<PACKED>(eP[j], ec[j], in[j]);
+                if (threadIdx.x % 64 >= D::kBX) in[j] = pass<PACKED, GROW>(eP[j], ec[j], in[j]);
             }
         } else {
-            lots_in<V, D::kBX, D::kWaves, PACKED, false>(eP, ec, carry, carryP, in, tot[buf]);
+            lots_in<V, D::kBX, D::kWaves, PACKED, GROW, false>(eP, ec, carry, carryP, in, tot[buf]);
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) h[j] = in[j];
@@ -552,6 +570,7 @@ __global__ __launch_bounds__(512, 4) void rec_rows_bwd(const RecParams p)
 {
     using D = RowDims<T, V, true>;
     constexpr int L = D::kL;
+    constexpr bool GROW = !SIG;
     __shared__ float tot[2][D::kWaves][D::kBX * V][2];
     const int cx = threadIdx.x % D::kBX, ty = threadIdx.x / D::kBX;
     const int tile = static_cast<int>((p.first + blockIdx.x) % p.tiles);
@@ -615,7 +634,7 @@ __global__ __launch_bounds__(512, 4) void rec_rows_bwd(const RecParams p)
                     P[j] = kCut;
                 } else {
                     h[j] = fmaf(a, h[j], wx);
-                    if (!(CUT && is_cut<PACKED>(P[j]))) P[j] *= a;
+                    if (!(CUT && is_cut<PACKED>(P[j]))) P[j] = no_nan<GROW>(P[j] * a);
                 }
             }
         }
@@ -636,12 +655,12 @@ __global__ __launch_bounds__(512, 4) void rec_rows_bwd(const RecParams p)
     float P2[V], out[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) P2[j] = P[j], one[j] = 1.0f;
-    join_lots<V, D::kBX, D::kWaves, PACKED, false>(P, h, enter, one, in, tot[0]);
+    join_lots<V, D::kBX, D::kWaves, PACKED, GROW, false>(P, h, enter, one, in, tot[0]);
     if (AGG && live && ty == 0) {
 #pragma unroll
         for (int j = 0; j < V; ++j) p.P[place + j] = one[j], p.H[place + j] = enter[j];
     }
-    join_lots<V, D::kBX, D::kWaves, PACKED, true>(P2, f, flow, one, out, tot[1]);
+    join_lots<V, D::kBX, D::kWaves, PACKED, GROW, true>(P2, f, flow, one, out, tot[1]);
     if (AGG) {
         if (live && ty == 0) {
 #pragma unroll
@@ -715,15 +734,15 @@ struct MapDims {
 };
 
 // Inclusive join over aligned groups of W lanes.
-template <int W>
+template <int W, bool GROW>
 __device__ __forceinline__ void wave_join(float &P, float &c)
 {
     auto step = [&](auto ctrl, auto rows) __attribute__((always_inline)) {
         constexpr int kCtrl = decltype(ctrl)::value, kRowMask = decltype(rows)::value;
         const float p0 = __int_as_float(__builtin_amdgcn_update_dpp(0x3f800000, __float_as_int(P), kCtrl, kRowMask, 0xf, false));
         const float c0 = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(c), kCtrl, kRowMask, 0xf, false));
-        c = fmaf(P, c0, c);
-        P *= p0;
+        c = state_after<GROW>(P, c, c0);
+        P = no_nan<GROW>(P * p0);
     };
     using std::integral_constant;
     step(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});  // row_shr:1, 2, 4, 8
@@ -751,27 +770,27 @@ __device__ __forceinline__ float last_lane(float v)
 
 // The product and sum of U stretches of each lane of a group (in token order: all
 // lanes' first, then all lanes' second); P, c become the joined ones up to each lane.
-template <int W, int U>
+template <int W, bool GROW, int U>
 __device__ __forceinline__ void wave_total(float (&P)[U], float (&c)[U], float &wP, float &wc)
 {
     wP = 1.0f, wc = 0.0f;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        wave_join<W>(P[u], c[u]);
+        wave_join<W, GROW>(P[u], c[u]);
         const float lP = last_lane<W>(P[u]), lc = last_lane<W>(c[u]);
-        wc = fmaf(lP, wc, lc);
-        wP *= lP;
+        wc = state_after<GROW>(lP, lc, wc);
+        wP = no_nan<GROW>(wP * lP);
     }
 }
 // The states before each of a lane's stretches given h before the group's.
-template <int W, int U>
+template <int W, bool GROW, int U>
 __device__ __forceinline__ void wave_states(const float (&P)[U], const float (&c)[U], float h, float (&in)[U])
 {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const float eP = lane_before<W>(P[u], 1.0f), ec = lane_before<W>(c[u], 0.0f);
-        in[u] = fmaf(eP, h, ec);
-        h = fmaf(last_lane<W>(P[u]), h, last_lane<W>(c[u]));
+        in[u] = state_after<GROW>(eP, ec, h);
+        h = state_after<GROW>(last_lane<W>(P[u]), last_lane<W>(c[u]), h);
     }
 }
 
@@ -814,7 +833,7 @@ __device__ __forceinline__ void store_run(T *row, long i, long n, const float (&
 // Over the workgroup's WPR waves of one row: the state before this wave given
 // `carry` before the first; carry and its product move to the end. Every wave
 // of the workgroup calls it. DOWN: from the last wave to the first.
-template <int WPR, bool DOWN>
+template <int WPR, bool GROW, bool DOWN>
 __device__ __forceinline__ float join_waves(float wP, float wc, float &carry, float &carryP, float (*tot)[2])
 {
     float in = carry;
@@ -827,13 +846,13 @@ __device__ __forceinline__ float join_waves(float wP, float wc, float &carry, fl
         for (int i = 0; i < WPR; ++i) {
             const int w = DOWN ? WPR - 1 - i : i;
             if (w == wave) in = h;
-            h = fmaf(tot[w][0], h, tot[w][1]);
-            carryP *= tot[w][0];
+            h = state_after<GROW>(tot[w][0], tot[w][1], h);
+            carryP = no_nan<GROW>(carryP * tot[w][0]);
         }
         carry = h;
     } else {
-        carry = fmaf(wP, carry, wc);
-        carryP *= wP;
+        carry = state_after<GROW>(wP, wc, carry);
+        carryP = no_nan<GROW>(carryP * wP);
     }
     return in;
 }
@@ -842,6 +861,7 @@ __device__ __forceinline__ float join_waves(float wP, float wc, float &carry, fl
 template <typename T, typename DIMS, bool REV, bool SIG, bool RELAY>
 __global__ __launch_bounds__(256) void rec_maps_fwd(const RecParams p, long units)
 {
+    constexpr bool GROW = !SIG;
     constexpr int V = kMapV<T>, U = DIMS::kU, W = DIMS::kWidth, kWaves = DIMS::kWaves, kChunk = DIMS::template kChunk<T>;
     __shared__ float tot[2][4][2];
     const int place_in = threadIdx.x % DIMS::kLpr, wave = place_in / 64, lane = place_in % 64;  // of the row
@@ -876,9 +896,10 @@ __global__ __launch_bounds__(256) void rec_maps_fwd(const RecParams p, long unit
                 h[u] = fmaf(a[u][j], h[u], wx[u][j]);
                 P[u] *= a[u][j];
             }
+            P[u] = no_nan<GROW>(P[u]);
         }
         float wP, wc;
-        wave_total<W, U>(P, h, wP, wc);
+        wave_total<W, GROW>(P, h, wP, wc);
         float enter;
         if constexpr (RELAY) {
             __shared__ float entering;
@@ -889,7 +910,7 @@ __global__ __launch_bounds__(256) void rec_maps_fwd(const RecParams p, long unit
             if (wave == 0) {
                 float sP = 1.0f, sc = 0.0f;
 #pragma unroll
-                for (int i = 0; i < kWaves; ++i) sc = fmaf(tot[0][i][0], sc, tot[0][i][1]), sP *= tot[0][i][0];
+                for (int i = 0; i < kWaves; ++i) sc = state_after<GROW>(tot[0][i][0], tot[0][i][1], sc), sP = no_nan<GROW>(sP * tot[0][i][0]);
                 if (lane == 0 && seg + 1 < p.S) put_down(p.parts + row * p.S + seg, sP, sc);
                 float pP = 1.0f, pc = 0.0f;
                 if (lane < k) {
@@ -900,22 +921,22 @@ __global__ __launch_bounds__(256) void rec_maps_fwd(const RecParams p, long unit
                 unsigned w[1] = {0u};
                 if (group > 0) take_up<1>(p.enter + row * groups + group, 0, 1, w);
                 else if (p.h_init) w[0] = __float_as_uint(p.h_init[row]);
-                wave_join<64>(pP, pc);
-                const float into = fmaf(last_lane<64>(pP), __uint_as_float(w[0]), last_lane<64>(pc));
+                wave_join<64, GROW>(pP, pc);
+                const float into = state_after<GROW>(last_lane<64>(pP), last_lane<64>(pc), __uint_as_float(w[0]));
                 if (lane == 0) {
                     entering = into;
-                    if (k + 1 == kGroup && seg + 1 < p.S) put_down(p.enter + row * groups + group + 1, fmaf(sP, into, sc));
+                    if (k + 1 == kGroup && seg + 1 < p.S) put_down(p.enter + row * groups + group + 1, state_after<GROW>(sP, sc, into));
                 }
             }
             __syncthreads();
             enter = entering;
 #pragma unroll
             for (int i = 0; i < kWaves; ++i)
-                if (i < wave) enter = fmaf(tot[0][i][0], enter, tot[0][i][1]);
+                if (i < wave) enter = state_after<GROW>(tot[0][i][0], tot[0][i][1], enter);
         } else {
-            enter = join_waves<kWaves, false>(wP, wc, carry, carryP, tot[buf]);
+            enter = join_waves<kWaves, GROW, false>(wP, wc, carry, carryP, tot[buf]);
         }
-        wave_states<W, U>(P, h, enter, in);
+        wave_states<W, GROW>(P, h, enter, in);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float o[V], v = in[u];
@@ -930,6 +951,7 @@ __global__ __launch_bounds__(256) void rec_maps_fwd(const RecParams p, long unit
 template <typename T, typename DIMS, bool REV, bool SIG, bool AGG>
 __global__ __launch_bounds__(256) void rec_maps_bwd(const RecParams p, long units)
 {
+    constexpr bool GROW = !SIG;
     constexpr int V = kMapV<T>, U = DIMS::kU, W = DIMS::kWidth, kWaves = DIMS::kWaves;
     __shared__ float tot[2][4][2];
     const int place_in = threadIdx.x % DIMS::kLpr, wave = place_in / 64, lane = place_in % 64;  // of the row
@@ -967,6 +989,7 @@ __global__ __launch_bounds__(256) void rec_maps_bwd(const RecParams p, long unit
             h[u] = fmaf(a[j], h[u], SIG ? w * rx[u].get(j) : rx[u].get(j));
             P[u] *= a[j];
         }
+        P[u] = no_nan<GROW>(P[u]);
 #pragma unroll
         for (int j = V - 1; j >= 0; --j) f[u] = a[j] * (rd[u].get(j) + f[u]);
     }
@@ -974,16 +997,16 @@ __global__ __launch_bounds__(256) void rec_maps_bwd(const RecParams p, long unit
 #pragma unroll
     for (int u = 0; u < U; ++u) Q[u] = __shfl(P[U - 1 - u], W - 1 - lane, W), G[u] = __shfl(f[U - 1 - u], W - 1 - lane, W);
     float wP, wc;
-    wave_total<W, U>(P, h, wP, wc);
-    const float enter_w = join_waves<kWaves, false>(wP, wc, enter, product, tot[0]);
-    wave_total<W, U>(Q, G, wP, wc);
-    const float flow_w = join_waves<kWaves, true>(wP, wc, flow, unused, tot[1]);
+    wave_total<W, GROW>(P, h, wP, wc);
+    const float enter_w = join_waves<kWaves, GROW, false>(wP, wc, enter, product, tot[0]);
+    wave_total<W, GROW>(Q, G, wP, wc);
+    const float flow_w = join_waves<kWaves, GROW, true>(wP, wc, flow, unused, tot[1]);
     if (AGG) {
         if (lane == 0 && wave == 0) p.P[place] = product, p.H[place] = enter, p.F[place] = flow;
         return;
     }
-    wave_states<W, U>(P, h, enter_w, in);
-    wave_states<W, U>(Q, G, flow_w, f);
+    wave_states<W, GROW>(P, h, enter_w, in);
+    wave_states<W, GROW>(Q, G, flow_w, f);
 #pragma unroll
     for (int u = 0; u < U; ++u) out[u] = __shfl(f[U - 1 - u], W - 1 - lane, W);
 #pragma unroll

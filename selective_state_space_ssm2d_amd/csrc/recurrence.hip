@@ -31,18 +31,18 @@ __global__ __launch_bounds__(256) void rec_join(const RecParams p)
         for (int i = s0; i < s1; ++i) {
             const int s = down ? s1 - 1 - (i - s0) : i;
             float q = p.P[at(s)], d = buf[at(s)];
-            join<PACKED>(P, c, q, d);
+            join<PACKED, true>(P, c, q, d);
             P = q, c = d;
         }
         sP[k][cx] = P, sc[k][cx] = c;
         __syncthreads();
         float h = enter;
-        for (int i = 0; i < (down ? 15 - k : k); ++i) h = pass<PACKED>(sP[down ? 15 - i : i][cx], sc[down ? 15 - i : i][cx], h);
+        for (int i = 0; i < (down ? 15 - k : k); ++i) h = pass<PACKED, true>(sP[down ? 15 - i : i][cx], sc[down ? 15 - i : i][cx], h);
         for (int i = s0; i < s1; ++i) {
             const int s = down ? s1 - 1 - (i - s0) : i;
             const float q = p.P[at(s)], d = buf[at(s)];
             if (live) buf[at(s)] = h;
-            h = pass<PACKED>(q, d, h);
+            h = pass<PACKED, true>(q, d, h);
         }
         __syncthreads();
     };

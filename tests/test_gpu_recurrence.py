@@ -416,3 +416,80 @@ def test_states_of_maps_in_place(tokens):
         st = s["h_init"].clone()
         h2 = pkg.recurrence_fwd(s["x"], s["g"], h_init=st, h_last=st, channels_first=True)
         assert torch.equal(h, h2) and torch.equal(st, last)
+
+
+# ------------------------------------------------------------------ growing gates
+
+# (kind, batch, tokens, channels, sequences): few tokens, chunks of their own and those walked over, in every layout
+GROWING = [("rows", 2, 7, 40, None), ("rows", 1, 300, 64, None), ("rows", 2, 3000, 37, None), ("rows", 1, 5000, 40, None), ("rows", 70, 300, 512, None),
+           ("maps", 3, 100, 4, None), ("maps", 2, 900, 3, None), ("maps", 2, 3000, 3, None), ("maps", 1, 9000, 2, None), ("maps", 24, 5000, 90, None),
+           ("packed", 1, 3900, 40, [3000, 0, 1, 899]), ("packed", 1, 700, 37, [50, 300, 350])]
+
+
+def _growing(kind, batch, tokens, n, lens, dtype, backward):
+    """Gates that grow over tokens where the state (backward: the flow) is 0: the
+    first 0.6 (the last) of each sequence. The gates' product there is beyond fp32."""
+    s = make(batch, tokens, n, dtype, tokens, maps=kind == "maps", lens=lens, state=False)
+    along = lambda t: t.transpose(1, 2) if kind == "maps" else t  # noqa: E731
+    lo = 0
+    for length in lens or [tokens]:
+        part = slice(lo + length - 6 * length // 10, lo + length) if backward else slice(lo, lo + 6 * length // 10)
+        along(s["g"])[:, part] = torch.tensor([0.05, 0.5, 5.0, 20.0], device="cuda").to(DT[dtype])[torch.arange(n, device="cuda") % 4]
+        along(s["dh" if backward else "x"])[:, part] = 0
+        lo += length
+    return s
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rev", [False, True])
+@pytest.mark.parametrize("kind,batch,tokens,n,lens", GROWING, ids=lambda v: str(v) if not isinstance(v, list) else f"{len(v)}seqs")
+def test_growing_gates_leave_zeros(kind, batch, tokens, n, lens, rev, dtype):
+    if rev and lens:
+        return
+    maps = kind == "maps"
+    turn = lambda s: dict(s, **{k: s[k].flip(2 if maps else 1) for k in ("x", "g", "dh")}) if rev else s  # noqa: E731
+    order = lambda t: (t.transpose(1, 2) if maps else t)  # noqa: E731
+    args = dict(channels_first=maps, reverse=rev)
+    small = dict(batch=slice(0, 2), n=slice(0, 8))  # (the reference walks over tokens: of many channels some)
+
+    def some(s):
+        cut = lambda t: t[small["batch"], small["n"]] if maps else t[small["batch"], :, small["n"]]  # noqa: E731
+        return dict(s, **{k: cut(s[k]).contiguous() for k in ("x", "g", "dh")}), cut
+
+    s = turn(_growing(kind, batch, tokens, n, lens, dtype, False))
+    h, last = pkg.recurrence_fwd(s["x"], s["g"], cu_seqlens=s["cu"], return_last_state=True, **args)
+    part, cut = some(s)
+    want = reference(part, False, maps, rev)
+    _near(cut(h), want["h"][0], want["h"][1] + _half(want["h"][0], h.dtype), "h")
+    _near(last[:len(lens) if lens else 2, :8], *want["h_last"], "h_last")
+    assert torch.isfinite(h).all() and torch.isfinite(last).all()
+    # backward: no state at all; then one that is cleared where the growing begins
+    for cleared in (False, True):
+        s = _growing(kind, batch, tokens, n, lens, dtype, True)
+        if cleared:
+            lo = 0
+            for length in lens or [tokens]:
+                first = lo + length - 6 * length // 10
+                if first < lo + length:
+                    order(s["g"])[:, first] = float("-inf")
+                    order(s["x"])[:, first:lo + length] = 0
+                lo += length
+        else:
+            s["x"].zero_()
+        s = turn(s)
+        g = pkg.recurrence_bwd(s["x"], s["g"], s["dh"], cu_seqlens=s["cu"], **args)
+        part, cut = some(s)
+        want = reference(part, False, maps, rev)
+        for k in ("dx", "dg"):
+            _near(cut(g[k]), want[k][0], want[k][1] + _half(want[k][0], g[k].dtype), f"{k} {cleared}")
+            assert torch.isfinite(g[k]).all(), (k, cleared)
+
+
+def test_growing_gates_of_a_state():
+    """A state that is not 0 grows as token by token while the product of the gates that come together is a float."""
+    for maps in (False, True):
+        s = make(1, 3000, 4, "f32", 3, maps=maps)
+        s["g"].fill_(88.0 / 3000)
+        s["x"].zero_(), s["dh"].zero_()
+        s["h_init"].fill_(1e-3), s["dh_last"].fill_(1e-3)
+        check(s, maps=maps, what="growing")
