@@ -374,8 +374,9 @@ int ssm2d_scan_fwd_noalloc(const float *x, const float *delta, const float *A, c
 const char *ssm2d_status_string(int status);
 
 /* Waits for `stream`, then returns and clears the timeout records of that
- * stream's workspace (the device error word and the host-visible flag), and
- * the error word of the device's ssm2d_scan_fwd_noalloc array: SSM2D_OK,
+ * stream's workspace (the device error word and the host-visible flag), the
+ * error word of the device's ssm2d_scan_fwd_noalloc array, and that of the
+ * device's ssm2d_recurrence_fwd calls (ssm2d_block.h): SSM2D_OK,
  * or SSM2D_ERR_DEVICE_TIMEOUT if a kernel gave up waiting for a neighbouring
  * tile's carries (its outputs from that point on are NaN). Returns
  * SSM2D_ERR_HIP if the wait fails. */
@@ -397,8 +398,9 @@ int ssm2d_release_workspaces(void *stream);
  * SSM2D_ERR_UNSUPPORTED if the stream has no workspace yet. */
 int ssm2d_test_set_epoch(void *stream, uint32_t epoch);
 
-/* Test hook: bound on the polls a kernel makes while waiting for carries
- * (0 = default, about one second). A tiny bound forces the timeout path. */
+/* Test hook: bound on the polls a kernel makes while waiting for carries, or
+ * a recurrence's for the state before its chunk (0 = default, about one
+ * second). A tiny bound forces the timeout path. */
 int ssm2d_set_spin_limit(int64_t polls);
 
 /* Text of the last HIP runtime error behind an SSM2D_ERR_HIP status

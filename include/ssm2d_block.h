@@ -178,6 +178,11 @@ int ssm2d_block_norm_bwd_bf16(const uint16_t *x, const uint16_t *gate, const voi
  * of g under 88; for the gradients the flow e likewise, from the last token on):
  * tokens are joined in stretches, and where a stretch's product overflows h may be
  * Inf or NaN from there on though a[t] h[t - 1], token by token, would not be.
+ * Of long rows chunks of tokens go to workgroups of their own, each of which waits
+ * for the state that the one before hands on. All that it waits for runs already; a
+ * wait that none the less takes more polls than ssm2d_set_spin_limit sets (seconds,
+ * if it is not called) is given up: h is NaN from that chunk on, and the device's
+ * next ssm2d_sync_check, of whichever stream, returns SSM2D_ERR_DEVICE_TIMEOUT.
  * Limits: batch, channels and tokens < 2^31 - 65536, channels * batch < 2^31. */
 #define SSM2D_RECUR_SIGMOID 1u
 #define SSM2D_RECUR_MAPS 2u

@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <exception>
+#include <map>
 #include <mutex>
 
 #include "ssm2d.h"
@@ -20,6 +21,11 @@ namespace ssm2d_impl {
 extern std::recursive_mutex g_mutex;
 int hip_fail(hipError_t e);
 int get_aux_ws(int dev, void *stream, int slot, size_t bytes, void **out);
+// ssm2d.hip: the bound on a kernel's polls (0: the default), and of devices that
+// have one a word that a kernel sets when it gives up waiting, which
+// ssm2d_sync_check reads and clears; both under the lock.
+extern long long g_spin_limit;
+extern std::map<int, unsigned int *> g_gave_up;
 
 // Scratch slots (0 .. 37 are the scan's).
 enum : int { kSlotNorm = 64, kSlotDelta = 65 };

@@ -34,6 +34,8 @@ struct RecParams {
     float *P, *H, *F;              // backward, [batch][segment][channel]: a segment's product and sums, then what enters it
     unsigned long *parts;          // forward, from workgroup to workgroup
     unsigned *tickets, *enter;
+    unsigned *gave_up;             // set by a workgroup that waited for all its polls
+    int polls;
     long chains;                   // rows of maps, or tiles of channels, of the batch
     long T;                        // tokens
     long seg;                      // tokens of a segment
@@ -156,7 +158,7 @@ __device__ __forceinline__ Place locate_first(const RecParams &p, long t)
 // Words say for themselves that they are there: all bits set, a NaN that nothing
 // else is put down as, they are not. No order between them is needed.
 constexpr unsigned long kNotYet = ~0ul;
-constexpr int kMostPolls = 1 << 22;  // (seconds, before it goes on with a NaN rather than never)
+constexpr int kMostPolls = 1 << 22;  // (seconds, before it goes on with a NaN rather than never, and says so)
 
 __device__ __forceinline__ void put_down(unsigned long *to, float P, float c)
 {
@@ -169,11 +171,13 @@ __device__ __forceinline__ void put_down(unsigned *to, float h)
     const unsigned w = __float_as_uint(h);
     __hip_atomic_store(to, w == ~0u ? 0x7fc00000u : w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-// Waits for the first `count` of V words.
+// Waits for the first `count` of V words. (Polls first, so that no path leaves w
+// unset: asked for the bound first, packed bf16 rows spill 11 registers, 50 us for the 45 above.)
 template <int V, typename W>
-__device__ __forceinline__ void take_up(const W *from, long step, int count, W (&w)[V])
+__device__ __forceinline__ void take_up(const RecParams &p, const W *from, long step, int count, W (&w)[V])
 {
-    for (int polls = 0; polls < kMostPolls; ++polls) {
+    int polls = 0;
+    do {
         bool there = true;
 #pragma unroll
         for (int j = 0; j < V; ++j) w[j] = __hip_atomic_load(from + min(j, count - 1) * step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -181,7 +185,8 @@ __device__ __forceinline__ void take_up(const W *from, long step, int count, W (
         for (int j = 0; j < V; ++j) there = there && w[j] != static_cast<W>(kNotYet);
         if (there) return;
         __builtin_amdgcn_s_sleep(2);
-    }
+    } while (++polls < p.polls);
+    __hip_atomic_store(p.gave_up, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 // The workgroup's segment of a row of maps or tile of channels.
 constexpr int kTicketWords = 32;  // from counter to counter, a line of their own
@@ -498,7 +503,7 @@ __global__ __launch_bounds__(RELAY ? 512 : 256, 4) void rec_rows_fwd(const RecPa
             }
             if (here && share * 4 < k) {
                 unsigned long w[4];
-                take_up<4>(p.parts + (b * p.S + seg - k + share * 4) * p.n + ch, static_cast<long>(p.n), min(k - share * 4, 4), w);
+                take_up<4>(p, p.parts + (b * p.S + seg - k + share * 4) * p.n + ch, static_cast<long>(p.n), min(k - share * 4, 4), w);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (share * 4 + i < k) also({__uint_as_float(static_cast<unsigned>(w[i] >> 32)), __uint_as_float(static_cast<unsigned>(w[i]))});
@@ -506,7 +511,7 @@ __global__ __launch_bounds__(RELAY ? 512 : 256, 4) void rec_rows_fwd(const RecPa
             before[share][l][0] = q, before[share][l][1] = d;
             unsigned w[1] = {0u};
             if (share == 0 && here) {
-                if (group > 0) take_up<1>(enter, 0, 1, w);
+                if (group > 0) take_up<1>(p, enter, 0, 1, w);
                 else if (!PACKED && p.h_init) w[0] = __float_as_uint(p.h_init[b * p.n + ch]);
             }
             __syncthreads();
@@ -915,11 +920,11 @@ __global__ __launch_bounds__(256) void rec_maps_fwd(const RecParams p, long unit
                 float pP = 1.0f, pc = 0.0f;
                 if (lane < k) {
                     unsigned long w[1];
-                    take_up<1>(p.parts + row * p.S + seg - k + lane, 0, 1, w);
+                    take_up<1>(p, p.parts + row * p.S + seg - k + lane, 0, 1, w);
                     pP = __uint_as_float(static_cast<unsigned>(w[0] >> 32)), pc = __uint_as_float(static_cast<unsigned>(w[0]));
                 }
                 unsigned w[1] = {0u};
-                if (group > 0) take_up<1>(p.enter + row * groups + group, 0, 1, w);
+                if (group > 0) take_up<1>(p, p.enter + row * groups + group, 0, 1, w);
                 else if (p.h_init) w[0] = __float_as_uint(p.h_init[row]);
                 wave_join<64, GROW>(pP, pc);
                 const float into = state_after<GROW>(last_lane<64>(pP), last_lane<64>(pc), __uint_as_float(w[0]));

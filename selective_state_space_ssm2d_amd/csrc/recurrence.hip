@@ -58,6 +58,30 @@ __global__ __launch_bounds__(256) void relay_open(uint4 *words, long quads, unsi
     if (i < chains) tickets[i * kTicketWords] = 0u;
 }
 
+// Set where a relay's wait was given up, read and cleared by ssm2d_sync_check.
+__device__ unsigned relay_gave_up;
+
+// How long the relay's workgroups of a call on the current device wait, and where they say that they did not.
+int bound_waits(RecParams &p)
+{
+    return guarded([&] {
+        int dev = 0;
+        hipError_t e = hipGetDevice(&dev);
+        if (e != hipSuccess) return hip_fail(e);
+        std::lock_guard<std::recursive_mutex> lock(g_mutex);
+        auto it = g_gave_up.find(dev);
+        if (it == g_gave_up.end()) {
+            void *at = nullptr;
+            e = hipGetSymbolAddress(&at, HIP_SYMBOL(relay_gave_up));
+            if (e != hipSuccess) return hip_fail(e);
+            it = g_gave_up.emplace(dev, static_cast<unsigned *>(at)).first;
+        }
+        p.gave_up = it->second;
+        p.polls = g_spin_limit > 0 ? static_cast<int>(std::min<long long>(g_spin_limit, kMostPolls)) : kMostPolls;
+        return static_cast<int>(SSM2D_OK);
+    });
+}
+
 __global__ void copy_floats(const float *src, float *dst, long n)
 {
     const long i = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x;
@@ -224,6 +248,7 @@ int rec_entry(const T *x, const T *g, const float *h_init, const int32_t *cu, co
     }
     if (!BWD) {
         if (p.S > 1) {
+            if ((st = bound_waits(p)) != SSM2D_OK) return st;
             const long quads = relay_words(c, B * n) / 16;
             const int opened = rec_launch(p, (std::max<long>(quads, c.chains) + 255) / 256, 256, [&](const RecParams &q, dim3 grid) {
                 relay_open<<<grid, dim3(256), 0, s>>>(static_cast<uint4 *>(ws), quads, p.tickets, c.chains, q.first);

@@ -113,6 +113,7 @@ int hip_fail(hipError_t e)
     } while (0)
 std::map<std::pair<int, void *>, WsEntry> g_ws;
 long long g_spin_limit = 0;
+std::map<int, unsigned int *> g_gave_up;
 
 // Zeroes n16 16-byte words (a kernel rather than a memset node, so that a
 // caller capturing a graph records nothing the replays could misapply).
@@ -1455,9 +1456,10 @@ int ssm2d_sync_check(void *stream)
     bool timeout = take_timeout_flag(dev, stream);
     // device error words, cleared here: the stream's workspace (a timeout
     // counts from there only when the workspace has no host-visible flag,
-    // which reports it once by itself), and the static scratch
-    unsigned int *words[2] = {nullptr, nullptr};
-    bool counts[2] = {false, true};
+    // which reports it once by itself), the static scratch, and the word of
+    // kernels whose workspaces are the caller's
+    unsigned int *words[3] = {nullptr, nullptr, nullptr};
+    bool counts[3] = {false, true, true};
     auto it = g_ws.find({dev, stream});
     if (it != g_ws.end() && it->second.head) {
         words[0] = it->second.head + 2;
@@ -1465,7 +1467,9 @@ int ssm2d_sync_check(void *stream)
     }
     auto sc = g_scratch.find(dev);
     if (sc != g_scratch.end()) words[1] = sc->second.head + 2;
-    for (int k = 0; k < 2; ++k) {
+    auto up = g_gave_up.find(dev);
+    if (up != g_gave_up.end()) words[2] = up->second;
+    for (int k = 0; k < 3; ++k) {
         if (!words[k]) continue;
         unsigned int v = 0;
         SSM2D_HIP_TRY(hipMemcpy(&v, words[k], sizeof(v), hipMemcpyDeviceToHost));

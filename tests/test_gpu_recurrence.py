@@ -493,3 +493,33 @@ def test_growing_gates_of_a_state():
         s["x"].zero_(), s["dh"].zero_()
         s["h_init"].fill_(1e-3), s["dh_last"].fill_(1e-3)
         check(s, maps=maps, what="growing")
+
+
+# ------------------------------------------------------------------ waits
+
+@pytest.mark.parametrize("kind", ["rows", "maps", "packed"])
+def test_wait_bound_is_reported(kind):
+    """A chunk that gives up waiting leaves NaN behind it, and ssm2d_sync_check says so, once."""
+    maps, lens = kind == "maps", [7000, 3, 997] if kind == "packed" else None
+    s = make(1, 400000 if maps else 8000, 2 if maps else 40, "f32", 3, maps=maps, lens=lens)
+    args = dict(h_init=s["h_init"], cu_seqlens=s["cu"], channels_first=maps)
+    pkg.sync_check()
+    want = pkg.recurrence_fwd(s["x"], s["g"], **args)
+    pkg.sync_check()
+    pkg.set_spin_limit(1)
+    try:
+        h = pkg.recurrence_fwd(s["x"], s["g"], **args)
+        torch.cuda.synchronize()
+    finally:
+        pkg.set_spin_limit(0)
+    gave_up = bool(torch.isnan(h).any())
+    print(f"  forced wait bound: NaN outputs={gave_up}")
+    if gave_up:
+        with pytest.raises(pkg.Ssm2dError) as e:
+            pkg.sync_check()
+        assert e.value.status == pkg.ERR_DEVICE_TIMEOUT
+    else:
+        assert torch.equal(h, want)
+    pkg.sync_check()
+    assert torch.equal(pkg.recurrence_fwd(s["x"], s["g"], **args), want)
+    pkg.sync_check()
