@@ -55,7 +55,8 @@ extern "C" {
  * gives Inf or NaN in the outputs that it enters (dbias too), not always the one
  * fp32 arithmetic would give.
  * Limits: rows, n, k, batch < 2^31 - 256, strides < 2^40, fewer than 2^31 tiles of
- * 64 x 64 in y and in x, and fewer than 2^31 steps of 32 rows in the batch.
+ * 64 x 64 in y, in x and in the weight, and fewer than 2^31 steps of 32 rows in the
+ * batch.
  * k = 0 gives z = bias. */
 #define SSM2D_ACT_NONE 0
 #define SSM2D_ACT_RELU 1
@@ -183,7 +184,8 @@ int ssm2d_block_norm_bwd_bf16(const uint16_t *x, const uint16_t *gate, const voi
  * wait that none the less takes more polls than ssm2d_set_spin_limit sets (seconds,
  * if it is not called) is given up: h is NaN from that chunk on, and the device's
  * next ssm2d_sync_check, of whichever stream, returns SSM2D_ERR_DEVICE_TIMEOUT.
- * Limits: batch, channels and tokens < 2^31 - 65536, channels * batch < 2^31. */
+ * Limits: batch, channels, tokens and n_seq < 2^31 - 65536, channels * batch < 2^31,
+ * channels * n_seq <= 2^32 - 256, batch * tokens * channels <= 10^14. */
 #define SSM2D_RECUR_SIGMOID 1u
 #define SSM2D_RECUR_MAPS 2u
 #define SSM2D_RECUR_REVERSE 4u

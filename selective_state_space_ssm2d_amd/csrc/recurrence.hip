@@ -100,7 +100,8 @@ int check_rec(const ssm2d_recurrence_shape *a, uint32_t flags)
         if (st[0] < 0 || st[1] < 0) return SSM2D_ERR_BAD_DIM;
     const int64_t most = (int64_t{1} << 31) - 65536;
     if (a->batch >= most || a->tokens >= most || a->channels >= most || a->n_seq >= most) return SSM2D_ERR_UNSUPPORTED;
-    if (a->batch * a->channels >= (int64_t{1} << 31) || a->n_seq * a->channels >= (int64_t{1} << 38)) return SSM2D_ERR_UNSUPPORTED;
+    // (states: one launch copies or clears them)
+    if (a->batch * a->channels >= (int64_t{1} << 31) || a->n_seq * a->channels > 256 * most_groups(256)) return SSM2D_ERR_UNSUPPORTED;
     if (static_cast<double>(a->batch) * static_cast<double>(a->tokens) * static_cast<double>(a->channels) > 1e14) return SSM2D_ERR_UNSUPPORTED;
     return SSM2D_OK;
 }
@@ -200,7 +201,6 @@ int rec_entry(const T *x, const T *g, const float *h_init, const int32_t *cu, co
     if (states == 0 || (T_ == 0 && !last)) return SSM2D_OK;
     if (off_by(h_init, 4) || off_by(dh_last, 4) || off_by(last, 4)) return SSM2D_ERR_MISALIGNED;
     auto blocks = [](long m) { return dim3(static_cast<unsigned>((m + 255) / 256)); };
-    if ((states + 255) / 256 > most_groups(256)) return SSM2D_ERR_UNSUPPORTED;
     if (T_ == 0) {
         if (last == state) return SSM2D_OK;
         if (state) copy_floats<<<blocks(states), dim3(256), 0, s>>>(state, last, states);

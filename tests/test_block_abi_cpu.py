@@ -199,6 +199,20 @@ def test_recurrence(kind, dtype):
     assert call(**long, ws=None) == pkg.ERR_NOMEM and call(**long, ws_bytes=8) == pkg.ERR_NOMEM
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("kind", ["fwd", "bwd"])
+def test_recurrence_limits_are_the_workspaces_too(kind, dtype):
+    """A shape has a workspace if the entry takes it, else the entry's status (here with no pointers: a shape that is taken lacks them)."""
+    n = 6 if kind == "fwd" else 9
+    for n_seq, channels in ((65535, 65537), (65536, 65535), (65536, 65536), (1 << 20, 1 << 12), (1 << 26, 1 << 11), (1 << 30, 1 << 10), (3, 5)):
+        d = dict(batch=1, tokens=20, channels=channels, n_seq=n_seq)
+        s = block._RecurrenceShape(x_stride=(0, channels), g_stride=(0, channels), dh_stride=(0, channels), **d)
+        status = _rec(kind, dtype, ptrs=[None] * n, shape=[s])
+        need = block._entry(f"ssm2d_recurrence_{kind}_workspace", dtype)(s, 0)
+        assert status == (pkg.ERR_UNSUPPORTED if n_seq * channels > 2 ** 32 - 256 else pkg.ERR_NULLPTR), (n_seq, channels)
+        assert need >= 0 if status == pkg.ERR_NULLPTR else need == -status, (n_seq, channels)
+
+
 # ------------------------------------------------------------------ the binding
 
 def test_binding_refuses_tensors_off_the_gpu():
