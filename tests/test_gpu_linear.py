@@ -137,7 +137,7 @@ def test_long(rows, k, n, dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows", range(1, 20))
-def test_few_rows(rows, dtype):
+def test_each_small_row_count(rows, dtype):
     for k, n in ((768, 200), (520, 33), (100, 64), (1025, 16)):
         x, w = _randn((rows, k), dtype, rows), _randn((n, k), dtype, k, k ** -0.5)
         b = torch.randn(n, generator=_gen(2), device="cuda")
