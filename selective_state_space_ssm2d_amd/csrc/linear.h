@@ -249,6 +249,14 @@ __device__ __forceinline__ TilePlace tile_place(const GemmParams &p, unsigned id
     return t;
 }
 
+// What a wave's lanes write to LDS and read of each other's stays in program order:
+// the hardware keeps a wave's LDS accesses in theirs, and this the compiler. No instruction.
+__device__ __forceinline__ void wave_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // A wave's accumulators to memory, by way of LDS: there its lanes hold 16 rows by
 // four columns each, and whole runs of rows go out (four times fewer requests).
 // Every wave of the workgroup calls it, when none reads the operands' tiles any more.
@@ -280,7 +288,7 @@ __device__ __forceinline__ void finish_tile(const GemmParams &p, const TilePlace
 #pragma unroll
                 for (int j = 0; j < WN / 16; ++j)
                     *reinterpret_cast<facc *>(mine + (i * 16 + l % 16) * kLd + j * 16 + 4 * (l / 16)) = acc[half * 2 + i][j];
-            // (its own lanes' writes, in order before its reads: no barrier)
+            wave_order();  // (its own lanes' writes before its reads: no barrier)
             auto pass = [&](int k, const Raw<T, V> &w) __attribute__((always_inline)) {
                 const int m = r0 + k * kRowsOnce;
                 float v[V];
@@ -307,6 +315,7 @@ __device__ __forceinline__ void finish_tile(const GemmParams &p, const TilePlace
 #pragma unroll 2
                 for (int k = 0; k < kPasses; ++k) pass(k, res[0]);
             }
+            wave_order();  // (and those before the next rows' writes)
         }
     };
     if (p.res && p.splits == 1) all(std::true_type{});

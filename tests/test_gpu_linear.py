@@ -281,3 +281,26 @@ def test_few_rows(k, n, dtype):
     assert pkg.linear_fwd(x, w[:n, :k], None, y, act="gelu", y=y) is y and torch.equal(y, want)
     # (both are few rows) a row alone, and with others: the same bits
     assert torch.equal(pkg.linear_fwd(x[1:2], w[:n, :k]), pkg.linear_fwd(x, w[:n, :k])[1:2])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cf,ocf", [(False, False), (False, True), (True, False), (True, True)])
+@pytest.mark.parametrize("rows,k,n", [(256, 64, 128), (300, 200, 136), (1030, 1000, 264), (4100, 520, 520), (70, 4096, 72)])
+def test_whole_numbers(rows, k, n, cf, ocf, dtype):
+    """Sums of small whole numbers are exact in any order: every element of every
+    tile, several times over, forward and both gradients."""
+    whole = lambda shape, seed: torch.randint(-3, 4, shape, generator=_gen(seed), device="cuda").to(DT[dtype])  # noqa: E731
+    mixed = cf or ocf
+    xs = (1, k, rows) if cf else ((1, rows, k) if mixed else (rows, k))
+    ys = (1, n, rows) if ocf else ((1, rows, n) if mixed else (rows, n))
+    x, w, r, dy = whole(xs, 1), whole((n, k), 2), whole(ys, 3), whole(ys, 4)
+    xr, up, res = (_rows(t, m).reshape(rows, -1).double() for t, m in ((x, cf), (dy, ocf), (r, ocf)))
+    # (all below 9 * 4100 + 3 < 2^24; a bf16 output is the sum rounded)
+    want = {"y": xr @ w.double().t() + res, "dx": up @ w.double(), "dweight": up.t() @ xr, "dbias": up.sum(0)}
+    for _ in range(3):
+        got = {"y": pkg.linear_fwd(x, w, None, r, channels_first=cf, out_channels_first=ocf),
+               **pkg.linear_bwd(x, w, dy, channels_first=cf, out_channels_first=ocf)}
+        for name, v in want.items():
+            g = got[name]
+            g = _rows(g, ocf if name == "y" else cf).reshape(rows, -1) if name in ("y", "dx") else g
+            assert torch.equal(g, v.to(g.dtype)), name
