@@ -504,12 +504,17 @@ struct StraightLoads {
 };
 
 // bf16 operands whose rows are whole 16-byte chunks: two stages of tiles in LDS,
-// one filled by loads that pass the registers by while the other is used (arrays
-// of their own, so that a read waits for its own stage's loads alone). Tiles of 128 x
-// 128 keep the matrix instructions busy from two workgroups a compute unit: 4096-cubes 132 us,
-// 1040 TFLOP/s; a ring of four stages of 32 and four workgroups of stages of 32 were
+// one filled by loads that pass the registers by while the other is used. Each wave
+// waits for its own loads of a stage before the barrier that opens it. Where both
+// operands have k contiguous the other stage's loads are under way meanwhile. The
+// transposing reads of the other layouts take a plain number as their address, from
+// which the compiler cannot tell the stages apart, and has all loads wait before the
+// first of them: there the two workgroups of a compute unit overlap, not the
+// stages of one. Tiles of 128 x
+// 128 keep the matrix instructions busy from two workgroups a compute unit: 4096-cubes 137 us,
+// 1000 TFLOP/s, 8192-cubes 1190 us, 924; a ring of four stages of 32 and four workgroups of stages of 32 were
 // slower. Short sums are bound by their rounds of tiles: 12544 x 768 to 1536 with GELU and
-// a residual 54 us, 2.3 rounds, 10 of it at the tiles' ends.
+// a residual 51 to 54 us, 2.3 rounds, 10 of it at the tiles' ends.
 template <bool A_KC, bool B_KC, int BM, int BN, bool SUMS>
 __device__ __forceinline__ void gemm_by_lds(const GemmParams &p, unsigned id, uint16_t *ring0, uint16_t *ring1)
 {
@@ -566,12 +571,16 @@ __device__ __forceinline__ void gemm_by_lds(const GemmParams &p, unsigned id, ui
             }
         }
     };
+    // the wave's own loads to LDS have arrived (vmcnt 0, the other counters as they are)
+    auto arrived = [] __attribute__((always_inline)) { __builtin_amdgcn_s_waitcnt(0x0f70); };
     if (ahead > 0) issue(ring0);
     for (int left = s2 - s1; left > 0; left -= 2) {
+        arrived();
         __syncthreads();  // (stage 0 is there, and stage 1 has been read)
         if (ahead > 0) issue(ring1);
         step(ring0);
         if (left == 1) break;
+        arrived();
         __syncthreads();
         if (ahead > 0) issue(ring0);
         step(ring1);
