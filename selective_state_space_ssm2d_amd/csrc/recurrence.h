@@ -110,14 +110,14 @@ struct Place {
     long end, next;
 };
 __device__ __forceinline__ long in_tokens(const RecParams &p, long v) { return v < 0 ? 0 : (v > p.T ? p.T : v); }
-__device__ __forceinline__ long cu_at(const RecParams &p, int i) { return in_tokens(p, p.cu[i]); }
+__device__ __forceinline__ long cu_at(const RecParams &p, long i) { return in_tokens(p, p.cu[i]); }
 // (by halves at each change: any contents end, and stay within the tokens)
 template <typename F>
 __device__ __forceinline__ Place locate_by(const RecParams &p, long t, F &&at)
 {
     int lo = -1, hi = p.n_seq;  // at(lo) <= t < at(hi), as far as they ascend
     while (hi - lo > 1) {
-        const int m = (lo + hi) / 2;
+        const int m = static_cast<int>((static_cast<unsigned>(lo) + static_cast<unsigned>(hi)) / 2);  // (as ints the sum may be beyond them)
         if (at(m) <= t) lo = m;
         else hi = m;
     }
@@ -390,9 +390,9 @@ __global__ __launch_bounds__(256) void rec_few(const RecParams p, long threads)
 template <int V>
 __device__ __forceinline__ void pass_on(const RecParams &p, const float *src, float *dst, int c, int first, int step)
 {
-    for (int s = first; s < p.n_seq; s += step) {
+    for (long s = first; s < p.n_seq; s += step) {
         if (cu_at(p, s + 1) > cu_at(p, s)) continue;
-        const long at = static_cast<long>(s) * p.n + c;
+        const long at = s * p.n + c;
 #pragma unroll
         for (int j = 0; j < V; ++j) dst[at + j] = src ? src[at + j] : 0.0f;
     }

@@ -523,3 +523,20 @@ def test_wait_bound_is_reported(kind):
     pkg.sync_check()
     assert torch.equal(pkg.recurrence_fwd(s["x"], s["g"], **args), want)
     pkg.sync_check()
+
+
+# ------------------------------------------------------------------ very many sequences
+
+def test_more_sequences_than_half_an_int():
+    """Over 2^30 offsets, all but the last two sequences empty: the same bits as those two alone."""
+    count = 3 << 29
+    free = torch.cuda.mem_get_info()[0]
+    if free < 24 << 30:
+        pytest.skip("needs 24 GiB of GPU memory")
+    s = make(1, 100, 1, "f32", 3, lens=[60, 40], state=False)
+    want = {"h": pkg.recurrence_fwd(s["x"], s["g"], cu_seqlens=s["cu"]), **pkg.recurrence_bwd(s["x"], s["g"], s["dh"], cu_seqlens=s["cu"])}
+    cu = torch.zeros(count + 1, dtype=torch.int32, device="cuda")
+    cu[-2:] = s["cu"][-2:]
+    got = {"h": pkg.recurrence_fwd(s["x"], s["g"], cu_seqlens=cu), **pkg.recurrence_bwd(s["x"], s["g"], s["dh"], cu_seqlens=cu)}
+    for name, t in want.items():
+        assert torch.equal(got[name], t), name
