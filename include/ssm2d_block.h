@@ -50,8 +50,10 @@ extern "C" {
  * act: SSM2D_ACT_NONE, _RELU, _SILU (z / (1 + exp(-z))) or _GELU
  * (z (1 + erf(z / sqrt 2)) / 2).
  * bf16 products are exact and summed in fp32. float32 operands go through the
- * bf16 matrix instructions in three exact parts and six products, which keeps
- * an error of about 2^-24 of the largest term; an operand that is Inf or NaN
+ * bf16 matrix instructions in three exact parts and six products: the three left
+ * out are under 2^-21 of a term, and of its sign. GELU errs by up to 0.75e-7 |z| in
+ * bf16 before its rounding (more than that rounding below z = -5.5, where GELU is under
+ * 1.1e-7) and by 2^-24 |z| in float32. An operand that is Inf or NaN
  * gives Inf or NaN in the outputs that it enters (dbias too), not always the one
  * fp32 arithmetic would give.
  * Limits: rows, n, k, batch < 2^31 - 256, strides < 2^40, fewer than 2^31 tiles of

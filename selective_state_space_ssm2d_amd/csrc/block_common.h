@@ -7,9 +7,10 @@
 
 namespace ssm2d_impl {
 
-// exp and 1 / x for values that leave as T: v_exp_f32 and v_rcp_f32 err by a
-// few 2^-24 of the value (the product with log2(e) by |x| 2^-24), far under a
-// rounding to bf16; for float32 the exact forms.
+// exp and 1 / x for what is computed of T: v_exp_f32 and v_rcp_f32 err by a
+// few 2^-24 of the value (the product with log2(e) by |x| 2^-24), far under the
+// rounding to bf16 that T had and its outputs get (the recurrence's gates, whose
+// state stays float32, come from such a T); for float32 the exact forms.
 template <typename T>
 __device__ __forceinline__ float exp_for(float x)
 {
@@ -28,7 +29,9 @@ __device__ __forceinline__ float sigmoid_for(float z) { return inverse_for<T>(1.
 
 // 1 + erf(z / sqrt 2), and exp(-z^2 / 2) in `e`. For bf16 by Abramowitz and
 // Stegun's 7.1.26 (their bound on the error of erf: 1.5e-7), which shares the
-// exponential with the density; for float32 by erff.
+// exponential with the density; for float32 by erff. Neither keeps the places of
+// the negative tail, where the sum is next to 0: for bf16 GELU is off by 0.16 % of itself at z = -5
+// (-1.4e-6), by 0.36 % at -6 (-5.9e-9, where a rounding takes 0.2 to 0.4 %), by 1 % at -8.
 template <typename T>
 __device__ __forceinline__ float one_plus_erf(float z, float &e)
 {

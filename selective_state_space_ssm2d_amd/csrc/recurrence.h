@@ -153,8 +153,8 @@ __device__ __forceinline__ Place locate_first(const RecParams &p, long t)
 // that a workgroup waits for belongs to workgroups that run already; they put their
 // products down before they wait, and the first of those that wait has all it
 // needs. (A counter for each row of maps or tile of channels: all workgroups at one
-// counter took 13 ns each, 175 us for the 73 below.) (196608 cells of 128 channels, float32: 73 us; 95 with a launch for the products,
-// one that joins them and one for the states. 16698 packed tokens of 1024, bf16: 45, 69 so.)
+// counter took 13 ns each, 175 us for the 71 below.) (196608 cells of 128 channels, float32: 71 us; 95 with a launch for the products,
+// one that joins them and one for the states. 16698 packed tokens of 1024, bf16: 43, 69 so.)
 // Words say for themselves that they are there: all bits set, a NaN that nothing
 // else is put down as, they are not. No order between them is needed.
 constexpr unsigned long kNotYet = ~0ul;
@@ -172,7 +172,7 @@ __device__ __forceinline__ void put_down(unsigned *to, float h)
     __hip_atomic_store(to, w == ~0u ? 0x7fc00000u : w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 // Waits for the first `count` of V words. (Polls first, so that no path leaves w
-// unset: asked for the bound first, packed bf16 rows spill 11 registers, 50 us for the 45 above.)
+// unset: asked for the bound first, packed bf16 rows spill 11 registers, 50 us for the 43 above.)
 template <int V, typename W>
 __device__ __forceinline__ void take_up(const RecParams &p, const W *from, long step, int count, W (&w)[V])
 {
@@ -482,7 +482,7 @@ __global__ __launch_bounds__(RELAY ? 512 : 256, 4) void rec_rows_fwd(const RecPa
         if constexpr (RELAY) {
             // A lane a channel here, so that words are asked for in whole lines and few
             // registers are held beside the tokens' (lanes of V channels, 4 times the
-            // requests past the caches, and spills: 71 us for those 45).
+            // requests past the caches, and spills: 71 us for those 43).
             constexpr int C = D::kBX * V, kShares = D::kThreads / C, kGroup = 4 * kShares;  // segments of a group
             __shared__ float before[kShares][C][2], into[D::kWaves][C];
             const int l = threadIdx.x % C, share = threadIdx.x / C, first = (tile * D::kBX + l / V) * V;
