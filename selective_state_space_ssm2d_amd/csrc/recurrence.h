@@ -326,10 +326,13 @@ struct Marks {
     __device__ __forceinline__ bool none(int i) const { return (outs >> i) & 1u; }
     __device__ __forceinline__ bool any() const { return (firsts | ends | outs) != 0; }
 };
-// A state of the sequence that token t belongs to (NULL: zeros).
+// A state of the sequence that token t belongs to (NULL: zeros). (Where offsets are out
+// of order a token may be marked by the look-up of one before it, and itself be in none.)
 __device__ __forceinline__ float state_at(const RecParams &p, const float *state, long t, long c)
 {
-    return state ? state[static_cast<long>(locate(p, t).seq) * p.n + c] : 0.0f;
+    if (!state) return 0.0f;
+    const long s = locate(p, t).seq;
+    return s >= 0 ? state[s * p.n + c] : 0.0f;
 }
 
 // A few tokens (serving: one): a thread walks over them all for V channels (the
@@ -541,6 +544,7 @@ __global__ __launch_bounds__(RELAY ? 512 : 256, 4) void rec_rows_fwd(const RecPa
             v.store_any(h_out + lo.base + (lo.first + i * lo.step));
         };
         auto keep = [&](long s) __attribute__((always_inline)) {
+            if (PACKED && s < 0) return;  // (as in state_at)
 #pragma unroll
             for (int j = 0; j < V; ++j) p.h_last[s * p.n + c + j] = h[j];
         };
@@ -716,7 +720,7 @@ __global__ __launch_bounds__(512, 4) void rec_rows_bwd(const RecParams p)
             v.set(dg);
             v.store_any(static_cast<T *>(p.dg) + lo.base + at);
             if ((PACKED ? CUT : i == 0) && p.dh_init && (PACKED ? marks.first(i) : mine == 0)) {
-                const long s = PACKED ? locate(p, mine + i).seq : b;
+                const long s = PACKED ? locate(p, mine + i).seq : b;  // (a first token is marked by its own look-up)
 #pragma unroll
                 for (int j = 0; j < V; ++j) p.dh_init[s * p.n + c + j] = fl[j];
             }

@@ -540,3 +540,25 @@ def test_more_sequences_than_half_an_int():
     got = {"h": pkg.recurrence_fwd(s["x"], s["g"], cu_seqlens=cu), **pkg.recurrence_bwd(s["x"], s["g"], s["dh"], cu_seqlens=cu)}
     for name, t in want.items():
         assert torch.equal(got[name], t), name
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_offsets_out_of_order_reach_no_state_outside(dtype):
+    """Where offsets are out of order, a lot of tokens may find an end that by its own look-up is in no sequence:
+    no state before the first one is written or read for it."""
+    for n in (48, 37):
+        s = make(1, 300, n, dtype, 5)
+        for cu in ([0, 0, 100, 98, 60, 0, 0, 0], [0, 0, 300, 297, 60, 0, 0, 0], [0, 0, 100, 98, 300, 99, 0, 300], [5, 0, 100, 97, 99, 98, 300, 1]):
+            c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+            seqs = len(cu) - 1
+            states = torch.full((3, seqs, n), float("nan"), device="cuda")
+            states[1] = _randn((seqs, n), "f32", 6)
+            last, first = (torch.full((3, seqs, n), 7.0, device="cuda") for _ in range(2))
+            h = pkg.recurrence_fwd(s["x"], s["g"], cu_seqlens=c, h_init=states[1], h=torch.zeros_like(s["x"]), h_last=last[1])
+            out = {"dx": torch.zeros_like(s["x"]), "dg": torch.zeros_like(s["x"]), "dh_init": first[1]}
+            g = pkg.recurrence_bwd(s["x"], s["g"], s["dh"], cu_seqlens=c, h_init=states[1], dh_last=states[1], out=out)
+            torch.cuda.synchronize()
+            for t in (last, first):
+                assert (t[0] == 7).all() and (t[2] == 7).all(), cu
+            for t in (h, last, *g.values()):
+                assert torch.isfinite(t).all(), cu
