@@ -15,7 +15,8 @@ the HIP stream to libssm2d.so; every operator runs in the library's kernels.
 
 x, gates, weights of products and their gradients: float32 or bfloat16 (one type
 in a call); biases, norms' weights, scales and states: float32. Inputs may be
-strided views (the inner dim contiguous); outputs are dense, and take no part in
+strided views (the inner dim contiguous); outputs are dense, share no memory with
+an input unless it is said so, and take no part in
 autograd: gradients come from the _bwd entries (examples/recurrent_block.py wraps
 them). Workspaces are allocated for each call, from torch's allocator and on the
 call's stream, so that calls may be captured into any number of graphs. Without
@@ -423,9 +424,10 @@ def recurrence_fwd(x, g, *, gates="decay", h_init=None, cu_seqlens=None, channel
     exp(g), w = 1 with ``gates`` "decay" (g the log decay), a = sigmoid(g), w = 1 - a
     with "sigmoid". x, g: [batch, tokens, channels], or with ``channels_first``
     [batch, channels, ...] with the cells as tokens; ``reverse`` goes from the last
-    token to the first. With ``cu_seqlens`` (int32 [sequences + 1], batch 1) the
-    tokens hold packed sequences; tokens behind the last one are left as they
-    were. h_init: float32 [sequences, channels] or None (zeros). Returns h (x's
+    token to the first. Growing gates (g > 0) leave a state of 0 as it is; through
+    tokens that another state passes their product has to be a float. With
+    ``cu_seqlens`` (int32 [sequences + 1], batch 1) the tokens hold packed
+    sequences; tokens behind the last one are left as they were. h_init: float32 [sequences, channels] or None (zeros). Returns h (x's
     shape and dtype), or (h, h_last)."""
     sig, maps, rev = _gates(gates), bool(channels_first), bool(reverse)
     key = ("recurrence", _meta(x), _meta(g), _meta(h_init), _meta(cu_seqlens), sig, maps, rev)

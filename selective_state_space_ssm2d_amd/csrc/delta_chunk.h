@@ -33,9 +33,9 @@
 // matrix ones, 27 to 42 wait).
 //
 // Precision: an fp32 operand goes through the matrix cores as the sum of
-// three bf16 parts, cut off exactly (8 + 8 + 8 bits); products keep the six
-// terms down to 2^-24 of the largest, so every product is as exact as in fp32
-// at 6/16 of its matrix instructions' time. bf16 inputs are one part (three
+// three bf16 parts, cut off exactly (8 + 8 + 8 bits); products keep six
+// terms, and the three left out are under 2^-21 of the product and of its sign, at 6/16
+// of the matrix instructions' time of fp32. bf16 inputs are one part (three
 // terms against an fp32 operand). Outputs are rounded once, from sums like these.
 //
 // Fragments: v_mfma_f32_16x16x32_bf16 with lane l holding row (column) l % 16
