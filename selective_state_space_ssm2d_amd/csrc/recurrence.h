@@ -57,7 +57,8 @@ __device__ __forceinline__ bool is_cut(float p)
 // token by token: c is then what is left, not the NaN of Inf by 0. Products of
 // gates, none of which is negative, are 0 where one of them is, not that NaN (where a
 // gate is NaN, c has it). GROW: gates may; a sigmoid's do not (64 x 196 tokens of 768,
-// backward: 28.4 us, 29.8 with what growing takes).
+// bf16, backward: 28.4 us, 29.8 with what growing takes; decays, of inputs in the caches, forward 12.7 for
+// 11.7 and backward 23.4 for 22.6; long rows and maps 0 to 3 %).
 template <bool GROW>
 __device__ __forceinline__ float state_after(float P, float c, float h)
 {
